@@ -8,10 +8,15 @@ Raw entry points carry the C names and take caller-allocated outputs:
 ``fp8bs_act_quant``, ``fp8bs_weight_quant``, ``fp8bs_weight_dequant``,
 ``fp8bs_gemm``, ``fp8bs_moe_gemm``, the BF16 path ``fp8bs_w8a16_gemm`` and
 the MoE dispatch/combine steps
-``fp8bs_moe_route``, ``fp8bs_moe_quant_scatter``, ``fp8bs_moe_combine``.
+``fp8bs_moe_route``, ``fp8bs_moe_quant_scatter``, ``fp8bs_moe_combine``, the
+absorb attention over a paged latent cache ``fp8bs_mla_attention`` between
+``fp8bs_mla_absorb_key`` and ``fp8bs_mla_absorb_value``, and that cache's
+``fp8bs_mla_cache_write``, ``fp8bs_cache_update``, ``fp8bs_cache_compact``.
 Allocating conveniences: ``act_quant``, ``weight_quant``, ``weight_dequant``,
 ``fp8_gemm``, ``moe_gemm``, ``linear``, ``w8a16_gemm``, ``moe_route``,
-``moe_quant_scatter``, ``moe_combine``.
+``moe_quant_scatter``, ``moe_combine``, ``mla_absorb_key``, ``mla_absorb_value``,
+``mla_cache_alloc``, ``mla_cache_write``, ``mla_attention``, ``cache_update``,
+``cache_compact``.
 
 The operations follow the DeepSeek-V3 inference pages ("DeepSeek-V3
 Administrator & Developer Guide", sections 6.3, 6.4, 8.5.1-8.5.3; "DeepSeek-V3
@@ -22,6 +27,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -32,14 +38,20 @@ __all__ = [
     "fp8bs_moe_combine", "w8a16_gemm", "fp8bs_gemm_ue8m0", "fp8bs_weight_quant_ue8m0",
     "fp8_gemm_ue8m0", "fp8bs_mla_absorb_key", "fp8bs_mla_absorb_value", "mla_absorb_key",
     "mla_absorb_value", "act_quant", "weight_quant", "weight_dequant", "fp8_gemm", "moe_gemm", "linear", "moe_route",
-    "moe_quant_scatter", "moe_combine",
+    "moe_quant_scatter", "moe_combine", "MlaCache", "mla_cache_alloc", "fp8bs_mla_cache_write", "mla_cache_write",
+    "fp8bs_mla_attention", "mla_attention", "fp8bs_cache_update", "cache_update", "fp8bs_cache_compact",
+    "cache_compact",
 ]
 
 SCALE_FP32 = 0
 SCALE_UE8M0 = 1
 OUT_BF16 = 0
 OUT_F32 = 1
+CACHE_BF16 = 0
+CACHE_FP8 = 1
 BLOCK = 128
+MLA_RANK = 512      # latent width of the MLA cache
+MLA_ROPE = 64       # its rotated width
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8bs.so")
 _lib = None
@@ -84,7 +96,21 @@ def lib() -> ctypes.CDLL:
     L.fp8bs_moe_combine.argtypes = [P, P, P, P, I64, I64, I64, I64, I, P]
     L.fp8bs_mla_absorb_key.argtypes = [P, I64, I64, P, P, P, I64, I64, I64, I64, I64, I, P]
     L.fp8bs_mla_absorb_value.argtypes = [P, I64, I64, P, P, P, I64, I64, I64, I64, I64, I, P]
-    for fn in ("fp8bs_act_quant", "fp8bs_weight_quant", "fp8bs_weight_dequant", "fp8bs_gemm",
+    F = ctypes.c_float
+    L.fp8bs_mla_cache_write.argtypes = [P, I64, I64, P, I64, P, I, F, P, I64, P, P, P, P, I, P, P, P,
+                                        I64, I64, I64, I64, I64, I64, I64, I64, P]
+    L.fp8bs_mla_attention_workspace_size.argtypes = [I64, I64, I64]
+    L.fp8bs_mla_attention.argtypes = [P, I64, I64, P, I64, I64, P, P, P, I, P, P, P, F, I, P, I, P,
+                                      I64, I64, I64, I64, I64, I64, I64, I64, P, I64, P]
+    L.fp8bs_cache_update_workspace_size.argtypes = [I64, I64]
+    L.fp8bs_cache_update.argtypes = [P, P, P, I, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, I64, P, I64, P]
+    L.fp8bs_cache_compact_workspace_size.argtypes = [I64]
+    L.fp8bs_cache_compact.argtypes = [P, P, P, I, P, P, P, P, I64, I64, I64, I64, I64, I64, P, I64, P]
+    for fn in ("fp8bs_mla_attention_workspace_size", "fp8bs_cache_update_workspace_size",
+               "fp8bs_cache_compact_workspace_size"):
+        getattr(L, fn).restype = I64
+    for fn in ("fp8bs_mla_cache_write", "fp8bs_mla_attention", "fp8bs_cache_update", "fp8bs_cache_compact",
+               "fp8bs_act_quant", "fp8bs_weight_quant", "fp8bs_weight_dequant", "fp8bs_gemm",
                "fp8bs_moe_gemm", "fp8bs_w8a16_gemm", "fp8bs_moe_route", "fp8bs_moe_quant_scatter",
                "fp8bs_moe_combine", "fp8bs_gemm_ue8m0", "fp8bs_weight_quant_ue8m0",
                "fp8bs_mla_absorb_key", "fp8bs_mla_absorb_value"):
@@ -425,3 +451,212 @@ def w8a16_gemm(x: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor, out_dtype=to
     c = torch.empty((x2.shape[0], w.shape[0]), dtype=out_dtype, device=x.device)
     fp8bs_w8a16_gemm(x2, w, w_s, c)
     return c.view(*x.shape[:-1], w.shape[0])
+
+
+# ------------------------------------------------------ the paged MLA cache
+
+class MlaCache(NamedTuple):
+    """A paged cache of MLA latents: ``latent`` [P, ps, 512] (bfloat16, or
+    float8_e4m3fn codes), ``rope`` bfloat16 [P, ps, 64], and for codes ``scale``
+    float32 [P, ps, 4], powers of two."""
+    latent: torch.Tensor
+    rope: torch.Tensor
+    scale: Optional[torch.Tensor] = None
+
+
+def mla_cache_alloc(pages: int, page_size: int, device, dtype=torch.bfloat16) -> MlaCache:
+    """An empty cache of ``pages`` pages of ``page_size`` tokens (``dtype``
+    torch.bfloat16 or torch.float8_e4m3fn); its contents are not initialised."""
+    if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError(f"cache dtype {dtype} is neither bfloat16 nor float8_e4m3fn")
+    latent = torch.empty((pages, page_size, MLA_RANK), dtype=dtype, device=device)
+    rope = torch.empty((pages, page_size, MLA_ROPE), dtype=torch.bfloat16, device=device)
+    scale = None
+    if dtype == torch.float8_e4m3fn:
+        scale = torch.empty((pages, page_size, MLA_RANK // BLOCK), dtype=torch.float32, device=device)
+    return MlaCache(latent, rope, scale)
+
+
+def _cache_args(cache: MlaCache):
+    """(latent, scale, rope, format, P, ps), checked."""
+    lat, rope, scale = cache
+    if not isinstance(lat, torch.Tensor) or lat.dim() != 3 or lat.shape[2] != MLA_RANK:
+        raise ValueError(f"cache.latent must be [P, ps, {MLA_RANK}]")
+    P, ps = lat.shape[:2]
+    if tuple(rope.shape) != (P, ps, MLA_ROPE):
+        raise ValueError(f"cache.rope must be [P, ps, {MLA_ROPE}]")
+    bf16 = lat.dtype == torch.bfloat16
+    if bf16 != (scale is None):
+        raise ValueError("cache.scale goes with a float8_e4m3fn cache, and only with one")
+    if not bf16 and tuple(scale.shape) != (P, ps, MLA_RANK // BLOCK):
+        raise ValueError(f"cache.scale must be [P, ps, {MLA_RANK // BLOCK}]")
+    return (_need(lat, (torch.bfloat16, *_F8), "cache.latent"),
+            None if bf16 else _need(scale, (torch.float32,), "cache.scale"),
+            _need(rope, (torch.bfloat16,), "cache.rope"), CACHE_BF16 if bf16 else CACHE_FP8, P, ps)
+
+
+def _one_device(*tensors) -> None:
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) > 1:
+        raise ValueError(f"tensors lie on different devices: {sorted(map(str, devs))}")
+
+
+def _i32(t: torch.Tensor, name: str, *shape) -> int:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return _need(t, (torch.int32,), name)
+
+
+def _rows3(t: torch.Tensor, T: int, H: int, width: int, name: str):
+    """A bf16 [T, H, width] view with a dense last dimension: (pointer, token stride, head stride)."""
+    if tuple(t.shape) != (T, H, width):
+        raise ValueError(f"{name} must be [T, H, {width}]")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected bfloat16")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.numel() and t.stride(2) != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return t.data_ptr(), (t.stride(0) if T > 1 else 0), (t.stride(1) if H > 1 else 0)
+
+
+def _batch_args(table, cu_q, lens):
+    if table.dim() != 2 or lens.dim() != 1:
+        raise ValueError("table must be [B, W] and lens [B]")
+    B, W = table.shape
+    return _i32(table, "table", B, W), _i32(cu_q, "cu_q", B + 1), _i32(lens, "lens", B), B, W
+
+
+def fp8bs_mla_cache_write(q_rope: torch.Tensor, kv: torch.Tensor, norm_w: torch.Tensor, eps: float,
+                          rope_cs: torch.Tensor, q_out: torch.Tensor, cache: MlaCache, table: torch.Tensor,
+                          cu_q: torch.Tensor, lens: torch.Tensor) -> None:
+    """New tokens into the cache: kv bf16 [T, 576] (token stride free) normalised
+    (norm_w [512] bf16 or float32), rotated and stored at the last positions of
+    their sequences; q_rope bf16 [T, H, 64] (a slice of q may be passed) rotated
+    into q_out bf16 [T, H, 64].  rope_cs float32 [n_pos, 32, 2] holds (cos, sin)."""
+    if q_rope.dim() != 3 or kv.dim() != 2 or kv.shape[0] != q_rope.shape[0] or kv.shape[1] != MLA_RANK + MLA_ROPE:
+        raise ValueError(f"q_rope must be [T, H, {MLA_ROPE}] and kv [T, {MLA_RANK + MLA_ROPE}]")
+    T, H = q_rope.shape[:2]
+    if tuple(q_out.shape) != (T, H, MLA_ROPE):
+        raise ValueError(f"q_out must be [T, H, {MLA_ROPE}]")
+    if tuple(norm_w.shape) != (MLA_RANK,) or rope_cs.dim() != 3 or tuple(rope_cs.shape[1:]) != (MLA_ROPE // 2, 2):
+        raise ValueError(f"norm_w must be [{MLA_RANK}] and rope_cs [n_pos, {MLA_ROPE // 2}, 2]")
+    _one_device(q_rope, kv, norm_w, rope_cs, q_out, *cache, table, cu_q, lens)
+    lat, scale, rope, fmt, P, ps = _cache_args(cache)
+    qp, ldt, ldh = _rows3(q_rope, T, H, MLA_ROPE, "q_rope")
+    kp, ldk, _ = _rows3(kv.unsqueeze(1), T, 1, MLA_RANK + MLA_ROPE, "kv")
+    tab, cu, ln, B, W = _batch_args(table, cu_q, lens)
+    with torch.cuda.device(kv.device):
+        _call("fp8bs_mla_cache_write", qp, ldt, ldh, kp, ldk, _need(norm_w, (torch.bfloat16, torch.float32), "norm_w"),
+              int(norm_w.dtype == torch.float32), eps, _need(rope_cs, (torch.float32,), "rope_cs"), rope_cs.shape[0],
+              _need(q_out, (torch.bfloat16,), "q_out"), lat, scale, rope, fmt, tab, cu, ln, T, H, B, W, P, ps,
+              MLA_RANK, MLA_ROPE, _stream(kv))
+
+
+def mla_cache_write(q_rope, kv, norm_w, eps, rope_cs, cache: MlaCache, table, cu_q, lens) -> torch.Tensor:
+    """fp8bs_mla_cache_write; returns the rotated queries [T, H, 64]."""
+    q_out = torch.empty(q_rope.shape, dtype=torch.bfloat16, device=q_rope.device)
+    fp8bs_mla_cache_write(q_rope, kv, norm_w, eps, rope_cs, q_out, cache, table, cu_q, lens)
+    return q_out
+
+
+def fp8bs_mla_attention(q_lat: torch.Tensor, q_rope: torch.Tensor, cache: MlaCache, table: torch.Tensor,
+                        cu_q: torch.Tensor, lens: torch.Tensor, scale: float, out: torch.Tensor,
+                        lse: Optional[torch.Tensor], workspace: torch.Tensor, causal: bool = True) -> None:
+    """The new tokens' attention over the cache: q_lat bf16 [T, H, 512] (from
+    mla_absorb_key) and q_rope bf16 [T, H, 64] (from mla_cache_write), any token
+    and head strides; out [T, H, 512] bf16 or float32, lse float32 [T, H] or None."""
+    if q_lat.dim() != 3:
+        raise ValueError(f"q_lat must be [T, H, {MLA_RANK}]")
+    T, H = q_lat.shape[:2]
+    if tuple(out.shape) != (T, H, MLA_RANK) or (lse is not None and tuple(lse.shape) != (T, H)):
+        raise ValueError(f"out must be [T, H, {MLA_RANK}] and lse [T, H]")
+    _one_device(q_lat, q_rope, *cache, table, cu_q, lens, out, lse, workspace)
+    lat, sc, rope, fmt, P, ps = _cache_args(cache)
+    qp, ldt, ldh = _rows3(q_lat, T, H, MLA_RANK, "q_lat")
+    rp, ldrt, ldrh = _rows3(q_rope, T, H, MLA_ROPE, "q_rope")
+    tab, cu, ln, B, W = _batch_args(table, cu_q, lens)
+    nbytes = workspace.numel() * workspace.element_size()
+    ws = _need(workspace, (torch.uint8, torch.float32), "workspace") if nbytes else None
+    with torch.cuda.device(q_lat.device):
+        _call("fp8bs_mla_attention", qp, ldt, ldh, rp, ldrt, ldrh, lat, sc, rope, fmt, tab, cu, ln, scale, int(causal),
+              _need(out, (torch.bfloat16, torch.float32), "out"), _out_code(out),
+              None if lse is None else _need(lse, (torch.float32,), "lse"), T, H, B, W, P, ps, MLA_RANK, MLA_ROPE,
+              ws, nbytes, _stream(q_lat))
+
+
+def mla_attention(q_lat, q_rope, cache: MlaCache, table, cu_q, lens, scale: float, causal: bool = True,
+                  return_lse: bool = False, out_dtype=torch.bfloat16):
+    """fp8bs_mla_attention: out [T, H, 512], with return_lse (out, lse)."""
+    T, H = q_lat.shape[:2]
+    need = lib().fp8bs_mla_attention_workspace_size(T, H, table.shape[0])
+    if need < 0:
+        raise ValueError("sizes out of range")
+    out = torch.empty((T, H, MLA_RANK), dtype=out_dtype, device=q_lat.device)
+    lse = torch.empty((T, H), dtype=torch.float32, device=q_lat.device) if return_lse else None
+    ws = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
+    fp8bs_mla_attention(q_lat, q_rope, cache, table, cu_q, lens, scale, out, lse, ws, causal)
+    return (out, lse) if return_lse else out
+
+
+def fp8bs_cache_update(cache: MlaCache, table: torch.Tensor, lens: torch.Tensor, parent: torch.Tensor,
+                       new_lens: torch.Tensor, table_out: torch.Tensor, lens_out: torch.Tensor,
+                       workspace: torch.Tensor) -> None:
+    """The next step's rows: row i continues old row parent[i] (else it is
+    empty) and is to hold new_lens[i] tokens; table_out [N, W], lens_out [N].
+    Forks, frees, truncates, grows and copies on write (see fp8bs.h)."""
+    if table.dim() != 2 or parent.dim() != 1:
+        raise ValueError("table must be [B, W] and parent [N]")
+    (B, W), N = table.shape, parent.shape[0]
+    _one_device(*cache, table, lens, parent, new_lens, table_out, lens_out, workspace)
+    lat, sc, rope, fmt, P, ps = _cache_args(cache)
+    nbytes = workspace.numel() * workspace.element_size()
+    ws = _need(workspace, (torch.uint8, torch.int32), "workspace") if nbytes else None
+    with torch.cuda.device(table.device):
+        _call("fp8bs_cache_update", lat, sc, rope, fmt, _i32(table, "table", B, W), _i32(lens, "lens", B),
+              _i32(parent, "parent", N), _i32(new_lens, "new_lens", N), _i32(table_out, "table_out", N, W),
+              _i32(lens_out, "lens_out", N), B, N, W, P, ps, MLA_RANK, MLA_ROPE, ws, nbytes, _stream(table))
+
+
+def cache_update(cache: MlaCache, table, lens, parent, new_lens):
+    """fp8bs_cache_update: (table_out [N, W], lens_out [N])."""
+    N, W = parent.shape[0], table.shape[1]
+    need = lib().fp8bs_cache_update_workspace_size(cache.latent.shape[0], N)
+    if need < 0:
+        raise ValueError("sizes out of range")
+    table_out = torch.empty((N, W), dtype=torch.int32, device=table.device)
+    lens_out = torch.empty(N, dtype=torch.int32, device=table.device)
+    ws = torch.empty(need, dtype=torch.uint8, device=table.device)
+    fp8bs_cache_update(cache, table, lens, parent, new_lens, table_out, lens_out, ws)
+    return table_out, lens_out
+
+
+def fp8bs_cache_compact(cache: MlaCache, table: torch.Tensor, lens: torch.Tensor, table_out: torch.Tensor,
+                        count: torch.Tensor, workspace: torch.Tensor) -> None:
+    """The pages that the rows use moved to the lowest indices; table_out
+    [B, W] holds the new ones, count [1] (or a 0-d tensor) how many."""
+    if table.dim() != 2:
+        raise ValueError("table must be [B, W]")
+    if count.numel() != 1:
+        raise ValueError("count must hold one value")
+    B, W = table.shape
+    _one_device(*cache, table, lens, table_out, count, workspace)
+    lat, sc, rope, fmt, P, ps = _cache_args(cache)
+    nbytes = workspace.numel() * workspace.element_size()
+    ws = _need(workspace, (torch.uint8, torch.int32), "workspace") if nbytes else None
+    with torch.cuda.device(table.device):
+        _call("fp8bs_cache_compact", lat, sc, rope, fmt, _i32(table, "table", B, W), _i32(lens, "lens", B),
+              _i32(table_out, "table_out", B, W), _need(count, (torch.int32,), "count"), B, W, P, ps, MLA_RANK,
+              MLA_ROPE, ws, nbytes, _stream(table))
+
+
+def cache_compact(cache: MlaCache, table, lens):
+    """fp8bs_cache_compact: (table_out [B, W], count, a 0-d tensor)."""
+    need = lib().fp8bs_cache_compact_workspace_size(cache.latent.shape[0])
+    if need < 0:
+        raise ValueError("sizes out of range")
+    table_out = torch.empty_like(table)
+    count = torch.empty((), dtype=torch.int32, device=table.device)
+    ws = torch.empty(need, dtype=torch.uint8, device=table.device)
+    fp8bs_cache_compact(cache, table, lens, table_out, count, ws)
+    return table_out, count

@@ -338,4 +338,192 @@ int fp8bs_moe_combine(const void* out_bf16, const float* w, const int32_t* row_o
                                              out_dtype == FP8BS_OUT_F32, (hipStream_t)stream));
 }
 
+// what the paged-cache entry points share: sizes, format, pointers and alignment of the cache
+static int cache_checks(const void* latent, const float* lat_scale, const void* rope, int cache_fmt,
+                        int64_t B, int64_t W, int64_t P, int64_t ps, int64_t R, int64_t dr) {
+  if (R != 512 || dr != 64 || B < 0 || B > kLimitInt || W < 1 || W > kLimitInt || P < 1 || ps < 1 || ps > 4096 || P > kLimitInt / ps ||
+      mul(B, W) < 0 || mul(mul(B, W), 4) < 0)
+    return FP8BS_ERR_SHAPE;
+  if (cache_fmt != FP8BS_CACHE_BF16 && cache_fmt != FP8BS_CACHE_FP8) return FP8BS_ERR_ENUM;
+  if (!latent || !rope || (cache_fmt == FP8BS_CACHE_FP8 && !lat_scale)) return FP8BS_ERR_NULL;
+  if (!aligned(latent, 16) || !aligned(rope, 16) ||
+      (cache_fmt == FP8BS_CACHE_FP8 && !aligned(lat_scale, 16)))
+    return FP8BS_ERR_ALIGN;
+  return FP8BS_OK;
+}
+
+// [out, out + bytes) meets one of the cache's arrays
+static bool over_cache(const void* out, int64_t bytes, const void* latent, const float* lat_scale,
+                       const void* rope, int cache_fmt, int64_t P, int64_t ps) {
+  const bool fp8 = cache_fmt == FP8BS_CACHE_FP8;
+  const int64_t rows = P * ps;
+  return overlap(out, bytes, latent, rows * (fp8 ? 512 : 1024)) || overlap(out, bytes, rope, rows * 128) ||
+         (fp8 && overlap(out, bytes, lat_scale, rows * 16));
+}
+
+// elements from the first to the last of a [T, H, width] view with strides ld_t, ld_h, or -1 when beyond int64
+static int64_t extent(int64_t T, int64_t H, int64_t ld_t, int64_t ld_h, int64_t width) {
+  const int64_t a = mul(T - 1, ld_t), b = mul(H - 1, ld_h);
+  if (a < 0 || b < 0 || a > INT64_MAX / 8 || b > INT64_MAX / 8) return -1;
+  return a + b + width;
+}
+
+int fp8bs_mla_cache_write(const void* q_rope, int64_t ldq_t, int64_t ldq_h, const void* kv,
+                          int64_t ld_kv, const void* norm_w, int norm_w_f32, float eps,
+                          const float* rope_cs, int64_t n_pos, void* q_out, void* latent,
+                          float* lat_scale, void* rope, int cache_fmt, const int32_t* table,
+                          const int32_t* cu_q, const int32_t* lens, int64_t T, int64_t H, int64_t B,
+                          int64_t W, int64_t P, int64_t ps, int64_t R, int64_t dr, void* stream) {
+  if (T < 0 || H < 0 || T > kLimitInt || H > kLimitInt || n_pos < 0 || ldq_t < 0 || ldq_h < 0 ||
+      ld_kv < 0 || !(eps >= 0.0f && eps <= 3.0e38f))
+    return FP8BS_ERR_SHAPE;
+  const int64_t nq = mul(mul(T, H), 64);
+  if (nq < 0 || mul(nq, 2) < 0 || mul(n_pos, 256) < 0) return FP8BS_ERR_SHAPE;
+  if (T == 0 || B == 0) return B < 0 ? FP8BS_ERR_SHAPE : FP8BS_OK;
+  if (ldq_t % 8 != 0 || ldq_h % 8 != 0 || ld_kv % 8 != 0) return FP8BS_ERR_ALIGN;
+  const int st = cache_checks(latent, lat_scale, rope, cache_fmt, B, W, P, ps, R, dr);
+  if (st != FP8BS_OK) return st;
+  if (!kv || !norm_w || !rope_cs || !table || !cu_q || !lens || (H > 0 && (!q_rope || !q_out)))
+    return FP8BS_ERR_NULL;
+  if (!aligned(kv, 16) || !aligned(norm_w, norm_w_f32 ? 4 : 2) || !aligned(rope_cs, 4) ||
+      !aligned(table, 4) || !aligned(cu_q, 4) || !aligned(lens, 4) ||
+      (H > 0 && (!aligned(q_rope, 16) || !aligned(q_out, 16))))
+    return FP8BS_ERR_ALIGN;
+  const int64_t eq = H > 0 ? extent(T, H, ldq_t, ldq_h, 64) : 0, ek = extent(T, 1, ld_kv, 0, 576);
+  if (eq < 0 || ek < 0) return FP8BS_ERR_SHAPE;
+  const void* in[] = {q_rope, kv, norm_w, rope_cs, table, cu_q, lens};
+  const int64_t size[] = {2 * eq, 2 * ek, norm_w_f32 ? 2048 : 1024, 256 * n_pos, 4 * B * W, 4 * (B + 1), 4 * B};
+  for (int i = 0; i < 7; ++i)
+    if (overlap(q_out, 2 * nq, in[i], size[i]) ||
+        over_cache(in[i], size[i], latent, lat_scale, rope, cache_fmt, P, ps))
+      return FP8BS_ERR_ALIAS;
+  if (over_cache(q_out, 2 * nq, latent, lat_scale, rope, cache_fmt, P, ps)) return FP8BS_ERR_ALIAS;
+  const fp8bs::MlaCacheWrite a{q_rope, kv, norm_w, rope_cs, q_out, latent, rope, lat_scale, table, cu_q, lens,
+                               ldq_t, ldq_h, ld_kv, n_pos, T, H, B, W, P, ps, eps, norm_w_f32 != 0,
+                               cache_fmt == FP8BS_CACHE_FP8};
+  return status_of(fp8bs::launch_mla_cache_write(a, (hipStream_t)stream));
+}
+
+int64_t fp8bs_mla_attention_workspace_size(int64_t T, int64_t H, int64_t B) {
+  if (T < 0 || H < 1 || B < 0 || B > 8192) return -1;
+  const int64_t rows = mul(T, H);
+  if (rows < 0 || rows > kLimitInt) return -1;
+  return rows == 0 || B == 0 ? 0 : fp8bs::mla_attention_workspace_bytes(T, H, B);
+}
+
+int fp8bs_mla_attention(const void* q_lat, int64_t ldq_t, int64_t ldq_h, const void* q_rope,
+                        int64_t ldr_t, int64_t ldr_h, const void* latent, const float* lat_scale,
+                        const void* rope, int cache_fmt, const int32_t* table, const int32_t* cu_q,
+                        const int32_t* lens, float scale, int causal, void* out, int out_dtype,
+                        float* lse, int64_t T, int64_t H, int64_t B, int64_t W, int64_t P,
+                        int64_t ps, int64_t R, int64_t dr, void* workspace, int64_t workspace_bytes,
+                        void* stream) {
+  const int64_t need = fp8bs_mla_attention_workspace_size(T, H, B);
+  if (need < 0 || ldq_t < 0 || ldq_h < 0 || ldr_t < 0 || ldr_h < 0 ||
+      !(scale >= -3.0e38f && scale <= 3.0e38f))
+    return FP8BS_ERR_SHAPE;
+  if (out_dtype != FP8BS_OUT_BF16 && out_dtype != FP8BS_OUT_F32) return FP8BS_ERR_ENUM;
+  if (T == 0 || B == 0) return FP8BS_OK;
+  if (workspace_bytes < need) return FP8BS_ERR_SHAPE;
+  if (ldq_t % 8 != 0 || ldq_h % 8 != 0 || ldr_t % 8 != 0 || ldr_h % 8 != 0) return FP8BS_ERR_ALIGN;
+  const int st = cache_checks(latent, lat_scale, rope, cache_fmt, B, W, P, ps, R, dr);
+  if (st != FP8BS_OK) return st;
+  if (!q_lat || !q_rope || !table || !cu_q || !lens || !out || (need > 0 && !workspace)) return FP8BS_ERR_NULL;
+  if (!aligned(q_lat, 16) || !aligned(q_rope, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
+      !aligned(table, 4) || !aligned(cu_q, 4) || !aligned(lens, 4) || !aligned(lse, 4))
+    return FP8BS_ERR_ALIGN;
+  const int64_t eq = extent(T, H, ldq_t, ldq_h, 512), er = extent(T, H, ldr_t, ldr_h, 64);
+  if (eq < 0 || er < 0) return FP8BS_ERR_SHAPE;
+  const int64_t ob = T * H * 512 * (out_dtype == FP8BS_OUT_F32 ? 4 : 2), lb = lse ? 4 * T * H : 0;
+  const void* in[] = {q_lat, q_rope, table, cu_q, lens};
+  const int64_t size[] = {2 * eq, 2 * er, 4 * B * W, 4 * (B + 1), 4 * B};
+  for (int i = 0; i < 5; ++i)
+    if (overlap(out, ob, in[i], size[i]) || overlap(lse, lb, in[i], size[i]) ||
+        overlap(workspace, need, in[i], size[i]))
+      return FP8BS_ERR_ALIAS;
+  if (overlap(out, ob, lse, lb) || overlap(workspace, need, out, ob) || overlap(workspace, need, lse, lb) ||
+      over_cache(out, ob, latent, lat_scale, rope, cache_fmt, P, ps) ||
+      over_cache(lse, lb, latent, lat_scale, rope, cache_fmt, P, ps) ||
+      over_cache(workspace, need, latent, lat_scale, rope, cache_fmt, P, ps))
+    return FP8BS_ERR_ALIAS;
+  const fp8bs::MlaAttention a{q_lat, q_rope, latent, rope, lat_scale, table, cu_q, lens, out, lse, workspace,
+                              ldq_t, ldq_h, ldr_t, ldr_h, T, H, B, W, P, ps, scale, causal != 0,
+                              out_dtype == FP8BS_OUT_F32, cache_fmt == FP8BS_CACHE_FP8};
+  return status_of(fp8bs::launch_mla_attention(a, (hipStream_t)stream));
+}
+
+int64_t fp8bs_cache_update_workspace_size(int64_t P, int64_t N) {
+  if (P < 1 || P > kLimitInt || N < 0 || N >= (1 << 18)) return -1;
+  return N == 0 ? 0 : fp8bs::cache_update_workspace_bytes(P, N);
+}
+
+int fp8bs_cache_update(void* latent, float* lat_scale, void* rope, int cache_fmt,
+                       const int32_t* table, const int32_t* lens, const int32_t* parent,
+                       const int32_t* new_lens, int32_t* table_out, int32_t* lens_out, int64_t B,
+                       int64_t N, int64_t W, int64_t P, int64_t ps, int64_t R, int64_t dr,
+                       void* workspace, int64_t workspace_bytes, void* stream) {
+  const int64_t need = fp8bs_cache_update_workspace_size(P, N);
+  if (need < 0) return FP8BS_ERR_SHAPE;
+  if (N == 0) return FP8BS_OK;
+  if (workspace_bytes < need || mul(N, W) < 0 || mul(mul(N, W), 4) < 0 || B + N > kLimitInt) return FP8BS_ERR_SHAPE;
+  const int st = cache_checks(latent, lat_scale, rope, cache_fmt, B, W, P, ps, R, dr);
+  if (st != FP8BS_OK) return st;
+  if (!parent || !new_lens || !table_out || !lens_out || !workspace || (B > 0 && (!table || !lens)))
+    return FP8BS_ERR_NULL;
+  if (!aligned(workspace, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(parent, 4) ||
+      !aligned(new_lens, 4) || !aligned(table_out, 4) || !aligned(lens_out, 4))
+    return FP8BS_ERR_ALIGN;
+  const void* in[] = {table, lens, parent, new_lens};
+  const int64_t is[] = {4 * B * W, 4 * B, 4 * N, 4 * N};
+  const void* outs[] = {table_out, lens_out, workspace};
+  const int64_t os[] = {4 * N * W, 4 * N, need};
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 4; ++i)
+      if (overlap(outs[o], os[o], in[i], is[i])) return FP8BS_ERR_ALIAS;
+    for (int q = o + 1; q < 3; ++q)
+      if (overlap(outs[o], os[o], outs[q], os[q])) return FP8BS_ERR_ALIAS;
+    if (over_cache(outs[o], os[o], latent, lat_scale, rope, cache_fmt, P, ps)) return FP8BS_ERR_ALIAS;
+  }
+  for (int i = 0; i < 4; ++i)
+    if (over_cache(in[i], is[i], latent, lat_scale, rope, cache_fmt, P, ps)) return FP8BS_ERR_ALIAS;
+  const fp8bs::PageTask a{latent, rope, lat_scale, table, lens, parent, new_lens, table_out, lens_out, nullptr,
+                          workspace, B, W, N, P, ps, cache_fmt == FP8BS_CACHE_FP8};
+  return status_of(fp8bs::launch_cache_update(a, (hipStream_t)stream));
+}
+
+int64_t fp8bs_cache_compact_workspace_size(int64_t P) {
+  if (P < 1 || P > kLimitInt) return -1;
+  return fp8bs::cache_compact_workspace_bytes(P);
+}
+
+int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fmt,
+                        const int32_t* table, const int32_t* lens, int32_t* table_out,
+                        int32_t* count, int64_t B, int64_t W, int64_t P, int64_t ps, int64_t R,
+                        int64_t dr, void* workspace, int64_t workspace_bytes, void* stream) {
+  const int64_t need = fp8bs_cache_compact_workspace_size(P);
+  if (need < 0 || workspace_bytes < need) return FP8BS_ERR_SHAPE;
+  const int st = cache_checks(latent, lat_scale, rope, cache_fmt, B, W, P, ps, R, dr);
+  if (st != FP8BS_OK) return st;
+  if (!count || !workspace || (B > 0 && (!table || !lens || !table_out))) return FP8BS_ERR_NULL;
+  if (!aligned(workspace, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(table_out, 4) ||
+      !aligned(count, 4))
+    return FP8BS_ERR_ALIGN;
+  const void* in[] = {table, lens};
+  const int64_t is[] = {4 * B * W, 4 * B};
+  const void* outs[] = {table_out, count, workspace};
+  const int64_t os[] = {4 * B * W, 4, need};
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 2; ++i)
+      if (overlap(outs[o], os[o], in[i], is[i])) return FP8BS_ERR_ALIAS;
+    for (int q = o + 1; q < 3; ++q)
+      if (overlap(outs[o], os[o], outs[q], os[q])) return FP8BS_ERR_ALIAS;
+    if (over_cache(outs[o], os[o], latent, lat_scale, rope, cache_fmt, P, ps)) return FP8BS_ERR_ALIAS;
+  }
+  for (int i = 0; i < 2; ++i)
+    if (over_cache(in[i], is[i], latent, lat_scale, rope, cache_fmt, P, ps)) return FP8BS_ERR_ALIAS;
+  const fp8bs::PageTask a{latent, rope, lat_scale, table, lens, nullptr, nullptr, table_out, nullptr, count,
+                          workspace, B, W, 0, P, ps, cache_fmt == FP8BS_CACHE_FP8};
+  return status_of(fp8bs::launch_cache_compact(a, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -56,4 +56,48 @@ hipError_t launch_mla_absorb_value(const void* x, int64_t ld_t, int64_t ld_h, co
                                    const float* ws, void* out, int64_t T, int64_t H, int64_t dn,
                                    int64_t dv, int64_t R, bool out_f32, hipStream_t stream);
 
+// fp8bs_mla_attention's arguments
+struct MlaAttention {
+  const void *q_lat, *q_rope, *latent, *rope;
+  const float* lat_scale;
+  const int32_t *table, *cu_q, *lens;
+  void* out;
+  float* lse;
+  void* workspace;
+  int64_t ldq_t, ldq_h, ldr_t, ldr_h;
+  int64_t T, H, B, W, P, ps;
+  float scale;
+  bool causal, out_f32, fp8;
+};
+hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream);
+int64_t mla_attention_workspace_bytes(int64_t T, int64_t H, int64_t B);
+
+// fp8bs_mla_cache_write's arguments
+struct MlaCacheWrite {
+  const void *q, *kv, *w;
+  const float* cs;
+  void *q_out, *latent, *rope;
+  float* scale;
+  const int32_t *table, *cu_q, *lens;
+  int64_t ldq_t, ldq_h, ld_kv, n_pos;
+  int64_t T, H, B, W, P, ps;
+  float eps;
+  bool w_f32, fp8;
+};
+hipError_t launch_mla_cache_write(const MlaCacheWrite& a, hipStream_t stream);
+
+// fp8bs_cache_update's and fp8bs_cache_compact's arguments (update: parent, new_lens, lens_out; compact: count)
+struct PageTask {
+  void *latent, *rope, *scale;
+  const int32_t *table, *lens, *parent, *new_lens;
+  int32_t *table_out, *lens_out, *count;
+  void* workspace;
+  int64_t B, W, N, P, ps;
+  bool fp8;
+};
+int64_t cache_update_workspace_bytes(int64_t P, int64_t N);
+int64_t cache_compact_workspace_bytes(int64_t P);
+hipError_t launch_cache_update(const PageTask& a, hipStream_t stream);
+hipError_t launch_cache_compact(const PageTask& a, hipStream_t stream);
+
 }  // namespace fp8bs

@@ -57,6 +57,10 @@ extern "C" {
 #define FP8BS_OUT_BF16    0
 #define FP8BS_OUT_F32     1
 
+/* Element types of an MLA cache's latents. */
+#define FP8BS_CACHE_BF16  0
+#define FP8BS_CACHE_FP8   1  /* e4m3 codes with a power-of-two float32 scale per 128 */
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fp8bs_status_string(int status);
 
@@ -369,6 +373,150 @@ int fp8bs_mla_absorb_key(const void* q_bf16, int64_t ld_t, int64_t ld_h, const v
 int fp8bs_mla_absorb_value(const void* x_bf16, int64_t ld_t, int64_t ld_h, const void* wkv_b,
                            const float* wkv_b_s, void* out, int64_t T, int64_t H, int64_t dn,
                            int64_t dv, int64_t R, int out_dtype, void* stream);
+
+/*
+ * The paged MLA cache -- what the absorb attention keeps of a token (Admin
+ * guide 8.3: kv_cache and pe_cache), in pages, and the attention between
+ * fp8bs_mla_absorb_key and fp8bs_mla_absorb_value.
+ *
+ * Shared by the entry points below:
+ *   latent     DEVICE [P, ps, 512]: the normalised latents, bf16
+ *              (FP8BS_CACHE_BF16) or e4m3 codes (FP8BS_CACHE_FP8)
+ *   rope       DEVICE bf16 [P, ps, 64]: the rotated part of the shared key
+ *   lat_scale  DEVICE float32 [P, ps, 4] with FP8BS_CACHE_FP8 (NULL otherwise):
+ *              the multipliers of 128 codes each, powers of two in 2^-100 ..
+ *              2^100, so that code * scale is exact in bf16
+ *   table      DEVICE int32 [B, W]: the pages of sequence b in order; token j
+ *              lies in page table[b][j / ps] at j % ps.  Entries behind the
+ *              sequence's last page are not read.
+ *   lens       DEVICE int32 [B]: tokens of each sequence, 0 .. W * ps, those
+ *              of this call included
+ *   cu_q       DEVICE int32 [B + 1]: sequence b's new tokens are rows cu_q[b]
+ *              .. cu_q[b+1] - 1; cu_q[0] = 0, non-decreasing, cu_q[B] <= T.
+ *              A sequence may have none.  Its new tokens are its last: with
+ *              n_b of them, the i-th has position lens[b] - n_b + i.
+ *   R = 512 and dr = 64 (the pages' configurations all use these).
+ *   1 <= ps <= 4096, P >= 1, W >= 1, P * ps < 2^31.
+ * Values of table, lens and cu_q lie on the device and are preconditions, not
+ * checked on the host; the kernels clamp lens to [0, W * ps] and cu_q to [0, T],
+ * never write outside the cache, and read no page outside [0, P), so a wrong
+ * value gives wrong results for its sequence, not faults.
+ * Byte pointers are 16-byte aligned, float32 and int32 ones 4-byte.
+ */
+
+/*
+ * mla_cache_write -- the new tokens into the cache, and their queries rotated:
+ *   c = kv[t, 0:512] / sqrt(mean(kv[t, 0:512]^2) + eps) * norm_w
+ *   latent <- bf16(c), or per 128: s = the power of two of act_quant's
+ *             FP8BS_SCALE_UE8M0 rule on c, code = e4m3(c / s)
+ *   rope   <- bf16(rotate(kv[t, 512:576])),  q_out[t, h] = bf16(rotate(q[t, h]))
+ * where rotate turns each pair (2i, 2i + 1) by the angle whose cosine and sine
+ * are rope_cs[position][i] (the interleaved pairs of the pages' complex
+ * product).  The sum of squares, the norm and the products are float32,
+ * rounded once.
+ *
+ *   q_rope   in   bf16, element (t, h, i) at [t*ldq_t + h*ldq_h + i], i < 64:
+ *                 the rope slice of the query; ldq_t, ldq_h >= 0, multiples of 8
+ *   kv       in   bf16, element (t, i) at [t*ld_kv + i], i < 576; multiple of 8
+ *   norm_w   in   [512] float32 (norm_w_f32 != 0) or bf16
+ *   eps           >= 0, finite
+ *   rope_cs  in   float32 [n_pos, 32, 2]: (cos, sin)
+ *   q_out    out  bf16 [T, H, 64]
+ *   T >= 0 (0 = no-op), H >= 0 (0 = no queries), B >= 0, n_pos >= 0.
+ * A token at a position outside [0, n_pos) is skipped: neither its cache row
+ * nor its q_out is written.  A token whose page lies outside [0, P) has its
+ * q_out written only.  Rows t >= cu_q[B] are left as they were.  Two tokens
+ * of one call must not share a cache row (a page that two sequences share is
+ * made one's own by fp8bs_cache_update first).
+ */
+int fp8bs_mla_cache_write(const void* q_rope, int64_t ldq_t, int64_t ldq_h, const void* kv,
+                          int64_t ld_kv, const void* norm_w, int norm_w_f32, float eps,
+                          const float* rope_cs, int64_t n_pos, void* q_out, void* latent,
+                          float* lat_scale, void* rope, int cache_fmt, const int32_t* table,
+                          const int32_t* cu_q, const int32_t* lens, int64_t T, int64_t H, int64_t B,
+                          int64_t W, int64_t P, int64_t ps, int64_t R, int64_t dr, void* stream);
+
+/*
+ * mla_attention -- the new tokens' attention over the cache:
+ *   s[t, h, j] = scale * (q_lat[t, h] . c_j + q_rope[t, h] . k_j),
+ *   out[t, h]  = sum_j softmax_j(s[t, h, :]) c_j
+ *   lse[t, h]  = log sum_j exp(s[t, h, j])
+ * over the tokens j of t's sequence: j <= position(t) when causal, else all
+ * lens[b].  c_j is the cached latent (code * scale for an FP8 cache), k_j its
+ * rope part.  A row that sees no token (a sequence of length 0, a position
+ * below 0) gives out = 0 and lse = -inf.  Rows t >= cu_q[B] are left as they
+ * were.
+ *
+ *   q_lat    in   bf16, element (t, h, i) at [t*ldq_t + h*ldq_h + i], i < 512
+ *                 (fp8bs_mla_absorb_key's output)
+ *   q_rope   in   bf16, the same with ldr_t, ldr_h, i < 64
+ *                 (fp8bs_mla_cache_write's q_out); strides >= 0, multiples of 8
+ *   scale         finite
+ *   out      out  [T, H, 512] bf16 or float32 (out_dtype)
+ *   lse      out  float32 [T, H], or NULL
+ *   workspace     DEVICE, >= fp8bs_mla_attention_workspace_size(T, H, B) bytes,
+ *                 16-byte aligned; scratch (nothing needs clearing), not to be
+ *                 shared by calls that may run at the same time
+ *   T, B >= 0 (either 0 = no-op), H >= 1, T * H < 2^31, B <= 8192.
+ * Products are of bf16 values (an FP8 cache's are exact in bf16) and summed in
+ * float32; the probabilities are rounded to bf16 for the second product, the
+ * softmax's maximum and sum are float32.  The result does not depend on
+ * timing.
+ */
+int64_t fp8bs_mla_attention_workspace_size(int64_t T, int64_t H, int64_t B);
+int fp8bs_mla_attention(const void* q_lat, int64_t ldq_t, int64_t ldq_h, const void* q_rope,
+                        int64_t ldr_t, int64_t ldr_h, const void* latent, const float* lat_scale,
+                        const void* rope, int cache_fmt, const int32_t* table, const int32_t* cu_q,
+                        const int32_t* lens, float scale, int causal, void* out, int out_dtype,
+                        float* lse, int64_t T, int64_t H, int64_t B, int64_t W, int64_t P,
+                        int64_t ps, int64_t R, int64_t dr, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
+/*
+ * cache_update -- the pages of the next step: N new rows from B old ones.
+ * New row i continues old row parent[i] (any other value: an empty row) and
+ * is to hold new_lens[i] tokens: it keeps the first min(lens[parent],
+ * new_lens) tokens in the parent's pages and, if it is longer, gets pages for
+ * the rest.  So a row continued twice is forked, one that nobody continues is
+ * freed, one given fewer tokens is truncated, one given more grows.
+ *
+ * Pages are given out in row order, lowest index first, from those that no old
+ * row uses (a page freed by this call is free for the next).  Rows share what
+ * they keep; a row that will write into a kept page (it grows and that page is
+ * not full) shares it only as the page's keeper, the lowest such row among
+ * those that keep the most of the page's tokens; any other gets a copy: a page
+ * of its own with the kept tokens.  A row for which too few pages are left
+ * is not grown: lens_out[i] is then what it keeps.
+ *
+ *   table, lens  in   old rows [B, W], [B]
+ *   parent, new_lens  in   DEVICE int32 [N]; new_lens is clamped to [0, W * ps]
+ *   table_out    out  DEVICE int32 [N, W], -1 behind each row's last page
+ *   lens_out     out  DEVICE int32 [N]
+ *   latent, lat_scale, rope   in/out: only pages that no old row uses are
+ *                     written, and only a copy's kept tokens
+ *   workspace    DEVICE, >= fp8bs_cache_update_workspace_size(P, N) bytes,
+ *                16-byte aligned, scratch; not shared by concurrent calls
+ *   B >= 0, 0 <= N < 2^18 (N = 0: no-op).
+ * The result depends on the inputs alone, and a repeated call gives it again.
+ *
+ * cache_compact -- the n pages that the rows use moved to pages 0 .. n - 1:
+ * pages in use at n and above go to the unused ones below n, both in
+ * ascending order; table_out is the table with the new indices (-1 behind
+ * each row's last page and for entries outside [0, P)), count = n.
+ *   table_out    out  DEVICE int32 [B, W];  count  out  DEVICE int32 [1]
+ *   workspace    >= fp8bs_cache_compact_workspace_size(P) bytes
+ */
+int64_t fp8bs_cache_update_workspace_size(int64_t P, int64_t N);
+int fp8bs_cache_update(void* latent, float* lat_scale, void* rope, int cache_fmt,
+                       const int32_t* table, const int32_t* lens, const int32_t* parent,
+                       const int32_t* new_lens, int32_t* table_out, int32_t* lens_out, int64_t B,
+                       int64_t N, int64_t W, int64_t P, int64_t ps, int64_t R, int64_t dr,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+int64_t fp8bs_cache_compact_workspace_size(int64_t P);
+int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fmt,
+                        const int32_t* table, const int32_t* lens, int32_t* table_out,
+                        int32_t* count, int64_t B, int64_t W, int64_t P, int64_t ps, int64_t R,
+                        int64_t dr, void* workspace, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

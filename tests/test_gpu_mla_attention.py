@@ -1,0 +1,184 @@
+"""GPU parity of fp8bs_mla_attention (new tokens over a paged MLA cache) against
+the formula in 64 bits: row tiles of every kind, both cache types, lengths from
+none to many pages, odd page sizes, strided queries, masks that leave rows
+empty, and garbage wherever the operator must not look."""
+import math
+
+import pytest
+import torch
+
+import block_scaled_fp8_03_amd as fp8bs
+from mla_util import (BF16, D, FP8, R, attention64, check_attention, cu_of, make_cache, make_table, to_dev)
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+SCALE = 192.0 ** -0.5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def batch(H, nq, lens, ps, dtype, seed, spare=2, W=None, behind=-1):
+    g = torch.Generator().manual_seed(seed)
+    P = sum(-(-n // ps) for n in lens) + spare
+    cache = make_cache(P, ps, dtype, g)
+    table = make_table(lens, ps, P, g, behind, W)
+    T = sum(nq)
+    q_lat = torch.randn((T, H, R), generator=g).to(BF16)
+    q_rope = torch.randn((T, H, D), generator=g).to(BF16)
+    return q_lat, q_rope, cache, table, cu_of(nq), torch.tensor(lens, dtype=torch.int32)
+
+
+def run(args, causal=True, dt=BF16, lse=True, scale=SCALE):
+    q_lat, q_rope, cache, table, cu, lens = args
+    got = fp8bs.mla_attention(q_lat.to(DEV), q_rope.to(DEV), to_dev(cache), table.to(DEV), cu.to(DEV), lens.to(DEV),
+                              scale, causal, lse, dt)
+    torch.cuda.synchronize()
+    return got if lse else (got, None)
+
+
+def compare(args, what, causal=True, dt=BF16, scale=SCALE):
+    q_lat, q_rope, cache, table, cu, lens = args
+    out, lse = run(args, causal, dt, True, scale)
+    ref = attention64(q_lat, q_rope, cache, table, cu, lens, scale, causal)
+    check_attention(out, lse, ref, int(lens.max()), what)
+    return out, lse
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("H,nq,lens,ps", [
+    (1, [1], [1], 1),
+    (16, [1], [31], 16),
+    (16, [1, 1, 1], [32, 33, 500], 64),
+    (5, [1, 2, 0, 1], [7, 40, 90, 129], 7),
+    (17, [1, 1], [64, 65], 32),               # a second row tile of one row
+    (32, [1, 1], [257, 100], 48),
+    (48, [1], [300], 64),
+    (64, [1, 1], [130, 1], 64),
+    (128, [1, 1, 1], [1, 257, 700], 64),
+    (100, [1], [95], 64),                     # ragged 128-row tile
+    (16, [9, 40], [9, 300], 16),              # chunks: eight tokens a tile
+    (128, [5], [261], 64),
+    (3, [50, 1, 17], [50, 200, 60], 100),
+    (24, [3, 3], [3, 1000], 1),
+    (8, [4, 4, 4, 4], [4, 40, 400, 401], 4096),
+])
+def test_attention(H, nq, lens, ps, dtype):
+    args = batch(H, nq, lens, ps, dtype, 7 * H + sum(lens))
+    compare(args, f"H {H} nq {nq} lens {lens} ps {ps}")
+
+
+@pytest.mark.parametrize("dt", [BF16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("H,nq", [(16, [1, 7, 30]), (128, [1, 2, 3])])
+def test_causal_and_output_types(H, nq, causal, dt):
+    compare(batch(H, nq, [70, 33, 200], 32, BF16, 11 + H), f"H {H} causal {causal} {dt}", causal, dt)
+
+
+@pytest.mark.parametrize("H", [1, 16, 40, 128])
+@pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
+def test_rows_that_see_nothing(H, dtype):
+    """A sequence of no tokens, and more new tokens than the cache holds: those
+    at positions below 0 see nothing, and give zeros and -inf."""
+    args = batch(H, [2, 5, 3, 1], [0, 3, 40, 0], 16, dtype, 21 + H)
+    out, lse = compare(args, f"empty rows, H {H}")
+    empty = torch.tensor([0, 1, 2, 3, 10])
+    assert (out[empty] == 0).all() and (lse[empty] == -math.inf).all()
+    assert not torch.isinf(lse[4:10]).any()
+
+
+@pytest.mark.parametrize("H,nq", [(16, [1, 1]), (64, [1, 1]), (128, [1, 3]), (32, [1, 1])])
+def test_garbage_out_of_sight(H, nq):
+    """NaN in every unused cache row and page and beside the table's used part
+    indices of no page at all: nothing behind a sequence is looked at."""
+    args = batch(H, nq, [45, 130], 32, BF16, 31 + H, W=9, behind=2 ** 30)
+    q_lat, q_rope, cache, table, cu, lens = args
+    used = torch.zeros(cache.latent.shape[:2], dtype=torch.bool)
+    for b, n in enumerate(lens.tolist()):
+        for j in range(n):
+            used[table[b, j // 32], j % 32] = True
+    lat, rope = cache.latent.clone(), cache.rope.clone()
+    lat[~used], rope[~used] = math.nan, math.nan
+    dirty = (q_lat, q_rope, fp8bs.MlaCache(lat, rope, None), table, cu, lens)
+    a, la = run(args)
+    b, lb = run(dirty)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    compare(args, "clean")
+
+
+def test_pages_outside_the_cache_do_not_fault():
+    """Entries that name no page: the sequence's result is unspecified, the others' is not touched by it."""
+    args = batch(16, [1, 1, 1], [100, 64, 90], 32, BF16, 41)
+    q_lat, q_rope, cache, table, cu, lens = args
+    ref = attention64(q_lat, q_rope, cache, table, cu, lens, SCALE, True)
+    bad = table.clone()
+    bad[1] = torch.tensor([-5, 2 ** 31 - 1, 12345678, -2 ** 31])[: bad.shape[1]]
+    out, lse = run((q_lat, q_rope, cache, bad, cu, lens))
+    keep = torch.tensor([0, 2])
+    check_attention(out[keep], lse[keep], tuple(x[keep] for x in ref), 100, "beside bad pages")
+
+
+def test_strided_queries_and_rows_behind():
+    """Queries as slices (token and head strides of their own), and rows behind
+    the last sequence, which keep what they held."""
+    H, nq, lens = 12, [3, 2], [50, 77]
+    args = batch(H, nq, lens, 32, FP8, 51)
+    q_lat, q_rope, cache, table, cu, lens = args
+    wide = torch.full((7, H + 1, R + 64), 5.0, dtype=BF16)
+    wide[:5, :H, :R], wide[:5, 1:, R:] = q_lat, q_rope
+    wide = wide.to(DEV)
+    ql, qr = wide[:, :H, :R], wide[:, 1:, R:]
+    out = torch.full((7, H, R), 3.0, dtype=BF16, device=DEV)
+    lse = torch.full((7, H), 3.0, device=DEV)
+    need = fp8bs.lib().fp8bs_mla_attention_workspace_size(7, H, 2)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    fp8bs.fp8bs_mla_attention(ql, qr, to_dev(cache), table.to(DEV), cu.to(DEV), lens.to(DEV), SCALE, out, lse, ws)
+    torch.cuda.synchronize()
+    ref = attention64(q_lat, q_rope, cache, table, cu, lens, SCALE, True)
+    check_attention(out[:5], lse[:5], ref, 77, "strided")
+    assert (out[5:] == 3).all() and (lse[5:] == 3).all()
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_late_maximum(H):
+    """Scores that grow along the sequence by far more than the lazy rescale's
+    margin, then fall: the running maximum moves many times."""
+    args = batch(H, [2], [400], 64, BF16, 61)
+    q_lat, q_rope, cache, table, cu, lens = args
+    size = torch.linspace(0.1, 6.0, 400)
+    size[300:] = torch.linspace(6.0, 0.1, 100)
+    lat = cache.latent.float()
+    for j in range(400):
+        lat[table[0, j // 64], j % 64] *= size[j]
+    cache = fp8bs.MlaCache(lat.to(BF16), cache.rope, None)
+    compare((q_lat, q_rope, cache, table, cu, lens), "growing scores")
+
+
+@pytest.mark.parametrize("scale", [-0.05, 0.0, 1.0])
+def test_any_scale(scale):
+    compare(batch(16, [2, 1], [60, 99], 32, BF16, 71), f"scale {scale}", scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
+def test_many_sequences(dtype):
+    """300 sequences of odd lengths, none, one or a few new tokens each."""
+    g = torch.Generator().manual_seed(81)
+    nq = torch.randint(0, 4, (300,), generator=g).tolist()
+    lens = torch.randint(0, 90, (300,), generator=g).tolist()
+    compare(batch(8, nq, lens, 16, dtype, 82), "300 sequences")
+
+
+@pytest.mark.parametrize("H,B,n", [(16, 1, 20000), (128, 2, 9000), (16, 3, 5000)])
+def test_long_sequences(H, B, n):
+    """Few rows over a long cache (the token axis is split and joined)."""
+    args = batch(H, [1] * B, [n - 37 * b for b in range(B)], 64, FP8 if H == 16 else BF16, 91 + n)
+    compare(args, f"long {H} {B} {n}")
+
+
+def test_no_new_tokens_and_no_sequences():
+    args = batch(16, [0, 0], [10, 20], 16, BF16, 95)
+    out, lse = run(args)
+    assert out.shape == (0, 16, R) and lse.shape == (0, 16)

@@ -1,0 +1,175 @@
+"""Host checks of the paged MLA cache's entry points: bad arguments are refused
+before any HIP call (the addresses below are never touched), and the binding
+refuses tensors that do not fit.  Also that the attention kernel's listing
+leaves the accumulator registers to the kernel."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+import block_scaled_fp8_03_amd as fp8bs
+
+OK, NULL, SHAPE, ALIGN, ENUM, HIP, ALIAS = 0, 1, 2, 3, 4, 5, 6
+A = [0x10000000 * (i + 1) for i in range(16)]
+INF = float("inf")
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(fp8bs.library_path):
+        from block_scaled_fp8_03_amd import build
+        build.build()
+    return fp8bs.lib()
+
+
+WRITE = dict(q=A[0], ldq_t=768, ldq_h=192, kv=A[1], ld_kv=576, w=A[2], w_f32=0, eps=1e-6, cs=A[3], n_pos=100, q_out=A[4],
+             latent=A[5], scale=None, rope=A[6], fmt=0, table=A[7], cu=A[8], lens=A[9], T=4, H=4, B=2, W=3, P=10, ps=16,
+             R=512, dr=64, stream=None)
+ATTN = dict(q=A[0], ldq_t=2048, ldq_h=512, qr=A[1], ldr_t=256, ldr_h=64, latent=A[2], scale=None, rope=A[3], fmt=0,
+            table=A[4], cu=A[5], lens=A[6], sm=0.1, causal=1, out=A[7], dt=0, lse=A[8], T=4, H=4, B=2, W=3, P=10, ps=16,
+            R=512, dr=64, ws=A[9], nws=1 << 40, stream=None)
+UPDATE = dict(latent=A[0], scale=None, rope=A[1], fmt=0, table=A[2], lens=A[3], parent=A[4], new=A[5], tout=A[6], lout=A[7],
+              B=2, N=3, W=3, P=10, ps=16, R=512, dr=64, ws=A[8], nws=1 << 40, stream=None)
+COMPACT = dict(latent=A[0], scale=None, rope=A[1], fmt=0, table=A[2], lens=A[3], tout=A[4], count=A[5], B=2, W=3, P=10,
+               ps=16, R=512, dr=64, ws=A[6], nws=1 << 40, stream=None)
+
+
+def call(f, base, **kw):
+    assert set(kw) <= set(base)
+    return f(*{**base, **kw}.values())
+
+
+@pytest.mark.parametrize("name,base,floats", [
+    ("fp8bs_mla_cache_write", WRITE, ["kv", "q", "q_out", "latent", "rope"]),
+    ("fp8bs_mla_attention", ATTN, ["q", "qr", "latent", "rope", "out", "ws"]),
+    ("fp8bs_cache_update", UPDATE, ["latent", "rope", "ws"]),
+    ("fp8bs_cache_compact", COMPACT, ["latent", "rope", "ws"]),
+])
+def test_shared_refusals(L, name, base, floats):
+    f = getattr(L, name)
+    for kw in (dict(R=256), dict(dr=32), dict(B=-1), dict(W=0), dict(P=0), dict(ps=0), dict(ps=4097),
+               dict(P=1 << 31), dict(P=1 << 20, ps=4096), dict(W=-3)):
+        assert call(f, base, **kw) == SHAPE, kw
+    for kw in (dict(fmt=2), dict(fmt=-1)):
+        assert call(f, base, **kw) == ENUM, kw
+    assert call(f, base, fmt=1) == NULL                       # codes without scales
+    assert call(f, base, fmt=1, scale=A[15] + 4) == ALIGN
+    for k in floats:
+        if k == "ws" and name == "fp8bs_mla_attention" and L.fp8bs_mla_attention_workspace_size(4, 4, 2) == 0:
+            continue
+        assert call(f, base, **{k: None}) == NULL, k
+        assert call(f, base, **{k: base[k] + 8}) == ALIGN, k
+    for k in ("table", "lens"):
+        assert call(f, base, **{k: None}) == NULL, k
+        assert call(f, base, **{k: base[k] + 2}) == ALIGN, k
+
+
+def test_write_refusals(L):
+    f = L.fp8bs_mla_cache_write
+    for kw in (dict(T=-1), dict(H=-1), dict(n_pos=-1), dict(eps=-1.0), dict(eps=INF), dict(eps=float("nan")),
+               dict(ldq_t=-8), dict(ld_kv=-8), dict(T=1 << 31), dict(ldq_t=1 << 62, T=1 << 20)):
+        assert call(f, WRITE, **kw) == SHAPE, kw
+    for kw in (dict(ldq_t=4), dict(ldq_h=12), dict(ld_kv=577), dict(w=A[2] + 1), dict(w=A[2] + 2, w_f32=1),
+               dict(cs=A[3] + 2), dict(cu=A[8] + 1)):
+        assert call(f, WRITE, **kw) == ALIGN, kw
+    for k in ("w", "cs", "cu"):
+        assert call(f, WRITE, **{k: None}) == NULL, k
+    for kw in (dict(q_out=A[0]), dict(q_out=A[1] + 16), dict(q_out=A[5] + 1024), dict(kv=A[5]), dict(table=A[6] + 128),
+               dict(q_out=A[9])):
+        assert call(f, WRITE, **kw) == ALIAS, kw
+    assert call(f, WRITE, T=0, kv=None, q=None, q_out=None, w=None) == OK
+    assert call(f, WRITE, B=0) == OK
+
+
+def test_attention_refusals(L):
+    f, ws = L.fp8bs_mla_attention, L.fp8bs_mla_attention_workspace_size
+    for kw in (dict(T=-1), dict(H=0), dict(T=1 << 24, H=128), dict(B=8193), dict(sm=INF), dict(sm=float("nan")),
+               dict(ldq_h=-8), dict(ldr_t=-8)):
+        assert call(f, ATTN, **kw) == SHAPE, kw
+    for kw in (dict(ldq_t=4), dict(ldr_h=12), dict(lse=A[8] + 2), dict(cu=A[5] + 3)):
+        assert call(f, ATTN, **kw) == ALIGN, kw
+    assert call(f, ATTN, dt=2) == ENUM
+    assert call(f, ATTN, cu=None) == NULL
+    need = ws(4, 4, 2)
+    for kw in (dict(out=A[0] + 64), dict(lse=A[1]), dict(out=A[2]), dict(lse=A[7] + 16), dict(out=A[4]),
+               *([dict(ws=A[7]), dict(ws=A[3] + 16)] if need else [])):
+        assert call(f, ATTN, **kw) == ALIAS, kw
+    assert call(f, ATTN, T=0, q=None, out=None) == OK
+    assert call(f, ATTN, B=0) == OK
+    assert ws(-1, 4, 2) == ws(4, 0, 2) == ws(4, 4, -1) == ws(1 << 24, 128, 2) == ws(4, 4, 8193) == -1
+    assert ws(0, 4, 2) == ws(4, 4, 0) == 0
+    if need:
+        assert call(f, ATTN, nws=need - 1) == SHAPE
+
+
+def test_update_and_compact_refusals(L):
+    f, g = L.fp8bs_cache_update, L.fp8bs_cache_compact
+    for kw in (dict(N=-1), dict(N=1 << 18), dict(nws=L.fp8bs_cache_update_workspace_size(10, 3) - 1)):
+        assert call(f, UPDATE, **kw) == SHAPE, kw
+    for k in ("parent", "new", "tout", "lout"):
+        assert call(f, UPDATE, **{k: None}) == NULL, k
+        assert call(f, UPDATE, **{k: UPDATE[k] + 2}) == ALIGN, k
+    for kw in (dict(tout=A[2]), dict(lout=A[3] + 4), dict(tout=A[0]), dict(ws=A[1] + 16), dict(lout=A[6] + 4), dict(ws=A[4]),
+               dict(table=A[0])):
+        assert call(f, UPDATE, **kw) == ALIAS, kw
+    assert call(f, UPDATE, N=0, parent=None, tout=None) == OK
+    assert call(g, COMPACT, nws=L.fp8bs_cache_compact_workspace_size(10) - 1) == SHAPE
+    for k in ("tout", "count"):
+        assert call(g, COMPACT, **{k: None}) == NULL, k
+        assert call(g, COMPACT, **{k: COMPACT[k] + 2}) == ALIGN, k
+    for kw in (dict(tout=A[2]), dict(count=A[3]), dict(tout=A[0]), dict(ws=A[1] + 16), dict(count=A[4] + 4)):
+        assert call(g, COMPACT, **kw) == ALIAS, kw
+    assert L.fp8bs_cache_update_workspace_size(0, 3) == L.fp8bs_cache_update_workspace_size(4, 1 << 18) == -1
+    assert L.fp8bs_cache_compact_workspace_size(0) == -1
+
+
+def test_binding_refusals():
+    """Shapes and types are refused before anything is asked of a device."""
+    bf, i32 = torch.bfloat16, torch.int32
+    cache = fp8bs.mla_cache_alloc(4, 16, "cpu")
+    table, cu, lens = torch.zeros((2, 2), dtype=i32), torch.zeros(3, dtype=i32), torch.zeros(2, dtype=i32)
+    q, qr = torch.zeros((3, 4, 512), dtype=bf), torch.zeros((3, 4, 64), dtype=bf)
+    kv, w, cs = torch.zeros((3, 576), dtype=bf), torch.zeros(512), torch.zeros((9, 32, 2))
+    with pytest.raises(TypeError):
+        fp8bs.mla_cache_alloc(4, 16, "cpu", torch.float16)
+    for bad in (dict(q=q[..., :256]), dict(q=q[0]), dict(qr=qr[:2]), dict(qr=qr[:, :3]), dict(cache=fp8bs.MlaCache(
+            cache.latent[..., :256], cache.rope)), dict(cache=fp8bs.MlaCache(cache.latent, cache.rope[:3])),
+            dict(cache=fp8bs.MlaCache(cache.latent.view(torch.uint8)[..., :512], cache.rope)),
+            dict(cache=cache._replace(scale=torch.zeros(4, 16, 4))), dict(q=q), dict(table=table[0])):
+        a = {**dict(q=q, qr=qr, cache=cache, table=table, cu=cu, lens=lens), **bad}
+        with pytest.raises((ValueError, TypeError)):
+            out = torch.empty((3, 4, 512), dtype=bf)
+            fp8bs.fp8bs_mla_attention(a["q"], a["qr"], a["cache"], a["table"], a["cu"], a["lens"], 0.1, out, None, out)
+    for bad in (dict(kv=kv[:, :512]), dict(kv=kv[:2]), dict(w=w[:8]), dict(cs=cs[..., :1]), dict(qr=qr[..., :32])):
+        a = {**dict(qr=qr, kv=kv, w=w, cs=cs), **bad}
+        with pytest.raises((ValueError, TypeError)):
+            fp8bs.mla_cache_write(a["qr"], a["kv"], a["w"], 1e-6, a["cs"], cache, table, cu, lens)
+    with pytest.raises((ValueError, TypeError)):
+        fp8bs.cache_update(cache, table, lens, torch.zeros(3, dtype=i32), torch.zeros(3, dtype=i32))
+    with pytest.raises((ValueError, TypeError)):
+        fp8bs.cache_compact(cache, table, lens)
+
+
+def test_attention_listing_leaves_the_accumulators_alone(tmp_path):
+    """mla_attention.hip keeps its output accumulators in AGPRs that it names
+    itself; the compiler must put nothing of its own there, and spill nothing."""
+    from block_scaled_fp8_03_amd import build
+    out = tmp_path / "a.s"
+    cmd = [build.HIPCC, *build.COMMON_FLAGS, *build.HIP_FLAGS, *build.VGPR_FORM, "-x", "hip", "--cuda-device-only", "-S",
+           os.path.join(build.CSRC, "mla_attention.hip"), "-o", str(out)]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    inside, kernels = False, 0
+    for line in out.read_text().splitlines():
+        if "ASMSTART" in line:
+            inside = True
+        elif "ASMEND" in line:
+            inside = False
+        elif not inside and re.match(r"\s+[vdsgb]\w*_\w+\s", line):
+            assert not re.search(r"[ ,]a(\d|\[)", line.split(";")[0]), line
+            assert "scratch_" not in line, line
+        kernels += "s_endpgm" in line
+    assert kernels
