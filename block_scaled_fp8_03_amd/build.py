@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import os
+import re
 import subprocess
 import sys
 
@@ -37,12 +38,39 @@ HIP_FLAGS = [
 # accumulators per lane in AGPRs, so it is built without this.
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 AGPR_SOURCES = {"gemm_e8.hip"}
+# mla_attention.hip names its accumulator AGPRs in inline assembly; a build in
+# which the compiler uses AGPRs (or memory) for anything of its own is refused.
+OWN_AGPR_SOURCES = {"mla_attention.hip"}
+OWN_AGPR_FLAGS = ["-mllvm", "-amdgpu-spill-vgpr-to-agpr=0"]
+
+
+def check_listing(src: str, text: str) -> None:
+    """Raises if the listing of a source in OWN_AGPR_SOURCES touches an AGPR
+    outside inline assembly, or spills."""
+    inside = False
+    for line in text.splitlines():
+        if "#ASMSTART" in line or "#ASMEND" in line:
+            inside = "#ASMSTART" in line
+        elif not inside and re.match(r"\s+[vdsgb]\w*_\w+\s", line):
+            if re.search(r"[ ,]a(\d|\[)", line.split(";")[0]) or "scratch_" in line:
+                raise RuntimeError(f"{src}: the compiler uses registers that the kernel keeps for itself: {line.strip()}")
+
+
+def _listing(cmd, src: str) -> str:
+    res = subprocess.run([*cmd, "--cuda-device-only", "-S", os.path.join(CSRC, src), "-o", "-"], capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"compile failed: {src}\n{res.stderr}")
+    return res.stdout
 
 
 def _compile(src: str, build_dir: str) -> str:
     obj = os.path.join(build_dir, os.path.basename(src) + ".o")
     form = [] if src in AGPR_SOURCES else VGPR_FORM
-    cmd = [HIPCC, *COMMON_FLAGS, *HIP_FLAGS, *form, "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
+    own = OWN_AGPR_FLAGS if src in OWN_AGPR_SOURCES else []
+    cmd = [HIPCC, *COMMON_FLAGS, *HIP_FLAGS, *form, *own, "-x", "hip"]
+    if own:
+        check_listing(src, _listing(cmd, src))
+    cmd += ["-c", os.path.join(CSRC, src), "-o", obj]
     if src.endswith(".cpp"):
         cmd = [HIPCC, *COMMON_FLAGS, "--offload-arch=gfx950", "-c", os.path.join(CSRC, src), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)

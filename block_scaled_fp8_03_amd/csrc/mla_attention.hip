@@ -59,6 +59,7 @@ constexpr int kRopeB = kD * 2;
 constexpr int kLatB = kTok * kRowB;
 constexpr int kTileB = kLatB + kTok * kRopeB;   // 36,864 bytes
 constexpr float kLazy = 8.0f;
+constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 struct AttnParams {
@@ -74,8 +75,18 @@ struct AttnParams {
   float* lse;               // [T, H] or null
   int64_t ldq_t, ldq_h, ldr_t, ldr_h;
   float scale2;             // scale * log2(e)
+  // workspace: [grid] Meta, then [grid][2][M] lse (base 2), then [grid][2][M][512] normalised output parts
+  struct Meta* meta;
+  float* part_lse;
+  float* part_out;
   int T, H, B, W, P, ps;
   int causal, out_f32;
+};
+
+// what a workgroup leaves for the join: the row tile that it begins and does not finish
+struct Meta {
+  int64_t row;      // its first row of [T * H]
+  int rows, parts;  // parts = 0: none.  Part 0 is this workgroup's, part k the k-th next one's.
 };
 
 // The 16-byte chunk c of latent row t sits at slot c ^ lat_swz(t), and of
@@ -151,6 +162,12 @@ __device__ __forceinline__ void acc_reserve() {
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
+// four consecutive output values
+__device__ __forceinline__ void store4(const AttnParams& p, int64_t at, v4f v) {
+  if (p.out_f32) *reinterpret_cast<v4f*>(static_cast<float*>(p.out) + at) = v;
+  else *reinterpret_cast<v2u*>(static_cast<uint16_t*>(p.out) + at) = v2u{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
+}
+
 // a sequence of the batch; every field is clamped to what the buffers hold
 struct Seq {
   int q0, nq, len;
@@ -168,32 +185,194 @@ __device__ __forceinline__ int visible(const AttnParams& p, const Seq& s, int i)
   return p.causal ? clampi(s.len - s.nq + i + 1, 0, s.len) : s.len;
 }
 
+// exclusive prefix sum over the workgroup's 256 threads; total gets the sum
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();
+  if (lane == 63) sums[wave] = x;
+  __syncthreads();
+  int64_t base = 0;
+  total = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (k < wave) base += sums[k];
+    total += sums[k];
+  }
+  return base + x - v;
+}
+
+// ---------------------------------------------------------------------------
+// The work split.  The grid is one workgroup per CU, whatever the batch.  The
+// row tiles of all sequences, in order, cost kStart + (steps of 32 TW cached
+// tokens) each; the sum of the costs is cut into equal shares, and workgroup w
+// works through share w: the end of one tile's tokens, whole tiles, the
+// beginning of another's.  So long and short sequences, few rows and many, all
+// fill the card evenly, from lengths that only the device knows.  A tile that
+// several workgroups share is joined by join_kernel from at most two parts per
+// workgroup.  Every workgroup computes the split itself: two prefix sums, over
+// the sequences (row tiles) and over the row tiles (costs).
+// ---------------------------------------------------------------------------
+constexpr int kStart = 2;    // a tile's queries and output, in steps
+constexpr int kLeast = 4;    // a share is no smaller, so that short work is not cut to pieces
+
+struct Cut {          // a place between two steps
+  int tile;           // row tile of the batch
+  int b, in_seq;      // its sequence, its index there
+  int step;
+  int64_t end;        // costs up to the tile's end
+};
+
+// values that all lanes share, moved to scalar registers
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+__device__ __forceinline__ Cut uniform(const Cut& c) {
+  return Cut{uniform(c.tile), uniform(c.b), uniform(c.in_seq), uniform(c.step), uniform(c.end)};
+}
+
+template <int M, int STEP>
+struct Plan {
+  Cut lo, hi;
+  int64_t total;
+  int shares;
+
+  static __device__ int tile_cost(const AttnParams& p, const Seq& s, int in_seq) {
+    const int r = (int)min((int64_t)(in_seq + 1) * M, (int64_t)s.nq * p.H) - 1;
+    return kStart + (visible(p, s, r / p.H) + STEP - 1) / STEP;
+  }
+
+  // false: this workgroup has no share
+  __device__ bool make(const AttnParams& p, int w, uint8_t* smem) {
+    int64_t* sums = reinterpret_cast<int64_t*>(smem);
+    Cut* cut = reinterpret_cast<Cut*>(smem + 64);
+    int* first = reinterpret_cast<int*>(smem + 256);       // [B + 1] row tiles before each sequence
+    const int tid = threadIdx.x;
+    const int per_b = (p.B + 255) / 256;
+    const int b0 = min(tid * per_b, p.B), b1 = min(b0 + per_b, p.B);
+    int64_t mine = 0, sum;
+    for (int b = b0; b < b1; ++b) mine += ((int64_t)load_seq(p, b).nq * p.H + M - 1) / M;
+    int64_t at = block_scan(mine, sums, sum);
+    const int tiles = (int)sum;
+    for (int b = b0; b < b1; ++b) {
+      first[b] = (int)at;
+      at += ((int64_t)load_seq(p, b).nq * p.H + M - 1) / M;
+    }
+    if (tid == 0) first[p.B] = tiles;
+    __syncthreads();
+
+    const int per_t = (tiles + 255) / 256;
+    const int t0 = min(tid * per_t, tiles), t1 = min(t0 + per_t, tiles);
+    int b = 0;
+    for (int n = p.B; n > 1;) {                            // the last b with first[b] <= t0
+      const int half = n / 2;
+      if (first[b + half] <= t0) b += half;
+      n -= half;
+    }
+    mine = 0;
+    const int bs = b;
+    Seq s = load_seq(p, b);
+    for (int t = t0; t < t1; ++t) {
+      while (t >= first[b + 1]) s = load_seq(p, ++b);
+      mine += tile_cost(p, s, t - first[b]);
+    }
+    int64_t base = block_scan(mine, sums, total);
+    shares = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kLeast));
+    if (w >= shares || total == 0) return false;
+
+    const int64_t want[2] = {total * w / shares, total * (w + 1) / shares};
+    if (t1 == tiles && t0 < t1 && want[1] == total) cut[1] = Cut{tiles, p.B, 0, 0, total};
+    if (t0 < t1 && ((want[0] >= base && want[0] < base + mine) || (want[1] >= base && want[1] < base + mine))) {
+      b = bs;
+      s = load_seq(p, b);
+      for (int t = t0; t < t1; ++t) {
+        while (t >= first[b + 1]) s = load_seq(p, ++b);
+        const int c = tile_cost(p, s, t - first[b]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (want[k] >= base && want[k] < base + c)
+            cut[k] = Cut{t, b, t - first[b], max(0, (int)(want[k] - base) - kStart), base + c};
+        base += c;
+      }
+    }
+    __syncthreads();
+    lo = uniform(cut[0]);
+    hi = uniform(cut[1]);
+    total = uniform(total);
+    shares = uniform(shares);
+    __syncthreads();
+    return true;
+  }
+};
+
+// the next sequence after b that has new tokens (there is one)
+__device__ __forceinline__ int next_seq(const AttnParams& p, int b) {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  for (++b; b < p.B; b += 64) {
+    const uint64_t some = __ballot(b + lane < p.B && load_seq(p, min(b + lane, p.B - 1)).nq > 0);
+    if (some) return b + __ffsll((unsigned long long)some) - 1;
+  }
+  return p.B - 1;
+}
+
 template <int RT, int RW, int TW, bool FP8>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 mla_attention_kernel(AttnParams p) {
-  constexpr int M = 16 * RT * RW;
+  constexpr int M = 16 * RT * RW, STEP = kTok * TW;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[std::max(kTileB * TW, TW > 1 ? 4 * 16 * kR * 4 : 0)];
   const int lane = threadIdx.x & 63;
   const int n = lane & 15, g = lane >> 4;
-  const int wave = threadIdx.x >> 6;
+  const int wave = uniform((int)threadIdx.x >> 6);
   const int rw = wave % RW, tw = wave / RW;
   uint8_t* const tile = smem + tw * kTileB;
 
-  // this workgroup's row tile
-  int b = 0, rt0 = blockIdx.x;
-  Seq sq;
-  for (;; ++b) {
-    if (b >= p.B) return;
-    sq = load_seq(p, b);
-    const int64_t nrt = ((int64_t)sq.nq * p.H + M - 1) / M;
-    if (rt0 < nrt) break;
-    rt0 -= (int)nrt;
+  // neighbouring shares on one XCD (workgroups go round the eight): they often stream the same tokens
+  const int w = gridDim.x % 8 == 0 ? (blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8 : blockIdx.x;
+  if (threadIdx.x == 0) p.meta[w].parts = 0;
+  Plan<M, STEP> plan;
+  if (!plan.make(p, w, smem)) return;
+
+  // The operand reads' LDS addresses.  A latent chunk's swizzle touches the low
+  // four bits of its index alone, so K steps k, k + 4, .. and channel tiles
+  // ct, ct + 8, .. share a base, and both halves of the 32 tokens do.
+  const uint32_t tile_at = lds_at(tile);
+  uint32_t kat[4], kro[2], vat[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) kat[k] = tile_at + n * kRowB + (((4 * k + g) ^ lat_swz(n)) << 4);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) kro[k] = tile_at + kLatB + n * kRopeB + (((4 * k + g) ^ rope_swz(n)) << 4);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int t = 4 * g + (n >> 2);                  // the lane points at this token, 4 channels from 4 (n % 4)
+    vat[k] = tile_at + t * kRowB + (((2 * k + ((n & 3) >> 1)) ^ lat_swz(t)) << 4) + ((n & 1) << 3);
   }
+  acc_reserve<RT>();
+
+  int b = plan.lo.b, in_seq = plan.lo.in_seq, step0 = plan.lo.step;
+  for (int j = plan.lo.tile; j < plan.hi.tile || (j == plan.hi.tile && plan.hi.step > 0); ++j, step0 = 0) {
+  if (j > plan.lo.tile) {
+    ++in_seq;
+    if ((int64_t)in_seq * M >= (int64_t)load_seq(p, b).nq * p.H) {
+      b = uniform(next_seq(p, b));
+      in_seq = 0;
+    }
+  }
+  const Seq sq = load_seq(p, b);
   const int rows = sq.nq * p.H;
-  const int r_tile = rt0 * M;
+  const int r_tile = in_seq * M;
   const int r_last = min(r_tile + M, rows) - 1;
   const int end_max = visible(p, sq, r_last / p.H);
   const int end_min = visible(p, sq, r_tile / p.H);
+  const int steps = (end_max + STEP - 1) / STEP;
+  const int step1 = j == plan.hi.tile ? plan.hi.step : steps;
+  const bool whole = step0 == 0 && step1 == steps;
 
   // query rows of this wave: their operands, and the tokens they see
   v8bf q[RT][kSteps];
@@ -216,38 +395,24 @@ mla_attention_kernel(AttnParams p) {
     m[rt] = kNegInf;
     l[rt] = 0.0f;
   }
-  acc_reserve<RT>();
   unroll<RT * kCt>([&](auto i) { acc_write<i>(v4f{0.0f, 0.0f, 0.0f, 0.0f}); });
 
-  // The operand reads' LDS addresses.  A latent chunk's swizzle touches the low
-  // four bits of its index alone, so K steps k, k + 4, .. and channel tiles
-  // ct, ct + 8, .. share a base, and both halves of the 32 tokens do.
-  const uint32_t tile_at = lds_at(tile);
-  uint32_t kat[4], kro[2], vat[8];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) kat[k] = tile_at + n * kRowB + (((4 * k + g) ^ lat_swz(n)) << 4);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) kro[k] = tile_at + kLatB + n * kRopeB + (((4 * k + g) ^ rope_swz(n)) << 4);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int t = 4 * g + (n >> 2);                  // the lane points at this token, 4 channels from 4 (n % 4)
-    vat[k] = tile_at + t * kRowB + (((2 * k + ((n & 3) >> 1)) ^ lat_swz(t)) << 4) + ((n & 1) << 3);
-  }
-
   const int32_t* trow = p.table + (int64_t)b * p.W;
-  for (int t0 = 0; t0 < end_max; t0 += kTok * TW) {
+  for (int t0 = step0 * STEP; t0 < step1 * STEP; t0 += STEP) {
     const int tb = t0 + tw * kTok;                   // first token of this wave
     __syncthreads();
+    int ln = lane;                                   // opaque, so that addresses are not kept over the loop
+    asm volatile("" : "+v"(ln));
     // Lane j < 32 finds token tb + j; tokens past the last visible one load that one again,
     // so masked places hold finite values and nothing behind the sequence is read.
-    const int tok = min(tb + (lane & 31), end_max - 1);
+    const int tok = min(tb + (ln & 31), end_max - 1);
     const int pg = clampi(trow[(uint32_t)tok / (uint32_t)p.ps], 0, p.P - 1);
     const int64_t row = (int64_t)pg * p.ps + (uint32_t)tok % (uint32_t)p.ps;
     const int row_lo = (int)row;                     // P * ps < 2^31
     if (FP8) {
-#pragma unroll 4
+#pragma unroll 2
       for (int i = 0; i < kTok / 2 / RW; ++i) {
-        const int t = 2 * (i * RW + rw) + (lane >> 5), c = lane & 31;
+        const int t = 2 * (i * RW + rw) + (ln >> 5), c = ln & 31;
         const int64_t src = __shfl(row_lo, t);
         const v4u w = *reinterpret_cast<const v4u*>(p.latent + src * kR + 16 * c);
         const float sc = p.lat_scale[src * (kR / 128) + (c >> 3)];
@@ -256,17 +421,17 @@ mla_attention_kernel(AttnParams p) {
         *reinterpret_cast<v4u*>(dst + (((2 * c + 1) ^ lat_swz(t)) << 4)) = __builtin_bit_cast(v4u, dequant8_bf16(w.z, w.w, sc));
       }
     } else {
-#pragma unroll 8
+#pragma unroll 4
       for (int i = 0; i < kTok / RW; ++i) {
         const int t = i * RW + rw;
         const int64_t src = __shfl(row_lo, t);
-        const v4u w = *reinterpret_cast<const v4u*>(p.latent + src * kRowB + 16 * lane);
-        *reinterpret_cast<v4u*>(tile + t * kRowB + ((lane ^ lat_swz(t)) << 4)) = w;
+        const v4u w = *reinterpret_cast<const v4u*>(p.latent + src * kRowB + 16 * ln);
+        *reinterpret_cast<v4u*>(tile + t * kRowB + ((ln ^ lat_swz(t)) << 4)) = w;
       }
     }
 #pragma unroll
     for (int i = 0; i < kTok / 8 / RW; ++i) {
-      const int t = 8 * (i * RW + rw) + (lane >> 3), c = lane & 7;
+      const int t = 8 * (i * RW + rw) + (ln >> 3), c = ln & 7;
       const int64_t src = __shfl(row_lo, t);
       const v4u w = *reinterpret_cast<const v4u*>(reinterpret_cast<const uint8_t*>(p.rope) + src * kRopeB + 16 * c);
       *reinterpret_cast<v4u*>(tile + kLatB + t * kRopeB + ((c ^ rope_swz(t)) << 4)) = w;
@@ -331,7 +496,7 @@ mla_attention_kernel(AttnParams p) {
   unroll<RT>([&](auto rt) {
     l[rt] += __shfl_xor(l[rt], 16);
     l[rt] += __shfl_xor(l[rt], 32);
-    float w = 1.0f;
+    float part = 1.0f;                               // this token wave's weight
     float mt = m[rt], lt = l[rt];
     if constexpr (TW > 1) {
       __syncthreads();
@@ -348,46 +513,109 @@ mla_attention_kernel(AttnParams p) {
         const float mk = red[(k * RW + rw) * 32 + n];
         if (mk > kNegInf) lt += red[(k * RW + rw) * 32 + 16 + n] * __builtin_amdgcn_exp2f(mk - mt);
       }
-      w = m[rt] > kNegInf ? __builtin_amdgcn_exp2f(m[rt] - mt) : 0.0f;
+      part = m[rt] > kNegInf ? __builtin_amdgcn_exp2f(m[rt] - mt) : 0.0f;
       __syncthreads();
       float* ow = red + wave * 16 * kR;
       unroll<kCt>([&](auto ct) {
-        const v4f v = acc_read<kCt * rt + ct>() * w;
+        const v4f v = acc_read<kCt * rt + ct>() * part;
 #pragma unroll
         for (int e = 0; e < 4; ++e) ow[(16 * ct + 4 * g + e) * 16 + n] = v[e];
       });
       __syncthreads();
     }
     // token wave tw adds and stores the channel tiles tw kCt / TW ..
-    const int r = r_tile + (rw * RT + rt) * 16 + n;
-    if (r <= r_last) {
+    const int r = (rw * RT + rt) * 16 + n;           // row of the tile
+    if (r_tile + r <= r_last) {
       const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
-      const int64_t orow = (int64_t)sq.q0 * p.H + r;
-      if (tw == 0 && g == 0 && p.lse)
-        p.lse[orow] = lt > 0.0f ? (mt + __builtin_log2f(lt)) * 0.693147180559945309f : kNegInf;
-      unroll<kCt / TW>([&](auto i) {
-        const int ct = tw * (kCt / TW) + i;
-        v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (TW > 1) {
+      const float lse = lt > 0.0f ? mt + __builtin_log2f(lt) : kNegInf;
+      const int64_t orow = (int64_t)sq.q0 * p.H + r_tile + r;
+      const int64_t prow = (2 * (int64_t)w + (step0 == 0)) * M + r;
+      if (tw == 0 && g == 0) {
+        if (!whole) p.part_lse[prow] = lse;
+        else if (p.lse) p.lse[orow] = lse * kLn2;
+      }
+      auto put = [&](int ct, v4f v) {
+        v *= inv;
+        const int c = 16 * ct + 4 * g;
+        if (!whole) *reinterpret_cast<v4f*>(p.part_out + prow * kR + c) = v;
+        else store4(p, orow * kR + c, v);
+      };
+      if constexpr (TW > 1) {
+#pragma unroll 2
+        for (int ct = tw * (kCt / TW); ct < (tw + 1) * (kCt / TW); ++ct) {
+          v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int k = 0; k < TW; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] += red[(k * RW + rw) * 16 * kR + (16 * ct + 4 * g + e) * 16 + n];
-        } else {
-          v = acc_read<kCt * rt + i>();
+          put(ct, v);
         }
-        v *= inv;
-        const int64_t at = orow * kR + 16 * ct + 4 * g;
-        if (p.out_f32) *reinterpret_cast<v4f*>(static_cast<float*>(p.out) + at) = v;
-        else *reinterpret_cast<v2u*>(static_cast<uint16_t*>(p.out) + at) = v2u{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
-      });
+      } else {
+        unroll<kCt>([&](auto ct) { put(ct, acc_read<kCt * rt + ct>()); });
+      }
     }
   });
+  if (threadIdx.x == 0 && step0 == 0 && !whole) {
+    // the share that reaches the tile's end is the first whose own end is not before it
+    const int64_t last = (plan.hi.end * plan.shares + plan.total - 1) / plan.total - 1;
+    p.meta[w] = Meta{(int64_t)sq.q0 * p.H + r_tile, r_last - r_tile + 1, (int)last - w + 1};
+  }
+  }
 }
+
+// Joins the parts of a split row tile: a wave per row, eight channels a lane;
+// weights 2^(lse_k - max).  Reads what the parts' workgroups wrote (mostly
+// still in the caches), writes the output once.
+template <int M>
+__global__ void __launch_bounds__(256) join_kernel(AttnParams p) {
+  const int w = blockIdx.x;
+  const Meta meta = p.meta[w];
+  const int r = blockIdx.y * 4 + (threadIdx.x >> 6);
+  if (meta.parts == 0 || r >= meta.rows) return;
+  const int lane = threadIdx.x & 63;
+  // part 0 is slot 1 of workgroup w, part k slot 0 of w + k
+  auto at = [&](int k) { return (k == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + k)) * M + r; };
+  float top = kNegInf;
+  for (int k = lane; k < meta.parts; k += 64) top = fmaxf(top, p.part_lse[at(k)]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  const float base = top == kNegInf ? 0.0f : top;
+  float sum = 0.0f;
+  v4f lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
+  for (int k0 = 0; k0 < meta.parts; k0 += 64) {
+    const int have = min(64, meta.parts - k0);
+    const float mine = lane < have ? __builtin_amdgcn_exp2f(p.part_lse[at(k0 + lane)] - base) : 0.0f;
+    for (int k = 0; k < have; k += 4)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {                  // lanes from `have` on hold weight 0
+        const float x = bits_f32(__builtin_amdgcn_readlane(f32_bits(mine), k + u));
+        const float* src = p.part_out + at(k0 + min(k + u, have - 1)) * kR + 4 * lane;
+        lo += *reinterpret_cast<const v4f*>(src) * x;
+        hi += *reinterpret_cast<const v4f*>(src + kR / 2) * x;
+        sum += x;
+      }
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const int64_t orow = meta.row + r;
+  store4(p, orow * kR + 4 * lane, lo * inv);
+  store4(p, orow * kR + kR / 2 + 4 * lane, hi * inv);
+  if (lane == 0 && p.lse) p.lse[orow] = sum > 0.0f ? (top + __builtin_log2f(sum)) * kLn2 : kNegInf;
+}
+
+// rows of an average sequence decide the tile
+int tile_rows(int64_t T, int64_t H, int64_t B) {
+  const int64_t per = T * H / B;
+  return per >= 96 ? 128 : per >= 48 ? 64 : per >= 24 ? 32 : 16;
+}
+constexpr int kGrid = 256;    // the MI355X's CUs
+
+constexpr int64_t part_bytes(int m) { return (int64_t)kGrid * 2 * m * (kR + 1) * 4; }
 
 }  // namespace
 
-int64_t mla_attention_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+int64_t mla_attention_workspace_bytes(int64_t T, int64_t H, int64_t B) {
+  return kGrid * (int64_t)sizeof(Meta) + part_bytes(tile_rows(T, H, B));
+}
 
 hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
   AttnParams p{};
@@ -414,24 +642,22 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
   p.ps = (int)a.ps;
   p.causal = a.causal;
   p.out_f32 = a.out_f32;
-  // rows of an average sequence decide the tile
-  const int64_t rows = a.T * a.H, per = rows / a.B;
-#define FP8BS_ATTN(RT_, RW_, TW_, F8_)                                                          \
-  {                                                                                             \
-    constexpr int M_ = 16 * RT_ * RW_;                                                          \
-    const dim3 grid((unsigned)((rows + M_ - 1) / M_ + a.B));                                    \
-    hipLaunchKernelGGL((mla_attention_kernel<RT_, RW_, TW_, F8_>), grid, dim3(256), 0, stream, p); \
+  const int m = tile_rows(a.T, a.H, a.B);
+  p.meta = static_cast<Meta*>(a.workspace);
+  p.part_lse = reinterpret_cast<float*>(p.meta + kGrid);
+  p.part_out = p.part_lse + (int64_t)kGrid * 2 * m;
+#define FP8BS_ATTN(RT_, RW_, TW_)                                                                              \
+  case 16 * RT_ * RW_:                                                                                         \
+    if (a.fp8) hipLaunchKernelGGL((mla_attention_kernel<RT_, RW_, TW_, true>), dim3(kGrid), dim3(256), 0, stream, p); \
+    else hipLaunchKernelGGL((mla_attention_kernel<RT_, RW_, TW_, false>), dim3(kGrid), dim3(256), 0, stream, p); \
+    hipLaunchKernelGGL(join_kernel<16 * RT_ * RW_>, dim3(kGrid, 4 * RT_ * RW_), dim3(256), 0, stream, p); \
+    break;
+  switch (m) {
+    FP8BS_ATTN(2, 4, 1)
+    FP8BS_ATTN(2, 2, 2)
+    FP8BS_ATTN(2, 1, 4)
+    default: FP8BS_ATTN(1, 1, 4)
   }
-#define FP8BS_ATTN_F(RT_, RW_, TW_)            \
-  {                                            \
-    if (a.fp8) FP8BS_ATTN(RT_, RW_, TW_, true) \
-    else FP8BS_ATTN(RT_, RW_, TW_, false)      \
-  }
-  if (per >= 96) FP8BS_ATTN_F(2, 4, 1)
-  else if (per >= 48) FP8BS_ATTN_F(2, 2, 2)
-  else if (per >= 24) FP8BS_ATTN_F(2, 1, 4)
-  else FP8BS_ATTN_F(1, 1, 4)
-#undef FP8BS_ATTN_F
 #undef FP8BS_ATTN
   return hipGetLastError();
 }

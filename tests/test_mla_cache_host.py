@@ -2,10 +2,7 @@
 before any HIP call (the addresses below are never touched), and the binding
 refuses tensors that do not fit.  Also that the attention kernel's listing
 leaves the accumulator registers to the kernel."""
-import ctypes
 import os
-import re
-import subprocess
 
 import pytest
 import torch
@@ -58,8 +55,6 @@ def test_shared_refusals(L, name, base, floats):
     assert call(f, base, fmt=1) == NULL                       # codes without scales
     assert call(f, base, fmt=1, scale=A[15] + 4) == ALIGN
     for k in floats:
-        if k == "ws" and name == "fp8bs_mla_attention" and L.fp8bs_mla_attention_workspace_size(4, 4, 2) == 0:
-            continue
         assert call(f, base, **{k: None}) == NULL, k
         assert call(f, base, **{k: base[k] + 8}) == ALIGN, k
     for k in ("table", "lens"):
@@ -95,14 +90,13 @@ def test_attention_refusals(L):
     assert call(f, ATTN, cu=None) == NULL
     need = ws(4, 4, 2)
     for kw in (dict(out=A[0] + 64), dict(lse=A[1]), dict(out=A[2]), dict(lse=A[7] + 16), dict(out=A[4]),
-               *([dict(ws=A[7]), dict(ws=A[3] + 16)] if need else [])):
+               dict(ws=A[7]), dict(ws=A[3] + 16)):
         assert call(f, ATTN, **kw) == ALIAS, kw
     assert call(f, ATTN, T=0, q=None, out=None) == OK
     assert call(f, ATTN, B=0) == OK
     assert ws(-1, 4, 2) == ws(4, 0, 2) == ws(4, 4, -1) == ws(1 << 24, 128, 2) == ws(4, 4, 8193) == -1
     assert ws(0, 4, 2) == ws(4, 4, 0) == 0
-    if need:
-        assert call(f, ATTN, nws=need - 1) == SHAPE
+    assert call(f, ATTN, nws=need - 1) == SHAPE
 
 
 def test_update_and_compact_refusals(L):
@@ -153,23 +147,14 @@ def test_binding_refusals():
         fp8bs.cache_compact(cache, table, lens)
 
 
-def test_attention_listing_leaves_the_accumulators_alone(tmp_path):
-    """mla_attention.hip keeps its output accumulators in AGPRs that it names
-    itself; the compiler must put nothing of its own there, and spill nothing."""
+def test_listing_check():
+    """The build refuses an attention kernel whose compiler-made instructions
+    touch AGPRs (the accumulators live there, named in inline assembly) or spill."""
     from block_scaled_fp8_03_amd import build
-    out = tmp_path / "a.s"
-    cmd = [build.HIPCC, *build.COMMON_FLAGS, *build.HIP_FLAGS, *build.VGPR_FORM, "-x", "hip", "--cuda-device-only", "-S",
-           os.path.join(build.CSRC, "mla_attention.hip"), "-o", str(out)]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    assert res.returncode == 0, res.stderr
-    inside, kernels = False, 0
-    for line in out.read_text().splitlines():
-        if "ASMSTART" in line:
-            inside = True
-        elif "ASMEND" in line:
-            inside = False
-        elif not inside and re.match(r"\s+[vdsgb]\w*_\w+\s", line):
-            assert not re.search(r"[ ,]a(\d|\[)", line.split(";")[0]), line
-            assert "scratch_" not in line, line
-        kernels += "s_endpgm" in line
-    assert kernels
+    asm = "\t;;#ASMSTART\n\tv_accvgpr_read_b32 v1, a[0x41]\n\t;;#ASMEND\n"
+    build.check_listing("x", asm + "\tv_add_f32_e32 v1, v2, v3\n\ts_add_i32 s1, s2, s3\n")
+    for line in ("\tv_accvgpr_write_b32 a3, v1", "\tv_mfma_f32_16x16x32_bf16 a[0:3], v[0:3], v[4:7], a[0:3]",
+                 "\tscratch_store_dword off, v1, s0", "\tds_read_b128 a[4:7], v1"):
+        with pytest.raises(RuntimeError):
+            build.check_listing("x", asm + line + "\n")
+    assert "mla_attention.hip" in build.OWN_AGPR_SOURCES
