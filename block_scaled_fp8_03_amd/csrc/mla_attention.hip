@@ -58,6 +58,8 @@ constexpr int kRowB = kR * 2;           // bytes of a latent row in LDS
 constexpr int kRopeB = kD * 2;
 constexpr int kLatB = kTok * kRowB;
 constexpr int kTileB = kLatB + kTok * kRopeB;   // 36,864 bytes
+constexpr int kCodeB = kTok * kR;                // the same 32 tokens of an FP8 cache as they come:
+constexpr int kRawB = kCodeB + kTok * kRopeB + 1024;   // codes, rope, scales (512 bytes, written twice)
 constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -75,6 +77,8 @@ struct AttnParams {
   float* lse;               // [T, H] or null
   int64_t ldq_t, ldq_h, ldr_t, ldr_h;
   float scale2;             // scale * log2(e)
+  uint32_t ps_mul;          // tok / ps = tok * ps_mul >> ps_shift for tok < 2^31
+  int ps_shift;
   // workspace: [grid] Meta, then [grid][2][M] lse (base 2), then [grid][2][M][512] normalised output parts
   struct Meta* meta;
   float* part_lse;
@@ -183,6 +187,31 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
 // cached tokens that query token i of a sequence sees
 __device__ __forceinline__ int visible(const AttnParams& p, const Seq& s, int i) {
   return p.causal ? clampi(s.len - s.nq + i + 1, 0, s.len) : s.len;
+}
+
+// Direct global -> LDS loads, 16 bytes a lane: lane i's bytes land at lds + 16 i.
+// In assembly, so that the compiler does not make every LDS read wait for all
+// of them; completion is awaited with wait_vmcnt.
+__device__ __forceinline__ void dma_row(const void* base, uint32_t off, uint32_t lds) {
+  // five wait states, should a VALU instruction have written the base's scalar registers just before
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma_lanes(const void* at, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(at) : "memory", "m0");
+}
+template <int n>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(n >= 0 && n < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
+  asm volatile("" ::: "memory");
+}
+// workgroup barrier that orders LDS accesses only
+__device__ __forceinline__ void barrier_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // exclusive prefix sum over the workgroup's 256 threads; total gets the sum
@@ -322,16 +351,33 @@ __device__ __forceinline__ int next_seq(const AttnParams& p, int b) {
   return p.B - 1;
 }
 
+// Stages of cached tokens under way per token wave, and LDS: with one stage (RW
+// = 1) every wave loads, waits and computes by itself, no barrier, the waves
+// covering each other's waits; else a ring of ST stages.  An FP8 cache's codes
+// come in as they are and are spread to bf16 in LDS once for all row waves;
+// with RW = 1 they wait in registers.
+template <int RW, int TW, bool FP8>
+constexpr int stages() { return RW == 1 ? 1 : TW == 1 ? 4 : 2; }
+template <int RW, int TW, bool FP8>
+constexpr int lds_bytes() {
+  constexpr int st = stages<RW, TW, FP8>();
+  constexpr int n = FP8 ? TW * (kTileB + (RW == 1 ? 0 : st * kRawB)) : TW * st * kTileB;
+  return TW > 1 ? std::max(n, 4 * 16 * kR * 4) : n;   // the token waves' accumulators meet here
+}
+
 template <int RT, int RW, int TW, bool FP8>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 mla_attention_kernel(AttnParams p) {
   constexpr int M = 16 * RT * RW, STEP = kTok * TW;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[std::max(kTileB * TW, TW > 1 ? 4 * 16 * kR * 4 : 0)];
+  constexpr int ST = stages<RW, TW, FP8>();
+  static_assert(RW * TW == 4 && lds_bytes<RW, TW, FP8>() <= 160 * 1024, "layout");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[lds_bytes<RW, TW, FP8>()];
   const int lane = threadIdx.x & 63;
   const int n = lane & 15, g = lane >> 4;
   const int wave = uniform((int)threadIdx.x >> 6);
   const int rw = wave % RW, tw = wave / RW;
-  uint8_t* const tile = smem + tw * kTileB;
+  uint8_t* const tile = smem + tw * (FP8 ? 1 : ST) * kTileB;               // bf16 tiles of this token wave
+  uint8_t* const raw = smem + TW * kTileB + tw * ST * kRawB;               // FP8: its stages
 
   // neighbouring shares on one XCD (workgroups go round the eight): they often stream the same tokens
   const int w = gridDim.x % 8 == 0 ? (blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8 : blockIdx.x;
@@ -397,46 +443,147 @@ mla_attention_kernel(AttnParams p) {
   }
   unroll<RT * kCt>([&](auto i) { acc_write<i>(v4f{0.0f, 0.0f, 0.0f, 0.0f}); });
 
+  // The pages of 64 consecutive table entries, one a lane, from entry pbase on.
+  // A wave reloads them when it comes to their end (every 64 pages).
   const int32_t* trow = p.table + (int64_t)b * p.W;
-  for (int t0 = step0 * STEP; t0 < step1 * STEP; t0 += STEP) {
-    const int tb = t0 + tw * kTok;                   // first token of this wave
-    __syncthreads();
-    int ln = lane;                                   // opaque, so that addresses are not kept over the loop
+  const int last = end_max - 1;
+  int pages = 0, pbase = -64;
+  // The cache row of token min(tb + lane % 32, last): a token behind the last visible one is that one
+  // again, so masked places hold finite values and nothing behind the sequence is read.
+  auto rows_of = [&](int tb) {
+    int ln = lane & 31;
+    asm volatile("" : "+v"(ln));                     // so that addresses are not kept over the loop
+    const uint32_t tok = (uint32_t)min(tb + ln, last);
+    const int at = (int)((uint64_t)tok * p.ps_mul >> p.ps_shift);
+    const int lo = uniform(at), hi = __builtin_amdgcn_readlane(at, 31);
+    if (lo < pbase || hi >= pbase + 64) {
+      pbase = lo;
+      const int most = (int)((uint64_t)(uint32_t)last * p.ps_mul >> p.ps_shift);
+      pages = clampi(trow[min(pbase + (int)(threadIdx.x & 63), most)], 0, p.P - 1);
+    }
+    return __shfl(pages, at - pbase) * p.ps + (int)(tok - (uint32_t)at * (uint32_t)p.ps);   // P * ps < 2^31
+  };
+  // 32 tokens from tb on, this wave's share of the RW waves, to LDS
+  auto fetch = [&](int tb, uint8_t* to) {
+    const int row = rows_of(tb);
+    int ln = lane;
     asm volatile("" : "+v"(ln));
-    // Lane j < 32 finds token tb + j; tokens past the last visible one load that one again,
-    // so masked places hold finite values and nothing behind the sequence is read.
-    const int tok = min(tb + (ln & 31), end_max - 1);
-    const int pg = clampi(trow[(uint32_t)tok / (uint32_t)p.ps], 0, p.P - 1);
-    const int64_t row = (int64_t)pg * p.ps + (uint32_t)tok % (uint32_t)p.ps;
-    const int row_lo = (int)row;                     // P * ps < 2^31
-    if (FP8) {
-#pragma unroll 2
+    const uint32_t at = lds_at(to);
+    if constexpr (FP8) {
+#pragma unroll
       for (int i = 0; i < kTok / 2 / RW; ++i) {
-        const int t = 2 * (i * RW + rw) + (ln >> 5), c = ln & 31;
-        const int64_t src = __shfl(row_lo, t);
-        const v4u w = *reinterpret_cast<const v4u*>(p.latent + src * kR + 16 * c);
-        const float sc = p.lat_scale[src * (kR / 128) + (c >> 3)];
-        uint8_t* dst = tile + t * kRowB;
-        *reinterpret_cast<v4u*>(dst + (((2 * c) ^ lat_swz(t)) << 4)) = __builtin_bit_cast(v4u, dequant8_bf16(w.x, w.y, sc));
-        *reinterpret_cast<v4u*>(dst + (((2 * c + 1) ^ lat_swz(t)) << 4)) = __builtin_bit_cast(v4u, dequant8_bf16(w.z, w.w, sc));
+        const int t = 2 * (i * RW + rw);
+        const int64_t src = __shfl(row, t + (ln >> 5));
+        dma_lanes(p.latent + src * kR + 16 * (ln & 31), at + t * kR);
       }
+      const int64_t src = __shfl(row, ln & 31);
+      dma_lanes(p.lat_scale + src * (kR / 128), at + kCodeB + kTok * kRopeB);
     } else {
-#pragma unroll 4
+#pragma unroll
       for (int i = 0; i < kTok / RW; ++i) {
         const int t = i * RW + rw;
-        const int64_t src = __shfl(row_lo, t);
-        const v4u w = *reinterpret_cast<const v4u*>(p.latent + src * kRowB + 16 * ln);
-        *reinterpret_cast<v4u*>(tile + t * kRowB + ((ln ^ lat_swz(t)) << 4)) = w;
+        const int64_t src = __builtin_amdgcn_readlane(row, t);
+        dma_row(p.latent + src * kRowB, (uint32_t)(ln ^ lat_swz(t)) << 4, at + t * kRowB);
       }
     }
 #pragma unroll
     for (int i = 0; i < kTok / 8 / RW; ++i) {
-      const int t = 8 * (i * RW + rw) + (ln >> 3), c = ln & 7;
-      const int64_t src = __shfl(row_lo, t);
-      const v4u w = *reinterpret_cast<const v4u*>(reinterpret_cast<const uint8_t*>(p.rope) + src * kRopeB + 16 * c);
-      *reinterpret_cast<v4u*>(tile + kLatB + t * kRopeB + ((c ^ rope_swz(t)) << 4)) = w;
+      const int t = 8 * (i * RW + rw) + (ln >> 3);
+      const int64_t src = __shfl(row, t);
+      const int c = (ln & 7) ^ (FP8 ? 0 : rope_swz(t));
+      dma_lanes(p.rope + src * kD + 8 * c, at + (FP8 ? kCodeB : kLatB) + 8 * (i * RW + rw) * kRopeB);
     }
-    __syncthreads();
+  };
+  constexpr int NB = (FP8 ? kTok / 2 / RW + 1 : kTok / RW) + kTok / 8 / RW;   // loads of a fetch
+  // 16 codes to 32 bytes of bf16, exactly (power-of-two scales), at chunks 2c and 2c + 1 of token t
+  auto spread = [&](int t, int c, v4u codes, float sc) {
+    uint8_t* dst = tile + t * kRowB;
+    *reinterpret_cast<v4u*>(dst + (((2 * c) ^ lat_swz(t)) << 4)) = __builtin_bit_cast(v4u, dequant8_bf16(codes.x, codes.y, sc));
+    *reinterpret_cast<v4u*>(dst + (((2 * c + 1) ^ lat_swz(t)) << 4)) = __builtin_bit_cast(v4u, dequant8_bf16(codes.z, codes.w, sc));
+  };
+  // FP8, RW = 1: the tile in registers
+  v4u code_reg[kTok / 2], rope_reg[kTok / 8];
+  float scale_reg[kTok / 2];
+  auto fetch_regs = [&](int tb) {
+    const int row = rows_of(tb);
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+#pragma unroll
+    for (int i = 0; i < kTok / 2; ++i) {
+      const int64_t src = __shfl(row, 2 * i + (ln >> 5));
+      code_reg[i] = *reinterpret_cast<const v4u*>(p.latent + src * kR + 16 * (ln & 31));
+      scale_reg[i] = p.lat_scale[src * (kR / 128) + ((ln & 31) >> 3)];
+    }
+#pragma unroll
+    for (int i = 0; i < kTok / 8; ++i) {
+      const int64_t src = __shfl(row, 8 * i + (ln >> 3));
+      rope_reg[i] = *reinterpret_cast<const v4u*>(p.rope + src * kD + 8 * (ln & 7));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  const int n_steps = step1 - step0;
+  const int t_seg = step0 * STEP + tw * kTok;        // this wave's first token
+  __syncthreads();                                   // the last tile's LDS is no longer read
+  if constexpr (RW > 1) {
+    wait_vmcnt<0>();
+    for (int k = 0; k < (FP8 ? ST : ST - 1) && k < n_steps; ++k)
+      fetch(t_seg + k * STEP, FP8 ? raw + k * kRawB : tile + k * kTileB);
+  } else if constexpr (FP8) {
+    if (t_seg < end_max && n_steps > 0) fetch_regs(t_seg);
+  }
+  int slot = 0;
+  for (int k = 0; k < n_steps; ++k) {
+    const int tb = t_seg + k * STEP;                 // first token of this wave
+    uint32_t slot_at = 0;
+    if constexpr (RW > 1 && !FP8) {
+      if (k + ST - 1 < n_steps) wait_vmcnt<(ST - 2) * NB>();
+      else wait_vmcnt<0>();
+      barrier_lds();                                 // everyone's share of tile k is here, tile k - 1 is done with
+      if (k + ST - 1 < n_steps) fetch(tb + (ST - 1) * STEP, tile + (slot == 0 ? ST - 1 : slot - 1) * kTileB);
+      slot_at = slot * kTileB;
+      slot = slot + 1 == ST ? 0 : slot + 1;
+    } else if constexpr (RW > 1) {
+      if (k + ST - 1 < n_steps) wait_vmcnt<(ST - 1) * NB>();
+      else wait_vmcnt<0>();
+      barrier_lds();
+      const uint8_t* from = raw + slot * kRawB;
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+#pragma unroll 4
+      for (int i = 0; i < kTok / 2 / RW; ++i) {
+        const int t = 2 * (i * RW + rw) + (ln >> 5), c = ln & 31;
+        const v4u w = *reinterpret_cast<const v4u*>(from + t * kR + 16 * c);
+        const float sc = reinterpret_cast<const float*>(from + kCodeB + kTok * kRopeB)[t * (kR / 128) + (c >> 3)];
+        spread(t, c, w, sc);
+      }
+#pragma unroll
+      for (int i = 0; i < kTok / 8 / RW; ++i) {
+        const int t = 8 * (i * RW + rw) + (ln >> 3), c = ln & 7;
+        *reinterpret_cast<v4u*>(tile + kLatB + t * kRopeB + ((c ^ rope_swz(t)) << 4)) =
+            *reinterpret_cast<const v4u*>(from + kCodeB + t * kRopeB + 16 * c);
+      }
+      barrier_lds();
+      if (k + ST < n_steps) fetch(tb + ST * STEP, raw + slot * kRawB);
+      slot = slot + 1 == ST ? 0 : slot + 1;
+    } else {
+      if (tb >= end_max) break;                      // the other token waves have the rest
+      if constexpr (FP8) {
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+#pragma unroll
+        for (int i = 0; i < kTok / 2; ++i) spread(2 * i + (ln >> 5), ln & 31, code_reg[i], scale_reg[i]);
+#pragma unroll
+        for (int i = 0; i < kTok / 8; ++i) {
+          const int t = 8 * i + (ln >> 3);
+          *reinterpret_cast<v4u*>(tile + kLatB + t * kRopeB + (((ln & 7) ^ rope_swz(t)) << 4)) = rope_reg[i];
+        }
+        if (k + 1 < n_steps && tb + STEP < end_max) fetch_regs(tb + STEP);
+      } else {
+        fetch(tb, tile);
+        wait_vmcnt<0>();
+      }
+    }
 
     // scores of 32 tokens
     v4f s[RT][2];
@@ -446,8 +593,8 @@ mla_attention_kernel(AttnParams p) {
     for (int k = 0; k < kSteps; ++k)
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt) {
-        const v8bf x = k < kR / 32 ? lds_b128(kat[k & 3], (k >> 2) * 256 + tt * 16 * kRowB)
-                                   : lds_b128(kro[k & 1], tt * 16 * kRopeB);
+        const v8bf x = k < kR / 32 ? lds_b128(kat[k & 3] + slot_at, (k >> 2) * 256 + tt * 16 * kRowB)
+                                   : lds_b128(kro[k & 1] + slot_at, tt * 16 * kRopeB);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) s[rt][tt] = mfma_bf16(x, q[rt][k], s[rt][tt]);
       }
@@ -485,7 +632,7 @@ mla_attention_kernel(AttnParams p) {
 
     // output
     unroll<kCt>([&](auto ct) {
-      const v8bf x = lds_tr(vat[ct & 7], (ct >> 3) * 256);
+      const v8bf x = lds_tr(vat[ct & 7] + slot_at, (ct >> 3) * 256);
       unroll<RT>([&](auto rt) { acc_mfma<kCt * rt + ct>(x, pr[rt]); });
     });
   }
@@ -634,6 +781,10 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
   p.ldr_t = a.ldr_t;
   p.ldr_h = a.ldr_h;
   p.scale2 = a.scale * 1.4426950408889634f;
+  int bits = 0;
+  while ((1 << bits) < a.ps) ++bits;
+  p.ps_shift = 31 + bits;
+  p.ps_mul = (uint32_t)((((uint64_t)1 << p.ps_shift) + a.ps - 1) / a.ps);
   p.T = (int)a.T;
   p.H = (int)a.H;
   p.B = (int)a.B;
@@ -646,18 +797,31 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
   p.meta = static_cast<Meta*>(a.workspace);
   p.part_lse = reinterpret_cast<float*>(p.meta + kGrid);
   p.part_out = p.part_lse + (int64_t)kGrid * 2 * m;
-#define FP8BS_ATTN(RT_, RW_, TW_)                                                                              \
-  case 16 * RT_ * RW_:                                                                                         \
-    if (a.fp8) hipLaunchKernelGGL((mla_attention_kernel<RT_, RW_, TW_, true>), dim3(kGrid), dim3(256), 0, stream, p); \
-    else hipLaunchKernelGGL((mla_attention_kernel<RT_, RW_, TW_, false>), dim3(kGrid), dim3(256), 0, stream, p); \
-    hipLaunchKernelGGL(join_kernel<16 * RT_ * RW_>, dim3(kGrid, 4 * RT_ * RW_), dim3(256), 0, stream, p); \
-    break;
+#define FP8BS_ATTN(RT_, RW_, TW_, F8_) \
+  hipLaunchKernelGGL((mla_attention_kernel<RT_, RW_, TW_, F8_>), dim3(kGrid), dim3(256), 0, stream, p)
+#define FP8BS_JOIN(M_) hipLaunchKernelGGL(join_kernel<M_>, dim3(kGrid, M_ / 4), dim3(256), 0, stream, p)
   switch (m) {
-    FP8BS_ATTN(2, 4, 1)
-    FP8BS_ATTN(2, 2, 2)
-    FP8BS_ATTN(2, 1, 4)
-    default: FP8BS_ATTN(1, 1, 4)
+    case 128:
+      if (a.fp8) FP8BS_ATTN(2, 4, 1, true);
+      else FP8BS_ATTN(2, 4, 1, false);
+      FP8BS_JOIN(128);
+      break;
+    case 64:
+      if (a.fp8) FP8BS_ATTN(2, 2, 2, true);
+      else FP8BS_ATTN(2, 2, 2, false);
+      FP8BS_JOIN(64);
+      break;
+    case 32:   // with codes waiting in registers there is no room for two row tiles a wave
+      if (a.fp8) FP8BS_ATTN(1, 2, 2, true);
+      else FP8BS_ATTN(2, 1, 4, false);
+      FP8BS_JOIN(32);
+      break;
+    default:
+      if (a.fp8) FP8BS_ATTN(1, 1, 4, true);
+      else FP8BS_ATTN(1, 1, 4, false);
+      FP8BS_JOIN(16);
   }
+#undef FP8BS_JOIN
 #undef FP8BS_ATTN
   return hipGetLastError();
 }
