@@ -60,6 +60,7 @@ constexpr int kLatB = kTok * kRowB;
 constexpr int kTileB = kLatB + kTok * kRopeB;   // 36,864 bytes
 constexpr int kCodeB = kTok * kR;                // the same 32 tokens of an FP8 cache as they come:
 constexpr int kRawB = kCodeB + kTok * kRopeB + 1024;   // codes, rope, scales (512 bytes, written twice)
+constexpr int kAhead = 6;
 constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -386,19 +387,15 @@ mla_attention_kernel(AttnParams p) {
   if (!plan.make(p, w, smem)) return;
 
   // The operand reads' LDS addresses.  A latent chunk's swizzle touches the low
-  // four bits of its index alone, so K steps k, k + 4, .. and channel tiles
-  // ct, ct + 8, .. share a base, and both halves of the 32 tokens do.
+  // four bits of its index alone and by exclusive or, so the address of K step k
+  // is that of step 0 with 64 (k % 4) xored in and 256 (k / 4) added, that of
+  // channel tile ct has 32 (ct % 8) xored in and 256 (ct / 8) added, and the second
+  // 16 tokens are 16 rows on.
   const uint32_t tile_at = lds_at(tile);
-  uint32_t kat[4], kro[2], vat[8];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) kat[k] = tile_at + n * kRowB + (((4 * k + g) ^ lat_swz(n)) << 4);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) kro[k] = tile_at + kLatB + n * kRopeB + (((4 * k + g) ^ rope_swz(n)) << 4);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int t = 4 * g + (n >> 2);                  // the lane points at this token, 4 channels from 4 (n % 4)
-    vat[k] = tile_at + t * kRowB + (((2 * k + ((n & 3) >> 1)) ^ lat_swz(t)) << 4) + ((n & 1) << 3);
-  }
+  const uint32_t key_at = tile_at + n * kRowB + ((g ^ lat_swz(n)) << 4);
+  const uint32_t key_rope_at = tile_at + kLatB + n * kRopeB + ((g ^ rope_swz(n)) << 4);
+  const int vt = 4 * g + (n >> 2);                   // the lane points at this token, 4 channels from 4 (n % 4)
+  const uint32_t value_at = tile_at + vt * kRowB + ((((n & 3) >> 1) ^ lat_swz(vt)) << 4) + ((n & 1) << 3);
   acc_reserve<RT>();
 
   int b = plan.lo.b, in_seq = plan.lo.in_seq, step0 = plan.lo.step;
@@ -589,15 +586,26 @@ mla_attention_kernel(AttnParams p) {
     v4f s[RT][2];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    // Operands are read kAhead fragments before their products: a wave is alone on its SIMD, so
+    // nothing else covers the LDS's latency.
+    v8bf x[kAhead];
+    uint32_t ka = key_at + slot_at, kr = key_rope_at + slot_at, va = value_at + slot_at;
+    asm volatile("" : "+v"(ka), "+v"(kr), "+v"(va));  // or the addresses below would stay in registers over the loop
+    auto key = [&](auto f) {                         // fragment f: K step f / 2, tokens 16 (f % 2) ..
+      constexpr int k = f / 2, tt = f % 2;
+      x[f % kAhead] = k < kR / 32 ? lds_b128(ka ^ (k % 4 * 64), k / 4 * 256 + tt * 16 * kRowB)
+                                  : lds_b128(kr ^ (k % 2 * 64), tt * 16 * kRopeB);
+    };
+    unroll<kAhead>([&](auto f) { key(f); });
+    unroll<2 * kSteps>([&](auto f) {
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-      for (int tt = 0; tt < 2; ++tt) {
-        const v8bf x = k < kR / 32 ? lds_b128(kat[k & 3] + slot_at, (k >> 2) * 256 + tt * 16 * kRowB)
-                                   : lds_b128(kro[k & 1] + slot_at, tt * 16 * kRopeB);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) s[rt][tt] = mfma_bf16(x, q[rt][k], s[rt][tt]);
-      }
+      for (int rt = 0; rt < RT; ++rt) s[rt][f % 2] = mfma_bf16(x[f % kAhead], q[rt][f / 2], s[rt][f % 2]);
+      if constexpr (f + kAhead < 2 * kSteps) key(std::integral_constant<int, f + kAhead>{});
+    });
+    auto value = [&](auto ct) { x[ct % kAhead] = lds_tr(va ^ (ct % 8 * 32), ct / 8 * 256); };
+    unroll<kAhead>([&](auto ct) { value(ct); });
+    __builtin_amdgcn_sched_barrier(0);
 
     // probabilities
     v8bf pr[RT];
@@ -632,8 +640,9 @@ mla_attention_kernel(AttnParams p) {
 
     // output
     unroll<kCt>([&](auto ct) {
-      const v8bf x = lds_tr(vat[ct & 7] + slot_at, (ct >> 3) * 256);
-      unroll<RT>([&](auto rt) { acc_mfma<kCt * rt + ct>(x, pr[rt]); });
+      __builtin_amdgcn_sched_barrier(0);
+      unroll<RT>([&](auto rt) { acc_mfma<kCt * rt + ct>(x[ct % kAhead], pr[rt]); });
+      if constexpr (ct + kAhead < kCt) value(std::integral_constant<int, ct + kAhead>{});
     });
   }
   acc_settle();
