@@ -250,6 +250,10 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t&
 // ---------------------------------------------------------------------------
 constexpr int kStart = 2;    // a tile's queries and output, in steps
 constexpr int kLeast = 4;    // a share is no smaller, so that short work is not cut to pieces
+// A cut this near a tile's edge moves to it: a split costs the writing and
+// reading of M rows of float32 twice, about M / 16 steps' time.
+template <int M>
+__device__ __forceinline__ int slack(int64_t total, int shares) { return (int)min((int64_t)(M / 16), total / shares / 4); }
 
 struct Cut {          // a place between two steps
   int tile;           // row tile of the batch
@@ -271,7 +275,7 @@ template <int M, int STEP>
 struct Plan {
   Cut lo, hi;
   int64_t total;
-  int shares;
+  int shares, near;
 
   static __device__ int tile_cost(const AttnParams& p, const Seq& s, int in_seq) {
     const int r = (int)min((int64_t)(in_seq + 1) * M, (int64_t)s.nq * p.H) - 1;
@@ -316,6 +320,7 @@ struct Plan {
     shares = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kLeast));
     if (w >= shares || total == 0) return false;
 
+    near = uniform(slack<M>(total, shares));
     const int64_t want[2] = {total * w / shares, total * (w + 1) / shares};
     if (t1 == tiles && t0 < t1 && want[1] == total) cut[1] = Cut{tiles, p.B, 0, 0, total};
     if (t0 < t1 && ((want[0] >= base && want[0] < base + mine) || (want[1] >= base && want[1] < base + mine))) {
@@ -326,8 +331,13 @@ struct Plan {
         const int c = tile_cost(p, s, t - first[b]);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          if (want[k] >= base && want[k] < base + c)
-            cut[k] = Cut{t, b, t - first[b], max(0, (int)(want[k] - base) - kStart), base + c};
+          if (want[k] >= base && want[k] < base + c) {
+            const int at = (int)(want[k] - base);
+            // (tile t + 1 may be the next sequence's first: the share that begins there looks)
+            if (at <= kStart + near) cut[k] = Cut{t, b, t - first[b], 0, base + c};
+            else if (at >= c - near) cut[k] = Cut{t + 1, b, t + 1 - first[b], 0, base + c};
+            else cut[k] = Cut{t, b, t - first[b], at - kStart, base + c};
+          }
         base += c;
       }
     }
@@ -399,13 +409,10 @@ mla_attention_kernel(AttnParams p) {
   acc_reserve<RT>();
 
   int b = plan.lo.b, in_seq = plan.lo.in_seq, step0 = plan.lo.step;
-  for (int j = plan.lo.tile; j < plan.hi.tile || (j == plan.hi.tile && plan.hi.step > 0); ++j, step0 = 0) {
-  if (j > plan.lo.tile) {
-    ++in_seq;
-    if ((int64_t)in_seq * M >= (int64_t)load_seq(p, b).nq * p.H) {
-      b = uniform(next_seq(p, b));
-      in_seq = 0;
-    }
+  for (int j = plan.lo.tile; j < plan.hi.tile || (j == plan.hi.tile && plan.hi.step > 0); ++j, ++in_seq, step0 = 0) {
+  if ((int64_t)in_seq * M >= (int64_t)load_seq(p, b).nq * p.H) {   // behind the sequence's last tile
+    b = uniform(next_seq(p, b));
+    in_seq = 0;
   }
   const Seq sq = load_seq(p, b);
   const int rows = sq.nq * p.H;
@@ -712,50 +719,78 @@ mla_attention_kernel(AttnParams p) {
     }
   });
   if (threadIdx.x == 0 && step0 == 0 && !whole) {
-    // the share that reaches the tile's end is the first whose own end is not before it
-    const int64_t last = (plan.hi.end * plan.shares + plan.total - 1) / plan.total - 1;
+    // the share that finishes the tile is the first whose own end is not before, or snaps to, the tile's
+    const int64_t last = ((plan.hi.end - plan.near) * plan.shares + plan.total - 1) / plan.total - 1;
     p.meta[w] = Meta{(int64_t)sq.q0 * p.H + r_tile, r_last - r_tile + 1, (int)last - w + 1};
   }
   }
 }
 
-// Joins the parts of a split row tile: a wave per row, eight channels a lane;
-// weights 2^(lse_k - max).  Reads what the parts' workgroups wrote (mostly
-// still in the caches), writes the output once.
-template <int M>
-__global__ void __launch_bounds__(256) join_kernel(AttnParams p) {
-  const int w = blockIdx.x;
-  const Meta meta = p.meta[w];
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 6);
-  if (meta.parts == 0 || r >= meta.rows) return;
-  const int lane = threadIdx.x & 63;
-  // part 0 is slot 1 of workgroup w, part k slot 0 of w + k
-  auto at = [&](int k) { return (k == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + k)) * M + r; };
-  float top = kNegInf;
-  for (int k = lane; k < meta.parts; k += 64) top = fmaxf(top, p.part_lse[at(k)]);
+// Joins the parts of split row tiles with weights 2^(lse_k - max).  A workgroup
+// finds the split tiles (one thread per share), then takes rows of them in
+// turn: two halves of 128 threads, each over every second part, 16 bytes a
+// thread.  Bound by reading the parts; rows, not tiles, are dealt out, so that
+// one tile in 128 parts and 128 tiles in two keep all CUs busy alike.
+constexpr int kGrid = 256;    // shares: the MI355X's CUs
+constexpr int kJoin = 1024;   // workgroups
+__global__ void __launch_bounds__(256) join_kernel(AttnParams p, int M) {
+  __shared__ Meta metas[kGrid];
+  __shared__ int64_t sums[4];
+  __shared__ int before[kGrid + 1];
+  __shared__ float lse_max[4], weight[kGrid];
+  __shared__ v4f half[128];
+  const int tid = threadIdx.x;
+  const Meta mine = p.meta[tid];
+  metas[tid] = mine;
+  int64_t all;
+  const int64_t at = block_scan(mine.parts ? mine.rows : 0, sums, all);
+  before[tid] = (int)at;
+  if (tid == 0) before[kGrid] = (int)all;
+  __syncthreads();
+  for (int item = blockIdx.x; item < (int)all; item += gridDim.x) {
+    int w = 0;                                       // the last share with before[w] <= item
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-  const float base = top == kNegInf ? 0.0f : top;
-  float sum = 0.0f;
-  v4f lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
-  for (int k0 = 0; k0 < meta.parts; k0 += 64) {
-    const int have = min(64, meta.parts - k0);
-    const float mine = lane < have ? __builtin_amdgcn_exp2f(p.part_lse[at(k0 + lane)] - base) : 0.0f;
-    for (int k = 0; k < have; k += 4)
+    for (int s = kGrid / 2; s; s >>= 1)
+      if (before[w + s] <= item) w += s;
+    const Meta meta = metas[w];
+    const int r = item - before[w];
+    // part 0 is slot 1 of share w, part k slot 0 of share w + k
+    auto slot = [&](int k) { return (k == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + k)) * M + r; };
+    const float l = tid < meta.parts ? p.part_lse[slot(tid)] : kNegInf;
+    float top = l;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {                  // lanes from `have` on hold weight 0
-        const float x = bits_f32(__builtin_amdgcn_readlane(f32_bits(mine), k + u));
-        const float* src = p.part_out + at(k0 + min(k + u, have - 1)) * kR + 4 * lane;
-        lo += *reinterpret_cast<const v4f*>(src) * x;
-        hi += *reinterpret_cast<const v4f*>(src + kR / 2) * x;
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    __syncthreads();                                 // the last row's weights and halves are used
+    if ((tid & 63) == 0) lse_max[tid >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(lse_max[0], lse_max[1]), fmaxf(lse_max[2], lse_max[3]));
+    weight[tid] = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(l - top);
+    __syncthreads();
+    const int c = 4 * (tid & 127), odd = tid >> 7;
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    float sum = 0.0f;
+    for (int k = odd; k < meta.parts; k += 16) {
+      v4f v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)                    // parts past the last read that one again, weighing nothing
+        v[u] = *reinterpret_cast<const v4f*>(p.part_out + slot(min(k + 2 * u, meta.parts - 1)) * kR + c);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float x = k + 2 * u < meta.parts ? weight[k + 2 * u] : 0.0f;
+        acc += v[u] * x;
         sum += x;
       }
+    }
+    if (odd) half[tid & 127] = acc;
+    if (tid == 128) lse_max[0] = sum;
+    __syncthreads();
+    if (!odd) {
+      acc += half[tid];
+      sum += lse_max[0];
+      store4(p, (meta.row + r) * kR + c, acc * (sum > 0.0f ? 1.0f / sum : 0.0f));
+      if (tid == 0 && p.lse) p.lse[meta.row + r] = sum > 0.0f ? (top + __builtin_log2f(sum)) * kLn2 : kNegInf;
+    }
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-  const int64_t orow = meta.row + r;
-  store4(p, orow * kR + 4 * lane, lo * inv);
-  store4(p, orow * kR + kR / 2 + 4 * lane, hi * inv);
-  if (lane == 0 && p.lse) p.lse[orow] = sum > 0.0f ? (top + __builtin_log2f(sum)) * kLn2 : kNegInf;
 }
 
 // rows of an average sequence decide the tile
@@ -763,7 +798,6 @@ int tile_rows(int64_t T, int64_t H, int64_t B) {
   const int64_t per = T * H / B;
   return per >= 96 ? 128 : per >= 48 ? 64 : per >= 24 ? 32 : 16;
 }
-constexpr int kGrid = 256;    // the MI355X's CUs
 
 constexpr int64_t part_bytes(int m) { return (int64_t)kGrid * 2 * m * (kR + 1) * 4; }
 
@@ -808,29 +842,24 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
   p.part_out = p.part_lse + (int64_t)kGrid * 2 * m;
 #define FP8BS_ATTN(RT_, RW_, TW_, F8_) \
   hipLaunchKernelGGL((mla_attention_kernel<RT_, RW_, TW_, F8_>), dim3(kGrid), dim3(256), 0, stream, p)
-#define FP8BS_JOIN(M_) hipLaunchKernelGGL(join_kernel<M_>, dim3(kGrid, M_ / 4), dim3(256), 0, stream, p)
   switch (m) {
     case 128:
       if (a.fp8) FP8BS_ATTN(2, 4, 1, true);
       else FP8BS_ATTN(2, 4, 1, false);
-      FP8BS_JOIN(128);
       break;
     case 64:
       if (a.fp8) FP8BS_ATTN(2, 2, 2, true);
       else FP8BS_ATTN(2, 2, 2, false);
-      FP8BS_JOIN(64);
       break;
     case 32:   // with codes waiting in registers there is no room for two row tiles a wave
       if (a.fp8) FP8BS_ATTN(1, 2, 2, true);
       else FP8BS_ATTN(2, 1, 4, false);
-      FP8BS_JOIN(32);
       break;
     default:
       if (a.fp8) FP8BS_ATTN(1, 1, 4, true);
       else FP8BS_ATTN(1, 1, 4, false);
-      FP8BS_JOIN(16);
   }
-#undef FP8BS_JOIN
+  hipLaunchKernelGGL(join_kernel, dim3(kJoin), dim3(256), 0, stream, p, m);
 #undef FP8BS_ATTN
   return hipGetLastError();
 }
