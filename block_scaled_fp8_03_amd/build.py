@@ -44,16 +44,38 @@ OWN_AGPR_SOURCES = {"mla_attention.hip"}
 OWN_AGPR_FLAGS = ["-mllvm", "-amdgpu-spill-vgpr-to-agpr=0"]
 
 
+def _vgprs(operand: str) -> range:
+    """The VGPRs that an operand of a listing names (``v7``, ``v[4:7]``); empty for others."""
+    m = re.fullmatch(r"v(\d+)|v\[(\w+):(\w+)\]", operand.strip())
+    if not m:
+        return range(0)
+    return range(int(m[1]), int(m[1]) + 1) if m[1] else range(int(m[2], 0), int(m[3], 0) + 1)
+
+
 def check_listing(src: str, text: str) -> None:
     """Raises if the listing of a source in OWN_AGPR_SOURCES touches an AGPR
-    outside inline assembly, or spills."""
-    inside = False
+    outside inline assembly, spills, or writes an operand of an MFMA of the
+    inline assembly within two instructions or wait states before it (which the
+    compiler would see to for its own)."""
+    inside, before = False, []
     for line in text.splitlines():
         if "#ASMSTART" in line or "#ASMEND" in line:
             inside = "#ASMSTART" in line
-        elif not inside and re.match(r"\s+[vdsgb]\w*_\w+\s", line):
-            if re.search(r"[ ,]a(\d|\[)", line.split(";")[0]) or "scratch_" in line:
-                raise RuntimeError(f"{src}: the compiler uses registers that the kernel keeps for itself: {line.strip()}")
+            continue
+        m = re.match(r"\s+([vdsgb]\w*_\w+)\s+(.*)", line.split(";")[0])
+        if not m:
+            continue
+        op, args = m[1], [a.strip() for a in m[2].split(",")]
+        if not inside and (re.search(r"(^|[ ,])a(\d|\[)", m[2]) or op.startswith("scratch_")):
+            raise RuntimeError(f"{src}: the compiler uses registers that the kernel keeps for itself: {line.strip()}")
+        if inside and op.startswith("v_mfma"):
+            read = {r for a in args[1:3] for r in _vgprs(a)}
+            if any(read & set(w) for w in before[-2:]):
+                raise RuntimeError(f"{src}: an operand is written just before its MFMA: {line.strip()}")
+        if op == "s_nop":
+            before += [range(0)] * (int(args[0], 0) + 1)
+        else:
+            before.append(_vgprs(args[0]) if op.startswith("v_") and not op.startswith("v_cmp") else range(0))
 
 
 def _listing(cmd, src: str) -> str:

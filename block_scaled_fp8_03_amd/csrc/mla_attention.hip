@@ -16,23 +16,23 @@
 // m and reach at most 2^8, which costs no precision (bf16 and float32 round
 // relatively) and leaves the accumulators alone.
 //
-// MFMA: v_mfma_f32_16x16x32_bf16, D[16 x 16] = X[16 x 32] . Y[32 x 16]; lane
-// (g = l / 16, n = l % 16) supplies row n of X and column n of Y at K values
-// 8g .. 8g+7, and register r of its result is D[4g + r][n].
-//   scores   X = 16 cached tokens, Y = 16 query rows: a lane holds tokens
-//            4g + r of one query row, so a row's maximum and sum are in-lane
-//            but for the four g.
-//   output   X = 16 latent channels (transposed reads), Y = the probabilities:
-//            over two score tiles (tokens 0..15 and 16..31) a lane owns tokens
-//            4g + r and 16 + 4g + r, which are taken as its K values 8g + r
-//            and 8g + 4 + r, so probabilities go from the score's registers to
-//            the operand without crossing lanes.  The latents are read in the
-//            same order by two 4-token transposed LDS reads.
+// MFMA: with 32 query rows a wave v_mfma_f32_32x32x16_bf16, with 16 rows
+// v_mfma_f32_16x16x32_bf16, D = X . Y; lane (g = l / ROWS, n = l % ROWS) supplies
+// row n of X and column n of Y at K values 8g .. 8g+7, and register r of its
+// result is D[TS (r / 4) + 4g + r % 4][n], TS = 8 or 16.
+//   scores   X = cached tokens, Y = query rows: a lane holds tokens of one query
+//            row, so a row's maximum and sum are in-lane but for the g.
+//   output   X = latent channels (transposed reads), Y = the probabilities: a
+//            lane's eight scores r are taken as its K values 8g + r, so they go from
+//            the score's registers to the operand without crossing lanes, and the
+//            latents' tokens are read in that order by two 4-token transposed LDS
+//            reads.
 //
-// A wave carries 16 RT query rows (Q in registers) over 32 cached tokens at a
+// A wave carries ROWS query rows (Q in registers) over 32 cached tokens at a
 // time; RW waves take different rows of the same tokens and TW waves different
 // tokens of the same rows.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <type_traits>
 
@@ -52,15 +52,16 @@ typedef __attribute__((address_space(3))) v4u lds_v4u;
 constexpr int kR = 512;                 // latent width
 constexpr int kD = 64;                  // rotated width
 constexpr int kTok = 32;                // cached tokens per wave and step
-constexpr int kSteps = (kR + kD) / 32;  // K steps of a score: 16 latent, 2 rotated
-constexpr int kCt = kR / 16;            // channel tiles of the output
-constexpr int kRowB = kR * 2;           // bytes of a latent row in LDS
 constexpr int kRopeB = kD * 2;
-constexpr int kLatB = kTok * kRowB;
-constexpr int kTileB = kLatB + kTok * kRopeB;   // 36,864 bytes
-constexpr int kCodeB = kTok * kR;                // the same 32 tokens of an FP8 cache as they come:
-constexpr int kRawB = kCodeB + kTok * kRopeB + 1024;   // codes, rope, scales (512 bytes, written twice)
-constexpr int kAhead = 6;
+// 32 tokens in LDS: four blocks of 8 tokens, each nine groups (eight of latents,
+// one rotated) of 128 bytes a token.  A group is one load instruction, and the
+// groups of a token are 128 bytes apart in memory and 1024 in LDS.
+constexpr int kGroupB = 8 * 128;
+constexpr int kBlockB = 9 * kGroupB;
+constexpr int kTileB = 4 * kBlockB;     // 36,864 bytes
+// FP8: 8 tokens as they come, four groups of codes, the rotated group, four scales a token (twice)
+constexpr int kRawB = 5 * kGroupB + 256;
+constexpr int kAhead = 6;                // fragments read ahead of their products
 constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -77,7 +78,8 @@ struct AttnParams {
   void* out;                // [T, H, 512]
   float* lse;               // [T, H] or null
   int64_t ldq_t, ldq_h, ldr_t, ldr_h;
-  float scale2;             // scale * log2(e)
+  float scale2;             // |scale| * log2(e)
+  uint32_t flip;            // scale < 0: the sign bits of two bf16, put on Q
   uint32_t ps_mul;          // tok / ps = tok * ps_mul >> ps_shift for tok < 2^31
   int ps_shift;
   // workspace: [grid] Meta, then [grid][2][M] lse (base 2), then [grid][2][M][512] normalised output parts
@@ -94,17 +96,23 @@ struct Meta {
   int rows, parts;  // parts = 0: none.  Part 0 is this workgroup's, part k the k-th next one's.
 };
 
-// The 16-byte chunk c of latent row t sits at slot c ^ lat_swz(t), and of
-// rope row t at c ^ rope_swz(t).  A linear map of the token's bits chosen for
-// the LDS's rule (a b128 read is served in four cycles of the 16 lanes of a
-// half-wave with equal parity of lane bits 2..4, a b64 read by half-waves, over
-// 64 banks): the score reads (16 tokens x chunks g of a K step) and the
-// transposed reads (8 tokens x 2 chunks) both touch 16 distinct slots a cycle.
-__device__ __forceinline__ int lat_swz(int t) { return ((t & 7) << 1) ^ ((t & 8) ? 9 : 0); }
-__device__ __forceinline__ int rope_swz(int t) { return ((t & 2) << 1) | ((t & 4) >> 1) | ((t & 4) >> 2); }
+// The 16-byte chunk c of token t sits in group c / 8 at place (c % 8) ^ swz(t): a
+// linear map of the token's bits chosen for the LDS's rule (a b128 read is
+// served in four cycles of the 16 lanes of a half-wave with equal parity of
+// lane bits 2..4, a b64 read by half-waves, over 64 banks), under which both the
+// score reads and the transposed reads touch 16 distinct slots of 16 bytes a cycle.
+template <int ROWS>
+__device__ __forceinline__ int swz(int t) {
+  const int t1 = (t >> 1) & 1, t2 = (t >> 2) & 1, t3 = (t >> 3) & 1;
+  return ROWS == 32 ? t1 << 2 | t3 << 1 | t2 : t1 << 2 | t2 << 1 | t2;
+}
 
+typedef float v16f __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ v4f mfma_bf16(v8bf x, v8bf y, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
+}
+__device__ __forceinline__ v16f mfma_bf16(v8bf x, v8bf y, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
 }
 
 __device__ __forceinline__ uint32_t lds_at(const void* q) {
@@ -113,29 +121,37 @@ __device__ __forceinline__ uint32_t lds_at(const void* q) {
 __device__ __forceinline__ v8bf lds_b128(uint32_t at, int off) {
   return __builtin_bit_cast(v8bf, *((const lds_v4u*)(uintptr_t)at + off / 16));
 }
-// 4 tokens x 16 channels, transposed, twice: tokens 4g .. + 3 and 16 + 4g .. + 3
-__device__ __forceinline__ v8bf lds_tr(uint32_t at, int off) {
+// 4 tokens x 16 channels a quarter-wave, transposed, twice
+__device__ __forceinline__ v8bf lds_tr(uint32_t at0, int off0, uint32_t at1, int off1) {
   typedef short v8s __attribute__((ext_vector_type(8)));
-  const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)at + off / 8);
-  const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)at + (off + 16 * kRowB) / 8);
+  const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)at0 + off0 / 8);
+  const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)at1 + off1 / 8);
   return __builtin_bit_cast(v8bf, (v8s)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// The output accumulators: tile (rt, ct) of a wave is the AGPRs 4 i .. 4 i + 3
-// with i = kCt rt + ct, 256 of them per lane with RT = 2, named in the
-// instructions below.  Left to the compiler they would be VGPRs (the rare
-// rescale is VALU work, which cannot take AGPRs), and with Q's 144 registers
+// The output accumulators: AGPRs 0 .. 8 ROWS - 1, named in the instructions
+// below; 256 a lane with 32 rows.  Left to the compiler they would be VGPRs (the
+// rare rescale is VALU work, which cannot take AGPRs), and with Q's registers
 // that spilled 230 of them to memory.  The source is built so that the
 // compiler itself puts nothing into AGPRs (its own MFMAs in the VGPR form, and
-// less than 256 VGPRs live), which a test of the listing checks.
-// Wait states: a VALU result may be an MFMA operand two cycles later (s_nop 1);
-// an MFMA's result may be read by another kind of instruction 19 cycles later.
-template <int I>
+// less than 256 VGPRs live); the build refuses a listing where it does.
+// Wait states: a VALU result may be an MFMA operand two instructions later, which
+// the build checks too; an MFMA's result may be read by another kind of
+// instruction 19 cycles later, for which acc_settle stands.
+template <int ROWS, int T>
 __device__ __forceinline__ void acc_mfma(v8bf x, v8bf y) {
-  asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 a[%0:%1], %2, %3, a[%0:%1]"
-               :: "n"(4 * I), "n"(4 * I + 3), "v"(x), "v"(y));
+  if constexpr (ROWS == 32)
+    asm volatile("v_mfma_f32_32x32x16_bf16 a[%0:%1], %2, %3, a[%0:%1]"
+                 :: "n"(16 * T), "n"(16 * T + 15), "v"(x), "v"(y));
+  else
+    asm volatile("v_mfma_f32_16x16x32_bf16 a[%0:%1], %2, %3, a[%0:%1]"
+                 :: "n"(4 * T), "n"(4 * T + 3), "v"(x), "v"(y));
 }
-__device__ __forceinline__ void acc_settle() { asm volatile("s_nop 15\n\ts_nop 7"); }
+__device__ __forceinline__ void acc_settle() { asm volatile("s_nop 15\n\ts_nop 15"); }
+__device__ __forceinline__ void operands_settle() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 1");
+}
 template <int I>
 __device__ __forceinline__ v4f acc_read() {
   float a, b, c, d;
@@ -158,12 +174,35 @@ __device__ __forceinline__ void unroll(const F& f) {
     unroll<N, I + 1>(f);
   }
 }
-// tells the compiler how many registers a kernel of RT row tiles takes
-template <int RT>
+// tells the compiler how many AGPRs a kernel takes
+template <int ROWS>
 __device__ __forceinline__ void acc_reserve() {
-  if constexpr (RT == 1) asm volatile("" ::: "a127");
+  if constexpr (ROWS == 16) asm volatile("" ::: "a127");
   else asm volatile("" ::: "a255");
 }
+
+// A lane's scores of 32 tokens: number e is that of token TS (e / 4) + 4g + e % 4
+template <int ROWS>
+struct Scores;
+template <>
+struct Scores<32> {
+  static constexpr int N = 16, TS = 8;
+  v16f v;
+  __device__ void clear() {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+  }
+  template <int E> __device__ float get() const { return v[E]; }
+  template <int E> __device__ void set(float x) { v[E] = x; }
+};
+template <>
+struct Scores<16> {
+  static constexpr int N = 8, TS = 16;
+  v4f v[2];
+  __device__ void clear() { v[0] = v[1] = v4f{0.0f, 0.0f, 0.0f, 0.0f}; }
+  template <int E> __device__ float get() const { return v[E / 4][E % 4]; }
+  template <int E> __device__ void set(float x) { v[E / 4][E % 4] = x; }
+};
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
@@ -190,16 +229,17 @@ __device__ __forceinline__ int visible(const AttnParams& p, const Seq& s, int i)
   return p.causal ? clampi(s.len - s.nq + i + 1, 0, s.len) : s.len;
 }
 
-// Direct global -> LDS loads, 16 bytes a lane: lane i's bytes land at lds + 16 i.
-// In assembly, so that the compiler does not make every LDS read wait for all
-// of them; completion is awaited with wait_vmcnt.
-__device__ __forceinline__ void dma_row(const void* base, uint32_t off, uint32_t lds) {
-  // five wait states, should a VALU instruction have written the base's scalar registers just before
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base) : "memory", "m0");
+// Direct global -> LDS loads of 16 (4) bytes a lane: lane i's bytes at `at` + OFF
+// land at lds + 16 i (4 i).  The instruction adds OFF to both addresses.  In
+// assembly, so that the compiler does not make every LDS read wait for all of
+// them; completion is awaited with wait_vmcnt.
+template <int OFF>
+__device__ __forceinline__ void dma_b128(const void* at, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2"
+               :: "s"(__builtin_amdgcn_readfirstlane(lds - OFF)), "v"(at), "n"(OFF) : "memory", "m0");
 }
-__device__ __forceinline__ void dma_lanes(const void* at, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+__device__ __forceinline__ void dma_b32(const void* at, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(at) : "memory", "m0");
 }
 template <int n>
@@ -362,33 +402,43 @@ __device__ __forceinline__ int next_seq(const AttnParams& p, int b) {
   return p.B - 1;
 }
 
-// Stages of cached tokens under way per token wave, and LDS: with one stage (RW
-// = 1) every wave loads, waits and computes by itself, no barrier, the waves
-// covering each other's waits; else a ring of ST stages.  An FP8 cache's codes
-// come in as they are and are spread to bf16 in LDS once for all row waves;
-// with RW = 1 they wait in registers.
-template <int RW, int TW, bool FP8>
-constexpr int stages() { return RW == 1 ? 1 : TW == 1 ? 4 : 2; }
-template <int RW, int TW, bool FP8>
+// LDS.  One token wave's tiles: with PIPE (RW = 4) a ring of four, or three and a
+// stage of codes for FP8; with RW = 2 two, or one and two stages of codes; with
+// RW = 1 one (FP8: the codes wait in registers).  A wave makes bf16 of the codes
+// that it loaded itself.
+template <int RW, bool FP8>
+constexpr int tiles() { return RW == 4 ? (FP8 ? 3 : 4) : RW == 2 && !FP8 ? 2 : 1; }
+template <int RW, bool FP8>
+constexpr int raws() { return !FP8 || RW == 1 ? 0 : RW == 2 ? 2 : 1; }
+template <int ROWS, int RW, int TW, bool FP8>
 constexpr int lds_bytes() {
-  constexpr int st = stages<RW, TW, FP8>();
-  constexpr int n = FP8 ? TW * (kTileB + (RW == 1 ? 0 : st * kRawB)) : TW * st * kTileB;
-  return TW > 1 ? std::max(n, 4 * 16 * kR * 4) : n;   // the token waves' accumulators meet here
+  const int n = TW * (tiles<RW, FP8>() * kTileB + raws<RW, FP8>() * 4 * kRawB) + (RW == 4 ? 4 * 4 * 1024 : 0);
+  return TW > 1 ? std::max(n, 4 * ROWS * (kR / (ROWS / 16)) * 4) : n;   // the token waves' accumulators meet here
 }
 
-template <int RT, int RW, int TW, bool FP8>
+template <int ROWS, int RW, int TW, bool FP8>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 mla_attention_kernel(AttnParams p) {
-  constexpr int M = 16 * RT * RW, STEP = kTok * TW;
-  constexpr int ST = stages<RW, TW, FP8>();
-  static_assert(RW * TW == 4 && lds_bytes<RW, TW, FP8>() <= 160 * 1024, "layout");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[lds_bytes<RW, TW, FP8>()];
+  constexpr int M = ROWS * RW, STEP = kTok * TW;
+  constexpr bool WIDE = ROWS == 32, PIPE = RW == 4;
+  constexpr int NT = tiles<RW, FP8>(), NR = raws<RW, FP8>();
+  constexpr int NSUB = 4 / RW;                       // blocks of 8 tokens that a wave loads of 32
+  constexpr int CH = 8 * 64 / ROWS;                  // channels of a K step of the scores
+  constexpr int QN = (kR + kD) / CH;                 // K steps
+  constexpr int QS = PIPE ? kR / CH : QN;            // those whose Q is in registers; PIPE: the rotated ones are in LDS
+  constexpr int NV = 32;                             // fragments of the latents as values
+  constexpr int NF = 36;                             // fragments of the latents as keys
+  constexpr int GS = Scores<ROWS>::TS, NG = kR / GS; // accumulators: NG groups of 4 channels from GS i + 4 g
+  static_assert(RW * TW == 4 && lds_bytes<ROWS, RW, TW, FP8>() <= 160 * 1024, "layout");
+  static_assert(NF % kAhead == 0 && kAhead % 2 == 0, "the two streams of fragments share x");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[lds_bytes<ROWS, RW, TW, FP8>()];
   const int lane = threadIdx.x & 63;
-  const int n = lane & 15, g = lane >> 4;
+  const int n = lane % ROWS, g = lane / ROWS;
   const int wave = uniform((int)threadIdx.x >> 6);
   const int rw = wave % RW, tw = wave / RW;
-  uint8_t* const tile = smem + tw * (FP8 ? 1 : ST) * kTileB;               // bf16 tiles of this token wave
-  uint8_t* const raw = smem + TW * kTileB + tw * ST * kRawB;               // FP8: its stages
+  const uint32_t tile_at = lds_at(smem) + tw * NT * kTileB;                             // this token wave's tiles
+  const uint32_t raw_at = lds_at(smem) + TW * NT * kTileB + wave * NR * NSUB * kRawB;   // this wave's codes
+  const uint32_t rest_at = lds_at(smem) + NT * kTileB + 4 * NR * kRawB + wave * 4096;   // PIPE: its Q, [4][lane] 16 bytes
 
   // neighbouring shares on one XCD (workgroups go round the eight): they often stream the same tokens
   const int w = gridDim.x % 8 == 0 ? (blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8 : blockIdx.x;
@@ -396,17 +446,16 @@ mla_attention_kernel(AttnParams p) {
   Plan<M, STEP> plan;
   if (!plan.make(p, w, smem)) return;
 
-  // The operand reads' LDS addresses.  A latent chunk's swizzle touches the low
-  // four bits of its index alone and by exclusive or, so the address of K step k
-  // is that of step 0 with 64 (k % 4) xored in and 256 (k / 4) added, that of
-  // channel tile ct has 32 (ct % 8) xored in and 256 (ct / 8) added, and the second
-  // 16 tokens are 16 rows on.
-  const uint32_t tile_at = lds_at(tile);
-  const uint32_t key_at = tile_at + n * kRowB + ((g ^ lat_swz(n)) << 4);
-  const uint32_t key_rope_at = tile_at + kLatB + n * kRopeB + ((g ^ rope_swz(n)) << 4);
-  const int vt = 4 * g + (n >> 2);                   // the lane points at this token, 4 channels from 4 (n % 4)
-  const uint32_t value_at = tile_at + vt * kRowB + ((((n & 3) >> 1) ^ lat_swz(vt)) << 4) + ((n & 1) << 3);
-  acc_reserve<RT>();
+  // The operand reads' addresses in a tile.  A chunk's swizzle touches the low three bits of its
+  // index alone and by exclusive or, so K step s (2 or 4 chunks on) has 16 (its chunk % 8) xored in and
+  // 1024 (its chunk / 8) added, and so have the channel tiles.
+  const uint32_t key_at = tile_at + n / 8 * kBlockB + n % 8 * 128 + ((g ^ swz<ROWS>(n)) << 4);
+  uint32_t value_at;
+  {
+    const int q = lane & 15, tok = 4 * g + (q >> 2), c = (WIDE ? (lane >> 4 & 1) * 2 : 0) + ((q & 3) >> 1);
+    value_at = tile_at + tok / 8 * kBlockB + tok % 8 * 128 + ((c ^ swz<ROWS>(tok)) << 4) + ((q & 1) << 3);
+  }
+  acc_reserve<ROWS>();
 
   int b = plan.lo.b, in_seq = plan.lo.in_seq, step0 = plan.lo.step;
   for (int j = plan.lo.tile; j < plan.hi.tile || (j == plan.hi.tile && plan.hi.step > 0); ++j, ++in_seq, step0 = 0) {
@@ -424,306 +473,443 @@ mla_attention_kernel(AttnParams p) {
   const int step1 = j == plan.hi.tile ? plan.hi.step : steps;
   const bool whole = step0 == 0 && step1 == steps;
 
-  // query rows of this wave: their operands, and the tokens they see
-  v8bf q[RT][kSteps];
-  int end[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int r = min(r_tile + (rw * RT + rt) * 16 + n, r_last);
+  wait_vmcnt<0>();
+  __syncthreads();                                   // the last tile's LDS is no longer read or written
+
+  // this lane's query row: its operands, and the tokens it sees
+  v8bf q[QS];
+  int end;
+  {
+    int ln = lane;
+    asm volatile("" : "+v"(ln));                     // addresses made here, and in the end, do not stay in registers
+    const int r = min(r_tile + rw * ROWS + ln % ROWS, r_last);
     const int i = r / p.H, h = r - i * p.H;
-    end[rt] = visible(p, sq, i);
-    const uint16_t* ql = p.q_lat + (sq.q0 + i) * p.ldq_t + h * p.ldq_h + 8 * g;
-    const uint16_t* qr = p.q_rope + (sq.q0 + i) * p.ldr_t + h * p.ldr_h + 8 * g;
+    end = visible(p, sq, i);
+    const uint16_t* ql = p.q_lat + (sq.q0 + i) * p.ldq_t + h * p.ldq_h + 8 * (ln / ROWS);
+    const uint16_t* qr = p.q_rope + (sq.q0 + i) * p.ldr_t + h * p.ldr_h + 8 * (ln / ROWS);
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-      q[rt][s] = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(s < kR / 32 ? ql + 32 * s : qr + 32 * s - kR));
+    for (int s = 0; s < QN; ++s) {
+      v4u v = *reinterpret_cast<const v4u*>(s < kR / CH ? ql + CH * s : qr + CH * s - kR);
+      v ^= p.flip;
+      if (s < QS) q[s] = __builtin_bit_cast(v8bf, v);
+      else *((lds_v4u*)(uintptr_t)(rest_at + ln * 16) + (s - QS) * 64) = v;
+    }
   }
 
-  float m[RT], l[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    m[rt] = kNegInf;
-    l[rt] = 0.0f;
-  }
-  unroll<RT * kCt>([&](auto i) { acc_write<i>(v4f{0.0f, 0.0f, 0.0f, 0.0f}); });
+  float m = kNegInf, l = 0.0f;
+  unroll<2 * ROWS>([&](auto i) { acc_write<i>(v4f{0.0f, 0.0f, 0.0f, 0.0f}); });
 
   // The pages of 64 consecutive table entries, one a lane, from entry pbase on.
   // A wave reloads them when it comes to their end (every 64 pages).
   const int32_t* trow = p.table + (int64_t)b * p.W;
   const int last = end_max - 1;
   int pages = 0, pbase = -64;
-  // The cache row of token min(tb + lane % 32, last): a token behind the last visible one is that one
-  // again, so masked places hold finite values and nothing behind the sequence is read.
-  auto rows_of = [&](int tb) {
-    int ln = lane & 31;
+  // 8 tokens from tb on to a block of LDS: token lane / 8, 16 bytes from 16 (lane % 8) of each group.
+  // A token behind the last visible one is that one again, so masked places hold finite values and
+  // nothing behind the sequence is read.
+  struct From {
+    const uint8_t* lat;
+    const uint16_t* rope;
+    const float* scale;
+  };
+  auto find = [&](int tb, int sub) {
+    int ln = lane;
     asm volatile("" : "+v"(ln));                     // so that addresses are not kept over the loop
-    const uint32_t tok = (uint32_t)min(tb + ln, last);
+    const uint32_t tok = (uint32_t)min(tb + 8 * sub + (ln >> 3), last);
     const int at = (int)((uint64_t)tok * p.ps_mul >> p.ps_shift);
-    const int lo = uniform(at), hi = __builtin_amdgcn_readlane(at, 31);
+    const int lo = uniform(at), hi = __builtin_amdgcn_readlane(at, 63);
     if (lo < pbase || hi >= pbase + 64) {
       pbase = lo;
       const int most = (int)((uint64_t)(uint32_t)last * p.ps_mul >> p.ps_shift);
-      pages = clampi(trow[min(pbase + (int)(threadIdx.x & 63), most)], 0, p.P - 1);
+      pages = clampi(trow[min(pbase + ln, most)], 0, p.P - 1);
     }
-    return __shfl(pages, at - pbase) * p.ps + (int)(tok - (uint32_t)at * (uint32_t)p.ps);   // P * ps < 2^31
+    // P * ps < 2^31
+    const int64_t row = __shfl(pages, at - pbase) * p.ps + (int)(tok - (uint32_t)at * (uint32_t)p.ps);
+    const int c = FP8 ? ln & 7 : (ln & 7) ^ swz<ROWS>(8 * sub + (ln >> 3));
+    From f;
+    f.lat = p.latent + row * (FP8 ? kR : 2 * kR) + 16 * c;
+    f.rope = p.rope + row * kD + 8 * c;
+    f.scale = FP8 ? p.lat_scale + row * (kR / 128) + (ln & 3) : nullptr;
+    return f;
   };
-  // 32 tokens from tb on, this wave's share of the RW waves, to LDS
-  auto fetch = [&](int tb, uint8_t* to) {
-    const int row = rows_of(tb);
+  constexpr int NL = FP8 ? 6 : 9;                    // loads of a block
+  auto ask = [&](const From& f, uint32_t to, auto i) {
+    if constexpr (i < NL - 1 - FP8) dma_b128<128 * i>(f.lat, to + i * kGroupB);
+    else if constexpr (i == NL - 1 - FP8) dma_b128<0>(f.rope, to + i * kGroupB);
+    else dma_b32(f.scale, to + i * kGroupB);
+  };
+  // this wave's blocks of 32 tokens; `to` is the tile, or (FP8) the wave's stage of codes
+  auto fetch = [&](int tb, uint32_t to) {
+#pragma unroll
+    for (int i = 0; i < NSUB; ++i) {
+      const int sub = rw * NSUB + i;
+      const From f = find(tb, sub);
+      unroll<NL>([&](auto u) { ask(f, to + (FP8 ? i * kRawB : sub * kBlockB), u); });
+    }
+  };
+  // Codes to bf16, exactly (power-of-two scales): the 16 codes of group i that this lane loaded, to
+  // chunks 2c and 2c + 1 of its token, c = lane % 8 + 8 i
+  auto spread = [&](int sub, int i, v4u codes, float sc, uint32_t to) {
     int ln = lane;
     asm volatile("" : "+v"(ln));
-    const uint32_t at = lds_at(to);
-    if constexpr (FP8) {
-#pragma unroll
-      for (int i = 0; i < kTok / 2 / RW; ++i) {
-        const int t = 2 * (i * RW + rw);
-        const int64_t src = __shfl(row, t + (ln >> 5));
-        dma_lanes(p.latent + src * kR + 16 * (ln & 31), at + t * kR);
-      }
-      const int64_t src = __shfl(row, ln & 31);
-      dma_lanes(p.lat_scale + src * (kR / 128), at + kCodeB + kTok * kRopeB);
+    const int t = ln >> 3, c = 2 * (ln & 3);
+    const uint32_t at = to + sub * kBlockB + (2 * i + ((ln & 7) >> 2)) * kGroupB + t * 128;
+    const int x = swz<ROWS>(8 * sub + t);
+    *(lds_v4u*)(uintptr_t)(at + ((c ^ x) << 4)) = __builtin_bit_cast(v4u, dequant8_bf16(codes.x, codes.y, sc));
+    *(lds_v4u*)(uintptr_t)(at + (((c + 1) ^ x) << 4)) = __builtin_bit_cast(v4u, dequant8_bf16(codes.z, codes.w, sc));
+  };
+  auto spread_rope = [&](int sub, v4u v, uint32_t to) {
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int t = ln >> 3;
+    *(lds_v4u*)(uintptr_t)(to + sub * kBlockB + 8 * kGroupB + t * 128 + (((ln & 7) ^ swz<ROWS>(8 * sub + t)) << 4)) = v;
+  };
+  // piece i < 5 of a block's codes from LDS: a group, or the rotated one
+  auto spread_raw = [&](int sub, auto i, uint32_t from, uint32_t to) {
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const v4u v = *(const lds_v4u*)(uintptr_t)(from + i * kGroupB + ln * 16);
+    if constexpr (i < 4) {
+      typedef const __attribute__((address_space(3))) float lds_f;
+      spread(sub, i, v, *(lds_f*)(uintptr_t)(from + 5 * kGroupB + (ln >> 3) * 32 + i * 4), to);
     } else {
-#pragma unroll
-      for (int i = 0; i < kTok / RW; ++i) {
-        const int t = i * RW + rw;
-        const int64_t src = __builtin_amdgcn_readlane(row, t);
-        dma_row(p.latent + src * kRowB, (uint32_t)(ln ^ lat_swz(t)) << 4, at + t * kRowB);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kTok / 8 / RW; ++i) {
-      const int t = 8 * (i * RW + rw) + (ln >> 3);
-      const int64_t src = __shfl(row, t);
-      const int c = (ln & 7) ^ (FP8 ? 0 : rope_swz(t));
-      dma_lanes(p.rope + src * kD + 8 * c, at + (FP8 ? kCodeB : kLatB) + 8 * (i * RW + rw) * kRopeB);
+      spread_rope(sub, v, to);
     }
   };
-  constexpr int NB = (FP8 ? kTok / 2 / RW + 1 : kTok / RW) + kTok / 8 / RW;   // loads of a fetch
-  // 16 codes to 32 bytes of bf16, exactly (power-of-two scales), at chunks 2c and 2c + 1 of token t
-  auto spread = [&](int t, int c, v4u codes, float sc) {
-    uint8_t* dst = tile + t * kRowB;
-    *reinterpret_cast<v4u*>(dst + (((2 * c) ^ lat_swz(t)) << 4)) = __builtin_bit_cast(v4u, dequant8_bf16(codes.x, codes.y, sc));
-    *reinterpret_cast<v4u*>(dst + (((2 * c + 1) ^ lat_swz(t)) << 4)) = __builtin_bit_cast(v4u, dequant8_bf16(codes.z, codes.w, sc));
-  };
-  // FP8, RW = 1: the tile in registers
-  v4u code_reg[kTok / 2], rope_reg[kTok / 8];
-  float scale_reg[kTok / 2];
+  // FP8, RW = 1: the codes in registers
+  v4u code_reg[16], rope_reg[4];
+  float scale_reg[16];
   auto fetch_regs = [&](int tb) {
-    const int row = rows_of(tb);
-    int ln = lane;
-    asm volatile("" : "+v"(ln));
 #pragma unroll
-    for (int i = 0; i < kTok / 2; ++i) {
-      const int64_t src = __shfl(row, 2 * i + (ln >> 5));
-      code_reg[i] = *reinterpret_cast<const v4u*>(p.latent + src * kR + 16 * (ln & 31));
-      scale_reg[i] = p.lat_scale[src * (kR / 128) + ((ln & 31) >> 3)];
-    }
+    for (int s = 0; s < 4; ++s) {
+      const From f = find(tb, s);
 #pragma unroll
-    for (int i = 0; i < kTok / 8; ++i) {
-      const int64_t src = __shfl(row, 8 * i + (ln >> 3));
-      rope_reg[i] = *reinterpret_cast<const v4u*>(p.rope + src * kD + 8 * (ln & 7));
+      for (int i = 0; i < 4; ++i) {
+        code_reg[4 * s + i] = *reinterpret_cast<const v4u*>(f.lat + 128 * i);
+        scale_reg[4 * s + i] = (f.scale - (lane & 3))[i];
+      }
+      rope_reg[s] = *reinterpret_cast<const v4u*>(f.rope);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
+
+  // Operands are read kAhead fragments before their products: a wave is alone on its SIMD, so
+  // nothing else covers the LDS's latency.
+  v8bf x[kAhead];
+  Scores<ROWS> s;
+  v8bf pr[WIDE ? 2 : 1];
+  uint32_t ka[WIDE ? 4 : 2], va[4];
+  // the tile's addresses, opaque, or those made from them would stay in registers over the loop
+  auto keys_at = [&](uint32_t off) {
+    uint32_t at = key_at + off;
+    asm volatile("" : "+v"(at));
+#pragma unroll
+    for (int i = 0; i < (WIDE ? 4 : 2); ++i) ka[i] = at ^ (i * (WIDE ? 32 : 64));
+  };
+  auto values_at = [&](uint32_t off) {
+    uint32_t at = value_at + off;
+    asm volatile("" : "+v"(at));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) va[i] = at ^ (i * 32);
+  };
+  // fragment f of the keys: WIDE: K step f, 32 tokens; else K step f / 2, 16 tokens from 16 (f % 2)
+  auto key = [&](auto f) {
+    if constexpr (WIDE) x[f % kAhead] = lds_b128(ka[f % 4], f / 4 * kGroupB);
+    else x[f % kAhead] = lds_b128(ka[f / 2 % 2], f / 4 * kGroupB + f % 2 * 2 * kBlockB);
+  };
+  // and its product; the rotated part of Q comes from LDS two steps before it is needed
+  v8bf qr[PIPE ? 4 : 1];
+  auto score = [&](auto f, Scores<ROWS>& to) {
+    if constexpr (WIDE) {
+      if constexpr (f < QS) to.v = mfma_bf16(x[f % kAhead], q[f], to.v);
+      else to.v = mfma_bf16(x[f % kAhead], qr[(f - QS) % 4], to.v);
+      if constexpr (PIPE && f + 4 >= QS && f < QS) qr[(f + 4 - QS) % 4] = lds_b128(rest_at + lane * 16, (f + 4 - QS) * 1024);
+    } else {
+      to.v[f % 2] = mfma_bf16(x[f % kAhead], q[f / 2], to.v[f % 2]);
+    }
+  };
+  // fragment f of the values: WIDE: 32 channels from 32 (f / 2), 16 tokens from 16 (f % 2); else 16
+  // channels from 16 f, 32 tokens
+  auto value = [&](auto f) {
+    if constexpr (WIDE) {
+      constexpr int off = f / 4 * kGroupB + f % 2 * 2 * kBlockB;
+      x[f % kAhead] = lds_tr(va[f / 2 % 2 * 2], off, va[f / 2 % 2 * 2 + 1], off + kBlockB);
+    } else {
+      constexpr int off = f / 4 * kGroupB;
+      x[f % kAhead] = lds_tr(va[f % 4], off, va[f % 4], off + 2 * kBlockB);
+    }
+  };
+  auto product = [&](auto f) {
+    if constexpr (WIDE) acc_mfma<ROWS, f / 2>(x[f % kAhead], pr[f % 2]);
+    else acc_mfma<ROWS, f>(x[f % kAhead], pr[0]);
+  };
+  // masked places of the scores of tokens tb .. (only in tiles that some row does not see whole)
+  auto hide = [&](int tb) {
+    if (tb + kTok <= end_min) return;
+    unroll<Scores<ROWS>::N>([&](auto e) {
+      if (tb + GS * (e / 4) + 4 * g + e % 4 >= end) s.template set<e>(kNegInf);
+    });
+  };
+  // Scores to probabilities in kSoft pieces of a few instructions each
+  constexpr int NP = Scores<ROWS>::N / 2, kSoft = 2 * NP + 1 + NP / 4;
+  float top = 0.0f;
+  auto soft = [&](auto i) {
+    if constexpr (i < NP) {
+      top = fmaxf(fmaxf(i == 0 ? kNegInf : top, s.template get<2 * i>()), s.template get<2 * i + 1>());
+    } else if constexpr (i == NP) {
+      if (__any(top * p.scale2 > m + kLazy)) {
+        if (!WIDE) top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m, top * p.scale2);
+        const float a = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= a;
+        acc_settle();
+        unroll<2 * ROWS>([&](auto t) { acc_write<t>(acc_read<t>() * a); });
+        acc_settle();
+      }
+      top = m == kNegInf ? 0.0f : -m;
+    } else if constexpr (i <= 2 * NP) {
+      constexpr int e = 2 * (i - NP - 1);
+      const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s.template get<e>(), p.scale2, top));
+      const float z = __builtin_amdgcn_exp2f(__builtin_fmaf(s.template get<e + 1>(), p.scale2, top));
+      s.template set<e>(y);
+      s.template set<e + 1>(z);
+      l += y;
+      l += z;
+    } else {
+      constexpr int k = i - 2 * NP - 1;
+      v4u u;
+      unroll<4>([&](auto d) { u[(int)d] = pack2_bf16(s.template get<8 * k + 2 * d>(), s.template get<8 * k + 2 * d + 1>()); });
+      pr[k] = __builtin_bit_cast(v8bf, u);
+    }
+  };
+  auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
 
   const int n_steps = step1 - step0;
   const int t_seg = step0 * STEP + tw * kTok;        // this wave's first token
-  __syncthreads();                                   // the last tile's LDS is no longer read
-  if constexpr (RW > 1) {
-    wait_vmcnt<0>();
-    for (int k = 0; k < (FP8 ? ST : ST - 1) && k < n_steps; ++k)
-      fetch(t_seg + k * STEP, FP8 ? raw + k * kRawB : tile + k * kTileB);
-  } else if constexpr (FP8) {
-    if (t_seg < end_max && n_steps > 0) fetch_regs(t_seg);
-  }
-  int slot = 0;
-  for (int k = 0; k < n_steps; ++k) {
-    const int tb = t_seg + k * STEP;                 // first token of this wave
-    uint32_t slot_at = 0;
-    if constexpr (RW > 1 && !FP8) {
-      if (k + ST - 1 < n_steps) wait_vmcnt<(ST - 2) * NB>();
-      else wait_vmcnt<0>();
-      barrier_lds();                                 // everyone's share of tile k is here, tile k - 1 is done with
-      if (k + ST - 1 < n_steps) fetch(tb + (ST - 1) * STEP, tile + (slot == 0 ? ST - 1 : slot - 1) * kTileB);
-      slot_at = slot * kTileB;
-      slot = slot + 1 == ST ? 0 : slot + 1;
-    } else if constexpr (RW > 1) {
-      if (k + ST - 1 < n_steps) wait_vmcnt<(ST - 1) * NB>();
-      else wait_vmcnt<0>();
+  if constexpr (PIPE) {
+    // Two tiles at once: the scores of tile k + 1 are multiplied while the probabilities of tile k are
+    // made (vector instructions in the matrix instructions' shadow), then tile k's output is, while
+    // tile k + 3 is asked for.  One barrier a step, put before the last kAhead products of the output,
+    // whose operands are in registers by then: behind it tile k's place is free, tile k + 2 is there,
+    // and the reads of its first fragments run under those products.  Tiles past the segment's end
+    // are asked for too (the last token again and again), so that the counts stay the same.
+    // FP8: three places; codes are asked for one step earlier, and tile k + 2 is made of them under
+    // the products of tile k's output.
+    Scores<ROWS> t;
+    auto meet = [&](auto outstanding) {
+      wait_vmcnt<outstanding>();
       barrier_lds();
-      const uint8_t* from = raw + slot * kRawB;
-      int ln = lane;
-      asm volatile("" : "+v"(ln));
-#pragma unroll 4
-      for (int i = 0; i < kTok / 2 / RW; ++i) {
-        const int t = 2 * (i * RW + rw) + (ln >> 5), c = ln & 31;
-        const v4u w = *reinterpret_cast<const v4u*>(from + t * kR + 16 * c);
-        const float sc = reinterpret_cast<const float*>(from + kCodeB + kTok * kRopeB)[t * (kR / 128) + (c >> 3)];
-        spread(t, c, w, sc);
-      }
-#pragma unroll
-      for (int i = 0; i < kTok / 8 / RW; ++i) {
-        const int t = 8 * (i * RW + rw) + (ln >> 3), c = ln & 7;
-        *reinterpret_cast<v4u*>(tile + kLatB + t * kRopeB + ((c ^ rope_swz(t)) << 4)) =
-            *reinterpret_cast<const v4u*>(from + kCodeB + t * kRopeB + 16 * c);
-      }
-      barrier_lds();
-      if (k + ST < n_steps) fetch(tb + ST * STEP, raw + slot * kRawB);
-      slot = slot + 1 == ST ? 0 : slot + 1;
-    } else {
-      if (tb >= end_max) break;                      // the other token waves have the rest
-      if constexpr (FP8) {
-        int ln = lane;
-        asm volatile("" : "+v"(ln));
-#pragma unroll
-        for (int i = 0; i < kTok / 2; ++i) spread(2 * i + (ln >> 5), ln & 31, code_reg[i], scale_reg[i]);
-#pragma unroll
-        for (int i = 0; i < kTok / 8; ++i) {
-          const int t = 8 * i + (ln >> 3);
-          *reinterpret_cast<v4u*>(tile + kLatB + t * kRopeB + (((ln & 7) ^ rope_swz(t)) << 4)) = rope_reg[i];
-        }
-        if (k + 1 < n_steps && tb + STEP < end_max) fetch_regs(tb + STEP);
-      } else {
-        fetch(tb, tile);
-        wait_vmcnt<0>();
-      }
-    }
-
-    // scores of 32 tokens
-    v4f s[RT][2];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    // Operands are read kAhead fragments before their products: a wave is alone on its SIMD, so
-    // nothing else covers the LDS's latency.
-    v8bf x[kAhead];
-    uint32_t ka = key_at + slot_at, kr = key_rope_at + slot_at, va = value_at + slot_at;
-    asm volatile("" : "+v"(ka), "+v"(kr), "+v"(va));  // or the addresses below would stay in registers over the loop
-    auto key = [&](auto f) {                         // fragment f: K step f / 2, tokens 16 (f % 2) ..
-      constexpr int k = f / 2, tt = f % 2;
-      x[f % kAhead] = k < kR / 32 ? lds_b128(ka ^ (k % 4 * 64), k / 4 * 256 + tt * 16 * kRowB)
-                                  : lds_b128(kr ^ (k % 2 * 64), tt * 16 * kRopeB);
     };
-    unroll<kAhead>([&](auto f) { key(f); });
-    unroll<2 * kSteps>([&](auto f) {
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) s[rt][f % 2] = mfma_bf16(x[f % kAhead], q[rt][f / 2], s[rt][f % 2]);
-      if constexpr (f + kAhead < 2 * kSteps) key(std::integral_constant<int, f + kAhead>{});
-    });
-    auto value = [&](auto ct) { x[ct % kAhead] = lds_tr(va ^ (ct % 8 * 32), ct / 8 * 256); };
-    unroll<kAhead>([&](auto ct) { value(ct); });
-    __builtin_amdgcn_sched_barrier(0);
-
-    // probabilities
-    v8bf pr[RT];
-    unroll<RT>([&](auto rt) {
-      float x[8];
-      float top = kNegInf;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = s[rt][e >> 2][e & 3] * p.scale2;
-        if (tb + kTok > end_min && tb + 16 * (e >> 2) + 4 * g + (e & 3) >= end[rt]) x[e] = kNegInf;
-        top = fmaxf(top, x[e]);
+    auto next = [](int place) { return place + 1 == NT ? 0 : place + 1; };
+    if (n_steps > 0) {
+      if constexpr (FP8) {
+        for (int k = 0; k < 2; ++k) {
+          fetch(t_seg + k * STEP, raw_at);
+          wait_vmcnt<0>();
+          unroll<5>([&](auto i) { spread_raw(rw, i, raw_at, tile_at + k * kTileB); });
+          __builtin_amdgcn_s_waitcnt(0xc07f);        // lgkmcnt(0): the codes are read before others land on them
+        }
+        fetch(t_seg + 2 * STEP, raw_at);
+        barrier_lds();
+      } else {
+        for (int k = 0; k < NT - 1; ++k) fetch(t_seg + k * STEP, tile_at + k * kTileB);
+        meet(std::integral_constant<int, 2 * NL>{});
       }
-      if (__any(top > m[rt] + kLazy)) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float mn = fmaxf(m[rt], top);
-        const float a = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
-        m[rt] = mn;
-        l[rt] *= a;
-        acc_settle();
-        unroll<kCt>([&](auto ct) { acc_write<kCt * rt + ct>(acc_read<kCt * rt + ct>() * a); });
+      keys_at(0);
+      unroll<kAhead>([&](auto f) { key(f); });
+      s.clear();
+      unroll<NF>([&](auto f) {
+        fence();
+        score(f, s);
+        if constexpr (f + kAhead < NF) key(std::integral_constant<int, f + kAhead>{});
+      });
+      if constexpr (!FP8) meet(std::integral_constant<int, NL>{});
+      keys_at(kTileB);
+      unroll<kAhead>([&](auto f) { key(f); });
+    }
+    int place = 0;                                   // of tile k
+    for (int k = 0; k < n_steps; ++k) {
+      const int tb = t_seg + k * STEP;
+      hide(tb);
+      values_at(place * kTileB);
+      if (k + 1 < n_steps) {
+        t.clear();
+        unroll<NF>([&](auto f) {
+          fence();
+          score(f, t);
+          if constexpr (f + kAhead < NF) key(std::integral_constant<int, f + kAhead>{});
+          else value(std::integral_constant<int, f + kAhead - NF>{});
+          if constexpr (f < kSoft) soft(f);
+        });
+      } else {
+        unroll<kAhead>([&](auto f) { value(f); });
+        unroll<kSoft>([&](auto i) { soft(i); });
+        operands_settle();
       }
-      const float base = m[rt] == kNegInf ? 0.0f : m[rt];
+      const int two = next(next(place));             // of tile k + 2
+      const int free = next(two);                    // bf16: of tile k + 3
+      From f3;
+      if constexpr (FP8) wait_vmcnt<0>();            // the codes of tile k + 2, asked for a step ago
+      unroll<NV - kAhead>([&](auto f) {
+        fence();
+        product(f);
+        value(std::integral_constant<int, f + kAhead>{});
+        if constexpr (FP8) {
+          if constexpr (f % 4 == 0 && f / 4 < 5) spread_raw(rw, std::integral_constant<int, f / 4>{}, raw_at, tile_at + two * kTileB);
+          if constexpr (f == 18) f3 = find(tb + 3 * STEP, rw);
+          if constexpr (f >= 20) ask(f3, raw_at, std::integral_constant<int, f - 20>{});
+        } else {
+          if constexpr (f == 0) f3 = find(tb + 3 * STEP, rw);
+          if constexpr (f >= 4 && f % 2 == 0 && f < 4 + 2 * NL) ask(f3, tile_at + free * kTileB + rw * kBlockB, std::integral_constant<int, (f - 4) / 2>{});
+        }
+      });
+      place = next(place);
+      if constexpr (FP8) barrier_lds();
+      else meet(std::integral_constant<int, NL>{});
+      keys_at(next(place) * kTileB);
+      unroll<kAhead>([&](auto i) {
+        fence();
+        product(std::integral_constant<int, NV - kAhead + i>{});
+      });
+      unroll<kAhead>([&](auto f) { key(f); });
+      s = t;
+    }
+  } else {
+    if constexpr (RW > 1) {
+      for (int k = 0; k < (FP8 ? 2 : 1) && k < n_steps; ++k)
+        fetch(t_seg + k * STEP, FP8 ? raw_at + k * NSUB * kRawB : tile_at);
+    } else if constexpr (FP8) {
+      if (t_seg < end_max && n_steps > 0) fetch_regs(t_seg);
+    }
+    for (int k = 0; k < n_steps; ++k) {
+      const int tb = t_seg + k * STEP;               // first token of this wave
+      uint32_t off = 0;
+      if constexpr (RW > 1 && !FP8) {
+        off = (k & 1) * kTileB;
+        wait_vmcnt<0>();
+        barrier_lds();                               // everyone's share of tile k is here, tile k - 1 is done with
+        if (k + 1 < n_steps) fetch(tb + STEP, tile_at + (kTileB - off));
+      } else if constexpr (RW > 1) {
+        const uint32_t from = raw_at + (k & 1) * NSUB * kRawB;
+        if (k + 1 < n_steps) wait_vmcnt<NSUB * NL>();
+        else wait_vmcnt<0>();
+        barrier_lds();                               // tile k - 1 is done with
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = __builtin_amdgcn_exp2f(x[e] - base);
-        l[rt] += x[e];
+        for (int i = 0; i < NSUB; ++i)
+          unroll<5>([&](auto u) { spread_raw(rw * NSUB + i, u, from + i * kRawB, tile_at); });
+        barrier_lds();                               // tile k is whole
+        if (k + 2 < n_steps) fetch(tb + 2 * STEP, from);
+      } else {
+        if (tb >= end_max) break;                    // the other token waves have the rest
+        if constexpr (FP8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) spread(i, u, code_reg[4 * i + u], scale_reg[4 * i + u], tile_at);
+            spread_rope(i, rope_reg[i], tile_at);
+          }
+          if (k + 1 < n_steps && tb + STEP < end_max) fetch_regs(tb + STEP);
+        } else {
+          fetch(tb, tile_at);
+          wait_vmcnt<0>();
+        }
       }
-      const v4u u = {pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]), pack2_bf16(x[4], x[5]), pack2_bf16(x[6], x[7])};
-      pr[rt] = __builtin_bit_cast(v8bf, u);
-    });
-
-    // output
-    unroll<kCt>([&](auto ct) {
-      __builtin_amdgcn_sched_barrier(0);
-      unroll<RT>([&](auto rt) { acc_mfma<kCt * rt + ct>(x[ct % kAhead], pr[rt]); });
-      if constexpr (ct + kAhead < kCt) value(std::integral_constant<int, ct + kAhead>{});
-    });
+      keys_at(off);
+      values_at(off);
+      s.clear();
+      unroll<kAhead>([&](auto f) { key(f); });
+      unroll<NF>([&](auto f) {
+        fence();
+        score(f, s);
+        if constexpr (f + kAhead < NF) key(std::integral_constant<int, f + kAhead>{});
+        else value(std::integral_constant<int, f + kAhead - NF>{});
+      });
+      fence();
+      hide(tb);
+      unroll<kSoft>([&](auto i) { soft(i); });
+      operands_settle();
+      unroll<NV>([&](auto f) {
+        fence();
+        product(f);
+        if constexpr (f + kAhead < NV) value(std::integral_constant<int, f + kAhead>{});
+      });
+    }
   }
   acc_settle();
 
-  // the row's sum over the four g, then over the token waves
-  float* const red = reinterpret_cast<float*>(smem);   // [4 waves][m 16, l 16], then [4 waves][512][16 rows]
-  unroll<RT>([&](auto rt) {
-    l[rt] += __shfl_xor(l[rt], 16);
-    l[rt] += __shfl_xor(l[rt], 32);
+  // the row's sum over the g, then over the token waves
+  {
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int n = ln % ROWS, g = ln / ROWS;
+    float* const red = reinterpret_cast<float*>(smem);   // [4 waves][m ROWS, l ROWS], then [4 waves][channels][ROWS]
+    if (!WIDE) l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
     float part = 1.0f;                               // this token wave's weight
-    float mt = m[rt], lt = l[rt];
+    float mt = m, lt = l;
     if constexpr (TW > 1) {
       __syncthreads();
       if (g == 0) {
-        red[wave * 32 + n] = m[rt];
-        red[wave * 32 + 16 + n] = l[rt];
+        red[wave * 2 * ROWS + n] = m;
+        red[wave * 2 * ROWS + ROWS + n] = l;
       }
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < TW; ++k) mt = fmaxf(mt, red[(k * RW + rw) * 32 + n]);
+      for (int k = 0; k < TW; ++k) mt = fmaxf(mt, red[(k * RW + rw) * 2 * ROWS + n]);
       lt = 0.0f;
 #pragma unroll
       for (int k = 0; k < TW; ++k) {
-        const float mk = red[(k * RW + rw) * 32 + n];
-        if (mk > kNegInf) lt += red[(k * RW + rw) * 32 + 16 + n] * __builtin_amdgcn_exp2f(mk - mt);
+        const float mk = red[(k * RW + rw) * 2 * ROWS + n];
+        if (mk > kNegInf) lt += red[(k * RW + rw) * 2 * ROWS + ROWS + n] * __builtin_amdgcn_exp2f(mk - mt);
       }
-      part = m[rt] > kNegInf ? __builtin_amdgcn_exp2f(m[rt] - mt) : 0.0f;
-      __syncthreads();
-      float* ow = red + wave * 16 * kR;
-      unroll<kCt>([&](auto ct) {
-        const v4f v = acc_read<kCt * rt + ct>() * part;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ow[(16 * ct + 4 * g + e) * 16 + n] = v[e];
-      });
-      __syncthreads();
+      part = m > kNegInf ? __builtin_amdgcn_exp2f(m - mt) : 0.0f;
     }
-    // token wave tw adds and stores the channel tiles tw kCt / TW ..
-    const int r = (rw * RT + rt) * 16 + n;           // row of the tile
-    if (r_tile + r <= r_last) {
-      const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
+    const int r = rw * ROWS + n;                     // row of the tile
+    const bool mine = r_tile + r <= r_last;
+    const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
+    const int64_t orow = (int64_t)sq.q0 * p.H + r_tile + r;
+    const int64_t prow = (2 * (int64_t)w + (step0 == 0)) * M + r;
+    if (mine && tw == 0 && g == 0) {
       const float lse = lt > 0.0f ? mt + __builtin_log2f(lt) : kNegInf;
-      const int64_t orow = (int64_t)sq.q0 * p.H + r_tile + r;
-      const int64_t prow = (2 * (int64_t)w + (step0 == 0)) * M + r;
-      if (tw == 0 && g == 0) {
-        if (!whole) p.part_lse[prow] = lse;
-        else if (p.lse) p.lse[orow] = lse * kLn2;
-      }
-      auto put = [&](int ct, v4f v) {
-        v *= inv;
-        const int c = 16 * ct + 4 * g;
-        if (!whole) *reinterpret_cast<v4f*>(p.part_out + prow * kR + c) = v;
-        else store4(p, orow * kR + c, v);
-      };
-      if constexpr (TW > 1) {
-#pragma unroll 2
-        for (int ct = tw * (kCt / TW); ct < (tw + 1) * (kCt / TW); ++ct) {
-          v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int k = 0; k < TW; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += red[(k * RW + rw) * 16 * kR + (16 * ct + 4 * g + e) * 16 + n];
-          put(ct, v);
-        }
-      } else {
-        unroll<kCt>([&](auto ct) { put(ct, acc_read<kCt * rt + ct>()); });
-      }
+      if (!whole) p.part_lse[prow] = lse;
+      else if (p.lse) p.lse[orow] = lse * kLn2;
     }
-  });
+    auto put = [&](int c, v4f v) {
+      v *= inv;
+      if (!whole) *reinterpret_cast<v4f*>(p.part_out + prow * kR + c) = v;
+      else store4(p, orow * kR + c, v);
+    };
+    if constexpr (TW > 1) {
+      // LDS holds four waves' accumulators of NG / PASS groups at a time; token wave tw adds and
+      // stores its share of them
+      constexpr int PASS = ROWS / 16, PG = NG / PASS, OWN = PG / TW;
+      float* ow = red + wave * PG * 4 * 64;
+      unroll<PASS>([&](auto ps) {
+        __syncthreads();
+        unroll<PG>([&](auto i) { *reinterpret_cast<v4f*>(ow + (i * 64 + ln) * 4) = acc_read<ps * PG + i>() * part; });
+        __syncthreads();
+        if (mine)
+#pragma unroll 2
+          for (int i = tw * OWN; i < (tw + 1) * OWN; ++i) {
+            v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < TW; ++k) v += *reinterpret_cast<const v4f*>(red + (k * RW + rw) * PG * 4 * 64 + (i * 64 + ln) * 4);
+            put(GS * (ps * PG + i) + 4 * g, v);
+          }
+      });
+    } else if (mine) {
+      unroll<NG>([&](auto i) { put(GS * i + 4 * g, acc_read<i>()); });
+    }
+  }
   if (threadIdx.x == 0 && step0 == 0 && !whole) {
     // the share that finishes the tile is the first whose own end is not before, or snaps to, the tile's
     const int64_t last = ((plan.hi.end - plan.near) * plan.shares + plan.total - 1) / plan.total - 1;
     p.meta[w] = Meta{(int64_t)sq.q0 * p.H + r_tile, r_last - r_tile + 1, (int)last - w + 1};
   }
   }
+  wait_vmcnt<0>();                                   // loads under way to LDS end before the workgroup does
 }
 
 // Joins the parts of split row tiles with weights 2^(lse_k - max).  A workgroup
@@ -823,7 +1009,9 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
   p.ldq_h = a.ldq_h;
   p.ldr_t = a.ldr_t;
   p.ldr_h = a.ldr_h;
-  p.scale2 = a.scale * 1.4426950408889634f;
+  // |scale|, its sign on Q; 0 is taken as 2^-126, so that masked scores stay infinite and the others vanish
+  p.scale2 = std::max(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
+  p.flip = a.scale < 0.0f ? 0x80008000u : 0u;
   int bits = 0;
   while ((1 << bits) < a.ps) ++bits;
   p.ps_shift = 31 + bits;
@@ -840,24 +1028,24 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
   p.meta = static_cast<Meta*>(a.workspace);
   p.part_lse = reinterpret_cast<float*>(p.meta + kGrid);
   p.part_out = p.part_lse + (int64_t)kGrid * 2 * m;
-#define FP8BS_ATTN(RT_, RW_, TW_, F8_) \
-  hipLaunchKernelGGL((mla_attention_kernel<RT_, RW_, TW_, F8_>), dim3(kGrid), dim3(256), 0, stream, p)
+#define FP8BS_ATTN(ROWS_, RW_, TW_, F8_) \
+  hipLaunchKernelGGL((mla_attention_kernel<ROWS_, RW_, TW_, F8_>), dim3(kGrid), dim3(256), 0, stream, p)
   switch (m) {
     case 128:
-      if (a.fp8) FP8BS_ATTN(2, 4, 1, true);
-      else FP8BS_ATTN(2, 4, 1, false);
+      if (a.fp8) FP8BS_ATTN(32, 4, 1, true);
+      else FP8BS_ATTN(32, 4, 1, false);
       break;
     case 64:
-      if (a.fp8) FP8BS_ATTN(2, 2, 2, true);
-      else FP8BS_ATTN(2, 2, 2, false);
+      if (a.fp8) FP8BS_ATTN(32, 2, 2, true);
+      else FP8BS_ATTN(32, 2, 2, false);
       break;
     case 32:   // with codes waiting in registers there is no room for two row tiles a wave
-      if (a.fp8) FP8BS_ATTN(1, 2, 2, true);
-      else FP8BS_ATTN(2, 1, 4, false);
+      if (a.fp8) FP8BS_ATTN(16, 2, 2, true);
+      else FP8BS_ATTN(32, 1, 4, false);
       break;
     default:
-      if (a.fp8) FP8BS_ATTN(1, 1, 4, true);
-      else FP8BS_ATTN(1, 1, 4, false);
+      if (a.fp8) FP8BS_ATTN(16, 1, 4, true);
+      else FP8BS_ATTN(16, 1, 4, false);
   }
   hipLaunchKernelGGL(join_kernel, dim3(kJoin), dim3(256), 0, stream, p, m);
 #undef FP8BS_ATTN

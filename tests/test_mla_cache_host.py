@@ -157,4 +157,10 @@ def test_listing_check():
                  "\tscratch_store_dword off, v1, s0", "\tds_read_b128 a[4:7], v1"):
         with pytest.raises(RuntimeError):
             build.check_listing("x", asm + line + "\n")
+    mfma = "\t;;#ASMSTART\n\tv_mfma_f32_32x32x16_bf16 a[0x10:0x1f], v[8:11], v[12:15], a[0x10:0x1f]\n\t;;#ASMEND\n"
+    build.check_listing("x", "\tv_mov_b32_e32 v9, v1\n\ts_nop 1\n" + mfma)
+    build.check_listing("x", "\tv_mov_b32_e32 v9, v1\n\ts_nop 0\n\tds_read_b128 v[8:11], v1\n" + mfma)
+    for line in ("\tv_mov_b32_e32 v9, v1\n", "\tv_cvt_pk_bf16_f32 v15, v1, v2\n\ts_nop 0\n"):
+        with pytest.raises(RuntimeError):
+            build.check_listing("x", line + mfma)
     assert "mla_attention.hip" in build.OWN_AGPR_SOURCES
