@@ -255,7 +255,8 @@ __device__ __forceinline__ void barrier_lds() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// exclusive prefix sum over the workgroup's 256 threads; total gets the sum
+// exclusive prefix sum over the workgroup's WAVES waves; total gets the sum
+template <int WAVES = 4>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t x = v;
@@ -270,7 +271,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t&
   int64_t base = 0;
   total = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < WAVES; ++k) {
     if (k < wave) base += sums[k];
     total += sums[k];
   }
@@ -289,7 +290,10 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t&
 // the sequences (row tiles) and over the row tiles (costs).
 // ---------------------------------------------------------------------------
 constexpr int kStart = 2;    // a tile's queries and output, in steps
-constexpr int kLeast = 4;    // a share is no smaller, so that short work is not cut to pieces
+// A share is no smaller, so that short work is not cut to pieces: 128 cached tokens with 128 rows a
+// tile (a step is 32), one step of 128 with 16 rows.
+template <int M>
+constexpr int least() { return M == 128 ? 4 : M == 64 ? 2 : 1; }
 // A cut this near a tile's edge moves to it: a split costs the writing and
 // reading of M rows of float32 twice, about M / 16 steps' time.
 template <int M>
@@ -299,7 +303,7 @@ struct Cut {          // a place between two steps
   int tile;           // row tile of the batch
   int b, in_seq;      // its sequence, its index there
   int step;
-  int64_t end;        // costs up to the tile's end
+  int64_t end;        // cuts from this cost on snap to the tile's end
 };
 
 // values that all lanes share, moved to scalar registers
@@ -311,15 +315,22 @@ __device__ __forceinline__ Cut uniform(const Cut& c) {
   return Cut{uniform(c.tile), uniform(c.b), uniform(c.in_seq), uniform(c.step), uniform(c.end)};
 }
 
+constexpr int kSeqs = 8192;  // sequences whose lengths the plan holds in LDS
+
 template <int M, int STEP>
 struct Plan {
   Cut lo, hi;
   int64_t total;
-  int shares, near;
+  int shares;
 
-  static __device__ int tile_cost(const AttnParams& p, const Seq& s, int in_seq) {
+  static __device__ int tile_steps(const AttnParams& p, const Seq& s, int in_seq) {
     const int r = (int)min((int64_t)(in_seq + 1) * M, (int64_t)s.nq * p.H) - 1;
-    return kStart + (visible(p, s, r / p.H) + STEP - 1) / STEP;
+    return (visible(p, s, r / p.H) + STEP - 1) / STEP;
+  }
+  // A short chunk's tiles all cost what its last does (at most an eighth more than
+  // they take): equal costs, and cuts fall on the tiles' edges where their number allows.
+  static __device__ int tile_cost(const AttnParams& p, const Seq& s, int in_seq) {
+    return kStart + (s.nq <= s.len / 8 ? (s.len + STEP - 1) / STEP : tile_steps(p, s, in_seq));
   }
 
   // false: this workgroup has no share
@@ -327,16 +338,20 @@ struct Plan {
     int64_t* sums = reinterpret_cast<int64_t*>(smem);
     Cut* cut = reinterpret_cast<Cut*>(smem + 64);
     int* first = reinterpret_cast<int*>(smem + 256);       // [B + 1] row tiles before each sequence
+    Seq* seq = reinterpret_cast<Seq*>(smem + 256 + 4 * (kSeqs + 4));
     const int tid = threadIdx.x;
     const int per_b = (p.B + 255) / 256;
     const int b0 = min(tid * per_b, p.B), b1 = min(b0 + per_b, p.B);
     int64_t mine = 0, sum;
-    for (int b = b0; b < b1; ++b) mine += ((int64_t)load_seq(p, b).nq * p.H + M - 1) / M;
+    for (int b = b0; b < b1; ++b) {
+      seq[b] = load_seq(p, b);
+      mine += ((int64_t)seq[b].nq * p.H + M - 1) / M;
+    }
     int64_t at = block_scan(mine, sums, sum);
     const int tiles = (int)sum;
     for (int b = b0; b < b1; ++b) {
       first[b] = (int)at;
-      at += ((int64_t)load_seq(p, b).nq * p.H + M - 1) / M;
+      at += ((int64_t)seq[b].nq * p.H + M - 1) / M;
     }
     if (tid == 0) first[p.B] = tiles;
     __syncthreads();
@@ -351,32 +366,32 @@ struct Plan {
     }
     mine = 0;
     const int bs = b;
-    Seq s = load_seq(p, b);
     for (int t = t0; t < t1; ++t) {
-      while (t >= first[b + 1]) s = load_seq(p, ++b);
-      mine += tile_cost(p, s, t - first[b]);
+      while (t >= first[b + 1]) ++b;
+      mine += tile_cost(p, seq[b], t - first[b]);
     }
     int64_t base = block_scan(mine, sums, total);
-    shares = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kLeast));
+    total = uniform(total);
+    shares = (int)max((int64_t)1, min((int64_t)gridDim.x, total / least<M>()));
     if (w >= shares || total == 0) return false;
 
-    near = uniform(slack<M>(total, shares));
+    const int near = slack<M>(total, shares);
     const int64_t want[2] = {total * w / shares, total * (w + 1) / shares};
     if (t1 == tiles && t0 < t1 && want[1] == total) cut[1] = Cut{tiles, p.B, 0, 0, total};
     if (t0 < t1 && ((want[0] >= base && want[0] < base + mine) || (want[1] >= base && want[1] < base + mine))) {
       b = bs;
-      s = load_seq(p, b);
       for (int t = t0; t < t1; ++t) {
-        while (t >= first[b + 1]) s = load_seq(p, ++b);
-        const int c = tile_cost(p, s, t - first[b]);
+        while (t >= first[b + 1]) ++b;
+        const int in_seq = t - first[b], c = tile_cost(p, seq[b], in_seq);
+        const int done = min(c - near, kStart + tile_steps(p, seq[b], in_seq));
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           if (want[k] >= base && want[k] < base + c) {
             const int at = (int)(want[k] - base);
             // (tile t + 1 may be the next sequence's first: the share that begins there looks)
-            if (at <= kStart + near) cut[k] = Cut{t, b, t - first[b], 0, base + c};
-            else if (at >= c - near) cut[k] = Cut{t + 1, b, t + 1 - first[b], 0, base + c};
-            else cut[k] = Cut{t, b, t - first[b], at - kStart, base + c};
+            if (at <= kStart + near) cut[k] = Cut{t, b, in_seq, 0, base + done};
+            else if (at >= done) cut[k] = Cut{t + 1, b, in_seq + 1, 0, base + done};
+            else cut[k] = Cut{t, b, in_seq, at - kStart, base + done};
           }
         base += c;
       }
@@ -384,8 +399,6 @@ struct Plan {
     __syncthreads();
     lo = uniform(cut[0]);
     hi = uniform(cut[1]);
-    total = uniform(total);
-    shares = uniform(shares);
     __syncthreads();
     return true;
   }
@@ -870,16 +883,17 @@ mla_attention_kernel(AttnParams p) {
     const bool mine = r_tile + r <= r_last;
     const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
     const int64_t orow = (int64_t)sq.q0 * p.H + r_tile + r;
-    const int64_t prow = (2 * (int64_t)w + (step0 == 0)) * M + r;
-    if (mine && tw == 0 && g == 0) {
+    const int64_t slot = 2 * (int64_t)w + (step0 == 0);
+    if (tw == 0 && g == 0) {
       const float lse = lt > 0.0f ? mt + __builtin_log2f(lt) : kNegInf;
-      if (!whole) p.part_lse[prow] = lse;
-      else if (p.lse) p.lse[orow] = lse * kLn2;
+      if (!whole) p.part_lse[slot * M + r] = lse;
+      else if (mine && p.lse) p.lse[orow] = lse * kLn2;
     }
-    auto put = [&](int c, v4f v) {
+    // group i of accumulators; a part keeps the registers' order, [RW][NG][lane][4], whole lines a store
+    auto put = [&](int i, v4f v) {
       v *= inv;
-      if (!whole) *reinterpret_cast<v4f*>(p.part_out + prow * kR + c) = v;
-      else store4(p, orow * kR + c, v);
+      if (!whole) *reinterpret_cast<v4f*>(p.part_out + ((slot * RW + rw) * NG + i) * 256 + 4 * ln) = v;
+      else if (mine) store4(p, orow * kR + GS * i + 4 * g, v);
     };
     if constexpr (TW > 1) {
       // LDS holds four waves' accumulators of NG / PASS groups at a time; token wave tw adds and
@@ -890,48 +904,55 @@ mla_attention_kernel(AttnParams p) {
         __syncthreads();
         unroll<PG>([&](auto i) { *reinterpret_cast<v4f*>(ow + (i * 64 + ln) * 4) = acc_read<ps * PG + i>() * part; });
         __syncthreads();
-        if (mine)
 #pragma unroll 2
           for (int i = tw * OWN; i < (tw + 1) * OWN; ++i) {
             v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < TW; ++k) v += *reinterpret_cast<const v4f*>(red + (k * RW + rw) * PG * 4 * 64 + (i * 64 + ln) * 4);
-            put(GS * (ps * PG + i) + 4 * g, v);
+            put(ps * PG + i, v);
           }
       });
-    } else if (mine) {
-      unroll<NG>([&](auto i) { put(GS * i + 4 * g, acc_read<i>()); });
+    } else {
+      unroll<NG>([&](auto i) { put(i, acc_read<i>()); });
     }
   }
   if (threadIdx.x == 0 && step0 == 0 && !whole) {
-    // the share that finishes the tile is the first whose own end is not before, or snaps to, the tile's
-    const int64_t last = ((plan.hi.end - plan.near) * plan.shares + plan.total - 1) / plan.total - 1;
+    // the share that finishes the tile is the first whose own end is at, or snaps to, the tile's
+    const int64_t last = (plan.hi.end * plan.shares + plan.total - 1) / plan.total - 1;
     p.meta[w] = Meta{(int64_t)sq.q0 * p.H + r_tile, r_last - r_tile + 1, (int)last - w + 1};
   }
   }
   wait_vmcnt<0>();                                   // loads under way to LDS end before the workgroup does
 }
 
-// Joins the parts of split row tiles with weights 2^(lse_k - max).  A workgroup
-// finds the split tiles (one thread per share), then takes rows of them in
-// turn: two halves of 128 threads, each over every second part, 16 bytes a
-// thread.  Bound by reading the parts; rows, not tiles, are dealt out, so that
-// one tile in 128 parts and 128 tiles in two keep all CUs busy alike.
+// Joins the parts of split row tiles with weights 2^(lse_k - max), in the order
+// of the accumulators that they were written in: a lane has one row and 4
+// channels of each group, so its weights are its own.  Bound by reading the
+// parts.  A workgroup finds the split tiles (a thread per share) and takes items
+// of them in turn: of a tile in few parts a wave does kRun groups of one row
+// wave; of one in many, the eight waves share the parts of kRunMany groups and
+// meet in LDS, so that one tile in 128 parts and 128 tiles in two keep the card
+// busy alike.
 constexpr int kGrid = 256;    // shares: the MI355X's CUs
-constexpr int kJoin = 1024;   // workgroups
-__global__ void __launch_bounds__(256) join_kernel(AttnParams p, int M) {
+constexpr int kJoin = 1024;   // workgroups of eight waves
+constexpr int kFew = 16, kRun = 8, kRunMany = 2;
+template <int ROWS>
+__global__ void __launch_bounds__(512) join_kernel(AttnParams p, int RW) {
+  constexpr int GS = Scores<ROWS>::TS, NG = kR / GS;
   __shared__ Meta metas[kGrid];
-  __shared__ int64_t sums[4];
+  __shared__ int64_t sums[8];
   __shared__ int before[kGrid + 1];
-  __shared__ float lse_max[4], weight[kGrid];
-  __shared__ v4f half[128];
-  const int tid = threadIdx.x;
-  const Meta mine = p.meta[tid];
-  metas[tid] = mine;
-  int64_t all;
-  const int64_t at = block_scan(mine.parts ? mine.rows : 0, sums, all);
-  before[tid] = (int)at;
-  if (tid == 0) before[kGrid] = (int)all;
+  __shared__ __attribute__((aligned(16))) float meet[8][kRunMany + 1][64][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int M = ROWS * RW;
+  int64_t items = 0, all;
+  if (tid < kGrid) {
+    const Meta mine = p.meta[tid];
+    metas[tid] = mine;
+    items = mine.parts == 0 ? 0 : mine.parts <= kFew ? (RW * (NG / kRun) + 7) / 8 : RW * (NG / kRunMany);
+  }
+  const int64_t at = block_scan<8>(items, sums, all);
+  if (tid < kGrid) before[tid] = (int)at;
   __syncthreads();
   for (int item = blockIdx.x; item < (int)all; item += gridDim.x) {
     int w = 0;                                       // the last share with before[w] <= item
@@ -939,42 +960,73 @@ __global__ void __launch_bounds__(256) join_kernel(AttnParams p, int M) {
     for (int s = kGrid / 2; s; s >>= 1)
       if (before[w + s] <= item) w += s;
     const Meta meta = metas[w];
-    const int r = item - before[w];
+    const int u = item - before[w];
+    const int n = lane % ROWS, g = lane / ROWS;
     // part 0 is slot 1 of share w, part k slot 0 of share w + k
-    auto slot = [&](int k) { return (k == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + k)) * M + r; };
-    const float l = tid < meta.parts ? p.part_lse[slot(tid)] : kNegInf;
-    float top = l;
+    auto slot = [&](int k) { return k == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + k); };
+    auto finish = [&](int r, int i, v4f v, float inv) {
+      if (r < meta.rows) store4(p, (meta.row + r) * kR + GS * i + 4 * g, v * inv);
+    };
+    if (meta.parts <= kFew) {
+      const int unit = 8 * u + wave;
+      if (unit >= RW * (NG / kRun)) continue;
+      const int rw = unit / (NG / kRun), i0 = unit % (NG / kRun) * kRun, r = rw * ROWS + n;
+      float top = kNegInf, sum = 0.0f;
+      for (int k = 0; k < meta.parts; ++k) top = fmaxf(top, p.part_lse[slot(k) * M + r]);
+      const float base = top == kNegInf ? 0.0f : top;
+      v4f acc[kRun];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    __syncthreads();                                 // the last row's weights and halves are used
-    if ((tid & 63) == 0) lse_max[tid >> 6] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(lse_max[0], lse_max[1]), fmaxf(lse_max[2], lse_max[3]));
-    weight[tid] = top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(l - top);
-    __syncthreads();
-    const int c = 4 * (tid & 127), odd = tid >> 7;
-    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    float sum = 0.0f;
-    for (int k = odd; k < meta.parts; k += 16) {
-      v4f v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u)                    // parts past the last read that one again, weighing nothing
-        v[u] = *reinterpret_cast<const v4f*>(p.part_out + slot(min(k + 2 * u, meta.parts - 1)) * kR + c);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float x = k + 2 * u < meta.parts ? weight[k + 2 * u] : 0.0f;
-        acc += v[u] * x;
+      for (int i = 0; i < kRun; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+      for (int k = 0; k < meta.parts; ++k) {
+        const float x = __builtin_amdgcn_exp2f(p.part_lse[slot(k) * M + r] - base);
+        const float* src = p.part_out + ((slot(k) * RW + rw) * NG + i0) * 256 + 4 * lane;
         sum += x;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) acc[i] += *reinterpret_cast<const v4f*>(src + i * 256) * x;
       }
-    }
-    if (odd) half[tid & 127] = acc;
-    if (tid == 128) lse_max[0] = sum;
-    __syncthreads();
-    if (!odd) {
-      acc += half[tid];
-      sum += lse_max[0];
-      store4(p, (meta.row + r) * kR + c, acc * (sum > 0.0f ? 1.0f / sum : 0.0f));
-      if (tid == 0 && p.lse) p.lse[meta.row + r] = sum > 0.0f ? (top + __builtin_log2f(sum)) * kLn2 : kNegInf;
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) finish(r, i0 + i, acc[i], inv);
+      if (i0 == 0 && g == 0 && r < meta.rows && p.lse)
+        p.lse[meta.row + r] = sum > 0.0f ? (top + __builtin_log2f(sum)) * kLn2 : kNegInf;
+    } else {
+      const int rw = u / (NG / kRunMany), i0 = u % (NG / kRunMany) * kRunMany, r = rw * ROWS + n;
+      float top = kNegInf, sum = 0.0f;
+      for (int k = wave; k < meta.parts; k += 8) top = fmaxf(top, p.part_lse[slot(k) * M + r]);
+      __syncthreads();                               // the last item's sums are used
+      meet[wave][kRunMany][lane][0] = top;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, meet[k][kRunMany][lane][0]);
+      const float base = top == kNegInf ? 0.0f : top;
+      v4f acc[kRunMany];
+#pragma unroll
+      for (int i = 0; i < kRunMany; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+      for (int k = wave; k < meta.parts; k += 8) {
+        const float x = __builtin_amdgcn_exp2f(p.part_lse[slot(k) * M + r] - base);
+        const float* src = p.part_out + ((slot(k) * RW + rw) * NG + i0) * 256 + 4 * lane;
+        sum += x;
+#pragma unroll
+        for (int i = 0; i < kRunMany; ++i) acc[i] += *reinterpret_cast<const v4f*>(src + i * 256) * x;
+      }
+#pragma unroll
+      for (int i = 0; i < kRunMany; ++i) *reinterpret_cast<v4f*>(meet[wave][i][lane]) = acc[i];
+      meet[wave][kRunMany][lane][1] = sum;
+      __syncthreads();
+      if (wave < kRunMany) {
+        sum = 0.0f;
+        v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          v += *reinterpret_cast<const v4f*>(meet[k][wave][lane]);
+          sum += meet[k][kRunMany][lane][1];
+        }
+        finish(r, i0 + wave, v, sum > 0.0f ? 1.0f / sum : 0.0f);
+        if (i0 == 0 && wave == 0 && g == 0 && r < meta.rows && p.lse)
+          p.lse[meta.row + r] = sum > 0.0f ? (top + __builtin_log2f(sum)) * kLn2 : kNegInf;
+      }
     }
   }
 }
@@ -1047,7 +1099,8 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
       if (a.fp8) FP8BS_ATTN(16, 1, 4, true);
       else FP8BS_ATTN(16, 1, 4, false);
   }
-  hipLaunchKernelGGL(join_kernel, dim3(kJoin), dim3(256), 0, stream, p, m);
+  if (m == 16 || (m == 32 && a.fp8)) hipLaunchKernelGGL(join_kernel<16>, dim3(kJoin), dim3(512), 0, stream, p, m / 16);
+  else hipLaunchKernelGGL(join_kernel<32>, dim3(kJoin), dim3(512), 0, stream, p, m / 32);
 #undef FP8BS_ATTN
   return hipGetLastError();
 }
