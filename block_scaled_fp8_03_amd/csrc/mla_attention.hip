@@ -438,7 +438,7 @@ mla_attention_kernel(AttnParams p) {
   constexpr int NSUB = 4 / RW;                       // blocks of 8 tokens that a wave loads of 32
   constexpr int CH = 8 * 64 / ROWS;                  // channels of a K step of the scores
   constexpr int QN = (kR + kD) / CH;                 // K steps
-  constexpr int QS = PIPE ? kR / CH : QN;            // those whose Q is in registers; PIPE: the rotated ones are in LDS
+  constexpr int QS = PIPE && WIDE ? kR / CH : QN;          // those whose Q is in registers; PIPE: the rotated ones are in LDS
   constexpr int NV = 32;                             // fragments of the latents as values
   constexpr int NF = 36;                             // fragments of the latents as keys
   constexpr int GS = Scores<ROWS>::TS, NG = kR / GS; // accumulators: NG groups of 4 channels from GS i + 4 g
@@ -488,26 +488,6 @@ mla_attention_kernel(AttnParams p) {
 
   wait_vmcnt<0>();
   __syncthreads();                                   // the last tile's LDS is no longer read or written
-
-  // this lane's query row: its operands, and the tokens it sees
-  v8bf q[QS];
-  int end;
-  {
-    int ln = lane;
-    asm volatile("" : "+v"(ln));                     // addresses made here, and in the end, do not stay in registers
-    const int r = min(r_tile + rw * ROWS + ln % ROWS, r_last);
-    const int i = r / p.H, h = r - i * p.H;
-    end = visible(p, sq, i);
-    const uint16_t* ql = p.q_lat + (sq.q0 + i) * p.ldq_t + h * p.ldq_h + 8 * (ln / ROWS);
-    const uint16_t* qr = p.q_rope + (sq.q0 + i) * p.ldr_t + h * p.ldr_h + 8 * (ln / ROWS);
-#pragma unroll
-    for (int s = 0; s < QN; ++s) {
-      v4u v = *reinterpret_cast<const v4u*>(s < kR / CH ? ql + CH * s : qr + CH * s - kR);
-      v ^= p.flip;
-      if (s < QS) q[s] = __builtin_bit_cast(v8bf, v);
-      else *((lds_v4u*)(uintptr_t)(rest_at + ln * 16) + (s - QS) * 64) = v;
-    }
-  }
 
   float m = kNegInf, l = 0.0f;
   unroll<2 * ROWS>([&](auto i) { acc_write<i>(v4f{0.0f, 0.0f, 0.0f, 0.0f}); });
@@ -606,6 +586,34 @@ mla_attention_kernel(AttnParams p) {
     __builtin_amdgcn_sched_barrier(0);
   };
 
+  const int n_steps = step1 - step0;
+  const int t_seg = step0 * STEP + tw * kTok;        // this wave's first token
+  if (PIPE && n_steps > 0) {                         // the first tokens are on their way before Q
+    if constexpr (FP8) fetch(t_seg, raw_at);
+    else if constexpr (PIPE)
+      for (int k = 0; k < NT - 1; ++k) fetch(t_seg + k * STEP, tile_at + k * kTileB);
+  }
+
+  // this lane's query row: its operands, and the tokens it sees
+  v8bf q[QS];
+  int end;
+  {
+    int ln = lane;
+    asm volatile("" : "+v"(ln));                     // addresses made here, and in the end, do not stay in registers
+    const int r = min(r_tile + rw * ROWS + ln % ROWS, r_last);
+    const int i = r / p.H, h = r - i * p.H;
+    end = visible(p, sq, i);
+    const uint16_t* ql = p.q_lat + (sq.q0 + i) * p.ldq_t + h * p.ldq_h + 8 * (ln / ROWS);
+    const uint16_t* qr = p.q_rope + (sq.q0 + i) * p.ldr_t + h * p.ldr_h + 8 * (ln / ROWS);
+#pragma unroll
+    for (int s = 0; s < QN; ++s) {
+      v4u v = *reinterpret_cast<const v4u*>(s < kR / CH ? ql + CH * s : qr + CH * s - kR);
+      v ^= p.flip;
+      if (s < QS) q[s] = __builtin_bit_cast(v8bf, v);
+      else *((lds_v4u*)(uintptr_t)(rest_at + ln * 16) + (s - QS) * 64) = v;
+    }
+  }
+
   // Operands are read kAhead fragments before their products: a wave is alone on its SIMD, so
   // nothing else covers the LDS's latency.
   v8bf x[kAhead];
@@ -699,8 +707,6 @@ mla_attention_kernel(AttnParams p) {
   };
   auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
 
-  const int n_steps = step1 - step0;
-  const int t_seg = step0 * STEP + tw * kTok;        // this wave's first token
   if constexpr (PIPE) {
     // Two tiles at once: the scores of tile k + 1 are multiplied while the probabilities of tile k are
     // made (vector instructions in the matrix instructions' shadow), then tile k's output is, while
@@ -719,7 +725,7 @@ mla_attention_kernel(AttnParams p) {
     if (n_steps > 0) {
       if constexpr (FP8) {
         for (int k = 0; k < 2; ++k) {
-          fetch(t_seg + k * STEP, raw_at);
+          if (k) fetch(t_seg + k * STEP, raw_at);
           wait_vmcnt<0>();
           unroll<5>([&](auto i) { spread_raw(rw, i, raw_at, tile_at + k * kTileB); });
           __builtin_amdgcn_s_waitcnt(0xc07f);        // lgkmcnt(0): the codes are read before others land on them
@@ -727,7 +733,6 @@ mla_attention_kernel(AttnParams p) {
         fetch(t_seg + 2 * STEP, raw_at);
         barrier_lds();
       } else {
-        for (int k = 0; k < NT - 1; ++k) fetch(t_seg + k * STEP, tile_at + k * kTileB);
         meet(std::integral_constant<int, 2 * NL>{});
       }
       keys_at(0);
@@ -1031,10 +1036,39 @@ __global__ void __launch_bounds__(512) join_kernel(AttnParams p, int RW) {
   }
 }
 
-// rows of an average sequence decide the tile
-int tile_rows(int64_t T, int64_t H, int64_t B) {
-  const int64_t per = T * H / B;
-  return per >= 96 ? 128 : per >= 48 ? 64 : per >= 24 ? 32 : 16;
+// The rows of a tile.  More rows read the cache fewer times and multiply at a
+// better rate; fewer have less to set up, to split and to join.  The estimate is
+// start + unit * (32 cached tokens' steps a share), in us, as measured with 16 to
+// 128 heads, 1 to 128 sequences of 300 to 100000 tokens and 1 to 128 new ones (a
+// graph of calls, bf16 / fp8; 128-row tiles: 1.75 / 2.15 us a unit when the matrix
+// cores bound it).  It takes the table's width for the sequences' length.
+// Measured both ways (us, bf16): 32 x 4096, 128 heads: 64 rows 76, 128 rows 81; 128
+// new tokens on 8192, 128 heads: 313 / 265; 32 x 4096, 16 heads: 16 rows 52, 64
+// rows 55, 128 rows 72; 16 new tokens each on 4 x 2000, 16 heads: 16 rows 37, 64
+// rows 45; fp8, 128 x 4096, 32 heads: 32 rows 118, 16 rows 131.
+struct TileCost {
+  int m;
+  float start[2], unit[2];   // bf16, fp8
+};
+constexpr TileCost kTiles[] = {
+    {16, {21, 22}, {0.65f, 0.8f}}, {32, {25, 26}, {1.0f, 1.3f}}, {64, {31, 33}, {1.2f, 1.6f}}, {128, {40, 42}, {1.9f, 2.2f}}};
+
+// the largest tile that an average sequence's rows fill by half
+int most_rows(int64_t T, int64_t H, int64_t B) {
+  const int64_t per = (T * H + B - 1) / B;
+  return per > 64 ? 128 : per > 32 ? 64 : per > 16 ? 32 : 16;
+}
+int tile_rows(int64_t T, int64_t H, int64_t B, int64_t len, bool fp8) {
+  const int most = most_rows(T, H, B);
+  int best = 16;
+  double least = 1e30;
+  for (const TileCost& c : kTiles) {
+    if (c.m > most) break;
+    const double tiles = (double)B * ((T * H + B * c.m - 1) / (B * c.m));
+    const double us = c.start[fp8] + c.unit[fp8] * std::ceil(tiles * ((len + kTok - 1) / kTok) / kGrid);
+    if (us < least) least = us, best = c.m;
+  }
+  return best;
 }
 
 constexpr int64_t part_bytes(int m) { return (int64_t)kGrid * 2 * m * (kR + 1) * 4; }
@@ -1042,7 +1076,7 @@ constexpr int64_t part_bytes(int m) { return (int64_t)kGrid * 2 * m * (kR + 1) *
 }  // namespace
 
 int64_t mla_attention_workspace_bytes(int64_t T, int64_t H, int64_t B) {
-  return kGrid * (int64_t)sizeof(Meta) + part_bytes(tile_rows(T, H, B));
+  return kGrid * (int64_t)sizeof(Meta) + part_bytes(most_rows(T, H, B));
 }
 
 hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
@@ -1076,7 +1110,7 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
   p.ps = (int)a.ps;
   p.causal = a.causal;
   p.out_f32 = a.out_f32;
-  const int m = tile_rows(a.T, a.H, a.B);
+  const int m = tile_rows(a.T, a.H, a.B, a.W * a.ps, a.fp8);
   p.meta = static_cast<Meta*>(a.workspace);
   p.part_lse = reinterpret_cast<float*>(p.meta + kGrid);
   p.part_out = p.part_lse + (int64_t)kGrid * 2 * m;
@@ -1088,19 +1122,19 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
       else FP8BS_ATTN(32, 4, 1, false);
       break;
     case 64:
-      if (a.fp8) FP8BS_ATTN(32, 2, 2, true);
-      else FP8BS_ATTN(32, 2, 2, false);
+      if (a.fp8) FP8BS_ATTN(16, 4, 1, true);
+      else FP8BS_ATTN(16, 4, 1, false);
       break;
-    case 32:   // with codes waiting in registers there is no room for two row tiles a wave
+    case 32:
       if (a.fp8) FP8BS_ATTN(16, 2, 2, true);
-      else FP8BS_ATTN(32, 1, 4, false);
+      else FP8BS_ATTN(16, 2, 2, false);
       break;
     default:
       if (a.fp8) FP8BS_ATTN(16, 1, 4, true);
       else FP8BS_ATTN(16, 1, 4, false);
   }
-  if (m == 16 || (m == 32 && a.fp8)) hipLaunchKernelGGL(join_kernel<16>, dim3(kJoin), dim3(512), 0, stream, p, m / 16);
-  else hipLaunchKernelGGL(join_kernel<32>, dim3(kJoin), dim3(512), 0, stream, p, m / 32);
+  if (m == 128) hipLaunchKernelGGL(join_kernel<32>, dim3(kJoin), dim3(512), 0, stream, p, 4);
+  else hipLaunchKernelGGL(join_kernel<16>, dim3(kJoin), dim3(512), 0, stream, p, m / 16);
 #undef FP8BS_ATTN
   return hipGetLastError();
 }
