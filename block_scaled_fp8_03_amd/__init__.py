@@ -477,54 +477,70 @@ def mla_cache_alloc(pages: int, page_size: int, device, dtype=torch.bfloat16) ->
     return MlaCache(latent, rope, scale)
 
 
+_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+_LATENT = (torch.bfloat16, *_F8)
+
+
+def _ptr(t: torch.Tensor, name: str, dtypes, shape, dev) -> int:
+    """The address of a contiguous tensor of one of `dtypes`, of `shape`, on device `dev`."""
+    if t.dtype in dtypes and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    _need(t, dtypes, name)
+    raise ValueError(f"{name} lies on {t.device}, other tensors on {dev}")
+
+
+def _rows3(t: torch.Tensor, name: str, shape, dev):
+    """A bf16 [T, H, width] view with a dense last dimension: (pointer, token stride, head stride)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected bfloat16")
+    if t.device != dev:
+        raise ValueError(f"{name} lies on {t.device}, other tensors on {dev}")
+    st, sh, sw = t.stride()
+    T, H, _ = shape
+    if sw != 1 and T * H > 0:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return t.data_ptr(), (st if T > 1 else 0), (sh if H > 1 else 0)
+
+
 def _cache_args(cache: MlaCache):
-    """(latent, scale, rope, format, P, ps), checked."""
+    """(device, latent, scale, rope, format, P, ps), checked."""
     lat, rope, scale = cache
-    if not isinstance(lat, torch.Tensor) or lat.dim() != 3 or lat.shape[2] != MLA_RANK:
+    dev = lat.device
+    if dev.type != "cuda":
+        raise ValueError("cache.latent must be a device tensor")
+    if lat.dim() != 3:
         raise ValueError(f"cache.latent must be [P, ps, {MLA_RANK}]")
-    P, ps = lat.shape[:2]
-    if tuple(rope.shape) != (P, ps, MLA_ROPE):
-        raise ValueError(f"cache.rope must be [P, ps, {MLA_ROPE}]")
+    P, ps, _ = lat.shape
     bf16 = lat.dtype == torch.bfloat16
     if bf16 != (scale is None):
         raise ValueError("cache.scale goes with a float8_e4m3fn cache, and only with one")
-    if not bf16 and tuple(scale.shape) != (P, ps, MLA_RANK // BLOCK):
-        raise ValueError(f"cache.scale must be [P, ps, {MLA_RANK // BLOCK}]")
-    return (_need(lat, (torch.bfloat16, *_F8), "cache.latent"),
-            None if bf16 else _need(scale, (torch.float32,), "cache.scale"),
-            _need(rope, (torch.bfloat16,), "cache.rope"), CACHE_BF16 if bf16 else CACHE_FP8, P, ps)
+    return (dev, _ptr(lat, "cache.latent", _LATENT, (P, ps, MLA_RANK), dev),
+            None if bf16 else _ptr(scale, "cache.scale", _F32, (P, ps, MLA_RANK // BLOCK), dev),
+            _ptr(rope, "cache.rope", _BF16, (P, ps, MLA_ROPE), dev), CACHE_BF16 if bf16 else CACHE_FP8, P, ps)
 
 
-def _one_device(*tensors) -> None:
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) > 1:
-        raise ValueError(f"tensors lie on different devices: {sorted(map(str, devs))}")
+def _scratch(workspace: torch.Tensor, dev):
+    """(pointer, bytes) of a workspace."""
+    n = workspace.numel()
+    if not n:
+        return None, 0
+    return (_ptr(workspace, "workspace", (torch.uint8, torch.int32, torch.float32), workspace.shape, dev),
+            n * workspace.element_size())
 
 
-def _i32(t: torch.Tensor, name: str, *shape) -> int:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return _need(t, (torch.int32,), name)
-
-
-def _rows3(t: torch.Tensor, T: int, H: int, width: int, name: str):
-    """A bf16 [T, H, width] view with a dense last dimension: (pointer, token stride, head stride)."""
-    if tuple(t.shape) != (T, H, width):
-        raise ValueError(f"{name} must be [T, H, {width}]")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected bfloat16")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.numel() and t.stride(2) != 1:
-        raise ValueError(f"{name} must have a contiguous last dimension")
-    return t.data_ptr(), (t.stride(0) if T > 1 else 0), (t.stride(1) if H > 1 else 0)
-
-
-def _batch_args(table, cu_q, lens):
-    if table.dim() != 2 or lens.dim() != 1:
-        raise ValueError("table must be [B, W] and lens [B]")
-    B, W = table.shape
-    return _i32(table, "table", B, W), _i32(cu_q, "cu_q", B + 1), _i32(lens, "lens", B), B, W
+def _call_on(dev, fn: str, *args) -> None:
+    """fn(*args, the current stream of device `dev`), with that device current."""
+    if torch.cuda.current_device() == dev.index:
+        _call(fn, *args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            _call(fn, *args, torch.cuda.current_stream(dev).cuda_stream)
 
 
 def fp8bs_mla_cache_write(q_rope: torch.Tensor, kv: torch.Tensor, norm_w: torch.Tensor, eps: float,
@@ -534,23 +550,18 @@ def fp8bs_mla_cache_write(q_rope: torch.Tensor, kv: torch.Tensor, norm_w: torch.
     (norm_w [512] bf16 or float32), rotated and stored at the last positions of
     their sequences; q_rope bf16 [T, H, 64] (a slice of q may be passed) rotated
     into q_out bf16 [T, H, 64].  rope_cs float32 [n_pos, 32, 2] holds (cos, sin)."""
-    if q_rope.dim() != 3 or kv.dim() != 2 or kv.shape[0] != q_rope.shape[0] or kv.shape[1] != MLA_RANK + MLA_ROPE:
-        raise ValueError(f"q_rope must be [T, H, {MLA_ROPE}] and kv [T, {MLA_RANK + MLA_ROPE}]")
-    T, H = q_rope.shape[:2]
-    if tuple(q_out.shape) != (T, H, MLA_ROPE):
-        raise ValueError(f"q_out must be [T, H, {MLA_ROPE}]")
-    if tuple(norm_w.shape) != (MLA_RANK,) or rope_cs.dim() != 3 or tuple(rope_cs.shape[1:]) != (MLA_ROPE // 2, 2):
-        raise ValueError(f"norm_w must be [{MLA_RANK}] and rope_cs [n_pos, {MLA_ROPE // 2}, 2]")
-    _one_device(q_rope, kv, norm_w, rope_cs, q_out, *cache, table, cu_q, lens)
-    lat, scale, rope, fmt, P, ps = _cache_args(cache)
-    qp, ldt, ldh = _rows3(q_rope, T, H, MLA_ROPE, "q_rope")
-    kp, ldk, _ = _rows3(kv.unsqueeze(1), T, 1, MLA_RANK + MLA_ROPE, "kv")
-    tab, cu, ln, B, W = _batch_args(table, cu_q, lens)
-    with torch.cuda.device(kv.device):
-        _call("fp8bs_mla_cache_write", qp, ldt, ldh, kp, ldk, _need(norm_w, (torch.bfloat16, torch.float32), "norm_w"),
-              int(norm_w.dtype == torch.float32), eps, _need(rope_cs, (torch.float32,), "rope_cs"), rope_cs.shape[0],
-              _need(q_out, (torch.bfloat16,), "q_out"), lat, scale, rope, fmt, tab, cu, ln, T, H, B, W, P, ps,
-              MLA_RANK, MLA_ROPE, _stream(kv))
+    if q_rope.dim() != 3 or kv.dim() != 2 or table.dim() != 2 or rope_cs.dim() != 3:
+        raise ValueError("q_rope must be [T, H, 64], kv [T, 576], table [B, W] and rope_cs [n_pos, 32, 2]")
+    (T, H, _), (B, W), n_pos = q_rope.shape, table.shape, rope_cs.shape[0]
+    dev, lat, scale, rope, fmt, P, ps = _cache_args(cache)
+    qp, ldt, ldh = _rows3(q_rope, "q_rope", (T, H, MLA_ROPE), dev)
+    kp, ldk, _ = _rows3(kv.unsqueeze(1), "kv", (T, 1, MLA_RANK + MLA_ROPE), dev)
+    _call_on(dev, "fp8bs_mla_cache_write", qp, ldt, ldh, kp, ldk,
+             _ptr(norm_w, "norm_w", (torch.bfloat16, torch.float32), (MLA_RANK,), dev), norm_w.dtype == torch.float32,
+             eps, _ptr(rope_cs, "rope_cs", _F32, (n_pos, MLA_ROPE // 2, 2), dev), n_pos,
+             _ptr(q_out, "q_out", _BF16, (T, H, MLA_ROPE), dev), lat, scale, rope, fmt,
+             _ptr(table, "table", _I32, (B, W), dev), _ptr(cu_q, "cu_q", _I32, (B + 1,), dev),
+             _ptr(lens, "lens", _I32, (B,), dev), T, H, B, W, P, ps, MLA_RANK, MLA_ROPE)
 
 
 def mla_cache_write(q_rope, kv, norm_w, eps, rope_cs, cache: MlaCache, table, cu_q, lens) -> torch.Tensor:
@@ -566,23 +577,19 @@ def fp8bs_mla_attention(q_lat: torch.Tensor, q_rope: torch.Tensor, cache: MlaCac
     """The new tokens' attention over the cache: q_lat bf16 [T, H, 512] (from
     mla_absorb_key) and q_rope bf16 [T, H, 64] (from mla_cache_write), any token
     and head strides; out [T, H, 512] bf16 or float32, lse float32 [T, H] or None."""
-    if q_lat.dim() != 3:
-        raise ValueError(f"q_lat must be [T, H, {MLA_RANK}]")
-    T, H = q_lat.shape[:2]
-    if tuple(out.shape) != (T, H, MLA_RANK) or (lse is not None and tuple(lse.shape) != (T, H)):
-        raise ValueError(f"out must be [T, H, {MLA_RANK}] and lse [T, H]")
-    _one_device(q_lat, q_rope, *cache, table, cu_q, lens, out, lse, workspace)
-    lat, sc, rope, fmt, P, ps = _cache_args(cache)
-    qp, ldt, ldh = _rows3(q_lat, T, H, MLA_RANK, "q_lat")
-    rp, ldrt, ldrh = _rows3(q_rope, T, H, MLA_ROPE, "q_rope")
-    tab, cu, ln, B, W = _batch_args(table, cu_q, lens)
-    nbytes = workspace.numel() * workspace.element_size()
-    ws = _need(workspace, (torch.uint8, torch.float32), "workspace") if nbytes else None
-    with torch.cuda.device(q_lat.device):
-        _call("fp8bs_mla_attention", qp, ldt, ldh, rp, ldrt, ldrh, lat, sc, rope, fmt, tab, cu, ln, scale, int(causal),
-              _need(out, (torch.bfloat16, torch.float32), "out"), _out_code(out),
-              None if lse is None else _need(lse, (torch.float32,), "lse"), T, H, B, W, P, ps, MLA_RANK, MLA_ROPE,
-              ws, nbytes, _stream(q_lat))
+    if q_lat.dim() != 3 or table.dim() != 2:
+        raise ValueError(f"q_lat must be [T, H, {MLA_RANK}] and table [B, W]")
+    (T, H, _), (B, W) = q_lat.shape, table.shape
+    dev, lat, sc, rope, fmt, P, ps = _cache_args(cache)
+    qp, ldt, ldh = _rows3(q_lat, "q_lat", (T, H, MLA_RANK), dev)
+    rp, ldrt, ldrh = _rows3(q_rope, "q_rope", (T, H, MLA_ROPE), dev)
+    ws, nbytes = _scratch(workspace, dev)
+    _call_on(dev, "fp8bs_mla_attention", qp, ldt, ldh, rp, ldrt, ldrh, lat, sc, rope, fmt,
+             _ptr(table, "table", _I32, (B, W), dev), _ptr(cu_q, "cu_q", _I32, (B + 1,), dev),
+             _ptr(lens, "lens", _I32, (B,), dev), scale, causal,
+             _ptr(out, "out", (torch.bfloat16, torch.float32), (T, H, MLA_RANK), dev), _out_code(out),
+             None if lse is None else _ptr(lse, "lse", _F32, (T, H), dev), T, H, B, W, P, ps, MLA_RANK, MLA_ROPE,
+             ws, nbytes)
 
 
 def mla_attention(q_lat, q_rope, cache: MlaCache, table, cu_q, lens, scale: float, causal: bool = True,
@@ -608,14 +615,12 @@ def fp8bs_cache_update(cache: MlaCache, table: torch.Tensor, lens: torch.Tensor,
     if table.dim() != 2 or parent.dim() != 1:
         raise ValueError("table must be [B, W] and parent [N]")
     (B, W), N = table.shape, parent.shape[0]
-    _one_device(*cache, table, lens, parent, new_lens, table_out, lens_out, workspace)
-    lat, sc, rope, fmt, P, ps = _cache_args(cache)
-    nbytes = workspace.numel() * workspace.element_size()
-    ws = _need(workspace, (torch.uint8, torch.int32), "workspace") if nbytes else None
-    with torch.cuda.device(table.device):
-        _call("fp8bs_cache_update", lat, sc, rope, fmt, _i32(table, "table", B, W), _i32(lens, "lens", B),
-              _i32(parent, "parent", N), _i32(new_lens, "new_lens", N), _i32(table_out, "table_out", N, W),
-              _i32(lens_out, "lens_out", N), B, N, W, P, ps, MLA_RANK, MLA_ROPE, ws, nbytes, _stream(table))
+    dev, lat, sc, rope, fmt, P, ps = _cache_args(cache)
+    ws, nbytes = _scratch(workspace, dev)
+    _call_on(dev, "fp8bs_cache_update", lat, sc, rope, fmt, _ptr(table, "table", _I32, (B, W), dev),
+             _ptr(lens, "lens", _I32, (B,), dev), _ptr(parent, "parent", _I32, (N,), dev),
+             _ptr(new_lens, "new_lens", _I32, (N,), dev), _ptr(table_out, "table_out", _I32, (N, W), dev),
+             _ptr(lens_out, "lens_out", _I32, (N,), dev), B, N, W, P, ps, MLA_RANK, MLA_ROPE, ws, nbytes)
 
 
 def cache_update(cache: MlaCache, table, lens, parent, new_lens):
@@ -640,14 +645,11 @@ def fp8bs_cache_compact(cache: MlaCache, table: torch.Tensor, lens: torch.Tensor
     if count.numel() != 1:
         raise ValueError("count must hold one value")
     B, W = table.shape
-    _one_device(*cache, table, lens, table_out, count, workspace)
-    lat, sc, rope, fmt, P, ps = _cache_args(cache)
-    nbytes = workspace.numel() * workspace.element_size()
-    ws = _need(workspace, (torch.uint8, torch.int32), "workspace") if nbytes else None
-    with torch.cuda.device(table.device):
-        _call("fp8bs_cache_compact", lat, sc, rope, fmt, _i32(table, "table", B, W), _i32(lens, "lens", B),
-              _i32(table_out, "table_out", B, W), _need(count, (torch.int32,), "count"), B, W, P, ps, MLA_RANK,
-              MLA_ROPE, ws, nbytes, _stream(table))
+    dev, lat, sc, rope, fmt, P, ps = _cache_args(cache)
+    ws, nbytes = _scratch(workspace, dev)
+    _call_on(dev, "fp8bs_cache_compact", lat, sc, rope, fmt, _ptr(table, "table", _I32, (B, W), dev),
+             _ptr(lens, "lens", _I32, (B,), dev), _ptr(table_out, "table_out", _I32, (B, W), dev),
+             _ptr(count, "count", _I32, count.shape, dev), B, W, P, ps, MLA_RANK, MLA_ROPE, ws, nbytes)
 
 
 def cache_compact(cache: MlaCache, table, lens):

@@ -146,11 +146,16 @@ __global__ void __launch_bounds__(256) mla_cache_write_kernel(WriteParams p) {
 // alone, write a new table beside the old one, and copy page data only from
 // pages that the old table uses to pages that it does not, so no copy reads
 // what another writes and a call repeated on the same inputs gives the same.
-//   clear  zeroes the keys and the bitmap of used pages
-//   mark   sets used bits from the old table; for update, each new row bids
-//          for the pages it keeps (an atomic max, so order does not matter)
-//   plan   one workgroup: prefix sums over the rows and over the bitmap
+//   mark   used bits from the old table; for update, each new row bids for the
+//          pages it keeps (a maximum, so order does not matter)
+//   plan   prefix sums over the rows and over the bitmap
 //   apply  the new table, and the copies
+// Small ones are one launch: every workgroup marks and plans for itself, in LDS,
+// and applies its share, so nothing passes between workgroups and nothing waits.
+// What does not fit (below, at the launchers) goes through four launches and the
+// workspace.  Small calls are bound by launches: us a call from a graph, four
+// launches / one: 16 rows of 2000 tokens 12.6 / FILL, 64 rows of 8000 to 256 FILL, compact
+// 300 pages FILL.
 // ---------------------------------------------------------------------------
 struct CacheArrays {
   uint8_t* p[3];
@@ -293,6 +298,7 @@ __global__ void __launch_bounds__(1024) page_plan_update_kernel(PageParams p) {
 }
 
 // a share of the bytes of `tokens` tokens of page `from` to page `to`
+template <int THREADS>
 __device__ __forceinline__ void copy_tokens(const PageParams& p, int from, int to, int tokens, int part, int parts) {
 #pragma unroll
   for (int a = 0; a < 3; ++a) {
@@ -302,8 +308,147 @@ __device__ __forceinline__ void copy_tokens(const PageParams& p, int from, int t
     v4u* dst = reinterpret_cast<v4u*>(p.c.p[a] + to * page);
     const int n = (int)((int64_t)tokens * p.c.row_bytes[a] / 16);
 #pragma unroll 4
-    for (int i = part * 256 + threadIdx.x; i < n; i += parts * 256) dst[i] = src[i];
+    for (int i = part * THREADS + threadIdx.x; i < n; i += parts * THREADS) dst[i] = src[i];
   }
+}
+
+// the k-th (from 0) set bit of a word
+__device__ __forceinline__ int nth_bit(uint32_t v, int k) {
+  for (; k; --k) v &= v - 1;
+  return __ffs(v) - 1;
+}
+// Index of the k-th set (SET) or clear bit of a bitmap with the number of set bits before each word
+template <bool SET>
+__device__ __forceinline__ int select(const uint32_t* used, const int* before, int words, int k) {
+  int w = 0;                                         // the last word with at most k such bits before it
+  for (int n = words; n > 1;) {
+    const int half = n / 2;
+    if ((SET ? before[w + half] : 32 * (w + half) - before[w + half]) <= k) w += half;
+    n -= half;
+  }
+  return 32 * w + nth_bit(SET ? used[w] : ~used[w], k - (SET ? before[w] : 32 * w - before[w]));
+}
+
+// used bits of the old table's entries, in LDS; ends with a barrier
+__device__ __forceinline__ void mark_used(const PageParams& p, uint32_t* used) {
+  const int n = p.B * p.W;                           // below kSmallEntries
+#pragma unroll 4
+  for (int e = threadIdx.x; e < n; e += 1024) {
+    const int r = e / p.W, j = e - r * p.W;
+    if (j >= pages_of((int)min((int64_t)max(p.lens[r], 0), (int64_t)p.W * p.ps), p.ps)) continue;
+    const int g = p.table[e];
+    if (g >= 0 && g < p.P) atomicOr(&used[g >> 5], 1u << (g & 31));
+  }
+  __syncthreads();
+}
+// the number of set bits before each word; returns all of them.  Ends with a barrier.
+__device__ __forceinline__ int count_before(const uint32_t* used, int* before, int words, int* sums) {
+  int all = 0;
+  for (int w0 = 0; w0 < words; w0 += 1024) {
+    const int w = w0 + threadIdx.x;
+    int total;
+    const int at = all + block_scan(w < words ? __popc(used[w]) : 0, sums, total);
+    if (w < words) before[w] = at;
+    all += total;
+  }
+  __syncthreads();
+  return all;
+}
+
+constexpr int kSmallEntries = 1 << 18;               // table entries that a workgroup reads for itself
+constexpr int kSmallPages = 1 << 14, kSmallRows = 2048;   // update
+constexpr int kSmallBits = 1 << 17;                  // compact: pages
+
+__global__ void __launch_bounds__(1024) update_small_kernel(PageParams p, int parts) {
+  __shared__ int key[kSmallPages];
+  __shared__ uint32_t used[kSmallPages / 32];
+  __shared__ int before[kSmallPages / 32];
+  __shared__ Row rows[kSmallRows];
+  __shared__ int info[kSmallRows][4];                // first new slot, new pages, their rank, tokens to copy
+  __shared__ int sums[16];
+  const int tid = threadIdx.x;
+  for (int i = tid; i < p.P; i += 1024) key[i] = 0;
+  for (int i = tid; i < p.words; i += 1024) used[i] = 0;
+  for (int i = tid; i < p.N; i += 1024) rows[i] = load_row(p, i);
+  __syncthreads();
+#pragma unroll 4
+  for (int e = tid; e < p.N * p.W; e += 1024) {
+    const int i = e / p.W, j = e - i * p.W;
+    const Row& row = rows[i];
+    if (j >= row.kept) continue;
+    const int g = p.table[(int64_t)row.parent * p.W + j];
+    if (g >= 0 && g < p.P) atomicMax(&key[g], bid(p, row, i, j));
+  }
+  mark_used(p, used);
+  const int n_free = p.P - count_before(used, before, p.words, sums);
+  int64_t base = 0;
+  for (int i0 = 0; i0 < p.N; i0 += 1024) {
+    const int i = i0 + tid;
+    Row row{};
+    int need = 0;
+    bool copy = false;
+    if (i < p.N) {
+      row = rows[i];
+      if (row.want > row.keep) {
+        if (row.grows) {
+          const int g = p.table[(int64_t)row.parent * p.W + row.kept - 1];
+          copy = g >= 0 && g < p.P && key[g] != bid(p, row, i, row.kept - 1);
+        }
+        need = pages_of(row.want, p.ps) - row.kept + copy;
+      }
+    }
+    int total;
+    const int64_t at = base + block_scan(need, sums, total);
+    base += total;
+    if (i < p.N) {
+      const bool ok = need == 0 || at + need <= n_free;
+      info[i][0] = row.kept - (ok && copy);
+      info[i][1] = ok ? need : 0;
+      info[i][2] = (int)min(at, (int64_t)p.P);
+      info[i][3] = ok && copy ? row.keep % p.ps : 0;
+      if (blockIdx.x == 0) p.lens_out[i] = ok ? row.want : row.keep;
+    }
+  }
+  __syncthreads();
+  for (int item = blockIdx.x; item < p.N * parts; item += gridDim.x) {
+    const int i = item / parts, part = item - i * parts;
+    const int first = info[i][0], need = info[i][1], rank = info[i][2], cut = info[i][3];
+    const int64_t old = (int64_t)max(rows[i].parent, 0) * p.W;
+    if (part == 0)
+      for (int j = tid; j < p.W; j += 1024) {
+        int g = -1;
+        if (j >= first && j < first + need) g = select<false>(used, before, p.words, rank + j - first);
+        else if (j < rows[i].kept) g = p.table[old + j];
+        p.table_out[(int64_t)i * p.W + j] = g;
+      }
+    if (cut) copy_tokens<1024>(p, p.table[old + first], select<false>(used, before, p.words, rank), cut, part, parts);
+  }
+}
+
+__global__ void __launch_bounds__(1024) compact_small_kernel(PageParams p) {
+  __shared__ uint32_t used[kSmallBits / 32];
+  __shared__ int before[kSmallBits / 32];
+  __shared__ int sums[16];
+  const int tid = threadIdx.x;
+  for (int i = tid; i < p.words; i += 1024) used[i] = 0;
+  __syncthreads();
+  mark_used(p, used);
+  const int live = count_before(used, before, p.words, sums);
+  auto rank = [&](int g) { return before[g >> 5] + __popc(used[g >> 5] & ((1u << (g & 31)) - 1)); };
+  const int kept = live < p.P ? rank(live) : live;   // of the pages in use, those below `live`
+  if (blockIdx.x == 0 && tid == 0) *p.count = live;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const int n = pages_of((int)min((int64_t)max(p.lens[b], 0), (int64_t)p.W * p.ps), p.ps);
+    for (int j = tid; j < p.W; j += 1024) {
+      int g = j < n ? p.table[(int64_t)b * p.W + j] : -1;
+      if (g < 0 || g >= p.P) g = -1;
+      else if (g >= live) g = select<false>(used, before, p.words, rank(g) - kept);
+      p.table_out[(int64_t)b * p.W + j] = g;
+    }
+  }
+  // the rows' blocks have had their work: copies go from the other end
+  for (int k = gridDim.x - 1 - blockIdx.x; k < live - kept; k += gridDim.x)
+    copy_tokens<1024>(p, select<true>(used, before, p.words, kept + k), select<false>(used, before, p.words, k), p.ps, 0, 1);
 }
 
 __global__ void __launch_bounds__(256) page_apply_update_kernel(PageParams p) {
@@ -320,7 +465,7 @@ __global__ void __launch_bounds__(256) page_apply_update_kernel(PageParams p) {
       else if (j < kept) g = p.table[old + j];
       p.table_out[(int64_t)i * p.W + j] = g;
     }
-  if (cut) copy_tokens(p, p.table[old + first], p.list[rank], cut, blockIdx.y, gridDim.y);
+  if (cut) copy_tokens<256>(p, p.table[old + first], p.list[rank], cut, blockIdx.y, gridDim.y);
 }
 
 __global__ void __launch_bounds__(1024) page_plan_compact_kernel(PageParams p) {
@@ -372,7 +517,7 @@ __global__ void __launch_bounds__(256) page_apply_compact_kernel(PageParams p) {
       p.table_out[(int64_t)b * p.W + j] = g;
     }
   }
-  for (int k = blockIdx.x; k < moves; k += gridDim.x) copy_tokens(p, p.list[p.P + k], p.list[k], p.ps, 0, 1);
+  for (int k = blockIdx.x; k < moves; k += gridDim.x) copy_tokens<256>(p, p.list[p.P + k], p.list[k], p.ps, 0, 1);
 }
 
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -456,8 +601,15 @@ hipError_t launch_mla_cache_write(const MlaCacheWrite& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// One launch when a workgroup's LDS holds the pages' keys and the rows (128 KB, the whole
+// card still has one each) and reading the tables once per workgroup stays cheap.
 hipError_t launch_cache_update(const PageTask& a, hipStream_t stream) {
   const PageParams p = page_params(a);
+  if (a.P <= kSmallPages && a.N <= kSmallRows && (a.B + a.N) * a.W <= kSmallEntries) {
+    const int parts = std::max(1, 256 / p.N);        // workgroups a row's copy is cut over
+    hipLaunchKernelGGL(update_small_kernel, dim3(std::min(256, p.N * parts)), dim3(1024), 0, stream, p, parts);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(page_clear_kernel, dim3((p.P + 255) / 256), dim3(256), 0, stream, p);
   hipLaunchKernelGGL(page_mark_kernel, dim3(p.B + p.N), dim3(256), 0, stream, p);
   hipLaunchKernelGGL(page_plan_update_kernel, dim3(1), dim3(1024), 0, stream, p);
@@ -467,6 +619,11 @@ hipError_t launch_cache_update(const PageTask& a, hipStream_t stream) {
 
 hipError_t launch_cache_compact(const PageTask& a, hipStream_t stream) {
   const PageParams p = page_params(a);
+  if (a.P <= kSmallBits && a.B * a.W <= kSmallEntries) {
+    const int grid = std::min(512, std::max(1, std::max(p.P / 2, p.B)));
+    hipLaunchKernelGGL(compact_small_kernel, dim3(grid), dim3(1024), 0, stream, p);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(page_clear_kernel, dim3((p.words + 255) / 256), dim3(256), 0, stream, p);
   if (p.B) hipLaunchKernelGGL(page_mark_kernel, dim3(p.B), dim3(256), 0, stream, p);
   hipLaunchKernelGGL(page_plan_compact_kernel, dim3(1), dim3(1024), 0, stream, p);
