@@ -534,13 +534,18 @@ def _scratch(workspace: torch.Tensor, dev):
             n * workspace.element_size())
 
 
+# the current stream's handle without the Stream object around it (2 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _call_on(dev, fn: str, *args) -> None:
     """fn(*args, the current stream of device `dev`), with that device current."""
+    stream = _raw_stream(dev.index)
     if torch.cuda.current_device() == dev.index:
-        _call(fn, *args, torch.cuda.current_stream(dev).cuda_stream)
+        _call(fn, *args, stream)
     else:
         with torch.cuda.device(dev):
-            _call(fn, *args, torch.cuda.current_stream(dev).cuda_stream)
+            _call(fn, *args, stream)
 
 
 def fp8bs_mla_cache_write(q_rope: torch.Tensor, kv: torch.Tensor, norm_w: torch.Tensor, eps: float,
@@ -555,7 +560,9 @@ def fp8bs_mla_cache_write(q_rope: torch.Tensor, kv: torch.Tensor, norm_w: torch.
     (T, H, _), (B, W), n_pos = q_rope.shape, table.shape, rope_cs.shape[0]
     dev, lat, scale, rope, fmt, P, ps = _cache_args(cache)
     qp, ldt, ldh = _rows3(q_rope, "q_rope", (T, H, MLA_ROPE), dev)
-    kp, ldk, _ = _rows3(kv.unsqueeze(1), "kv", (T, 1, MLA_RANK + MLA_ROPE), dev)
+    if kv.shape != (T, MLA_RANK + MLA_ROPE) or kv.dtype != torch.bfloat16 or kv.device != dev or (T and kv.stride(1) != 1):
+        raise ValueError(f"kv must be bfloat16 [{T}, {MLA_RANK + MLA_ROPE}] on {dev} with a contiguous last dimension")
+    kp, ldk = kv.data_ptr(), (kv.stride(0) if T > 1 else 0)
     _call_on(dev, "fp8bs_mla_cache_write", qp, ldt, ldh, kp, ldk,
              _ptr(norm_w, "norm_w", (torch.bfloat16, torch.float32), (MLA_RANK,), dev), norm_w.dtype == torch.float32,
              eps, _ptr(rope_cs, "rope_cs", _F32, (n_pos, MLA_ROPE // 2, 2), dev), n_pos,
@@ -566,7 +573,7 @@ def fp8bs_mla_cache_write(q_rope: torch.Tensor, kv: torch.Tensor, norm_w: torch.
 
 def mla_cache_write(q_rope, kv, norm_w, eps, rope_cs, cache: MlaCache, table, cu_q, lens) -> torch.Tensor:
     """fp8bs_mla_cache_write; returns the rotated queries [T, H, 64]."""
-    q_out = torch.empty(q_rope.shape, dtype=torch.bfloat16, device=q_rope.device)
+    q_out = q_rope.new_empty(q_rope.shape)
     fp8bs_mla_cache_write(q_rope, kv, norm_w, eps, rope_cs, q_out, cache, table, cu_q, lens)
     return q_out
 
@@ -599,9 +606,9 @@ def mla_attention(q_lat, q_rope, cache: MlaCache, table, cu_q, lens, scale: floa
     need = lib().fp8bs_mla_attention_workspace_size(T, H, table.shape[0])
     if need < 0:
         raise ValueError("sizes out of range")
-    out = torch.empty((T, H, MLA_RANK), dtype=out_dtype, device=q_lat.device)
-    lse = torch.empty((T, H), dtype=torch.float32, device=q_lat.device) if return_lse else None
-    ws = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
+    out = q_lat.new_empty((T, H, MLA_RANK), dtype=out_dtype)
+    lse = q_lat.new_empty((T, H), dtype=torch.float32) if return_lse else None
+    ws = q_lat.new_empty(need, dtype=torch.uint8)
     fp8bs_mla_attention(q_lat, q_rope, cache, table, cu_q, lens, scale, out, lse, ws, causal)
     return (out, lse) if return_lse else out
 
@@ -629,9 +636,8 @@ def cache_update(cache: MlaCache, table, lens, parent, new_lens):
     need = lib().fp8bs_cache_update_workspace_size(cache.latent.shape[0], N)
     if need < 0:
         raise ValueError("sizes out of range")
-    table_out = torch.empty((N, W), dtype=torch.int32, device=table.device)
-    lens_out = torch.empty(N, dtype=torch.int32, device=table.device)
-    ws = torch.empty(need, dtype=torch.uint8, device=table.device)
+    table_out, lens_out = table.new_empty((N, W)), table.new_empty(N)
+    ws = table.new_empty((need + 3) // 4)
     fp8bs_cache_update(cache, table, lens, parent, new_lens, table_out, lens_out, ws)
     return table_out, lens_out
 
@@ -657,8 +663,7 @@ def cache_compact(cache: MlaCache, table, lens):
     need = lib().fp8bs_cache_compact_workspace_size(cache.latent.shape[0])
     if need < 0:
         raise ValueError("sizes out of range")
-    table_out = torch.empty_like(table)
-    count = torch.empty((), dtype=torch.int32, device=table.device)
-    ws = torch.empty(need, dtype=torch.uint8, device=table.device)
+    table_out, count = table.new_empty(table.shape), table.new_empty(())
+    ws = table.new_empty((need + 3) // 4)
     fp8bs_cache_compact(cache, table, lens, table_out, count, ws)
     return table_out, count
