@@ -59,8 +59,10 @@ constexpr int kRopeB = kD * 2;
 constexpr int kGroupB = 8 * 128;
 constexpr int kBlockB = 9 * kGroupB;
 constexpr int kTileB = 4 * kBlockB;     // 36,864 bytes
-// FP8: 8 tokens as they come, four groups of codes, the rotated group, four scales a token (twice)
-constexpr int kRawB = 5 * kGroupB + 256;
+// FP8: 8 tokens as they come: four groups of codes, the rotated group (with PIPE it goes to its
+// place in the tile at once), four scales a token (twice)
+template <bool PIPE>
+constexpr int raw_bytes() { return (PIPE ? 4 : 5) * kGroupB + 256; }
 constexpr int kAhead = 6;                // fragments read ahead of their products
 constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
@@ -415,17 +417,17 @@ __device__ __forceinline__ int next_seq(const AttnParams& p, int b) {
   return p.B - 1;
 }
 
-// LDS.  One token wave's tiles: with PIPE (RW = 4) a ring of four, or three and a
-// stage of codes for FP8; with RW = 2 two, or one and two stages of codes; with
+// LDS.  One token wave's tiles: with PIPE (RW = 4) a ring of four, or three and two
+// stages of codes for FP8; with RW = 2 two, or one and two stages of codes; with
 // RW = 1 one (FP8: the codes wait in registers).  A wave makes bf16 of the codes
 // that it loaded itself.
 template <int RW, bool FP8>
 constexpr int tiles() { return RW == 4 ? (FP8 ? 3 : 4) : RW == 2 && !FP8 ? 2 : 1; }
 template <int RW, bool FP8>
-constexpr int raws() { return !FP8 || RW == 1 ? 0 : RW == 2 ? 2 : 1; }
+constexpr int raws() { return !FP8 || RW == 1 ? 0 : 2; }
 template <int ROWS, int RW, int TW, bool FP8>
 constexpr int lds_bytes() {
-  const int n = TW * (tiles<RW, FP8>() * kTileB + raws<RW, FP8>() * 4 * kRawB) + (RW == 4 ? 4 * 4 * 1024 : 0);
+  const int n = TW * (tiles<RW, FP8>() * kTileB + raws<RW, FP8>() * 4 * raw_bytes<RW == 4>()) + (RW == 4 ? 4 * 4 * 1024 : 0);
   return TW > 1 ? std::max(n, 4 * ROWS * (kR / (ROWS / 16)) * 4) : n;   // the token waves' accumulators meet here
 }
 
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))
 mla_attention_kernel(AttnParams p) {
   constexpr int M = ROWS * RW, STEP = kTok * TW;
   constexpr bool WIDE = ROWS == 32, PIPE = RW == 4;
-  constexpr int NT = tiles<RW, FP8>(), NR = raws<RW, FP8>();
+  constexpr int NT = tiles<RW, FP8>(), NR = raws<RW, FP8>(), kRawB = raw_bytes<PIPE>();
   constexpr int NSUB = 4 / RW;                       // blocks of 8 tokens that a wave loads of 32
   constexpr int CH = 8 * 64 / ROWS;                  // channels of a K step of the scores
   constexpr int QN = (kR + kD) / CH;                 // K steps
@@ -518,26 +520,28 @@ mla_attention_kernel(AttnParams p) {
     }
     // P * ps < 2^31
     const int64_t row = __shfl(pages, at - pbase) * p.ps + (int)(tok - (uint32_t)at * (uint32_t)p.ps);
-    const int c = FP8 ? ln & 7 : (ln & 7) ^ swz<ROWS>(8 * sub + (ln >> 3));
+    const int c = (ln & 7) ^ swz<ROWS>(8 * sub + (ln >> 3));   // the chunk for this lane's place
     From f;
-    f.lat = p.latent + row * (FP8 ? kR : 2 * kR) + 16 * c;
-    f.rope = p.rope + row * kD + 8 * c;
+    f.lat = p.latent + row * (FP8 ? kR : 2 * kR) + 16 * (FP8 ? ln & 7 : c);
+    f.rope = p.rope + row * kD + 8 * (FP8 && !PIPE ? ln & 7 : c);
     f.scale = FP8 ? p.lat_scale + row * (kR / 128) + (ln & 3) : nullptr;
     return f;
   };
   constexpr int NL = FP8 ? 6 : 9;                    // loads of a block
-  auto ask = [&](const From& f, uint32_t to, auto i) {
-    if constexpr (i < NL - 1 - FP8) dma_b128<128 * i>(f.lat, to + i * kGroupB);
-    else if constexpr (i == NL - 1 - FP8) dma_b128<0>(f.rope, to + i * kGroupB);
-    else dma_b32(f.scale, to + i * kGroupB);
+  // load i of a block; `to` is the block in the tile, `codes` (FP8) the block's stage
+  auto ask = [&](const From& f, uint32_t to, uint32_t codes, auto i) {
+    constexpr int rope = FP8 ? 4 : 8;
+    if constexpr (i < rope) dma_b128<128 * i>(f.lat, (FP8 ? codes : to) + i * kGroupB);
+    else if constexpr (i == rope) dma_b128<0>(f.rope, FP8 && !PIPE ? codes + 4 * kGroupB : to + 8 * kGroupB);
+    else dma_b32(f.scale, codes + (PIPE ? 4 : 5) * kGroupB);
   };
-  // this wave's blocks of 32 tokens; `to` is the tile, or (FP8) the wave's stage of codes
-  auto fetch = [&](int tb, uint32_t to) {
+  // this wave's blocks of 32 tokens, to a tile and (FP8) a stage of the wave's codes
+  auto fetch = [&](int tb, uint32_t to, uint32_t codes) {
 #pragma unroll
     for (int i = 0; i < NSUB; ++i) {
       const int sub = rw * NSUB + i;
       const From f = find(tb, sub);
-      unroll<NL>([&](auto u) { ask(f, to + (FP8 ? i * kRawB : sub * kBlockB), u); });
+      unroll<NL>([&](auto u) { ask(f, to + sub * kBlockB, codes + i * kRawB, u); });
     }
   };
   // Codes to bf16, exactly (power-of-two scales): the 16 codes of group i that this lane loaded, to
@@ -569,6 +573,30 @@ mla_attention_kernel(AttnParams p) {
       spread_rope(sub, v, to);
     }
   };
+  // PIPE: the same in 24 pieces of a few instructions, six a group: read, convert four codes at a time, write
+  v4u some_codes, some_bf16[2];
+  float some_scale = 0.0f;
+  auto spread_bit = [&](auto u, uint32_t from, uint32_t to) {
+    constexpr int i = u / 6, k = u % 6;
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    if constexpr (k == 0) {
+      typedef const __attribute__((address_space(3))) float lds_f;
+      some_codes = *(const lds_v4u*)(uintptr_t)(from + i * kGroupB + ln * 16);
+      some_scale = *(lds_f*)(uintptr_t)(from + 4 * kGroupB + (ln >> 3) * 32 + i * 4);
+    } else if constexpr (k < 5) {
+      const v2f a = __builtin_amdgcn_cvt_pk_f32_fp8((int)some_codes[k - 1], false);
+      const v2f c = __builtin_amdgcn_cvt_pk_f32_fp8((int)some_codes[k - 1], true);
+      some_bf16[(k - 1) / 2][(k - 1) % 2 * 2] = pack2_bf16(__fmul_rn(a.x, some_scale), __fmul_rn(a.y, some_scale));
+      some_bf16[(k - 1) / 2][(k - 1) % 2 * 2 + 1] = pack2_bf16(__fmul_rn(c.x, some_scale), __fmul_rn(c.y, some_scale));
+    } else {
+      const int t = ln >> 3, c = 2 * (ln & 3);
+      const uint32_t at = to + rw * kBlockB + (2 * i + ((ln & 7) >> 2)) * kGroupB + t * 128;
+      const int x = swz<ROWS>(8 * rw + t);
+      *(lds_v4u*)(uintptr_t)(at + ((c ^ x) << 4)) = some_bf16[0];
+      *(lds_v4u*)(uintptr_t)(at + (((c + 1) ^ x) << 4)) = some_bf16[1];
+    }
+  };
   // FP8, RW = 1: the codes in registers
   v4u code_reg[16], rope_reg[4];
   float scale_reg[16];
@@ -589,9 +617,7 @@ mla_attention_kernel(AttnParams p) {
   const int n_steps = step1 - step0;
   const int t_seg = step0 * STEP + tw * kTok;        // this wave's first token
   if (PIPE && n_steps > 0) {                         // the first tokens are on their way before Q
-    if constexpr (FP8) fetch(t_seg, raw_at);
-    else if constexpr (PIPE)
-      for (int k = 0; k < NT - 1; ++k) fetch(t_seg + k * STEP, tile_at + k * kTileB);
+    for (int k = 0; k < (FP8 ? 2 : NT - 1); ++k) fetch(t_seg + k * STEP, tile_at + k * kTileB, raw_at + (FP8 ? k * kRawB : 0));
   }
 
   // this lane's query row: its operands, and the tokens it sees
@@ -671,13 +697,15 @@ mla_attention_kernel(AttnParams p) {
       if (tb + GS * (e / 4) + 4 * g + e % 4 >= end) s.template set<e>(kNegInf);
     });
   };
-  // Scores to probabilities in kSoft pieces of a few instructions each
-  constexpr int NP = Scores<ROWS>::N / 2, kSoft = 2 * NP + 1 + NP / 4;
+  // Scores to probabilities in kSoft pieces that fit beside a matrix instruction: the maximum of four
+  // scores; the check of it; one probability; eight of them packed
+  constexpr int NS = Scores<ROWS>::N, kSoft = NS / 4 + 1 + NS + NS / 8;
   float top = 0.0f;
   auto soft = [&](auto i) {
-    if constexpr (i < NP) {
-      top = fmaxf(fmaxf(i == 0 ? kNegInf : top, s.template get<2 * i>()), s.template get<2 * i + 1>());
-    } else if constexpr (i == NP) {
+    if constexpr (i < NS / 4) {
+      top = fmaxf(fmaxf(i == 0 ? kNegInf : top, s.template get<4 * i>()), s.template get<4 * i + 1>());
+      top = fmaxf(fmaxf(top, s.template get<4 * i + 2>()), s.template get<4 * i + 3>());
+    } else if constexpr (i == NS / 4) {
       if (__any(top * p.scale2 > m + kLazy)) {
         if (!WIDE) top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -690,16 +718,13 @@ mla_attention_kernel(AttnParams p) {
         acc_settle();
       }
       top = m == kNegInf ? 0.0f : -m;
-    } else if constexpr (i <= 2 * NP) {
-      constexpr int e = 2 * (i - NP - 1);
+    } else if constexpr (i <= NS / 4 + NS) {
+      constexpr int e = i - NS / 4 - 1;
       const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s.template get<e>(), p.scale2, top));
-      const float z = __builtin_amdgcn_exp2f(__builtin_fmaf(s.template get<e + 1>(), p.scale2, top));
       s.template set<e>(y);
-      s.template set<e + 1>(z);
       l += y;
-      l += z;
     } else {
-      constexpr int k = i - 2 * NP - 1;
+      constexpr int k = i - NS / 4 - 1 - NS;
       v4u u;
       unroll<4>([&](auto d) { u[(int)d] = pack2_bf16(s.template get<8 * k + 2 * d>(), s.template get<8 * k + 2 * d + 1>()); });
       pr[k] = __builtin_bit_cast(v8bf, u);
@@ -714,8 +739,9 @@ mla_attention_kernel(AttnParams p) {
     // whose operands are in registers by then: behind it tile k's place is free, tile k + 2 is there,
     // and the reads of its first fragments run under those products.  Tiles past the segment's end
     // are asked for too (the last token again and again), so that the counts stay the same.
-    // FP8: three places; codes are asked for one step earlier, and tile k + 2 is made of them under
-    // the products of tile k's output.
+    // FP8: three places.  Tile k + 2 is made of its codes under the products of tile k's output, and
+    // then tile k + 4's codes are asked for, into the stage that got free, and its rotated part
+    // into the place of tile k + 1, whose scores every wave has by then.
     Scores<ROWS> t;
     auto meet = [&](auto outstanding) {
       wait_vmcnt<outstanding>();
@@ -724,13 +750,12 @@ mla_attention_kernel(AttnParams p) {
     auto next = [](int place) { return place + 1 == NT ? 0 : place + 1; };
     if (n_steps > 0) {
       if constexpr (FP8) {
+        wait_vmcnt<0>();
         for (int k = 0; k < 2; ++k) {
-          if (k) fetch(t_seg + k * STEP, raw_at);
-          wait_vmcnt<0>();
-          unroll<5>([&](auto i) { spread_raw(rw, i, raw_at, tile_at + k * kTileB); });
-          __builtin_amdgcn_s_waitcnt(0xc07f);        // lgkmcnt(0): the codes are read before others land on them
+          unroll<24>([&](auto u) { spread_bit(u, raw_at + k * kRawB, tile_at + k * kTileB); });
         }
-        fetch(t_seg + 2 * STEP, raw_at);
+        __builtin_amdgcn_s_waitcnt(0xc07f);          // lgkmcnt(0): the codes are read before others land on them
+        fetch(t_seg + 2 * STEP, tile_at + 2 * kTileB, raw_at);
         barrier_lds();
       } else {
         meet(std::integral_constant<int, 2 * NL>{});
@@ -743,7 +768,12 @@ mla_attention_kernel(AttnParams p) {
         score(f, s);
         if constexpr (f + kAhead < NF) key(std::integral_constant<int, f + kAhead>{});
       });
-      if constexpr (!FP8) meet(std::integral_constant<int, NL>{});
+      if constexpr (FP8) {
+        barrier_lds();                               // everyone has tile 0's scores: its rotated part makes room
+        fetch(t_seg + 3 * STEP, tile_at, raw_at + kRawB);
+      } else {
+        meet(std::integral_constant<int, NL>{});
+      }
       keys_at(kTileB);
       unroll<kAhead>([&](auto f) { key(f); });
     }
@@ -768,19 +798,19 @@ mla_attention_kernel(AttnParams p) {
       }
       const int two = next(next(place));             // of tile k + 2
       const int free = next(two);                    // bf16: of tile k + 3
+      const uint32_t codes = raw_at + (k & 1) * kRawB;   // of tiles k + 2 and k + 4
       From f3;
-      if constexpr (FP8) wait_vmcnt<0>();            // the codes of tile k + 2, asked for a step ago
+      if constexpr (FP8) wait_vmcnt<NL>();           // the codes of tile k + 2, asked for two steps ago
       unroll<NV - kAhead>([&](auto f) {
         fence();
         product(f);
         value(std::integral_constant<int, f + kAhead>{});
         if constexpr (FP8) {
-          if constexpr (f % 4 == 0 && f / 4 < 5) spread_raw(rw, std::integral_constant<int, f / 4>{}, raw_at, tile_at + two * kTileB);
-          if constexpr (f == 18) f3 = find(tb + 3 * STEP, rw);
-          if constexpr (f >= 20) ask(f3, raw_at, std::integral_constant<int, f - 20>{});
+          if constexpr (f < 24) spread_bit(f, codes, tile_at + two * kTileB);
+          else if constexpr (f == 24) f3 = find(tb + 4 * STEP, rw);
         } else {
           if constexpr (f == 0) f3 = find(tb + 3 * STEP, rw);
-          if constexpr (f >= 4 && f % 2 == 0 && f < 4 + 2 * NL) ask(f3, tile_at + free * kTileB + rw * kBlockB, std::integral_constant<int, (f - 4) / 2>{});
+          if constexpr (f >= 4 && f % 2 == 0 && f < 4 + 2 * NL) ask(f3, tile_at + free * kTileB + rw * kBlockB, 0u, std::integral_constant<int, (f - 4) / 2>{});
         }
       });
       place = next(place);
@@ -790,6 +820,7 @@ mla_attention_kernel(AttnParams p) {
       unroll<kAhead>([&](auto i) {
         fence();
         product(std::integral_constant<int, NV - kAhead + i>{});
+        if constexpr (FP8) ask(f3, tile_at + place * kTileB + rw * kBlockB, codes, i);
       });
       unroll<kAhead>([&](auto f) { key(f); });
       s = t;
@@ -797,7 +828,7 @@ mla_attention_kernel(AttnParams p) {
   } else {
     if constexpr (RW > 1) {
       for (int k = 0; k < (FP8 ? 2 : 1) && k < n_steps; ++k)
-        fetch(t_seg + k * STEP, FP8 ? raw_at + k * NSUB * kRawB : tile_at);
+        fetch(t_seg + k * STEP, tile_at, raw_at + k * NSUB * kRawB);
     } else if constexpr (FP8) {
       if (t_seg < end_max && n_steps > 0) fetch_regs(t_seg);
     }
@@ -808,7 +839,7 @@ mla_attention_kernel(AttnParams p) {
         off = (k & 1) * kTileB;
         wait_vmcnt<0>();
         barrier_lds();                               // everyone's share of tile k is here, tile k - 1 is done with
-        if (k + 1 < n_steps) fetch(tb + STEP, tile_at + (kTileB - off));
+        if (k + 1 < n_steps) fetch(tb + STEP, tile_at + (kTileB - off), 0u);
       } else if constexpr (RW > 1) {
         const uint32_t from = raw_at + (k & 1) * NSUB * kRawB;
         if (k + 1 < n_steps) wait_vmcnt<NSUB * NL>();
@@ -818,7 +849,7 @@ mla_attention_kernel(AttnParams p) {
         for (int i = 0; i < NSUB; ++i)
           unroll<5>([&](auto u) { spread_raw(rw * NSUB + i, u, from + i * kRawB, tile_at); });
         barrier_lds();                               // tile k is whole
-        if (k + 2 < n_steps) fetch(tb + 2 * STEP, from);
+        if (k + 2 < n_steps) fetch(tb + 2 * STEP, tile_at, from);
       } else {
         if (tb >= end_max) break;                    // the other token waves have the rest
         if constexpr (FP8) {
@@ -830,7 +861,7 @@ mla_attention_kernel(AttnParams p) {
           }
           if (k + 1 < n_steps && tb + STEP < end_max) fetch_regs(tb + STEP);
         } else {
-          fetch(tb, tile_at);
+          fetch(tb, tile_at, 0u);
           wait_vmcnt<0>();
         }
       }

@@ -297,18 +297,33 @@ __global__ void __launch_bounds__(1024) page_plan_update_kernel(PageParams p) {
   }
 }
 
-// a share of the bytes of `tokens` tokens of page `from` to page `to`
+// a share of the bytes of `tokens` tokens of page `from` to page `to`: the arrays' 16-byte pieces in
+// one row, eight loads a thread under way before their stores
 template <int THREADS>
 __device__ __forceinline__ void copy_tokens(const PageParams& p, int from, int to, int tokens, int part, int parts) {
+  int64_t src[3], dst[3];                            // byte addresses, less those of the pieces before
+  int end[3], n = 0;
 #pragma unroll
   for (int a = 0; a < 3; ++a) {
-    if (!p.c.row_bytes[a]) continue;
     const int64_t page = (int64_t)p.ps * p.c.row_bytes[a];
-    const v4u* src = reinterpret_cast<const v4u*>(p.c.p[a] + from * page);
-    v4u* dst = reinterpret_cast<v4u*>(p.c.p[a] + to * page);
-    const int n = (int)((int64_t)tokens * p.c.row_bytes[a] / 16);
-#pragma unroll 4
-    for (int i = part * THREADS + threadIdx.x; i < n; i += parts * THREADS) dst[i] = src[i];
+    src[a] = (int64_t)(uintptr_t)p.c.p[a] + from * page - 16 * (int64_t)n;
+    dst[a] = (int64_t)(uintptr_t)p.c.p[a] + to * page - 16 * (int64_t)n;
+    n += (int)((int64_t)tokens * p.c.row_bytes[a] / 16);
+    end[a] = n;
+  }
+  constexpr int U = 8;
+  for (int i0 = part * THREADS + threadIdx.x; i0 < n; i0 += parts * THREADS * U) {
+    v4u v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * parts * THREADS;
+      if (i < n) v[u] = *reinterpret_cast<const v4u*>((i < end[0] ? src[0] : i < end[1] ? src[1] : src[2]) + 16 * (int64_t)i);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * parts * THREADS;
+      if (i < n) *reinterpret_cast<v4u*>((i < end[0] ? dst[0] : i < end[1] ? dst[1] : dst[2]) + 16 * (int64_t)i) = v[u];
+    }
   }
 }
 
@@ -329,16 +344,32 @@ __device__ __forceinline__ int select(const uint32_t* used, const int* before, i
   return 32 * w + nth_bit(SET ? used[w] : ~used[w], k - (SET ? before[w] : 32 * w - before[w]));
 }
 
+// f(row, slot, page) for every page of n rows, pages_in(row) of them at row_at(row): a wave takes every
+// sixteenth row, 64 slots at a time, four rows' loads under way
+template <typename Pages, typename At, typename F>
+__device__ __forceinline__ void for_pages(const PageParams& p, int n, const Pages& pages_in, const At& row_at, const F& f) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int j = lane; j < p.W + lane; j += 64)
+    for (int r0 = wave; r0 < n; r0 += 64) {
+      int g[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = r0 + 16 * u;
+        g[u] = r < n && j < pages_in(r) ? row_at(r)[j] : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (g[u] >= 0 && g[u] < p.P) f(r0 + 16 * u, j, g[u]);
+    }
+}
+
 // used bits of the old table's entries, in LDS; ends with a barrier
 __device__ __forceinline__ void mark_used(const PageParams& p, uint32_t* used) {
-  const int n = p.B * p.W;                           // below kSmallEntries
-#pragma unroll 4
-  for (int e = threadIdx.x; e < n; e += 1024) {
-    const int r = e / p.W, j = e - r * p.W;
-    if (j >= pages_of((int)min((int64_t)max(p.lens[r], 0), (int64_t)p.W * p.ps), p.ps)) continue;
-    const int g = p.table[e];
-    if (g >= 0 && g < p.P) atomicOr(&used[g >> 5], 1u << (g & 31));
-  }
+  for_pages(
+      p, p.B,
+      [&](int r) { return pages_of((int)min((int64_t)max(p.lens[r], 0), (int64_t)p.W * p.ps), p.ps); },
+      [&](int r) { return p.table + (int64_t)r * p.W; },
+      [&](int, int, int g) { atomicOr(&used[g >> 5], 1u << (g & 31)); });
   __syncthreads();
 }
 // the number of set bits before each word; returns all of them.  Ends with a barrier.
@@ -371,14 +402,9 @@ __global__ void __launch_bounds__(1024) update_small_kernel(PageParams p, int pa
   for (int i = tid; i < p.words; i += 1024) used[i] = 0;
   for (int i = tid; i < p.N; i += 1024) rows[i] = load_row(p, i);
   __syncthreads();
-#pragma unroll 4
-  for (int e = tid; e < p.N * p.W; e += 1024) {
-    const int i = e / p.W, j = e - i * p.W;
-    const Row& row = rows[i];
-    if (j >= row.kept) continue;
-    const int g = p.table[(int64_t)row.parent * p.W + j];
-    if (g >= 0 && g < p.P) atomicMax(&key[g], bid(p, row, i, j));
-  }
+  for_pages(
+      p, p.N, [&](int i) { return rows[i].kept; }, [&](int i) { return p.table + (int64_t)max(rows[i].parent, 0) * p.W; },
+      [&](int i, int j, int g) { atomicMax(&key[g], bid(p, rows[i], i, j)); });
   mark_used(p, used);
   const int n_free = p.P - count_before(used, before, p.words, sums);
   int64_t base = 0;

@@ -1,7 +1,11 @@
 """GPU parity of fp8bs_mla_attention (new tokens over a paged MLA cache) against
 the formula in 64 bits: row tiles of every kind, both cache types, lengths from
 none to many pages, odd page sizes, strided queries, masks that leave rows
-empty, and garbage wherever the operator must not look."""
+empty, and garbage wherever the operator must not look.
+
+The library takes larger row tiles (up to what a sequence's rows fill) the more
+work the table's width lets it expect, so every case runs twice, with a table
+as wide as its sequences ("narrow") and with one for a million tokens ("wide")."""
 import math
 
 import pytest
@@ -19,6 +23,15 @@ SCALE = 192.0 ** -0.5
 def _need_gpu():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
+
+
+@pytest.fixture(params=["narrow", "wide"])
+def width(request):
+    return request.param
+
+
+def columns(width, lens, ps):
+    return None if width == "narrow" else max((1 << 20) // ps, -(-max(lens) // ps))
 
 
 def batch(H, nq, lens, ps, dtype, seed, spare=2, W=None, behind=-1):
@@ -66,24 +79,26 @@ def compare(args, what, causal=True, dt=BF16, scale=SCALE):
     (24, [3, 3], [3, 1000], 1),
     (8, [4, 4, 4, 4], [4, 40, 400, 401], 4096),
 ])
-def test_attention(H, nq, lens, ps, dtype):
-    args = batch(H, nq, lens, ps, dtype, 7 * H + sum(lens))
+def test_attention(H, nq, lens, ps, dtype, width):
+    args = batch(H, nq, lens, ps, dtype, 7 * H + sum(lens), W=columns(width, lens, ps))
     compare(args, f"H {H} nq {nq} lens {lens} ps {ps}")
 
 
 @pytest.mark.parametrize("dt", [BF16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
 @pytest.mark.parametrize("H,nq", [(16, [1, 7, 30]), (128, [1, 2, 3])])
-def test_causal_and_output_types(H, nq, causal, dt):
-    compare(batch(H, nq, [70, 33, 200], 32, BF16, 11 + H), f"H {H} causal {causal} {dt}", causal, dt)
+def test_causal_and_output_types(H, nq, causal, dt, width):
+    lens = [70, 33, 200]
+    compare(batch(H, nq, lens, 32, BF16, 11 + H, W=columns(width, lens, 32)), f"H {H} causal {causal} {dt}", causal, dt)
 
 
 @pytest.mark.parametrize("H", [1, 16, 40, 128])
 @pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
-def test_rows_that_see_nothing(H, dtype):
+def test_rows_that_see_nothing(H, dtype, width):
     """A sequence of no tokens, and more new tokens than the cache holds: those
     at positions below 0 see nothing, and give zeros and -inf."""
-    args = batch(H, [2, 5, 3, 1], [0, 3, 40, 0], 16, dtype, 21 + H)
+    lens = [0, 3, 40, 0]
+    args = batch(H, [2, 5, 3, 1], lens, 16, dtype, 21 + H, W=columns(width, lens, 16))
     out, lse = compare(args, f"empty rows, H {H}")
     empty = torch.tensor([0, 1, 2, 3, 10])
     assert (out[empty] == 0).all() and (lse[empty] == -math.inf).all()
@@ -91,10 +106,10 @@ def test_rows_that_see_nothing(H, dtype):
 
 
 @pytest.mark.parametrize("H,nq", [(16, [1, 1]), (64, [1, 1]), (128, [1, 3]), (32, [1, 1])])
-def test_garbage_out_of_sight(H, nq):
+def test_garbage_out_of_sight(H, nq, width):
     """NaN in every unused cache row and page and beside the table's used part
     indices of no page at all: nothing behind a sequence is looked at."""
-    args = batch(H, nq, [45, 130], 32, BF16, 31 + H, W=9, behind=2 ** 30)
+    args = batch(H, nq, [45, 130], 32, BF16, 31 + H, W=9 if width == "narrow" else 1 << 15, behind=2 ** 30)
     q_lat, q_rope, cache, table, cu, lens = args
     used = torch.zeros(cache.latent.shape[:2], dtype=torch.bool)
     for b, n in enumerate(lens.tolist()):
@@ -109,23 +124,27 @@ def test_garbage_out_of_sight(H, nq):
     compare(args, "clean")
 
 
-def test_pages_outside_the_cache_do_not_fault():
+@pytest.mark.parametrize("H", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
+def test_pages_outside_the_cache_do_not_fault(H, dtype, width):
     """Entries that name no page: the sequence's result is unspecified, the others' is not touched by it."""
-    args = batch(16, [1, 1, 1], [100, 64, 90], 32, BF16, 41)
+    lens = [100, 64, 90]
+    args = batch(H, [1, 1, 1], lens, 32, dtype, 41, W=columns(width, lens, 32))
     q_lat, q_rope, cache, table, cu, lens = args
     ref = attention64(q_lat, q_rope, cache, table, cu, lens, SCALE, True)
     bad = table.clone()
-    bad[1] = torch.tensor([-5, 2 ** 31 - 1, 12345678, -2 ** 31])[: bad.shape[1]]
+    bad[1, :4] = torch.tensor([-5, 2 ** 31 - 1, 12345678, -2 ** 31])
     out, lse = run((q_lat, q_rope, cache, bad, cu, lens))
     keep = torch.tensor([0, 2])
     check_attention(out[keep], lse[keep], tuple(x[keep] for x in ref), 100, "beside bad pages")
 
 
-def test_strided_queries_and_rows_behind():
+@pytest.mark.parametrize("H", [6, 12, 24, 48])
+def test_strided_queries_and_rows_behind(H, width):
     """Queries as slices (token and head strides of their own), and rows behind
     the last sequence, which keep what they held."""
-    H, nq, lens = 12, [3, 2], [50, 77]
-    args = batch(H, nq, lens, 32, FP8, 51)
+    nq, lens = [3, 2], [50, 77]
+    args = batch(H, nq, lens, 32, FP8, 51, W=columns(width, lens, 32))
     q_lat, q_rope, cache, table, cu, lens = args
     wide = torch.full((7, H + 1, R + 64), 5.0, dtype=BF16)
     wide[:5, :H, :R], wide[:5, 1:, R:] = q_lat, q_rope
@@ -142,11 +161,11 @@ def test_strided_queries_and_rows_behind():
     assert (out[5:] == 3).all() and (lse[5:] == 3).all()
 
 
-@pytest.mark.parametrize("H", [16, 128])
-def test_late_maximum(H):
+@pytest.mark.parametrize("H", [16, 32, 64, 128])
+def test_late_maximum(H, width):
     """Scores that grow along the sequence by far more than the lazy rescale's
     margin, then fall: the running maximum moves many times."""
-    args = batch(H, [2], [400], 64, BF16, 61)
+    args = batch(H, [1 if H < 100 else 2], [400], 64, BF16, 61, W=columns(width, [400], 64))
     q_lat, q_rope, cache, table, cu, lens = args
     size = torch.linspace(0.1, 6.0, 400)
     size[300:] = torch.linspace(6.0, 0.1, 100)
@@ -158,24 +177,34 @@ def test_late_maximum(H):
 
 
 @pytest.mark.parametrize("scale", [-0.05, 0.0, 1.0])
-def test_any_scale(scale):
-    compare(batch(16, [2, 1], [60, 99], 32, BF16, 71), f"scale {scale}", scale=scale)
+def test_any_scale(scale, width):
+    lens = [60, 99]
+    compare(batch(96, [2, 1], lens, 32, BF16, 71, W=columns(width, lens, 32)), f"scale {scale}", scale=scale)
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
-def test_many_sequences(dtype):
+def test_many_sequences(dtype, width):
     """300 sequences of odd lengths, none, one or a few new tokens each."""
     g = torch.Generator().manual_seed(81)
     nq = torch.randint(0, 4, (300,), generator=g).tolist()
     lens = torch.randint(0, 90, (300,), generator=g).tolist()
-    compare(batch(8, nq, lens, 16, dtype, 82), "300 sequences")
+    compare(batch(8, nq, lens, 16, dtype, 82, W=columns(width, lens, 16)), "300 sequences")
 
 
-@pytest.mark.parametrize("H,B,n", [(16, 1, 20000), (128, 2, 9000), (16, 3, 5000)])
-def test_long_sequences(H, B, n):
-    """Few rows over a long cache (the token axis is split and joined)."""
-    args = batch(H, [1] * B, [n - 37 * b for b in range(B)], 64, FP8 if H == 16 else BF16, 91 + n)
+@pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("H,B,n", [(16, 1, 20000), (128, 2, 5000), (16, 3, 5000), (64, 1, 7000), (32, 2, 6000)])
+def test_long_sequences(H, B, n, dtype, width):
+    """Few rows over a long cache: the token axis is split, and joined from a few parts or from many."""
+    lens = [n - 37 * b for b in range(B)]
+    args = batch(H, [1] * B, lens, 64, dtype, 91 + n, W=columns(width, lens, 64))
     compare(args, f"long {H} {B} {n}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
+def test_chunk_over_many_tiles(dtype, width):
+    """More row tiles than one workgroup takes, whole and split, in sequences of several lengths."""
+    nq, lens = [70, 3, 90, 1], [300, 800, 90, 1000]
+    compare(batch(40, nq, lens, 48, dtype, 96, W=columns(width, lens, 48)), "chunk over many tiles")
 
 
 def test_no_new_tokens_and_no_sequences():

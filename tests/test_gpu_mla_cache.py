@@ -189,6 +189,7 @@ def run_update(cache, table, lens, parent, want):
     (1, 1, 16, 8, 40, 6), (4, 9, 8, 60, 50, 8), (7, 3, 1, 90, 12, 20), (3, 20, 64, 40, 200, 5),
     (30, 40, 16, 400, 100, 9), (5, 12, 7, 33, 60, 12),          # the last runs out of pages
     (40, 300, 4, 3000, 60, 70), (6, 1500, 16, 70000, 300, 24), (2, 5, 4096, 6, 5000, 3),
+    (20, 30, 16, 300, 100, 6000), (3, 2500, 4, 9000, 60, 16),   # wide tables, many rows: not one launch
 ])
 def test_update(B, N, ps, P, ctx, W, dtype):
     table, lens, parent, want = random_rows(B * 100 + N, B, N, ps, P, ctx, W)
@@ -256,7 +257,8 @@ def test_update_beam_search_steps():
 
 @pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
 @pytest.mark.parametrize("B,ps,P,ctx,W", [(1, 16, 40, 100, 9), (9, 8, 333, 100, 14), (20, 1, 500, 30, 30),
-                                          (5, 64, 31, 400, 8), (0, 16, 9, 10, 3), (3, 16, 6, 32, 2), (50, 4, 40000, 90, 30)])
+                                          (5, 64, 31, 400, 8), (0, 16, 9, 10, 3), (3, 16, 6, 32, 2), (50, 4, 40000, 90, 30),
+                                          (30, 8, 700, 100, 9000)])
 def test_compact(B, ps, P, ctx, W, dtype):
     table, lens, _, _ = random_rows(300 + B + P, B, 1, ps, P, ctx, W) if B else (
         torch.zeros((0, W), dtype=torch.int32), torch.zeros(0, dtype=torch.int32), None, None)
