@@ -63,7 +63,6 @@ constexpr int kTileB = 4 * kBlockB;     // 36,864 bytes
 // place in the tile at once), four scales a token (twice)
 template <bool PIPE>
 constexpr int raw_bytes() { return (PIPE ? 4 : 5) * kGroupB + 256; }
-constexpr int kAhead = 6;                // fragments read ahead of their products
 constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -168,6 +167,13 @@ __device__ __forceinline__ void acc_write(v4f v) {
                "v_accvgpr_write_b32 a[%6], %2\n\tv_accvgpr_write_b32 a[%7], %3"
                :: "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "n"(4 * I), "n"(4 * I + 1), "n"(4 * I + 2), "n"(4 * I + 3));
 }
+// Four e4m3 codes times a power-of-two scale, exactly, in bf16: the instruction takes the scale's
+// exponent (checked over all codes and the scales 2^-100 .. 2^100).
+__device__ __forceinline__ v2u codes4_bf16(uint32_t codes, float scale) {
+  return v2u{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, false)),
+             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, true))};
+}
+
 // calls f with the constants 0 .. N-1
 template <int N, int I = 0, typename F>
 __device__ __forceinline__ void unroll(const F& f) {
@@ -441,6 +447,9 @@ mla_attention_kernel(AttnParams p) {
   constexpr int CH = 8 * 64 / ROWS;                  // channels of a K step of the scores
   constexpr int QN = (kR + kD) / CH;                 // K steps
   constexpr int QS = PIPE && WIDE ? kR / CH : QN;          // those whose Q is in registers; PIPE: the rotated ones are in LDS
+  // Fragments read ahead of their products: the LDS's latency in products of 32 cycles, or of 16
+  // (16 rows: 6 ahead left the waves waiting half the time; with the codes in registers there is no room)
+  constexpr int kAhead = WIDE || (FP8 && RW == 1) ? 6 : 12;
   constexpr int NV = 32;                             // fragments of the latents as values
   constexpr int NF = 36;                             // fragments of the latents as keys
   constexpr int GS = Scores<ROWS>::TS, NG = kR / GS; // accumulators: NG groups of 4 channels from GS i + 4 g
@@ -552,8 +561,9 @@ mla_attention_kernel(AttnParams p) {
     const int t = ln >> 3, c = 2 * (ln & 3);
     const uint32_t at = to + sub * kBlockB + (2 * i + ((ln & 7) >> 2)) * kGroupB + t * 128;
     const int x = swz<ROWS>(8 * sub + t);
-    *(lds_v4u*)(uintptr_t)(at + ((c ^ x) << 4)) = __builtin_bit_cast(v4u, dequant8_bf16(codes.x, codes.y, sc));
-    *(lds_v4u*)(uintptr_t)(at + (((c + 1) ^ x) << 4)) = __builtin_bit_cast(v4u, dequant8_bf16(codes.z, codes.w, sc));
+    const v2u d0 = codes4_bf16(codes.x, sc), d1 = codes4_bf16(codes.y, sc), d2 = codes4_bf16(codes.z, sc), d3 = codes4_bf16(codes.w, sc);
+    *(lds_v4u*)(uintptr_t)(at + ((c ^ x) << 4)) = v4u{d0.x, d0.y, d1.x, d1.y};
+    *(lds_v4u*)(uintptr_t)(at + (((c + 1) ^ x) << 4)) = v4u{d2.x, d2.y, d3.x, d3.y};
   };
   auto spread_rope = [&](int sub, v4u v, uint32_t to) {
     int ln = lane;
@@ -573,22 +583,20 @@ mla_attention_kernel(AttnParams p) {
       spread_rope(sub, v, to);
     }
   };
-  // PIPE: the same in 24 pieces of a few instructions, six a group: read, convert four codes at a time, write
+  // PIPE: the same in 16 pieces of a few instructions, four a group: read, convert, convert, write
   v4u some_codes, some_bf16[2];
   float some_scale = 0.0f;
   auto spread_bit = [&](auto u, uint32_t from, uint32_t to) {
-    constexpr int i = u / 6, k = u % 6;
+    constexpr int i = u / 4, k = u % 4;
     int ln = lane;
     asm volatile("" : "+v"(ln));
     if constexpr (k == 0) {
       typedef const __attribute__((address_space(3))) float lds_f;
       some_codes = *(const lds_v4u*)(uintptr_t)(from + i * kGroupB + ln * 16);
       some_scale = *(lds_f*)(uintptr_t)(from + 4 * kGroupB + (ln >> 3) * 32 + i * 4);
-    } else if constexpr (k < 5) {
-      const v2f a = __builtin_amdgcn_cvt_pk_f32_fp8((int)some_codes[k - 1], false);
-      const v2f c = __builtin_amdgcn_cvt_pk_f32_fp8((int)some_codes[k - 1], true);
-      some_bf16[(k - 1) / 2][(k - 1) % 2 * 2] = pack2_bf16(__fmul_rn(a.x, some_scale), __fmul_rn(a.y, some_scale));
-      some_bf16[(k - 1) / 2][(k - 1) % 2 * 2 + 1] = pack2_bf16(__fmul_rn(c.x, some_scale), __fmul_rn(c.y, some_scale));
+    } else if constexpr (k < 3) {
+      const v2u a = codes4_bf16(some_codes[2 * k - 2], some_scale), c = codes4_bf16(some_codes[2 * k - 1], some_scale);
+      some_bf16[k - 1] = v4u{a.x, a.y, c.x, c.y};
     } else {
       const int t = ln >> 3, c = 2 * (ln & 3);
       const uint32_t at = to + rw * kBlockB + (2 * i + ((ln & 7) >> 2)) * kGroupB + t * 128;
@@ -752,7 +760,7 @@ mla_attention_kernel(AttnParams p) {
       if constexpr (FP8) {
         wait_vmcnt<0>();
         for (int k = 0; k < 2; ++k) {
-          unroll<24>([&](auto u) { spread_bit(u, raw_at + k * kRawB, tile_at + k * kTileB); });
+          unroll<16>([&](auto u) { spread_bit(u, raw_at + k * kRawB, tile_at + k * kTileB); });
         }
         __builtin_amdgcn_s_waitcnt(0xc07f);          // lgkmcnt(0): the codes are read before others land on them
         fetch(t_seg + 2 * STEP, tile_at + 2 * kTileB, raw_at);
@@ -806,11 +814,11 @@ mla_attention_kernel(AttnParams p) {
         product(f);
         value(std::integral_constant<int, f + kAhead>{});
         if constexpr (FP8) {
-          if constexpr (f < 24) spread_bit(f, codes, tile_at + two * kTileB);
-          else if constexpr (f == 24) f3 = find(tb + 4 * STEP, rw);
+          if constexpr (f < 16) spread_bit(f, codes, tile_at + two * kTileB);
+          else if constexpr (f == 16) f3 = find(tb + 4 * STEP, rw);
         } else {
           if constexpr (f == 0) f3 = find(tb + 3 * STEP, rw);
-          if constexpr (f >= 4 && f % 2 == 0 && f < 4 + 2 * NL) ask(f3, tile_at + free * kTileB + rw * kBlockB, 0u, std::integral_constant<int, (f - 4) / 2>{});
+          if constexpr (f >= 3 && f % 2 == 1 && f < 3 + 2 * NL) ask(f3, tile_at + free * kTileB + rw * kBlockB, 0u, std::integral_constant<int, (f - 3) / 2>{});
         }
       });
       place = next(place);
@@ -820,7 +828,7 @@ mla_attention_kernel(AttnParams p) {
       unroll<kAhead>([&](auto i) {
         fence();
         product(std::integral_constant<int, NV - kAhead + i>{});
-        if constexpr (FP8) ask(f3, tile_at + place * kTileB + rw * kBlockB, codes, i);
+        if constexpr (FP8 && i < NL) ask(f3, tile_at + place * kTileB + rw * kBlockB, codes, i);
       });
       unroll<kAhead>([&](auto f) { key(f); });
       s = t;
