@@ -583,26 +583,32 @@ mla_attention_kernel(AttnParams p) {
       spread_rope(sub, v, to);
     }
   };
-  // PIPE: the same in 16 pieces of a few instructions, four a group: read, convert, convert, write
-  v4u some_codes, some_bf16[2];
-  float some_scale = 0.0f;
-  auto spread_bit = [&](auto u, uint32_t from, uint32_t to) {
-    constexpr int i = u / 4, k = u % 4;
+  // PIPE: the same in 20 pieces of a few instructions: group i is read in piece 4 i, and converted and
+  // written in the pieces 4 i + 5 .. + 7, when it has come
+  v4u some_codes[2], some_bf16[2];
+  float some_scale[2];
+  uint32_t codes_from = 0, scales_from = 0, bf16_to = 0;
+  auto spread_at = [&](uint32_t from, uint32_t to) {
     int ln = lane;
     asm volatile("" : "+v"(ln));
-    if constexpr (k == 0) {
-      typedef const __attribute__((address_space(3))) float lds_f;
-      some_codes = *(const lds_v4u*)(uintptr_t)(from + i * kGroupB + ln * 16);
-      some_scale = *(lds_f*)(uintptr_t)(from + 4 * kGroupB + (ln >> 3) * 32 + i * 4);
-    } else if constexpr (k < 3) {
-      const v2u a = codes4_bf16(some_codes[2 * k - 2], some_scale), c = codes4_bf16(some_codes[2 * k - 1], some_scale);
+    const int t = ln >> 3, c = 2 * (ln & 3);
+    codes_from = from + ln * 16;
+    scales_from = from + 4 * kGroupB + t * 32;
+    bf16_to = to + rw * kBlockB + ((ln & 7) >> 2) * kGroupB + t * 128 + ((c ^ swz<ROWS>(8 * rw + t)) << 4);
+  };
+  auto spread_bit = [&](auto u) {
+    constexpr int i = u / 4, k = u % 4;
+    typedef const __attribute__((address_space(3))) float lds_f;
+    if constexpr (k == 0 && i < 4) {
+      some_codes[i % 2] = *((const lds_v4u*)(uintptr_t)codes_from + i * 64);
+      some_scale[i % 2] = *((lds_f*)(uintptr_t)scales_from + i);
+    } else if constexpr (i > 0 && k > 0 && k < 3) {
+      const v4u w = some_codes[(i - 1) % 2];
+      const v2u a = codes4_bf16(w[2 * k - 2], some_scale[(i - 1) % 2]), c = codes4_bf16(w[2 * k - 1], some_scale[(i - 1) % 2]);
       some_bf16[k - 1] = v4u{a.x, a.y, c.x, c.y};
-    } else {
-      const int t = ln >> 3, c = 2 * (ln & 3);
-      const uint32_t at = to + rw * kBlockB + (2 * i + ((ln & 7) >> 2)) * kGroupB + t * 128;
-      const int x = swz<ROWS>(8 * rw + t);
-      *(lds_v4u*)(uintptr_t)(at + ((c ^ x) << 4)) = some_bf16[0];
-      *(lds_v4u*)(uintptr_t)(at + (((c + 1) ^ x) << 4)) = some_bf16[1];
+    } else if constexpr (i > 0 && k == 3) {
+      *((lds_v4u*)(uintptr_t)bf16_to + (i - 1) * 2 * 64) = some_bf16[0];
+      *((lds_v4u*)(uintptr_t)(bf16_to ^ 16) + (i - 1) * 2 * 64) = some_bf16[1];
     }
   };
   // FP8, RW = 1: the codes in registers
@@ -728,11 +734,11 @@ mla_attention_kernel(AttnParams p) {
       top = m == kNegInf ? 0.0f : -m;
     } else if constexpr (i <= NS / 4 + NS) {
       constexpr int e = i - NS / 4 - 1;
-      const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s.template get<e>(), p.scale2, top));
-      s.template set<e>(y);
-      l += y;
+      s.template set<e>(__builtin_amdgcn_exp2f(__builtin_fmaf(s.template get<e>(), p.scale2, top)));
+      if constexpr (e > 0) l += s.template get<e - 1>();   // the one before: this one is not there at once
     } else {
       constexpr int k = i - NS / 4 - 1 - NS;
+      if constexpr (k == 0) l += s.template get<NS - 1>();
       v4u u;
       unroll<4>([&](auto d) { u[(int)d] = pack2_bf16(s.template get<8 * k + 2 * d>(), s.template get<8 * k + 2 * d + 1>()); });
       pr[k] = __builtin_bit_cast(v8bf, u);
@@ -760,7 +766,8 @@ mla_attention_kernel(AttnParams p) {
       if constexpr (FP8) {
         wait_vmcnt<0>();
         for (int k = 0; k < 2; ++k) {
-          unroll<16>([&](auto u) { spread_bit(u, raw_at + k * kRawB, tile_at + k * kTileB); });
+          spread_at(raw_at + k * kRawB, tile_at + k * kTileB);
+          unroll<20>([&](auto u) { spread_bit(u); });
         }
         __builtin_amdgcn_s_waitcnt(0xc07f);          // lgkmcnt(0): the codes are read before others land on them
         fetch(t_seg + 2 * STEP, tile_at + 2 * kTileB, raw_at);
@@ -814,8 +821,9 @@ mla_attention_kernel(AttnParams p) {
         product(f);
         value(std::integral_constant<int, f + kAhead>{});
         if constexpr (FP8) {
-          if constexpr (f < 16) spread_bit(f, codes, tile_at + two * kTileB);
-          else if constexpr (f == 16) f3 = find(tb + 4 * STEP, rw);
+          if constexpr (f == 0) spread_at(codes, tile_at + two * kTileB);
+          if constexpr (f < 20) spread_bit(f);
+          if constexpr (f == 16) f3 = find(tb + 4 * STEP, rw);
         } else {
           if constexpr (f == 0) f3 = find(tb + 3 * STEP, rw);
           if constexpr (f >= 3 && f % 2 == 1 && f < 3 + 2 * NL) ask(f3, tile_at + free * kTileB + rw * kBlockB, 0u, std::integral_constant<int, (f - 3) / 2>{});
