@@ -338,6 +338,9 @@ int fp8bs_moe_combine(const void* out_bf16, const float* w, const int32_t* row_o
                                              out_dtype == FP8BS_OUT_F32, (hipStream_t)stream));
 }
 
+// rows that a launch has a workgroup of 256 threads for (it has at most 2^32 - 1 threads)
+static const int64_t kLimitRows = (1 << 24) - 1;
+
 // what the paged-cache entry points share: sizes, format, pointers and alignment of the cache
 static int cache_checks(const void* latent, const float* lat_scale, const void* rope, int cache_fmt,
                         int64_t B, int64_t W, int64_t P, int64_t ps, int64_t R, int64_t dr) {
@@ -374,7 +377,7 @@ int fp8bs_mla_cache_write(const void* q_rope, int64_t ldq_t, int64_t ldq_h, cons
                           float* lat_scale, void* rope, int cache_fmt, const int32_t* table,
                           const int32_t* cu_q, const int32_t* lens, int64_t T, int64_t H, int64_t B,
                           int64_t W, int64_t P, int64_t ps, int64_t R, int64_t dr, void* stream) {
-  if (T < 0 || H < 0 || T > kLimitInt || H > kLimitInt || n_pos < 0 || ldq_t < 0 || ldq_h < 0 ||
+  if (T < 0 || H < 0 || T > kLimitRows || H > kLimitInt || n_pos < 0 || ldq_t < 0 || ldq_h < 0 ||
       ld_kv < 0 || !(eps >= 0.0f && eps <= 3.0e38f))
     return FP8BS_ERR_SHAPE;
   const int64_t nq = mul(mul(T, H), 64);
@@ -383,7 +386,7 @@ int fp8bs_mla_cache_write(const void* q_rope, int64_t ldq_t, int64_t ldq_h, cons
   if (ldq_t % 8 != 0 || ldq_h % 8 != 0 || ld_kv % 8 != 0) return FP8BS_ERR_ALIGN;
   const int st = cache_checks(latent, lat_scale, rope, cache_fmt, B, W, P, ps, R, dr);
   if (st != FP8BS_OK) return st;
-  if (!kv || !norm_w || !rope_cs || !table || !cu_q || !lens || (H > 0 && (!q_rope || !q_out)))
+  if (!kv || !norm_w || (n_pos > 0 && !rope_cs) || !table || !cu_q || !lens || (H > 0 && (!q_rope || !q_out)))
     return FP8BS_ERR_NULL;
   if (!aligned(kv, 16) || !aligned(norm_w, norm_w_f32 ? 4 : 2) || !aligned(rope_cs, 4) ||
       !aligned(table, 4) || !aligned(cu_q, 4) || !aligned(lens, 4) ||
@@ -465,7 +468,7 @@ int fp8bs_cache_update(void* latent, float* lat_scale, void* rope, int cache_fmt
   const int64_t need = fp8bs_cache_update_workspace_size(P, N);
   if (need < 0) return FP8BS_ERR_SHAPE;
   if (N == 0) return FP8BS_OK;
-  if (workspace_bytes < need || mul(N, W) < 0 || mul(mul(N, W), 4) < 0 || B + N > kLimitInt) return FP8BS_ERR_SHAPE;
+  if (workspace_bytes < need || mul(N, W) < 0 || mul(mul(N, W), 4) < 0 || B > kLimitRows - N) return FP8BS_ERR_SHAPE;
   const int st = cache_checks(latent, lat_scale, rope, cache_fmt, B, W, P, ps, R, dr);
   if (st != FP8BS_OK) return st;
   if (!parent || !new_lens || !table_out || !lens_out || !workspace || (B > 0 && (!table || !lens)))
@@ -501,7 +504,7 @@ int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fm
                         int32_t* count, int64_t B, int64_t W, int64_t P, int64_t ps, int64_t R,
                         int64_t dr, void* workspace, int64_t workspace_bytes, void* stream) {
   const int64_t need = fp8bs_cache_compact_workspace_size(P);
-  if (need < 0 || workspace_bytes < need) return FP8BS_ERR_SHAPE;
+  if (need < 0 || workspace_bytes < need || B > kLimitRows) return FP8BS_ERR_SHAPE;
   const int st = cache_checks(latent, lat_scale, rope, cache_fmt, B, W, P, ps, R, dr);
   if (st != FP8BS_OK) return st;
   if (!count || !workspace || (B > 0 && (!table || !lens || !table_out))) return FP8BS_ERR_NULL;

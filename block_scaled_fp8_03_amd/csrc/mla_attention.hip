@@ -341,6 +341,7 @@ struct Plan {
     return kStart + (s.nq <= s.len / 8 ? (s.len + STEP - 1) / STEP : tile_steps(p, s, in_seq));
   }
 
+  static constexpr int kBytes = 256 + 4 * (kSeqs + 4) + (int)sizeof(Seq) * kSeqs;
   // false: this workgroup has no share
   __device__ bool make(const AttnParams& p, int w, uint8_t* smem) {
     int64_t* sums = reinterpret_cast<int64_t*>(smem);
@@ -356,6 +357,9 @@ struct Plan {
       mine += ((int64_t)seq[b].nq * p.H + M - 1) / M;
     }
     int64_t at = block_scan(mine, sums, sum);
+    // a cu_q that decreases lays sequences over each other: such a batch is left undone when its rows are more
+    // than there are, so that the counts stay in range and the work bounded
+    if (sum > (int64_t)p.T * p.H / M + p.B) return false;
     const int tiles = (int)sum;
     for (int b = b0; b < b1; ++b) {
       first[b] = (int)at;
@@ -453,7 +457,8 @@ mla_attention_kernel(AttnParams p) {
   constexpr int NV = 32;                             // fragments of the latents as values
   constexpr int NF = 36;                             // fragments of the latents as keys
   constexpr int GS = Scores<ROWS>::TS, NG = kR / GS; // accumulators: NG groups of 4 channels from GS i + 4 g
-  static_assert(RW * TW == 4 && lds_bytes<ROWS, RW, TW, FP8>() <= 160 * 1024, "layout");
+  static_assert(RW * TW == 4 && lds_bytes<ROWS, RW, TW, FP8>() <= 160 * 1024 &&
+                Plan<M, STEP>::kBytes <= lds_bytes<ROWS, RW, TW, FP8>(), "layout");
   static_assert(NF % kAhead == 0 && kAhead % 2 == 0, "the two streams of fragments share x");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[lds_bytes<ROWS, RW, TW, FP8>()];
   const int lane = threadIdx.x & 63;
@@ -705,11 +710,34 @@ mla_attention_kernel(AttnParams p) {
     else acc_mfma<ROWS, f>(x[f % kAhead], pr[0]);
   };
   // masked places of the scores of tokens tb .. (only in tiles that some row does not see whole)
-  auto hide = [&](int tb) {
-    if (tb + kTok <= end_min) return;
+  // A token that some row of the tile does not see may hold infinities or NaN, which a probability of 0
+  // does not take out of the product.  Every row's score of it is then not finite either, so the
+  // masked scores tell; what is not finite in the values becomes 0 (a row that sees it has NaN in its sum).
+  auto hide = [&](int tb, uint32_t tile) {
+    if (tb + kTok <= end_min) return false;
+    bool odd = false;
     unroll<Scores<ROWS>::N>([&](auto e) {
-      if (tb + GS * (e / 4) + 4 * g + e % 4 >= end) s.template set<e>(kNegInf);
+      if (tb + GS * (e / 4) + 4 * g + e % 4 >= end) {
+        odd |= __builtin_amdgcn_classf(s.template get<e>(), 0x207);   // NaN, -inf, inf
+        s.template set<e>(kNegInf);
+      }
     });
+    if (end_min == end_max || !__any(odd)) return false;
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    uint32_t at = tile + ln * 16;
+#pragma unroll 1
+    for (int i = 0; i < 4 * 8; ++i) {
+      v4u v = *(const lds_v4u*)(uintptr_t)at;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        if ((v[d] & 0x7F80u) == 0x7F80u) v[d] &= 0xFFFF0000u;
+        if ((v[d] & 0x7F800000u) == 0x7F800000u) v[d] &= 0xFFFFu;
+      }
+      *(lds_v4u*)(uintptr_t)at = v;
+      at += i % 8 == 7 ? 2 * kGroupB : kGroupB;      // past the rotated group
+    }
+    return true;
   };
   // Scores to probabilities in kSoft pieces that fit beside a matrix instruction: the maximum of four
   // scores; the check of it; one probability; eight of them packed
@@ -795,7 +823,7 @@ mla_attention_kernel(AttnParams p) {
     int place = 0;                                   // of tile k
     for (int k = 0; k < n_steps; ++k) {
       const int tb = t_seg + k * STEP;
-      hide(tb);
+      hide(tb, tile_at + place * kTileB);            // every wave has this tile's scores
       values_at(place * kTileB);
       if (k + 1 < n_steps) {
         t.clear();
@@ -892,7 +920,9 @@ mla_attention_kernel(AttnParams p) {
         else value(std::integral_constant<int, f + kAhead - NF>{});
       });
       fence();
-      hide(tb);
+      if constexpr (RW > 1)                          // the other row waves have the boundary tile's scores
+        if (end_min < end_max && (step0 + k + 1) * STEP > end_min) barrier_lds();
+      if (hide(tb, tile_at + off)) unroll<kAhead>([&](auto f) { value(f); });
       unroll<kSoft>([&](auto i) { soft(i); });
       operands_settle();
       unroll<NV>([&](auto f) {
@@ -923,21 +953,22 @@ mla_attention_kernel(AttnParams p) {
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < TW; ++k) mt = fmaxf(mt, red[(k * RW + rw) * 2 * ROWS + n]);
+      const float base = mt == kNegInf ? 0.0f : mt;
       lt = 0.0f;
 #pragma unroll
       for (int k = 0; k < TW; ++k) {
-        const float mk = red[(k * RW + rw) * 2 * ROWS + n];
-        if (mk > kNegInf) lt += red[(k * RW + rw) * 2 * ROWS + ROWS + n] * __builtin_amdgcn_exp2f(mk - mt);
+        const float* rk = red + (k * RW + rw) * 2 * ROWS + n;
+        lt += rk[ROWS] * __builtin_amdgcn_exp2f(rk[0] - base);
       }
-      part = m > kNegInf ? __builtin_amdgcn_exp2f(m - mt) : 0.0f;
+      part = __builtin_amdgcn_exp2f(m - base);
     }
     const int r = rw * ROWS + n;                     // row of the tile
     const bool mine = r_tile + r <= r_last;
-    const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
+    const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;   // (a sum that is NaN gives NaN)
     const int64_t orow = (int64_t)sq.q0 * p.H + r_tile + r;
     const int64_t slot = 2 * (int64_t)w + (step0 == 0);
     if (tw == 0 && g == 0) {
-      const float lse = lt > 0.0f ? mt + __builtin_log2f(lt) : kNegInf;
+      const float lse = lt == 0.0f ? kNegInf : mt + __builtin_log2f(lt);
       if (!whole) p.part_lse[slot * M + r] = lse;
       else if (mine && p.lse) p.lse[orow] = lse * kLn2;
     }
@@ -1037,11 +1068,11 @@ __global__ void __launch_bounds__(512) join_kernel(AttnParams p, int RW) {
 #pragma unroll
         for (int i = 0; i < kRun; ++i) acc[i] += *reinterpret_cast<const v4f*>(src + i * 256) * x;
       }
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
       for (int i = 0; i < kRun; ++i) finish(r, i0 + i, acc[i], inv);
       if (i0 == 0 && g == 0 && r < meta.rows && p.lse)
-        p.lse[meta.row + r] = sum > 0.0f ? (top + __builtin_log2f(sum)) * kLn2 : kNegInf;
+        p.lse[meta.row + r] = sum == 0.0f ? kNegInf : (top + __builtin_log2f(sum)) * kLn2;
     } else {
       const int rw = u / (NG / kRunMany), i0 = u % (NG / kRunMany) * kRunMany, r = rw * ROWS + n;
       float top = kNegInf, sum = 0.0f;
@@ -1075,9 +1106,9 @@ __global__ void __launch_bounds__(512) join_kernel(AttnParams p, int RW) {
           v += *reinterpret_cast<const v4f*>(meet[k][wave][lane]);
           sum += meet[k][kRunMany][lane][1];
         }
-        finish(r, i0 + wave, v, sum > 0.0f ? 1.0f / sum : 0.0f);
+        finish(r, i0 + wave, v, sum == 0.0f ? 0.0f : 1.0f / sum);
         if (i0 == 0 && wave == 0 && g == 0 && r < meta.rows && p.lse)
-          p.lse[meta.row + r] = sum > 0.0f ? (top + __builtin_log2f(sum)) * kLn2 : kNegInf;
+          p.lse[meta.row + r] = sum == 0.0f ? kNegInf : (top + __builtin_log2f(sum)) * kLn2;
       }
     }
   }

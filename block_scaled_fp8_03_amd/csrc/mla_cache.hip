@@ -231,18 +231,19 @@ __global__ void __launch_bounds__(256) page_mark_kernel(PageParams p) {
 }
 
 // exclusive prefix sum over the workgroup's 1024 threads; total gets the sum
-__device__ __forceinline__ int block_scan(int v, int* sums, int& total) {
+template <typename I>
+__device__ __forceinline__ I block_scan(I v, I* sums, I& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int x = v;
+  I x = v;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d);
+    const I y = __shfl_up(x, d);
     if (lane >= d) x += y;
   }
   __syncthreads();
   if (lane == 63) sums[wave] = x;
   __syncthreads();
-  int base = 0;
+  I base = 0;
   total = 0;
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
@@ -254,6 +255,7 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int& total) {
 
 __global__ void __launch_bounds__(1024) page_plan_update_kernel(PageParams p) {
   __shared__ int sums[16];
+  __shared__ int64_t long_sums[16];                  // 1024 rows may ask for more than 2^31 pages
   int n_free = 0;
   for (int w0 = 0; w0 < p.words; w0 += 1024) {
     const int w = w0 + threadIdx.x;
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(1024) page_plan_update_kernel(PageParams p) {
       bits = ~p.used[w];
       if (w == p.P / 32) bits &= (1u << (p.P & 31)) - 1;
     }
-    int total, at = n_free + block_scan(__popc(bits), sums, total);
+    int total, at = n_free + block_scan((int)__popc(bits), sums, total);
     for (; bits; bits &= bits - 1) p.list[at++] = 32 * w + __ffs(bits) - 1;
     n_free += total;
   }
@@ -282,8 +284,8 @@ __global__ void __launch_bounds__(1024) page_plan_update_kernel(PageParams p) {
         need = pages_of(row.want, p.ps) - row.kept + copy;
       }
     }
-    int total;
-    const int64_t at = base + block_scan(need, sums, total);
+    int64_t total;
+    const int64_t at = base + block_scan((int64_t)need, long_sums, total);
     base += total;
     if (i < p.N) {
       const bool ok = need == 0 || at + need <= n_free;
@@ -378,7 +380,7 @@ __device__ __forceinline__ int count_before(const uint32_t* used, int* before, i
   for (int w0 = 0; w0 < words; w0 += 1024) {
     const int w = w0 + threadIdx.x;
     int total;
-    const int at = all + block_scan(w < words ? __popc(used[w]) : 0, sums, total);
+    const int at = all + block_scan(w < words ? (int)__popc(used[w]) : 0, sums, total);
     if (w < words) before[w] = at;
     all += total;
   }

@@ -400,7 +400,8 @@ int fp8bs_mla_absorb_value(const void* x_bf16, int64_t ld_t, int64_t ld_h, const
  * Values of table, lens and cu_q lie on the device and are preconditions, not
  * checked on the host; the kernels clamp lens to [0, W * ps] and cu_q to [0, T],
  * never write outside the cache, and read no page outside [0, P), so a wrong
- * value gives wrong results for its sequence, not faults.
+ * value gives wrong results for its sequence, not faults (a cu_q that decreases:
+ * for the batch).
  * Byte pointers are 16-byte aligned, float32 and int32 ones 4-byte.
  */
 
@@ -422,7 +423,7 @@ int fp8bs_mla_absorb_value(const void* x_bf16, int64_t ld_t, int64_t ld_h, const
  *   eps           >= 0, finite
  *   rope_cs  in   float32 [n_pos, 32, 2]: (cos, sin)
  *   q_out    out  bf16 [T, H, 64]
- *   T >= 0 (0 = no-op), H >= 0 (0 = no queries), B >= 0, n_pos >= 0.
+ *   0 <= T < 2^24 (0 = no-op), H >= 0 (0 = no queries), B >= 0, n_pos >= 0.
  * A token at a position outside [0, n_pos) is skipped: neither its cache row
  * nor its q_out is written.  A token whose page lies outside [0, P) has its
  * q_out written only.  Rows t >= cu_q[B] are left as they were.  Two tokens
@@ -460,8 +461,9 @@ int fp8bs_mla_cache_write(const void* q_rope, int64_t ldq_t, int64_t ldq_h, cons
  *   T, B >= 0 (either 0 = no-op), H >= 1, T * H < 2^31, B <= 8192.
  * Products are of bf16 values (an FP8 cache's are exact in bf16) and summed in
  * float32; the probabilities are rounded to bf16 for the second product, the
- * softmax's maximum and sum are float32.  The result does not depend on
- * timing.
+ * softmax's maximum and sum are float32.  A token that a row does not see has
+ * no part in it, whatever it holds (infinities and NaN too); a row that sees a
+ * NaN is NaN.  The result does not depend on timing.
  */
 int64_t fp8bs_mla_attention_workspace_size(int64_t T, int64_t H, int64_t B);
 int fp8bs_mla_attention(const void* q_lat, int64_t ldq_t, int64_t ldq_h, const void* q_rope,
@@ -486,7 +488,8 @@ int fp8bs_mla_attention(const void* q_lat, int64_t ldq_t, int64_t ldq_h, const v
  * not full) shares it only as the page's keeper, the lowest such row among
  * those that keep the most of the page's tokens; any other gets a copy: a page
  * of its own with the kept tokens.  A row for which too few pages are left
- * is not grown: lens_out[i] is then what it keeps.
+ * is not grown: lens_out[i] is then what it keeps (the pages that it asked for
+ * count as given out for the rows after it).
  *
  *   table, lens  in   old rows [B, W], [B]
  *   parent, new_lens  in   DEVICE int32 [N]; new_lens is clamped to [0, W * ps]
@@ -496,7 +499,7 @@ int fp8bs_mla_attention(const void* q_lat, int64_t ldq_t, int64_t ldq_h, const v
  *                     written, and only a copy's kept tokens
  *   workspace    DEVICE, >= fp8bs_cache_update_workspace_size(P, N) bytes,
  *                16-byte aligned, scratch; not shared by concurrent calls
- *   B >= 0, 0 <= N < 2^18 (N = 0: no-op).
+ *   B >= 0, 0 <= N < 2^18 (N = 0: no-op), B + N < 2^24.
  * The result depends on the inputs alone, and a repeated call gives it again.
  *
  * cache_compact -- the n pages that the rows use moved to pages 0 .. n - 1:
@@ -504,7 +507,7 @@ int fp8bs_mla_attention(const void* q_lat, int64_t ldq_t, int64_t ldq_h, const v
  * ascending order; table_out is the table with the new indices (-1 behind
  * each row's last page and for entries outside [0, P)), count = n.
  *   table_out    out  DEVICE int32 [B, W];  count  out  DEVICE int32 [1]
- *   workspace    >= fp8bs_cache_compact_workspace_size(P) bytes
+ *   workspace    >= fp8bs_cache_compact_workspace_size(P) bytes;  B < 2^24
  */
 int64_t fp8bs_cache_update_workspace_size(int64_t P, int64_t N);
 int fp8bs_cache_update(void* latent, float* lat_scale, void* rope, int cache_fmt,

@@ -124,6 +124,50 @@ def test_garbage_out_of_sight(H, nq, width):
     compare(args, "clean")
 
 
+@pytest.mark.parametrize("H,nq", [(16, [3, 40]), (4, [30, 9]), (2, [16, 12]), (1, [12, 7]), (128, [3, 2])])
+@pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
+def test_not_finite_where_masked(H, nq, dtype, width):
+    """NaN (and in bf16 infinities) in tokens that only a chunk's later rows see:
+    the rows before them are what they are without, those that see a NaN are NaN."""
+    lens = [70, 131]
+    args = batch(H, nq, lens, 16, dtype, 61 + H, W=columns(width, lens, 16))
+    q_lat, q_rope, cache, table, cu, ln = args
+    for b, (n, m) in enumerate(zip(lens, nq)):
+        first = n - m + (m + 1) // 2                 # the first bad token
+        for at, kind in ((first, math.nan), (first + 1, math.inf), (first + 2, math.nan)):
+            if at < n:
+                page = cache.latent[table[b, at // 16], at % 16]
+                if dtype == FP8:
+                    page.view(torch.uint8)[7 * b + 3] = 0x7F
+                    page.view(torch.uint8)[500] = 0xFF
+                else:
+                    page[7 * b + 3], page[500] = kind, -kind
+        cache.rope[table[b, first // 16], first % 16, 9] = math.inf
+    out, lse = run(args)
+    ref = attention64(q_lat, q_rope, cache, table, cu, ln, SCALE, True)
+    clean = ~torch.isnan(ref[1]).any(1)
+    sees = torch.cat([torch.arange(m) >= (m + 1) // 2 for m in nq])
+    assert torch.equal(clean, ~sees)
+    check_attention(out[clean.to(DEV)], lse[clean.to(DEV)], tuple(x[clean] for x in ref), 131, "rows that do not see it")
+    assert torch.isnan(out[sees.to(DEV)]).all() and torch.isnan(lse[sees.to(DEV)]).all()
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_boundaries_that_decrease(H, width):
+    """cu_q out of order is outside the contract, but writes only rows of the
+    call; sequences laid over each other many times are left undone."""
+    lens = [40] * 5
+    q_lat, q_rope, cache, table, _, ln = batch(H, [40], lens, 16, BF16, 71, W=columns(width, lens, 16))
+    for cu, undone in (([0, 30, 10, 40, 40, 40], False), ([0, 40, 0, 40, 0, 40], True)):
+        out = torch.full((48, H, R), 3.0, dtype=BF16, device=DEV)
+        ws = torch.empty(fp8bs.lib().fp8bs_mla_attention_workspace_size(40, H, 5), dtype=torch.uint8, device=DEV)
+        fp8bs.fp8bs_mla_attention(q_lat.to(DEV), q_rope.to(DEV), to_dev(cache), table.to(DEV),
+                                  torch.tensor(cu, dtype=torch.int32, device=DEV), ln.to(DEV), SCALE, out[4:44], None, ws)
+        torch.cuda.synchronize()
+        assert (out[:4] == 3).all() and (out[44:] == 3).all()
+        assert not undone or (out == 3).all()
+
+
 @pytest.mark.parametrize("H", [16, 32, 64, 128])
 @pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
 def test_pages_outside_the_cache_do_not_fault(H, dtype, width):

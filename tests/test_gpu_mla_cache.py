@@ -124,6 +124,24 @@ def test_write_skips_what_has_no_place():
     assert (q_out[[3, 6, 7]] == 9).all() and not (q_out[[0, 1, 2, 4, 5]] == 9).all(-1).any()
 
 
+@pytest.mark.parametrize("B", [64, 65, 300, 5000])
+def test_write_many_sequences(B):
+    """The sequence of a token among many, some without new tokens."""
+    g = torch.Generator().manual_seed(B)
+    nq = torch.randint(0, 3, (B,), generator=g).tolist()
+    lens = [n + int(x) for n, x in zip(nq, torch.randint(0, 5, (B,), generator=g))]
+    q, kv, w, cs, cache, table, cu, ln = write_case(1, nq, lens, 4, BF16, BF16, B)
+    dev = to_dev(cache)
+    q_out = fp8bs.mla_cache_write(q.to(DEV)[..., 128:], kv.to(DEV), w.to(DEV), 1e-6, cs.to(DEV), dev, table.to(DEV),
+                                  cu.to(DEV), ln.to(DEV))
+    tok, pos, pg, off = (torch.tensor(x) for x in zip(*slots(nq, lens, table, 4)))
+    c, k, qr = write64(q[tok][..., 128:], kv[tok], w, 1e-6, cs, pos)
+    x = latent64(fp8bs.MlaCache(*(None if t is None else t.cpu() for t in dev)))[pg, off]
+    assert ((x - c).abs() <= (U8 + 2.0 ** -20) * c.abs()).all()
+    size = q[tok][..., 128:].double().unflatten(-1, (-1, 2)).abs().sum(-1).repeat_interleave(2, -1)
+    assert ((q_out.double().cpu()[tok] - qr).abs() <= U8 * qr.abs() + 2.0 ** -22 * size).all()
+
+
 def test_write_quantises_as_act_quant():
     """With the norm switched off (unit-size rows, weight 1) the 8-bit cache
     holds exactly act_quant's ue8m0 codes and scales of the bf16 latents."""
@@ -301,3 +319,18 @@ def test_bad_tables_stay_inside():
     t, l = fp8bs.cache_update(dev, table.to(DEV), lens.to(DEV), torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV),
                               torch.tensor([25, 5, 2 ** 31 - 1], dtype=torch.int32, device=DEV))
     assert l.tolist() == [24, 5, 24] and t[0].tolist() == [3, 4, 5] and t[2].tolist() == [0, 1, 2]
+
+
+def test_update_rows_that_ask_for_more_than_int32():
+    """1024 rows that ask for 2^21 pages each, 2^31 together: none is grown, nor
+    is the row behind them, whose turn comes after theirs."""
+    W, N = 1 << 21, 1100
+    cache = fp8bs.mla_cache_alloc(64, 1, DEV)
+    want = torch.full((N,), W, dtype=torch.int32)
+    want[0], want[-1] = 3, 1
+    none = torch.full((N,), -1, dtype=torch.int32, device=DEV)
+    t, l = fp8bs.cache_update(cache, torch.full((1, W), -1, dtype=torch.int32, device=DEV),
+                              torch.zeros(1, dtype=torch.int32, device=DEV), none, want.to(DEV))
+    assert l[0] == 3 and (l[1:] == 0).all()
+    assert t[0, :4].tolist() == [0, 1, 2, -1] and (t[0, 3:] == -1).all()
+    assert all((part == -1).all() for part in t[1:].split(128))

@@ -120,6 +120,13 @@ def test_update_and_compact_refusals(L):
     assert L.fp8bs_cache_compact_workspace_size(0) == -1
 
 
+def test_sizes_beyond_one_launch(L):
+    """A workgroup of 256 threads a token or row: 2^24 of them is one too many."""
+    assert call(L.fp8bs_mla_cache_write, WRITE, T=1 << 24) == SHAPE
+    assert call(L.fp8bs_cache_update, UPDATE, B=(1 << 24) - 3) == SHAPE
+    assert call(L.fp8bs_cache_compact, COMPACT, B=1 << 24) == SHAPE
+
+
 def test_binding_refusals():
     """Shapes and types are refused before anything is asked of a device."""
     bf, i32 = torch.bfloat16, torch.int32
