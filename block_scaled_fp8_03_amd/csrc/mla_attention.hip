@@ -635,8 +635,15 @@ mla_attention_kernel(AttnParams p) {
 
   const int n_steps = step1 - step0;
   const int t_seg = step0 * STEP + tw * kTok;        // this wave's first token
-  if (PIPE && n_steps > 0) {                         // the first tokens are on their way before Q
-    for (int k = 0; k < (FP8 ? 2 : NT - 1); ++k) fetch(t_seg + k * STEP, tile_at + k * kTileB, raw_at + (FP8 ? k * kRawB : 0));
+  // the first tokens are on their way before Q
+  if constexpr (PIPE) {
+    if (n_steps > 0)
+      for (int k = 0; k < (FP8 ? 2 : NT - 1); ++k) fetch(t_seg + k * STEP, tile_at + k * kTileB, raw_at + (FP8 ? k * kRawB : 0));
+  } else if constexpr (RW > 1) {
+    for (int k = 0; k < (FP8 ? 2 : 1) && k < n_steps; ++k) fetch(t_seg + k * STEP, tile_at, raw_at + k * NSUB * kRawB);
+  } else if (t_seg < end_max && n_steps > 0) {
+    if constexpr (FP8) fetch_regs(t_seg);
+    else fetch(t_seg, tile_at, 0u);
   }
 
   // this lane's query row: its operands, and the tokens it sees
@@ -870,12 +877,6 @@ mla_attention_kernel(AttnParams p) {
       s = t;
     }
   } else {
-    if constexpr (RW > 1) {
-      for (int k = 0; k < (FP8 ? 2 : 1) && k < n_steps; ++k)
-        fetch(t_seg + k * STEP, tile_at, raw_at + k * NSUB * kRawB);
-    } else if constexpr (FP8) {
-      if (t_seg < end_max && n_steps > 0) fetch_regs(t_seg);
-    }
     for (int k = 0; k < n_steps; ++k) {
       const int tb = t_seg + k * STEP;               // first token of this wave
       uint32_t off = 0;
@@ -905,7 +906,6 @@ mla_attention_kernel(AttnParams p) {
           }
           if (k + 1 < n_steps && tb + STEP < end_max) fetch_regs(tb + STEP);
         } else {
-          fetch(tb, tile_at, 0u);
           wait_vmcnt<0>();
         }
       }
@@ -930,6 +930,8 @@ mla_attention_kernel(AttnParams p) {
         product(f);
         if constexpr (f + kAhead < NV) value(std::integral_constant<int, f + kAhead>{});
       });
+      if constexpr (RW == 1 && !FP8)                 // its reads are over: the next tokens into the same tile
+        if (k + 1 < n_steps && tb + STEP < end_max) fetch(tb + STEP, tile_at, 0u);
     }
   }
   acc_settle();
@@ -987,7 +989,7 @@ mla_attention_kernel(AttnParams p) {
         __syncthreads();
         unroll<PG>([&](auto i) { *reinterpret_cast<v4f*>(ow + (i * 64 + ln) * 4) = acc_read<ps * PG + i>() * part; });
         __syncthreads();
-#pragma unroll 2
+#pragma unroll 4
           for (int i = tw * OWN; i < (tw + 1) * OWN; ++i) {
             v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -1055,7 +1057,11 @@ __global__ void __launch_bounds__(512) join_kernel(AttnParams p, int RW) {
       if (unit >= RW * (NG / kRun)) continue;
       const int rw = unit / (NG / kRun), i0 = unit % (NG / kRun) * kRun, r = rw * ROWS + n;
       float top = kNegInf, sum = 0.0f;
-      for (int k = 0; k < meta.parts; ++k) top = fmaxf(top, p.part_lse[slot(k) * M + r]);
+      float lse[kFew];                               // all under way at once; the last again behind it
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) lse[k] = p.part_lse[slot(min(k, meta.parts - 1)) * M + r];
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) top = fmaxf(top, lse[k]);
       const float base = top == kNegInf ? 0.0f : top;
       v4f acc[kRun];
 #pragma unroll
@@ -1076,7 +1082,10 @@ __global__ void __launch_bounds__(512) join_kernel(AttnParams p, int RW) {
     } else {
       const int rw = u / (NG / kRunMany), i0 = u % (NG / kRunMany) * kRunMany, r = rw * ROWS + n;
       float top = kNegInf, sum = 0.0f;
-      for (int k = wave; k < meta.parts; k += 8) top = fmaxf(top, p.part_lse[slot(k) * M + r]);
+      for (int k = wave; k < meta.parts; k += 32) {
+#pragma unroll
+        for (int d = 0; d < 32; d += 8) top = fmaxf(top, p.part_lse[slot(min(k + d, meta.parts - 1)) * M + r]);
+      }
       __syncthreads();                               // the last item's sums are used
       meet[wave][kRunMany][lane][0] = top;
       __syncthreads();
@@ -1086,13 +1095,16 @@ __global__ void __launch_bounds__(512) join_kernel(AttnParams p, int RW) {
       v4f acc[kRunMany];
 #pragma unroll
       for (int i = 0; i < kRunMany; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-      for (int k = wave; k < meta.parts; k += 8) {
-        const float x = __builtin_amdgcn_exp2f(p.part_lse[slot(k) * M + r] - base);
-        const float* src = p.part_out + ((slot(k) * RW + rw) * NG + i0) * 256 + 4 * lane;
-        sum += x;
+      for (int k0 = wave; k0 < meta.parts; k0 += 32) {
 #pragma unroll
-        for (int i = 0; i < kRunMany; ++i) acc[i] += *reinterpret_cast<const v4f*>(src + i * 256) * x;
+        for (int d = 0; d < 32; d += 8) {            // behind the last: that one again, with weight 0
+          const int k = min(k0 + d, meta.parts - 1);
+          const float y = p.part_lse[slot(k) * M + r] - base, x = k0 + d < meta.parts ? __builtin_amdgcn_exp2f(y) : 0.0f;
+          const float* src = p.part_out + ((slot(k) * RW + rw) * NG + i0) * 256 + 4 * lane;
+          sum += x;
+#pragma unroll
+          for (int i = 0; i < kRunMany; ++i) acc[i] += *reinterpret_cast<const v4f*>(src + i * 256) * x;
+        }
       }
 #pragma unroll
       for (int i = 0; i < kRunMany; ++i) *reinterpret_cast<v4f*>(meet[wave][i][lane]) = acc[i];
@@ -1118,7 +1130,7 @@ __global__ void __launch_bounds__(512) join_kernel(AttnParams p, int RW) {
 // better rate; fewer have less to set up, to split and to join.  The estimate is
 // start + unit * (32 cached tokens' steps a share), in us, as measured with 16 to
 // 128 heads, 1 to 128 sequences of 300 to 100000 tokens and 1 to 128 new ones (a
-// graph of calls, bf16 / fp8; 128-row tiles: 1.75 / 2.15 us a unit when the matrix
+// graph of calls, bf16 / fp8; 128-row tiles: 1.75 / 1.85 us a unit when the matrix
 // cores bound it).  It takes the table's width for the sequences' length.
 // Measured both ways (us, bf16): 32 x 4096, 128 heads: 64 rows 76, 128 rows 81; 128
 // new tokens on 8192, 128 heads: 313 / 265; 32 x 4096, 16 heads: 16 rows 52, 64
@@ -1129,7 +1141,7 @@ struct TileCost {
   float start[2], unit[2];   // bf16, fp8
 };
 constexpr TileCost kTiles[] = {
-    {16, {21, 22}, {0.65f, 0.8f}}, {32, {25, 26}, {1.0f, 1.3f}}, {64, {31, 33}, {1.2f, 1.6f}}, {128, {40, 42}, {1.9f, 2.2f}}};
+    {16, {21, 22}, {0.65f, 0.8f}}, {32, {25, 26}, {1.0f, 1.3f}}, {64, {31, 31}, {1.2f, 1.4f}}, {128, {40, 42}, {1.9f, 2.2f}}};
 
 // the largest tile that an average sequence's rows fill by half
 int most_rows(int64_t T, int64_t H, int64_t B) {
@@ -1211,8 +1223,11 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
       if (a.fp8) FP8BS_ATTN(16, 1, 4, true);
       else FP8BS_ATTN(16, 1, 4, false);
   }
-  if (m == 128) hipLaunchKernelGGL(join_kernel<32>, dim3(kJoin), dim3(512), 0, stream, p, 4);
-  else hipLaunchKernelGGL(join_kernel<16>, dim3(kJoin), dim3(512), 0, stream, p, m / 16);
+  // no more workgroups than the split tiles can have items
+  const int64_t items = std::min((int64_t)kGrid, a.T * a.H / m + a.B) * (2 * m / kRunMany);
+  const dim3 join((unsigned)std::min(items, (int64_t)kJoin));
+  if (m == 128) hipLaunchKernelGGL(join_kernel<32>, join, dim3(512), 0, stream, p, 4);
+  else hipLaunchKernelGGL(join_kernel<16>, join, dim3(512), 0, stream, p, m / 16);
 #undef FP8BS_ATTN
   return hipGetLastError();
 }
