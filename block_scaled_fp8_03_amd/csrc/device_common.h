@@ -70,6 +70,26 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return v;
 }
 
+// v of another lane by a DPP control, 0 where there is none or the row is not in ROWS
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_or_0(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, true); }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t dpp_or_0(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)dpp_or_0<CTRL, ROWS>((int)(v >> 32)) << 32 | (uint32_t)dpp_or_0<CTRL, ROWS>((int)v));
+}
+// Inclusive prefix sum over a full wave (all 64 lanes active), in the VALU: six
+// steps of a shuffle through LDS would wait for LDS six (for 64 bits twelve) times.
+template <typename I>
+__device__ __forceinline__ I wave_scan(I v) {
+  v += dpp_or_0<0x111, 0xF>(v);   // row_shr 1, 2, 4, 8: within rows of 16
+  v += dpp_or_0<0x112, 0xF>(v);
+  v += dpp_or_0<0x114, 0xF>(v);
+  v += dpp_or_0<0x118, 0xF>(v);
+  v += dpp_or_0<0x142, 0xA>(v);   // row_bcast 15: the sum of row 0 to row 1, of row 2 to row 3
+  v += dpp_or_0<0x143, 0xC>(v);   // row_bcast 31: of rows 0 and 1 to rows 2 and 3
+  return v;
+}
+
 // Block scale: s = RN32(max(amax, 1e-4) / 448) with an IEEE division; for
 // the ue8m0 format the smallest power of two >= s (s is always a normal
 // number here, so bumping the exponent field is exact).

@@ -267,12 +267,7 @@ __device__ __forceinline__ void barrier_lds() {
 template <int WAVES = 4>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t x = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
+  const int64_t x = wave_scan(v);
   __syncthreads();
   if (lane == 63) sums[wave] = x;
   __syncthreads();

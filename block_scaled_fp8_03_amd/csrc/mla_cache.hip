@@ -234,12 +234,7 @@ __global__ void __launch_bounds__(256) page_mark_kernel(PageParams p) {
 template <typename I>
 __device__ __forceinline__ I block_scan(I v, I* sums, I& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  I x = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const I y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
+  const I x = wave_scan(v);
   __syncthreads();
   if (lane == 63) sums[wave] = x;
   __syncthreads();
