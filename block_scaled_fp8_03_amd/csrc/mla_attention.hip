@@ -1126,11 +1126,13 @@ __global__ void __launch_bounds__(512) join_kernel(AttnParams p, int RW) {
 // start + unit * (32 cached tokens' steps a share), in us, as measured with 16 to
 // 128 heads, 1 to 128 sequences of 300 to 100000 tokens and 1 to 128 new ones (a
 // graph of calls, bf16 / fp8; 128-row tiles: 1.75 / 1.85 us a unit when the matrix
-// cores bound it).  It takes the table's width for the sequences' length.
+// cores bound it).  It takes the table's width for the sequences' length, and
+// when the new tokens cannot be shared out evenly half a tile a sequence as lost.
 // Measured both ways (us, bf16): 32 x 4096, 128 heads: 64 rows 76, 128 rows 81; 128
 // new tokens on 8192, 128 heads: 313 / 265; 32 x 4096, 16 heads: 16 rows 52, 64
 // rows 55, 128 rows 72; 16 new tokens each on 4 x 2000, 16 heads: 16 rows 37, 64
-// rows 45; fp8, 128 x 4096, 32 heads: 32 rows 118, 16 rows 131.
+// rows 45; 1 to 8 new each on 64 x up to 4000, 16 heads: 64 rows 85, 128 rows 102; fp8,
+// 128 x 4096, 32 heads: 32 rows 118, 16 rows 131.
 struct TileCost {
   int m;
   float start[2], unit[2];   // bf16, fp8
@@ -1149,7 +1151,7 @@ int tile_rows(int64_t T, int64_t H, int64_t B, int64_t len, bool fp8) {
   double least = 1e30;
   for (const TileCost& c : kTiles) {
     if (c.m > most) break;
-    const double tiles = (double)B * ((T * H + B * c.m - 1) / (B * c.m));
+    const double tiles = T % B == 0 ? (double)B * ((T * H + B * c.m - 1) / (B * c.m)) : (double)T * H / c.m + 0.5 * B;
     const double us = c.start[fp8] + c.unit[fp8] * std::ceil(tiles * ((len + kTok - 1) / kTok) / kGrid);
     if (us < least) least = us, best = c.m;
   }
