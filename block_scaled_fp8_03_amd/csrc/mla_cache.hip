@@ -152,10 +152,8 @@ __global__ void __launch_bounds__(256) mla_cache_write_kernel(WriteParams p) {
 //   apply  the new table, and the copies
 // Small ones are one launch: every workgroup marks and plans for itself, in LDS,
 // and applies its share, so nothing passes between workgroups and nothing waits.
-// What does not fit (below, at the launchers) goes through four launches and the
-// workspace.  Small calls are bound by launches: us a call from a graph, four
-// launches / one: 16 rows of 2000 tokens 12.6 / FILL, 64 rows of 8000 to 256 FILL, compact
-// 300 pages FILL.
+// What does not fit, or makes that reading the longer part (below, at the
+// launchers), goes through four launches and the workspace.
 // ---------------------------------------------------------------------------
 struct CacheArrays {
   uint8_t* p[3];
@@ -383,9 +381,9 @@ __device__ __forceinline__ int count_before(const uint32_t* used, int* before, i
   return all;
 }
 
-constexpr int kSmallEntries = 1 << 18;               // table entries that a workgroup reads for itself
-constexpr int kSmallPages = 1 << 14, kSmallRows = 2048;   // update
-constexpr int kSmallBits = 1 << 17;                  // compact: pages
+// what one launch takes: update's pages, rows and table entries, compact's pages and entries
+constexpr int kSmallPages = 1 << 14, kSmallRows = 512, kSmallEntries = 1 << 16;
+constexpr int kCompactPages = 1 << 17, kCompactEntries = 1 << 14;
 
 __global__ void __launch_bounds__(1024) update_small_kernel(PageParams p, int parts) {
   __shared__ int key[kSmallPages];
@@ -449,8 +447,8 @@ __global__ void __launch_bounds__(1024) update_small_kernel(PageParams p, int pa
 }
 
 __global__ void __launch_bounds__(1024) compact_small_kernel(PageParams p) {
-  __shared__ uint32_t used[kSmallBits / 32];
-  __shared__ int before[kSmallBits / 32];
+  __shared__ uint32_t used[kCompactPages / 32];
+  __shared__ int before[kCompactPages / 32];
   __shared__ int sums[16];
   const int tid = threadIdx.x;
   for (int i = tid; i < p.words; i += 1024) used[i] = 0;
@@ -624,8 +622,12 @@ hipError_t launch_mla_cache_write(const MlaCacheWrite& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// One launch when a workgroup's LDS holds the pages' keys and the rows (128 KB, the whole
-// card still has one each) and reading the tables once per workgroup stays cheap.
+// One launch when a workgroup's LDS holds the pages' keys and the rows (86 KB) and its own
+// reading of the tables takes no longer than three launches more.  us a call from a graph, one
+// launch / four: 16 rows of 2000 tokens 8.1 / 12.8, 64 of 4000 to 256 rows (fp8) 13.8 / 16.9, 64 of
+// 8000 to 256 (40,000 entries) 17.7 / 17.0, of 12000 21.7 / 17.4, 4 rows to 1024 33.5 / 29.0.  Calls
+// that are not in a graph pay 2 us or so of the host's time for each launch, so the line is drawn
+// behind the third of these.  The copies of the 256 beams move 9.6 MB.
 hipError_t launch_cache_update(const PageTask& a, hipStream_t stream) {
   const PageParams p = page_params(a);
   if (a.P <= kSmallPages && a.N <= kSmallRows && (a.B + a.N) * a.W <= kSmallEntries) {
@@ -640,9 +642,11 @@ hipError_t launch_cache_update(const PageTask& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The same for compact (one / four): 300 pages 6.3 / 12.7, 8192 pages with 60 rows (298 MB moved)
+// 70.2 / 74.4, 12,800 entries 86.5 / 86.6, 50,800 entries 299 / 279.
 hipError_t launch_cache_compact(const PageTask& a, hipStream_t stream) {
   const PageParams p = page_params(a);
-  if (a.P <= kSmallBits && a.B * a.W <= kSmallEntries) {
+  if (a.P <= kCompactPages && a.B * a.W <= kCompactEntries) {
     const int grid = std::min(512, std::max(1, std::max(p.P / 2, p.B)));
     hipLaunchKernelGGL(compact_small_kernel, dim3(grid), dim3(1024), 0, stream, p);
     return hipGetLastError();
