@@ -102,9 +102,9 @@ def lib() -> ctypes.CDLL:
     L.fp8bs_mla_attention_workspace_size.argtypes = [I64, I64, I64]
     L.fp8bs_mla_attention.argtypes = [P, I64, I64, P, I64, I64, P, P, P, I, P, P, P, F, I, P, I, P,
                                       I64, I64, I64, I64, I64, I64, I64, I64, P, I64, P]
-    L.fp8bs_cache_update_workspace_size.argtypes = [I64, I64]
+    L.fp8bs_cache_update_workspace_size.argtypes = [I64, I64, I64, I64]
     L.fp8bs_cache_update.argtypes = [P, P, P, I, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, I64, P, I64, P]
-    L.fp8bs_cache_compact_workspace_size.argtypes = [I64]
+    L.fp8bs_cache_compact_workspace_size.argtypes = [I64, I64, I64]
     L.fp8bs_cache_compact.argtypes = [P, P, P, I, P, P, P, P, I64, I64, I64, I64, I64, I64, P, I64, P]
     for fn in ("fp8bs_mla_attention_workspace_size", "fp8bs_cache_update_workspace_size",
                "fp8bs_cache_compact_workspace_size"):
@@ -525,9 +525,9 @@ def _cache_args(cache: MlaCache):
             _ptr(rope, "cache.rope", _BF16, (P, ps, MLA_ROPE), dev), CACHE_BF16 if bf16 else CACHE_FP8, P, ps)
 
 
-def _scratch(workspace: torch.Tensor, dev):
+def _scratch(workspace: Optional[torch.Tensor], dev):
     """(pointer, bytes) of a workspace."""
-    n = workspace.numel()
+    n = 0 if workspace is None else workspace.numel()
     if not n:
         return None, 0
     return (_ptr(workspace, "workspace", (torch.uint8, torch.int32, torch.float32), workspace.shape, dev),
@@ -615,7 +615,7 @@ def mla_attention(q_lat, q_rope, cache: MlaCache, table, cu_q, lens, scale: floa
 
 def fp8bs_cache_update(cache: MlaCache, table: torch.Tensor, lens: torch.Tensor, parent: torch.Tensor,
                        new_lens: torch.Tensor, table_out: torch.Tensor, lens_out: torch.Tensor,
-                       workspace: torch.Tensor) -> None:
+                       workspace: Optional[torch.Tensor]) -> None:
     """The next step's rows: row i continues old row parent[i] (else it is
     empty) and is to hold new_lens[i] tokens; table_out [N, W], lens_out [N].
     Forks, frees, truncates, grows and copies on write (see fp8bs.h)."""
@@ -632,18 +632,18 @@ def fp8bs_cache_update(cache: MlaCache, table: torch.Tensor, lens: torch.Tensor,
 
 def cache_update(cache: MlaCache, table, lens, parent, new_lens):
     """fp8bs_cache_update: (table_out [N, W], lens_out [N])."""
-    N, W = parent.shape[0], table.shape[1]
-    need = lib().fp8bs_cache_update_workspace_size(cache.latent.shape[0], N)
+    (B, W), N = table.shape, parent.shape[0]
+    need = lib().fp8bs_cache_update_workspace_size(B, N, W, cache.latent.shape[0])
     if need < 0:
         raise ValueError("sizes out of range")
     table_out, lens_out = table.new_empty((N, W)), table.new_empty(N)
-    ws = table.new_empty((need + 3) // 4)
+    ws = table.new_empty((need + 3) // 4) if need else None
     fp8bs_cache_update(cache, table, lens, parent, new_lens, table_out, lens_out, ws)
     return table_out, lens_out
 
 
 def fp8bs_cache_compact(cache: MlaCache, table: torch.Tensor, lens: torch.Tensor, table_out: torch.Tensor,
-                        count: torch.Tensor, workspace: torch.Tensor) -> None:
+                        count: torch.Tensor, workspace: Optional[torch.Tensor]) -> None:
     """The pages that the rows use moved to the lowest indices; table_out
     [B, W] holds the new ones, count [1] (or a 0-d tensor) how many."""
     if table.dim() != 2:
@@ -660,10 +660,11 @@ def fp8bs_cache_compact(cache: MlaCache, table: torch.Tensor, lens: torch.Tensor
 
 def cache_compact(cache: MlaCache, table, lens):
     """fp8bs_cache_compact: (table_out [B, W], count, a 0-d tensor)."""
-    need = lib().fp8bs_cache_compact_workspace_size(cache.latent.shape[0])
+    B, W = table.shape
+    need = lib().fp8bs_cache_compact_workspace_size(B, W, cache.latent.shape[0])
     if need < 0:
         raise ValueError("sizes out of range")
     table_out, count = table.new_empty(table.shape), table.new_empty(())
-    ws = table.new_empty((need + 3) // 4)
+    ws = table.new_empty((need + 3) // 4) if need else None
     fp8bs_cache_compact(cache, table, lens, table_out, count, ws)
     return table_out, count

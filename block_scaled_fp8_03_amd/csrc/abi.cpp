@@ -455,9 +455,10 @@ int fp8bs_mla_attention(const void* q_lat, int64_t ldq_t, int64_t ldq_h, const v
   return status_of(fp8bs::launch_mla_attention(a, (hipStream_t)stream));
 }
 
-int64_t fp8bs_cache_update_workspace_size(int64_t P, int64_t N) {
-  if (P < 1 || P > kLimitInt || N < 0 || N >= (1 << 18)) return -1;
-  return N == 0 ? 0 : fp8bs::cache_update_workspace_bytes(P, N);
+int64_t fp8bs_cache_update_workspace_size(int64_t B, int64_t N, int64_t W, int64_t P) {
+  if (P < 1 || P > kLimitInt || N < 0 || N >= (1 << 18) || B < 0 || B > kLimitRows - N || W < 1 || W > kLimitInt)
+    return -1;
+  return N == 0 ? 0 : fp8bs::cache_update_workspace_bytes(B, N, W, P);
 }
 
 int fp8bs_cache_update(void* latent, float* lat_scale, void* rope, int cache_fmt,
@@ -465,13 +466,13 @@ int fp8bs_cache_update(void* latent, float* lat_scale, void* rope, int cache_fmt
                        const int32_t* new_lens, int32_t* table_out, int32_t* lens_out, int64_t B,
                        int64_t N, int64_t W, int64_t P, int64_t ps, int64_t R, int64_t dr,
                        void* workspace, int64_t workspace_bytes, void* stream) {
-  const int64_t need = fp8bs_cache_update_workspace_size(P, N);
+  const int64_t need = fp8bs_cache_update_workspace_size(B, N, W, P);
   if (need < 0) return FP8BS_ERR_SHAPE;
   if (N == 0) return FP8BS_OK;
-  if (workspace_bytes < need || mul(N, W) < 0 || mul(mul(N, W), 4) < 0 || B > kLimitRows - N) return FP8BS_ERR_SHAPE;
+  if (workspace_bytes < need || mul(N, W) < 0 || mul(mul(N, W), 4) < 0) return FP8BS_ERR_SHAPE;
   const int st = cache_checks(latent, lat_scale, rope, cache_fmt, B, W, P, ps, R, dr);
   if (st != FP8BS_OK) return st;
-  if (!parent || !new_lens || !table_out || !lens_out || !workspace || (B > 0 && (!table || !lens)))
+  if (!parent || !new_lens || !table_out || !lens_out || (need > 0 && !workspace) || (B > 0 && (!table || !lens)))
     return FP8BS_ERR_NULL;
   if (!aligned(workspace, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(parent, 4) ||
       !aligned(new_lens, 4) || !aligned(table_out, 4) || !aligned(lens_out, 4))
@@ -494,20 +495,20 @@ int fp8bs_cache_update(void* latent, float* lat_scale, void* rope, int cache_fmt
   return status_of(fp8bs::launch_cache_update(a, (hipStream_t)stream));
 }
 
-int64_t fp8bs_cache_compact_workspace_size(int64_t P) {
-  if (P < 1 || P > kLimitInt) return -1;
-  return fp8bs::cache_compact_workspace_bytes(P);
+int64_t fp8bs_cache_compact_workspace_size(int64_t B, int64_t W, int64_t P) {
+  if (P < 1 || P > kLimitInt || B < 0 || B > kLimitRows || W < 1 || W > kLimitInt) return -1;
+  return fp8bs::cache_compact_workspace_bytes(B, W, P);
 }
 
 int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fmt,
                         const int32_t* table, const int32_t* lens, int32_t* table_out,
                         int32_t* count, int64_t B, int64_t W, int64_t P, int64_t ps, int64_t R,
                         int64_t dr, void* workspace, int64_t workspace_bytes, void* stream) {
-  const int64_t need = fp8bs_cache_compact_workspace_size(P);
-  if (need < 0 || workspace_bytes < need || B > kLimitRows) return FP8BS_ERR_SHAPE;
+  const int64_t need = fp8bs_cache_compact_workspace_size(B, W, P);
+  if (need < 0 || workspace_bytes < need) return FP8BS_ERR_SHAPE;
   const int st = cache_checks(latent, lat_scale, rope, cache_fmt, B, W, P, ps, R, dr);
   if (st != FP8BS_OK) return st;
-  if (!count || !workspace || (B > 0 && (!table || !lens || !table_out))) return FP8BS_ERR_NULL;
+  if (!count || (need > 0 && !workspace) || (B > 0 && (!table || !lens || !table_out))) return FP8BS_ERR_NULL;
   if (!aligned(workspace, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(table_out, 4) ||
       !aligned(count, 4))
     return FP8BS_ERR_ALIGN;

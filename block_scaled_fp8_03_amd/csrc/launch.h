@@ -95,8 +95,8 @@ struct PageTask {
   int64_t B, W, N, P, ps;
   bool fp8;
 };
-int64_t cache_update_workspace_bytes(int64_t P, int64_t N);
-int64_t cache_compact_workspace_bytes(int64_t P);
+int64_t cache_update_workspace_bytes(int64_t B, int64_t N, int64_t W, int64_t P);
+int64_t cache_compact_workspace_bytes(int64_t B, int64_t W, int64_t P);
 hipError_t launch_cache_update(const PageTask& a, hipStream_t stream);
 hipError_t launch_cache_compact(const PageTask& a, hipStream_t stream);
 

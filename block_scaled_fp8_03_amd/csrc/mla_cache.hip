@@ -541,6 +541,19 @@ __global__ void __launch_bounds__(256) page_apply_compact_kernel(PageParams p) {
   for (int k = blockIdx.x; k < moves; k += gridDim.x) copy_tokens<256>(p, p.list[p.P + k], p.list[k], p.ps, 0, 1);
 }
 
+// One launch when a workgroup's LDS holds the pages' keys and the rows (86 KB) and its own
+// reading of the tables takes no longer than three launches more.  us a call from a graph, one
+// launch / four: 16 rows of 2000 tokens 8.1 / 12.8, 64 of 4000 to 256 rows (fp8) 13.8 / 16.9, 64 of
+// 8000 to 256 (40,000 entries) 17.7 / 17.0, of 12000 21.7 / 17.4, 4 rows to 1024 33.5 / 29.0.  Calls
+// that are not in a graph pay 2 us or so of the host's time for each launch, so the line is drawn
+// behind the third of these.  The copies of the 256 beams move 9.6 MB.
+bool update_is_small(int64_t B, int64_t N, int64_t W, int64_t P) {
+  return P <= kSmallPages && N <= kSmallRows && (B + N) * W <= kSmallEntries;
+}
+// The same for compact (one / four): 300 pages 6.3 / 12.7, 8192 pages with 60 rows (298 MB moved)
+// 70.2 / 74.4, 12,800 entries 86.5 / 86.6, 50,800 entries 299 / 279.
+bool compact_is_small(int64_t B, int64_t W, int64_t P) { return P <= kCompactPages && B * W <= kCompactEntries; }
+
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
 PageParams page_params(const PageTask& a) {
@@ -585,10 +598,12 @@ PageParams page_params(const PageTask& a) {
 
 }  // namespace
 
-int64_t cache_update_workspace_bytes(int64_t P, int64_t N) {
+int64_t cache_update_workspace_bytes(int64_t B, int64_t N, int64_t W, int64_t P) {
+  if (update_is_small(B, N, W, P)) return 0;
   return up16(4 * ((P + 31) / 32)) + 2 * up16(4 * P) + up16(16 * N);
 }
-int64_t cache_compact_workspace_bytes(int64_t P) {
+int64_t cache_compact_workspace_bytes(int64_t B, int64_t W, int64_t P) {
+  if (compact_is_small(B, W, P)) return 0;
   return 2 * up16(4 * ((P + 31) / 32)) + up16(8 * P) + 16;
 }
 
@@ -622,15 +637,9 @@ hipError_t launch_mla_cache_write(const MlaCacheWrite& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// One launch when a workgroup's LDS holds the pages' keys and the rows (86 KB) and its own
-// reading of the tables takes no longer than three launches more.  us a call from a graph, one
-// launch / four: 16 rows of 2000 tokens 8.1 / 12.8, 64 of 4000 to 256 rows (fp8) 13.8 / 16.9, 64 of
-// 8000 to 256 (40,000 entries) 17.7 / 17.0, of 12000 21.7 / 17.4, 4 rows to 1024 33.5 / 29.0.  Calls
-// that are not in a graph pay 2 us or so of the host's time for each launch, so the line is drawn
-// behind the third of these.  The copies of the 256 beams move 9.6 MB.
 hipError_t launch_cache_update(const PageTask& a, hipStream_t stream) {
   const PageParams p = page_params(a);
-  if (a.P <= kSmallPages && a.N <= kSmallRows && (a.B + a.N) * a.W <= kSmallEntries) {
+  if (update_is_small(a.B, a.N, a.W, a.P)) {
     const int parts = std::max(1, 256 / p.N);        // workgroups a row's copy is cut over
     hipLaunchKernelGGL(update_small_kernel, dim3(std::min(256, p.N * parts)), dim3(1024), 0, stream, p, parts);
     return hipGetLastError();
@@ -642,11 +651,9 @@ hipError_t launch_cache_update(const PageTask& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The same for compact (one / four): 300 pages 6.3 / 12.7, 8192 pages with 60 rows (298 MB moved)
-// 70.2 / 74.4, 12,800 entries 86.5 / 86.6, 50,800 entries 299 / 279.
 hipError_t launch_cache_compact(const PageTask& a, hipStream_t stream) {
   const PageParams p = page_params(a);
-  if (a.P <= kCompactPages && a.B * a.W <= kCompactEntries) {
+  if (compact_is_small(a.B, a.W, a.P)) {
     const int grid = std::min(512, std::max(1, std::max(p.P / 2, p.B)));
     hipLaunchKernelGGL(compact_small_kernel, dim3(grid), dim3(1024), 0, stream, p);
     return hipGetLastError();

@@ -497,7 +497,8 @@ int fp8bs_mla_attention(const void* q_lat, int64_t ldq_t, int64_t ldq_h, const v
  *   lens_out     out  DEVICE int32 [N]
  *   latent, lat_scale, rope   in/out: only pages that no old row uses are
  *                     written, and only a copy's kept tokens
- *   workspace    DEVICE, >= fp8bs_cache_update_workspace_size(P, N) bytes,
+ *   workspace    DEVICE, >= fp8bs_cache_update_workspace_size(B, N, W, P) bytes
+ *                (0 for small tables: NULL then),
  *                16-byte aligned, scratch; not shared by concurrent calls
  *   B >= 0, 0 <= N < 2^18 (N = 0: no-op), B + N < 2^24.
  * The result depends on the inputs alone, and a repeated call gives it again.
@@ -507,15 +508,16 @@ int fp8bs_mla_attention(const void* q_lat, int64_t ldq_t, int64_t ldq_h, const v
  * ascending order; table_out is the table with the new indices (-1 behind
  * each row's last page and for entries outside [0, P)), count = n.
  *   table_out    out  DEVICE int32 [B, W];  count  out  DEVICE int32 [1]
- *   workspace    >= fp8bs_cache_compact_workspace_size(P) bytes;  B < 2^24
+ *   workspace    >= fp8bs_cache_compact_workspace_size(B, W, P) bytes, as above
+ *   0 <= B < 2^24
  */
-int64_t fp8bs_cache_update_workspace_size(int64_t P, int64_t N);
+int64_t fp8bs_cache_update_workspace_size(int64_t B, int64_t N, int64_t W, int64_t P);
 int fp8bs_cache_update(void* latent, float* lat_scale, void* rope, int cache_fmt,
                        const int32_t* table, const int32_t* lens, const int32_t* parent,
                        const int32_t* new_lens, int32_t* table_out, int32_t* lens_out, int64_t B,
                        int64_t N, int64_t W, int64_t P, int64_t ps, int64_t R, int64_t dr,
                        void* workspace, int64_t workspace_bytes, void* stream);
-int64_t fp8bs_cache_compact_workspace_size(int64_t P);
+int64_t fp8bs_cache_compact_workspace_size(int64_t B, int64_t W, int64_t P);
 int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fmt,
                         const int32_t* table, const int32_t* lens, int32_t* table_out,
                         int32_t* count, int64_t B, int64_t W, int64_t P, int64_t ps, int64_t R,

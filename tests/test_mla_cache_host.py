@@ -29,9 +29,9 @@ ATTN = dict(q=A[0], ldq_t=2048, ldq_h=512, qr=A[1], ldr_t=256, ldr_h=64, latent=
             table=A[4], cu=A[5], lens=A[6], sm=0.1, causal=1, out=A[7], dt=0, lse=A[8], T=4, H=4, B=2, W=3, P=10, ps=16,
             R=512, dr=64, ws=A[9], nws=1 << 40, stream=None)
 UPDATE = dict(latent=A[0], scale=None, rope=A[1], fmt=0, table=A[2], lens=A[3], parent=A[4], new=A[5], tout=A[6], lout=A[7],
-              B=2, N=3, W=3, P=10, ps=16, R=512, dr=64, ws=A[8], nws=1 << 40, stream=None)
-COMPACT = dict(latent=A[0], scale=None, rope=A[1], fmt=0, table=A[2], lens=A[3], tout=A[4], count=A[5], B=2, W=3, P=10,
-               ps=16, R=512, dr=64, ws=A[6], nws=1 << 40, stream=None)
+              B=2, N=3, W=3, P=20000, ps=1, R=512, dr=64, ws=A[8], nws=1 << 40, stream=None)
+COMPACT = dict(latent=A[0], scale=None, rope=A[1], fmt=0, table=A[2], lens=A[3], tout=A[4], count=A[5], B=2, W=3, P=140000,
+               ps=1, R=512, dr=64, ws=A[6], nws=1 << 40, stream=None)
 
 
 def call(f, base, **kw):
@@ -101,7 +101,7 @@ def test_attention_refusals(L):
 
 def test_update_and_compact_refusals(L):
     f, g = L.fp8bs_cache_update, L.fp8bs_cache_compact
-    for kw in (dict(N=-1), dict(N=1 << 18), dict(nws=L.fp8bs_cache_update_workspace_size(10, 3) - 1)):
+    for kw in (dict(N=-1), dict(N=1 << 18), dict(nws=L.fp8bs_cache_update_workspace_size(2, 3, 3, 20000) - 1)):
         assert call(f, UPDATE, **kw) == SHAPE, kw
     for k in ("parent", "new", "tout", "lout"):
         assert call(f, UPDATE, **{k: None}) == NULL, k
@@ -110,14 +110,19 @@ def test_update_and_compact_refusals(L):
                dict(table=A[0])):
         assert call(f, UPDATE, **kw) == ALIAS, kw
     assert call(f, UPDATE, N=0, parent=None, tout=None) == OK
-    assert call(g, COMPACT, nws=L.fp8bs_cache_compact_workspace_size(10) - 1) == SHAPE
+    assert call(g, COMPACT, nws=L.fp8bs_cache_compact_workspace_size(2, 3, 140000) - 1) == SHAPE
     for k in ("tout", "count"):
         assert call(g, COMPACT, **{k: None}) == NULL, k
         assert call(g, COMPACT, **{k: COMPACT[k] + 2}) == ALIGN, k
     for kw in (dict(tout=A[2]), dict(count=A[3]), dict(tout=A[0]), dict(ws=A[1] + 16), dict(count=A[4] + 4)):
         assert call(g, COMPACT, **kw) == ALIAS, kw
-    assert L.fp8bs_cache_update_workspace_size(0, 3) == L.fp8bs_cache_update_workspace_size(4, 1 << 18) == -1
-    assert L.fp8bs_cache_compact_workspace_size(0) == -1
+    for sizes in ((2, 3, 3, 0), (2, 1 << 18, 3, 10), (2, -1, 3, 10), (-1, 3, 3, 10), (2, 3, 0, 10), (1 << 24, 3, 3, 10)):
+        assert L.fp8bs_cache_update_workspace_size(*sizes) == -1, sizes
+    for sizes in ((2, 3, 0), (-1, 3, 10), (2, 0, 10), (1 << 24, 3, 10)):
+        assert L.fp8bs_cache_compact_workspace_size(*sizes) == -1, sizes
+    assert L.fp8bs_cache_update_workspace_size(2, 0, 3, 20000) == 0
+    # small tables need none
+    assert L.fp8bs_cache_update_workspace_size(2, 3, 3, 10) == L.fp8bs_cache_compact_workspace_size(2, 3, 10) == 0
 
 
 def test_sizes_beyond_one_launch(L):
