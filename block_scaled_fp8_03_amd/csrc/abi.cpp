@@ -341,10 +341,13 @@ int fp8bs_moe_combine(const void* out_bf16, const float* w, const int32_t* row_o
 // rows that a launch has a workgroup of 256 threads for (it has at most 2^32 - 1 threads)
 static const int64_t kLimitRows = (1 << 24) - 1;
 
+// columns of a page table
+static const int64_t kLimitPages = 1 << 30;
+
 // what the paged-cache entry points share: sizes, format, pointers and alignment of the cache
 static int cache_checks(const void* latent, const float* lat_scale, const void* rope, int cache_fmt,
                         int64_t B, int64_t W, int64_t P, int64_t ps, int64_t R, int64_t dr) {
-  if (R != 512 || dr != 64 || B < 0 || B > kLimitInt || W < 1 || W > kLimitInt || P < 1 || ps < 1 || ps > 4096 || P > kLimitInt / ps ||
+  if (R != 512 || dr != 64 || B < 0 || B > kLimitInt || W < 1 || W > kLimitPages || P < 1 || ps < 1 || ps > 4096 || P > kLimitInt / ps ||
       mul(B, W) < 0 || mul(mul(B, W), 4) < 0)
     return FP8BS_ERR_SHAPE;
   if (cache_fmt != FP8BS_CACHE_BF16 && cache_fmt != FP8BS_CACHE_FP8) return FP8BS_ERR_ENUM;

@@ -103,6 +103,7 @@ struct AttnParams {
   float* part_lse;
   float* part_out;
   int T, H, B, W, P, ps;
+  int longest;              // tokens of a sequence: W * ps, and so few that positions some tiles ahead fit 32 bits
   int causal, out_f32;
 };
 
@@ -243,7 +244,7 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   Seq s;
   s.q0 = clampi(p.cu_q[b], 0, p.T);
   s.nq = clampi(p.cu_q[b + 1], s.q0, p.T) - s.q0;
-  s.len = (int)min((int64_t)max(p.lens[b], 0), (int64_t)p.W * p.ps);
+  s.len = clampi(p.lens[b], 0, p.longest);
   return s;
 }
 
@@ -1212,6 +1213,7 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
   p.W = (int)a.W;
   p.P = (int)a.P;
   p.ps = (int)a.ps;
+  p.longest = (int)std::min(a.W * a.ps, ((int64_t)1 << 31) - 4096);
   p.causal = a.causal;
   p.out_f32 = a.out_f32;
   const int m = tile_rows(a.T, a.H, a.B, a.W * a.ps, a.fp8);

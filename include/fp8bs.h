@@ -396,9 +396,11 @@ int fp8bs_mla_absorb_value(const void* x_bf16, int64_t ld_t, int64_t ld_h, const
  *              A sequence may have none.  Its new tokens are its last: with
  *              n_b of them, the i-th has position lens[b] - n_b + i.
  *   R = 512 and dr = 64 (the pages' configurations all use these).
- *   1 <= ps <= 4096, P >= 1, W >= 1, P * ps < 2^31.
+ *   1 <= ps <= 4096, P >= 1, 1 <= W <= 2^30, P * ps < 2^31, a sequence of at most
+ *   2^31 - 4096 tokens.
  * Values of table, lens and cu_q lie on the device and are preconditions, not
- * checked on the host; the kernels clamp lens to [0, W * ps] and cu_q to [0, T],
+ * checked on the host; the kernels clamp lens to [0, W * ps] (the attention also to
+ * 2^31 - 4096) and cu_q to [0, T],
  * never write outside the cache, and read no page outside [0, P), so a wrong
  * value gives wrong results for its sequence, not faults (a cu_q that decreases:
  * for the batch).

@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import block_scaled_fp8_03_amd as fp8bs
-from mla_util import (BF16, D, FP8, R, attention64, check_attention, cu_of, make_cache, make_table, to_dev)
+from mla_util import (BF16, D, FP8, R, U8, attention64, check_attention, cu_of, make_cache, make_table, to_dev)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -249,6 +249,23 @@ def test_chunk_over_many_tiles(dtype, width):
     """More row tiles than one workgroup takes, whole and split, in sequences of several lengths."""
     nq, lens = [70, 3, 90, 1], [300, 800, 90, 1000]
     compare(batch(40, nq, lens, 48, dtype, 96, W=columns(width, lens, 48)), "chunk over many tiles")
+
+
+def test_longest_sequence():
+    """A length beyond the limit: 2^31 - 4096 tokens, all one page of one token's
+    copies, so that the output is its latent and the sum counts the tokens."""
+    n, W = 2 ** 31 - 4096, 2 ** 31 // 4096
+    q_lat, q_rope, cache, _, cu, _ = batch(4, [1], [1], 4096, BF16, 81, spare=0)
+    cache.latent[:], cache.rope[:] = cache.latent[0, 0].clone(), cache.rope[0, 0].clone()
+    args = (q_lat, q_rope, cache, torch.zeros((1, W), dtype=torch.int32), cu, torch.tensor([2 ** 31 - 1], dtype=torch.int32))
+    out, lse = run(args)
+    c, k = cache.latent[0, 0].double(), cache.rope[0, 0].double()
+    s = SCALE * (q_lat[0].double() @ c + q_rope[0].double() @ k)
+    # each probability is 1 but for its exponent's rounding (2^-19); a wave adds 2^31 / (256 * 4 * 32) = 2^16 times
+    # to its accumulators (2^-24 each); the output's bf16
+    assert ((out[0].double().cpu() - c).abs() <= (U8 + 2.0 ** -8 + 2.0 ** -19) * c.abs()).all()
+    size = SCALE * (q_lat[0].double().abs() @ c.abs() + q_rope[0].double().abs() @ k.abs())
+    assert ((lse[0].double().cpu() - s - math.log(n)).abs() <= 2.0 ** -19 * size + 2.0 ** -18).all()
 
 
 def test_no_new_tokens_and_no_sequences():

@@ -48,7 +48,7 @@ def call(f, base, **kw):
 def test_shared_refusals(L, name, base, floats):
     f = getattr(L, name)
     for kw in (dict(R=256), dict(dr=32), dict(B=-1), dict(W=0), dict(P=0), dict(ps=0), dict(ps=4097),
-               dict(P=1 << 31), dict(P=1 << 20, ps=4096), dict(W=-3)):
+               dict(P=1 << 31), dict(P=1 << 20, ps=4096), dict(W=-3), dict(W=(1 << 30) + 1)):
         assert call(f, base, **kw) == SHAPE, kw
     for kw in (dict(fmt=2), dict(fmt=-1)):
         assert call(f, base, **kw) == ENUM, kw
