@@ -299,7 +299,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t&
 
 // ---------------------------------------------------------------------------
 // The work split.  The grid is one workgroup per CU, whatever the batch.  The
-// row tiles of all sequences, in order, cost kStart + (steps of 32 TW cached
+// row tiles of all sequences, in order, cost start_cost + (steps of 32 TW cached
 // tokens) each; the sum of the costs is cut into equal shares, and workgroup w
 // works through share w: the end of one tile's tokens, whole tiles, the
 // beginning of another's.  So long and short sequences, few rows and many, all
@@ -309,15 +309,20 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t&
 // the sequences (row tiles) and over the row tiles (costs).
 // ---------------------------------------------------------------------------
 // It takes about 2 us of each workgroup: the batch's lengths read, two prefix sums, the search.
-constexpr int kStart = 2;    // a tile's queries and output, in steps
+// A tile's queries and output, in steps.  Measured with 2 and 4 (24 sequences of up to 2777 tokens, 61
+// new each, us): 16 heads 95.6 / 90.6, 128 heads 419 / 406; with 6 the same.  16 rows' steps are of 128
+// tokens: 91 single tokens on up to 4319, 16 heads 69.2 / 70.8.
+template <int M>
+constexpr int start_cost() { return M == 16 ? 2 : 4; }
 // A share is no smaller, so that short work is not cut to pieces: 128 cached tokens with 128 rows a
 // tile (a step is 32), one step of 128 with 16 rows.
 template <int M>
 constexpr int least() { return M == 128 ? 4 : M == 64 ? 2 : 1; }
 // A cut this near a tile's edge moves to it: a split costs the writing and
-// reading of M rows of float32 twice, about M / 16 steps' time.
+// reading of M rows of float32 twice, about M / 16 steps' time.  (Twice as near loses more
+// balance than it saves: the 16 heads above 89.5 / 102.)
 template <int M>
-__device__ __forceinline__ int slack(int64_t total, int shares) { return (int)min((int64_t)(M / 16), total / shares / 4); }
+__device__ __forceinline__ int slack(int64_t total, int shares) { return (int)min((int64_t)(M / 16), total / shares / 2); }
 
 struct Cut {          // a place between two steps
   int tile;           // row tile of the batch
@@ -350,7 +355,7 @@ struct Plan {
   // A short chunk's tiles all cost what its last does (at most an eighth more than
   // they take): equal costs, and cuts fall on the tiles' edges where their number allows.
   static __device__ int tile_cost(const AttnParams& p, const Seq& s, int in_seq) {
-    return kStart + (s.nq <= s.len / 8 ? (s.len + STEP - 1) / STEP : tile_steps(p, s, in_seq));
+    return start_cost<M>() + (s.nq <= s.len / 8 ? (s.len + STEP - 1) / STEP : tile_steps(p, s, in_seq));
   }
 
   static constexpr int kBytes = 256 + 4 * (kSeqs + 4) + (int)sizeof(Seq) * kSeqs;
@@ -407,15 +412,15 @@ struct Plan {
       for (int t = t0; t < t1; ++t) {
         while (t >= first[b + 1]) ++b;
         const int in_seq = t - first[b], c = tile_cost(p, seq[b], in_seq);
-        const int done = min(c - near, kStart + tile_steps(p, seq[b], in_seq));
+        const int done = min(c - near, start_cost<M>() + tile_steps(p, seq[b], in_seq));
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           if (want[k] >= base && want[k] < base + c) {
             const int at = (int)(want[k] - base);
             // (tile t + 1 may be the next sequence's first: the share that begins there looks)
-            if (at <= kStart + near) cut[k] = Cut{t, b, in_seq, 0, base + done};
+            if (at <= start_cost<M>() + near) cut[k] = Cut{t, b, in_seq, 0, base + done};
             else if (at >= done) cut[k] = Cut{t + 1, b, in_seq + 1, 0, base + done};
-            else cut[k] = Cut{t, b, in_seq, at - kStart, base + done};
+            else cut[k] = Cut{t, b, in_seq, at - start_cost<M>(), base + done};
           }
         base += c;
       }
