@@ -1244,6 +1244,9 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
       if (a.fp8) FP8BS_ATTN(16, 1, 4, true);
       else FP8BS_ATTN(16, 1, 4, false);
   }
+  // A table no wider than a step of the plan: tiles are one step, none is split.  (One token, 16 heads, 100
+  // cached, us a call from a graph: 13.0, with the join's launch 14.9.)
+  if (a.W * a.ps <= kTok * (m == 16 ? 4 : m == 32 ? 2 : 1)) return hipGetLastError();
   // no more workgroups than the split tiles can have items
   const int64_t items = std::min((int64_t)kGrid, a.T * a.H / m + a.B) * (2 * m / kRunMany);
   const dim3 join((unsigned)std::min(items, (int64_t)kJoin));
