@@ -235,6 +235,16 @@ def test_many_sequences(dtype, width):
     compare(batch(8, nq, lens, 16, dtype, 82, W=columns(width, lens, 16)), "300 sequences")
 
 
+@pytest.mark.parametrize("H,B", [(2, 8192), (48, 1500), (128, 1100)])
+def test_as_many_sequences_as_there_may_be(H, B, width):
+    """Up to the limit of 8192 sequences, some empty, some without new tokens."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 12, (B,), generator=g).tolist()
+    nq = torch.randint(0, 3, (B,), generator=g).tolist()
+    args = batch(H, nq, lens, 4, BF16, 91 + H, W=max(3, columns(width, lens, 64 * 4) or 0) if width == "wide" else None)
+    compare(args, f"{B} sequences")
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
 @pytest.mark.parametrize("H,B,n", [(16, 1, 20000), (128, 2, 5000), (16, 3, 5000), (64, 1, 7000), (32, 2, 6000)])
 def test_long_sequences(H, B, n, dtype, width):
