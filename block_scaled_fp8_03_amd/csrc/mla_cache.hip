@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(256) mla_cache_write_kernel(WriteParams p) {
   const int lane = threadIdx.x & 63;
   const int b = find_seq(p.cu_q, p.B, t);
   if (b >= p.B || t < p.cu_q[b]) return;             // a row behind the last sequence
+  if (t >= p.cu_q[b + 1]) return;                    // boundaries that decrease: below, pos < len holds for the others
   const int64_t len = min((int64_t)max(p.lens[b], 0), (int64_t)p.W * p.ps);
   const int64_t pos = len - min(p.cu_q[b + 1], p.T) + t;
   if (pos < 0 || pos >= p.n_pos) return;

@@ -142,6 +142,33 @@ def test_write_many_sequences(B):
     assert ((q_out.double().cpu()[tok] - qr).abs() <= U8 * qr.abs() + 2.0 ** -22 * size).all()
 
 
+@pytest.mark.parametrize("cu", [[0, 10, 2, 3], [0, 10, 2, 20], [0, 20, 0, 20], [-3, 4, -7, 6], [0, -(2 ** 31), 5, 2 ** 31 - 1],
+                                [20, 10, 5, 0], [7, 7, 3, 3]])
+@pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
+def test_write_boundaries_that_decrease(cu, dtype):
+    """cu_q out of order is outside the contract, but nothing is written but tokens
+    below a sequence's length, in its own pages: not to the page that the entries
+    behind the table name, nor to another row's."""
+    T, ps, W, B = 20, 4, 3, 3
+    for lens in ([12, 12, 12], [5, 12, 7], [0, 3, 2 ** 31 - 1]):
+        cache = make_cache(12, ps, dtype, torch.Generator().manual_seed(17))
+        entries = torch.full((64, W), 11, dtype=torch.int32)         # page 11 is no sequence's
+        entries[:B] = torch.tensor([[4, 0, 7], [2, 9, 5], [8, 1, 3]])
+        g = torch.Generator().manual_seed(18)
+        q, kv = torch.randn((T, 4, D), generator=g).to(BF16), torch.randn((T, R + D), generator=g).to(BF16)
+        dev = to_dev(cache)
+        fp8bs.mla_cache_write(q.to(DEV), kv.to(DEV), torch.ones(R, device=DEV), 1e-6, rope_table(64).to(DEV), dev,
+                              entries.to(DEV)[:B], torch.tensor(cu, dtype=torch.int32, device=DEV),
+                              torch.tensor(lens, dtype=torch.int32, device=DEV))
+        torch.cuda.synchronize()
+        own = torch.zeros(cache.latent.shape[:2], dtype=torch.bool)
+        for b in range(B):
+            for p in range(min(lens[b], W * ps)):
+                own[entries[b, p // ps], p % ps] = True
+        for a, b in zip(dev, cache):
+            assert a is None or torch.equal(bits(a.cpu()[~own]), bits(b[~own])), (cu, lens)
+
+
 def test_write_quantises_as_act_quant():
     """With the norm switched off (unit-size rows, weight 1) the 8-bit cache
     holds exactly act_quant's ue8m0 codes and scales of the bf16 latents."""
