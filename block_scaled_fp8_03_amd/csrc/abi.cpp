@@ -341,8 +341,8 @@ int fp8bs_moe_combine(const void* out_bf16, const float* w, const int32_t* row_o
 // rows that a launch has a workgroup of 256 threads for (it has at most 2^32 - 1 threads)
 static const int64_t kLimitRows = (1 << 24) - 1;
 
-// columns of a page table
-static const int64_t kLimitPages = 1 << 30;
+// columns of a page table, and sequences (the search for a token's looks up to 64 boundaries past them)
+static const int64_t kLimitPages = 1 << 30, kLimitSeqs = 1 << 30;
 
 // what the paged-cache entry points share: sizes, format, pointers and alignment of the cache
 static int cache_checks(const void* latent, const float* lat_scale, const void* rope, int cache_fmt,
@@ -380,7 +380,7 @@ int fp8bs_mla_cache_write(const void* q_rope, int64_t ldq_t, int64_t ldq_h, cons
                           float* lat_scale, void* rope, int cache_fmt, const int32_t* table,
                           const int32_t* cu_q, const int32_t* lens, int64_t T, int64_t H, int64_t B,
                           int64_t W, int64_t P, int64_t ps, int64_t R, int64_t dr, void* stream) {
-  if (T < 0 || H < 0 || T > kLimitRows || H > kLimitInt || n_pos < 0 || ldq_t < 0 || ldq_h < 0 ||
+  if (T < 0 || H < 0 || T > kLimitRows || H > kLimitInt || B > kLimitSeqs || n_pos < 0 || ldq_t < 0 || ldq_h < 0 ||
       ld_kv < 0 || !(eps >= 0.0f && eps <= 3.0e38f))
     return FP8BS_ERR_SHAPE;
   const int64_t nq = mul(mul(T, H), 64);

@@ -426,7 +426,8 @@ int fp8bs_mla_absorb_value(const void* x_bf16, int64_t ld_t, int64_t ld_h, const
  *   eps           >= 0, finite
  *   rope_cs  in   float32 [n_pos, 32, 2]: (cos, sin)
  *   q_out    out  bf16 [T, H, 64]
- *   0 <= T < 2^24 (0 = no-op), H >= 0 (0 = no queries), B >= 0, n_pos >= 0.
+ *   0 <= T < 2^24 (0 = no-op), H >= 0 (0 = no queries), 0 <= B <= 2^30 (0 =
+ *   no-op), n_pos >= 0.
  * A token at a position outside [0, n_pos) is skipped: neither its cache row
  * nor its q_out is written.  A token whose page lies outside [0, P) has its
  * q_out written only.  Rows t >= cu_q[B] are left as they were.  Two tokens

@@ -132,6 +132,12 @@ def test_sizes_beyond_one_launch(L):
     assert call(L.fp8bs_cache_compact, COMPACT, B=1 << 24) == SHAPE
 
 
+def test_write_number_of_sequences(L):
+    """The kernel's search looks at places up to 64 behind the last boundary, in 32 bits."""
+    for B in ((1 << 30) + 1, (1 << 31) - 1):
+        assert call(L.fp8bs_mla_cache_write, WRITE, B=B, W=1, H=0, table=1 << 44, cu=1 << 45, lens=1 << 46) == SHAPE
+
+
 def test_binding_refusals():
     """Shapes and types are refused before anything is asked of a device."""
     bf, i32 = torch.bfloat16, torch.int32
