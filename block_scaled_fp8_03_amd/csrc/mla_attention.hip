@@ -720,33 +720,59 @@ mla_attention_kernel(AttnParams p) {
   };
   // fragment f of the values: WIDE: 32 channels from 32 (f / 2), 16 tokens from 16 (f % 2); else 16
   // channels from 16 f, 32 tokens
-  auto value = [&](auto f) {
+  auto read_value = [&](auto f) {
     if constexpr (WIDE) {
       constexpr int off = f / 4 * kGroupB + f % 2 * 2 * kBlockB;
-      x[f % kAhead] = lds_tr(va[f / 2 % 2 * 2], off, va[f / 2 % 2 * 2 + 1], off + kBlockB);
+      return lds_tr(va[f / 2 % 2 * 2], off, va[f / 2 % 2 * 2 + 1], off + kBlockB);
     } else {
       constexpr int off = f / 4 * kGroupB;
-      x[f % kAhead] = lds_tr(va[f % 4], off, va[f % 4], off + 2 * kBlockB);
+      return lds_tr(va[f % 4], off, va[f % 4], off + 2 * kBlockB);
     }
   };
+  auto value = [&](auto f) { x[f % kAhead] = read_value(f); };
   auto product = [&](auto f) {
     if constexpr (WIDE) acc_mfma<ROWS, f / 2>(x[f % kAhead], pr[f % 2]);
     else acc_mfma<ROWS, f>(x[f % kAhead], pr[0]);
   };
-  // masked places of the scores of tokens tb .. (only in tiles that some row does not see whole)
+  // Tiles that some row does not see whole: the scores' masked places, and tokens that are not finite.
   // A token that some row of the tile does not see may hold infinities or NaN, which a probability of 0
   // does not take out of the product.  Every row's score of it is then not finite either, so the
-  // masked scores tell; what is not finite in the values becomes 0 (a row that sees it has NaN in its sum).
-  auto hide = [&](int tb, uint32_t tile) {
-    if (tb + kTok <= end_min) return false;
-    bool odd = false;
+  // masked scores tell (`hidden`), and what is not finite in the values becomes 0.  A row that sees such a
+  // token has NaN in its sum, unless the score is -inf (`low`): its probability is 0, and 0 times an infinity
+  // is NaN in that channel alone, which is put into the accumulators before.
+  auto mask = [&](int tb, float& hidden, float& low) {   // hidden becomes NaN, low -inf
+    if (tb + kTok <= end_min) return;
     unroll<Scores<ROWS>::N>([&](auto e) {
-      if (tb + GS * (e / 4) + 4 * g + e % 4 >= end) {
-        odd |= __builtin_amdgcn_classf(s.template get<e>(), 0x207);   // NaN, -inf, inf
-        s.template set<e>(kNegInf);
-      }
+      const float v = s.template get<e>();
+      const bool sees = tb + GS * (e / 4) + 4 * g + e % 4 < end;
+      hidden = __builtin_fmaf(sees ? 0.0f : v, 0.0f, hidden);
+      low = fminf(low, sees ? v : 0.0f);
+      s.template set<e>(sees ? v : kNegInf);
     });
-    if (end_min == end_max || !__any(odd)) return false;
+  };
+  // NaN into the accumulators of the channels where a token that the row sees with a score of -inf holds
+  // what is not finite: 2^127.99 squared overflows to inf, and inf - inf is NaN
+  auto mark = [&](int tb) {
+    v4u u[2];
+    unroll<Scores<ROWS>::N>([&](auto e) {
+      const bool in = tb + GS * (e / 4) + 4 * g + e % 4 < end && s.template get<e>() == kNegInf;
+      const uint32_t one = in ? e % 2 ? 0x7F7F0000u : 0x7F7Fu : 0u;
+      if constexpr (e % 2 == 0) u[e / 8][e % 8 / 2] = one;
+      else u[e / 8][e % 8 / 2] |= one;
+    });
+    unroll<Scores<ROWS>::N / 8>([&](auto k) { pr[k] = __builtin_bit_cast(v8bf, u[k]); });
+    unroll<NV>([&](auto f) {
+      v4u v = __builtin_bit_cast(v4u, read_value(f));
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        v[d] = ((v[d] & 0x7F80u) == 0x7F80u ? 0x7F7Fu : 0u) | ((v[d] & 0x7F800000u) == 0x7F800000u ? 0x7F7F0000u : 0u);
+      const v8bf plus = __builtin_bit_cast(v8bf, v), minus = __builtin_bit_cast(v8bf, v ^ (v << 1 & 0x80008000u));
+      operands_settle();
+      acc_mfma<ROWS, WIDE ? f / 2 : f>(plus, pr[WIDE ? f % 2 : 0]);
+      acc_mfma<ROWS, WIDE ? f / 2 : f>(minus, pr[WIDE ? f % 2 : 0]);
+    });
+  };
+  auto clear = [&](uint32_t tile) {
     int ln = lane;
     asm volatile("" : "+v"(ln));
     uint32_t at = tile + ln * 16;
@@ -761,6 +787,20 @@ mla_attention_kernel(AttnParams p) {
       *(lds_v4u*)(uintptr_t)at = v;
       at += i % 8 == 7 ? 2 * kGroupB : kGroupB;      // past the rotated group
     }
+  };
+  // all of it for step k, its tokens from tb on (values_at is set); true if the tile's values changed.  The other
+  // row waves' scores and marks are of the values as they came, hence the barrier; their products may
+  // take the cleared values or not: theirs are rows that do not see the token, or have NaN by now.
+  // (No bf16 of a code is infinite, and a NaN gives no score of -inf: FP8 has nothing to mark.)
+  auto hide = [&](int k, int tb, uint32_t tile) {
+    float hidden = 0.0f, low = 0.0f;
+    mask(tb, hidden, low);
+    if (end_min == end_max || (step0 + k + 1) * STEP <= end_min) return false;
+    if constexpr (!FP8)
+      if (__any(low == kNegInf)) mark(tb);
+    if constexpr (RW > 1 && !(FP8 && PIPE)) barrier_lds();   // (PIPE: the scores are a barrier ago)
+    if (!__any(hidden != hidden)) return false;
+    clear(tile);
     return true;
   };
   // Scores to probabilities in kSoft pieces that fit beside a matrix instruction: the maximum of four
@@ -847,8 +887,8 @@ mla_attention_kernel(AttnParams p) {
     int place = 0;                                   // of tile k
     for (int k = 0; k < n_steps; ++k) {
       const int tb = t_seg + k * STEP;
-      hide(tb, tile_at + place * kTileB);            // every wave has this tile's scores
       values_at(place * kTileB);
+      hide(k, tb, tile_at + place * kTileB);
       if (k + 1 < n_steps) {
         t.clear();
         unroll<NF>([&](auto f) {
@@ -937,9 +977,7 @@ mla_attention_kernel(AttnParams p) {
         else value(std::integral_constant<int, f + kAhead - NF>{});
       });
       fence();
-      if constexpr (RW > 1)                          // the other row waves have the boundary tile's scores
-        if (end_min < end_max && (step0 + k + 1) * STEP > end_min) barrier_lds();
-      if (hide(tb, tile_at + off)) unroll<kAhead>([&](auto f) { value(f); });
+      if (hide(k, tb, tile_at + off)) unroll<kAhead>([&](auto f) { value(f); });
       unroll<kSoft>([&](auto i) { soft(i); });
       operands_settle();
       unroll<NV>([&](auto f) {

@@ -467,7 +467,9 @@ int fp8bs_mla_cache_write(const void* q_rope, int64_t ldq_t, int64_t ldq_h, cons
  * float32; the probabilities are rounded to bf16 for the second product, the
  * softmax's maximum and sum are float32.  A token that a row does not see has
  * no part in it, whatever it holds (infinities and NaN too); a row that sees a
- * NaN is NaN.  The result does not depend on timing.
+ * NaN is NaN, and so is one with a score of +inf (lse too).  A score of -inf
+ * weighs its token with 0, which leaves NaN in the channels where its latent is
+ * infinite and nowhere else.  The result does not depend on timing.
  */
 int64_t fp8bs_mla_attention_workspace_size(int64_t T, int64_t H, int64_t B);
 int fp8bs_mla_attention(const void* q_lat, int64_t ldq_t, int64_t ldq_h, const void* q_rope,

@@ -152,6 +152,64 @@ def test_not_finite_where_masked(H, nq, dtype, width):
     assert torch.isnan(out[sees.to(DEV)]).all() and torch.isnan(lse[sees.to(DEV)]).all()
 
 
+def compare_not_finite(args, what, scale=SCALE):
+    """Element by element what the formula gives where cached tokens hold infinities: NaN in a channel where a
+    weight of 0 (a score of -inf) meets an infinity, in all of a row with a score of +inf or NaN, and the others
+    within the bars, whose size of a score is that of the tokens with finite ones.  Calls repeated give the same bytes."""
+    q_lat, q_rope, cache, table, cu, lens = args
+    ref, ref_lse, A, _ = attention64(*args, scale, True)
+    tame = fp8bs.MlaCache(*(None if t is None else t.clone() for t in cache))
+    for t in (tame.latent, tame.rope):
+        if t.dtype == BF16:
+            t[torch.isinf(t)] = 0
+    S = attention64(q_lat, q_rope, tame, table, cu, lens, scale, True)[3]
+    runs = [run(args, dt=torch.float32, scale=scale) for _ in range(3)]
+    out, lse = (t.cpu() for t in runs[0])
+    for a, b in runs[1:]:
+        assert torch.equal(a.cpu().view(torch.int32), out.view(torch.int32))
+        assert torch.equal(b.cpu().view(torch.int32), lse.view(torch.int32))
+    nan = torch.isnan(ref)
+    assert nan.any() and not nan.all(-1).all()
+    got = torch.isnan(out)
+    assert torch.equal(got, nan), f"{what}: NaN differs in {(got != nan).sum()} of {nan.sum()}, first {(got != nan).nonzero()[:4].tolist()}"
+    lost = nan.all(-1)
+    assert torch.isnan(lse[lost]).all()
+    fill = [torch.where(nan, 0.0, t.double()) for t in (out, ref, A)]
+    ok = ~lost
+    check_attention(fill[0][ok].float(), lse[ok], (fill[1][ok], ref_lse[ok], fill[2][ok], S[ok]), int(lens.max()), what)
+
+
+@pytest.mark.parametrize("H,nq", [(16, [3, 40]), (4, [30, 9]), (2, [16, 12]), (1, [12, 7]), (3, [7, 14]), (40, [4, 7]),
+                                  (128, [3, 2])])
+@pytest.mark.parametrize("scale", [SCALE, -SCALE], ids=["plus", "minus"])
+@pytest.mark.parametrize("where", ["later", "all", "both"])
+def test_infinities_that_rows_see(H, nq, scale, where, width):
+    """One infinite latent in a token that a chunk's later rows see, one in a token that all see right before
+    the chunk, or both beside one that the last row sees: about half of a row's scores of it are -inf."""
+    lens = [70, 131]
+    args = batch(H, nq, lens, 16, BF16, 67 + H, W=columns(width, lens, 16))
+    q_lat, q_rope, cache, table, cu, ln = args
+    for b, (n, m) in enumerate(zip(lens, nq)):
+        spots = {"later": [(n - m + (m + 1) // 2, 7 + 8 * b)], "all": [(n - m - 1, 130 + b)],
+                 "both": [(n - m - 1, 64 + b), (n - m + (m + 1) // 2, 511 - b), (n - 1, 300)]}[where]
+        for at, channel in spots:
+            cache.latent[table[b, at // 16], at % 16, channel] = -math.inf if (at + H) % 2 else math.inf
+    compare_not_finite(args, f"H {H} nq {nq} {where}", scale)
+
+
+@pytest.mark.parametrize("H,nq", [(16, [9, 40]), (2, [16, 12]), (1, [12, 7]), (128, [3, 2])])
+@pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
+def test_infinite_keys(H, nq, dtype, width):
+    """Infinities in the rotated part alone: a score of -inf takes its token out, with nothing to spread."""
+    lens = [70, 131]
+    args = batch(H, nq, lens, 16, dtype, 73 + H, W=columns(width, lens, 16))
+    cache, table = args[2], args[3]
+    for b, (n, m) in enumerate(zip(lens, nq)):
+        for at, d in ((n - m - 2, 5), (n - m + m // 2, 40)):
+            cache.rope[table[b, at // 16], at % 16, d] = math.inf
+    compare_not_finite(args, f"H {H} nq {nq}")
+
+
 @pytest.mark.parametrize("H", [16, 128])
 def test_boundaries_that_decrease(H, width):
     """cu_q out of order is outside the contract, but writes only rows of the
