@@ -2,6 +2,7 @@
 // its arguments on the host (no HIP call happens before the checks pass) and
 // then enqueues the kernels on the caller's stream.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "fp8bs.h"
@@ -426,7 +427,7 @@ int fp8bs_mla_attention(const void* q_lat, int64_t ldq_t, int64_t ldq_h, const v
                         void* stream) {
   const int64_t need = fp8bs_mla_attention_workspace_size(T, H, B);
   if (need < 0 || ldq_t < 0 || ldq_h < 0 || ldr_t < 0 || ldr_h < 0 ||
-      !(scale >= -3.0e38f && scale <= 3.0e38f))
+      !(fabsf(scale) <= 2.3e38f))                    // times log2(e) it is still finite
     return FP8BS_ERR_SHAPE;
   if (out_dtype != FP8BS_OUT_BF16 && out_dtype != FP8BS_OUT_F32) return FP8BS_ERR_ENUM;
   if (T == 0 || B == 0) return FP8BS_OK;

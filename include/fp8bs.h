@@ -456,7 +456,8 @@ int fp8bs_mla_cache_write(const void* q_rope, int64_t ldq_t, int64_t ldq_h, cons
  *                 (fp8bs_mla_absorb_key's output)
  *   q_rope   in   bf16, the same with ldr_t, ldr_h, i < 64
  *                 (fp8bs_mla_cache_write's q_out); strides >= 0, multiples of 8
- *   scale         finite
+ *   scale         |scale| <= 2.3e38; one below 2^-126 / log2(e) is taken as that
+ *                 (0: the scores vanish, as long as the products are below 2^100)
  *   out      out  [T, H, 512] bf16 or float32 (out_dtype)
  *   lse      out  float32 [T, H], or NULL
  *   workspace     DEVICE, >= fp8bs_mla_attention_workspace_size(T, H, B) bytes,

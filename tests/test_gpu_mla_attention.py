@@ -284,6 +284,14 @@ def test_any_scale(scale, width):
     compare(batch(96, [2, 1], lens, 32, BF16, 71, W=columns(width, lens, 32)), f"scale {scale}", scale=scale)
 
 
+@pytest.mark.parametrize("scale", [2.3e38, -2.3e38])
+def test_largest_scale(scale, width):
+    """Queries of zero: every score is 0, whatever the scale, and the output the mean."""
+    lens = [60, 99]
+    q_lat, q_rope, *rest = batch(96, [2, 1], lens, 32, BF16, 72, W=columns(width, lens, 32))
+    compare((q_lat * 0, q_rope * 0, *rest), f"scale {scale}", scale=scale)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP8], ids=["bf16", "fp8"])
 def test_many_sequences(dtype, width):
     """300 sequences of odd lengths, none, one or a few new tokens each."""

@@ -99,6 +99,14 @@ def test_attention_refusals(L):
     assert call(f, ATTN, nws=need - 1) == SHAPE
 
 
+def test_attention_scale_limit(L):
+    """|scale| log2(e) has to be a float32: beyond, a score of 0 would be NaN."""
+    for sm in (2.31e38, -2.31e38, 3.0e38):
+        assert call(L.fp8bs_mla_attention, ATTN, sm=sm) == SHAPE, sm
+    for sm in (2.3e38, -2.3e38):                              # accepted: the next check's answer
+        assert call(L.fp8bs_mla_attention, ATTN, sm=sm, ldq_t=4) == ALIGN, sm
+
+
 def test_update_and_compact_refusals(L):
     f, g = L.fp8bs_cache_update, L.fp8bs_cache_compact
     for kw in (dict(N=-1), dict(N=1 << 18), dict(nws=L.fp8bs_cache_update_workspace_size(2, 3, 3, 20000) - 1)):
