@@ -387,7 +387,7 @@ __device__ __forceinline__ int count_before(const uint32_t* used, int* before, i
 }
 
 // what one launch takes: update's pages, rows and table entries, compact's pages and entries
-constexpr int kSmallPages = 1 << 14, kSmallRows = 512, kSmallEntries = 1 << 16;
+constexpr int kSmallPages = 1 << 14, kSmallRows = 512, kSmallEntries = 45 << 10;
 constexpr int kCompactPages = 1 << 17, kCompactEntries = 1 << 14;
 
 __global__ void __launch_bounds__(1024) update_small_kernel(PageParams p, int parts) {
@@ -548,10 +548,11 @@ __global__ void __launch_bounds__(256) page_apply_compact_kernel(PageParams p) {
 
 // One launch when a workgroup's LDS holds the pages' keys and the rows (86 KB) and its own
 // reading of the tables takes no longer than three launches more.  us a call from a graph, one
-// launch / four: 16 rows of 2000 tokens 8.1 / 12.8, 64 of 4000 to 256 rows (fp8) 13.8 / 16.9, 64 of
-// 8000 to 256 (40,000 entries) 17.7 / 17.0, of 12000 21.7 / 17.4, 4 rows to 1024 33.5 / 29.0.  Calls
-// that are not in a graph pay 2 us or so of the host's time for each launch, so the line is drawn
-// behind the third of these.  The copies of the 256 beams move 9.6 MB.
+// launch / four, fp8, by table entries (B + N) W: 16 rows of 2000 tokens 8.1 / 12.8; 64 rows to 256 with
+// 10,560 13.8 / 15.9, 20,480 14.1 / 17.2, 30,400 18.0 / 18.5, 40,640 18.5 / 19.0, 50,560 21.8 / 19.0, 60,480
+// 22.8 / 19.1; 128 rows with 32,512 17.1 / 16.8; 16 to 512 with 33,792 21.1 / 23.4, 50,160 27.0 / 23.7.
+// Calls that are not in a graph pay the host's time for each launch (22 for four): with 50,560 20.6 / 22.3.
+// The line is drawn between those on which the graph's calls lose and the others.
 bool update_is_small(int64_t B, int64_t N, int64_t W, int64_t P) {
   return P <= kSmallPages && N <= kSmallRows && (B + N) * W <= kSmallEntries;
 }

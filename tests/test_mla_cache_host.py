@@ -133,6 +133,15 @@ def test_update_and_compact_refusals(L):
     assert L.fp8bs_cache_update_workspace_size(2, 3, 3, 10) == L.fp8bs_cache_compact_workspace_size(2, 3, 10) == 0
 
 
+def test_update_leaves_one_launch_where_four_are_faster(L):
+    """Where four launches win in a graph (50,000 table entries and more) they are taken: they need a workspace."""
+    size = L.fp8bs_cache_update_workspace_size
+    for B, N, W in ((64, 256, 100), (128, 128, 125), (256, 256, 64)):
+        assert size(B, N, W, 16000) == 0, (B, N, W)
+    for B, N, W in ((64, 256, 158), (64, 256, 189), (16, 512, 95), (4, 500, 110)):
+        assert size(B, N, W, 16000) > 0, (B, N, W)
+
+
 def test_sizes_beyond_one_launch(L):
     """A workgroup of 256 threads a token or row: 2^24 of them is one too many."""
     assert call(L.fp8bs_mla_cache_write, WRITE, T=1 << 24) == SHAPE
