@@ -483,18 +483,31 @@ _LATENT = (torch.bfloat16, *_F8)
 
 def _ptr(t: torch.Tensor, name: str, dtypes, shape, dev) -> int:
     """The address of a contiguous tensor of one of `dtypes`, of `shape`, on device `dev`."""
-    if t.dtype in dtypes and t.shape == shape and t.device == dev and t.is_contiguous():
+    if getattr(t, "dtype", None) in dtypes and t.shape == shape and t.device == dev and t.is_contiguous():
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    _need(t, dtypes, name)
-    raise ValueError(f"{name} lies on {t.device}, other tensors on {dev}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.device != dev:
+        raise ValueError(f"{name} lies on {t.device}, other tensors on {dev}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _misfit(message: str, **tensors) -> Exception:
+    """What to raise for arguments without the dimensions that `message` asks for."""
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            return TypeError(f"{name} must be a torch.Tensor")
+    return ValueError(message)
 
 
 def _rows3(t: torch.Tensor, name: str, shape, dev):
     """A bf16 [T, H, width] view with a dense last dimension: (pointer, token stride, head stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != torch.bfloat16:
@@ -509,14 +522,16 @@ def _rows3(t: torch.Tensor, name: str, shape, dev):
 
 
 def _cache_args(cache: MlaCache):
-    """(device, latent, scale, rope, format, P, ps), checked."""
-    lat, rope, scale = cache
-    dev = lat.device
-    if dev.type != "cuda":
-        raise ValueError("cache.latent must be a device tensor")
-    if lat.dim() != 3:
-        raise ValueError(f"cache.latent must be [P, ps, {MLA_RANK}]")
-    P, ps, _ = lat.shape
+    """(device, latent, scale, rope, format, P, ps), checked but for the device's kind (_call_on)."""
+    try:
+        lat, rope, scale = cache
+    except (TypeError, ValueError):
+        raise TypeError("cache must be an MlaCache") from None
+    try:
+        dev = lat.device
+        P, ps, _ = lat.shape
+    except (AttributeError, ValueError):
+        raise _misfit(f"cache.latent must be [P, ps, {MLA_RANK}]", **{"cache.latent": lat}) from None
     bf16 = lat.dtype == torch.bfloat16
     if bf16 != (scale is None):
         raise ValueError("cache.scale goes with a float8_e4m3fn cache, and only with one")
@@ -540,6 +555,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i:
 
 def _call_on(dev, fn: str, *args) -> None:
     """fn(*args, the current stream of device `dev`), with that device current."""
+    if dev.type != "cuda":
+        raise ValueError("cache.latent must be a device tensor")
     stream = _raw_stream(dev.index)
     if torch.cuda.current_device() == dev.index:
         _call(fn, *args, stream)
@@ -555,11 +572,15 @@ def fp8bs_mla_cache_write(q_rope: torch.Tensor, kv: torch.Tensor, norm_w: torch.
     (norm_w [512] bf16 or float32), rotated and stored at the last positions of
     their sequences; q_rope bf16 [T, H, 64] (a slice of q may be passed) rotated
     into q_out bf16 [T, H, 64].  rope_cs float32 [n_pos, 32, 2] holds (cos, sin)."""
-    if q_rope.dim() != 3 or kv.dim() != 2 or table.dim() != 2 or rope_cs.dim() != 3:
-        raise ValueError("q_rope must be [T, H, 64], kv [T, 576], table [B, W] and rope_cs [n_pos, 32, 2]")
-    (T, H, _), (B, W), n_pos = q_rope.shape, table.shape, rope_cs.shape[0]
+    try:
+        (T, H, _), (_, _), (B, W), (n_pos, _, _) = q_rope.shape, kv.shape, table.shape, rope_cs.shape
+    except (AttributeError, TypeError, ValueError):
+        raise _misfit("q_rope must be [T, H, 64], kv [T, 576], table [B, W] and rope_cs [n_pos, 32, 2]",
+                      q_rope=q_rope, kv=kv, table=table, rope_cs=rope_cs) from None
     dev, lat, scale, rope, fmt, P, ps = _cache_args(cache)
     qp, ldt, ldh = _rows3(q_rope, "q_rope", (T, H, MLA_ROPE), dev)
+    if not isinstance(kv, torch.Tensor):
+        raise TypeError("kv must be a torch.Tensor")
     if kv.shape != (T, MLA_RANK + MLA_ROPE) or kv.dtype != torch.bfloat16 or kv.device != dev or (T and kv.stride(1) != 1):
         raise ValueError(f"kv must be bfloat16 [{T}, {MLA_RANK + MLA_ROPE}] on {dev} with a contiguous last dimension")
     kp, ldk = kv.data_ptr(), (kv.stride(0) if T > 1 else 0)
@@ -572,7 +593,10 @@ def fp8bs_mla_cache_write(q_rope: torch.Tensor, kv: torch.Tensor, norm_w: torch.
 
 
 def mla_cache_write(q_rope, kv, norm_w, eps, rope_cs, cache: MlaCache, table, cu_q, lens) -> torch.Tensor:
-    """fp8bs_mla_cache_write; returns the rotated queries [T, H, 64]."""
+    """fp8bs_mla_cache_write; returns the rotated queries [T, H, 64] (not
+    initialised where the call writes none: tokens without a position)."""
+    if not isinstance(q_rope, torch.Tensor):
+        raise TypeError("q_rope must be a torch.Tensor")
     q_out = q_rope.new_empty(q_rope.shape)
     fp8bs_mla_cache_write(q_rope, kv, norm_w, eps, rope_cs, q_out, cache, table, cu_q, lens)
     return q_out
@@ -584,9 +608,10 @@ def fp8bs_mla_attention(q_lat: torch.Tensor, q_rope: torch.Tensor, cache: MlaCac
     """The new tokens' attention over the cache: q_lat bf16 [T, H, 512] (from
     mla_absorb_key) and q_rope bf16 [T, H, 64] (from mla_cache_write), any token
     and head strides; out [T, H, 512] bf16 or float32, lse float32 [T, H] or None."""
-    if q_lat.dim() != 3 or table.dim() != 2:
-        raise ValueError(f"q_lat must be [T, H, {MLA_RANK}] and table [B, W]")
-    (T, H, _), (B, W) = q_lat.shape, table.shape
+    try:
+        (T, H, _), (B, W) = q_lat.shape, table.shape
+    except (AttributeError, TypeError, ValueError):
+        raise _misfit(f"q_lat must be [T, H, {MLA_RANK}] and table [B, W]", q_lat=q_lat, table=table) from None
     dev, lat, sc, rope, fmt, P, ps = _cache_args(cache)
     qp, ldt, ldh = _rows3(q_lat, "q_lat", (T, H, MLA_RANK), dev)
     rp, ldrt, ldrh = _rows3(q_rope, "q_rope", (T, H, MLA_ROPE), dev)
@@ -601,14 +626,19 @@ def fp8bs_mla_attention(q_lat: torch.Tensor, q_rope: torch.Tensor, cache: MlaCac
 
 def mla_attention(q_lat, q_rope, cache: MlaCache, table, cu_q, lens, scale: float, causal: bool = True,
                   return_lse: bool = False, out_dtype=torch.bfloat16):
-    """fp8bs_mla_attention: out [T, H, 512], with return_lse (out, lse)."""
-    T, H = q_lat.shape[:2]
-    need = lib().fp8bs_mla_attention_workspace_size(T, H, table.shape[0])
+    """fp8bs_mla_attention: out [T, H, 512], with return_lse (out, lse); not
+    initialised in rows behind the last sequence."""
+    try:
+        (T, H, _), (B, _) = q_lat.shape, table.shape
+        new_empty = q_lat.new_empty
+    except (AttributeError, TypeError, ValueError):
+        raise _misfit(f"q_lat must be [T, H, {MLA_RANK}] and table [B, W]", q_lat=q_lat, table=table) from None
+    need = lib().fp8bs_mla_attention_workspace_size(T, H, B)
     if need < 0:
         raise ValueError("sizes out of range")
-    out = q_lat.new_empty((T, H, MLA_RANK), dtype=out_dtype)
-    lse = q_lat.new_empty((T, H), dtype=torch.float32) if return_lse else None
-    ws = q_lat.new_empty(need, dtype=torch.uint8)
+    out = new_empty((T, H, MLA_RANK), dtype=out_dtype)
+    lse = new_empty((T, H), dtype=torch.float32) if return_lse else None
+    ws = new_empty(need, dtype=torch.uint8)
     fp8bs_mla_attention(q_lat, q_rope, cache, table, cu_q, lens, scale, out, lse, ws, causal)
     return (out, lse) if return_lse else out
 
@@ -619,9 +649,10 @@ def fp8bs_cache_update(cache: MlaCache, table: torch.Tensor, lens: torch.Tensor,
     """The next step's rows: row i continues old row parent[i] (else it is
     empty) and is to hold new_lens[i] tokens; table_out [N, W], lens_out [N].
     Forks, frees, truncates, grows and copies on write (see fp8bs.h)."""
-    if table.dim() != 2 or parent.dim() != 1:
-        raise ValueError("table must be [B, W] and parent [N]")
-    (B, W), N = table.shape, parent.shape[0]
+    try:
+        (B, W), (N,) = table.shape, parent.shape
+    except (AttributeError, TypeError, ValueError):
+        raise _misfit("table must be [B, W] and parent [N]", table=table, parent=parent) from None
     dev, lat, sc, rope, fmt, P, ps = _cache_args(cache)
     ws, nbytes = _scratch(workspace, dev)
     _call_on(dev, "fp8bs_cache_update", lat, sc, rope, fmt, _ptr(table, "table", _I32, (B, W), dev),
@@ -632,12 +663,17 @@ def fp8bs_cache_update(cache: MlaCache, table: torch.Tensor, lens: torch.Tensor,
 
 def cache_update(cache: MlaCache, table, lens, parent, new_lens):
     """fp8bs_cache_update: (table_out [N, W], lens_out [N])."""
-    (B, W), N = table.shape, parent.shape[0]
-    need = lib().fp8bs_cache_update_workspace_size(B, N, W, cache.latent.shape[0])
+    try:
+        (B, W), (N,), P = table.shape, parent.shape, cache[0].shape[0]
+        new_empty = table.new_empty
+    except (AttributeError, IndexError, TypeError, ValueError):
+        _cache_args(cache)
+        raise _misfit("table must be [B, W] and parent [N]", table=table, parent=parent) from None
+    need = lib().fp8bs_cache_update_workspace_size(B, N, W, P)
     if need < 0:
         raise ValueError("sizes out of range")
-    table_out, lens_out = table.new_empty((N, W)), table.new_empty(N)
-    ws = table.new_empty((need + 3) // 4) if need else None
+    table_out, lens_out = new_empty((N, W)), new_empty(N)
+    ws = new_empty((need + 3) // 4) if need else None
     fp8bs_cache_update(cache, table, lens, parent, new_lens, table_out, lens_out, ws)
     return table_out, lens_out
 
@@ -646,11 +682,13 @@ def fp8bs_cache_compact(cache: MlaCache, table: torch.Tensor, lens: torch.Tensor
                         count: torch.Tensor, workspace: Optional[torch.Tensor]) -> None:
     """The pages that the rows use moved to the lowest indices; table_out
     [B, W] holds the new ones, count [1] (or a 0-d tensor) how many."""
-    if table.dim() != 2:
-        raise ValueError("table must be [B, W]")
-    if count.numel() != 1:
+    try:
+        B, W = table.shape
+        one = count.numel() == 1
+    except (AttributeError, TypeError, ValueError):
+        raise _misfit("table must be [B, W]", table=table, count=count) from None
+    if not one:
         raise ValueError("count must hold one value")
-    B, W = table.shape
     dev, lat, sc, rope, fmt, P, ps = _cache_args(cache)
     ws, nbytes = _scratch(workspace, dev)
     _call_on(dev, "fp8bs_cache_compact", lat, sc, rope, fmt, _ptr(table, "table", _I32, (B, W), dev),
@@ -660,11 +698,16 @@ def fp8bs_cache_compact(cache: MlaCache, table: torch.Tensor, lens: torch.Tensor
 
 def cache_compact(cache: MlaCache, table, lens):
     """fp8bs_cache_compact: (table_out [B, W], count, a 0-d tensor)."""
-    B, W = table.shape
-    need = lib().fp8bs_cache_compact_workspace_size(B, W, cache.latent.shape[0])
+    try:
+        (B, W), P = table.shape, cache[0].shape[0]
+        new_empty = table.new_empty
+    except (AttributeError, IndexError, TypeError, ValueError):
+        _cache_args(cache)
+        raise _misfit("table must be [B, W]", table=table) from None
+    need = lib().fp8bs_cache_compact_workspace_size(B, W, P)
     if need < 0:
         raise ValueError("sizes out of range")
-    table_out, count = table.new_empty(table.shape), table.new_empty(())
-    ws = table.new_empty((need + 3) // 4) if need else None
+    table_out, count = new_empty((B, W)), new_empty(())
+    ws = new_empty((need + 3) // 4) if need else None
     fp8bs_cache_compact(cache, table, lens, table_out, count, ws)
     return table_out, count

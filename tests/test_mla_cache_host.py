@@ -182,6 +182,44 @@ def test_binding_refusals():
         fp8bs.cache_compact(cache, table, lens)
 
 
+def test_binding_refuses_what_is_no_tensor():
+    """None, numbers and arrays in a tensor's place: a TypeError that names the argument."""
+    i32 = torch.int32
+    cache = fp8bs.mla_cache_alloc(4, 16, "cpu")
+    table, cu, lens = torch.zeros((2, 2), dtype=i32), torch.zeros(3, dtype=i32), torch.zeros(2, dtype=i32)
+    q, qr = torch.zeros((3, 4, 512), dtype=torch.bfloat16), torch.zeros((3, 4, 64), dtype=torch.bfloat16)
+    kv, w, cs = torch.zeros((3, 576), dtype=torch.bfloat16), torch.zeros(512), torch.zeros((9, 32, 2))
+    out = torch.empty((3, 4, 512), dtype=torch.bfloat16)
+    calls = {
+        "attention": (fp8bs.fp8bs_mla_attention, dict(q_lat=q, q_rope=qr, cache=cache, table=table, cu_q=cu, lens=lens,
+                                                      scale=0.1, out=out, lse=None, workspace=None)),
+        "write": (fp8bs.fp8bs_mla_cache_write, dict(q_rope=qr, kv=kv, norm_w=w, eps=1e-6, rope_cs=cs, q_out=qr.clone(),
+                                                    cache=cache, table=table, cu_q=cu, lens=lens)),
+        "update": (fp8bs.fp8bs_cache_update, dict(cache=cache, table=table, lens=lens, parent=lens, new_lens=lens,
+                                                  table_out=table.clone(), lens_out=lens.clone(), workspace=None)),
+        "compact": (fp8bs.fp8bs_cache_compact, dict(cache=cache, table=table, lens=lens, table_out=table.clone(),
+                                                    count=torch.zeros((), dtype=i32), workspace=None)),
+    }
+    for what, (f, args) in calls.items():
+        for name, value in args.items():
+            if isinstance(value, torch.Tensor):
+                for bad in (None, 3, [1, 2], value.float().numpy()):
+                    with pytest.raises(TypeError, match=name):
+                        f(**{**args, name: bad})
+        for bad in (None, cache.latent, (cache.latent, cache.rope), cache._replace(latent=None), cache._replace(rope=None)):
+            with pytest.raises(TypeError, match="cache"):
+                f(**{**args, "cache": bad})
+    for f, args in ((fp8bs.mla_attention, (None, qr, cache, table, cu, lens, 0.1)),
+                    (fp8bs.mla_attention, (q, qr, None, table, cu, lens, 0.1)),
+                    (fp8bs.mla_attention, (q, qr, cache, None, cu, lens, 0.1)),
+                    (fp8bs.mla_cache_write, (None, kv, w, 1e-6, cs, cache, table, cu, lens)),
+                    (fp8bs.cache_update, (cache, None, lens, lens, lens)), (fp8bs.cache_update, (cache, table, lens, None, lens)),
+                    (fp8bs.cache_update, (None, table, lens, lens, lens)), (fp8bs.cache_compact, (None, table, lens)),
+                    (fp8bs.cache_compact, (cache, None, lens))):
+        with pytest.raises(TypeError):
+            f(*args)
+
+
 def test_listing_check():
     """The build refuses an attention kernel whose compiler-made instructions
     touch AGPRs (the accumulators live there, named in inline assembly) or spill."""
