@@ -368,6 +368,14 @@ static bool over_cache(const void* out, int64_t bytes, const void* latent, const
          (fp8 && overlap(out, bytes, lat_scale, rows * 16));
 }
 
+// the cache's arrays meet each other (the entry points that write them refuse it)
+static bool cache_overlaps(const void* latent, const float* lat_scale, const void* rope, int cache_fmt, int64_t P, int64_t ps) {
+  const bool fp8 = cache_fmt == FP8BS_CACHE_FP8;
+  const int64_t rows = P * ps, nl = rows * (fp8 ? 512 : 1024);
+  return overlap(latent, nl, rope, rows * 128) ||
+         (fp8 && (overlap(lat_scale, rows * 16, latent, nl) || overlap(lat_scale, rows * 16, rope, rows * 128)));
+}
+
 // elements from the first to the last of a [T, H, width] view with strides ld_t, ld_h, or -1 when beyond int64
 static int64_t extent(int64_t T, int64_t H, int64_t ld_t, int64_t ld_h, int64_t width) {
   const int64_t a = mul(T - 1, ld_t), b = mul(H - 1, ld_h);
@@ -404,7 +412,9 @@ int fp8bs_mla_cache_write(const void* q_rope, int64_t ldq_t, int64_t ldq_h, cons
     if (overlap(q_out, 2 * nq, in[i], size[i]) ||
         over_cache(in[i], size[i], latent, lat_scale, rope, cache_fmt, P, ps))
       return FP8BS_ERR_ALIAS;
-  if (over_cache(q_out, 2 * nq, latent, lat_scale, rope, cache_fmt, P, ps)) return FP8BS_ERR_ALIAS;
+  if (over_cache(q_out, 2 * nq, latent, lat_scale, rope, cache_fmt, P, ps) ||
+      cache_overlaps(latent, lat_scale, rope, cache_fmt, P, ps))
+    return FP8BS_ERR_ALIAS;
   const fp8bs::MlaCacheWrite a{q_rope, kv, norm_w, rope_cs, q_out, latent, rope, lat_scale, table, cu_q, lens,
                                ldq_t, ldq_h, ld_kv, n_pos, T, H, B, W, P, ps, eps, norm_w_f32 != 0,
                                cache_fmt == FP8BS_CACHE_FP8};
@@ -494,6 +504,7 @@ int fp8bs_cache_update(void* latent, float* lat_scale, void* rope, int cache_fmt
   }
   for (int i = 0; i < 4; ++i)
     if (over_cache(in[i], is[i], latent, lat_scale, rope, cache_fmt, P, ps)) return FP8BS_ERR_ALIAS;
+  if (cache_overlaps(latent, lat_scale, rope, cache_fmt, P, ps)) return FP8BS_ERR_ALIAS;
   const fp8bs::PageTask a{latent, rope, lat_scale, table, lens, parent, new_lens, table_out, lens_out, nullptr,
                           workspace, B, W, N, P, ps, cache_fmt == FP8BS_CACHE_FP8};
   return status_of(fp8bs::launch_cache_update(a, (hipStream_t)stream));
@@ -529,6 +540,7 @@ int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fm
   }
   for (int i = 0; i < 2; ++i)
     if (over_cache(in[i], is[i], latent, lat_scale, rope, cache_fmt, P, ps)) return FP8BS_ERR_ALIAS;
+  if (cache_overlaps(latent, lat_scale, rope, cache_fmt, P, ps)) return FP8BS_ERR_ALIAS;
   const fp8bs::PageTask a{latent, rope, lat_scale, table, lens, nullptr, nullptr, table_out, nullptr, count,
                           workspace, B, W, 0, P, ps, cache_fmt == FP8BS_CACHE_FP8};
   return status_of(fp8bs::launch_cache_compact(a, (hipStream_t)stream));

@@ -404,6 +404,7 @@ int fp8bs_mla_absorb_value(const void* x_bf16, int64_t ld_t, int64_t ld_h, const
  * never write outside the cache, and read no page outside [0, P), so a wrong
  * value gives wrong results for its sequence, not faults (a cu_q that decreases:
  * for the batch).
+ * latent, rope and lat_scale do not overlap (the entry points that write them check).
  * Byte and bf16 pointers and lat_scale are 16-byte aligned, the other float32 and
  * the int32 ones 4-byte, a bf16 norm_w 2-byte.
  */

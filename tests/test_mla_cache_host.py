@@ -155,6 +155,17 @@ def test_write_number_of_sequences(L):
         assert call(L.fp8bs_mla_cache_write, WRITE, B=B, W=1, H=0, table=1 << 44, cu=1 << 45, lens=1 << 46) == SHAPE
 
 
+def test_cache_arrays_that_overlap(L):
+    """The writing entry points refuse a cache whose arrays lie over each other."""
+    for name, base in (("fp8bs_mla_cache_write", WRITE), ("fp8bs_cache_update", UPDATE), ("fp8bs_cache_compact", COMPACT)):
+        f, tokens = getattr(L, name), base["P"] * base["ps"]
+        codes = dict(fmt=1, scale=A[15])
+        for kw in (dict(rope=base["latent"]), dict(rope=base["latent"] + tokens * 1024 - 16),
+                   dict(latent=base["rope"] + tokens * 128 - 16), dict(codes, rope=base["latent"] + tokens * 512 - 16),
+                   dict(codes, scale=base["latent"] + 16), dict(codes, scale=base["rope"] + tokens * 128 - 16)):
+            assert call(f, base, **kw) == ALIAS, (name, kw)
+
+
 def test_binding_refusals():
     """Shapes and types are refused before anything is asked of a device."""
     bf, i32 = torch.bfloat16, torch.int32
