@@ -52,52 +52,99 @@ def _vgprs(operand: str) -> range:
     return range(int(m[1]), int(m[1]) + 1) if m[1] else range(int(m[2], 0), int(m[3], 0) + 1)
 
 
+def _written(op: str, args) -> frozenset:
+    """The VGPRs that an instruction of the vector ALU writes."""
+    if not op.startswith("v_") or op.startswith("v_cmp"):
+        return frozenset()
+    return frozenset(r for a in args[:2 if "swap" in op else 1] for r in _vgprs(a))
+
+
 def check_listing(src: str, text: str) -> None:
     """Raises if the listing of a source in OWN_AGPR_SOURCES touches an AGPR
     outside inline assembly, spills, or writes an operand of an MFMA of the
     inline assembly within two instructions or wait states before it (which the
-    compiler would see to for its own)."""
-    inside, before = False, []
-    for line in text.splitlines():
-        if "#ASMSTART" in line or "#ASMEND" in line:
-            inside = "#ASMSTART" in line
-            continue
-        m = re.match(r"\s+([vdsgb]\w*_\w+)\s+(.*)", line.split(";")[0])
-        if not m:
-            continue
-        op, args = m[1], [a.strip() for a in m[2].split(",")]
-        if not inside and (re.search(r"(^|[ ,])a(\d|\[)", m[2]) or op.startswith("scratch_")):
-            raise RuntimeError(f"{src}: the compiler uses registers that the kernel keeps for itself: {line.strip()}")
-        if inside and op.startswith("v_mfma"):
-            read = {r for a in args[1:3] for r in _vgprs(a)}
-            if any(read & set(w) for w in before[-2:]):
-                raise RuntimeError(f"{src}: an operand is written just before its MFMA: {line.strip()}")
-        if op == "s_nop":
-            before += [range(0)] * (int(args[0], 0) + 1)
-        else:
-            before.append(_vgprs(args[0]) if op.startswith("v_") and not op.startswith("v_cmp") else range(0))
+    compiler would see to for its own), on any way there: the two places before
+    the start of a block are those before each jump to it, and above it if that falls through."""
+    tails = {}                     # label -> VGPRs written in the two places before it, over all ways
+    lines = text.splitlines()
+    # in the order of the text, until what jumps back bring to earlier labels changes no more
+    changed = True
+    while changed:
+        changed, inside, falls = False, False, False
+        before = [frozenset(), frozenset()]
+
+        def reach(label):
+            nonlocal changed
+            old = tails.get(label, [frozenset(), frozenset()])
+            new = [o | w for o, w in zip(old, before)]
+            if new != old:
+                tails[label], changed = new, True
+
+        for line in lines:
+            if "#ASMSTART" in line or "#ASMEND" in line:
+                inside = "#ASMSTART" in line
+                continue
+            label = re.match(r"([.\w$]+):", line)
+            if label:
+                if falls and label[1].startswith(".L"):
+                    reach(label[1])
+                before, falls = list(tails.get(label[1], [frozenset(), frozenset()])), True
+                continue
+            m = re.match(r"\s+([vdsgb]\w*_\w+)\s*(.*)", line.split(";")[0])
+            if not m:
+                continue
+            op, args = m[1], [a.strip() for a in m[2].split(",")]
+            if not inside and (re.search(r"(^|[ ,])a(\d|\[)", m[2]) or op.startswith("scratch_")):
+                raise RuntimeError(f"{src}: the compiler uses registers that the kernel keeps for itself: {line.strip()}")
+            if inside and op.startswith("v_mfma"):
+                if {r for a in args[1:3] for r in _vgprs(a)} & (before[0] | before[1]):
+                    raise RuntimeError(f"{src}: an operand is written just before its MFMA: {line.strip()}")
+            if op == "s_endpgm":
+                falls, before = False, [frozenset(), frozenset()]
+            elif op.startswith(("s_branch", "s_cbranch")):
+                before = [before[1], frozenset()]
+                reach(args[0])
+                if op == "s_branch":
+                    falls, before = False, [frozenset(), frozenset()]
+                else:
+                    falls = True
+            elif op.startswith(("s_setpc", "s_swappc", "s_call")):
+                raise RuntimeError(f"{src}: a jump whose target the check does not follow: {line.strip()}")
+            else:
+                n = min(int(args[0], 0) + 1, 2) if op == "s_nop" else 1
+                before = (before + [frozenset()] * n if op == "s_nop" else before + [_written(op, args)])[-2:]
+                falls = True
 
 
-def _listing(cmd, src: str) -> str:
-    res = subprocess.run([*cmd, "--cuda-device-only", "-S", os.path.join(CSRC, src), "-o", "-"], capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"compile failed: {src}\n{res.stderr}")
-    return res.stdout
-
-
-def _compile(src: str, build_dir: str) -> str:
+def compile_listed(cmd, src: str, build_dir: str):
+    """(object, device listing) of one compilation."""
+    name = os.path.splitext(os.path.basename(src))[0]
     obj = os.path.join(build_dir, os.path.basename(src) + ".o")
-    form = [] if src in AGPR_SOURCES else VGPR_FORM
-    own = OWN_AGPR_FLAGS if src in OWN_AGPR_SOURCES else []
-    cmd = [HIPCC, *COMMON_FLAGS, *HIP_FLAGS, *form, *own, "-x", "hip"]
-    if own:
-        check_listing(src, _listing(cmd, src))
-    cmd += ["-c", os.path.join(CSRC, src), "-o", obj]
-    if src.endswith(".cpp"):
-        cmd = [HIPCC, *COMMON_FLAGS, "--offload-arch=gfx950", "-c", os.path.join(CSRC, src), "-o", obj]
+    _run([*cmd, "-c", src, "-o", obj, "-save-temps=obj"])
+    with open(os.path.join(build_dir, f"{name}-hip-amdgcn-amd-amdhsa-gfx950.s")) as f:
+        return obj, f.read()
+
+
+def _run(cmd) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+
+
+def _compile(src: str, build_dir: str) -> str:
+    path = os.path.join(CSRC, src)
+    obj = os.path.join(build_dir, src + ".o")
+    if src.endswith(".cpp"):
+        _run([HIPCC, *COMMON_FLAGS, "--offload-arch=gfx950", "-c", path, "-o", obj])
+        return obj
+    own = OWN_AGPR_FLAGS if src in OWN_AGPR_SOURCES else []
+    form = [] if src in AGPR_SOURCES else VGPR_FORM
+    cmd = [HIPCC, *COMMON_FLAGS, *HIP_FLAGS, *form, *own, "-x", "hip"]
+    if own:
+        obj, text = compile_listed(cmd, path, build_dir)
+        check_listing(src, text)
+    else:
+        _run([*cmd, "-c", path, "-o", obj])
     return obj
 
 

@@ -248,3 +248,36 @@ def test_listing_check():
         with pytest.raises(RuntimeError):
             build.check_listing("x", line + mfma)
     assert "mla_attention.hip" in build.OWN_AGPR_SOURCES
+
+
+def test_listing_check_across_branches():
+    """What runs before an MFMA is not always what stands above it: the end of a
+    loop comes before its start, a jump's source before its target, and nothing falls
+    out of a jump that is always taken."""
+    from block_scaled_fp8_03_amd import build
+    mfma = "\t;;#ASMSTART\n\tv_mfma_f32_32x32x16_bf16 a[0x10:0x1f], v[8:11], v[12:15], a[0x10:0x1f]\n\t;;#ASMEND\n"
+    write, other = "\tv_mov_b32_e32 v9, v1\n", "\tv_mov_b32_e32 v30, v1\n"
+    loop = ".LBB0_1:\n" + mfma + "{}\ts_cbranch_scc1 .LBB0_1\n; %bb.2:\n\ts_endpgm\n"
+    jump = "{}\ts_cbranch_execz .LBB0_3\n" + 3 * other + "\ts_branch .LBB0_4\n.LBB0_3:\n" + mfma + ".LBB0_4:\n\ts_endpgm\n"
+    past = "\ts_cbranch_scc0 .LBB0_6\n; %bb.5:\n{}\ts_branch .LBB0_7\n.LBB0_6:\n" + mfma + ".LBB0_7:\n\ts_endpgm\n"
+    chain = "{}\ts_branch .LBB0_9\n.LBB0_8:\n" + 2 * other + ".LBB0_9:\n" + mfma
+    swap = "\tv_swap_b32 v30, v9\n"
+    for text in (loop.format(write), loop.format(swap), jump.format(write), chain.format(write)):
+        with pytest.raises(RuntimeError):
+            build.check_listing("x", text)
+    for text in (loop.format(write + "\ts_nop 1\n"), loop.format(write + 2 * other), loop.format(other),
+                 jump.format(write + 2 * other), jump.format(other), past.format(write), chain.format(other)):
+        build.check_listing("x", text)
+    # each kernel stands for itself
+    build.check_listing("x", "one:\n" + write + "\ts_endpgm\ntwo:\n" + mfma + "\ts_endpgm\n")
+
+
+def test_the_listing_checked_is_that_of_the_object(tmp_path):
+    """The object and its listing come from one compilation."""
+    from block_scaled_fp8_03_amd import build
+    src = tmp_path / "small.hip"
+    src.write_text("#include <hip/hip_runtime.h>\n__global__ void k(int* p) { p[threadIdx.x] += 1; }\n")
+    obj, text = build.compile_listed([build.HIPCC, "--offload-arch=gfx950", "-x", "hip"], str(src), str(tmp_path))
+    assert os.path.exists(obj) and "s_endpgm" in text
+    listing, = [f for f in os.listdir(tmp_path) if f.endswith("gfx950.s")]
+    assert (tmp_path / listing).read_text() == text
