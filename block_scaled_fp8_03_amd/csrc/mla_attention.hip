@@ -41,9 +41,9 @@
 //   128 rows  512 new tokens on 8192, 128 heads: 890 to 960 us, 1.18 to 1.27 PFLOP/s; matrix
 //             cores busy 67% of the cycles, at 1.7 to 2.0 GHz.  1.75 us a step of 32 tokens with
 //             bf16, 1.85 with FP8; the products alone are 1.1 us.
-//   64 rows   32 x 4096 tokens, 128 heads: 66 us with the join, 40 of them the loop, at 3.8 TB/s
+//   64 rows   32 x 4096 tokens, 128 heads: 66 to 71 us with the join, 40 of them the loop, at 3.8 TB/s
 //             with each token read by two tiles
-//   16 rows   128 sequences of up to 8192 tokens, 16 heads, FP8: 98 us, 4.1 TB/s
+//   16 rows   128 sequences of up to 8192 tokens, 16 heads, FP8: 98 to 101 us, 4.1 TB/s
 //   least     one token, 16 heads, 500 cached: 19 us; 12 of them this kernel (plan 2, pages, Q
 //             and tokens 4, a step of 128 tokens 1.7, the four token waves' sum 3.1), the join 5
 #include <algorithm>
@@ -309,9 +309,9 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t&
 // the sequences (row tiles) and over the row tiles (costs).
 // ---------------------------------------------------------------------------
 // It takes about 2 us of each workgroup: the batch's lengths read, two prefix sums, the search.
-// A tile's queries and output, in steps.  Measured with 2 and 4 (24 sequences of up to 2777 tokens, 61
-// new each, us): 16 heads 95.6 / 90.6, 128 heads 419 / 406; with 6 the same.  16 rows' steps are of 128
-// tokens: 91 single tokens on up to 4319, 16 heads 69.2 / 70.8.
+// A tile's queries and output, in steps.  Measured with 2, 4 and 6 (24 sequences of up to 2777 tokens, 61
+// new each, us): 16 heads 88.4 / 89.1 / 93.1, 128 heads 401 / 392 / 394.  16 rows' steps are of 128
+// tokens: 91 single tokens on up to 4319, 16 heads, with 2 and 4 69.4 / 70.9.
 template <int M>
 constexpr int start_cost() { return M == 16 ? 2 : 4; }
 // A share is no smaller, so that short work is not cut to pieces: 128 cached tokens with 128 rows a
@@ -320,7 +320,7 @@ template <int M>
 constexpr int least() { return M == 128 ? 4 : M == 64 ? 2 : 1; }
 // A cut this near a tile's edge moves to it: a split costs the writing and
 // reading of M rows of float32 twice, about M / 16 steps' time.  (Twice as near loses more
-// balance than it saves: the 16 heads above 89.5 / 102.)
+// balance than it saves: the 16 heads above 89 / 103.)
 template <int M>
 __device__ __forceinline__ int slack(int64_t total, int shares) { return (int)min((int64_t)(M / 16), total / shares / 2); }
 
@@ -352,8 +352,9 @@ struct Plan {
     const int r = (int)min((int64_t)(in_seq + 1) * M, (int64_t)s.nq * p.H) - 1;
     return (visible(p, s, r / p.H) + STEP - 1) / STEP;
   }
-  // A short chunk's tiles all cost what its last does (at most an eighth more than
-  // they take): equal costs, and cuts fall on the tiles' edges where their number allows.
+  // A short chunk's tiles all cost what its last does (at most a seventh more than they
+  // take, and a step: its first token sees over 7/8 of the sequence): equal costs, and cuts
+  // fall on the tiles' edges where their number allows.
   static __device__ int tile_cost(const AttnParams& p, const Seq& s, int in_seq) {
     return start_cost<M>() + (s.nq <= s.len / 8 ? (s.len + STEP - 1) / STEP : tile_steps(p, s, in_seq));
   }
@@ -804,7 +805,11 @@ mla_attention_kernel(AttnParams p) {
     return true;
   };
   // Scores to probabilities in kSoft pieces that fit beside a matrix instruction: the maximum of four
-  // scores; the check of it; one probability; eight of them packed
+  // scores; the check of it; one probability; eight of them packed.
+  // The probabilities are rounded to bf16 (half a step, 2^-8 of each, with its own sign): the product takes both
+  // operands in 16 bits, and a second product with what the rounding left would lengthen the matrix-bound
+  // loop by nearly half.  It is the largest error here: relative to 64 bits, 0.0017 to 0.0022 with a bf16
+  // output, which alone is 0.0017.  The sum l has them unrounded, in float32.
   constexpr int NS = Scores<ROWS>::N, kSoft = NS / 4 + 1 + NS + NS / 8;
   float top = 0.0f;
   auto soft = [&](auto i) {
@@ -1073,7 +1078,8 @@ mla_attention_kernel(AttnParams p) {
 // wave; of one in many, the eight waves share the parts of kRunMany groups and
 // meet in LDS, so that one tile in 128 parts and 128 tiles in two keep the card
 // busy alike.  Measured: two tiles of 128 rows in 128 parts each (67 MB) 15 us, 4.5
-// TB/s; 90 such tiles in 3 or 4 (79 MB) 19 us; nothing to join 5 us.
+// TB/s; such tiles in two to four parts (24 sequences of up to 61 new tokens, 16 heads, 70 MB) 18
+// us; nothing to join 5 us.
 constexpr int kGrid = 256;    // shares: the MI355X's CUs
 constexpr int kJoin = 1024;   // workgroups of eight waves
 constexpr int kFew = 16, kRun = 8, kRunMany = 2;
@@ -1189,11 +1195,14 @@ __global__ void __launch_bounds__(512) join_kernel(AttnParams p, int RW) {
 // graph of calls, bf16 / fp8; 128-row tiles: 1.75 / 1.85 us a unit when the matrix
 // cores bound it).  It takes the table's width for the sequences' length, and
 // when the new tokens cannot be shared out evenly half a tile a sequence as lost.
-// Measured both ways (us, bf16): 32 x 4096, 128 heads: 64 rows 76, 128 rows 81; 128
-// new tokens on 8192, 128 heads: 313 / 265; 32 x 4096, 16 heads: 16 rows 52, 64
-// rows 55, 128 rows 72; 16 new tokens each on 4 x 2000, 16 heads: 16 rows 37, 64
-// rows 45; 1 to 8 new each on 64 x up to 4000, 16 heads: 64 rows 85, 128 rows 102; fp8,
-// 128 x 4096, 32 heads: 32 rows 118, 16 rows 131.
+// Measured with 16 / 32 / 64 / 128 rows (us, bf16): 32 x 4096, 128 heads 98 / 84 / 69 / 79; 128
+// new tokens on 8192, 128 heads 514 / 398 / 313 / 267; 32 x 4096, 16 heads 48 / 50 / 52 / 70;
+// 16 new tokens each on 4 x 2000, 16 heads 34 / 37 / 41 / 52; 1 to 8 new each on 64 x up to
+// 4000, 16 heads 114 / 87 / 80 / 96; fp8, 2 x 100000, 128 heads 164 / 154 / 98 / 91; fp8,
+// 128 x 4096, 32 heads 118 / 119 / 132 / 170.
+// A table much wider than its sequences makes short ones pay for larger tiles and the join
+// (own width / 131,072 tokens): 32 x 500, 128 heads 24 / 43; 8 x 1000 27 / 39; 4 x 30 13 / 24;
+// 32 x 4096 71 / 76; 16 heads the same both ways.
 struct TileCost {
   int m;
   float start[2], unit[2];   // bf16, fp8
@@ -1283,7 +1292,7 @@ hipError_t launch_mla_attention(const MlaAttention& a, hipStream_t stream) {
       else FP8BS_ATTN(16, 1, 4, false);
   }
   // A table no wider than a step of the plan: tiles are one step, none is split.  (One token, 16 heads, 100
-  // cached, us a call from a graph: 13.0, with the join's launch 14.9.)
+  // cached, us a call from a graph: 14.0, with the join's launch 16.0.)
   if (a.W * a.ps <= kTok * (m == 16 ? 4 : m == 32 ? 2 : 1)) return hipGetLastError();
   // no more workgroups than the split tiles can have items
   const int64_t items = std::min((int64_t)kGrid, a.T * a.H / m + a.B) * (2 * m / kRunMany);

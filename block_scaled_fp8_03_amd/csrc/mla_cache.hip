@@ -29,8 +29,8 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v,
 // channels a lane), rotates the shared key and stores both; the other waves
 // rotate the heads' query parts, 16 bytes a lane.  All lanes of a wave share
 // the token, so its sequence is found 64 boundaries at a time.  HBM-bound:
-// 4096 tokens of 128 heads into an FP8 cache (57 MB) in 12.9 us, 4.4 TB/s of the
-// 4.9 that a copy reaches; 32 tokens 5.4 us, a launch and four dependent reads
+// 4096 tokens of 128 heads into an FP8 cache (57 MB) in 13.1 us, 4.4 TB/s of the
+// 4.9 that a copy reaches; 32 tokens 5.2 us, a launch and four dependent reads
 // (boundaries, length, page, data).  The norm and the rotation are float32
 // throughout; what is stored is rounded once, to bf16 or e4m3, as the cache's type says.
 // ---------------------------------------------------------------------------
