@@ -11,12 +11,18 @@ the MoE dispatch/combine steps
 ``fp8bs_moe_route``, ``fp8bs_moe_quant_scatter``, ``fp8bs_moe_combine``, the
 absorb attention over a paged latent cache ``fp8bs_mla_attention`` between
 ``fp8bs_mla_absorb_key`` and ``fp8bs_mla_absorb_value``, and that cache's
-``fp8bs_mla_cache_write``, ``fp8bs_cache_update``, ``fp8bs_cache_compact``.
+``fp8bs_mla_cache_write``, ``fp8bs_cache_update``, ``fp8bs_cache_compact``, and
+what stands between the FP8 products of a block with experts:
+``fp8bs_rmsnorm``, ``fp8bs_moe_gate``, ``fp8bs_moe_balance``, ``fp8bs_swiglu``
+with their gradients ``fp8bs_rmsnorm_bwd``, ``fp8bs_moe_gate_bwd``,
+``fp8bs_swiglu_bwd`` and ``fp8bs_moe_combine_bwd``.
 Allocating conveniences: ``act_quant``, ``weight_quant``, ``weight_dequant``,
 ``fp8_gemm``, ``moe_gemm``, ``linear``, ``w8a16_gemm``, ``moe_route``,
 ``moe_quant_scatter``, ``moe_combine``, ``mla_absorb_key``, ``mla_absorb_value``,
 ``mla_cache_alloc``, ``mla_cache_write``, ``mla_attention``, ``cache_update``,
-``cache_compact``.
+``cache_compact``, ``rmsnorm``, ``rmsnorm_quant``, ``rmsnorm_bwd``, ``moe_gate``,
+``moe_balance``, ``moe_gate_bwd``, ``swiglu``, ``swiglu_quant``, ``swiglu_bwd``,
+``moe_combine_bwd``.
 
 The operations follow the DeepSeek-V3 inference pages ("DeepSeek-V3
 Administrator & Developer Guide", sections 6.3, 6.4, 8.5.1-8.5.3; "DeepSeek-V3
@@ -40,13 +46,18 @@ __all__ = [
     "mla_absorb_value", "act_quant", "weight_quant", "weight_dequant", "fp8_gemm", "moe_gemm", "linear", "moe_route",
     "moe_quant_scatter", "moe_combine", "MlaCache", "mla_cache_alloc", "fp8bs_mla_cache_write", "mla_cache_write",
     "fp8bs_mla_attention", "mla_attention", "fp8bs_cache_update", "cache_update", "fp8bs_cache_compact",
-    "cache_compact",
+    "cache_compact", "SCORE_SIGMOID", "SCORE_SOFTMAX", "fp8bs_rmsnorm", "rmsnorm", "rmsnorm_quant",
+    "fp8bs_rmsnorm_bwd", "rmsnorm_bwd", "fp8bs_moe_gate", "moe_gate", "fp8bs_moe_balance", "moe_balance",
+    "fp8bs_moe_gate_bwd", "moe_gate_bwd", "fp8bs_swiglu", "swiglu", "swiglu_quant", "fp8bs_swiglu_bwd", "swiglu_bwd",
+    "fp8bs_moe_combine_bwd", "moe_combine_bwd",
 ]
 
 SCALE_FP32 = 0
 SCALE_UE8M0 = 1
 OUT_BF16 = 0
 OUT_F32 = 1
+SCORE_SIGMOID = 0
+SCORE_SOFTMAX = 1
 CACHE_BF16 = 0
 CACHE_FP8 = 1
 BLOCK = 128
@@ -99,6 +110,16 @@ def lib() -> ctypes.CDLL:
     F = ctypes.c_float
     L.fp8bs_mla_cache_write.argtypes = [P, I64, I64, P, I64, P, I, F, P, I64, P, P, P, P, I, P, P, P,
                                         I64, I64, I64, I64, I64, I64, I64, I64, P]
+    L.fp8bs_rmsnorm.argtypes = [P, I64, P, P, I, P, I, F, P, P, P, I, I64, I64, P]
+    L.fp8bs_rmsnorm_bwd_workspace_size.argtypes = [I64, I64]
+    L.fp8bs_rmsnorm_bwd.argtypes = [P, P, I64, I, P, I, F, P, P, P, I64, I64, P, I64, P]
+    L.fp8bs_moe_gate.argtypes = [P, I64, I, P, I64, I64, I64, I64, I64, I, I, F, P, P, P]
+    L.fp8bs_moe_balance_workspace_size.argtypes = [I64, I64, I64]
+    L.fp8bs_moe_balance.argtypes = [P, I64, I, P, P, I64, I64, I64, I64, I, P, P, P, P, I64, P]
+    L.fp8bs_moe_gate_bwd.argtypes = [P, I64, I, P, P, I, I, F, P, P, P, I64, I64, I64, I64, P, I, P]
+    L.fp8bs_swiglu.argtypes = [P, I64, P, I64, P, P, P, P, I, I64, I64, P]
+    L.fp8bs_swiglu_bwd.argtypes = [P, P, I64, P, I64, P, P, I64, P, I64, I64, I64, P]
+    L.fp8bs_moe_combine_bwd.argtypes = [P, I, P, P, P, P, P, I64, I64, I64, I64, P]
     L.fp8bs_mla_attention_workspace_size.argtypes = [I64, I64, I64]
     L.fp8bs_mla_attention.argtypes = [P, I64, I64, P, I64, I64, P, P, P, I, P, P, P, F, I, P, I, P,
                                       I64, I64, I64, I64, I64, I64, I64, I64, P, I64, P]
@@ -107,13 +128,16 @@ def lib() -> ctypes.CDLL:
     L.fp8bs_cache_compact_workspace_size.argtypes = [I64, I64, I64]
     L.fp8bs_cache_compact.argtypes = [P, P, P, I, P, P, P, P, I64, I64, I64, I64, I64, I64, P, I64, P]
     for fn in ("fp8bs_mla_attention_workspace_size", "fp8bs_cache_update_workspace_size",
-               "fp8bs_cache_compact_workspace_size"):
+               "fp8bs_cache_compact_workspace_size", "fp8bs_rmsnorm_bwd_workspace_size",
+               "fp8bs_moe_balance_workspace_size"):
         getattr(L, fn).restype = I64
     for fn in ("fp8bs_mla_cache_write", "fp8bs_mla_attention", "fp8bs_cache_update", "fp8bs_cache_compact",
                "fp8bs_act_quant", "fp8bs_weight_quant", "fp8bs_weight_dequant", "fp8bs_gemm",
                "fp8bs_moe_gemm", "fp8bs_w8a16_gemm", "fp8bs_moe_route", "fp8bs_moe_quant_scatter",
                "fp8bs_moe_combine", "fp8bs_gemm_ue8m0", "fp8bs_weight_quant_ue8m0",
-               "fp8bs_mla_absorb_key", "fp8bs_mla_absorb_value"):
+               "fp8bs_mla_absorb_key", "fp8bs_mla_absorb_value", "fp8bs_rmsnorm", "fp8bs_rmsnorm_bwd",
+               "fp8bs_moe_gate", "fp8bs_moe_balance", "fp8bs_moe_gate_bwd", "fp8bs_swiglu", "fp8bs_swiglu_bwd",
+               "fp8bs_moe_combine_bwd"):
         getattr(L, fn).restype = I
     _lib = L
     return L
@@ -553,10 +577,10 @@ def _scratch(workspace: Optional[torch.Tensor], dev):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _call_on(dev, fn: str, *args) -> None:
-    """fn(*args, the current stream of device `dev`), with that device current."""
+def _call_on(dev, fn: str, *args, first: str = "cache.latent") -> None:
+    """fn(*args, the current stream of device `dev`, that of the tensor `first`), with that device current."""
     if dev.type != "cuda":
-        raise ValueError("cache.latent must be a device tensor")
+        raise ValueError(f"{first} must be a device tensor")
     stream = _raw_stream(dev.index)
     if torch.cuda.current_device() == dev.index:
         _call(fn, *args, stream)
@@ -711,3 +735,296 @@ def cache_compact(cache: MlaCache, table, lens):
     ws = new_empty((need + 3) // 4) if need else None
     fp8bs_cache_compact(cache, table, lens, table_out, count, ws)
     return table_out, count
+
+
+# ------------------------------------------- what stands between the products
+
+_FLOATS = (torch.bfloat16, torch.float32)
+_COUNT = (torch.Size([]), torch.Size([1]))
+
+
+def _rows2(t: torch.Tensor, name: str, dtypes, shape, dev):
+    """A [M, width] view with a dense last dimension: (pointer, row stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.device != dev:
+        raise ValueError(f"{name} lies on {t.device}, other tensors on {dev}")
+    M, width = shape
+    sm, sw = t.stride()
+    if sw != 1 and M > 0 and width > 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return t.data_ptr(), (sm if M > 1 else 0)
+
+
+def _opt(t: Optional[torch.Tensor], name: str, dtypes, shape, dev) -> Optional[int]:
+    return None if t is None else _ptr(t, name, dtypes, shape, dev)
+
+
+def _count(n_rows: Optional[torch.Tensor], dev) -> Optional[int]:
+    """The address of a count of rows on the device: one int32."""
+    if n_rows is None:
+        return None
+    if isinstance(n_rows, torch.Tensor) and n_rows.shape not in _COUNT:
+        raise ValueError("n_rows must hold one value")
+    return _ptr(n_rows, "n_rows", _I32, getattr(n_rows, "shape", None), dev)
+
+
+def _score(score) -> int:
+    if score in (SCORE_SIGMOID, "sigmoid"):
+        return SCORE_SIGMOID
+    if score in (SCORE_SOFTMAX, "softmax"):
+        return SCORE_SOFTMAX
+    raise ValueError(f"unknown score {score!r}")
+
+
+def _shape2(t, message: str, name: str):
+    """The two sizes of a 2-D tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise _misfit(message, **{name: t})
+    return t.shape
+
+
+def fp8bs_rmsnorm(x: torch.Tensor, res: Optional[torch.Tensor], res_out: Optional[torch.Tensor], norm_w: torch.Tensor,
+                  eps: float, y: Optional[torch.Tensor], q: Optional[torch.Tensor], s: Optional[torch.Tensor],
+                  scale_fmt=SCALE_FP32) -> None:
+    """RMSNorm of x + res: x bf16 [M, K] (row stride free), res [M, K] bf16 or
+    float32 or None, the sum into res_out (res itself if you like), the norm
+    times norm_w [K] (bf16 or float32) into y bf16 [M, K] and / or as codes q
+    e4m3 [M, K] with scales s float32 [M, K/128]."""
+    M, K = _shape2(x, "x must be [M, K]", "x")
+    dev = x.device
+    xp, ld = _rows2(x, "x", _BF16, (M, K), dev)
+    res_type = _BF16 if res is None else (res.dtype,) if getattr(res, "dtype", None) in _FLOATS else _FLOATS
+    _call_on(dev, "fp8bs_rmsnorm", xp, ld, _opt(res, "res", res_type, (M, K), dev),
+             _opt(res_out, "res_out", res_type, (M, K), dev), OUT_F32 if res_type == _F32 else OUT_BF16,
+             _ptr(norm_w, "norm_w", _FLOATS, (K,), dev), norm_w.dtype == torch.float32, eps,
+             _opt(y, "y", _BF16, (M, K), dev), _opt(q, "q", _F8, (M, K), dev),
+             _opt(s, "s", _F32, (M, K // BLOCK), dev), _fmt(scale_fmt), M, K, first="x")
+
+
+def rmsnorm(x, norm_w, eps: float, residual=None):
+    """fp8bs_rmsnorm: y bf16 [M, K]; with a residual (y, x + residual)."""
+    M, K = _shape2(x, "x must be [M, K]", "x")
+    y = x.new_empty((M, K), dtype=torch.bfloat16)
+    h = None if residual is None else torch.empty_like(residual)
+    fp8bs_rmsnorm(x, residual, h, norm_w, eps, y, None, None)
+    return y if residual is None else (y, h)
+
+
+def rmsnorm_quant(x, norm_w, eps: float, residual=None, scale_fmt="fp32", return_y: bool = False):
+    """fp8bs_rmsnorm: (q e4m3 [M, K], s float32 [M, K/128]), then y bf16 if
+    return_y, then x + residual if there is a residual."""
+    M, K = _shape2(x, "x must be [M, K]", "x")
+    q = x.new_empty((M, K), dtype=torch.float8_e4m3fn)
+    s = x.new_empty((M, K // BLOCK), dtype=torch.float32)
+    y = x.new_empty((M, K), dtype=torch.bfloat16) if return_y else None
+    h = None if residual is None else torch.empty_like(residual)
+    fp8bs_rmsnorm(x, residual, h, norm_w, eps, y, q, s, scale_fmt)
+    return tuple(t for t in (q, s, y, h) if t is not None)
+
+
+def fp8bs_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, norm_w: torch.Tensor, eps: float,
+                      dres: Optional[torch.Tensor], dx: torch.Tensor, dw: Optional[torch.Tensor],
+                      workspace: Optional[torch.Tensor]) -> None:
+    """The norm's gradient: dy bf16 [M, K], h [M, K] what was normalised (bf16 or
+    float32, row stride free), dres [M, K] of h's type or None, added to dx [M, K]
+    of h's type (dx itself if you like); dw float32 [K] or None."""
+    M, K = _shape2(h, "h must be [M, K]", "h")
+    dev = h.device
+    hp, ld = _rows2(h, "h", _FLOATS, (M, K), dev)
+    like = (h.dtype,)
+    ws, nbytes = _scratch(workspace, dev)
+    _call_on(dev, "fp8bs_rmsnorm_bwd", _ptr(dy, "dy", _BF16, (M, K), dev), hp, ld, _out_code(h),
+             _ptr(norm_w, "norm_w", _FLOATS, (K,), dev), norm_w.dtype == torch.float32, eps,
+             _opt(dres, "dres", like, (M, K), dev), _ptr(dx, "dx", like, (M, K), dev),
+             _opt(dw, "dw", _F32, (K,), dev), M, K, ws, nbytes, first="h")
+
+
+def rmsnorm_bwd(dy, h, norm_w, eps: float, dres=None):
+    """fp8bs_rmsnorm_bwd: (dx [M, K] of h's type, dw float32 [K])."""
+    M, K = _shape2(h, "h must be [M, K]", "h")
+    need = lib().fp8bs_rmsnorm_bwd_workspace_size(M, K)
+    if need < 0:
+        raise ValueError("sizes out of range")
+    dx = h.new_empty((M, K))
+    dw = h.new_empty(K, dtype=torch.float32)
+    ws = h.new_empty(need, dtype=torch.uint8) if need else None
+    fp8bs_rmsnorm_bwd(dy, h, norm_w, eps, dres, dx, dw, ws)
+    return dx, dw
+
+
+def fp8bs_moe_gate(logits: torch.Tensor, bias: Optional[torch.Tensor], groups: int, topk_groups: int, score,
+                   normalize: bool, route_scale: float, indices: torch.Tensor, weights: torch.Tensor) -> None:
+    """The gate: logits [T, E] (bf16 or float32, row stride free) -> indices
+    int32 [T, topk] (-1 where no expert is left) and weights float32 [T, topk]."""
+    T, E = _shape2(logits, "logits must be [T, E]", "logits")
+    topk = _shape2(indices, "indices must be [T, topk]", "indices")[1]
+    dev = logits.device
+    zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
+    _call_on(dev, "fp8bs_moe_gate", zp, ld, _out_code(logits), _opt(bias, "bias", _F32, (E,), dev), T, E, topk, groups,
+             topk_groups, _score(score), normalize, route_scale, _ptr(indices, "indices", _I32, (T, topk), dev),
+             _ptr(weights, "weights", _F32, (T, topk), dev), first="logits")
+
+
+def moe_gate(logits, topk: int, bias=None, groups: int = 1, topk_groups: Optional[int] = None, score="sigmoid",
+             normalize: bool = True, route_scale: float = 1.0):
+    """fp8bs_moe_gate: (indices int32 [T, topk], weights float32 [T, topk]), for
+    moe_route and moe_combine.  All groups are kept unless topk_groups says so."""
+    T, _ = _shape2(logits, "logits must be [T, E]", "logits")
+    indices = logits.new_empty((T, topk), dtype=torch.int32)
+    weights = logits.new_empty((T, topk), dtype=torch.float32)
+    fp8bs_moe_gate(logits, bias, groups, groups if topk_groups is None else topk_groups, score, normalize, route_scale,
+                   indices, weights)
+    return indices, weights
+
+
+def _sequences(cu_seq: Optional[torch.Tensor], dev):
+    """(pointer, sequences) of boundaries [S + 1]; one sequence without them."""
+    if cu_seq is None:
+        return None, 1
+    if not isinstance(cu_seq, torch.Tensor) or cu_seq.dim() != 1 or cu_seq.shape[0] < 1:
+        raise _misfit("cu_seq must be [S + 1]", cu_seq=cu_seq)
+    return _ptr(cu_seq, "cu_seq", _I32, cu_seq.shape, dev), cu_seq.shape[0] - 1
+
+
+def fp8bs_moe_balance(logits: torch.Tensor, indices: torch.Tensor, cu_seq: Optional[torch.Tensor], score,
+                      counts: torch.Tensor, probs: torch.Tensor, loss: torch.Tensor,
+                      workspace: Optional[torch.Tensor]) -> None:
+    """Of each sequence (cu_seq int32 [S + 1]; None: one of all tokens): counts
+    int32 [S, E] of the gate's indices [T, topk], probs float32 [S, E] the mean
+    share of the token's scores, loss float32 [S]."""
+    T, E = _shape2(logits, "logits must be [T, E]", "logits")
+    topk = _shape2(indices, "indices must be [T, topk]", "indices")[1]
+    dev = logits.device
+    zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
+    cu, S = _sequences(cu_seq, dev)
+    ws, nbytes = _scratch(workspace, dev)
+    _call_on(dev, "fp8bs_moe_balance", zp, ld, _out_code(logits), _ptr(indices, "indices", _I32, (T, topk), dev), cu,
+             T, S, E, topk, _score(score), _ptr(counts, "counts", _I32, (S, E), dev),
+             _ptr(probs, "probs", _F32, (S, E), dev), _ptr(loss, "loss", _F32, (S,), dev), ws, nbytes, first="logits")
+
+
+def moe_balance(logits, indices, cu_seq=None, score="sigmoid"):
+    """fp8bs_moe_balance: (loss float32 [S], counts int32 [S, E], probs float32 [S, E])."""
+    T, E = _shape2(logits, "logits must be [T, E]", "logits")
+    S = _sequences(cu_seq, logits.device)[1]
+    need = lib().fp8bs_moe_balance_workspace_size(T, S, E)
+    if need < 0:
+        raise ValueError("sizes out of range")
+    counts = logits.new_empty((S, E), dtype=torch.int32)
+    probs = logits.new_empty((S, E), dtype=torch.float32)
+    loss = logits.new_empty(S, dtype=torch.float32)
+    ws = logits.new_empty(need, dtype=torch.uint8) if need else None
+    fp8bs_moe_balance(logits, indices, cu_seq, score, counts, probs, loss, ws)
+    return loss, counts, probs
+
+
+def fp8bs_moe_gate_bwd(logits: torch.Tensor, indices: torch.Tensor, d_weights: Optional[torch.Tensor], score,
+                       normalize: bool, route_scale: float, cu_seq: Optional[torch.Tensor],
+                       counts: Optional[torch.Tensor], d_loss: Optional[torch.Tensor], d_logits: torch.Tensor) -> None:
+    """The gradient by the logits of the gate's weights (d_weights float32 [T,
+    topk] or None) and of the balance losses (d_loss float32 [S] with their
+    counts, or None): d_logits [T, E] bf16 or float32."""
+    T, E = _shape2(logits, "logits must be [T, E]", "logits")
+    topk = _shape2(indices, "indices must be [T, topk]", "indices")[1]
+    dev = logits.device
+    zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
+    cu, S = _sequences(cu_seq, dev)
+    _call_on(dev, "fp8bs_moe_gate_bwd", zp, ld, _out_code(logits), _ptr(indices, "indices", _I32, (T, topk), dev),
+             _opt(d_weights, "d_weights", _F32, (T, topk), dev), _score(score), normalize, route_scale, cu,
+             _opt(counts, "counts", _I32, (S, E), dev), _opt(d_loss, "d_loss", _F32, (S,), dev), T, S, E, topk,
+             _ptr(d_logits, "d_logits", _FLOATS, (T, E), dev), _out_code(d_logits), first="logits")
+
+
+def moe_gate_bwd(logits, indices, d_weights=None, score="sigmoid", normalize: bool = True, route_scale: float = 1.0,
+                 cu_seq=None, counts=None, d_loss=None, out_dtype=torch.float32) -> torch.Tensor:
+    """fp8bs_moe_gate_bwd: d_logits [T, E]."""
+    T, E = _shape2(logits, "logits must be [T, E]", "logits")
+    d_logits = logits.new_empty((T, E), dtype=out_dtype)
+    fp8bs_moe_gate_bwd(logits, indices, d_weights, score, normalize, route_scale, cu_seq, counts, d_loss, d_logits)
+    return d_logits
+
+
+def fp8bs_swiglu(gate: torch.Tensor, up: torch.Tensor, y: Optional[torch.Tensor], q: Optional[torch.Tensor],
+                 s: Optional[torch.Tensor], scale_fmt=SCALE_FP32, n_rows: Optional[torch.Tensor] = None) -> None:
+    """silu(gate) * up, both bf16 [M, N] (row strides free, e.g. the halves of one
+    product's output), into y bf16 [M, N] and / or as codes q e4m3 [M, N] with
+    scales s float32 [M, N/128].  Rows from n_rows (one int32 on the device, e.g.
+    offsets[-1:] of moe_route) on are left alone."""
+    M, N = _shape2(gate, "gate must be [M, N]", "gate")
+    dev = gate.device
+    gp, ldg = _rows2(gate, "gate", _BF16, (M, N), dev)
+    up_, ldu = _rows2(up, "up", _BF16, (M, N), dev)
+    _call_on(dev, "fp8bs_swiglu", gp, ldg, up_, ldu, _count(n_rows, dev), _opt(y, "y", _BF16, (M, N), dev),
+             _opt(q, "q", _F8, (M, N), dev), _opt(s, "s", _F32, (M, N // BLOCK), dev), _fmt(scale_fmt), M, N,
+             first="gate")
+
+
+def swiglu(gate, up, n_rows=None) -> torch.Tensor:
+    """fp8bs_swiglu: bf16 [M, N], not initialised from row n_rows on."""
+    M, N = _shape2(gate, "gate must be [M, N]", "gate")
+    y = gate.new_empty((M, N))
+    fp8bs_swiglu(gate, up, y, None, None, n_rows=n_rows)
+    return y
+
+
+def swiglu_quant(gate, up, scale_fmt="fp32", n_rows=None, return_y: bool = False):
+    """fp8bs_swiglu: (q e4m3 [M, N], s float32 [M, N/128]), then y bf16 if
+    return_y; not initialised from row n_rows on."""
+    M, N = _shape2(gate, "gate must be [M, N]", "gate")
+    q = gate.new_empty((M, N), dtype=torch.float8_e4m3fn)
+    s = gate.new_empty((M, N // BLOCK), dtype=torch.float32)
+    y = gate.new_empty((M, N)) if return_y else None
+    fp8bs_swiglu(gate, up, y, q, s, scale_fmt, n_rows)
+    return (q, s, y) if return_y else (q, s)
+
+
+def fp8bs_swiglu_bwd(dy: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, dgate: torch.Tensor, dup: torch.Tensor,
+                     n_rows: Optional[torch.Tensor] = None) -> None:
+    """The gradient of fp8bs_swiglu: dy bf16 [M, N] -> dgate, dup bf16 [M, N] (row
+    strides free, e.g. the halves of one tensor); rows from n_rows on are left alone."""
+    M, N = _shape2(gate, "gate must be [M, N]", "gate")
+    dev = gate.device
+    gp, ldg = _rows2(gate, "gate", _BF16, (M, N), dev)
+    up_, ldu = _rows2(up, "up", _BF16, (M, N), dev)
+    dgp, lddg = _rows2(dgate, "dgate", _BF16, (M, N), dev)
+    dup_, lddu = _rows2(dup, "dup", _BF16, (M, N), dev)
+    _call_on(dev, "fp8bs_swiglu_bwd", _ptr(dy, "dy", _BF16, (M, N), dev), gp, ldg, up_, ldu, _count(n_rows, dev), dgp,
+             lddg, dup_, lddu, M, N, first="gate")
+
+
+def swiglu_bwd(dy, gate, up, n_rows=None):
+    """fp8bs_swiglu_bwd: (dgate, dup) bf16 [M, N], the halves of one [M, 2N]
+    tensor; not initialised from row n_rows on."""
+    M, N = _shape2(gate, "gate must be [M, N]", "gate")
+    d = gate.new_empty((M, 2 * N))
+    dgate, dup = d[:, :N], d[:, N:]
+    fp8bs_swiglu_bwd(dy, gate, up, dgate, dup, n_rows)
+    return dgate, dup
+
+
+def fp8bs_moe_combine_bwd(dy: torch.Tensor, out: torch.Tensor, w: torch.Tensor, row_of: torch.Tensor,
+                          d_out: torch.Tensor, d_w: torch.Tensor) -> None:
+    """The gradient of fp8bs_moe_combine: dy [T, N] bf16 or float32 -> d_out bf16
+    [R, N] (rows without a pair untouched) and d_w float32 [T, topk]."""
+    R, N = _shape2(out, "out must be [R, N]", "out")
+    T, topk = _shape2(w, "w must be [T, topk]", "w")
+    dev = out.device
+    _call_on(dev, "fp8bs_moe_combine_bwd", _ptr(dy, "dy", _FLOATS, (T, N), dev), _out_code(dy),
+             _ptr(out, "out", _BF16, (R, N), dev), _ptr(w, "w", _F32, (T, topk), dev),
+             _ptr(row_of, "row_of", _I32, (T, topk), dev), _ptr(d_out, "d_out", _BF16, (R, N), dev),
+             _ptr(d_w, "d_w", _F32, (T, topk), dev), T, topk, R, N, first="out")
+
+
+def moe_combine_bwd(dy, out, w, row_of):
+    """fp8bs_moe_combine_bwd: (d_out bf16 [R, N], d_w float32 [T, topk]); rows
+    of d_out that no pair maps to are not initialised."""
+    R, N = _shape2(out, "out must be [R, N]", "out")
+    T, topk = _shape2(w, "w must be [T, topk]", "w")
+    d_out, d_w = out.new_empty((R, N)), w.new_empty((T, topk))
+    fp8bs_moe_combine_bwd(dy, out, w, row_of, d_out, d_w)
+    return d_out, d_w

@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfp8bs.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["quant.hip", "gemm.hip", "gemm_e8.hip", "moe_dispatch.hip", "mla.hip",
+SOURCES = ["quant.hip", "gemm.hip", "gemm_e8.hip", "moe_dispatch.hip", "norm.hip", "gate.hip",
+           "swiglu.hip", "mla.hip",
            "mla_attention.hip", "mla_cache.hip", "abi.cpp"]
 
 COMMON_FLAGS = [

@@ -46,7 +46,7 @@ const char* fp8bs_status_string(int status) {
     case FP8BS_ERR_NULL: return "a required pointer is NULL";
     case FP8BS_ERR_SHAPE: return "invalid shape (negative size, K not a multiple of 128, or size limit exceeded)";
     case FP8BS_ERR_ALIGN: return "a pointer is not aligned as required (16 bytes for tensors, 4 for scales)";
-    case FP8BS_ERR_ENUM: return "unknown scale_fmt or out_dtype";
+    case FP8BS_ERR_ENUM: return "unknown scale_fmt, out_dtype or score";
     case FP8BS_ERR_HIP: return "HIP kernel launch failed";
     case FP8BS_ERR_ALIAS: return "an output buffer overlaps an input buffer";
     default: return "unknown status";
@@ -544,6 +544,241 @@ int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fm
   const fp8bs::PageTask a{latent, rope, lat_scale, table, lens, nullptr, nullptr, table_out, nullptr, count,
                           workspace, B, W, 0, P, ps, cache_fmt == FP8BS_CACHE_FP8};
   return status_of(fp8bs::launch_cache_compact(a, (hipStream_t)stream));
+}
+
+}  // extern "C"
+
+// ---- an expert block's operators: norm, gate, balance, activation, the combine's gradient
+
+namespace {
+
+// an argument's bytes; one that is NULL or empty meets nothing
+struct Span {
+  const void* p;
+  int64_t n;
+};
+bool meet(const Span& a, const Span& b) { return a.p && b.p && overlap(a.p, a.n, b.p, b.n); }
+// an output meets an input or another output
+template <int NO, int NI>
+bool clash(const Span (&outs)[NO], const Span (&ins)[NI]) {
+  for (int o = 0; o < NO; ++o) {
+    for (int i = 0; i < NI; ++i)
+      if (meet(outs[o], ins[i])) return true;
+    for (int q = o + 1; q < NO; ++q)
+      if (meet(outs[o], outs[q])) return true;
+  }
+  return false;
+}
+bool dtype_ok(int d) { return d == FP8BS_OUT_BF16 || d == FP8BS_OUT_F32; }
+int64_t size_of(int d) { return d == FP8BS_OUT_F32 ? 4 : 2; }
+bool score_ok(int s) { return s == FP8BS_SCORE_SIGMOID || s == FP8BS_SCORE_SOFTMAX; }
+bool eps_ok(float eps) { return eps >= 0.0f && eps <= 3.0e38f; }
+
+// what the gate's entry points share: sizes of [T, E] logits with row stride ld and [T, topk] slots
+int gate_sizes(int64_t T, int64_t E, int64_t topk, int64_t ld, int logits_dtype, int score) {
+  if (T < 0 || T > kLimitRows || E < 1 || E > 1024 || topk < 1 || topk > 64 || topk > E || ld < 0 ||
+      T * topk > kLimitInt || (T > 0 && extent(T, 1, ld, 0, E) < 0))
+    return FP8BS_ERR_SHAPE;
+  return dtype_ok(logits_dtype) && score_ok(score) ? FP8BS_OK : FP8BS_ERR_ENUM;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8bs_rmsnorm(const void* x_bf16, int64_t ld_x, const void* res, void* res_out, int res_dtype,
+                  const void* norm_w, int norm_w_f32, float eps, void* y_bf16, void* q_e4m3, float* s,
+                  int scale_fmt, int64_t M, int64_t K, void* stream) {
+  if (M < 0 || K < 0 || K % 128 != 0 || ld_x < 0 || !eps_ok(eps) || !fp8bs::rmsnorm_fits(M, K)) return FP8BS_ERR_SHAPE;
+  if (!dtype_ok(res_dtype) || (scale_fmt != FP8BS_SCALE_FP32 && scale_fmt != FP8BS_SCALE_UE8M0)) return FP8BS_ERR_ENUM;
+  if (M == 0 || K == 0) return FP8BS_OK;
+  if (ld_x % 8 != 0) return FP8BS_ERR_ALIGN;
+  if (!x_bf16 || !norm_w || (!res) != (!res_out) || (!q_e4m3) != (!s) || (!y_bf16 && !q_e4m3)) return FP8BS_ERR_NULL;
+  if (!aligned(x_bf16, 16) || !aligned(res, 16) || !aligned(res_out, 16) || !aligned(norm_w, 16) ||
+      !aligned(y_bf16, 16) || !aligned(q_e4m3, 16) || !aligned(s, 4))
+    return FP8BS_ERR_ALIGN;
+  const int64_t ex = extent(M, 1, ld_x, 0, K), n = M * K, rb = n * size_of(res_dtype);
+  if (ex < 0) return FP8BS_ERR_SHAPE;
+  const bool in_place = res == res_out;                      // each element is read before it is written
+  const Span outs[] = {{res_out, rb}, {y_bf16, 2 * n}, {q_e4m3, n}, {s, n / 32}};
+  const Span ins[] = {{x_bf16, 2 * ex}, {in_place ? nullptr : res, rb}, {norm_w, K * (norm_w_f32 ? 4 : 2)}};
+  if (clash(outs, ins)) return FP8BS_ERR_ALIAS;
+  const fp8bs::RmsNorm a{x_bf16, res, norm_w, res_out, y_bf16, q_e4m3, s, ld_x, M, K, eps,
+                         res_dtype == FP8BS_OUT_F32, norm_w_f32 != 0, scale_fmt == FP8BS_SCALE_UE8M0};
+  return status_of(fp8bs::launch_rmsnorm(a, (hipStream_t)stream));
+}
+
+int64_t fp8bs_rmsnorm_bwd_workspace_size(int64_t M, int64_t K) {
+  if (M < 0 || K < 0 || K % 128 != 0 || !fp8bs::rmsnorm_fits(M, K)) return -1;
+  return M == 0 || K == 0 ? 0 : fp8bs::rmsnorm_bwd_workspace_bytes(M, K);
+}
+
+int fp8bs_rmsnorm_bwd(const void* dy_bf16, const void* h, int64_t ld_h, int h_dtype, const void* norm_w,
+                      int norm_w_f32, float eps, const void* dres, void* dx, float* dw, int64_t M, int64_t K,
+                      void* workspace, int64_t workspace_bytes, void* stream) {
+  const int64_t size = fp8bs_rmsnorm_bwd_workspace_size(M, K), need = dw ? size : 0;
+  if (size < 0 || ld_h < 0 || !eps_ok(eps)) return FP8BS_ERR_SHAPE;
+  if (!dtype_ok(h_dtype)) return FP8BS_ERR_ENUM;
+  if (K == 0 || (M == 0 && !dw)) return FP8BS_OK;
+  if (workspace_bytes < need) return FP8BS_ERR_SHAPE;
+  if (ld_h % 8 != 0) return FP8BS_ERR_ALIGN;
+  if (M > 0 && (!dy_bf16 || !h || !norm_w || !dx || (need > 0 && !workspace))) return FP8BS_ERR_NULL;
+  if (!aligned(dy_bf16, 16) || !aligned(h, 16) || !aligned(norm_w, 16) || !aligned(dres, 16) || !aligned(dx, 16) ||
+      !aligned(dw, 16) || !aligned(workspace, 16))
+    return FP8BS_ERR_ALIGN;
+  const int64_t eh = M > 0 ? extent(M, 1, ld_h, 0, K) : 0, n = M * K, hb = size_of(h_dtype);
+  if (eh < 0) return FP8BS_ERR_SHAPE;
+  const Span outs[] = {{dx, n * hb}, {dw, 4 * K}, {workspace, need}};
+  const Span ins[] = {{dy_bf16, 2 * n}, {h, eh * hb}, {norm_w, K * (norm_w_f32 ? 4 : 2)},
+                      {dres == dx ? nullptr : dres, n * hb}};
+  if (clash(outs, ins)) return FP8BS_ERR_ALIAS;
+  const fp8bs::RmsNormBwd a{dy_bf16, h, norm_w, dres, dx, dw, workspace, ld_h, M, K, eps,
+                            h_dtype == FP8BS_OUT_F32, norm_w_f32 != 0};
+  return status_of(fp8bs::launch_rmsnorm_bwd(a, (hipStream_t)stream));
+}
+
+int fp8bs_moe_gate(const void* logits, int64_t ld, int logits_dtype, const float* bias, int64_t T, int64_t E,
+                   int64_t topk, int64_t groups, int64_t topk_groups, int score, int normalize, float route_scale,
+                   int32_t* indices, float* weights, void* stream) {
+  const int st = gate_sizes(T, E, topk, ld, logits_dtype, score);
+  if (st != FP8BS_OK) return st;
+  if (groups < 1 || groups > 64 || E % groups != 0 || topk_groups < 1 || topk_groups > groups || !isfinite(route_scale))
+    return FP8BS_ERR_SHAPE;
+  if (T == 0) return FP8BS_OK;
+  if (!logits || !indices || !weights) return FP8BS_ERR_NULL;
+  if (!aligned(logits, size_of(logits_dtype)) || !aligned(bias, 4) || !aligned(indices, 4) || !aligned(weights, 4))
+    return FP8BS_ERR_ALIGN;
+  const Span outs[] = {{indices, 4 * T * topk}, {weights, 4 * T * topk}};
+  const Span ins[] = {{logits, extent(T, 1, ld, 0, E) * size_of(logits_dtype)}, {bias, 4 * E}};
+  if (clash(outs, ins)) return FP8BS_ERR_ALIAS;
+  const fp8bs::MoeGate a{logits, bias, indices, weights, ld, T, E, topk, groups, topk_groups, route_scale,
+                         logits_dtype == FP8BS_OUT_F32, score == FP8BS_SCORE_SOFTMAX, normalize != 0};
+  return status_of(fp8bs::launch_moe_gate(a, (hipStream_t)stream));
+}
+
+// sequences that a launch has a workgroup of 512 threads for
+static const int64_t kLimitBalance = 1 << 22;
+
+int64_t fp8bs_moe_balance_workspace_size(int64_t T, int64_t S, int64_t E) {
+  if (T < 0 || T > kLimitRows || S < 0 || S > kLimitBalance || E < 1 || E > 1024) return -1;
+  return S == 0 ? 0 : fp8bs::moe_balance_workspace_bytes(T, S, E);
+}
+
+int fp8bs_moe_balance(const void* logits, int64_t ld, int logits_dtype, const int32_t* indices, const int32_t* cu_seq,
+                      int64_t T, int64_t S, int64_t E, int64_t topk, int score, int32_t* counts, float* probs,
+                      float* loss, void* workspace, int64_t workspace_bytes, void* stream) {
+  const int64_t need = fp8bs_moe_balance_workspace_size(T, S, E);
+  const int st = gate_sizes(T, E, topk, ld, logits_dtype, score);
+  if (st != FP8BS_OK) return st;
+  if (need < 0) return FP8BS_ERR_SHAPE;
+  if (S == 0) return FP8BS_OK;
+  if (workspace_bytes < need || (!cu_seq && S != 1)) return FP8BS_ERR_SHAPE;
+  if ((T > 0 && (!logits || !indices)) || !counts || !probs || !loss || (need > 0 && !workspace)) return FP8BS_ERR_NULL;
+  if (!aligned(logits, size_of(logits_dtype)) || !aligned(indices, 4) || !aligned(cu_seq, 4) || !aligned(counts, 4) ||
+      !aligned(probs, 4) || !aligned(loss, 4) || !aligned(workspace, 16))
+    return FP8BS_ERR_ALIGN;
+  const Span outs[] = {{counts, 4 * S * E}, {probs, 4 * S * E}, {loss, 4 * S}, {workspace, need}};
+  const Span ins[] = {{logits, T > 0 ? extent(T, 1, ld, 0, E) * size_of(logits_dtype) : 0}, {indices, 4 * T * topk},
+                      {cu_seq, 4 * (S + 1)}};
+  if (clash(outs, ins)) return FP8BS_ERR_ALIAS;
+  const fp8bs::MoeBalance a{logits, indices, cu_seq, counts, probs, loss, workspace, ld, T, S, E, topk,
+                            logits_dtype == FP8BS_OUT_F32, score == FP8BS_SCORE_SOFTMAX, nullptr, nullptr};
+  return status_of(fp8bs::launch_moe_balance(a, (hipStream_t)stream));
+}
+
+int fp8bs_moe_gate_bwd(const void* logits, int64_t ld, int logits_dtype, const int32_t* indices,
+                       const float* d_weights, int score, int normalize, float route_scale, const int32_t* cu_seq,
+                       const int32_t* counts, const float* d_loss, int64_t T, int64_t S, int64_t E, int64_t topk,
+                       void* d_logits, int out_dtype, void* stream) {
+  const int st = gate_sizes(T, E, topk, ld, logits_dtype, score);
+  if (st != FP8BS_OK) return st;
+  if (S < 0 || S > kLimitBalance || !isfinite(route_scale)) return FP8BS_ERR_SHAPE;
+  if (!dtype_ok(out_dtype)) return FP8BS_ERR_ENUM;
+  if (d_loss && (S == 0 || (!cu_seq && S != 1))) return FP8BS_ERR_SHAPE;
+  if (T == 0) return FP8BS_OK;
+  if (!logits || !d_logits || (d_weights && !indices) || (d_loss && !counts)) return FP8BS_ERR_NULL;
+  if (!aligned(logits, size_of(logits_dtype)) || !aligned(indices, 4) || !aligned(d_weights, 4) ||
+      !aligned(cu_seq, 4) || !aligned(counts, 4) || !aligned(d_loss, 4) || !aligned(d_logits, 16))
+    return FP8BS_ERR_ALIGN;
+  const Span outs[] = {{d_logits, T * E * size_of(out_dtype)}};
+  const Span ins[] = {{logits, extent(T, 1, ld, 0, E) * size_of(logits_dtype)}, {indices, 4 * T * topk},
+                      {d_weights, 4 * T * topk}, {cu_seq, 4 * (S + 1)}, {counts, 4 * S * E}, {d_loss, 4 * S}};
+  if (clash(outs, ins)) return FP8BS_ERR_ALIAS;
+  const fp8bs::MoeGateBwd a{logits, indices, cu_seq, counts, d_weights, d_loss, d_logits, ld, T, S, E, topk,
+                            route_scale, logits_dtype == FP8BS_OUT_F32, score == FP8BS_SCORE_SOFTMAX, normalize != 0,
+                            out_dtype == FP8BS_OUT_F32};
+  return status_of(fp8bs::launch_moe_gate_bwd(a, (hipStream_t)stream));
+}
+
+int fp8bs_swiglu(const void* gate_bf16, int64_t ld_g, const void* up_bf16, int64_t ld_u, const int32_t* n_rows,
+                 void* y_bf16, void* q_e4m3, float* s, int scale_fmt, int64_t M, int64_t N, void* stream) {
+  if (M < 0 || N < 0 || N % 128 != 0 || ld_g < 0 || ld_u < 0 || !fp8bs::swiglu_fits(M, N)) return FP8BS_ERR_SHAPE;
+  if (scale_fmt != FP8BS_SCALE_FP32 && scale_fmt != FP8BS_SCALE_UE8M0) return FP8BS_ERR_ENUM;
+  if (M == 0 || N == 0) return FP8BS_OK;
+  if (ld_g % 8 != 0 || ld_u % 8 != 0) return FP8BS_ERR_ALIGN;
+  if (!gate_bf16 || !up_bf16 || (!q_e4m3) != (!s) || (!y_bf16 && !q_e4m3)) return FP8BS_ERR_NULL;
+  if (!aligned(gate_bf16, 16) || !aligned(up_bf16, 16) || !aligned(n_rows, 4) || !aligned(y_bf16, 16) ||
+      !aligned(q_e4m3, 16) || !aligned(s, 4))
+    return FP8BS_ERR_ALIGN;
+  const int64_t eg = extent(M, 1, ld_g, 0, N), eu = extent(M, 1, ld_u, 0, N), n = M * N;
+  if (eg < 0 || eu < 0) return FP8BS_ERR_SHAPE;
+  const Span outs[] = {{y_bf16, 2 * n}, {q_e4m3, n}, {s, n / 32}};
+  const Span ins[] = {{gate_bf16, 2 * eg}, {up_bf16, 2 * eu}, {n_rows, 4}};
+  if (clash(outs, ins)) return FP8BS_ERR_ALIAS;
+  const fp8bs::SwiGlu a{gate_bf16, up_bf16, n_rows, y_bf16, q_e4m3, s, ld_g, ld_u, M, N,
+                        scale_fmt == FP8BS_SCALE_UE8M0};
+  return status_of(fp8bs::launch_swiglu(a, (hipStream_t)stream));
+}
+
+// two [M, N] outputs of 2-byte elements with row strides ld_a, ld_b share an element: of one stride, they may be
+// columns of the same rows
+static bool columns_meet(const void* a, int64_t ld_a, const void* b, int64_t ld_b, int64_t M, int64_t N) {
+  const Span sa{a, 2 * extent(M, 1, ld_a, 0, N)}, sb{b, 2 * extent(M, 1, ld_b, 0, N)};
+  if (!meet(sa, sb)) return false;
+  if (ld_a != ld_b || M == 1) return true;
+  const int64_t step = 2 * ld_a, off = (((int64_t)((intptr_t)b - (intptr_t)a)) % step + step) % step;
+  return off < 2 * N || off + 2 * N > step;
+}
+
+int fp8bs_swiglu_bwd(const void* dy_bf16, const void* gate_bf16, int64_t ld_g, const void* up_bf16, int64_t ld_u,
+                     const int32_t* n_rows, void* dgate_bf16, int64_t ld_dg, void* dup_bf16, int64_t ld_du,
+                     int64_t M, int64_t N, void* stream) {
+  if (M < 0 || N < 0 || N % 128 != 0 || ld_g < 0 || ld_u < 0 || ld_dg < 0 || ld_du < 0 || !fp8bs::swiglu_fits(M, N) ||
+      (M > 1 && (ld_dg < N || ld_du < N)))
+    return FP8BS_ERR_SHAPE;
+  if (M == 0 || N == 0) return FP8BS_OK;
+  if (ld_g % 8 != 0 || ld_u % 8 != 0 || ld_dg % 8 != 0 || ld_du % 8 != 0) return FP8BS_ERR_ALIGN;
+  if (!dy_bf16 || !gate_bf16 || !up_bf16 || !dgate_bf16 || !dup_bf16) return FP8BS_ERR_NULL;
+  if (!aligned(dy_bf16, 16) || !aligned(gate_bf16, 16) || !aligned(up_bf16, 16) || !aligned(n_rows, 4) ||
+      !aligned(dgate_bf16, 16) || !aligned(dup_bf16, 16))
+    return FP8BS_ERR_ALIGN;
+  const int64_t eg = extent(M, 1, ld_g, 0, N), eu = extent(M, 1, ld_u, 0, N), dg = extent(M, 1, ld_dg, 0, N),
+                du = extent(M, 1, ld_du, 0, N);
+  if (eg < 0 || eu < 0 || dg < 0 || du < 0) return FP8BS_ERR_SHAPE;
+  const Span ins[] = {{dy_bf16, 2 * M * N}, {gate_bf16, 2 * eg}, {up_bf16, 2 * eu}, {n_rows, 4}};
+  const Span a_out[] = {{dgate_bf16, 2 * dg}}, b_out[] = {{dup_bf16, 2 * du}};
+  if (clash(a_out, ins) || clash(b_out, ins) || columns_meet(dgate_bf16, ld_dg, dup_bf16, ld_du, M, N))
+    return FP8BS_ERR_ALIAS;
+  const fp8bs::SwiGluBwd a{dy_bf16, gate_bf16, up_bf16, n_rows, dgate_bf16, dup_bf16, ld_g, ld_u, ld_dg, ld_du, M, N};
+  return status_of(fp8bs::launch_swiglu_bwd(a, (hipStream_t)stream));
+}
+
+int fp8bs_moe_combine_bwd(const void* dy, int dy_dtype, const void* out_bf16, const float* w, const int32_t* row_of,
+                          void* d_out_bf16, float* d_w, int64_t T, int64_t topk, int64_t R, int64_t N, void* stream) {
+  if (T < 0 || T >= (1 << 23) || topk < 1 || R < 0 || R > kLimitInt || N < 0) return FP8BS_ERR_SHAPE;
+  if (!dtype_ok(dy_dtype)) return FP8BS_ERR_ENUM;
+  const int64_t no = mul(R, N), ny = mul(T, N), P = mul(T, topk);
+  if (no < 0 || ny < 0 || P < 0 || P > kLimitInt || mul(no, 2) < 0 || mul(ny, 4) < 0) return FP8BS_ERR_SHAPE;
+  if (T == 0) return FP8BS_OK;
+  if (!w || !row_of || !d_w || (ny > 0 && !dy) || (no > 0 && (!out_bf16 || !d_out_bf16))) return FP8BS_ERR_NULL;
+  if (!aligned(dy, 16) || !aligned(out_bf16, 16) || !aligned(d_out_bf16, 16) || !aligned(w, 4) || !aligned(row_of, 4) ||
+      !aligned(d_w, 4))
+    return FP8BS_ERR_ALIGN;
+  const Span outs[] = {{d_out_bf16, 2 * no}, {d_w, 4 * P}};
+  const Span ins[] = {{dy, ny * size_of(dy_dtype)}, {out_bf16, 2 * no}, {w, 4 * P}, {row_of, 4 * P}};
+  if (clash(outs, ins)) return FP8BS_ERR_ALIAS;
+  return status_of(fp8bs::launch_moe_combine_bwd(dy, out_bf16, w, row_of, d_out_bf16, d_w, T, topk, R, N,
+                                                 dy_dtype == FP8BS_OUT_F32, (hipStream_t)stream));
 }
 
 }  // extern "C"

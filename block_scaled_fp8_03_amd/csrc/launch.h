@@ -49,6 +49,9 @@ hipError_t launch_moe_route_noalloc(const int32_t* indices, int64_t T, int64_t t
 hipError_t launch_moe_combine(const void* out, const float* w, const int32_t* row_of, void* y,
                               int64_t T, int64_t topk, int64_t R, int64_t N, bool out_f32,
                               hipStream_t stream);
+hipError_t launch_moe_combine_bwd(const void* dy, const void* out, const float* w, const int32_t* row_of, void* d_out,
+                                  float* d_w, int64_t T, int64_t topk, int64_t R, int64_t N, bool dy_f32,
+                                  hipStream_t stream);
 hipError_t launch_mla_absorb_key(const void* q, int64_t ld_t, int64_t ld_h, const void* w,
                                  const float* ws, void* out, int64_t T, int64_t H, int64_t dn,
                                  int64_t dv, int64_t R, bool out_f32, hipStream_t stream);
@@ -99,5 +102,84 @@ int64_t cache_update_workspace_bytes(int64_t B, int64_t N, int64_t W, int64_t P)
 int64_t cache_compact_workspace_bytes(int64_t B, int64_t W, int64_t P);
 hipError_t launch_cache_update(const PageTask& a, hipStream_t stream);
 hipError_t launch_cache_compact(const PageTask& a, hipStream_t stream);
+
+// fp8bs_rmsnorm's arguments (res and res_out, y, q and s: NULL where there is none)
+struct RmsNorm {
+  const void *x, *res, *w;
+  void *res_out, *y, *q;
+  float* s;
+  int64_t ld_x, M, K;
+  float eps;
+  bool res_f32, w_f32, ue8m0;
+};
+bool rmsnorm_fits(int64_t M, int64_t K);
+hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t stream);
+
+// fp8bs_rmsnorm_bwd's arguments (h and dx, dres: of h's type)
+struct RmsNormBwd {
+  const void *dy, *h, *w, *dres;
+  void* dx;
+  float* dw;
+  void* workspace;
+  int64_t ld_h, M, K;
+  float eps;
+  bool h_f32, w_f32;
+};
+int64_t rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K);
+hipError_t launch_rmsnorm_bwd(const RmsNormBwd& p, hipStream_t stream);
+
+// fp8bs_moe_gate's, fp8bs_moe_balance's and fp8bs_moe_gate_bwd's arguments
+struct MoeGate {
+  const void* logits;
+  const float* bias;
+  int32_t* indices;
+  float* weights;
+  int64_t ld, T, E, topk, groups, keep;
+  float route_scale;
+  bool f32, softmax, normalize;
+};
+hipError_t launch_moe_gate(const MoeGate& p, hipStream_t stream);
+struct MoeBalance {
+  const void* logits;
+  const int32_t *indices, *cu;
+  int32_t* counts;
+  float *probs, *loss;
+  void* workspace;
+  int64_t ld, T, S, E, topk;
+  bool f32, softmax;
+  float* part_probs;       // in the workspace
+  int32_t* part_counts;
+};
+int64_t moe_balance_workspace_bytes(int64_t T, int64_t S, int64_t E);
+hipError_t launch_moe_balance(const MoeBalance& p, hipStream_t stream);
+struct MoeGateBwd {
+  const void* logits;
+  const int32_t *indices, *cu, *counts;
+  const float *d_weights, *d_loss;
+  void* d_logits;
+  int64_t ld, T, S, E, topk;
+  float route_scale;
+  bool f32, softmax, normalize, out_f32;
+};
+hipError_t launch_moe_gate_bwd(const MoeGateBwd& p, hipStream_t stream);
+
+// fp8bs_swiglu's and fp8bs_swiglu_bwd's arguments
+struct SwiGlu {
+  const void *gate, *up;
+  const int32_t* n_rows;
+  void *y, *q;
+  float* s;
+  int64_t ld_g, ld_u, M, N;
+  bool ue8m0;
+};
+struct SwiGluBwd {
+  const void *dy, *gate, *up;
+  const int32_t* n_rows;
+  void *dgate, *dup;
+  int64_t ld_g, ld_u, ld_dg, ld_du, M, N;
+};
+bool swiglu_fits(int64_t M, int64_t N);
+hipError_t launch_swiglu(const SwiGlu& p, hipStream_t stream);
+hipError_t launch_swiglu_bwd(const SwiGluBwd& p, hipStream_t stream);
 
 }  // namespace fp8bs

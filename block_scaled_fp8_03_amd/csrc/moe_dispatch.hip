@@ -477,4 +477,87 @@ hipError_t launch_moe_combine(const void* out, const float* w, const int32_t* ro
   return hipGetLastError();
 }
 
+// ----------------------------------------------------------------------------
+// combine's gradient: d_out[row] = w * dy[t], d_w = <dy[t], out[row]> of each pair
+// ----------------------------------------------------------------------------
+// A workgroup is a token, a wave takes every kPairWaves-th of its pairs: the
+// token's dy comes from HBM once and then from the CU's L1.  Each row of `out` is
+// read and each of d_out written once, in whole lines.
+constexpr int kPairWaves = 8;
+constexpr int kPairUnroll = 4;
+
+template <bool DY_F32, bool VEC>
+__global__ __launch_bounds__(64 * kPairWaves) void moe_combine_bwd_kernel(
+    const void* __restrict__ dy, const uint16_t* __restrict__ out, const float* __restrict__ w,
+    const int32_t* __restrict__ row_of, uint16_t* __restrict__ d_out, float* __restrict__ d_w, int topk,
+    int64_t R, int64_t N) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = blockIdx.x;
+  for (int k = threadIdx.x >> 6; k < topk; k += blockDim.x >> 6) {
+    const int64_t r = row_of[t * topk + k];
+    float sum = 0.0f;
+    if (r >= 0 && r < R) {
+      const float wk = w[t * topk + k];
+      if (VEC) {
+        const int64_t nv = N / 8;
+        const uint4* o = (const uint4*)out + r * nv;
+        uint4* to = (uint4*)d_out + r * nv;
+        for (int64_t v0 = lane; v0 < nv; v0 += 64 * kPairUnroll) {
+          uint4 ov[kPairUnroll];
+          float f[kPairUnroll][8];
+#pragma unroll
+          for (int i = 0; i < kPairUnroll; ++i) {
+            const int64_t v = min(v0 + 64 * i, nv - 1);
+            ov[i] = o[v];
+            if (DY_F32) {
+              const float4 a = ((const float4*)dy)[2 * (t * nv + v)], b = ((const float4*)dy)[2 * (t * nv + v) + 1];
+              f[i][0] = a.x, f[i][1] = a.y, f[i][2] = a.z, f[i][3] = a.w;
+              f[i][4] = b.x, f[i][5] = b.y, f[i][6] = b.z, f[i][7] = b.w;
+            } else {
+              const uint4 a = ((const uint4*)dy)[t * nv + v];
+              const uint32_t h[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) f[i][2 * j] = bf16_lo(h[j]), f[i][2 * j + 1] = bf16_hi(h[j]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kPairUnroll; ++i) {
+            if (v0 + 64 * i >= nv) break;
+            const uint32_t h[4] = {ov[i].x, ov[i].y, ov[i].z, ov[i].w};
+            uint32_t d[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              sum = __builtin_fmaf(f[i][2 * j], bf16_lo(h[j]), sum);
+              sum = __builtin_fmaf(f[i][2 * j + 1], bf16_hi(h[j]), sum);
+              d[j] = pack2_bf16(wk * f[i][2 * j], wk * f[i][2 * j + 1]);
+            }
+            store_nt(to + v0 + 64 * i, make_uint4(d[0], d[1], d[2], d[3]));
+          }
+        }
+      } else {
+        for (int64_t n = lane; n < N; n += 64) {
+          const float f = DY_F32 ? ((const float*)dy)[t * N + n]
+                                 : bits_f32((uint32_t)((const uint16_t*)dy)[t * N + n] << 16);
+          sum = __builtin_fmaf(f, bits_f32((uint32_t)out[r * N + n] << 16), sum);
+          d_out[r * N + n] = (uint16_t)pack2_bf16(wk * f, 0.0f);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) sum += __shfl_xor(sum, i);
+    if (lane == 0) d_w[t * topk + k] = sum;
+  }
+}
+
+hipError_t launch_moe_combine_bwd(const void* dy, const void* out, const float* w, const int32_t* row_of, void* d_out,
+                                  float* d_w, int64_t T, int64_t topk, int64_t R, int64_t N, bool dy_f32,
+                                  hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  const dim3 grid((unsigned)T), block(64 * (unsigned)(topk < kPairWaves ? topk : kPairWaves));
+  const auto kernel = N % 8 == 0 ? (dy_f32 ? moe_combine_bwd_kernel<true, true> : moe_combine_bwd_kernel<false, true>)
+                                 : (dy_f32 ? moe_combine_bwd_kernel<true, false> : moe_combine_bwd_kernel<false, false>);
+  kernel<<<grid, block, 0, stream>>>(dy, (const uint16_t*)out, w, row_of, (uint16_t*)d_out, d_w, (int)topk, R, N);
+  return hipGetLastError();
+}
+
 }  // namespace fp8bs

@@ -1,0 +1,361 @@
+// norm.hip -- RMSNorm with the residual's addition and block-scaled FP8 output,
+// and its gradient (the norms of the pages' blocks: "DeepSeek-V3 Administrator &
+// Developer Guide" 1.1, in front of the FP8 linears of 6.3).
+//
+//   t = x + res,  c = t / sqrt(mean(t^2) + eps) * w,
+//   res_out = round(t), y = bf16(c), per 128: s = act_quant's rule on c, q = e4m3(c / s)
+//
+// HBM-bound: a row is read once, held in registers while its squares are summed,
+// and written once.
+#include <algorithm>
+
+#include "device_common.h"
+#include "launch.h"
+
+namespace fp8bs {
+
+namespace {
+
+constexpr int kThreads = 256;        // of a workgroup with several rows
+constexpr int kMaxThreads = 1024;    // of a workgroup with one
+constexpr int kMaxVpl = 4;           // 8-element vectors of a row that a lane holds
+
+// Sum over the 16 lanes of a DPP row; every lane receives it.
+__device__ __forceinline__ float row16_sum(float v) {
+  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0xB1, 0xF, 0xF, false));
+  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0x4E, 0xF, 0xF, false));
+  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0x124, 0xF, 0xF, false));
+  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0x128, 0xF, 0xF, false));
+  return v;
+}
+
+// Sum over the TPR lanes of a row (TPR 16, 32, 64: inside a wave; 0: the workgroup,
+// through `red`, one float a wave).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = row16_sum(v);
+  if (TPR == 16) return v;
+  v += __shfl_xor(v, 16);
+  if (TPR == 32) return v;
+  v += __shfl_xor(v, 32);
+  if (TPR == 64) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float sum = 0.0f;
+  for (int i = 0; i < (int)blockDim.x / 64; ++i) sum += red[i];
+  return sum;
+}
+
+// 8 elements of a row as floats
+__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(w[i]);
+    f[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void load8(const void* p, int64_t v, float* f) {
+  if (F32) {
+    const float4 a = ((const float4*)p)[2 * v], b = ((const float4*)p)[2 * v + 1];
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+    unpack8(((const uint4*)p)[v], f);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7]));
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, int64_t v, const float* f) {
+  if (F32) {
+    store_nt((uint4*)p + 2 * v, make_uint4(f32_bits(f[0]), f32_bits(f[1]), f32_bits(f[2]), f32_bits(f[3])));
+    store_nt((uint4*)p + 2 * v + 1, make_uint4(f32_bits(f[4]), f32_bits(f[5]), f32_bits(f[6]), f32_bits(f[7])));
+  } else {
+    store_nt((uint4*)p + v, pack8(f));
+  }
+}
+__device__ __forceinline__ void load_w(const RmsNorm& p, int64_t v, float* f) {
+  if (p.w_f32) load8<true>(p.w, v, f);
+  else load8<false>(p.w, v, f);
+}
+
+}  // namespace
+
+// ----------------------------------------------------------------------------
+// forward: TPR lanes a row (0: the workgroup), VPL vectors of 8 a lane; RES 0
+// none, 1 bf16, 2 float32.  16 consecutive lanes hold a block of 128.
+// ----------------------------------------------------------------------------
+template <int TPR, int VPL, int RES>
+__global__ __launch_bounds__(TPR ? kThreads : kMaxThreads) void rmsnorm_kernel(const RmsNorm p) {
+  __shared__ float red[kMaxThreads / 64];
+  const int tpr = TPR ? TPR : (int)blockDim.x;
+  const int lane = TPR ? (int)threadIdx.x % TPR : (int)threadIdx.x;
+  const int64_t m = TPR ? (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR : (int64_t)blockIdx.x;
+  const int64_t mm = TPR ? min(m, p.M - 1) : m;              // a row to read from where there is none
+  const int nv = (int)(p.K / 8);
+  const uint4* xr = (const uint4*)((const uint16_t*)p.x + mm * p.ld_x);
+  float t[VPL][8];
+  float sum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const int v = lane + j * tpr, vv = min(v, nv - 1);
+    unpack8(xr[vv], t[j]);
+    if (RES) {
+      float r[8];
+      load8<RES == 2>(p.res, mm * nv + vv, r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[j][i] += r[i];
+    }
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = __builtin_fmaf(t[j][i], t[j][i], a);
+    sum += v < nv ? a : 0.0f;
+  }
+  sum = row_sum<TPR>(sum, red);
+  const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, (float)p.K) + p.eps));
+  if (TPR && m >= p.M) return;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const int v = lane + j * tpr;
+    if (v >= nv) break;                                      // whole blocks of 128: nv is a multiple of 16
+    const int64_t at = m * nv + v;
+    if (RES) store8<RES == 2>(p.res_out, at, t[j]);
+    float c[8];
+    load_w(p, v, c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = t[j][i] * r * c[i];
+    if (p.y) store_nt((uint4*)p.y + at, pack8(c));
+    if (p.q) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, f32_bits(c[i]) & 0x7FFFFFFFu);
+      top = row16_max_u32(top);
+      const float sc = p.ue8m0 ? block_scale<true>(bits_f32(top)) : block_scale<false>(bits_f32(top));
+      const float rs = __fdiv_rn(1.0f, sc);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = div_markstein(c[i], sc, rs);
+      store_nt((uint2*)p.q + at, make_uint2(pack4_e4m3(c[0], c[1], c[2], c[3]), pack4_e4m3(c[4], c[5], c[6], c[7])));
+      if ((lane & 15) == 0) p.s[at / 16] = sc;
+    }
+  }
+}
+
+namespace {
+
+// Lanes a row (16, 32, 64 inside a wave; else the threads of its workgroup) and vectors a lane.
+struct RowPlan {
+  int tpr, vpl;
+};
+RowPlan plan_of(int64_t K) {
+  const int64_t nv = K / 8;
+  if (nv <= 64) return {nv <= 16 ? 16 : nv <= 32 ? 32 : 64, 1};
+  int vpl = nv <= 512 ? 1 : nv <= 2048 ? 2 : 4;
+  return {(int)((nv + 64 * vpl - 1) / (64 * vpl)) * 64, vpl};
+}
+
+template <int RES>
+void launch_fwd(const RmsNorm& p, hipStream_t stream) {
+  const RowPlan plan = plan_of(p.K);
+  if (plan.tpr <= 64) {
+    const int rows = kThreads / plan.tpr;
+    const dim3 grid((unsigned)((p.M + rows - 1) / rows)), block(kThreads);
+    if (plan.tpr == 16) rmsnorm_kernel<16, 1, RES><<<grid, block, 0, stream>>>(p);
+    else if (plan.tpr == 32) rmsnorm_kernel<32, 1, RES><<<grid, block, 0, stream>>>(p);
+    else rmsnorm_kernel<64, 1, RES><<<grid, block, 0, stream>>>(p);
+    return;
+  }
+  const dim3 grid((unsigned)p.M), block(plan.tpr);
+  if (plan.vpl == 1) rmsnorm_kernel<0, 1, RES><<<grid, block, 0, stream>>>(p);
+  else if (plan.vpl == 2) rmsnorm_kernel<0, 2, RES><<<grid, block, 0, stream>>>(p);
+  else rmsnorm_kernel<0, 4, RES><<<grid, block, 0, stream>>>(p);
+}
+
+}  // namespace
+
+// A row's widest workgroup: K up to 32768, one workgroup a row, at most 2^32 - 1 threads.
+bool rmsnorm_fits(int64_t M, int64_t K) {
+  return K <= (int64_t)kMaxThreads * kMaxVpl * 8 && M <= (((int64_t)1 << 32) - 1) / kMaxThreads;
+}
+
+hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t stream) {
+  if (p.res == nullptr) launch_fwd<0>(p, stream);
+  else if (p.res_f32) launch_fwd<2>(p, stream);
+  else launch_fwd<1>(p, stream);
+  return hipGetLastError();
+}
+
+// ----------------------------------------------------------------------------
+// gradient
+//   g = dy * w, r = 1 / sqrt(mean(h^2) + eps)
+//   dx = r * (g - h * r^2 * mean(g * h)) + dres,  dw = sum over rows of dy * h * r
+// A workgroup goes through rows m, m + grid, ..., keeps its part of dw in
+// registers and leaves it in the workspace; a second kernel adds the parts in a
+// fixed order.
+// ----------------------------------------------------------------------------
+namespace {
+
+constexpr int kBwdGroups = 512;       // parts of dw at most
+
+// rows that a workgroup takes at a time
+int rows_at_once(const RowPlan& plan) { return plan.tpr <= 64 ? kThreads / plan.tpr : 1; }
+int64_t bwd_groups(int64_t M, int64_t K) {
+  const int rows = rows_at_once(plan_of(K));
+  return std::min<int64_t>((M + rows - 1) / rows, kBwdGroups);
+}
+
+}  // namespace
+
+template <int TPR, int VPL, bool F32>
+__global__ __launch_bounds__(TPR ? kThreads : kMaxThreads) void rmsnorm_bwd_kernel(const RmsNormBwd p, float* parts) {
+  __shared__ float red[4][kMaxThreads / 64];
+  __shared__ float rows_dw[TPR ? kThreads * 8 : 1];
+  const int tpr = TPR ? TPR : (int)blockDim.x;
+  const int lane = TPR ? (int)threadIdx.x % TPR : (int)threadIdx.x;
+  const int rows = TPR ? kThreads / TPR : 1;
+  const int mine = TPR ? (int)threadIdx.x / TPR : 0;
+  const int nv = (int)(p.K / 8);
+  const float rk = (float)p.K;
+  float w[VPL][8], dw[VPL][8];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const int vv = min(lane + j * tpr, nv - 1);
+    if (p.w_f32) load8<true>(p.w, vv, w[j]);
+    else load8<false>(p.w, vv, w[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
+  }
+  int turn = 0;
+  for (int64_t m0 = (int64_t)blockIdx.x * rows; m0 < p.M; m0 += (int64_t)gridDim.x * rows, turn ^= 1) {
+    const int64_t m = m0 + mine, mm = min(m, p.M - 1);
+    float h[VPL][8], d[VPL][8];
+    float hh = 0.0f, gh = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int v = lane + j * tpr, vv = min(v, nv - 1);
+      load8<F32>((const char*)p.h + mm * p.ld_h * (F32 ? 4 : 2), vv, h[j]);
+      load8<false>(p.dy, mm * nv + vv, d[j]);
+      float a = 0.0f, b = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a = __builtin_fmaf(h[j][i], h[j][i], a);
+        b = __builtin_fmaf(d[j][i] * w[j][i], h[j][i], b);
+      }
+      hh += v < nv ? a : 0.0f;
+      gh += v < nv ? b : 0.0f;
+    }
+    // two buffers in turn: a wave may be at the next row's sums while another still reads this one's
+    if (TPR) {
+      hh = row_sum<TPR>(hh, nullptr);
+      gh = row_sum<TPR>(gh, nullptr);
+    } else {
+      hh = row_sum<64>(hh, nullptr);
+      gh = row_sum<64>(gh, nullptr);
+      if ((threadIdx.x & 63) == 0) {
+        red[2 * turn][threadIdx.x >> 6] = hh;
+        red[2 * turn + 1][threadIdx.x >> 6] = gh;
+      }
+      __syncthreads();
+      hh = gh = 0.0f;
+      for (int i = 0; i < (int)blockDim.x / 64; ++i) {
+        hh += red[2 * turn][i];
+        gh += red[2 * turn + 1][i];
+      }
+    }
+    const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(hh, rk) + p.eps));
+    const float c = r * r * __fdiv_rn(gh, rk);
+    if (m < p.M) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        const int v = lane + j * tpr;
+        if (v >= nv) break;
+        float o[8], e[8];
+        if (p.dres) load8<F32>(p.dres, m * nv + v, e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o[i] = r * __builtin_fmaf(-h[j][i], c, d[j][i] * w[j][i]);
+          if (p.dres) o[i] += e[i];
+          dw[j][i] = __builtin_fmaf(d[j][i], h[j][i] * r, dw[j][i]);
+        }
+        store8<F32>(p.dx, m * nv + v, o);
+      }
+    }
+  }
+  if (!parts) return;
+  float* out = parts + (int64_t)blockIdx.x * p.K;
+  if (TPR) {
+    // the rows' parts of a column lie tpr * 8 floats apart
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rows_dw[threadIdx.x * 8 + i] = dw[0][i];
+    __syncthreads();
+    for (int k = threadIdx.x; k < p.K; k += kThreads) {
+      float a = 0.0f;
+      for (int r = 0; r < rows; ++r) a += rows_dw[r * tpr * 8 + k];
+      out[k] = a;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int v = lane + j * tpr;
+      if (v >= nv) break;
+      ((float4*)out)[2 * v] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+      ((float4*)out)[2 * v + 1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+    }
+  }
+}
+
+// dw[k] = the sum of G parts: 16 threads of a workgroup take every 16th part of 4 columns, then their sums in order.
+__global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* __restrict__ parts, float* __restrict__ dw,
+                                                          int64_t G, int64_t K) {
+  __shared__ float4 sums[16][16];
+  const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
+  const int64_t c4 = (int64_t)blockIdx.x * 16 + col;         // K is a multiple of 64
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float4* p = (const float4*)parts + c4;
+  for (int64_t g = grp; g < G; g += 16) {
+    const float4 b = p[g * (K / 4)];
+    a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+  }
+  sums[grp][col] = a;
+  __syncthreads();
+  if (grp == 0) {
+    for (int g = 1; g < 16; ++g) {
+      const float4 b = sums[g][col];
+      a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+    }
+    ((float4*)dw)[c4] = a;
+  }
+}
+
+int64_t rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K) {
+  const int64_t G = bwd_groups(M, K);
+  return G > 1 ? G * K * 4 : 0;                              // one workgroup writes dw itself
+}
+
+template <bool F32>
+static void launch_bwd(const RmsNormBwd& p, float* parts, hipStream_t stream) {
+  const RowPlan plan = plan_of(p.K);
+  const dim3 grid((unsigned)bwd_groups(p.M, p.K)), block(plan.tpr <= 64 ? kThreads : plan.tpr);
+  if (plan.tpr == 16) rmsnorm_bwd_kernel<16, 1, F32><<<grid, block, 0, stream>>>(p, parts);
+  else if (plan.tpr == 32) rmsnorm_bwd_kernel<32, 1, F32><<<grid, block, 0, stream>>>(p, parts);
+  else if (plan.tpr == 64) rmsnorm_bwd_kernel<64, 1, F32><<<grid, block, 0, stream>>>(p, parts);
+  else if (plan.vpl == 1) rmsnorm_bwd_kernel<0, 1, F32><<<grid, block, 0, stream>>>(p, parts);
+  else if (plan.vpl == 2) rmsnorm_bwd_kernel<0, 2, F32><<<grid, block, 0, stream>>>(p, parts);
+  else rmsnorm_bwd_kernel<0, 4, F32><<<grid, block, 0, stream>>>(p, parts);
+}
+
+hipError_t launch_rmsnorm_bwd(const RmsNormBwd& p, hipStream_t stream) {
+  const int64_t G = bwd_groups(p.M, p.K);
+  float* parts = !p.dw ? nullptr : G > 1 ? (float*)p.workspace : p.dw;
+  if (G > 0) {
+    if (p.h_f32) launch_bwd<true>(p, parts, stream);
+    else launch_bwd<false>(p, parts, stream);
+  }
+  if (p.dw && G != 1)                                        // no rows: dw is zero
+    rmsnorm_dw_kernel<<<dim3((unsigned)(p.K / 64)), dim3(256), 0, stream>>>((const float*)p.workspace, p.dw, G, p.K);
+  return hipGetLastError();
+}
+
+}  // namespace fp8bs

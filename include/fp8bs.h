@@ -53,13 +53,17 @@ extern "C" {
 #define FP8BS_SCALE_FP32  0  /* s = max(amax, 1e-4) / 448 as float32 */
 #define FP8BS_SCALE_UE8M0 1  /* s rounded up to the next power of two */
 
-/* Output element types of the GEMMs. */
+/* Output element types of the GEMMs (and element types of arguments that may be either). */
 #define FP8BS_OUT_BF16    0
 #define FP8BS_OUT_F32     1
 
 /* Element types of an MLA cache's latents. */
 #define FP8BS_CACHE_BF16  0
 #define FP8BS_CACHE_FP8   1  /* e4m3 codes with a power-of-two float32 scale per 128 */
+
+/* Scores of the gate. */
+#define FP8BS_SCORE_SIGMOID 0
+#define FP8BS_SCORE_SOFTMAX 1
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fp8bs_status_string(int status);
@@ -535,6 +539,160 @@ int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fm
                         const int32_t* table, const int32_t* lens, int32_t* table_out,
                         int32_t* count, int64_t B, int64_t W, int64_t P, int64_t ps, int64_t R,
                         int64_t dr, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * What stands between the FP8 products of a block with experts (Admin guide
+ * 1.1 and 8.4): the norm in front of them, the gate that makes the ids and
+ * weights of fp8bs_moe_route and fp8bs_moe_combine, its balance loss, the
+ * activation between an expert's two products; and their gradients, those of
+ * fp8bs_moe_combine among them.  (The gradient of fp8bs_moe_quant_scatter is
+ * fp8bs_moe_combine with weights of 1.)
+ *
+ * rmsnorm -- with the residual's addition and FP8 output:
+ *   t = x + res (x without a residual),  c = t / sqrt(mean(t^2) + eps) * norm_w
+ *   res_out = t rounded to its type,  y = bf16(c)
+ *   per 128 columns: s by act_quant's rule on c, q = e4m3(c / s)
+ * All in float32 from the inputs on, each output rounded once: the norm is
+ * that of the unrounded sum, the codes are those of the unrounded norm.  A row
+ * whose squares sum to infinity in float32 gives zeros, as does one of zeros;
+ * with eps = 0 the latter is NaN.
+ *
+ *   x        in   bf16, element (m, k) at [m*ld_x + k]; ld_x >= 0, a multiple of 8
+ *   res      in   [M, K] bf16 or float32 (res_dtype, FP8BS_OUT_*), or NULL
+ *   res_out  out  [M, K] of res's type; may be res itself.  NULL with res NULL
+ *   norm_w   in   [K] float32 (norm_w_f32 != 0) or bf16
+ *   eps           0 .. 3e38
+ *   y        out  bf16 [M, K], or NULL
+ *   q, s     out  e4m3 [M, K] and float32 [M, K/128], or both NULL; y or q is there
+ *   scale_fmt     FP8BS_SCALE_FP32 or FP8BS_SCALE_UE8M0
+ *   0 <= M <= 4194303, K % 128 == 0, 0 <= K <= 32768 (M or K 0: no-op).
+ * All pointers 16-byte aligned but s (4).
+ *
+ * rmsnorm_bwd -- of y by the norm's input h (x, or res_out) and by norm_w:
+ *   g = dy * norm_w, r = 1 / sqrt(mean(h^2) + eps)
+ *   dx = r * (g - h * r^2 * mean(g * h)) + dres,   dw = sum over rows of dy * h * r
+ * dx is the gradient of x and of res alike; dres is what reaches res_out from
+ * elsewhere.  The codes' rounding is passed straight through.
+ *   dy       in   bf16 [M, K]
+ *   h        in   bf16 or float32 (h_dtype), element (m, k) at [m*ld_h + k]
+ *   dres     in   [M, K] of h's type, or NULL; may be dx itself
+ *   dx       out  [M, K] of h's type
+ *   dw       out  float32 [K] (M = 0: zeros), or NULL
+ *   workspace     DEVICE, >= fp8bs_rmsnorm_bwd_workspace_size(M, K) bytes (not
+ *                 needed without dw; 0 for few rows), 16-byte aligned, scratch,
+ *                 not shared by calls that may run at the same time
+ * The sums are float32 in a fixed order: the result does not depend on timing.
+ */
+int fp8bs_rmsnorm(const void* x_bf16, int64_t ld_x, const void* res, void* res_out, int res_dtype,
+                  const void* norm_w, int norm_w_f32, float eps, void* y_bf16, void* q_e4m3, float* s,
+                  int scale_fmt, int64_t M, int64_t K, void* stream);
+int64_t fp8bs_rmsnorm_bwd_workspace_size(int64_t M, int64_t K);
+int fp8bs_rmsnorm_bwd(const void* dy_bf16, const void* h, int64_t ld_h, int h_dtype, const void* norm_w,
+                      int norm_w_f32, float eps, const void* dres, void* dx, float* dw, int64_t M, int64_t K,
+                      void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * moe_gate -- the experts and routing weights of every token:
+ *   score = sigmoid(logit), or softmax over the token's logits
+ *   key = float32(score) + bias; the logit itself where there is no bias (the
+ *         scores have its order)
+ *   groups > 1: the experts lie in `groups` runs of E / groups; a group counts
+ *         as the sum of its two largest keys (without a bias: its largest);
+ *         only the topk_groups groups that count most are looked at
+ *   indices = the topk largest keys' experts, the largest first
+ *   weights = score / (sum of the chosen scores, if normalize) * route_scale
+ * Ties go to the lowest index, among groups too.  An expert whose logit is -inf
+ * or NaN, or whose key is -inf or NaN, is masked: it is never chosen, and a
+ * softmax leaves it out.  Slots without an expert (all others masked) hold
+ * index -1, which fp8bs_moe_route does not route, and weight 0.  Logits of
+ * +inf share a softmax's weight.  With a bias the scores are computed in 64
+ * bits and rounded once, so that the choice does not turn on the last bit of
+ * an exponential; all else is float32.
+ *
+ *   logits   in   float32 or bf16 (logits_dtype), element (t, e) at [t*ld + e], ld >= 0
+ *   bias     in   float32 [E], or NULL
+ *   indices  out  int32 [T, topk];  weights  out  float32 [T, topk]
+ *   score         FP8BS_SCORE_SIGMOID or FP8BS_SCORE_SOFTMAX
+ *   0 <= T < 2^24 (0 = no-op), 1 <= E <= 1024, 1 <= topk <= min(E, 64),
+ *   1 <= topk_groups <= groups <= 64, E % groups == 0; route_scale finite.
+ *
+ * moe_balance -- per-expert counts and the balance loss of each sequence s,
+ * tokens cu_seq[s] .. cu_seq[s+1] - 1, n of them:
+ *   counts[s, e] = how often its tokens' indices name e
+ *   probs[s, e]  = mean over its tokens of score_e / (sum of the token's scores)
+ *   loss[s]      = E / (topk * n) * sum_e counts[s, e] * probs[s, e]
+ * (1 where all experts are used alike).  A sequence without tokens gives zeros;
+ * a token whose experts are all masked adds none; indices outside [0, E) are
+ * not counted.
+ *   indices  in   int32 [T, topk] (from fp8bs_moe_gate)
+ *   cu_seq   in   DEVICE int32 [S + 1], non-decreasing, or NULL: one sequence
+ *                 of all T tokens, S = 1.  Clamped to [0, T], and a sequence's
+ *                 end to its start
+ *   counts   out  int32 [S, E];  probs  out  float32 [S, E];  loss  out  float32 [S]
+ *   workspace     DEVICE, >= fp8bs_moe_balance_workspace_size(T, S, E) bytes (0:
+ *                 NULL), 16-byte aligned, scratch, not shared by concurrent calls
+ *   0 <= S <= 2^22 (0 = no-op); T = 0 gives zeros.
+ *
+ * moe_gate_bwd -- the gradient by the logits of both: of the weights, given
+ * d_weights, and of the losses, given d_loss (the counts and the choice of
+ * experts are constants):
+ *   d_weights in  float32 [T, topk], or NULL (no part); needs indices
+ *   d_loss    in  float32 [S], or NULL (no part); needs counts of fp8bs_moe_balance
+ *   d_logits  out float32 or bf16 (out_dtype) [T, E], 16-byte aligned; 0 for masked
+ *             experts.  Tokens outside all sequences get d_weights' part alone
+ *   score, normalize, route_scale  as given to fp8bs_moe_gate
+ * An index that a token names twice counts twice; one outside [0, E) is left
+ * out.  Sums of no scores (all underflowed or masked) give 0.
+ * Results do not depend on timing.  Pointers are aligned to their elements.
+ */
+int fp8bs_moe_gate(const void* logits, int64_t ld, int logits_dtype, const float* bias, int64_t T, int64_t E,
+                   int64_t topk, int64_t groups, int64_t topk_groups, int score, int normalize, float route_scale,
+                   int32_t* indices, float* weights, void* stream);
+int64_t fp8bs_moe_balance_workspace_size(int64_t T, int64_t S, int64_t E);
+int fp8bs_moe_balance(const void* logits, int64_t ld, int logits_dtype, const int32_t* indices, const int32_t* cu_seq,
+                      int64_t T, int64_t S, int64_t E, int64_t topk, int score, int32_t* counts, float* probs,
+                      float* loss, void* workspace, int64_t workspace_bytes, void* stream);
+int fp8bs_moe_gate_bwd(const void* logits, int64_t ld, int logits_dtype, const int32_t* indices,
+                       const float* d_weights, int score, int normalize, float route_scale, const int32_t* cu_seq,
+                       const int32_t* counts, const float* d_loss, int64_t T, int64_t S, int64_t E, int64_t topk,
+                       void* d_logits, int out_dtype, void* stream);
+
+/*
+ * swiglu -- the activation between an expert's two products:
+ *   a = g * sigmoid(g) * u   (float32),  y = bf16(a),
+ *   per 128 columns: s by act_quant's rule on a, q = e4m3(a / s)
+ *   gate, up in   bf16, element (m, n) at [m*ld + n]: two tensors, or the halves
+ *                 of one; ld_g, ld_u >= 0, multiples of 8
+ *   n_rows   in   DEVICE int32 [1], or NULL: rows from *n_rows (clamped to [0, M])
+ *                 on are neither read nor written (offsets + E of fp8bs_moe_route)
+ *   y        out  bf16 [M, N], or NULL;  q, s  out  e4m3 [M, N] and float32
+ *                 [M, N/128], or both NULL; y or q is there
+ *   M, N >= 0 (either 0 = no-op), N % 128 == 0, M * N < about 2^37 (one launch).
+ *
+ * swiglu_bwd --
+ *   du = dy * g * sig,  dg = dy * u * sig * (1 + g * (1 - sig)),  sig = sigmoid(g)
+ *   dy       in   bf16 [M, N]
+ *   dgate, dup  out  bf16, strided as gate and up are (ld >= N for more than one
+ *                 row); they may be columns of the same rows, but share no element
+ * All pointers 16-byte aligned but s and n_rows (4).
+ *
+ * moe_combine_bwd -- the gradient of fp8bs_moe_combine:
+ *   d_out[row_of[t, k]] = bf16(w[t, k] * dy[t]),  d_w[t, k] = <dy[t], out[row_of[t, k]]>
+ *   dy       in   bf16 or float32 (dy_dtype) [T, N]
+ *   out      in   bf16 [R, N];  w, row_of  in  float32, int32 [T, topk]
+ *   d_out    out  bf16 [R, N]; rows that no pair maps to are left untouched
+ *   d_w      out  float32 [T, topk]; 0 for pairs outside [0, R)
+ *   0 <= T < 2^23, topk >= 1, T * topk < 2^31, R, N >= 0.
+ * If row_of maps two pairs to one row, that row of d_out receives either's.
+ * dy, out and d_out 16-byte aligned, the others 4-byte.
+ */
+int fp8bs_swiglu(const void* gate_bf16, int64_t ld_g, const void* up_bf16, int64_t ld_u, const int32_t* n_rows,
+                 void* y_bf16, void* q_e4m3, float* s, int scale_fmt, int64_t M, int64_t N, void* stream);
+int fp8bs_swiglu_bwd(const void* dy_bf16, const void* gate_bf16, int64_t ld_g, const void* up_bf16, int64_t ld_u,
+                     const int32_t* n_rows, void* dgate_bf16, int64_t ld_dg, void* dup_bf16, int64_t ld_du,
+                     int64_t M, int64_t N, void* stream);
+int fp8bs_moe_combine_bwd(const void* dy, int dy_dtype, const void* out_bf16, const float* w, const int32_t* row_of,
+                          void* d_out_bf16, float* d_w, int64_t T, int64_t topk, int64_t R, int64_t N, void* stream);
 
 #ifdef __cplusplus
 }
