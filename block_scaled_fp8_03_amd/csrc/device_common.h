@@ -158,4 +158,80 @@ __device__ __forceinline__ v8bf dequant8_bf16(uint32_t w0, uint32_t w1, float sc
   return __builtin_bit_cast(v8bf, u);
 }
 
+// Sum over a wave, all 64 lanes active, in VALU steps of a fixed order; the result is uniform.
+__device__ __forceinline__ float row16_sum(float v) {
+  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0xB1, 0xF, 0xF, false));   // quad_perm 1,0,3,2
+  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0x4E, 0xF, 0xF, false));   // quad_perm 2,3,0,1
+  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0x124, 0xF, 0xF, false));  // row_ror 4
+  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0x128, 0xF, 0xF, false));  // row_ror 8
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row16_sum(v);
+  v += bits_f32((uint32_t)dpp_or_0<0x142, 0xA>((int)f32_bits(v)));   // row 0 to row 1, row 2 to row 3
+  v += bits_f32((uint32_t)dpp_or_0<0x143, 0xC>((int)f32_bits(v)));   // rows 0 and 1 to rows 2 and 3
+  return bits_f32((uint32_t)__builtin_amdgcn_readlane((int)f32_bits(v), 63));
+}
+// Maximum over a wave of unsigned numbers, uniform.
+__device__ __forceinline__ uint32_t wave_max_uniform(uint32_t v) {
+  v = row16_max_u32(v);
+  v = max(v, (uint32_t)dpp_or_0<0x142, 0xA>((int)v));
+  v = max(v, (uint32_t)dpp_or_0<0x143, 0xC>((int)v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// e^x within 2 units in the last place (0 and infinity beyond float32's range): the
+// hardware's power of two of x log2(e) less its whole part, both of whose roundings
+// are made up for by the second half of log2(e).  6 instructions where the library's
+// function takes 14.
+__device__ __forceinline__ float exp_f32(float x) {
+  constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;
+  x = __builtin_amdgcn_fmed3f(x, -150.0f, 150.0f);
+  const float n = __builtin_rintf(x * kHi);
+  const float f = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -n));
+  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
+}
+// 1 / (1 + e^-x) within 4 units in the last place
+__device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x)); }
+
+// 8 bf16 of a vector as floats, and back
+__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(w[i]);
+    f[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7]));
+}
+
+// Codes of 8 computed values a lane, 16 lanes a block of 128; its scale to *scale.
+// The scale is act_quant's.  The quotient c / s is the product with 1 / s (exact for
+// powers of two, else within 2 units in the last place): c itself has come out of
+// float32 arithmetic and is no nearer to its value, and the correctly rounded quotient
+// that act_quant makes of exact inputs takes three instructions more a value.  It is
+// at most 448 (1 + 2^-21), which the converter rounds to 448.
+__device__ __forceinline__ uint2 quant8(const float* c, bool ue8m0, float* scale) {
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(c[i]));
+  top = bits_f32(row16_max_u32(f32_bits(top)));
+  float s, r;
+  if (ue8m0) {
+    s = block_scale<true>(top);
+    r = bits_f32(0x7F000000u - f32_bits(s));                 // 2^-e of 2^e
+  } else {
+    s = block_scale<false>(top);
+    r = __builtin_amdgcn_rcpf(s);
+  }
+  *scale = s;
+  int a = __builtin_amdgcn_cvt_pk_fp8_f32(c[0] * r, c[1] * r, 0, false);
+  a = __builtin_amdgcn_cvt_pk_fp8_f32(c[2] * r, c[3] * r, a, true);
+  int b = __builtin_amdgcn_cvt_pk_fp8_f32(c[4] * r, c[5] * r, 0, false);
+  b = __builtin_amdgcn_cvt_pk_fp8_f32(c[6] * r, c[7] * r, b, true);
+  return make_uint2((uint32_t)a, (uint32_t)b);
+}
+
 }  // namespace fp8bs

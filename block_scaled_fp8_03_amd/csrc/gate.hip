@@ -3,7 +3,9 @@
 // balance loss over its scores, and the gradient of both by the logits.
 //
 // One wave a token: lane l holds experts l*V .. l*V + V - 1, so the lowest lane
-// and the lowest register of a maximum are the lowest expert.
+// and the lowest register of a maximum are the lowest expert.  A token's logits are
+// a few hundred bytes: what these kernels take is a wave's chain of instructions
+// (few tokens) or the instructions of all waves (many), not HBM.
 #include <algorithm>
 
 #include "device_common.h"
@@ -17,20 +19,15 @@ constexpr int kWaves = 4;            // tokens that a workgroup of the gate take
 
 __device__ __forceinline__ float minus_inf() { return bits_f32(0xFF800000u); }
 
-// Sum over a wave, the same order everywhere; every lane receives it.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int i = 1; i < 64; i <<= 1) v += __shfl_xor(v, i);
-  return v;
+__device__ __forceinline__ float wave_max(float v) {
+  uint32_t b = f32_bits(v);
+  b ^= (uint32_t)((int32_t)b >> 31) | 0x80000000u;           // of the same order as unsigned numbers
+  b = wave_max_uniform(b);
+  return bits_f32(b ^ ((uint32_t)((int32_t)~b >> 31) | 0x80000000u));
 }
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int i = 1; i < 64; i <<= 1) v += __shfl_xor(v, i);
-  return v;
-}
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int i = 1; i < 64; i <<= 1) v = fmaxf(v, __shfl_xor(v, i));
   return v;
 }
 
@@ -43,27 +40,90 @@ __device__ __forceinline__ float float_of(uint32_t k) {
   return bits_f32(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
 }
 
+// V consecutive 4-byte words from e on, as wide as they go; `fill` behind E.  VEC: V
+// divides E and the address is aligned to V words.
+template <int V, bool VEC>
+__device__ __forceinline__ void load_words(const uint32_t* p, int e, int E, uint32_t fill, uint32_t* w) {
+  if (VEC && V == 2) {
+    const uint2 u = e < E ? *(const uint2*)(p + e) : make_uint2(fill, fill);
+    w[0] = u.x, w[V > 1 ? 1 : 0] = u.y;
+  } else if (VEC && V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const uint4 u = e < E ? *(const uint4*)(p + e + i) : make_uint4(fill, fill, fill, fill);
+      w[i] = u.x, w[(i + 1) % V] = u.y, w[(i + 2) % V] = u.z, w[(i + 3) % V] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) w[v] = e + v < E ? p[e + v] : fill;
+  }
+}
+
 // The token's logits: z[v] of expert lane*V + v; one that is masked (-inf), NaN or
 // behind the last expert gives -inf.
-template <int V>
+template <int V, bool VEC>
 __device__ __forceinline__ void load_logits(const void* logits, bool f32, int64_t at, int E, int lane, float* z) {
+  const int e = lane * V;
+  if (f32) {
+    uint32_t w[V];
+    load_words<V, VEC>((const uint32_t*)logits + at, e, E, 0xFF800000u, w);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = lane * V + v;
-    float f = minus_inf();
-    if (e < E) f = f32 ? ((const float*)logits)[at + e] : bits_f32((uint32_t)((const uint16_t*)logits)[at + e] << 16);
-    z[v] = f > minus_inf() ? f : minus_inf();
+    for (int v = 0; v < V; ++v) z[v] = bits_f32(w[v]);
+  } else if (VEC && V > 1) {
+    constexpr int W = V / 2 > 0 ? V / 2 : 1;                  // two logits a word
+    uint32_t w[W];
+    load_words<W, true>((const uint32_t*)((const uint16_t*)logits + at), lane * W, E / 2, 0xFF80FF80u, w);
+#pragma unroll
+    for (int v = 0; v < V; ++v) z[v] = v % 2 ? bf16_hi(w[v / 2]) : bf16_lo(w[v / 2]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      z[v] = e + v < E ? bits_f32((uint32_t)((const uint16_t*)logits)[at + e + v] << 16) : minus_inf();
   }
+#pragma unroll
+  for (int v = 0; v < V; ++v) z[v] = z[v] > minus_inf() ? z[v] : minus_inf();
+}
+
+// e^x for x <= 0 in 64 bits, within 2^-45 of it: x = n ln 2 + r, |r| <= ln 2 / 2, the
+// exponential series of r to r^11 (the next term is below 2^-47 of it).
+__device__ __forceinline__ double exp_f64(double x) {
+  x = fmax(x, -745.0);                                        // below float32's and float64's smallest numbers
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  double r = __builtin_fma(n, -0.6931471805599453, x);
+  r = __builtin_fma(n, -2.3190468138462996e-17, r);
+  double p = 1.0 / 39916800;
+  p = __builtin_fma(p, r, 1.0 / 3628800);
+  p = __builtin_fma(p, r, 1.0 / 362880);
+  p = __builtin_fma(p, r, 1.0 / 40320);
+  p = __builtin_fma(p, r, 1.0 / 5040);
+  p = __builtin_fma(p, r, 1.0 / 720);
+  p = __builtin_fma(p, r, 1.0 / 120);
+  p = __builtin_fma(p, r, 1.0 / 24);
+  p = __builtin_fma(p, r, 1.0 / 6);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_amdgcn_ldexp(p, (int)n);
+}
+// 1 / d of a normal d: the hardware's estimate and two steps of Newton's iteration
+__device__ __forceinline__ double rcp_f64(double d) {
+  double y = __builtin_amdgcn_rcp(d);
+  y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+  return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
 }
 
 // score[v] in 64 bits, rounded once; 0 for masked experts (all of a token masked: all 0).
 // Two scores that float32 arithmetic would leave a rounding apart, or exchange, decide
-// which expert a token takes, so they are computed where that cannot happen.
+// which expert a token takes: of 4096 tokens over 256 experts one or two have such a
+// pair.  Here the sum of errors is 2^-20 of a rounding.
 template <int V>
 __device__ __forceinline__ void exact_scores(const float* z, bool softmax, float* score) {
   if (!softmax) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) score[v] = (float)(1.0 / (1.0 + exp(-(double)z[v])));
+    for (int v = 0; v < V; ++v) {
+      const double x = exp_f64(-fabs((double)z[v]));
+      score[v] = (float)((z[v] < 0.0f ? x : 1.0) * rcp_f64(1.0 + x));
+    }
     return;
   }
   float top = z[0];
@@ -73,12 +133,18 @@ __device__ __forceinline__ void exact_scores(const float* z, bool softmax, float
   double e[V], sum = 0.0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    e[v] = z[v] == minus_inf() ? 0.0 : z[v] == top ? 1.0 : exp((double)z[v] - (double)top);
+    e[v] = z[v] == minus_inf() ? 0.0 : z[v] == top ? 1.0 : exp_f64((double)z[v] - (double)top);
     sum += e[v];
   }
   sum = wave_sum(sum);
+  const double by = sum > 0.0 ? rcp_f64(sum) : 0.0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) score[v] = sum > 0.0 ? (float)(e[v] / sum) : 0.0f;
+  for (int v = 0; v < V; ++v) score[v] = (float)(e[v] * by);
+}
+
+// e^-|z|, of which the sigmoid is made: scores go down to float32's smallest numbers
+__device__ __forceinline__ float sigmoid_of(float z, float x) {
+  return (z < 0.0f ? x : 1.0f) * __builtin_amdgcn_rcpf(1.0f + x);
 }
 
 // score[v] in float32, and the sum of all of them (1 for a softmax, 0 where all are masked).
@@ -88,9 +154,7 @@ __device__ __forceinline__ float scores(const float* z, bool softmax, float* sco
   if (!softmax) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      // the exponential of what is below 0 alone: scores go down to float32's smallest numbers
-      const float x = expf(-fabsf(z[v]));
-      score[v] = __fdiv_rn(z[v] < 0.0f ? x : 1.0f, 1.0f + x);
+      score[v] = sigmoid_of(z[v], exp_f32(-fabsf(z[v])));
       sum += score[v];
     }
     return wave_sum(sum);
@@ -101,7 +165,7 @@ __device__ __forceinline__ float scores(const float* z, bool softmax, float* sco
   top = wave_max(top);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    score[v] = z[v] == minus_inf() ? 0.0f : z[v] == top ? 1.0f : expf(z[v] - top);
+    score[v] = z[v] == minus_inf() ? 0.0f : z[v] == top ? 1.0f : exp_f32(z[v] - top);
     sum += score[v];
   }
   sum = wave_sum(sum);
@@ -111,13 +175,47 @@ __device__ __forceinline__ float scores(const float* z, bool softmax, float* sco
   return sum > 0.0f ? 1.0f : 0.0f;
 }
 
-// score[v] over their sum; a softmax's are that already.  A quotient, not a product
-// with 1 / sum: that is infinite for the sum of the smallest scores.
+// score[v] over their sum; a softmax's are that already.
 template <int V>
 __device__ __forceinline__ void shares(float* score, float sum, bool softmax) {
   if (softmax) return;
+  // 1 / sum is infinite for the sum of the smallest scores: those are taken times 2^64 before it
+  const bool tiny = sum < 1e-30f;
+  const float up = tiny ? 18446744073709551616.0f : 1.0f;
+  const float by = sum > 0.0f ? __fdiv_rn(1.0f, sum * up) : 0.0f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) score[v] = sum > 0.0f ? __fdiv_rn(score[v], sum) : 0.0f;
+  for (int v = 0; v < V; ++v) score[v] = score[v] * up * by;
+}
+
+// Sequence s's tokens [a, b), inside [0, T)
+__device__ __forceinline__ void bounds_of(const int32_t* cu, int64_t s, int64_t T, int64_t* a, int64_t* b) {
+  *a = cu ? min(max<int64_t>(cu[s], 0), T) : 0;
+  *b = cu ? max(min(max<int64_t>(cu[s + 1], 0), T), *a) : T;
+}
+
+// The last of S sequences that starts at token t or before, 0 if none does, by the
+// wave's 64 probes at a time.
+__device__ __forceinline__ int64_t sequence_of(const int32_t* cu, int64_t S, int64_t t, int lane) {
+  int64_t lo = 0;
+  while (S > 1) {
+    const int64_t step = (S + 63) / 64, at = lane * step;
+    const int before = __popcll(__ballot(at < S && cu[lo + at] <= t));
+    const int64_t skip = (int64_t)max(before - 1, 0) * step;
+    lo += skip;
+    S = min(step, S - skip);
+  }
+  return lo;
+}
+
+// The two largest of two disjoint sets, each given by its two largest
+__device__ __forceinline__ void join_two(uint32_t& a, uint32_t& b, uint32_t c, uint32_t d) {
+  b = max(min(a, c), max(b, d));
+  a = max(a, c);
+}
+template <int CTRL>
+__device__ __forceinline__ void join_dpp(uint32_t& a, uint32_t& b) {
+  join_two(a, b, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, CTRL, 0xF, 0xF, false),
+           (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, CTRL, 0xF, 0xF, false));
 }
 
 }  // namespace
@@ -125,80 +223,117 @@ __device__ __forceinline__ void shares(float* score, float sum, bool softmax) {
 // ----------------------------------------------------------------------------
 // gate
 // ----------------------------------------------------------------------------
-template <int V>
+template <int V, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void moe_gate_kernel(const MoeGate p) {
-  __shared__ uint32_t keys[kWaves][64 * V];
+  __shared__ uint32_t slots[kWaves][64 * V];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
   if (t >= p.T) return;                                       // waves work apart: no barrier follows
-  const int E = (int)p.E, G = (int)p.groups, size = E / G;
-  float z[V], score[V];
-  load_logits<V>(p.logits, p.f32, t * p.ld, E, lane, z);
+  const int E = (int)p.E, G = (int)p.groups;
+  float z[V], top_z = 0.0f, all = 0.0f;
+  load_logits<V, VEC>(p.logits, p.f32, t * p.ld, E, lane, z);
   uint32_t key[V];
   if (p.bias) {
+    uint32_t b[V];
+    load_words<V, false>((const uint32_t*)p.bias, lane * V, E, 0, b);
+    float score[V];
     exact_scores<V>(z, p.softmax, score);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = lane * V + v;
-      const float k = score[v] + (e < E ? p.bias[e] : 0.0f);
+      const float k = score[v] + bits_f32(b[v]);
       key[v] = z[v] > minus_inf() && k > minus_inf() ? order_of(k) : 0;
+      slots[wave][lane * V + v] = f32_bits(score[v]);
     }
   } else {
-    scores<V>(z, p.softmax, score);
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = z[v] > minus_inf() ? order_of(z[v]) : 0;
+    if (p.softmax) {
+      top_z = z[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) top_z = fmaxf(top_z, z[v]);
+      top_z = wave_max(top_z);
+#pragma unroll
+      for (int v = 0; v < V; ++v) all += z[v] == minus_inf() ? 0.0f : z[v] == top_z ? 1.0f : exp_f32(z[v] - top_z);
+      all = wave_sum(all);
+    }
   }
   if (G > 1) {
+    const int size = E / G, lanes = size / V;                 // a group's lanes, where it has whole ones
+    uint32_t a = 0, b = 0;                                    // the two largest keys of the lane's group
+    if (size % V == 0 && (lanes & (lanes - 1)) == 0) {
+      a = key[0];
 #pragma unroll
-    for (int v = 0; v < V; ++v) keys[wave][lane * V + v] = key[v];
-    __builtin_amdgcn_wave_barrier();
-    __threadfence_block();
-    // lane g: the value of group g
-    uint32_t value = 0;
-    if (lane < G) {
-      uint32_t a = 0, b = 0;
-      for (int i = 0; i < size; ++i) {
-        const uint32_t k = keys[wave][lane * size + i];
-        b = max(b, min(a, k));
-        a = max(a, k);
+      for (int v = 1; v < V; ++v) join_two(a, b, key[v], 0);
+      // over 2, 4, 8, 16 lanes: those of a set already joined hold the same, so a mirror
+      // of a row's half, or of the row, brings the other half's
+      if (lanes >= 2) join_dpp<0xB1>(a, b);                   // quad_perm 1,0,3,2
+      if (lanes >= 4) join_dpp<0x4E>(a, b);                   // quad_perm 2,3,0,1
+      if (lanes >= 8) join_dpp<0x141>(a, b);                  // row_half_mirror
+      if (lanes >= 16) join_dpp<0x140>(a, b);                 // row_mirror
+      if (lanes >= 32) join_two(a, b, (uint32_t)__shfl_xor((int)a, 16), (uint32_t)__shfl_xor((int)b, 16));
+      const uint32_t value = p.bias && b ? order_of(float_of(a) + float_of(b)) : a;
+      const int mine = lane / lanes;
+      int before = 0;                                         // groups that come before the lane's
+      for (int g = 0; g < G; ++g) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)value, g * lanes);
+        before += o > value || (o == value && g < mine);
       }
-      value = p.bias && b ? order_of(float_of(a) + float_of(b)) : a;
-    }
-    int before = 0;                                           // groups that come before this one
-    for (int g = 0; g < G; ++g) {
-      const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)value, g);
-      before += o > value || (o == value && g < lane);
-    }
-    const uint64_t kept = __ballot(lane < G && before < (int)p.keep);
+      if (before >= (int)p.keep) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int g = min((lane * V + v) / size, G - 1);
-      if (!(kept >> g & 1)) key[v] = 0;
+        for (int v = 0; v < V; ++v) key[v] = 0;
+      }
+    } else {
+      // any size: keys through LDS, lane g looks at group g
+      __shared__ uint32_t keys[kWaves][64 * V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) keys[wave][lane * V + v] = key[v];
+      __threadfence_block();
+      __builtin_amdgcn_wave_barrier();
+      if (lane < G)
+        for (int i = 0; i < size; ++i) join_two(a, b, keys[wave][lane * size + i], 0);
+      const uint32_t value = p.bias && b ? order_of(float_of(a) + float_of(b)) : a;
+      int before = 0;
+      for (int g = 0; g < G; ++g) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)value, g);
+        before += o > value || (o == value && g < lane);
+      }
+      const uint64_t kept = __ballot(lane < G && before < (int)p.keep);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int g = min((lane * V + v) / size, G - 1);
+        if (!(kept >> g & 1)) key[v] = 0;
+      }
     }
   }
   int id = -1;
-  float w = 0.0f;
+  uint32_t mine = 0;
   for (int k = 0; k < (int)p.topk; ++k) {
     uint32_t best = key[0];
-    int at = 0;
 #pragma unroll
-    for (int v = 1; v < V; ++v)
-      if (key[v] > best) best = key[v], at = v;
-    const uint32_t top = wave_max_u32(best);
+    for (int v = 1; v < V; ++v) best = max(best, key[v]);
+    const uint32_t top = wave_max_uniform(best);
     if (top == 0) break;                                      // no expert is left
     const int who = __ffsll((unsigned long long)__ballot(best == top)) - 1;
-    float s = score[0];
+    int at = V - 1;
 #pragma unroll
-    for (int v = 1; v < V; ++v)
-      if (v == at) s = score[v];
+    for (int v = V - 2; v >= 0; --v)
+      if (key[v] == top) at = v;
     const int e = who * V + __builtin_amdgcn_readlane(at, who);
-    s = bits_f32((uint32_t)__builtin_amdgcn_readlane((int)f32_bits(s), who));
-    if (lane == k) id = e, w = s;
-    if (lane == who) {
+    if (lane == k) id = e, mine = top;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (v == at) key[v] = 0;
-    }
+    for (int v = 0; v < V; ++v)
+      if (lane * V + v == e) key[v] = 0;
+  }
+  // lane k: the score of the token's k-th expert
+  float w = 0.0f;
+  if (p.bias) {
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+    if (id >= 0) w = bits_f32(slots[wave][id]);
+  } else if (id >= 0) {
+    const float zk = float_of(mine);
+    if (!p.softmax) w = sigmoid_of(zk, exp_f32(-fabsf(zk)));
+    else w = (zk == top_z ? 1.0f : exp_f32(zk - top_z)) * __fdiv_rn(1.0f, all);
   }
   if (p.normalize) {
     const float sum = wave_sum(w);
@@ -210,145 +345,210 @@ __global__ __launch_bounds__(64 * kWaves) void moe_gate_kernel(const MoeGate p) 
   }
 }
 
-// V registers a lane for E experts
-#define FP8BS_BY_EXPERTS(E, CALL)      \
-  if ((E) <= 64) { CALL(1); }          \
-  else if ((E) <= 128) { CALL(2); }    \
-  else if ((E) <= 256) { CALL(4); }    \
-  else if ((E) <= 512) { CALL(8); }    \
-  else { CALL(16); }
+namespace {
+
+// Calls CALL(V, VEC) with V registers a lane for E experts; VEC where rows are read V logits at a time.
+#define FP8BS_BY_EXPERTS(p, CALL)                                                   \
+  {                                                                                 \
+    const int V = experts_a_lane((p).E);                                            \
+    const bool vec = wide_rows((p).logits, (p).ld, (p).E, V, (p).f32);              \
+    if (V == 1) { CALL(1, false); }                                                 \
+    else if (V == 2) { if (vec) { CALL(2, true); } else { CALL(2, false); } }       \
+    else if (V == 4) { if (vec) { CALL(4, true); } else { CALL(4, false); } }       \
+    else if (V == 8) { if (vec) { CALL(8, true); } else { CALL(8, false); } }       \
+    else { if (vec) { CALL(16, true); } else { CALL(16, false); } }                 \
+  }
+int experts_a_lane(int64_t E) { return E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16; }
+bool wide_rows(const void* p, int64_t ld, int64_t E, int V, bool f32) {
+  const int wide = std::min(V * (f32 ? 4 : 2), 16);
+  return V > 1 && E % V == 0 && ld % V == 0 && (uintptr_t)p % wide == 0;
+}
+
+}  // namespace
 
 hipError_t launch_moe_gate(const MoeGate& p, hipStream_t stream) {
   const dim3 grid((unsigned)((p.T + kWaves - 1) / kWaves)), block(64 * kWaves);
-#define CALL(V) moe_gate_kernel<V><<<grid, block, 0, stream>>>(p)
-  FP8BS_BY_EXPERTS(p.E, CALL)
+#define CALL(V, VEC) moe_gate_kernel<V, VEC><<<grid, block, 0, stream>>>(p)
+  FP8BS_BY_EXPERTS(p, CALL)
 #undef CALL
   return hipGetLastError();
 }
 
 // ----------------------------------------------------------------------------
-// balance: workgroup (c, s) takes part c of sequence s's tokens, one a wave at a
-// time; a lane adds its experts' shares up in registers.  The second kernel adds
-// the parts in order and makes the loss; one part needs none.
+// balance.  Workgroup b takes tokens [b*R, (b+1)*R), whatever the sequences'
+// lengths; of each sequence that has some of them it leaves the sums of shares and
+// the counts in slot b + s of the workspace (b + s grows by one from a workgroup's
+// sequence to the next one's, so no two share a slot).  The second kernel adds a
+// sequence's slots up, which lie next to each other, in order, and makes its loss.
 // ----------------------------------------------------------------------------
 namespace {
 
 constexpr int kBalanceWaves = 8;
-constexpr int kBalanceRows = 64;     // tokens that a part is meant to have
-constexpr int kBalanceParts = 2048;  // workgroups that more parts are not worth
+constexpr int kBalanceRows = 16;     // tokens of a workgroup: two a wave
+constexpr int kBalanceGroups = 512;  // more workgroups than this take more tokens each
 
-int64_t balance_parts(int64_t T, int64_t S) {
-  const int64_t by_rows = (T + kBalanceRows - 1) / kBalanceRows;
-  return std::max<int64_t>(1, std::min<int64_t>(by_rows, kBalanceParts / std::max<int64_t>(S, 1)));
+struct BalancePlan {
+  int64_t rows, groups, width;       // tokens a workgroup, workgroups, floats of a slot
+};
+BalancePlan balance_plan(int64_t T, int64_t E) {
+  const int64_t least = (T + kBalanceGroups - 1) / kBalanceGroups;
+  const int64_t rows = std::max<int64_t>(kBalanceRows, (least + kBalanceWaves - 1) / kBalanceWaves * kBalanceWaves);
+  return {rows, (T + rows - 1) / rows, (E + 3) / 4 * 4};
 }
 
-// Sequence s's tokens [a, b), inside [0, T)
-__device__ __forceinline__ void bounds_of(const int32_t* cu, int64_t s, int64_t T, int64_t* a, int64_t* b) {
-  *a = cu ? min(max<int64_t>(cu[s], 0), T) : 0;
-  *b = cu ? max(min(max<int64_t>(cu[s + 1], 0), T), *a) : T;
-}
-
-// loss of one sequence, by the first wave: E / (topk * n) * sum counts * probs
-__device__ __forceinline__ void write_loss(float part, int64_t n, const MoeBalance& p, int64_t s) {
+// A sequence's results from its sums, by one workgroup: probs, counts, and the loss
+// E / (topk * n) * sum counts * probs.  get(e, &shares, &hits); `red` one float a wave.
+template <typename F>
+__device__ __forceinline__ void finish_sequence(const MoeBalance& p, int64_t s, int64_t n, float* red, F get) {
+  const int E = (int)p.E;
+  const float mean = n > 0 ? __fdiv_rn(1.0f, (float)n) : 0.0f;
+  float part = 0.0f;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    float q;
+    int32_t h;
+    get(e, &q, &h);
+    q *= mean;
+    p.probs[s * E + e] = q;
+    p.counts[s * E + e] = h;
+    part = __builtin_fmaf(q, (float)h, part);
+  }
   part = wave_sum(part);
-  if (threadIdx.x == 0) p.loss[s] = n > 0 ? part * __fdiv_rn((float)p.E, (float)p.topk * (float)n) : 0.0f;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = part;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    part = 0.0f;
+    for (int w = 0; w < (int)blockDim.x / 64; ++w) part += red[w];
+    p.loss[s] = n > 0 ? part * __fdiv_rn((float)E, (float)p.topk * (float)n) : 0.0f;
+  }
+  __syncthreads();
 }
 
 }  // namespace
 
-template <int V>
-__global__ __launch_bounds__(64 * kBalanceWaves) void moe_balance_kernel(const MoeBalance p, int64_t parts) {
+// ONE: the only workgroup, which makes the results of every sequence itself.
+template <int V, bool VEC, bool ONE>
+__global__ __launch_bounds__(64 * kBalanceWaves) void moe_balance_kernel(const MoeBalance p, int64_t rows, int64_t width) {
   __shared__ float sums[kBalanceWaves][64 * V];
   __shared__ int32_t hits[64 * V];
+  __shared__ float red[kBalanceWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t s = blockIdx.x / parts, c = blockIdx.x % parts;
   const int E = (int)p.E;
-  for (int i = threadIdx.x; i < 64 * V; i += 64 * kBalanceWaves) hits[i] = 0;
-  __syncthreads();
-  int64_t a, b;
-  bounds_of(p.cu, s, p.T, &a, &b);
-  const int64_t n = b - a, lo = a + n * c / parts, hi = a + n * (c + 1) / parts;
-  float acc[V];
+  const int64_t lo = (int64_t)blockIdx.x * rows, hi = min(lo + rows, p.T);
+  int64_t s = p.cu && !ONE ? sequence_of(p.cu, p.S, lo, lane) : 0;
+  for (; s < p.S; ++s) {
+    int64_t a, b;
+    bounds_of(p.cu, s, p.T, &a, &b);
+    if (!ONE && a >= hi) break;
+    const int64_t n = b - a;
+    a = max(a, lo);
+    b = min(b, hi);
+    if (!ONE && a >= b) continue;
+    for (int i = threadIdx.x; i < 64 * V; i += 64 * kBalanceWaves) hits[i] = 0;
+    __syncthreads();
+    float acc[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-  for (int64_t t = lo + wave; t < hi; t += kBalanceWaves) {
-    float z[V], score[V];
-    load_logits<V>(p.logits, p.f32, t * p.ld, E, lane, z);
-    const float sum = scores<V>(z, p.softmax, score);
-    shares<V>(score, sum, p.softmax);
+    for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+    for (int64_t t = a + wave; t < b; t += kBalanceWaves) {
+      int32_t id = lane < (int)p.topk ? p.indices[t * p.topk + lane] : -1;
+      float z[V], score[V];
+      load_logits<V, VEC>(p.logits, p.f32, t * p.ld, E, lane, z);
+      const float sum = scores<V>(z, p.softmax, score);
+      shares<V>(score, sum, p.softmax);
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] += score[v];
-    for (int k = lane; k < (int)p.topk; k += 64) {
-      const int32_t e = p.indices[t * p.topk + k];
-      if (e >= 0 && e < E) atomicAdd(&hits[e], 1);            // whole numbers: any order gives the same
+      for (int v = 0; v < V; ++v) acc[v] += score[v];
+      if (id >= 0 && id < E) atomicAdd(&hits[id], 1);         // whole numbers: any order gives the same
     }
-  }
 #pragma unroll
-  for (int v = 0; v < V; ++v) sums[wave][lane * V + v] = acc[v];
-  __syncthreads();
-  const float mean = n > 0 ? __fdiv_rn(1.0f, (float)n) : 0.0f;
-  float* pr = parts > 1 ? p.part_probs + (s * parts + c) * p.E : p.probs + s * p.E;
-  int32_t* co = parts > 1 ? p.part_counts + (s * parts + c) * p.E : p.counts + s * p.E;
-  for (int e = threadIdx.x; e < E; e += 64 * kBalanceWaves) {
-    float q = 0.0f;
-    for (int w = 0; w < kBalanceWaves; ++w) q += sums[w][e];
-    if (parts == 1) q *= mean;
-    pr[e] = q;
-    co[e] = hits[e];
-    sums[0][e] = q * (float)hits[e];
-  }
-  if (parts > 1) return;
-  __syncthreads();
-  if (wave == 0) {
-    float part = 0.0f;
-    for (int e = lane; e < E; e += 64) part += sums[0][e];
-    write_loss(part, n, p, s);
+    for (int v = 0; v < V; ++v) sums[wave][lane * V + v] = acc[v];
+    __syncthreads();
+    const auto get = [&](int e, float* q, int32_t* h) {
+      *q = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kBalanceWaves; ++w) *q += sums[w][e];
+      *h = hits[e];
+    };
+    if (ONE) {
+      finish_sequence(p, s, n, red, get);
+    } else {
+      const int64_t slot = (blockIdx.x + s) * width;
+      for (int e = threadIdx.x; e < (int)width; e += 64 * kBalanceWaves) {
+        float q = 0.0f;
+        int32_t h = 0;
+        if (e < E) get(e, &q, &h);
+        p.part_probs[slot + e] = q;
+        p.part_counts[slot + e] = h;
+      }
+      __syncthreads();
+    }
   }
 }
 
-__global__ __launch_bounds__(256) void moe_balance_join_kernel(const MoeBalance p, int64_t parts) {
-  __shared__ float red[1024];
+constexpr int kJoinThreads = 1024;
+__global__ __launch_bounds__(kJoinThreads) void moe_balance_join_kernel(const MoeBalance p, int64_t rows, int64_t width) {
+  __shared__ float4 sums[kJoinThreads];
+  __shared__ int4 hits[kJoinThreads];
+  __shared__ float red[kJoinThreads / 64];
   const int64_t s = blockIdx.x;
-  const int E = (int)p.E;
   int64_t a, b;
   bounds_of(p.cu, s, p.T, &a, &b);
-  const int64_t n = b - a;
-  const float mean = n > 0 ? __fdiv_rn(1.0f, (float)n) : 0.0f;
-  for (int e = threadIdx.x; e < E; e += 256) {
-    float q = 0.0f;
-    int32_t h = 0;
-    for (int64_t c = 0; c < parts; ++c) {
-      q += p.part_probs[(s * parts + c) * p.E + e];
-      h += p.part_counts[(s * parts + c) * p.E + e];
+  const int64_t first = a / rows, last = b > a ? (b - 1) / rows + 1 : first;   // workgroups with some of its tokens
+  // a thread adds up 4 experts of every `groups`-th slot, 4 slots' loads at a time
+  const int cols = (int)(width / 4), groups = min(kJoinThreads / cols, 64);
+  const int col = (int)threadIdx.x % cols, grp = (int)threadIdx.x / cols;
+  float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  int4 h = make_int4(0, 0, 0, 0);
+  if (grp < groups) {
+    for (int64_t g = first + grp; g < last; g += 4 * groups) {
+      float4 x[4];
+      int4 y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t slot = min(g + i * groups, last - 1) + s;
+        x[i] = ((const float4*)(p.part_probs + slot * width))[col];
+        y[i] = ((const int4*)(p.part_counts + slot * width))[col];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (g + i * groups >= last) break;
+        q.x += x[i].x, q.y += x[i].y, q.z += x[i].z, q.w += x[i].w;
+        h.x += y[i].x, h.y += y[i].y, h.z += y[i].z, h.w += y[i].w;
+      }
     }
-    q *= mean;
-    p.probs[s * p.E + e] = q;
-    p.counts[s * p.E + e] = h;
-    red[e] = q * (float)h;
+    sums[grp * cols + col] = q;
+    hits[grp * cols + col] = h;
   }
   __syncthreads();
-  if (threadIdx.x < 64) {
-    float part = 0.0f;
-    for (int e = threadIdx.x; e < E; e += 64) part += red[e];
-    write_loss(part, n, p, s);
-  }
+  finish_sequence(p, s, b - a, red, [&](int e, float* q, int32_t* h) {
+    *q = 0.0f;
+    *h = 0;
+    for (int g = 0; g < groups; ++g) {
+      *q += ((const float*)sums)[g * width + e];
+      *h += ((const int32_t*)hits)[g * width + e];
+    }
+  });
 }
+
+// One workgroup makes all of few tokens' results, unless there are many (empty) sequences to go through.
+static bool balance_at_once(const BalancePlan& plan, int64_t S) { return plan.groups <= 1 && S <= 64; }
 
 int64_t moe_balance_workspace_bytes(int64_t T, int64_t S, int64_t E) {
-  const int64_t parts = balance_parts(T, S);
-  return parts > 1 ? 8 * S * parts * E : 0;
+  const BalancePlan plan = balance_plan(T, E);
+  return balance_at_once(plan, S) ? 0 : 8 * (plan.groups + S) * plan.width;
 }
 
 hipError_t launch_moe_balance(const MoeBalance& q, hipStream_t stream) {
   MoeBalance p = q;
-  const int64_t parts = balance_parts(p.T, p.S);
+  const BalancePlan plan = balance_plan(p.T, p.E);
+  const bool one = balance_at_once(plan, p.S);
   p.part_probs = (float*)p.workspace;
-  p.part_counts = (int32_t*)p.workspace + p.S * parts * p.E;
-  const dim3 grid((unsigned)(p.S * parts)), block(64 * kBalanceWaves);
-#define CALL(V) moe_balance_kernel<V><<<grid, block, 0, stream>>>(p, parts)
-  FP8BS_BY_EXPERTS(p.E, CALL)
+  p.part_counts = (int32_t*)p.workspace + (plan.groups + p.S) * plan.width;
+  const dim3 grid((unsigned)std::max<int64_t>(plan.groups, 1)), block(64 * kBalanceWaves);
+#define CALL(V, VEC)                                                                                        \
+  if (one) moe_balance_kernel<V, VEC, true><<<grid, block, 0, stream>>>(p, plan.rows, plan.width);          \
+  else moe_balance_kernel<V, VEC, false><<<grid, block, 0, stream>>>(p, plan.rows, plan.width)
+  FP8BS_BY_EXPERTS(p, CALL)
 #undef CALL
-  if (parts > 1) moe_balance_join_kernel<<<dim3((unsigned)p.S), dim3(256), 0, stream>>>(p, parts);
+  if (!one) moe_balance_join_kernel<<<dim3((unsigned)p.S), dim3(kJoinThreads), 0, stream>>>(p, plan.rows, plan.width);
   return hipGetLastError();
 }
 
@@ -362,64 +562,58 @@ hipError_t launch_moe_balance(const MoeBalance& q, hipStream_t stream) {
 //     (not normalised: scale * dw_k score_k)
 //   sigmoid: dz_i = u_i (1 - score_i);  softmax: dz_i = u_i - score_i sum_j u_j
 // ----------------------------------------------------------------------------
-template <int V>
+template <int V, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void moe_gate_bwd_kernel(const MoeGateBwd p) {
+  __shared__ float slots[kWaves][64 * V];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
   if (t >= p.T) return;
-  const int E = (int)p.E;
+  const int E = (int)p.E, K = (int)p.topk;
+  int e = -1;
+  float uk = 0.0f;
+  if (p.d_weights && lane < K) {
+    e = p.indices[t * p.topk + lane];
+    uk = p.d_weights[t * p.topk + lane];
+    if (e < 0 || e >= E) e = -1, uk = 0.0f;
+  }
   float z[V], score[V], u[V];
-  load_logits<V>(p.logits, p.f32, t * p.ld, E, lane, z);
+  load_logits<V, VEC>(p.logits, p.f32, t * p.ld, E, lane, z);
+  // the token's sequence, asked for before the scores are made
+  int64_t a = 0, b = 0;
+  uint32_t hits[V];
+  float dl = 0.0f;
+  if (p.d_loss) {
+    const int64_t s = p.cu ? sequence_of(p.cu, p.S, t, lane) : 0;
+    bounds_of(p.cu, s, p.T, &a, &b);
+    load_words<V, false>((const uint32_t*)p.counts + s * E, lane * V, E, 0, hits);
+    dl = p.d_loss[s];
+  }
   const float sum = scores<V>(z, p.softmax, score);
 #pragma unroll
   for (int v = 0; v < V; ++v) u[v] = 0.0f;
-  if (p.d_loss) {
-    // the sequence that holds t: the last with cu[s] <= t
-    int64_t s = 0;
-    if (p.cu) {
-      int64_t hi = p.S;
-      while (hi - s > 1) {
-        const int64_t mid = (s + hi) / 2;
-        if (p.cu[mid] <= t) s = mid;
-        else hi = mid;
-      }
-    }
-    int64_t a, b;
-    bounds_of(p.cu, s, p.T, &a, &b);
-    if (t >= a && t < b && sum > 0.0f) {
-      const float n = (float)(b - a);
-      const float c = __fdiv_rn(__fdiv_rn(p.d_loss[s] * (float)E, (float)p.topk * n), n);
-      float share[V], mean = 0.0f;
+  if (p.d_loss && t >= a && t < b) {
+    const float n = (float)(b - a);
+    const float c = __fdiv_rn(__fdiv_rn(dl * (float)E, (float)K * n), n);
+    float share[V], mean = 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) share[v] = score[v];
-      shares<V>(share, sum, p.softmax);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = lane * V + v;
-        u[v] = e < E ? c * (float)p.counts[s * p.E + e] : 0.0f;
-        mean = __builtin_fmaf(u[v], share[v], mean);
-      }
-      mean = wave_sum(mean);
-#pragma unroll
-      for (int v = 0; v < V; ++v) u[v] = (u[v] - mean) * share[v];
-    }
-  }
-  if (p.d_weights) {
-    const int K = (int)p.topk;
-    int e = -1;
-    float uk = 0.0f, own = 0.0f;
-    if (lane < K) {
-      e = p.indices[t * p.topk + lane];
-      uk = p.d_weights[t * p.topk + lane];
-      if (e < 0 || e >= E) e = -1;
-    }
-    // lane k: the score of the token's k-th expert
+    for (int v = 0; v < V; ++v) share[v] = score[v];
+    shares<V>(share, sum, p.softmax);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float o = __shfl(score[v], e < 0 ? 0 : e / V);
-      if (e >= 0 && e % V == v) own = o;
+      u[v] = c * (float)(int32_t)hits[v];
+      mean = __builtin_fmaf(u[v], share[v], mean);
     }
-    if (e < 0) uk = 0.0f;
+    mean = wave_sum(mean);
+#pragma unroll
+    for (int v = 0; v < V; ++v) u[v] = (u[v] - mean) * share[v];
+  }
+  if (p.d_weights) {
+    // lane k: the score of the token's k-th expert
+#pragma unroll
+    for (int v = 0; v < V; ++v) slots[wave][lane * V + v] = score[v];
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+    float own = e >= 0 ? slots[wave][e] : 0.0f;
     if (p.normalize) {
       const float S = wave_sum(own);
       own = S > 0.0f ? __fdiv_rn(own, S) : 0.0f;
@@ -430,8 +624,7 @@ __global__ __launch_bounds__(64 * kWaves) void moe_gate_bwd_kernel(const MoeGate
       const int ek = __builtin_amdgcn_readlane(e, k);
       const float add = bits_f32((uint32_t)__builtin_amdgcn_readlane((int)f32_bits(uk), k));
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (ek == lane * V + v) u[v] += add;
+      for (int v = 0; v < V; ++v) u[v] += ek == lane * V + v ? add : 0.0f;
     }
   }
   float all = 0.0f;
@@ -440,26 +633,51 @@ __global__ __launch_bounds__(64 * kWaves) void moe_gate_bwd_kernel(const MoeGate
     for (int v = 0; v < V; ++v) all += u[v];
     all = wave_sum(all);
   }
+  float dz[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = lane * V + v;
-    if (e >= E) continue;
-    float dz;
     if (p.softmax) {
-      dz = __builtin_fmaf(-score[v], all, u[v]);
+      dz[v] = __builtin_fmaf(-score[v], all, u[v]);
     } else {
-      const float x = expf(-fabsf(z[v]));                     // 1 - score without the cancellation near 1
-      dz = u[v] * __fdiv_rn(z[v] < 0.0f ? 1.0f : x, 1.0f + x);
+      const float x = exp_f32(-fabsf(z[v]));                  // 1 - score without the cancellation near 1
+      dz[v] = u[v] * sigmoid_of(-z[v], x);
     }
-    if (p.out_f32) ((float*)p.d_logits)[t * p.E + e] = dz;
-    else ((uint16_t*)p.d_logits)[t * p.E + e] = (uint16_t)pack2_bf16(dz, 0.0f);
+  }
+  const int64_t at = t * E + lane * V;
+  if (VEC) {
+    if (lane * V >= E) return;
+    if (p.out_f32) {
+      if (V >= 4) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4)
+          *(float4*)((float*)p.d_logits + at + v) = make_float4(dz[v], dz[(v + 1) % V], dz[(v + 2) % V], dz[(v + 3) % V]);
+      } else {
+        *(float2*)((float*)p.d_logits + at) = make_float2(dz[0], dz[1 % V]);
+      }
+    } else {
+      if (V >= 4) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4)
+          *(uint2*)((uint16_t*)p.d_logits + at + v) =
+              make_uint2(pack2_bf16(dz[v], dz[(v + 1) % V]), pack2_bf16(dz[(v + 2) % V], dz[(v + 3) % V]));
+      } else {
+        *(uint32_t*)((uint16_t*)p.d_logits + at) = pack2_bf16(dz[0], dz[1 % V]);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (lane * V + v >= E) continue;
+    if (p.out_f32) ((float*)p.d_logits)[at + v] = dz[v];
+    else ((uint16_t*)p.d_logits)[at + v] = (uint16_t)pack2_bf16(dz[v], 0.0f);
   }
 }
 
 hipError_t launch_moe_gate_bwd(const MoeGateBwd& p, hipStream_t stream) {
   const dim3 grid((unsigned)((p.T + kWaves - 1) / kWaves)), block(64 * kWaves);
-#define CALL(V) moe_gate_bwd_kernel<V><<<grid, block, 0, stream>>>(p)
-  FP8BS_BY_EXPERTS(p.E, CALL)
+#define CALL(V, VEC) moe_gate_bwd_kernel<V, VEC><<<grid, block, 0, stream>>>(p)
+  FP8BS_BY_EXPERTS(p, CALL)
 #undef CALL
   return hipGetLastError();
 }

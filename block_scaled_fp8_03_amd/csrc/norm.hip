@@ -18,26 +18,18 @@ namespace {
 
 constexpr int kThreads = 256;        // of a workgroup with several rows
 constexpr int kMaxThreads = 1024;    // of a workgroup with one
-constexpr int kMaxVpl = 4;           // 8-element vectors of a row that a lane holds
-
-// Sum over the 16 lanes of a DPP row; every lane receives it.
-__device__ __forceinline__ float row16_sum(float v) {
-  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0xB1, 0xF, 0xF, false));
-  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0x4E, 0xF, 0xF, false));
-  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0x124, 0xF, 0xF, false));
-  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0x128, 0xF, 0xF, false));
-  return v;
-}
+constexpr int kMaxK = 32768;
 
 // Sum over the TPR lanes of a row (TPR 16, 32, 64: inside a wave; 0: the workgroup,
 // through `red`, one float a wave).
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* red) {
-  v = row16_sum(v);
-  if (TPR == 16) return v;
-  v += __shfl_xor(v, 16);
-  if (TPR == 32) return v;
-  v += __shfl_xor(v, 32);
+  if (TPR == 16) return row16_sum(v);
+  if (TPR == 32) {
+    v = row16_sum(v);
+    return v + __shfl_xor(v, 16);
+  }
+  v = wave_sum(v);
   if (TPR == 64) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -47,14 +39,6 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 }
 
 // 8 elements of a row as floats
-__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
 template <bool F32>
 __device__ __forceinline__ void load8(const void* p, int64_t v, float* f) {
   if (F32) {
@@ -64,9 +48,6 @@ __device__ __forceinline__ void load8(const void* p, int64_t v, float* f) {
   } else {
     unpack8(((const uint4*)p)[v], f);
   }
-}
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7]));
 }
 template <bool F32>
 __device__ __forceinline__ void store8(void* p, int64_t v, const float* f) {
@@ -129,15 +110,8 @@ __global__ __launch_bounds__(TPR ? kThreads : kMaxThreads) void rmsnorm_kernel(c
     for (int i = 0; i < 8; ++i) c[i] = t[j][i] * r * c[i];
     if (p.y) store_nt((uint4*)p.y + at, pack8(c));
     if (p.q) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, f32_bits(c[i]) & 0x7FFFFFFFu);
-      top = row16_max_u32(top);
-      const float sc = p.ue8m0 ? block_scale<true>(bits_f32(top)) : block_scale<false>(bits_f32(top));
-      const float rs = __fdiv_rn(1.0f, sc);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = div_markstein(c[i], sc, rs);
-      store_nt((uint2*)p.q + at, make_uint2(pack4_e4m3(c[0], c[1], c[2], c[3]), pack4_e4m3(c[4], c[5], c[6], c[7])));
+      float sc;
+      store_nt((uint2*)p.q + at, quant8(c, p.ue8m0, &sc));
       if ((lane & 15) == 0) p.s[at / 16] = sc;
     }
   }
@@ -177,7 +151,7 @@ void launch_fwd(const RmsNorm& p, hipStream_t stream) {
 
 // A row's widest workgroup: K up to 32768, one workgroup a row, at most 2^32 - 1 threads.
 bool rmsnorm_fits(int64_t M, int64_t K) {
-  return K <= (int64_t)kMaxThreads * kMaxVpl * 8 && M <= (((int64_t)1 << 32) - 1) / kMaxThreads;
+  return K <= kMaxK && M <= (((int64_t)1 << 32) - 1) / kMaxThreads;
 }
 
 hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t stream) {
@@ -197,62 +171,145 @@ hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t stream) {
 // ----------------------------------------------------------------------------
 namespace {
 
-constexpr int kBwdGroups = 512;       // parts of dw at most
+#ifndef GROUPS
+#define GROUPS 512
+#endif
+#ifndef AHEAD_
+#define AHEAD_ 1
+#endif
+constexpr int kBwdGroups = GROUPS;       // parts of dw at most
+constexpr int kBwdThreads = 512;      // of a workgroup at most: 256 registers a lane
+
+// as plan_of, with at most kBwdThreads where a row is held
+RowPlan bwd_plan_of(int64_t K) {
+  const int64_t nv = K / 8;
+  if (nv <= 64) return plan_of(K);
+  if (nv > 4 * kBwdThreads) return {kMaxThreads, 0};         // rows read twice
+  const int vpl = nv <= kBwdThreads ? 1 : nv <= 2 * kBwdThreads ? 2 : 4;
+  return {(int)((nv + 64 * vpl - 1) / (64 * vpl)) * 64, vpl};
+}
 
 // rows that a workgroup takes at a time
 int rows_at_once(const RowPlan& plan) { return plan.tpr <= 64 ? kThreads / plan.tpr : 1; }
 int64_t bwd_groups(int64_t M, int64_t K) {
-  const int rows = rows_at_once(plan_of(K));
+  const int rows = rows_at_once(bwd_plan_of(K));
   return std::min<int64_t>((M + rows - 1) / rows, kBwdGroups);
 }
 
 }  // namespace
 
-template <int TPR, int VPL, bool F32>
-__global__ __launch_bounds__(TPR ? kThreads : kMaxThreads) void rmsnorm_bwd_kernel(const RmsNormBwd p, float* parts) {
+namespace {
+
+// 8 elements as they lie in memory: they are held so, and made floats where they are used
+template <bool F32>
+struct Raw8 {
+  uint4 u[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t v) {
+    u[0] = ((const uint4*)p)[F32 ? 2 * v : v];
+    if (F32) u[F32 ? 1 : 0] = ((const uint4*)p)[2 * v + 1];
+  }
+  __device__ __forceinline__ void floats(float* f) const {
+    if (F32) {
+      const uint4 a = u[0], b = u[F32 ? 1 : 0];
+      f[0] = bits_f32(a.x), f[1] = bits_f32(a.y), f[2] = bits_f32(a.z), f[3] = bits_f32(a.w);
+      f[4] = bits_f32(b.x), f[5] = bits_f32(b.y), f[6] = bits_f32(b.z), f[7] = bits_f32(b.w);
+    } else {
+      unpack8(u[0], f);
+    }
+  }
+};
+
+// What a lane holds of a row
+template <int VPL, bool F32>
+struct RowHeld {
+  Raw8<F32> h[VPL], e[VPL];
+  Raw8<false> d[VPL];
+  __device__ __forceinline__ void load(const RmsNormBwd& p, int64_t m, int j, int v, bool res) {
+    h[j].load((const char*)p.h + m * p.ld_h * (F32 ? 4 : 2), v);
+    d[j].load((const char*)p.dy + m * p.K * 2, v);
+    if (res && p.dres) e[j].load((const char*)p.dres + m * p.K * (F32 ? 4 : 2), v);
+  }
+};
+
+}  // namespace
+
+// HOLD 2: VPL vectors a lane are held, and the next row's asked for before this one's
+// sums are waited for; 1: held; 0: rows too wide for that are read twice (the second
+// time from L2), vector by vector, and dw lies in LDS.
+template <int TPR, int VPL, int HOLD, bool F32, bool W_F32>
+__global__ __launch_bounds__(TPR ? kThreads : HOLD ? kBwdThreads : kMaxThreads) void rmsnorm_bwd_kernel(
+    const RmsNormBwd p, float* parts) {
   __shared__ float red[4][kMaxThreads / 64];
   __shared__ float rows_dw[TPR ? kThreads * 8 : 1];
+  __shared__ float4 wide_dw[HOLD ? 1 : kMaxK / 4];
   const int tpr = TPR ? TPR : (int)blockDim.x;
   const int lane = TPR ? (int)threadIdx.x % TPR : (int)threadIdx.x;
   const int rows = TPR ? kThreads / TPR : 1;
   const int mine = TPR ? (int)threadIdx.x / TPR : 0;
   const int nv = (int)(p.K / 8);
   const float rk = (float)p.K;
-  float w[VPL][8], dw[VPL][8];
+  const int64_t step = (int64_t)gridDim.x * rows;
+  constexpr int HV = HOLD ? VPL : 1;
+  Raw8<W_F32> w[HV];
+  RowHeld<HV, F32> row, next;
+  float dw[HV][8];
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int vv = min(lane + j * tpr, nv - 1);
-    if (p.w_f32) load8<true>(p.w, vv, w[j]);
-    else load8<false>(p.w, vv, w[j]);
+  for (int j = 0; j < HV; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
-  }
-  int turn = 0;
-  for (int64_t m0 = (int64_t)blockIdx.x * rows; m0 < p.M; m0 += (int64_t)gridDim.x * rows, turn ^= 1) {
-    const int64_t m = m0 + mine, mm = min(m, p.M - 1);
-    float h[VPL][8], d[VPL][8];
-    float hh = 0.0f, gh = 0.0f;
+  int64_t m0 = (int64_t)blockIdx.x * rows;
+  if (HOLD) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int v = lane + j * tpr, vv = min(v, nv - 1);
-      load8<F32>((const char*)p.h + mm * p.ld_h * (F32 ? 4 : 2), vv, h[j]);
-      load8<false>(p.dy, mm * nv + vv, d[j]);
+    for (int j = 0; j < HV; ++j) {
+      const int v = min(lane + j * tpr, nv - 1);
+      w[j].load(p.w, v);
+      if (HOLD == 2) next.load(p, min(m0 + mine, p.M - 1), j, v, true);
+    }
+  } else {
+    for (int v = lane; v < nv; v += tpr) wide_dw[2 * v] = wide_dw[2 * v + 1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  for (int turn = 0; m0 < p.M; m0 += step, turn ^= 1) {
+    const int64_t m = m0 + mine;
+    float hh = 0.0f, gh = 0.0f;
+    const auto add_up = [&](int j, bool on) {
+      float h[8], d[8], g[8];
+      row.h[j].floats(h);
+      row.d[j].floats(d);
+      w[j].floats(g);
       float a = 0.0f, b = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        a = __builtin_fmaf(h[j][i], h[j][i], a);
-        b = __builtin_fmaf(d[j][i] * w[j][i], h[j][i], b);
+        a = __builtin_fmaf(h[i], h[i], a);
+        b = __builtin_fmaf(d[i] * g[i], h[i], b);
       }
-      hh += v < nv ? a : 0.0f;
-      gh += v < nv ? b : 0.0f;
+      hh += on ? a : 0.0f;
+      gh += on ? b : 0.0f;
+    };
+    if (HOLD) {
+      if (HOLD == 2) row = next;
+#pragma unroll
+      for (int j = 0; j < HV; ++j) {
+        const int v = min(lane + j * tpr, nv - 1);
+        if (HOLD == 2) next.load(p, min(m + step, p.M - 1), j, v, true);
+        else row.load(p, m, j, v, true);
+      }
+#pragma unroll
+      for (int j = 0; j < HV; ++j) add_up(j, lane + j * tpr < nv);
+    } else {
+#pragma unroll 2
+      for (int v = lane; v < nv; v += tpr) {
+        row.load(p, m, 0, v, false);
+        w[0].load(p.w, v);
+        add_up(0, true);
+      }
     }
     // two buffers in turn: a wave may be at the next row's sums while another still reads this one's
     if (TPR) {
       hh = row_sum<TPR>(hh, nullptr);
       gh = row_sum<TPR>(gh, nullptr);
     } else {
-      hh = row_sum<64>(hh, nullptr);
-      gh = row_sum<64>(gh, nullptr);
+      hh = wave_sum(hh);
+      gh = wave_sum(gh);
       if ((threadIdx.x & 63) == 0) {
         red[2 * turn][threadIdx.x >> 6] = hh;
         red[2 * turn + 1][threadIdx.x >> 6] = gh;
@@ -266,20 +323,39 @@ __global__ __launch_bounds__(TPR ? kThreads : kMaxThreads) void rmsnorm_bwd_kern
     }
     const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(hh, rk) + p.eps));
     const float c = r * r * __fdiv_rn(gh, rk);
-    if (m < p.M) {
+    const auto finish = [&](int j, int v, float* sum) {
+      float h[8], d[8], g[8], e[8];
+      row.h[j].floats(h);
+      row.d[j].floats(d);
+      w[j].floats(g);
+      if (p.dres) row.e[j].floats(e);
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        const int v = lane + j * tpr;
-        if (v >= nv) break;
-        float o[8], e[8];
-        if (p.dres) load8<F32>(p.dres, m * nv + v, e);
+      for (int i = 0; i < 8; ++i) {
+        float o = r * __builtin_fmaf(-h[i], c, d[i] * g[i]);
+        if (p.dres) o += e[i];
+        sum[i] = __builtin_fmaf(d[i], h[i] * r, sum[i]);
+        e[i] = o;
+      }
+      store8<F32>(p.dx, m * nv + v, e);
+    };
+    if (HOLD) {
+      if (m < p.M) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i] = r * __builtin_fmaf(-h[j][i], c, d[j][i] * w[j][i]);
-          if (p.dres) o[i] += e[i];
-          dw[j][i] = __builtin_fmaf(d[j][i], h[j][i] * r, dw[j][i]);
+        for (int j = 0; j < HV; ++j) {
+          const int v = lane + j * tpr;
+          if (v >= nv) break;
+          finish(j, v, dw[j]);
         }
-        store8<F32>(p.dx, m * nv + v, o);
+      }
+    } else {
+      for (int v = lane; v < nv; v += tpr) {
+        row.load(p, m, 0, v, true);
+        w[0].load(p.w, v);
+        float sum[8];
+        load8<true>(wide_dw, v, sum);
+        finish(0, v, sum);
+        wide_dw[2 * v] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        wide_dw[2 * v + 1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
       }
     }
   }
@@ -295,33 +371,42 @@ __global__ __launch_bounds__(TPR ? kThreads : kMaxThreads) void rmsnorm_bwd_kern
       for (int r = 0; r < rows; ++r) a += rows_dw[r * tpr * 8 + k];
       out[k] = a;
     }
-  } else {
+  } else if (HOLD) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
+    for (int j = 0; j < HV; ++j) {
       const int v = lane + j * tpr;
       if (v >= nv) break;
       ((float4*)out)[2 * v] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
       ((float4*)out)[2 * v + 1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
     }
+  } else {
+    for (int v = lane; v < nv; v += tpr)
+      for (int i = 0; i < 2; ++i) ((float4*)out)[2 * v + i] = wide_dw[2 * v + i];
   }
 }
 
-// dw[k] = the sum of G parts: 16 threads of a workgroup take every 16th part of 4 columns, then their sums in order.
+// dw[k] = the sum of G parts: of 32 columns (a line of each part), 32 groups of 8 threads take every 32nd part, 8
+// loads at a time; then their sums in order.
+constexpr int kDwGroups = 32;
 __global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* __restrict__ parts, float* __restrict__ dw,
                                                           int64_t G, int64_t K) {
-  __shared__ float4 sums[16][16];
-  const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
-  const int64_t c4 = (int64_t)blockIdx.x * 16 + col;         // K is a multiple of 64
+  __shared__ float4 sums[kDwGroups][8];
+  const int col = threadIdx.x & 7, grp = threadIdx.x >> 3;
+  const int64_t c4 = (int64_t)blockIdx.x * 8 + col;          // K is a multiple of 32
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const float4* p = (const float4*)parts + c4;
-  for (int64_t g = grp; g < G; g += 16) {
-    const float4 b = p[g * (K / 4)];
-    a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+  for (int64_t g0 = grp; g0 < G; g0 += 8 * kDwGroups) {
+    float4 b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = p[min(g0 + i * kDwGroups, G - 1) * (K / 4)];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (g0 + i * kDwGroups < G) a.x += b[i].x, a.y += b[i].y, a.z += b[i].z, a.w += b[i].w;
   }
   sums[grp][col] = a;
   __syncthreads();
   if (grp == 0) {
-    for (int g = 1; g < 16; ++g) {
+    for (int g = 1; g < kDwGroups; ++g) {
       const float4 b = sums[g][col];
       a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
     }
@@ -334,27 +419,29 @@ int64_t rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K) {
   return G > 1 ? G * K * 4 : 0;                              // one workgroup writes dw itself
 }
 
-template <bool F32>
+template <bool F32, bool W_F32>
 static void launch_bwd(const RmsNormBwd& p, float* parts, hipStream_t stream) {
-  const RowPlan plan = plan_of(p.K);
+  const RowPlan plan = bwd_plan_of(p.K);
   const dim3 grid((unsigned)bwd_groups(p.M, p.K)), block(plan.tpr <= 64 ? kThreads : plan.tpr);
-  if (plan.tpr == 16) rmsnorm_bwd_kernel<16, 1, F32><<<grid, block, 0, stream>>>(p, parts);
-  else if (plan.tpr == 32) rmsnorm_bwd_kernel<32, 1, F32><<<grid, block, 0, stream>>>(p, parts);
-  else if (plan.tpr == 64) rmsnorm_bwd_kernel<64, 1, F32><<<grid, block, 0, stream>>>(p, parts);
-  else if (plan.vpl == 1) rmsnorm_bwd_kernel<0, 1, F32><<<grid, block, 0, stream>>>(p, parts);
-  else if (plan.vpl == 2) rmsnorm_bwd_kernel<0, 2, F32><<<grid, block, 0, stream>>>(p, parts);
-  else rmsnorm_bwd_kernel<0, 4, F32><<<grid, block, 0, stream>>>(p, parts);
+  const auto kernel = plan.tpr == 16  ? rmsnorm_bwd_kernel<16, 1, 2, F32, W_F32>
+                      : plan.tpr == 32 ? rmsnorm_bwd_kernel<32, 1, 2, F32, W_F32>
+                      : plan.tpr == 64 ? rmsnorm_bwd_kernel<64, 1, 2, F32, W_F32>
+                      : plan.vpl == 1  ? rmsnorm_bwd_kernel<0, 1, 2, F32, W_F32>
+                      : plan.vpl == 2  ? rmsnorm_bwd_kernel<0, 2, 1 + AHEAD_, F32, W_F32>
+                      : plan.vpl == 4  ? rmsnorm_bwd_kernel<0, 4, 1, F32, W_F32>
+                                       : rmsnorm_bwd_kernel<0, 0, 0, F32, W_F32>;
+  kernel<<<grid, block, 0, stream>>>(p, parts);
 }
 
 hipError_t launch_rmsnorm_bwd(const RmsNormBwd& p, hipStream_t stream) {
   const int64_t G = bwd_groups(p.M, p.K);
   float* parts = !p.dw ? nullptr : G > 1 ? (float*)p.workspace : p.dw;
   if (G > 0) {
-    if (p.h_f32) launch_bwd<true>(p, parts, stream);
-    else launch_bwd<false>(p, parts, stream);
+    if (p.h_f32) p.w_f32 ? launch_bwd<true, true>(p, parts, stream) : launch_bwd<true, false>(p, parts, stream);
+    else p.w_f32 ? launch_bwd<false, true>(p, parts, stream) : launch_bwd<false, false>(p, parts, stream);
   }
   if (p.dw && G != 1)                                        // no rows: dw is zero
-    rmsnorm_dw_kernel<<<dim3((unsigned)(p.K / 64)), dim3(256), 0, stream>>>((const float*)p.workspace, p.dw, G, p.K);
+    rmsnorm_dw_kernel<<<dim3((unsigned)(p.K / 32)), dim3(256), 0, stream>>>((const float*)p.workspace, p.dw, G, p.K);
   return hipGetLastError();
 }
 

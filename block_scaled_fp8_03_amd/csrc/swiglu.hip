@@ -12,109 +12,82 @@ namespace fp8bs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPasses = 4;           // vectors of 8 elements that a thread takes
+constexpr int kPasses = 4;           // rows that a thread takes where there are many
 
-// Where thread i of a run of vectors lies: rows of nv vectors, the run starting at row
-// `row`, vector `col`.  Less than 2^31 vectors behind it.
-struct Run {
-  int64_t row;
-  uint32_t col, nv;
+// A workgroup's 256 threads are R = 256 / C rows of C vectors, C the largest power of
+// two, up to 256, that divides a row's vectors: no lane is idle and a thread's row and
+// column cost shifts.  C >= 16, so 16 lanes hold a block of 128.
+struct Tile {
+  int64_t row;         // a thread's first row; the next ones lie `step` apart
+  uint32_t col;        // its vector in them
+  int step;
 };
-__device__ __forceinline__ Run run_of(int64_t first, int64_t nv) {
-  const int64_t r = first / nv;      // the same for the workgroup
-  return {r, (uint32_t)(first - r * nv), (uint32_t)nv};
+__device__ __forceinline__ Tile tile_of(int shift, uint32_t chunks, int passes) {
+  const uint32_t band = blockIdx.x / chunks, chunk = blockIdx.x - band * chunks;
+  const int step = kThreads >> shift;
+  return {(int64_t)band * (step * passes) + (threadIdx.x >> shift),
+          (chunk << shift) + (threadIdx.x & ((1u << shift) - 1)), step};
 }
-__device__ __forceinline__ void place(const Run& run, uint32_t i, int64_t* row, uint32_t* col) {
-  const uint32_t at = run.col + i;   // nv < 2^28 and i < 2^10
-  const uint32_t down = at / run.nv;
-  *row = run.row + down;
-  *col = at - down * run.nv;
-}
-
-__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack2_bf16(f[0], f[1]), pack2_bf16(f[2], f[3]), pack2_bf16(f[4], f[5]), pack2_bf16(f[6], f[7]));
-}
-
-__device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
 
 // rows that the call has: all, or fewer by the device's count
 __device__ __forceinline__ int64_t rows_of(const int32_t* n_rows, int64_t M) {
   return n_rows ? min(max<int64_t>(*n_rows, 0), M) : M;
 }
 
+__device__ __forceinline__ uint4 load_row(const void* p, int64_t row, int64_t ld, uint32_t col) {
+  return ((const uint4*)((const uint16_t*)p + row * ld))[col];
+}
+
 }  // namespace
 
-__global__ __launch_bounds__(kThreads) void swiglu_kernel(const SwiGlu p) {
+template <int PASSES>
+__global__ __launch_bounds__(kThreads) void swiglu_kernel(const SwiGlu p, int shift, uint32_t chunks) {
+  const Tile t = tile_of(shift, chunks, PASSES);
   const int64_t nv = p.N / 8, rows = rows_of(p.n_rows, p.M);
-  const Run run = run_of((int64_t)blockIdx.x * (kThreads * kPasses), nv);
-  if (run.row >= rows) return;
-  uint4 g[kPasses], u[kPasses];
+  if (t.row >= rows) return;                                 // 16 lanes together, as below
+  uint4 g[PASSES], u[PASSES];
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    int64_t r;
-    uint32_t c;
-    place(run, threadIdx.x + k * kThreads, &r, &c);
-    r = min(r, rows - 1);
-    g[k] = *((const uint4*)((const uint16_t*)p.gate + r * p.ld_g) + c);
-    u[k] = *((const uint4*)((const uint16_t*)p.up + r * p.ld_u) + c);
+  for (int k = 0; k < PASSES; ++k) {
+    const int64_t r = t.row + k * t.step < rows ? t.row + k * t.step : t.row;
+    g[k] = load_row(p.gate, r, p.ld_g, t.col);
+    u[k] = load_row(p.up, r, p.ld_u, t.col);
   }
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    int64_t r;
-    uint32_t c;
-    place(run, threadIdx.x + k * kThreads, &r, &c);
-    if (r >= rows) return;                                   // blocks of 128 lie in one row: 16 lanes go together
+  for (int k = 0; k < PASSES; ++k) {
+    const int64_t r = t.row + k * t.step;
+    if (r >= rows) return;
     float a[8], b[8];
     unpack8(g[k], a);
     unpack8(u[k], b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = a[i] * sigmoid(a[i]) * b[i];
-    const int64_t at = r * nv + c;
+    for (int i = 0; i < 8; ++i) a[i] = a[i] * sigmoid_f32(a[i]) * b[i];
+    const int64_t at = r * nv + t.col;
     if (p.y) store_nt((uint4*)p.y + at, pack8(a));
     if (p.q) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, f32_bits(a[i]) & 0x7FFFFFFFu);
-      top = row16_max_u32(top);
-      const float sc = p.ue8m0 ? block_scale<true>(bits_f32(top)) : block_scale<false>(bits_f32(top));
-      const float rs = __fdiv_rn(1.0f, sc);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = div_markstein(a[i], sc, rs);
-      store_nt((uint2*)p.q + at, make_uint2(pack4_e4m3(a[0], a[1], a[2], a[3]), pack4_e4m3(a[4], a[5], a[6], a[7])));
+      float sc;
+      store_nt((uint2*)p.q + at, quant8(a, p.ue8m0, &sc));
       if ((threadIdx.x & 15) == 0) p.s[at / 16] = sc;
     }
   }
 }
 
 // du = dy * g * sigmoid(g),  dg = dy * u * sigmoid(g) * (1 + g * (1 - sigmoid(g)))
-__global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const SwiGluBwd p) {
-  const int64_t nv = p.N / 8, rows = rows_of(p.n_rows, p.M);
-  const Run run = run_of((int64_t)blockIdx.x * (kThreads * kPasses), nv);
-  if (run.row >= rows) return;
-  uint4 g[kPasses], u[kPasses], d[kPasses];
+template <int PASSES>
+__global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const SwiGluBwd p, int shift, uint32_t chunks) {
+  const Tile t = tile_of(shift, chunks, PASSES);
+  const int64_t rows = rows_of(p.n_rows, p.M);
+  if (t.row >= rows) return;
+  uint4 g[PASSES], u[PASSES], d[PASSES];
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    int64_t r;
-    uint32_t c;
-    place(run, threadIdx.x + k * kThreads, &r, &c);
-    r = min(r, rows - 1);
-    g[k] = *((const uint4*)((const uint16_t*)p.gate + r * p.ld_g) + c);
-    u[k] = *((const uint4*)((const uint16_t*)p.up + r * p.ld_u) + c);
-    d[k] = ((const uint4*)p.dy)[r * nv + c];
+  for (int k = 0; k < PASSES; ++k) {
+    const int64_t r = t.row + k * t.step < rows ? t.row + k * t.step : t.row;
+    g[k] = load_row(p.gate, r, p.ld_g, t.col);
+    u[k] = load_row(p.up, r, p.ld_u, t.col);
+    d[k] = load_row(p.dy, r, p.N, t.col);
   }
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    int64_t r;
-    uint32_t c;
-    place(run, threadIdx.x + k * kThreads, &r, &c);
+  for (int k = 0; k < PASSES; ++k) {
+    const int64_t r = t.row + k * t.step;
     if (r >= rows) return;
     float a[8], b[8], e[8];
     unpack8(g[k], a);
@@ -122,33 +95,56 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const SwiGluBwd p)
     unpack8(d[k], e);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = sigmoid(a[i]), x = e[i] * s;
+      const float s = sigmoid_f32(a[i]), x = e[i] * s;
       e[i] = x * b[i] * __builtin_fmaf(a[i], 1.0f - s, 1.0f);
       b[i] = x * a[i];
     }
-    store_nt((uint4*)((uint16_t*)p.dgate + r * p.ld_dg) + c, pack8(e));
-    store_nt((uint4*)((uint16_t*)p.dup + r * p.ld_du) + c, pack8(b));
+    store_nt((uint4*)((uint16_t*)p.dgate + r * p.ld_dg) + t.col, pack8(e));
+    store_nt((uint4*)((uint16_t*)p.dup + r * p.ld_du) + t.col, pack8(b));
   }
 }
 
-// One launch: at most 2^32 - 1 threads, kPasses vectors of 8 a thread.
-bool swiglu_fits(int64_t M, int64_t N) {
-  if (M <= 0 || N <= 0) return true;
-  const int64_t most = (((int64_t)1 << 32) - 1) / kThreads * (kThreads * kPasses);
-  return N < ((int64_t)1 << 31) && M <= most / (N / 8);
+namespace {
+
+struct Plan {
+  int shift;
+  uint32_t chunks;
+  int passes;
+  int64_t grid;
+};
+// One row a thread while that leaves no more than 8 workgroups a CU, so that few rows
+// are spread over the card.
+Plan plan_of(int64_t M, int64_t N) {
+  const int64_t nv = N / 8;
+  int shift = 4;
+  while (shift < 8 && nv % (2 << shift) == 0) ++shift;
+  const int64_t chunks = nv >> shift, step = kThreads >> shift;
+  const int64_t one = (M + step - 1) / step;
+  const int passes = one <= 2048 / chunks ? 1 : kPasses;
+  return {shift, (uint32_t)chunks, passes, (one + passes - 1) / passes * chunks};
 }
 
-static dim3 grid_of(int64_t M, int64_t N) {
-  return dim3((unsigned)((M * (N / 8) + kThreads * kPasses - 1) / (kThreads * kPasses)));
+}  // namespace
+
+// One launch: at most 2^32 - 1 threads.
+bool swiglu_fits(int64_t M, int64_t N) {
+  if (M <= 0 || N <= 0) return true;
+  if (N >= (int64_t)1 << 31 || M >= (int64_t)1 << 40) return false;
+  const Plan q = plan_of(M, N);
+  return q.grid / q.chunks <= (((int64_t)1 << 32) - 1) / kThreads / q.chunks;
 }
 
 hipError_t launch_swiglu(const SwiGlu& p, hipStream_t stream) {
-  swiglu_kernel<<<grid_of(p.M, p.N), dim3(kThreads), 0, stream>>>(p);
+  const Plan q = plan_of(p.M, p.N);
+  const auto kernel = q.passes == 1 ? swiglu_kernel<1> : swiglu_kernel<kPasses>;
+  kernel<<<dim3((unsigned)q.grid), dim3(kThreads), 0, stream>>>(p, q.shift, q.chunks);
   return hipGetLastError();
 }
 
 hipError_t launch_swiglu_bwd(const SwiGluBwd& p, hipStream_t stream) {
-  swiglu_bwd_kernel<<<grid_of(p.M, p.N), dim3(kThreads), 0, stream>>>(p);
+  const Plan q = plan_of(p.M, p.N);
+  const auto kernel = q.passes == 1 ? swiglu_bwd_kernel<1> : swiglu_bwd_kernel<kPasses>;
+  kernel<<<dim3((unsigned)q.grid), dim3(kThreads), 0, stream>>>(p, q.shift, q.chunks);
   return hipGetLastError();
 }
 

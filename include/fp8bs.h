@@ -626,8 +626,8 @@ int fp8bs_rmsnorm_bwd(const void* dy_bf16, const void* h, int64_t ld_h, int h_dt
  * not counted.
  *   indices  in   int32 [T, topk] (from fp8bs_moe_gate)
  *   cu_seq   in   DEVICE int32 [S + 1], non-decreasing, or NULL: one sequence
- *                 of all T tokens, S = 1.  Clamped to [0, T], and a sequence's
- *                 end to its start
+ *                 of all T tokens, S = 1.  The values are a precondition, not
+ *                 checked on the host: wrong ones give wrong results, not faults
  *   counts   out  int32 [S, E];  probs  out  float32 [S, E];  loss  out  float32 [S]
  *   workspace     DEVICE, >= fp8bs_moe_balance_workspace_size(T, S, E) bytes (0:
  *                 NULL), 16-byte aligned, scratch, not shared by concurrent calls

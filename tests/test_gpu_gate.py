@@ -187,13 +187,38 @@ def test_masks_in_the_loss_and_gradients(kind):
 
 
 def test_bounds_that_are_wrong_stay_inside():
-    """Boundaries out of range or falling: clamped, nothing outside is read or written."""
-    z, idx = eu.normal((50, 64), 1, 1.0, F32).to(DEV), torch.zeros((50, 2), dtype=torch.int32, device=DEV)
-    cu = torch.tensor([-5, 30, 10, 99], dtype=torch.int32, device=DEV)
-    loss, counts, _ = fp8bs.moe_balance(z, idx, cu)
-    assert counts[:, 0].tolist() == [60, 0, 80] and loss[1] == 0
-    d = fp8bs.moe_gate_bwd(z, idx, None, cu_seq=cu, counts=counts, d_loss=torch.ones(3, device=DEV))
-    assert torch.isfinite(d).all()
+    """Boundaries out of range or falling: nothing outside the buffers is written."""
+    E, guard = 64, 4096
+    z, idx = eu.normal((500, E), 1, 1.0, F32).to(DEV), torch.zeros((500, 2), dtype=torch.int32, device=DEV)
+    for cu in ([-5, 300, 10, 999], [400, 300, 200, 100], [1 << 30, -(1 << 30), 1 << 30, 0], [7, 7, 7, 7], [600, 700, 800, 900]):
+        cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        need = fp8bs.lib().fp8bs_moe_balance_workspace_size(500, 3, E)
+        buf = torch.zeros(need + 2 * guard, dtype=torch.uint8, device=DEV)
+        out = torch.full((3 * E * 2 + 3 + 200,), -7, dtype=torch.int32, device=DEV)
+        counts, probs = out[50:50 + 3 * E].view(3, E), out[100 + 3 * E:100 + 6 * E].view(F32).view(3, E)
+        loss = out[150 + 6 * E:153 + 6 * E].view(F32)
+        buf[:guard], buf[-guard:] = 1, 1
+        fp8bs.fp8bs_moe_balance(z, idx, cu, "sigmoid", counts, probs, loss, buf[guard:-guard])
+        assert (buf[:guard] == 1).all() and (buf[-guard:] == 1).all()
+        for part in (out[:50], out[50 + 3 * E:100 + 3 * E], out[100 + 6 * E:150 + 6 * E], out[153 + 6 * E:]):
+            assert (part == -7).all()
+        fp8bs.moe_gate_bwd(z, idx, None, cu_seq=cu, counts=counts, d_loss=torch.ones(3, device=DEV))
+    torch.cuda.synchronize()
+
+
+def test_balance_many_sequences_and_long_ones():
+    """More sequences than probes of a wave, of no, one and many tokens; more tokens than two a wave."""
+    E, topk = 32, 4
+    T = 20000
+    lens = ([0, 1, 2, 0, 0, 17, 3] * 800)[:5000]
+    lens[77] = 0
+    lens[77] = T - sum(lens)
+    cu = [0] + np.cumsum(lens).tolist()
+    z = eu.normal((T, E), 1, 2.0, F32)
+    idx = torch.randint(0, E, (T, topk), generator=eu.gen(2), dtype=torch.int32)
+    _, counts, _ = _balance(z, idx, cu, "sigmoid")
+    _gate_bwd(z, idx, None, "sigmoid", True, 1.0, cu, counts, eu.normal((len(lens),), 3, 1.0, F32), F32)
+    _balance(z, idx, None, "softmax")
 
 
 def test_balance_no_tokens_and_no_sequences():
