@@ -577,12 +577,15 @@ def _scratch(workspace: Optional[torch.Tensor], dev):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _call_on(dev, fn: str, *args, first: str = "cache.latent") -> None:
     """fn(*args, the current stream of device `dev`, that of the tensor `first`), with that device current."""
     if dev.type != "cuda":
         raise ValueError(f"{first} must be a device tensor")
     stream = _raw_stream(dev.index)
-    if torch.cuda.current_device() == dev.index:
+    if _current_device() == dev.index:
         _call(fn, *args, stream)
     else:
         with torch.cuda.device(dev):
@@ -738,39 +741,46 @@ def cache_compact(cache: MlaCache, table, lens):
 
 
 # ------------------------------------------- what stands between the products
+#
+# Each operator's raw form checks its outputs and the allocating one makes them;
+# both hand their addresses to one function that checks the inputs and calls (the
+# checks of a tensor cost as much as its allocation: 1 us).
 
 _FLOATS = (torch.bfloat16, torch.float32)
-_COUNT = (torch.Size([]), torch.Size([1]))
+_EMPTY, _ONE = torch.Size([]), torch.Size([1])
 
 
 def _rows2(t: torch.Tensor, name: str, dtypes, shape, dev):
     """A [M, width] view with a dense last dimension: (pointer, row stride)."""
+    if getattr(t, "dtype", None) in dtypes and t.shape == shape and t.device == dev:
+        sm, sw = t.stride()
+        M, width = shape
+        if sw == 1 or M == 0 or width <= 1:
+            return t.data_ptr(), (sm if M > 1 else 0)
+        raise ValueError(f"{name} must have a contiguous last dimension")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if t.device != dev:
-        raise ValueError(f"{name} lies on {t.device}, other tensors on {dev}")
-    M, width = shape
-    sm, sw = t.stride()
-    if sw != 1 and M > 0 and width > 1:
-        raise ValueError(f"{name} must have a contiguous last dimension")
-    return t.data_ptr(), (sm if M > 1 else 0)
+    raise ValueError(f"{name} lies on {t.device}, other tensors on {dev}")
 
 
 def _opt(t: Optional[torch.Tensor], name: str, dtypes, shape, dev) -> Optional[int]:
     return None if t is None else _ptr(t, name, dtypes, shape, dev)
 
 
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    """The address of a tensor that was made here."""
+    return None if t is None else t.data_ptr()
+
+
 def _count(n_rows: Optional[torch.Tensor], dev) -> Optional[int]:
     """The address of a count of rows on the device: one int32."""
     if n_rows is None:
         return None
-    if isinstance(n_rows, torch.Tensor) and n_rows.shape not in _COUNT:
-        raise ValueError("n_rows must hold one value")
-    return _ptr(n_rows, "n_rows", _I32, getattr(n_rows, "shape", None), dev)
+    return _ptr(n_rows, "n_rows", _I32, _EMPTY if getattr(n_rows, "shape", None) == _EMPTY else _ONE, dev)
 
 
 def _score(score) -> int:
@@ -783,9 +793,28 @@ def _score(score) -> int:
 
 def _shape2(t, message: str, name: str):
     """The two sizes of a 2-D tensor."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+    try:
+        a, b = t.shape
+        t.device
+    except (AttributeError, TypeError, ValueError):
+        raise _misfit(message, **{name: t}) from None
+    if not isinstance(t, torch.Tensor):
         raise _misfit(message, **{name: t})
-    return t.shape
+    return a, b
+
+
+def _empty(like: torch.Tensor, shape, dtype) -> torch.Tensor:
+    return like.new_empty(shape, dtype=dtype)
+
+
+def _rmsnorm(x, M, K, res, norm_w, eps, res_out, y, q, s, scale_fmt) -> None:
+    """fp8bs_rmsnorm of outputs given by their addresses."""
+    dev = x.device
+    xp, ld = _rows2(x, "x", _BF16, (M, K), dev)
+    res_f32 = res is not None and getattr(res, "dtype", None) == torch.float32
+    _call_on(dev, "fp8bs_rmsnorm", xp, ld, _opt(res, "res", _FLOATS, (M, K), dev), res_out,
+             OUT_F32 if res_f32 else OUT_BF16, _ptr(norm_w, "norm_w", _FLOATS, (K,), dev),
+             norm_w.dtype == torch.float32, eps, y, q, s, _fmt(scale_fmt), M, K, first="x")
 
 
 def fp8bs_rmsnorm(x: torch.Tensor, res: Optional[torch.Tensor], res_out: Optional[torch.Tensor], norm_w: torch.Tensor,
@@ -797,21 +826,17 @@ def fp8bs_rmsnorm(x: torch.Tensor, res: Optional[torch.Tensor], res_out: Optiona
     e4m3 [M, K] with scales s float32 [M, K/128]."""
     M, K = _shape2(x, "x must be [M, K]", "x")
     dev = x.device
-    xp, ld = _rows2(x, "x", _BF16, (M, K), dev)
-    res_type = _BF16 if res is None else (res.dtype,) if getattr(res, "dtype", None) in _FLOATS else _FLOATS
-    _call_on(dev, "fp8bs_rmsnorm", xp, ld, _opt(res, "res", res_type, (M, K), dev),
-             _opt(res_out, "res_out", res_type, (M, K), dev), OUT_F32 if res_type == _F32 else OUT_BF16,
-             _ptr(norm_w, "norm_w", _FLOATS, (K,), dev), norm_w.dtype == torch.float32, eps,
-             _opt(y, "y", _BF16, (M, K), dev), _opt(q, "q", _F8, (M, K), dev),
-             _opt(s, "s", _F32, (M, K // BLOCK), dev), _fmt(scale_fmt), M, K, first="x")
+    like = (getattr(res, "dtype", None),) if getattr(res, "dtype", None) in _FLOATS else _FLOATS
+    _rmsnorm(x, M, K, res, norm_w, eps, _opt(res_out, "res_out", like, (M, K), dev), _opt(y, "y", _BF16, (M, K), dev),
+             _opt(q, "q", _F8, (M, K), dev), _opt(s, "s", _F32, (M, K // BLOCK), dev), scale_fmt)
 
 
 def rmsnorm(x, norm_w, eps: float, residual=None):
     """fp8bs_rmsnorm: y bf16 [M, K]; with a residual (y, x + residual)."""
     M, K = _shape2(x, "x must be [M, K]", "x")
-    y = x.new_empty((M, K), dtype=torch.bfloat16)
-    h = None if residual is None else torch.empty_like(residual)
-    fp8bs_rmsnorm(x, residual, h, norm_w, eps, y, None, None)
+    y = _empty(x, (M, K), torch.bfloat16)
+    h = None if residual is None else _empty(x, (M, K), getattr(residual, "dtype", None))
+    _rmsnorm(x, M, K, residual, norm_w, eps, _at(h), y.data_ptr(), None, None, SCALE_FP32)
     return y if residual is None else (y, h)
 
 
@@ -819,12 +844,20 @@ def rmsnorm_quant(x, norm_w, eps: float, residual=None, scale_fmt="fp32", return
     """fp8bs_rmsnorm: (q e4m3 [M, K], s float32 [M, K/128]), then y bf16 if
     return_y, then x + residual if there is a residual."""
     M, K = _shape2(x, "x must be [M, K]", "x")
-    q = x.new_empty((M, K), dtype=torch.float8_e4m3fn)
-    s = x.new_empty((M, K // BLOCK), dtype=torch.float32)
-    y = x.new_empty((M, K), dtype=torch.bfloat16) if return_y else None
-    h = None if residual is None else torch.empty_like(residual)
-    fp8bs_rmsnorm(x, residual, h, norm_w, eps, y, q, s, scale_fmt)
+    q, s = _empty(x, (M, K), torch.float8_e4m3fn), _empty(x, (M, K // BLOCK), torch.float32)
+    y = _empty(x, (M, K), torch.bfloat16) if return_y else None
+    h = None if residual is None else _empty(x, (M, K), getattr(residual, "dtype", None))
+    _rmsnorm(x, M, K, residual, norm_w, eps, _at(h), _at(y), q.data_ptr(), s.data_ptr(), scale_fmt)
     return tuple(t for t in (q, s, y, h) if t is not None)
+
+
+def _rmsnorm_bwd(dy, h, M, K, norm_w, eps, dres, dx, dw, ws, nbytes) -> None:
+    """fp8bs_rmsnorm_bwd of outputs given by their addresses."""
+    dev = h.device
+    hp, ld = _rows2(h, "h", _FLOATS, (M, K), dev)
+    _call_on(dev, "fp8bs_rmsnorm_bwd", _ptr(dy, "dy", _BF16, (M, K), dev), hp, ld, _out_code(h),
+             _ptr(norm_w, "norm_w", _FLOATS, (K,), dev), norm_w.dtype == torch.float32, eps,
+             _opt(dres, "dres", (h.dtype,), (M, K), dev), dx, dw, M, K, ws, nbytes, first="h")
 
 
 def fp8bs_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, norm_w: torch.Tensor, eps: float,
@@ -835,13 +868,8 @@ def fp8bs_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, norm_w: torch.Tensor, e
     of h's type (dx itself if you like); dw float32 [K] or None."""
     M, K = _shape2(h, "h must be [M, K]", "h")
     dev = h.device
-    hp, ld = _rows2(h, "h", _FLOATS, (M, K), dev)
-    like = (h.dtype,)
-    ws, nbytes = _scratch(workspace, dev)
-    _call_on(dev, "fp8bs_rmsnorm_bwd", _ptr(dy, "dy", _BF16, (M, K), dev), hp, ld, _out_code(h),
-             _ptr(norm_w, "norm_w", _FLOATS, (K,), dev), norm_w.dtype == torch.float32, eps,
-             _opt(dres, "dres", like, (M, K), dev), _ptr(dx, "dx", like, (M, K), dev),
-             _opt(dw, "dw", _F32, (K,), dev), M, K, ws, nbytes, first="h")
+    _rmsnorm_bwd(dy, h, M, K, norm_w, eps, dres, _ptr(dx, "dx", (h.dtype,), (M, K), dev),
+                 _opt(dw, "dw", _F32, (K,), dev), *_scratch(workspace, dev))
 
 
 def rmsnorm_bwd(dy, h, norm_w, eps: float, dres=None):
@@ -850,11 +878,18 @@ def rmsnorm_bwd(dy, h, norm_w, eps: float, dres=None):
     need = lib().fp8bs_rmsnorm_bwd_workspace_size(M, K)
     if need < 0:
         raise ValueError("sizes out of range")
-    dx = h.new_empty((M, K))
-    dw = h.new_empty(K, dtype=torch.float32)
-    ws = h.new_empty(need, dtype=torch.uint8) if need else None
-    fp8bs_rmsnorm_bwd(dy, h, norm_w, eps, dres, dx, dw, ws)
+    dx, dw = h.new_empty((M, K)), _empty(h, (K,), torch.float32)
+    ws = _empty(h, (need,), torch.uint8) if need else None
+    _rmsnorm_bwd(dy, h, M, K, norm_w, eps, dres, dx.data_ptr(), dw.data_ptr(), _at(ws), need)
     return dx, dw
+
+
+def _moe_gate(logits, T, E, topk, bias, groups, topk_groups, score, normalize, route_scale, indices, weights) -> None:
+    """fp8bs_moe_gate of outputs given by their addresses."""
+    dev = logits.device
+    zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
+    _call_on(dev, "fp8bs_moe_gate", zp, ld, _out_code(logits), _opt(bias, "bias", _F32, (E,), dev), T, E, topk, groups,
+             topk_groups, _score(score), normalize, route_scale, indices, weights, first="logits")
 
 
 def fp8bs_moe_gate(logits: torch.Tensor, bias: Optional[torch.Tensor], groups: int, topk_groups: int, score,
@@ -864,21 +899,18 @@ def fp8bs_moe_gate(logits: torch.Tensor, bias: Optional[torch.Tensor], groups: i
     T, E = _shape2(logits, "logits must be [T, E]", "logits")
     topk = _shape2(indices, "indices must be [T, topk]", "indices")[1]
     dev = logits.device
-    zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
-    _call_on(dev, "fp8bs_moe_gate", zp, ld, _out_code(logits), _opt(bias, "bias", _F32, (E,), dev), T, E, topk, groups,
-             topk_groups, _score(score), normalize, route_scale, _ptr(indices, "indices", _I32, (T, topk), dev),
-             _ptr(weights, "weights", _F32, (T, topk), dev), first="logits")
+    _moe_gate(logits, T, E, topk, bias, groups, topk_groups, score, normalize, route_scale,
+              _ptr(indices, "indices", _I32, (T, topk), dev), _ptr(weights, "weights", _F32, (T, topk), dev))
 
 
 def moe_gate(logits, topk: int, bias=None, groups: int = 1, topk_groups: Optional[int] = None, score="sigmoid",
              normalize: bool = True, route_scale: float = 1.0):
     """fp8bs_moe_gate: (indices int32 [T, topk], weights float32 [T, topk]), for
     moe_route and moe_combine.  All groups are kept unless topk_groups says so."""
-    T, _ = _shape2(logits, "logits must be [T, E]", "logits")
-    indices = logits.new_empty((T, topk), dtype=torch.int32)
-    weights = logits.new_empty((T, topk), dtype=torch.float32)
-    fp8bs_moe_gate(logits, bias, groups, groups if topk_groups is None else topk_groups, score, normalize, route_scale,
-                   indices, weights)
+    T, E = _shape2(logits, "logits must be [T, E]", "logits")
+    indices, weights = _empty(logits, (T, topk), torch.int32), _empty(logits, (T, topk), torch.float32)
+    _moe_gate(logits, T, E, topk, bias, groups, groups if topk_groups is None else topk_groups, score, normalize,
+              route_scale, indices.data_ptr(), weights.data_ptr())
     return indices, weights
 
 
@@ -891,6 +923,15 @@ def _sequences(cu_seq: Optional[torch.Tensor], dev):
     return _ptr(cu_seq, "cu_seq", _I32, cu_seq.shape, dev), cu_seq.shape[0] - 1
 
 
+def _moe_balance(logits, T, E, indices, cu, S, score, counts, probs, loss, ws, nbytes) -> None:
+    """fp8bs_moe_balance of boundaries and outputs given by their addresses."""
+    topk = _shape2(indices, "indices must be [T, topk]", "indices")[1]
+    dev = logits.device
+    zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
+    _call_on(dev, "fp8bs_moe_balance", zp, ld, _out_code(logits), _ptr(indices, "indices", _I32, (T, topk), dev), cu,
+             T, S, E, topk, _score(score), counts, probs, loss, ws, nbytes, first="logits")
+
+
 def fp8bs_moe_balance(logits: torch.Tensor, indices: torch.Tensor, cu_seq: Optional[torch.Tensor], score,
                       counts: torch.Tensor, probs: torch.Tensor, loss: torch.Tensor,
                       workspace: Optional[torch.Tensor]) -> None:
@@ -898,29 +939,37 @@ def fp8bs_moe_balance(logits: torch.Tensor, indices: torch.Tensor, cu_seq: Optio
     int32 [S, E] of the gate's indices [T, topk], probs float32 [S, E] the mean
     share of the token's scores, loss float32 [S]."""
     T, E = _shape2(logits, "logits must be [T, E]", "logits")
-    topk = _shape2(indices, "indices must be [T, topk]", "indices")[1]
     dev = logits.device
-    zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
     cu, S = _sequences(cu_seq, dev)
-    ws, nbytes = _scratch(workspace, dev)
-    _call_on(dev, "fp8bs_moe_balance", zp, ld, _out_code(logits), _ptr(indices, "indices", _I32, (T, topk), dev), cu,
-             T, S, E, topk, _score(score), _ptr(counts, "counts", _I32, (S, E), dev),
-             _ptr(probs, "probs", _F32, (S, E), dev), _ptr(loss, "loss", _F32, (S,), dev), ws, nbytes, first="logits")
+    _moe_balance(logits, T, E, indices, cu, S, score, _ptr(counts, "counts", _I32, (S, E), dev),
+                 _ptr(probs, "probs", _F32, (S, E), dev), _ptr(loss, "loss", _F32, (S,), dev), *_scratch(workspace, dev))
 
 
 def moe_balance(logits, indices, cu_seq=None, score="sigmoid"):
     """fp8bs_moe_balance: (loss float32 [S], counts int32 [S, E], probs float32 [S, E])."""
     T, E = _shape2(logits, "logits must be [T, E]", "logits")
-    S = _sequences(cu_seq, logits.device)[1]
+    cu, S = _sequences(cu_seq, logits.device)
     need = lib().fp8bs_moe_balance_workspace_size(T, S, E)
     if need < 0:
         raise ValueError("sizes out of range")
-    counts = logits.new_empty((S, E), dtype=torch.int32)
-    probs = logits.new_empty((S, E), dtype=torch.float32)
-    loss = logits.new_empty(S, dtype=torch.float32)
-    ws = logits.new_empty(need, dtype=torch.uint8) if need else None
-    fp8bs_moe_balance(logits, indices, cu_seq, score, counts, probs, loss, ws)
+    counts, probs = _empty(logits, (S, E), torch.int32), _empty(logits, (S, E), torch.float32)
+    loss = _empty(logits, (S,), torch.float32)
+    ws = _empty(logits, (need,), torch.uint8) if need else None
+    _moe_balance(logits, T, E, indices, cu, S, score, counts.data_ptr(), probs.data_ptr(), loss.data_ptr(), _at(ws), need)
     return loss, counts, probs
+
+
+def _moe_gate_bwd(logits, T, E, indices, d_weights, score, normalize, route_scale, cu_seq, counts, d_loss, d_logits,
+                  out_code) -> None:
+    """fp8bs_moe_gate_bwd of an output given by its address."""
+    topk = _shape2(indices, "indices must be [T, topk]", "indices")[1]
+    dev = logits.device
+    zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
+    cu, S = _sequences(cu_seq, dev)
+    _call_on(dev, "fp8bs_moe_gate_bwd", zp, ld, _out_code(logits), _ptr(indices, "indices", _I32, (T, topk), dev),
+             _opt(d_weights, "d_weights", _F32, (T, topk), dev), _score(score), normalize, route_scale, cu,
+             _opt(counts, "counts", _I32, (S, E), dev), _opt(d_loss, "d_loss", _F32, (S,), dev), T, S, E, topk,
+             d_logits, out_code, first="logits")
 
 
 def fp8bs_moe_gate_bwd(logits: torch.Tensor, indices: torch.Tensor, d_weights: Optional[torch.Tensor], score,
@@ -930,23 +979,26 @@ def fp8bs_moe_gate_bwd(logits: torch.Tensor, indices: torch.Tensor, d_weights: O
     topk] or None) and of the balance losses (d_loss float32 [S] with their
     counts, or None): d_logits [T, E] bf16 or float32."""
     T, E = _shape2(logits, "logits must be [T, E]", "logits")
-    topk = _shape2(indices, "indices must be [T, topk]", "indices")[1]
-    dev = logits.device
-    zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
-    cu, S = _sequences(cu_seq, dev)
-    _call_on(dev, "fp8bs_moe_gate_bwd", zp, ld, _out_code(logits), _ptr(indices, "indices", _I32, (T, topk), dev),
-             _opt(d_weights, "d_weights", _F32, (T, topk), dev), _score(score), normalize, route_scale, cu,
-             _opt(counts, "counts", _I32, (S, E), dev), _opt(d_loss, "d_loss", _F32, (S,), dev), T, S, E, topk,
-             _ptr(d_logits, "d_logits", _FLOATS, (T, E), dev), _out_code(d_logits), first="logits")
+    _moe_gate_bwd(logits, T, E, indices, d_weights, score, normalize, route_scale, cu_seq, counts, d_loss,
+                  _ptr(d_logits, "d_logits", _FLOATS, (T, E), logits.device), _out_code(d_logits))
 
 
 def moe_gate_bwd(logits, indices, d_weights=None, score="sigmoid", normalize: bool = True, route_scale: float = 1.0,
                  cu_seq=None, counts=None, d_loss=None, out_dtype=torch.float32) -> torch.Tensor:
     """fp8bs_moe_gate_bwd: d_logits [T, E]."""
     T, E = _shape2(logits, "logits must be [T, E]", "logits")
-    d_logits = logits.new_empty((T, E), dtype=out_dtype)
-    fp8bs_moe_gate_bwd(logits, indices, d_weights, score, normalize, route_scale, cu_seq, counts, d_loss, d_logits)
+    d_logits = _empty(logits, (T, E), out_dtype)
+    _moe_gate_bwd(logits, T, E, indices, d_weights, score, normalize, route_scale, cu_seq, counts, d_loss,
+                  d_logits.data_ptr(), _out_code(d_logits))
     return d_logits
+
+
+def _swiglu(gate, up, M, N, y, q, s, scale_fmt, n_rows) -> None:
+    """fp8bs_swiglu of outputs given by their addresses."""
+    dev = gate.device
+    gp, ldg = _rows2(gate, "gate", _BF16, (M, N), dev)
+    up_, ldu = _rows2(up, "up", _BF16, (M, N), dev)
+    _call_on(dev, "fp8bs_swiglu", gp, ldg, up_, ldu, _count(n_rows, dev), y, q, s, _fmt(scale_fmt), M, N, first="gate")
 
 
 def fp8bs_swiglu(gate: torch.Tensor, up: torch.Tensor, y: Optional[torch.Tensor], q: Optional[torch.Tensor],
@@ -957,18 +1009,15 @@ def fp8bs_swiglu(gate: torch.Tensor, up: torch.Tensor, y: Optional[torch.Tensor]
     offsets[-1:] of moe_route) on are left alone."""
     M, N = _shape2(gate, "gate must be [M, N]", "gate")
     dev = gate.device
-    gp, ldg = _rows2(gate, "gate", _BF16, (M, N), dev)
-    up_, ldu = _rows2(up, "up", _BF16, (M, N), dev)
-    _call_on(dev, "fp8bs_swiglu", gp, ldg, up_, ldu, _count(n_rows, dev), _opt(y, "y", _BF16, (M, N), dev),
-             _opt(q, "q", _F8, (M, N), dev), _opt(s, "s", _F32, (M, N // BLOCK), dev), _fmt(scale_fmt), M, N,
-             first="gate")
+    _swiglu(gate, up, M, N, _opt(y, "y", _BF16, (M, N), dev), _opt(q, "q", _F8, (M, N), dev),
+            _opt(s, "s", _F32, (M, N // BLOCK), dev), scale_fmt, n_rows)
 
 
 def swiglu(gate, up, n_rows=None) -> torch.Tensor:
     """fp8bs_swiglu: bf16 [M, N], not initialised from row n_rows on."""
     M, N = _shape2(gate, "gate must be [M, N]", "gate")
-    y = gate.new_empty((M, N))
-    fp8bs_swiglu(gate, up, y, None, None, n_rows=n_rows)
+    y = _empty(gate, (M, N), torch.bfloat16)
+    _swiglu(gate, up, M, N, y.data_ptr(), None, None, SCALE_FP32, n_rows)
     return y
 
 
@@ -976,10 +1025,9 @@ def swiglu_quant(gate, up, scale_fmt="fp32", n_rows=None, return_y: bool = False
     """fp8bs_swiglu: (q e4m3 [M, N], s float32 [M, N/128]), then y bf16 if
     return_y; not initialised from row n_rows on."""
     M, N = _shape2(gate, "gate must be [M, N]", "gate")
-    q = gate.new_empty((M, N), dtype=torch.float8_e4m3fn)
-    s = gate.new_empty((M, N // BLOCK), dtype=torch.float32)
-    y = gate.new_empty((M, N)) if return_y else None
-    fp8bs_swiglu(gate, up, y, q, s, scale_fmt, n_rows)
+    q, s = _empty(gate, (M, N), torch.float8_e4m3fn), _empty(gate, (M, N // BLOCK), torch.float32)
+    y = _empty(gate, (M, N), torch.bfloat16) if return_y else None
+    _swiglu(gate, up, M, N, _at(y), q.data_ptr(), s.data_ptr(), scale_fmt, n_rows)
     return (q, s, y) if return_y else (q, s)
 
 
@@ -1001,10 +1049,18 @@ def swiglu_bwd(dy, gate, up, n_rows=None):
     """fp8bs_swiglu_bwd: (dgate, dup) bf16 [M, N], the halves of one [M, 2N]
     tensor; not initialised from row n_rows on."""
     M, N = _shape2(gate, "gate must be [M, N]", "gate")
-    d = gate.new_empty((M, 2 * N))
+    d = _empty(gate, (M, 2 * N), torch.bfloat16)
     dgate, dup = d[:, :N], d[:, N:]
     fp8bs_swiglu_bwd(dy, gate, up, dgate, dup, n_rows)
     return dgate, dup
+
+
+def _moe_combine_bwd(dy, out, R, N, w, T, topk, row_of, d_out, d_w) -> None:
+    """fp8bs_moe_combine_bwd of outputs given by their addresses."""
+    dev = out.device
+    _call_on(dev, "fp8bs_moe_combine_bwd", _ptr(dy, "dy", _FLOATS, (T, N), dev), _out_code(dy),
+             _ptr(out, "out", _BF16, (R, N), dev), _ptr(w, "w", _F32, (T, topk), dev),
+             _ptr(row_of, "row_of", _I32, (T, topk), dev), d_out, d_w, T, topk, R, N, first="out")
 
 
 def fp8bs_moe_combine_bwd(dy: torch.Tensor, out: torch.Tensor, w: torch.Tensor, row_of: torch.Tensor,
@@ -1014,10 +1070,8 @@ def fp8bs_moe_combine_bwd(dy: torch.Tensor, out: torch.Tensor, w: torch.Tensor, 
     R, N = _shape2(out, "out must be [R, N]", "out")
     T, topk = _shape2(w, "w must be [T, topk]", "w")
     dev = out.device
-    _call_on(dev, "fp8bs_moe_combine_bwd", _ptr(dy, "dy", _FLOATS, (T, N), dev), _out_code(dy),
-             _ptr(out, "out", _BF16, (R, N), dev), _ptr(w, "w", _F32, (T, topk), dev),
-             _ptr(row_of, "row_of", _I32, (T, topk), dev), _ptr(d_out, "d_out", _BF16, (R, N), dev),
-             _ptr(d_w, "d_w", _F32, (T, topk), dev), T, topk, R, N, first="out")
+    _moe_combine_bwd(dy, out, R, N, w, T, topk, row_of, _ptr(d_out, "d_out", _BF16, (R, N), dev),
+                     _ptr(d_w, "d_w", _F32, (T, topk), dev))
 
 
 def moe_combine_bwd(dy, out, w, row_of):
@@ -1025,6 +1079,6 @@ def moe_combine_bwd(dy, out, w, row_of):
     of d_out that no pair maps to are not initialised."""
     R, N = _shape2(out, "out must be [R, N]", "out")
     T, topk = _shape2(w, "w must be [T, topk]", "w")
-    d_out, d_w = out.new_empty((R, N)), w.new_empty((T, topk))
-    fp8bs_moe_combine_bwd(dy, out, w, row_of, d_out, d_w)
+    d_out, d_w = _empty(out, (R, N), torch.bfloat16), _empty(out, (T, topk), torch.float32)
+    _moe_combine_bwd(dy, out, R, N, w, T, topk, row_of, d_out.data_ptr(), d_w.data_ptr())
     return d_out, d_w

@@ -47,6 +47,12 @@ __device__ __forceinline__ void store_nt<uint4>(uint4* p, const uint4& v) {
   __builtin_nontemporal_store(v.w, &((uint32_t*)p)[3]);
 }
 
+__device__ __forceinline__ uint4 load_nt(const uint4* p) {
+  typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+  const v4u v = __builtin_nontemporal_load((const v4u*)p);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+
 // Two bf16 values packed in one dword -> two floats (exact).
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return bits_f32(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return bits_f32(w & 0xFFFF0000u); }

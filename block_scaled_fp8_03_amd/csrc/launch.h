@@ -103,6 +103,14 @@ int64_t cache_compact_workspace_bytes(int64_t B, int64_t W, int64_t P);
 hipError_t launch_cache_update(const PageTask& a, hipStream_t stream);
 hipError_t launch_cache_compact(const PageTask& a, hipStream_t stream);
 
+// Calls that move at least this many bytes read their inputs with the non-temporal hint;
+// below, what the call before left in the Infinity Cache (256 MB) is found there, which
+// the hint gives up.  us, with the hint / without (inputs of three calls in turn):
+// SwiGLU 84 MB 17.6 / 17.1, 169 MB 31.4 / 33.3, 338 MB 58.0 / 63.0; its gradient 84 MB
+// 15.0 / 13.7, 168 MB 28.1 / 29.4; RMSNorm 132 MB 25.4 / 21.3, 265 MB 46.2 / 47.0; the
+// combine's gradient 98 MB 24.6 / 18.1, 196 MB 48.5 / 51.4, 999 MB 190 / 203.
+constexpr int64_t kHintBytes = (int64_t)160 << 20;
+
 // fp8bs_rmsnorm's arguments (res and res_out, y, q and s: NULL where there is none)
 struct RmsNorm {
   const void *x, *res, *w;

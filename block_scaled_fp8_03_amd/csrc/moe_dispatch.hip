@@ -486,7 +486,7 @@ hipError_t launch_moe_combine(const void* out, const float* w, const int32_t* ro
 constexpr int kPairWaves = 8;
 constexpr int kPairUnroll = 4;
 
-template <bool DY_F32, bool VEC>
+template <bool DY_F32, bool VEC, bool NT>
 __global__ __launch_bounds__(64 * kPairWaves) void moe_combine_bwd_kernel(
     const void* __restrict__ dy, const uint16_t* __restrict__ out, const float* __restrict__ w,
     const int32_t* __restrict__ row_of, uint16_t* __restrict__ d_out, float* __restrict__ d_w, int topk,
@@ -508,7 +508,7 @@ __global__ __launch_bounds__(64 * kPairWaves) void moe_combine_bwd_kernel(
 #pragma unroll
           for (int i = 0; i < kPairUnroll; ++i) {
             const int64_t v = min(v0 + 64 * i, nv - 1);
-            ov[i] = o[v];
+            ov[i] = NT ? load_nt(o + v) : o[v];
             if (DY_F32) {
               const float4 a = ((const float4*)dy)[2 * (t * nv + v)], b = ((const float4*)dy)[2 * (t * nv + v) + 1];
               f[i][0] = a.x, f[i][1] = a.y, f[i][2] = a.z, f[i][3] = a.w;
@@ -554,8 +554,11 @@ hipError_t launch_moe_combine_bwd(const void* dy, const void* out, const float* 
                                   hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const dim3 grid((unsigned)T), block(64 * (unsigned)(topk < kPairWaves ? topk : kPairWaves));
-  const auto kernel = N % 8 == 0 ? (dy_f32 ? moe_combine_bwd_kernel<true, true> : moe_combine_bwd_kernel<false, true>)
-                                 : (dy_f32 ? moe_combine_bwd_kernel<true, false> : moe_combine_bwd_kernel<false, false>);
+  const bool nt = T * topk * N * 4 >= kHintBytes;
+  const auto vec = dy_f32 ? (nt ? moe_combine_bwd_kernel<true, true, true> : moe_combine_bwd_kernel<true, true, false>)
+                          : (nt ? moe_combine_bwd_kernel<false, true, true> : moe_combine_bwd_kernel<false, true, false>);
+  const auto kernel = N % 8 == 0 ? vec
+                      : dy_f32 ? moe_combine_bwd_kernel<true, false, false> : moe_combine_bwd_kernel<false, false, false>;
   kernel<<<grid, block, 0, stream>>>(dy, (const uint16_t*)out, w, row_of, (uint16_t*)d_out, d_w, (int)topk, R, N);
   return hipGetLastError();
 }

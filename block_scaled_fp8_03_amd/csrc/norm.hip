@@ -40,14 +40,25 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 
 // 8 elements of a row as floats
 template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t v, float* f) {
+__device__ __forceinline__ void floats_of(const uint4* u, float* f) {
   if (F32) {
-    const float4 a = ((const float4*)p)[2 * v], b = ((const float4*)p)[2 * v + 1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = bits_f32(w[i]);
   } else {
-    unpack8(((const uint4*)p)[v], f);
+    unpack8(u[0], f);
   }
+}
+// NT: read once (the norm's weight is read by every row)
+template <bool F32, bool NT>
+__device__ __forceinline__ void load8(const void* p, int64_t v, float* f) {
+  uint4 u[F32 ? 2 : 1];
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+    const uint4* at = (const uint4*)p + (F32 ? 2 * v + i : v);
+    u[i] = NT ? load_nt(at) : *at;
+  }
+  floats_of<F32>(u, f);
 }
 template <bool F32>
 __device__ __forceinline__ void store8(void* p, int64_t v, const float* f) {
@@ -59,8 +70,8 @@ __device__ __forceinline__ void store8(void* p, int64_t v, const float* f) {
   }
 }
 __device__ __forceinline__ void load_w(const RmsNorm& p, int64_t v, float* f) {
-  if (p.w_f32) load8<true>(p.w, v, f);
-  else load8<false>(p.w, v, f);
+  if (p.w_f32) load8<true, false>(p.w, v, f);
+  else load8<false, false>(p.w, v, f);
 }
 
 }  // namespace
@@ -69,7 +80,7 @@ __device__ __forceinline__ void load_w(const RmsNorm& p, int64_t v, float* f) {
 // forward: TPR lanes a row (0: the workgroup), VPL vectors of 8 a lane; RES 0
 // none, 1 bf16, 2 float32.  16 consecutive lanes hold a block of 128.
 // ----------------------------------------------------------------------------
-template <int TPR, int VPL, int RES>
+template <int TPR, int VPL, int RES, bool NT>
 __global__ __launch_bounds__(TPR ? kThreads : kMaxThreads) void rmsnorm_kernel(const RmsNorm p) {
   __shared__ float red[kMaxThreads / 64];
   const int tpr = TPR ? TPR : (int)blockDim.x;
@@ -83,10 +94,10 @@ __global__ __launch_bounds__(TPR ? kThreads : kMaxThreads) void rmsnorm_kernel(c
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     const int v = lane + j * tpr, vv = min(v, nv - 1);
-    unpack8(xr[vv], t[j]);
+    unpack8(NT ? load_nt(xr + vv) : xr[vv], t[j]);
     if (RES) {
       float r[8];
-      load8<RES == 2>(p.res, mm * nv + vv, r);
+      load8<RES == 2, NT>(p.res, mm * nv + vv, r);
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[j][i] += r[i];
     }
@@ -126,25 +137,22 @@ struct RowPlan {
 RowPlan plan_of(int64_t K) {
   const int64_t nv = K / 8;
   if (nv <= 64) return {nv <= 16 ? 16 : nv <= 32 ? 32 : 64, 1};
-  int vpl = nv <= 512 ? 1 : nv <= 2048 ? 2 : 4;
+  const int vpl = nv <= kMaxThreads ? 1 : nv <= 2 * kMaxThreads ? 2 : 4;
   return {(int)((nv + 64 * vpl - 1) / (64 * vpl)) * 64, vpl};
 }
 
-template <int RES>
+template <int RES, bool NT>
 void launch_fwd(const RmsNorm& p, hipStream_t stream) {
   const RowPlan plan = plan_of(p.K);
-  if (plan.tpr <= 64) {
-    const int rows = kThreads / plan.tpr;
-    const dim3 grid((unsigned)((p.M + rows - 1) / rows)), block(kThreads);
-    if (plan.tpr == 16) rmsnorm_kernel<16, 1, RES><<<grid, block, 0, stream>>>(p);
-    else if (plan.tpr == 32) rmsnorm_kernel<32, 1, RES><<<grid, block, 0, stream>>>(p);
-    else rmsnorm_kernel<64, 1, RES><<<grid, block, 0, stream>>>(p);
-    return;
-  }
-  const dim3 grid((unsigned)p.M), block(plan.tpr);
-  if (plan.vpl == 1) rmsnorm_kernel<0, 1, RES><<<grid, block, 0, stream>>>(p);
-  else if (plan.vpl == 2) rmsnorm_kernel<0, 2, RES><<<grid, block, 0, stream>>>(p);
-  else rmsnorm_kernel<0, 4, RES><<<grid, block, 0, stream>>>(p);
+  const int rows = plan.tpr <= 64 ? kThreads / plan.tpr : 1;
+  const dim3 grid((unsigned)((p.M + rows - 1) / rows)), block(plan.tpr <= 64 ? kThreads : plan.tpr);
+  const auto kernel = plan.tpr == 16   ? rmsnorm_kernel<16, 1, RES, NT>
+                      : plan.tpr == 32 ? rmsnorm_kernel<32, 1, RES, NT>
+                      : plan.tpr == 64 ? rmsnorm_kernel<64, 1, RES, NT>
+                      : plan.vpl == 1  ? rmsnorm_kernel<0, 1, RES, NT>
+                      : plan.vpl == 2  ? rmsnorm_kernel<0, 2, RES, NT>
+                                       : rmsnorm_kernel<0, 4, RES, NT>;
+  kernel<<<grid, block, 0, stream>>>(p);
 }
 
 }  // namespace
@@ -155,9 +163,11 @@ bool rmsnorm_fits(int64_t M, int64_t K) {
 }
 
 hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t stream) {
-  if (p.res == nullptr) launch_fwd<0>(p, stream);
-  else if (p.res_f32) launch_fwd<2>(p, stream);
-  else launch_fwd<1>(p, stream);
+  const int64_t bytes = p.M * p.K * (2 + (!p.res ? 0 : p.res_f32 ? 8 : 4) + (p.y ? 2 : 0) + (p.q ? 1 : 0));
+  const bool nt = bytes >= kHintBytes;
+  if (p.res == nullptr) nt ? launch_fwd<0, true>(p, stream) : launch_fwd<0, false>(p, stream);
+  else if (p.res_f32) nt ? launch_fwd<2, true>(p, stream) : launch_fwd<2, false>(p, stream);
+  else nt ? launch_fwd<1, true>(p, stream) : launch_fwd<1, false>(p, stream);
   return hipGetLastError();
 }
 
@@ -171,13 +181,10 @@ hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t stream) {
 // ----------------------------------------------------------------------------
 namespace {
 
-#ifndef GROUPS
-#define GROUPS 512
-#endif
-#ifndef AHEAD_
-#define AHEAD_ 1
-#endif
-constexpr int kBwdGroups = GROUPS;       // parts of dw at most
+// Parts of dw at most: each costs what a row does (written and read again as float32), and fewer leave CUs idle.
+// Below 1024 rows two to a part, as long as that leaves 128: 512 rows of 7168 14.9 us, in 512 parts 17.2, in 128 15.6;
+// 256 rows 11.4, in 256 parts 12.4.
+constexpr int kBwdGroups = 512, kBwdFew = 128;
 constexpr int kBwdThreads = 512;      // of a workgroup at most: 256 registers a lane
 
 // as plan_of, with at most kBwdThreads where a row is held
@@ -193,7 +200,8 @@ RowPlan bwd_plan_of(int64_t K) {
 int rows_at_once(const RowPlan& plan) { return plan.tpr <= 64 ? kThreads / plan.tpr : 1; }
 int64_t bwd_groups(int64_t M, int64_t K) {
   const int rows = rows_at_once(bwd_plan_of(K));
-  return std::min<int64_t>((M + rows - 1) / rows, kBwdGroups);
+  const int64_t units = (M + rows - 1) / rows;
+  return std::min<int64_t>(std::max((units + 1) / 2, std::min<int64_t>(units, kBwdFew)), kBwdGroups);
 }
 
 }  // namespace
@@ -204,19 +212,15 @@ namespace {
 template <bool F32>
 struct Raw8 {
   uint4 u[F32 ? 2 : 1];
+  template <bool NT>
   __device__ __forceinline__ void load(const void* p, int64_t v) {
-    u[0] = ((const uint4*)p)[F32 ? 2 * v : v];
-    if (F32) u[F32 ? 1 : 0] = ((const uint4*)p)[2 * v + 1];
-  }
-  __device__ __forceinline__ void floats(float* f) const {
-    if (F32) {
-      const uint4 a = u[0], b = u[F32 ? 1 : 0];
-      f[0] = bits_f32(a.x), f[1] = bits_f32(a.y), f[2] = bits_f32(a.z), f[3] = bits_f32(a.w);
-      f[4] = bits_f32(b.x), f[5] = bits_f32(b.y), f[6] = bits_f32(b.z), f[7] = bits_f32(b.w);
-    } else {
-      unpack8(u[0], f);
+#pragma unroll
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+      const uint4* at = (const uint4*)p + (F32 ? 2 * v + i : v);
+      u[i] = NT ? load_nt(at) : *at;
     }
   }
+  __device__ __forceinline__ void floats(float* f) const { floats_of<F32>(u, f); }
 };
 
 // What a lane holds of a row
@@ -224,24 +228,26 @@ template <int VPL, bool F32>
 struct RowHeld {
   Raw8<F32> h[VPL], e[VPL];
   Raw8<false> d[VPL];
-  __device__ __forceinline__ void load(const RmsNormBwd& p, int64_t m, int j, int v, bool res) {
-    h[j].load((const char*)p.h + m * p.ld_h * (F32 ? 4 : 2), v);
-    d[j].load((const char*)p.dy + m * p.K * 2, v);
-    if (res && p.dres) e[j].load((const char*)p.dres + m * p.K * (F32 ? 4 : 2), v);
+  template <bool NT, bool RES>
+  __device__ __forceinline__ void load(const RmsNormBwd& p, int64_t m, int j, int v) {
+    h[j].template load<NT>((const char*)p.h + m * p.ld_h * (F32 ? 4 : 2), v);
+    d[j].template load<NT>((const char*)p.dy + m * p.K * 2, v);
+    if (RES && p.dres) e[j].template load<NT>((const char*)p.dres + m * p.K * (F32 ? 4 : 2), v);
   }
 };
 
 }  // namespace
 
-// HOLD 2: VPL vectors a lane are held, and the next row's asked for before this one's
-// sums are waited for; 1: held; 0: rows too wide for that are read twice (the second
-// time from L2), vector by vector, and dw lies in LDS.
-template <int TPR, int VPL, int HOLD, bool F32, bool W_F32>
-__global__ __launch_bounds__(TPR ? kThreads : HOLD ? kBwdThreads : kMaxThreads) void rmsnorm_bwd_kernel(
+// HELD: a lane holds VPL vectors of its row; rows too wide for that are read twice
+// (the second time from L2), vector by vector, and dw lies in LDS.  (To ask for the
+// next row before this one's sums are waited for costs the registers of half the
+// waves: 4096 x 7168 59 us instead of 52.)
+template <int TPR, int VPL, bool HELD, bool F32, bool W_F32, bool NT>
+__global__ __launch_bounds__(TPR ? kThreads : HELD ? kBwdThreads : kMaxThreads) void rmsnorm_bwd_kernel(
     const RmsNormBwd p, float* parts) {
   __shared__ float red[4][kMaxThreads / 64];
   __shared__ float rows_dw[TPR ? kThreads * 8 : 1];
-  __shared__ float4 wide_dw[HOLD ? 1 : kMaxK / 4];
+  __shared__ float4 wide_dw[HELD ? 1 : kMaxK / 4];
   const int tpr = TPR ? TPR : (int)blockDim.x;
   const int lane = TPR ? (int)threadIdx.x % TPR : (int)threadIdx.x;
   const int rows = TPR ? kThreads / TPR : 1;
@@ -249,26 +255,22 @@ __global__ __launch_bounds__(TPR ? kThreads : HOLD ? kBwdThreads : kMaxThreads) 
   const int nv = (int)(p.K / 8);
   const float rk = (float)p.K;
   const int64_t step = (int64_t)gridDim.x * rows;
-  constexpr int HV = HOLD ? VPL : 1;
+  constexpr int HV = HELD ? VPL : 1;
   Raw8<W_F32> w[HV];
-  RowHeld<HV, F32> row, next;
+  RowHeld<HV, F32> row;
   float dw[HV][8];
 #pragma unroll
   for (int j = 0; j < HV; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
-  int64_t m0 = (int64_t)blockIdx.x * rows;
-  if (HOLD) {
+  if (HELD) {
 #pragma unroll
-    for (int j = 0; j < HV; ++j) {
-      const int v = min(lane + j * tpr, nv - 1);
-      w[j].load(p.w, v);
-      if (HOLD == 2) next.load(p, min(m0 + mine, p.M - 1), j, v, true);
-    }
+    for (int j = 0; j < HV; ++j) w[j].template load<false>(p.w, min(lane + j * tpr, nv - 1));
   } else {
     for (int v = lane; v < nv; v += tpr) wide_dw[2 * v] = wide_dw[2 * v + 1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
-  for (int turn = 0; m0 < p.M; m0 += step, turn ^= 1) {
+  int turn = 0;
+  for (int64_t m0 = (int64_t)blockIdx.x * rows; m0 < p.M; m0 += step, turn ^= 1) {
     const int64_t m = m0 + mine;
     float hh = 0.0f, gh = 0.0f;
     const auto add_up = [&](int j, bool on) {
@@ -285,21 +287,16 @@ __global__ __launch_bounds__(TPR ? kThreads : HOLD ? kBwdThreads : kMaxThreads) 
       hh += on ? a : 0.0f;
       gh += on ? b : 0.0f;
     };
-    if (HOLD) {
-      if (HOLD == 2) row = next;
+    if (HELD) {
 #pragma unroll
-      for (int j = 0; j < HV; ++j) {
-        const int v = min(lane + j * tpr, nv - 1);
-        if (HOLD == 2) next.load(p, min(m + step, p.M - 1), j, v, true);
-        else row.load(p, m, j, v, true);
-      }
+      for (int j = 0; j < HV; ++j) row.template load<NT, true>(p, min(m, p.M - 1), j, min(lane + j * tpr, nv - 1));
 #pragma unroll
       for (int j = 0; j < HV; ++j) add_up(j, lane + j * tpr < nv);
     } else {
 #pragma unroll 2
       for (int v = lane; v < nv; v += tpr) {
-        row.load(p, m, 0, v, false);
-        w[0].load(p.w, v);
+        row.template load<false, false>(p, m, 0, v);
+        w[0].template load<false>(p.w, v);
         add_up(0, true);
       }
     }
@@ -338,7 +335,7 @@ __global__ __launch_bounds__(TPR ? kThreads : HOLD ? kBwdThreads : kMaxThreads) 
       }
       store8<F32>(p.dx, m * nv + v, e);
     };
-    if (HOLD) {
+    if (HELD) {
       if (m < p.M) {
 #pragma unroll
         for (int j = 0; j < HV; ++j) {
@@ -349,10 +346,10 @@ __global__ __launch_bounds__(TPR ? kThreads : HOLD ? kBwdThreads : kMaxThreads) 
       }
     } else {
       for (int v = lane; v < nv; v += tpr) {
-        row.load(p, m, 0, v, true);
-        w[0].load(p.w, v);
+        row.template load<NT, true>(p, m, 0, v);
+        w[0].template load<false>(p.w, v);
         float sum[8];
-        load8<true>(wide_dw, v, sum);
+        load8<true, false>(wide_dw, v, sum);
         finish(0, v, sum);
         wide_dw[2 * v] = make_float4(sum[0], sum[1], sum[2], sum[3]);
         wide_dw[2 * v + 1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
@@ -371,7 +368,7 @@ __global__ __launch_bounds__(TPR ? kThreads : HOLD ? kBwdThreads : kMaxThreads) 
       for (int r = 0; r < rows; ++r) a += rows_dw[r * tpr * 8 + k];
       out[k] = a;
     }
-  } else if (HOLD) {
+  } else if (HELD) {
 #pragma unroll
     for (int j = 0; j < HV; ++j) {
       const int v = lane + j * tpr;
@@ -419,18 +416,25 @@ int64_t rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K) {
   return G > 1 ? G * K * 4 : 0;                              // one workgroup writes dw itself
 }
 
-template <bool F32, bool W_F32>
-static void launch_bwd(const RmsNormBwd& p, float* parts, hipStream_t stream) {
+template <bool F32, bool W_F32, bool NT>
+static void launch_bwd_of(const RmsNormBwd& p, float* parts, hipStream_t stream) {
   const RowPlan plan = bwd_plan_of(p.K);
   const dim3 grid((unsigned)bwd_groups(p.M, p.K)), block(plan.tpr <= 64 ? kThreads : plan.tpr);
-  const auto kernel = plan.tpr == 16  ? rmsnorm_bwd_kernel<16, 1, 2, F32, W_F32>
-                      : plan.tpr == 32 ? rmsnorm_bwd_kernel<32, 1, 2, F32, W_F32>
-                      : plan.tpr == 64 ? rmsnorm_bwd_kernel<64, 1, 2, F32, W_F32>
-                      : plan.vpl == 1  ? rmsnorm_bwd_kernel<0, 1, 2, F32, W_F32>
-                      : plan.vpl == 2  ? rmsnorm_bwd_kernel<0, 2, 1 + AHEAD_, F32, W_F32>
-                      : plan.vpl == 4  ? rmsnorm_bwd_kernel<0, 4, 1, F32, W_F32>
-                                       : rmsnorm_bwd_kernel<0, 0, 0, F32, W_F32>;
+  const auto kernel = plan.tpr == 16  ? rmsnorm_bwd_kernel<16, 1, true, F32, W_F32, NT>
+                      : plan.tpr == 32 ? rmsnorm_bwd_kernel<32, 1, true, F32, W_F32, NT>
+                      : plan.tpr == 64 ? rmsnorm_bwd_kernel<64, 1, true, F32, W_F32, NT>
+                      : plan.vpl == 1  ? rmsnorm_bwd_kernel<0, 1, true, F32, W_F32, NT>
+                      : plan.vpl == 2  ? rmsnorm_bwd_kernel<0, 2, true, F32, W_F32, NT>
+                      : plan.vpl == 4  ? rmsnorm_bwd_kernel<0, 4, true, F32, W_F32, NT>
+                                       : rmsnorm_bwd_kernel<0, 0, false, F32, W_F32, NT>;
   kernel<<<grid, block, 0, stream>>>(p, parts);
+}
+
+template <bool F32, bool W_F32>
+static void launch_bwd(const RmsNormBwd& p, float* parts, hipStream_t stream) {
+  const int64_t size = F32 ? 4 : 2, bytes = p.M * p.K * (2 + (p.dres ? 3 : 2) * size);
+  if (bytes >= kHintBytes) launch_bwd_of<F32, W_F32, true>(p, parts, stream);
+  else launch_bwd_of<F32, W_F32, false>(p, parts, stream);
 }
 
 hipError_t launch_rmsnorm_bwd(const RmsNormBwd& p, hipStream_t stream) {

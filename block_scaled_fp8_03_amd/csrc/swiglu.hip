@@ -12,7 +12,7 @@ namespace fp8bs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPasses = 4;           // rows that a thread takes where there are many
+constexpr int kPasses = 4, kBwdPasses = 2;   // rows that a thread takes where there are many
 
 // A workgroup's 256 threads are R = 256 / C rows of C vectors, C the largest power of
 // two, up to 256, that divides a row's vectors: no lane is idle and a thread's row and
@@ -34,13 +34,15 @@ __device__ __forceinline__ int64_t rows_of(const int32_t* n_rows, int64_t M) {
   return n_rows ? min(max<int64_t>(*n_rows, 0), M) : M;
 }
 
+template <bool NT>
 __device__ __forceinline__ uint4 load_row(const void* p, int64_t row, int64_t ld, uint32_t col) {
-  return ((const uint4*)((const uint16_t*)p + row * ld))[col];
+  const uint4* at = (const uint4*)((const uint16_t*)p + row * ld) + col;
+  return NT ? load_nt(at) : *at;
 }
 
 }  // namespace
 
-template <int PASSES>
+template <int PASSES, bool NT>
 __global__ __launch_bounds__(kThreads) void swiglu_kernel(const SwiGlu p, int shift, uint32_t chunks) {
   const Tile t = tile_of(shift, chunks, PASSES);
   const int64_t nv = p.N / 8, rows = rows_of(p.n_rows, p.M);
@@ -49,8 +51,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(const SwiGlu p, int sh
 #pragma unroll
   for (int k = 0; k < PASSES; ++k) {
     const int64_t r = t.row + k * t.step < rows ? t.row + k * t.step : t.row;
-    g[k] = load_row(p.gate, r, p.ld_g, t.col);
-    u[k] = load_row(p.up, r, p.ld_u, t.col);
+    g[k] = load_row<NT>(p.gate, r, p.ld_g, t.col);
+    u[k] = load_row<NT>(p.up, r, p.ld_u, t.col);
   }
 #pragma unroll
   for (int k = 0; k < PASSES; ++k) {
@@ -72,7 +74,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(const SwiGlu p, int sh
 }
 
 // du = dy * g * sigmoid(g),  dg = dy * u * sigmoid(g) * (1 + g * (1 - sigmoid(g)))
-template <int PASSES>
+template <int PASSES, bool NT>
 __global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const SwiGluBwd p, int shift, uint32_t chunks) {
   const Tile t = tile_of(shift, chunks, PASSES);
   const int64_t rows = rows_of(p.n_rows, p.M);
@@ -81,9 +83,9 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const SwiGluBwd p,
 #pragma unroll
   for (int k = 0; k < PASSES; ++k) {
     const int64_t r = t.row + k * t.step < rows ? t.row + k * t.step : t.row;
-    g[k] = load_row(p.gate, r, p.ld_g, t.col);
-    u[k] = load_row(p.up, r, p.ld_u, t.col);
-    d[k] = load_row(p.dy, r, p.N, t.col);
+    g[k] = load_row<NT>(p.gate, r, p.ld_g, t.col);
+    u[k] = load_row<NT>(p.up, r, p.ld_u, t.col);
+    d[k] = load_row<NT>(p.dy, r, p.N, t.col);
   }
 #pragma unroll
   for (int k = 0; k < PASSES; ++k) {
@@ -114,13 +116,13 @@ struct Plan {
 };
 // One row a thread while that leaves no more than 8 workgroups a CU, so that few rows
 // are spread over the card.
-Plan plan_of(int64_t M, int64_t N) {
+Plan plan_of(int64_t M, int64_t N, int most) {
   const int64_t nv = N / 8;
   int shift = 4;
   while (shift < 8 && nv % (2 << shift) == 0) ++shift;
   const int64_t chunks = nv >> shift, step = kThreads >> shift;
   const int64_t one = (M + step - 1) / step;
-  const int passes = one <= 2048 / chunks ? 1 : kPasses;
+  const int passes = one <= 2048 / chunks ? 1 : most;
   return {shift, (uint32_t)chunks, passes, (one + passes - 1) / passes * chunks};
 }
 
@@ -130,20 +132,24 @@ Plan plan_of(int64_t M, int64_t N) {
 bool swiglu_fits(int64_t M, int64_t N) {
   if (M <= 0 || N <= 0) return true;
   if (N >= (int64_t)1 << 31 || M >= (int64_t)1 << 40) return false;
-  const Plan q = plan_of(M, N);
+  const Plan q = plan_of(M, N, kBwdPasses);
   return q.grid / q.chunks <= (((int64_t)1 << 32) - 1) / kThreads / q.chunks;
 }
 
 hipError_t launch_swiglu(const SwiGlu& p, hipStream_t stream) {
-  const Plan q = plan_of(p.M, p.N);
-  const auto kernel = q.passes == 1 ? swiglu_kernel<1> : swiglu_kernel<kPasses>;
+  const Plan q = plan_of(p.M, p.N, kPasses);
+  const int64_t bytes = p.M * p.N * (4 + (p.y ? 2 : 0) + (p.q ? 1 : 0));
+  const auto kernel = q.passes == 1 ? swiglu_kernel<1, false>
+                      : bytes >= kHintBytes ? swiglu_kernel<kPasses, true> : swiglu_kernel<kPasses, false>;
   kernel<<<dim3((unsigned)q.grid), dim3(kThreads), 0, stream>>>(p, q.shift, q.chunks);
   return hipGetLastError();
 }
 
 hipError_t launch_swiglu_bwd(const SwiGluBwd& p, hipStream_t stream) {
-  const Plan q = plan_of(p.M, p.N);
-  const auto kernel = q.passes == 1 ? swiglu_bwd_kernel<1> : swiglu_bwd_kernel<kPasses>;
+  const Plan q = plan_of(p.M, p.N, kBwdPasses);
+  const auto kernel = q.passes == 1 ? swiglu_bwd_kernel<1, false>
+                      : 10 * p.M * p.N >= kHintBytes ? swiglu_bwd_kernel<kBwdPasses, true>
+                                                       : swiglu_bwd_kernel<kBwdPasses, false>;
   kernel<<<dim3((unsigned)q.grid), dim3(kThreads), 0, stream>>>(p, q.shift, q.chunks);
   return hipGetLastError();
 }
