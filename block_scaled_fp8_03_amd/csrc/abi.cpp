@@ -656,8 +656,8 @@ int fp8bs_moe_gate(const void* logits, int64_t ld, int logits_dtype, const float
   return status_of(fp8bs::launch_moe_gate(a, (hipStream_t)stream));
 }
 
-// sequences that a launch has a workgroup of 512 threads for
-static const int64_t kLimitBalance = 1 << 22;
+// sequences that a launch has a workgroup of 1024 threads for
+static const int64_t kLimitBalance = (1 << 22) - 1;
 
 int64_t fp8bs_moe_balance_workspace_size(int64_t T, int64_t S, int64_t E) {
   if (T < 0 || T > kLimitRows || S < 0 || S > kLimitBalance || E < 1 || E > 1024) return -1;

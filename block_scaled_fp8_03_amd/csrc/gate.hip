@@ -187,20 +187,20 @@ __device__ __forceinline__ void shares(float* score, float sum, bool softmax) {
   for (int v = 0; v < V; ++v) score[v] = score[v] * up * by;
 }
 
-// Sequence s's tokens [a, b), inside [0, T)
-__device__ __forceinline__ void bounds_of(const int32_t* cu, int64_t s, int64_t T, int64_t* a, int64_t* b) {
-  *a = cu ? min(max<int64_t>(cu[s], 0), T) : 0;
-  *b = cu ? max(min(max<int64_t>(cu[s + 1], 0), T), *a) : T;
+// Sequence s's tokens [a, b), inside [0, T); T < 2^24
+__device__ __forceinline__ void bounds_of(const int32_t* cu, int s, int T, int* a, int* b) {
+  *a = cu ? min(max(cu[s], 0), T) : 0;
+  *b = cu ? max(min(max(cu[s + 1], 0), T), *a) : T;
 }
 
 // The last of S sequences that starts at token t or before, 0 if none does, by the
 // wave's 64 probes at a time.
-__device__ __forceinline__ int64_t sequence_of(const int32_t* cu, int64_t S, int64_t t, int lane) {
-  int64_t lo = 0;
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int S, int t, int lane) {
+  int lo = 0;
   while (S > 1) {
-    const int64_t step = (S + 63) / 64, at = lane * step;
-    const int before = __popcll(__ballot(at < S && cu[lo + at] <= t));
-    const int64_t skip = (int64_t)max(before - 1, 0) * step;
+    const int step = (S + 63) / 64, at = lane * step;
+    const int before = __popcll(__ballot(at < S && cu[lo + min(at, S - 1)] <= t));
+    const int skip = max(before - 1, 0) * step;
     lo += skip;
     S = min(step, S - skip);
   }
@@ -227,7 +227,7 @@ template <int V, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void moe_gate_kernel(const MoeGate p) {
   __shared__ uint32_t slots[kWaves][64 * V];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
+  const int t = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * kWaves + wave));
   if (t >= p.T) return;                                       // waves work apart: no barrier follows
   const int E = (int)p.E, G = (int)p.groups;
   float z[V], top_z = 0.0f, all = 0.0f;
@@ -340,8 +340,8 @@ __global__ __launch_bounds__(64 * kWaves) void moe_gate_kernel(const MoeGate p) 
     w = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;
   }
   if (lane < (int)p.topk) {
-    p.indices[t * p.topk + lane] = id;
-    p.weights[t * p.topk + lane] = w * p.route_scale;
+    p.indices[t * (int)p.topk + lane] = id;                   // T * topk < 2^31
+    p.weights[t * (int)p.topk + lane] = w * p.route_scale;
   }
 }
 
@@ -399,7 +399,7 @@ BalancePlan balance_plan(int64_t T, int64_t E) {
 // A sequence's results from its sums, by one workgroup: probs, counts, and the loss
 // E / (topk * n) * sum counts * probs.  get(e, &shares, &hits); `red` one float a wave.
 template <typename F>
-__device__ __forceinline__ void finish_sequence(const MoeBalance& p, int64_t s, int64_t n, float* red, F get) {
+__device__ __forceinline__ void finish_sequence(const MoeBalance& p, int s, int n, float* red, F get) {
   const int E = (int)p.E;
   const float mean = n > 0 ? __fdiv_rn(1.0f, (float)n) : 0.0f;
   float part = 0.0f;
@@ -408,8 +408,8 @@ __device__ __forceinline__ void finish_sequence(const MoeBalance& p, int64_t s, 
     int32_t h;
     get(e, &q, &h);
     q *= mean;
-    p.probs[s * E + e] = q;
-    p.counts[s * E + e] = h;
+    p.probs[(int64_t)s * E + e] = q;
+    p.counts[(int64_t)s * E + e] = h;
     part = __builtin_fmaf(q, (float)h, part);
   }
   part = wave_sum(part);
@@ -427,19 +427,19 @@ __device__ __forceinline__ void finish_sequence(const MoeBalance& p, int64_t s, 
 
 // ONE: the only workgroup, which makes the results of every sequence itself.
 template <int V, bool VEC, bool ONE>
-__global__ __launch_bounds__(64 * kBalanceWaves) void moe_balance_kernel(const MoeBalance p, int64_t rows, int64_t width) {
+__global__ __launch_bounds__(64 * kBalanceWaves) void moe_balance_kernel(const MoeBalance p, int rows, int width) {
   __shared__ float sums[kBalanceWaves][64 * V];
   __shared__ int32_t hits[64 * V];
   __shared__ float red[kBalanceWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int E = (int)p.E;
-  const int64_t lo = (int64_t)blockIdx.x * rows, hi = min(lo + rows, p.T);
-  int64_t s = p.cu && !ONE ? sequence_of(p.cu, p.S, lo, lane) : 0;
-  for (; s < p.S; ++s) {
-    int64_t a, b;
-    bounds_of(p.cu, s, p.T, &a, &b);
+  const int lo = (int)blockIdx.x * rows, hi = min(lo + rows, (int)p.T);
+  int s = p.cu && !ONE ? __builtin_amdgcn_readfirstlane(sequence_of(p.cu, (int)p.S, lo, lane)) : 0;
+  for (; s < (int)p.S; ++s) {
+    int a, b;
+    bounds_of(p.cu, s, (int)p.T, &a, &b);
     if (!ONE && a >= hi) break;
-    const int64_t n = b - a;
+    const int n = b - a;
     a = max(a, lo);
     b = min(b, hi);
     if (!ONE && a >= b) continue;
@@ -448,8 +448,8 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void moe_balance_kernel(const M
     float acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-    for (int64_t t = a + wave; t < b; t += kBalanceWaves) {
-      int32_t id = lane < (int)p.topk ? p.indices[t * p.topk + lane] : -1;
+    for (int t = a + wave; t < b; t += kBalanceWaves) {
+      const int32_t id = lane < (int)p.topk ? p.indices[t * (int)p.topk + lane] : -1;
       float z[V], score[V];
       load_logits<V, VEC>(p.logits, p.f32, t * p.ld, E, lane, z);
       const float sum = scores<V>(z, p.softmax, score);
@@ -470,8 +470,8 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void moe_balance_kernel(const M
     if (ONE) {
       finish_sequence(p, s, n, red, get);
     } else {
-      const int64_t slot = (blockIdx.x + s) * width;
-      for (int e = threadIdx.x; e < (int)width; e += 64 * kBalanceWaves) {
+      const int64_t slot = (int64_t)((int)blockIdx.x + s) * width;
+      for (int e = threadIdx.x; e < width; e += 64 * kBalanceWaves) {
         float q = 0.0f;
         int32_t h = 0;
         if (e < E) get(e, &q, &h);
@@ -483,29 +483,29 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void moe_balance_kernel(const M
   }
 }
 
-constexpr int kJoinThreads = 1024;
-__global__ __launch_bounds__(kJoinThreads) void moe_balance_join_kernel(const MoeBalance p, int64_t rows, int64_t width) {
+constexpr int kJoinThreads = 1024, kJoinGroups = 32;
+__global__ __launch_bounds__(kJoinThreads) void moe_balance_join_kernel(const MoeBalance p, int rows, int width) {
   __shared__ float4 sums[kJoinThreads];
   __shared__ int4 hits[kJoinThreads];
   __shared__ float red[kJoinThreads / 64];
-  const int64_t s = blockIdx.x;
-  int64_t a, b;
-  bounds_of(p.cu, s, p.T, &a, &b);
-  const int64_t first = a / rows, last = b > a ? (b - 1) / rows + 1 : first;   // workgroups with some of its tokens
+  const int s = blockIdx.x;
+  int a, b;
+  bounds_of(p.cu, s, (int)p.T, &a, &b);
+  const int first = a / rows, last = b > a ? (b - 1) / rows + 1 : first;       // workgroups with some of its tokens
   // a thread adds up 4 experts of every `groups`-th slot, 4 slots' loads at a time
-  const int cols = (int)(width / 4), groups = min(kJoinThreads / cols, 64);
-  const int col = (int)threadIdx.x % cols, grp = (int)threadIdx.x / cols;
+  const int cols = width / 4, groups = min(kJoinThreads / cols, kJoinGroups);
+  const int grp = (int)threadIdx.x / cols, col = (int)threadIdx.x - grp * cols;
   float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   int4 h = make_int4(0, 0, 0, 0);
   if (grp < groups) {
-    for (int64_t g = first + grp; g < last; g += 4 * groups) {
+    for (int g = first + grp; g < last; g += 4 * groups) {
       float4 x[4];
       int4 y[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t slot = min(g + i * groups, last - 1) + s;
-        x[i] = ((const float4*)(p.part_probs + slot * width))[col];
-        y[i] = ((const int4*)(p.part_counts + slot * width))[col];
+        const int64_t at = (int64_t)(min(g + i * groups, last - 1) + s) * width;
+        x[i] = ((const float4*)(p.part_probs + at))[col];
+        y[i] = ((const int4*)(p.part_counts + at))[col];
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -521,6 +521,7 @@ __global__ __launch_bounds__(kJoinThreads) void moe_balance_join_kernel(const Mo
   finish_sequence(p, s, b - a, red, [&](int e, float* q, int32_t* h) {
     *q = 0.0f;
     *h = 0;
+#pragma unroll 4
     for (int g = 0; g < groups; ++g) {
       *q += ((const float*)sums)[g * width + e];
       *h += ((const int32_t*)hits)[g * width + e];
@@ -544,11 +545,11 @@ hipError_t launch_moe_balance(const MoeBalance& q, hipStream_t stream) {
   p.part_counts = (int32_t*)p.workspace + (plan.groups + p.S) * plan.width;
   const dim3 grid((unsigned)std::max<int64_t>(plan.groups, 1)), block(64 * kBalanceWaves);
 #define CALL(V, VEC)                                                                                        \
-  if (one) moe_balance_kernel<V, VEC, true><<<grid, block, 0, stream>>>(p, plan.rows, plan.width);          \
-  else moe_balance_kernel<V, VEC, false><<<grid, block, 0, stream>>>(p, plan.rows, plan.width)
+  if (one) moe_balance_kernel<V, VEC, true><<<grid, block, 0, stream>>>(p, (int)plan.rows, (int)plan.width);          \
+  else moe_balance_kernel<V, VEC, false><<<grid, block, 0, stream>>>(p, (int)plan.rows, (int)plan.width)
   FP8BS_BY_EXPERTS(p, CALL)
 #undef CALL
-  if (!one) moe_balance_join_kernel<<<dim3((unsigned)p.S), dim3(kJoinThreads), 0, stream>>>(p, plan.rows, plan.width);
+  if (!one) moe_balance_join_kernel<<<dim3((unsigned)p.S), dim3(kJoinThreads), 0, stream>>>(p, (int)plan.rows, (int)plan.width);
   return hipGetLastError();
 }
 
@@ -566,26 +567,26 @@ template <int V, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void moe_gate_bwd_kernel(const MoeGateBwd p) {
   __shared__ float slots[kWaves][64 * V];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
+  const int t = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * kWaves + wave));
   if (t >= p.T) return;
   const int E = (int)p.E, K = (int)p.topk;
   int e = -1;
   float uk = 0.0f;
   if (p.d_weights && lane < K) {
-    e = p.indices[t * p.topk + lane];
-    uk = p.d_weights[t * p.topk + lane];
+    e = p.indices[t * K + lane];                              // T * topk < 2^31
+    uk = p.d_weights[t * K + lane];
     if (e < 0 || e >= E) e = -1, uk = 0.0f;
   }
   float z[V], score[V], u[V];
   load_logits<V, VEC>(p.logits, p.f32, t * p.ld, E, lane, z);
   // the token's sequence, asked for before the scores are made
-  int64_t a = 0, b = 0;
+  int a = 0, b = 0;
   uint32_t hits[V];
   float dl = 0.0f;
   if (p.d_loss) {
-    const int64_t s = p.cu ? sequence_of(p.cu, p.S, t, lane) : 0;
-    bounds_of(p.cu, s, p.T, &a, &b);
-    load_words<V, false>((const uint32_t*)p.counts + s * E, lane * V, E, 0, hits);
+    const int s = p.cu ? sequence_of(p.cu, (int)p.S, t, lane) : 0;
+    bounds_of(p.cu, s, (int)p.T, &a, &b);
+    load_words<V, false>((const uint32_t*)p.counts + (int64_t)s * E, lane * V, E, 0, hits);
     dl = p.d_loss[s];
   }
   const float sum = scores<V>(z, p.softmax, score);
@@ -643,7 +644,7 @@ __global__ __launch_bounds__(64 * kWaves) void moe_gate_bwd_kernel(const MoeGate
       dz[v] = u[v] * sigmoid_of(-z[v], x);
     }
   }
-  const int64_t at = t * E + lane * V;
+  const int64_t at = (int64_t)t * E + lane * V;
   if (VEC) {
     if (lane * V >= E) return;
     if (p.out_f32) {

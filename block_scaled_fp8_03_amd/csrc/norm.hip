@@ -157,9 +157,9 @@ void launch_fwd(const RmsNorm& p, hipStream_t stream) {
 
 }  // namespace
 
-// A row's widest workgroup: K up to 32768, one workgroup a row, at most 2^32 - 1 threads.
+// One launch has at most 2^32 - 1 threads: 64 a row at most up to 512 columns, then 1024.
 bool rmsnorm_fits(int64_t M, int64_t K) {
-  return K <= kMaxK && M <= (((int64_t)1 << 32) - 1) / kMaxThreads;
+  return K <= kMaxK && M <= (((int64_t)1 << 32) - 1) / (K <= 512 ? 64 : kMaxThreads);
 }
 
 hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t stream) {

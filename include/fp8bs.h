@@ -551,7 +551,8 @@ int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fm
  * rmsnorm -- with the residual's addition and FP8 output:
  *   t = x + res (x without a residual),  c = t / sqrt(mean(t^2) + eps) * norm_w
  *   res_out = t rounded to its type,  y = bf16(c)
- *   per 128 columns: s by act_quant's rule on c, q = e4m3(c / s)
+ *   per 128 columns: s by act_quant's rule on c, q = e4m3(c / s), the quotient
+ *   within two roundings (a product with 1 / s)
  * All in float32 from the inputs on, each output rounded once: the norm is
  * that of the unrounded sum, the codes are those of the unrounded norm.  A row
  * whose squares sum to infinity in float32 gives zeros, as does one of zeros;
@@ -565,7 +566,8 @@ int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fm
  *   y        out  bf16 [M, K], or NULL
  *   q, s     out  e4m3 [M, K] and float32 [M, K/128], or both NULL; y or q is there
  *   scale_fmt     FP8BS_SCALE_FP32 or FP8BS_SCALE_UE8M0
- *   0 <= M <= 4194303, K % 128 == 0, 0 <= K <= 32768 (M or K 0: no-op).
+ *   0 <= M <= 4194303 (67108863 for K <= 512), K % 128 == 0, 0 <= K <= 32768 (M
+ *   or K 0: no-op).
  * All pointers 16-byte aligned but s (4).
  *
  * rmsnorm_bwd -- of y by the norm's input h (x, or res_out) and by norm_w:
@@ -631,7 +633,7 @@ int fp8bs_rmsnorm_bwd(const void* dy_bf16, const void* h, int64_t ld_h, int h_dt
  *   counts   out  int32 [S, E];  probs  out  float32 [S, E];  loss  out  float32 [S]
  *   workspace     DEVICE, >= fp8bs_moe_balance_workspace_size(T, S, E) bytes (0:
  *                 NULL), 16-byte aligned, scratch, not shared by concurrent calls
- *   0 <= S <= 2^22 (0 = no-op); T = 0 gives zeros.
+ *   0 <= S < 2^22 (0 = no-op); T = 0 gives zeros.
  *
  * moe_gate_bwd -- the gradient by the logits of both: of the weights, given
  * d_weights, and of the losses, given d_loss (the counts and the choice of
@@ -660,7 +662,7 @@ int fp8bs_moe_gate_bwd(const void* logits, int64_t ld, int logits_dtype, const i
 /*
  * swiglu -- the activation between an expert's two products:
  *   a = g * sigmoid(g) * u   (float32),  y = bf16(a),
- *   per 128 columns: s by act_quant's rule on a, q = e4m3(a / s)
+ *   per 128 columns: s by act_quant's rule on a, q = e4m3(a / s) as rmsnorm's
  *   gate, up in   bf16, element (m, n) at [m*ld + n]: two tensors, or the halves
  *                 of one; ld_g, ld_u >= 0, multiples of 8
  *   n_rows   in   DEVICE int32 [1], or NULL: rows from *n_rows (clamped to [0, M])

@@ -34,8 +34,8 @@ ALL = {"fp8bs_rmsnorm": NORM, "fp8bs_rmsnorm_bwd": NORM_BWD, "fp8bs_moe_gate": G
 
 # (entry point, status): changes of one argument or more that give it
 REFUSED = [
-    ("fp8bs_rmsnorm", SHAPE, [dict(M=-1), dict(K=-128), dict(K=200), dict(K=32768 + 128), dict(M=1 << 22), dict(ld=-8),
-                              dict(eps=-1.0), dict(eps=INF), dict(eps=NAN), dict(ld=1 << 62)]),
+    ("fp8bs_rmsnorm", SHAPE, [dict(M=-1), dict(K=-128), dict(K=200), dict(K=32768 + 128), dict(M=1 << 22, K=640), dict(M=1 << 26),
+                              dict(ld=-8),                              dict(eps=-1.0), dict(eps=INF), dict(eps=NAN), dict(ld=1 << 62)]),
     ("fp8bs_rmsnorm", ENUM, [dict(res_type=2), dict(fmt=2), dict(fmt=-1)]),
     ("fp8bs_rmsnorm", NULL, [dict(x=None), dict(w=None), dict(res=None), dict(res_out=None), dict(q=None), dict(s=None),
                              dict(y=None, q=None, s=None)]),
@@ -59,7 +59,7 @@ REFUSED = [
     ("fp8bs_moe_gate", ALIGN, [dict(z=A[0] + 2), dict(z=A[0] + 1, z_type=0), dict(bias=A[1] + 2), dict(idx=A[2] + 1),
                                dict(w=A[3] + 2)]),
     ("fp8bs_moe_gate", ALIAS, [dict(idx=A[0] + 64), dict(w=A[2] + 16), dict(w=A[1])]),
-    ("fp8bs_moe_balance", SHAPE, [dict(T=-1), dict(S=-1), dict(S=(1 << 22) + 1), dict(E=1025), dict(topk=65), dict(nws=0),
+    ("fp8bs_moe_balance", SHAPE, [dict(T=-1), dict(S=-1), dict(S=1 << 22), dict(E=1025), dict(topk=65), dict(nws=0),
                                   dict(cu=None), dict(ld=-1)]),
     ("fp8bs_moe_balance", ENUM, [dict(z_type=3), dict(score=7)]),
     ("fp8bs_moe_balance", NULL, [dict(z=None), dict(idx=None), dict(counts=None), dict(probs=None), dict(loss=None),
@@ -136,9 +136,9 @@ def test_nothing_to_do(L, name, kw):
 def test_workspace_sizes(L):
     f, g = L.fp8bs_rmsnorm_bwd_workspace_size, L.fp8bs_moe_balance_workspace_size
     assert f(0, 256) == 0 and f(1, 7168) == 0 and f(4096, 7168) > 0
-    assert f(-1, 256) == f(1, 100) == f(1, 1 << 16) == f(1 << 22, 128) == -1
+    assert f(-1, 256) == f(1, 100) == f(1, 1 << 16) == f(1 << 22, 1024) == f(1 << 26, 128) == -1
     assert g(0, 1, 64) == g(100, 0, 64) == 0 and g(4096, 1, 256) > 0
-    assert g(-1, 1, 64) == g(1 << 24, 1, 64) == g(1, -1, 64) == g(1, 1, 0) == g(1, 1, 1025) == g(1, 1 << 23, 64) == -1
+    assert g(-1, 1, 64) == g(1 << 24, 1, 64) == g(1, -1, 64) == g(1, 1, 0) == g(1, 1, 1025) == g(1, 1 << 22, 64) == -1
 
 
 # --------------------------------------------------------------- the binding
