@@ -35,7 +35,7 @@ ALL = {"fp8bs_rmsnorm": NORM, "fp8bs_rmsnorm_bwd": NORM_BWD, "fp8bs_moe_gate": G
 # (entry point, status): changes of one argument or more that give it
 REFUSED = [
     ("fp8bs_rmsnorm", SHAPE, [dict(M=-1), dict(K=-128), dict(K=200), dict(K=32768 + 128), dict(M=1 << 22, K=640), dict(M=1 << 26),
-                              dict(ld=-8),                              dict(eps=-1.0), dict(eps=INF), dict(eps=NAN), dict(ld=1 << 62)]),
+                              dict(ld=-8), dict(eps=-1.0), dict(eps=INF), dict(eps=NAN), dict(ld=1 << 62)]),
     ("fp8bs_rmsnorm", ENUM, [dict(res_type=2), dict(fmt=2), dict(fmt=-1)]),
     ("fp8bs_rmsnorm", NULL, [dict(x=None), dict(w=None), dict(res=None), dict(res_out=None), dict(q=None), dict(s=None),
                              dict(y=None, q=None, s=None)]),
