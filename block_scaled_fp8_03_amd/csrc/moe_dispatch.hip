@@ -486,65 +486,75 @@ hipError_t launch_moe_combine(const void* out, const float* w, const int32_t* ro
 constexpr int kPairWaves = 8;
 constexpr int kPairUnroll = 4;
 
-template <bool DY_F32, bool VEC, bool NT>
+
+// 8 elements of a row whose width is no multiple of 8: aligned to an element only, which
+// the hardware's global loads and stores take
+struct __attribute__((packed, aligned(2))) Loose4 { uint32_t x, y, z, w; };
+struct __attribute__((packed, aligned(4))) Floats4 { float x, y, z, w; };
+template <bool ALIGNED, bool NT>
+__device__ __forceinline__ uint4 load_row8(const uint16_t* p) {
+  if (!ALIGNED) {
+    const Loose4 u = *(const Loose4*)p;
+    return make_uint4(u.x, u.y, u.z, u.w);
+  }
+  return NT ? load_nt((const uint4*)p) : *(const uint4*)p;
+}
+
+template <bool DY_F32, bool ALIGNED, bool NT>
 __global__ __launch_bounds__(64 * kPairWaves) void moe_combine_bwd_kernel(
     const void* __restrict__ dy, const uint16_t* __restrict__ out, const float* __restrict__ w,
     const int32_t* __restrict__ row_of, uint16_t* __restrict__ d_out, float* __restrict__ d_w, int topk,
     int64_t R, int64_t N) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = blockIdx.x;
+  const int64_t t = blockIdx.x, nv = N / 8;
+  const float* dy32 = (const float*)dy + t * N;
+  const uint16_t* dy16 = (const uint16_t*)dy + t * N;
   for (int k = threadIdx.x >> 6; k < topk; k += blockDim.x >> 6) {
     const int64_t r = row_of[t * topk + k];
     float sum = 0.0f;
     if (r >= 0 && r < R) {
       const float wk = w[t * topk + k];
-      if (VEC) {
-        const int64_t nv = N / 8;
-        const uint4* o = (const uint4*)out + r * nv;
-        uint4* to = (uint4*)d_out + r * nv;
-        for (int64_t v0 = lane; v0 < nv; v0 += 64 * kPairUnroll) {
-          uint4 ov[kPairUnroll];
-          float f[kPairUnroll][8];
+      const uint16_t* o = out + r * N;
+      uint16_t* to = d_out + r * N;
+      for (int64_t v0 = lane; v0 < nv; v0 += 64 * kPairUnroll) {
+        uint4 ov[kPairUnroll];
+        float f[kPairUnroll][8];
 #pragma unroll
-          for (int i = 0; i < kPairUnroll; ++i) {
-            const int64_t v = min(v0 + 64 * i, nv - 1);
-            ov[i] = NT ? load_nt(o + v) : o[v];
-            if (DY_F32) {
-              const float4 a = ((const float4*)dy)[2 * (t * nv + v)], b = ((const float4*)dy)[2 * (t * nv + v) + 1];
-              f[i][0] = a.x, f[i][1] = a.y, f[i][2] = a.z, f[i][3] = a.w;
-              f[i][4] = b.x, f[i][5] = b.y, f[i][6] = b.z, f[i][7] = b.w;
-            } else {
-              const uint4 a = ((const uint4*)dy)[t * nv + v];
-              const uint32_t h[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) f[i][2 * j] = bf16_lo(h[j]), f[i][2 * j + 1] = bf16_hi(h[j]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < kPairUnroll; ++i) {
-            if (v0 + 64 * i >= nv) break;
-            const uint32_t h[4] = {ov[i].x, ov[i].y, ov[i].z, ov[i].w};
-            uint32_t d[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              sum = __builtin_fmaf(f[i][2 * j], bf16_lo(h[j]), sum);
-              sum = __builtin_fmaf(f[i][2 * j + 1], bf16_hi(h[j]), sum);
-              d[j] = pack2_bf16(wk * f[i][2 * j], wk * f[i][2 * j + 1]);
-            }
-            store_nt(to + v0 + 64 * i, make_uint4(d[0], d[1], d[2], d[3]));
+        for (int i = 0; i < kPairUnroll; ++i) {
+          const int64_t at = 8 * min(v0 + 64 * i, nv - 1);
+          ov[i] = load_row8<ALIGNED, NT>(o + at);
+          if (DY_F32) {
+            const Floats4 a = *(const Floats4*)(dy32 + at), b = *(const Floats4*)(dy32 + at + 4);
+            f[i][0] = a.x, f[i][1] = a.y, f[i][2] = a.z, f[i][3] = a.w;
+            f[i][4] = b.x, f[i][5] = b.y, f[i][6] = b.z, f[i][7] = b.w;
+          } else {
+            unpack8(load_row8<ALIGNED, false>(dy16 + at), f[i]);
           }
         }
-      } else {
-        for (int64_t n = lane; n < N; n += 64) {
-          const float f = DY_F32 ? ((const float*)dy)[t * N + n]
-                                 : bits_f32((uint32_t)((const uint16_t*)dy)[t * N + n] << 16);
-          sum = __builtin_fmaf(f, bits_f32((uint32_t)out[r * N + n] << 16), sum);
-          d_out[r * N + n] = (uint16_t)pack2_bf16(wk * f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < kPairUnroll; ++i) {
+          if (v0 + 64 * i >= nv) break;
+          float h[8];
+          unpack8(ov[i], h);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            sum = __builtin_fmaf(f[i][j], h[j], sum);
+            h[j] = wk * f[i][j];
+          }
+          const uint4 d = pack8(h);
+          uint16_t* at = to + 8 * (v0 + 64 * i);
+          if (ALIGNED) store_nt((uint4*)at, d);
+          else *(Loose4*)at = Loose4{d.x, d.y, d.z, d.w};
         }
       }
+      if (!ALIGNED && lane < (int)(N - 8 * nv)) {             // less than 8 elements behind the last vector
+        const int64_t n = 8 * nv + lane;
+        const float f = DY_F32 ? dy32[n] : bits_f32((uint32_t)dy16[n] << 16);
+        sum = __builtin_fmaf(f, bits_f32((uint32_t)o[n] << 16), sum);
+        to[n] = (uint16_t)pack2_bf16(wk * f, 0.0f);
+      }
     }
-#pragma unroll
-    for (int i = 1; i < 64; i <<= 1) sum += __shfl_xor(sum, i);
+    sum = wave_sum(sum);
     if (lane == 0) d_w[t * topk + k] = sum;
   }
 }
