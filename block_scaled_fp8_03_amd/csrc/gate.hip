@@ -5,7 +5,9 @@
 // One wave a token: lane l holds experts l*V .. l*V + V - 1, so the lowest lane
 // and the lowest register of a maximum are the lowest expert.  A token's logits are
 // a few hundred bytes: what these kernels take is a wave's chain of instructions
-// (few tokens) or the instructions of all waves (many), not HBM.
+// (few tokens) or the instructions of all waves (many), not HBM.  256 experts in 8
+// groups, top 8, from a graph: 32 tokens 4.5 us, 2.2 of it the launch, 4096 tokens 7.1
+// (580 vector instructions a token); counts, loss and both gradients of 4096 tokens 17.7.
 #include <algorithm>
 
 #include "device_common.h"
@@ -113,9 +115,9 @@ __device__ __forceinline__ double rcp_f64(double d) {
 }
 
 // score[v] in 64 bits, rounded once; 0 for masked experts (all of a token masked: all 0).
-// Two scores that float32 arithmetic would leave a rounding apart, or exchange, decide
-// which expert a token takes: of 4096 tokens over 256 experts one or two have such a
-// pair.  Here the sum of errors is 2^-20 of a rounding.
+// Two scores that float32 arithmetic would exchange, or make equal, change which expert
+// a token takes or their order: with a float32 exponential one token in about 40,000
+// (256 experts in 8 groups, top 8).  Here the sum of errors is 2^-20 of a rounding.
 template <int V>
 __device__ __forceinline__ void exact_scores(const float* z, bool softmax, float* score) {
   if (!softmax) {

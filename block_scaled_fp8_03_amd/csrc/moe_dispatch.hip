@@ -482,7 +482,9 @@ hipError_t launch_moe_combine(const void* out, const float* w, const int32_t* ro
 // ----------------------------------------------------------------------------
 // A workgroup is a token, a wave takes every kPairWaves-th of its pairs: the
 // token's dy comes from HBM once and then from the CU's L1.  Each row of `out` is
-// read and each of d_out written once, in whole lines.
+// read and each of d_out written once, in whole lines: 4096 x 8 x 7168 move 999 MB in
+// 190 us, 5.3 TB/s, what a copy reaches.  A workgroup a pair instead (its sum through
+// LDS, a token's pairs on one XCD) takes 189; plain stores 204.
 constexpr int kPairWaves = 8;
 constexpr int kPairUnroll = 4;
 

@@ -6,7 +6,10 @@
 //   res_out = round(t), y = bf16(c), per 128: s = act_quant's rule on c, q = e4m3(c / s)
 //
 // HBM-bound: a row is read once, held in registers while its squares are summed,
-// and written once.
+// and written once.  One vector of 8 a lane up to 8192 columns, that is a row spread
+// over as many waves as it has 512 columns: 1 x 7168 3.07 us (two vectors a lane 3.29,
+// four 4.0), 4096 x 7168 46.1 (46.3, 47.8).  4096 x 7168 with a bf16 residual, codes and
+// bf16 out move 265 MB at 5.7 TB/s.
 #include <algorithm>
 
 #include "device_common.h"
@@ -177,7 +180,9 @@ hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t stream) {
 //   dx = r * (g - h * r^2 * mean(g * h)) + dres,  dw = sum over rows of dy * h * r
 // A workgroup goes through rows m, m + grid, ..., keeps its part of dw in
 // registers and leaves it in the workspace; a second kernel adds the parts in a
-// fixed order.
+// fixed order.  4096 x 7168 with dres: 235 MB and 29 MB of parts, 44 us and 5.2 for the
+// parts, together 49.5 (5.3 TB/s of both).  Two rows at a time in workgroups of twice
+// the size, and half the parts: 50.1; 1024 parts 56.6, 256 56.7.
 // ----------------------------------------------------------------------------
 namespace {
 
