@@ -566,7 +566,7 @@ hipError_t launch_moe_combine_bwd(const void* dy, const void* out, const float* 
                                   hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const dim3 grid((unsigned)T), block(64 * (unsigned)(topk < kPairWaves ? topk : kPairWaves));
-  const bool nt = T * topk * N * 4 >= kHintBytes;
+  const bool nt = N > 0 && T * topk >= kHintBytes / 4 / N;       // rows read and written
   const auto vec = dy_f32 ? (nt ? moe_combine_bwd_kernel<true, true, true> : moe_combine_bwd_kernel<true, true, false>)
                           : (nt ? moe_combine_bwd_kernel<false, true, true> : moe_combine_bwd_kernel<false, true, false>);
   const auto kernel = N % 8 == 0 ? vec

@@ -160,9 +160,11 @@ void launch_fwd(const RmsNorm& p, hipStream_t stream) {
 
 }  // namespace
 
-// One launch has at most 2^32 - 1 threads: 64 a row at most up to 512 columns, then 1024.
+// One launch has at most 2^32 - 1 threads: workgroups of 256 take 4 rows at least up to
+// 512 columns, those of 1024 at most one row.
 bool rmsnorm_fits(int64_t M, int64_t K) {
-  return K <= kMaxK && M <= (((int64_t)1 << 32) - 1) / (K <= 512 ? 64 : kMaxThreads);
+  constexpr int64_t kLimit = ((int64_t)1 << 32) - 1;
+  return K <= kMaxK && M <= (K <= 512 ? kLimit / kThreads * 4 : kLimit / kMaxThreads);
 }
 
 hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t stream) {

@@ -566,7 +566,7 @@ int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fm
  *   y        out  bf16 [M, K], or NULL
  *   q, s     out  e4m3 [M, K] and float32 [M, K/128], or both NULL; y or q is there
  *   scale_fmt     FP8BS_SCALE_FP32 or FP8BS_SCALE_UE8M0
- *   0 <= M <= 4194303 (67108863 for K <= 512), K % 128 == 0, 0 <= K <= 32768 (M
+ *   0 <= M <= 4194303 (67108860 for K <= 512), K % 128 == 0, 0 <= K <= 32768 (M
  *   or K 0: no-op).
  * All pointers 16-byte aligned but s (4).
  *
@@ -604,9 +604,9 @@ int fp8bs_rmsnorm_bwd(const void* dy_bf16, const void* h, int64_t ld_h, int h_dt
  *   indices = the topk largest keys' experts, the largest first
  *   weights = score / (sum of the chosen scores, if normalize) * route_scale
  * Ties go to the lowest index, among groups too.  An expert whose logit is -inf
- * or NaN, or whose key is -inf or NaN, is masked: it is never chosen, and a
- * softmax leaves it out.  Slots without an expert (all others masked) hold
- * index -1, which fp8bs_moe_route does not route, and weight 0.  Logits of
+ * or NaN is masked: its score is 0, a softmax leaves it out, and it is never
+ * chosen; nor is one whose key is -inf or NaN.  Slots for which no expert is left
+ * hold index -1, which fp8bs_moe_route does not route, and weight 0.  Logits of
  * +inf share a softmax's weight.  With a bias the scores are computed in 64
  * bits and rounded once, so that the choice does not turn on the last bit of
  * an exponential; all else is float32.
@@ -624,8 +624,8 @@ int fp8bs_rmsnorm_bwd(const void* dy_bf16, const void* h, int64_t ld_h, int h_dt
  *   probs[s, e]  = mean over its tokens of score_e / (sum of the token's scores)
  *   loss[s]      = E / (topk * n) * sum_e counts[s, e] * probs[s, e]
  * (1 where all experts are used alike).  A sequence without tokens gives zeros;
- * a token whose experts are all masked adds none; indices outside [0, E) are
- * not counted.
+ * a token whose experts are all masked (as above) adds no shares; indices outside
+ * [0, E) are not counted.
  *   indices  in   int32 [T, topk] (from fp8bs_moe_gate)
  *   cu_seq   in   DEVICE int32 [S + 1], non-decreasing, or NULL: one sequence
  *                 of all T tokens, S = 1.  The values are a precondition, not

@@ -267,3 +267,25 @@ def test_gradient_differences(kind, normalize):
         diff = (f(z.double() + step * v) - f(z.double() - step * v)) / (2 * step)
         bound = (size * (4 * eu.score_rel(z, E) + 8 * eu.H_F32) * v.abs()).sum() + 1e-6
         eu.inside((d.double().cpu() * v).sum(), diff, bound, "along a direction")
+
+
+def test_most_tokens():
+    """As many tokens as one launch has; all alike, read by a stride of 0."""
+    T, E, topk = (1 << 24) - 1, 8, 2
+    one = eu.normal((1, E), 1, 1.0, F32).to(DEV)
+    z = one.expand(T, E)
+    idx, w = fp8bs.moe_gate(z, topk)
+    i1, w1 = fp8bs.moe_gate(one, topk)
+    assert (idx == i1).all() and (w == w1).all()
+    cu = torch.tensor([0, 5, T - 1, T], dtype=torch.int32, device=DEV)
+    loss, counts, probs = fp8bs.moe_balance(z, idx, cu)
+    n = [5, T - 6, 1]
+    for s in range(3):
+        assert counts[s, i1[0].long()].tolist() == [n[s]] * topk and int(counts[s].sum()) == topk * n[s]
+    share = torch.sigmoid(one.double())
+    share = (share / share.sum()).expand(3, E)
+    # a wave of a workgroup adds 4096 tokens up one by one, and 512 workgroups' sums follow
+    eu.inside(probs, share, share.cpu() * (eu.score_rel(one.cpu(), E) + (4096 + 600) * eu.H_F32), "probs")
+    d = fp8bs.moe_gate_bwd(z, idx, None, cu_seq=cu, counts=counts, d_loss=torch.ones(3, device=DEV))
+    lone = fp8bs.moe_gate_bwd(one, i1, None, counts=counts[2:], d_loss=torch.ones(1, device=DEV))
+    assert torch.equal(d[T - 1:], lone) and torch.equal(d[5:6], d[T - 2:T - 1])

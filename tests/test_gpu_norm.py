@@ -139,3 +139,14 @@ def test_norm_last_rows_beyond_32_bits():
     w = eu.normal((K,), 2).to(DEV)
     y = fp8bs.rmsnorm(x, w, EPS)
     assert torch.equal(y[M - 3:], fp8bs.rmsnorm(some.to(DEV), w, EPS)) and (y[:M - 3] == 0).all()
+
+
+@pytest.mark.parametrize("M,K", [(67108860, 128), (4194303, 640)])
+def test_norm_most_rows(M, K):
+    """As many rows as one launch has; all alike, read by a stride of 0."""
+    one, w = eu.normal((1, K), 1).to(DEV), eu.normal((K,), 2).to(DEV)
+    y = fp8bs.rmsnorm(one.expand(M, K), w, EPS)
+    want = fp8bs.rmsnorm(one, w, EPS)
+    for at in (0, M // 2, M - 5):
+        assert torch.equal(y[at:at + 5], want.expand(5, K))
+    assert torch.equal(y[::4099], want.expand(y[::4099].shape[0], K))
