@@ -580,10 +580,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i:
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _call_on(dev, fn: str, *args, first: str = "cache.latent") -> None:
-    """fn(*args, the current stream of device `dev`, that of the tensor `first`), with that device current."""
+def _call_on(dev, fn: str, *args) -> None:
+    """fn(*args, the current stream of device `dev`), with that device current."""
     if dev.type != "cuda":
-        raise ValueError(f"{first} must be a device tensor")
+        raise ValueError("cache.latent must be a device tensor")
     stream = _raw_stream(dev.index)
     if _current_device() == dev.index:
         st = getattr(lib(), fn)(*args, stream)
@@ -805,8 +805,18 @@ def _shape2(t, message: str, name: str):
     return a, b
 
 
-def _empty(like: torch.Tensor, shape, dtype) -> torch.Tensor:
-    return like.new_empty(*shape, dtype=dtype)       # sizes one by one: 0.2 us less than as a tuple
+def _launch(first: str, dev, fn, *args) -> None:
+    """fn(*args, the current stream of `dev`), with that device current; `first` names the tensor that lies there."""
+    index = dev.index
+    if index is None:                                # what is not on a device has none
+        raise ValueError(f"{first} must be a device tensor")
+    if _current_device() == index:
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(index))
+    if st != 0:
+        raise Fp8bsError(fn.__name__, st)
 
 
 def _rmsnorm(x, M, K, res, norm_w, eps, res_out, y, q, s, scale_fmt) -> None:
@@ -814,9 +824,9 @@ def _rmsnorm(x, M, K, res, norm_w, eps, res_out, y, q, s, scale_fmt) -> None:
     dev = x.device
     xp, ld = _rows2(x, "x", _BF16, (M, K), dev)
     res_f32 = res is not None and getattr(res, "dtype", None) == torch.float32
-    _call_on(dev, "fp8bs_rmsnorm", xp, ld, _opt(res, "res", _FLOATS, (M, K), dev), res_out,
-             OUT_F32 if res_f32 else OUT_BF16, _ptr(norm_w, "norm_w", _FLOATS, (K,), dev),
-             norm_w.dtype == torch.float32, eps, y, q, s, _fmt(scale_fmt), M, K, first="x")
+    _launch("x", dev, lib().fp8bs_rmsnorm, xp, ld, _opt(res, "res", _FLOATS, (M, K), dev), res_out,
+            OUT_F32 if res_f32 else OUT_BF16, _ptr(norm_w, "norm_w", _FLOATS, (K,), dev),
+            norm_w.dtype == torch.float32, eps, y, q, s, _fmt(scale_fmt), M, K)
 
 
 def fp8bs_rmsnorm(x: torch.Tensor, res: Optional[torch.Tensor], res_out: Optional[torch.Tensor], norm_w: torch.Tensor,
@@ -836,8 +846,8 @@ def fp8bs_rmsnorm(x: torch.Tensor, res: Optional[torch.Tensor], res_out: Optiona
 def rmsnorm(x, norm_w, eps: float, residual=None):
     """fp8bs_rmsnorm: y bf16 [M, K]; with a residual (y, x + residual)."""
     M, K = _shape2(x, "x must be [M, K]", "x")
-    y = _empty(x, (M, K), torch.bfloat16)
-    h = None if residual is None else _empty(x, (M, K), getattr(residual, "dtype", None))
+    y = x.new_empty(M, K, dtype=torch.bfloat16)
+    h = None if residual is None else x.new_empty(M, K, dtype=getattr(residual, "dtype", None))
     _rmsnorm(x, M, K, residual, norm_w, eps, _at(h), y.data_ptr(), None, None, SCALE_FP32)
     return y if residual is None else (y, h)
 
@@ -846,9 +856,9 @@ def rmsnorm_quant(x, norm_w, eps: float, residual=None, scale_fmt="fp32", return
     """fp8bs_rmsnorm: (q e4m3 [M, K], s float32 [M, K/128]), then y bf16 if
     return_y, then x + residual if there is a residual."""
     M, K = _shape2(x, "x must be [M, K]", "x")
-    q, s = _empty(x, (M, K), torch.float8_e4m3fn), _empty(x, (M, K // BLOCK), torch.float32)
-    y = _empty(x, (M, K), torch.bfloat16) if return_y else None
-    h = None if residual is None else _empty(x, (M, K), getattr(residual, "dtype", None))
+    q, s = x.new_empty(M, K, dtype=torch.float8_e4m3fn), x.new_empty(M, K // BLOCK, dtype=torch.float32)
+    y = x.new_empty(M, K, dtype=torch.bfloat16) if return_y else None
+    h = None if residual is None else x.new_empty(M, K, dtype=getattr(residual, "dtype", None))
     _rmsnorm(x, M, K, residual, norm_w, eps, _at(h), _at(y), q.data_ptr(), s.data_ptr(), scale_fmt)
     return tuple(t for t in (q, s, y, h) if t is not None)
 
@@ -857,9 +867,9 @@ def _rmsnorm_bwd(dy, h, M, K, norm_w, eps, dres, dx, dw, ws, nbytes) -> None:
     """fp8bs_rmsnorm_bwd of outputs given by their addresses."""
     dev = h.device
     hp, ld = _rows2(h, "h", _FLOATS, (M, K), dev)
-    _call_on(dev, "fp8bs_rmsnorm_bwd", _ptr(dy, "dy", _BF16, (M, K), dev), hp, ld, _out_code(h),
-             _ptr(norm_w, "norm_w", _FLOATS, (K,), dev), norm_w.dtype == torch.float32, eps,
-             _opt(dres, "dres", (h.dtype,), (M, K), dev), dx, dw, M, K, ws, nbytes, first="h")
+    _launch("h", dev, lib().fp8bs_rmsnorm_bwd, _ptr(dy, "dy", _BF16, (M, K), dev), hp, ld, _out_code(h),
+            _ptr(norm_w, "norm_w", _FLOATS, (K,), dev), norm_w.dtype == torch.float32, eps,
+            _opt(dres, "dres", (h.dtype,), (M, K), dev), dx, dw, M, K, ws, nbytes)
 
 
 def fp8bs_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, norm_w: torch.Tensor, eps: float,
@@ -880,8 +890,8 @@ def rmsnorm_bwd(dy, h, norm_w, eps: float, dres=None):
     need = lib().fp8bs_rmsnorm_bwd_workspace_size(M, K)
     if need < 0:
         raise ValueError("sizes out of range")
-    dx, dw = _empty(h, (M, K), h.dtype), _empty(h, (K,), torch.float32)
-    ws = _empty(h, (need,), torch.uint8) if need else None
+    dx, dw = h.new_empty(M, K, dtype=h.dtype), h.new_empty(K, dtype=torch.float32)
+    ws = h.new_empty(need, dtype=torch.uint8) if need else None
     _rmsnorm_bwd(dy, h, M, K, norm_w, eps, dres, dx.data_ptr(), dw.data_ptr(), _at(ws), need)
     return dx, dw
 
@@ -890,8 +900,8 @@ def _moe_gate(logits, T, E, topk, bias, groups, topk_groups, score, normalize, r
     """fp8bs_moe_gate of outputs given by their addresses."""
     dev = logits.device
     zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
-    _call_on(dev, "fp8bs_moe_gate", zp, ld, _out_code(logits), _opt(bias, "bias", _F32, (E,), dev), T, E, topk, groups,
-             topk_groups, _score(score), normalize, route_scale, indices, weights, first="logits")
+    _launch("logits", dev, lib().fp8bs_moe_gate, zp, ld, _out_code(logits), _opt(bias, "bias", _F32, (E,), dev), T, E,
+            topk, groups, topk_groups, _score(score), normalize, route_scale, indices, weights)
 
 
 def fp8bs_moe_gate(logits: torch.Tensor, bias: Optional[torch.Tensor], groups: int, topk_groups: int, score,
@@ -910,7 +920,7 @@ def moe_gate(logits, topk: int, bias=None, groups: int = 1, topk_groups: Optiona
     """fp8bs_moe_gate: (indices int32 [T, topk], weights float32 [T, topk]), for
     moe_route and moe_combine.  All groups are kept unless topk_groups says so."""
     T, E = _shape2(logits, "logits must be [T, E]", "logits")
-    indices, weights = _empty(logits, (T, topk), torch.int32), _empty(logits, (T, topk), torch.float32)
+    indices, weights = logits.new_empty(T, topk, dtype=torch.int32), logits.new_empty(T, topk, dtype=torch.float32)
     _moe_gate(logits, T, E, topk, bias, groups, groups if topk_groups is None else topk_groups, score, normalize,
               route_scale, indices.data_ptr(), weights.data_ptr())
     return indices, weights
@@ -930,8 +940,8 @@ def _moe_balance(logits, T, E, indices, cu, S, score, counts, probs, loss, ws, n
     topk = _shape2(indices, "indices must be [T, topk]", "indices")[1]
     dev = logits.device
     zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
-    _call_on(dev, "fp8bs_moe_balance", zp, ld, _out_code(logits), _ptr(indices, "indices", _I32, (T, topk), dev), cu,
-             T, S, E, topk, _score(score), counts, probs, loss, ws, nbytes, first="logits")
+    _launch("logits", dev, lib().fp8bs_moe_balance, zp, ld, _out_code(logits),
+            _ptr(indices, "indices", _I32, (T, topk), dev), cu, T, S, E, topk, _score(score), counts, probs, loss, ws, nbytes)
 
 
 def fp8bs_moe_balance(logits: torch.Tensor, indices: torch.Tensor, cu_seq: Optional[torch.Tensor], score,
@@ -954,9 +964,9 @@ def moe_balance(logits, indices, cu_seq=None, score="sigmoid"):
     need = lib().fp8bs_moe_balance_workspace_size(T, S, E)
     if need < 0:
         raise ValueError("sizes out of range")
-    counts, probs = _empty(logits, (S, E), torch.int32), _empty(logits, (S, E), torch.float32)
-    loss = _empty(logits, (S,), torch.float32)
-    ws = _empty(logits, (need,), torch.uint8) if need else None
+    counts, probs = logits.new_empty(S, E, dtype=torch.int32), logits.new_empty(S, E, dtype=torch.float32)
+    loss = logits.new_empty(S, dtype=torch.float32)
+    ws = logits.new_empty(need, dtype=torch.uint8) if need else None
     _moe_balance(logits, T, E, indices, cu, S, score, counts.data_ptr(), probs.data_ptr(), loss.data_ptr(), _at(ws), need)
     return loss, counts, probs
 
@@ -968,10 +978,10 @@ def _moe_gate_bwd(logits, T, E, indices, d_weights, score, normalize, route_scal
     dev = logits.device
     zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
     cu, S = _sequences(cu_seq, dev)
-    _call_on(dev, "fp8bs_moe_gate_bwd", zp, ld, _out_code(logits), _ptr(indices, "indices", _I32, (T, topk), dev),
-             _opt(d_weights, "d_weights", _F32, (T, topk), dev), _score(score), normalize, route_scale, cu,
-             _opt(counts, "counts", _I32, (S, E), dev), _opt(d_loss, "d_loss", _F32, (S,), dev), T, S, E, topk,
-             d_logits, out_code, first="logits")
+    _launch("logits", dev, lib().fp8bs_moe_gate_bwd, zp, ld, _out_code(logits),
+            _ptr(indices, "indices", _I32, (T, topk), dev), _opt(d_weights, "d_weights", _F32, (T, topk), dev),
+            _score(score), normalize, route_scale, cu, _opt(counts, "counts", _I32, (S, E), dev),
+            _opt(d_loss, "d_loss", _F32, (S,), dev), T, S, E, topk, d_logits, out_code)
 
 
 def fp8bs_moe_gate_bwd(logits: torch.Tensor, indices: torch.Tensor, d_weights: Optional[torch.Tensor], score,
@@ -989,7 +999,7 @@ def moe_gate_bwd(logits, indices, d_weights=None, score="sigmoid", normalize: bo
                  cu_seq=None, counts=None, d_loss=None, out_dtype=torch.float32) -> torch.Tensor:
     """fp8bs_moe_gate_bwd: d_logits [T, E]."""
     T, E = _shape2(logits, "logits must be [T, E]", "logits")
-    d_logits = _empty(logits, (T, E), out_dtype)
+    d_logits = logits.new_empty(T, E, dtype=out_dtype)
     _moe_gate_bwd(logits, T, E, indices, d_weights, score, normalize, route_scale, cu_seq, counts, d_loss,
                   d_logits.data_ptr(), _out_code(d_logits))
     return d_logits
@@ -1000,7 +1010,7 @@ def _swiglu(gate, up, M, N, y, q, s, scale_fmt, n_rows) -> None:
     dev = gate.device
     gp, ldg = _rows2(gate, "gate", _BF16, (M, N), dev)
     up_, ldu = _rows2(up, "up", _BF16, (M, N), dev)
-    _call_on(dev, "fp8bs_swiglu", gp, ldg, up_, ldu, _count(n_rows, dev), y, q, s, _fmt(scale_fmt), M, N, first="gate")
+    _launch("gate", dev, lib().fp8bs_swiglu, gp, ldg, up_, ldu, _count(n_rows, dev), y, q, s, _fmt(scale_fmt), M, N)
 
 
 def fp8bs_swiglu(gate: torch.Tensor, up: torch.Tensor, y: Optional[torch.Tensor], q: Optional[torch.Tensor],
@@ -1018,7 +1028,7 @@ def fp8bs_swiglu(gate: torch.Tensor, up: torch.Tensor, y: Optional[torch.Tensor]
 def swiglu(gate, up, n_rows=None) -> torch.Tensor:
     """fp8bs_swiglu: bf16 [M, N], not initialised from row n_rows on."""
     M, N = _shape2(gate, "gate must be [M, N]", "gate")
-    y = _empty(gate, (M, N), torch.bfloat16)
+    y = gate.new_empty(M, N, dtype=torch.bfloat16)
     _swiglu(gate, up, M, N, y.data_ptr(), None, None, SCALE_FP32, n_rows)
     return y
 
@@ -1027,8 +1037,8 @@ def swiglu_quant(gate, up, scale_fmt="fp32", n_rows=None, return_y: bool = False
     """fp8bs_swiglu: (q e4m3 [M, N], s float32 [M, N/128]), then y bf16 if
     return_y; not initialised from row n_rows on."""
     M, N = _shape2(gate, "gate must be [M, N]", "gate")
-    q, s = _empty(gate, (M, N), torch.float8_e4m3fn), _empty(gate, (M, N // BLOCK), torch.float32)
-    y = _empty(gate, (M, N), torch.bfloat16) if return_y else None
+    q, s = gate.new_empty(M, N, dtype=torch.float8_e4m3fn), gate.new_empty(M, N // BLOCK, dtype=torch.float32)
+    y = gate.new_empty(M, N, dtype=torch.bfloat16) if return_y else None
     _swiglu(gate, up, M, N, _at(y), q.data_ptr(), s.data_ptr(), scale_fmt, n_rows)
     return (q, s, y) if return_y else (q, s)
 
@@ -1043,15 +1053,15 @@ def fp8bs_swiglu_bwd(dy: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, dga
     up_, ldu = _rows2(up, "up", _BF16, (M, N), dev)
     dgp, lddg = _rows2(dgate, "dgate", _BF16, (M, N), dev)
     dup_, lddu = _rows2(dup, "dup", _BF16, (M, N), dev)
-    _call_on(dev, "fp8bs_swiglu_bwd", _ptr(dy, "dy", _BF16, (M, N), dev), gp, ldg, up_, ldu, _count(n_rows, dev), dgp,
-             lddg, dup_, lddu, M, N, first="gate")
+    _launch("gate", dev, lib().fp8bs_swiglu_bwd, _ptr(dy, "dy", _BF16, (M, N), dev), gp, ldg, up_, ldu,
+            _count(n_rows, dev), dgp, lddg, dup_, lddu, M, N)
 
 
 def swiglu_bwd(dy, gate, up, n_rows=None):
     """fp8bs_swiglu_bwd: (dgate, dup) bf16 [M, N], the halves of one [M, 2N]
     tensor; not initialised from row n_rows on."""
     M, N = _shape2(gate, "gate must be [M, N]", "gate")
-    d = _empty(gate, (M, 2 * N), torch.bfloat16)
+    d = gate.new_empty(M, 2 * N, dtype=torch.bfloat16)
     dgate, dup = d[:, :N], d[:, N:]
     fp8bs_swiglu_bwd(dy, gate, up, dgate, dup, n_rows)
     return dgate, dup
@@ -1060,9 +1070,9 @@ def swiglu_bwd(dy, gate, up, n_rows=None):
 def _moe_combine_bwd(dy, out, R, N, w, T, topk, row_of, d_out, d_w) -> None:
     """fp8bs_moe_combine_bwd of outputs given by their addresses."""
     dev = out.device
-    _call_on(dev, "fp8bs_moe_combine_bwd", _ptr(dy, "dy", _FLOATS, (T, N), dev), _out_code(dy),
-             _ptr(out, "out", _BF16, (R, N), dev), _ptr(w, "w", _F32, (T, topk), dev),
-             _ptr(row_of, "row_of", _I32, (T, topk), dev), d_out, d_w, T, topk, R, N, first="out")
+    _launch("out", dev, lib().fp8bs_moe_combine_bwd, _ptr(dy, "dy", _FLOATS, (T, N), dev), _out_code(dy),
+            _ptr(out, "out", _BF16, (R, N), dev), _ptr(w, "w", _F32, (T, topk), dev),
+            _ptr(row_of, "row_of", _I32, (T, topk), dev), d_out, d_w, T, topk, R, N)
 
 
 def fp8bs_moe_combine_bwd(dy: torch.Tensor, out: torch.Tensor, w: torch.Tensor, row_of: torch.Tensor,
@@ -1081,6 +1091,6 @@ def moe_combine_bwd(dy, out, w, row_of):
     of d_out that no pair maps to are not initialised."""
     R, N = _shape2(out, "out must be [R, N]", "out")
     T, topk = _shape2(w, "w must be [T, topk]", "w")
-    d_out, d_w = _empty(out, (R, N), torch.bfloat16), _empty(out, (T, topk), torch.float32)
+    d_out, d_w = out.new_empty(R, N, dtype=torch.bfloat16), out.new_empty(T, topk, dtype=torch.float32)
     _moe_combine_bwd(dy, out, R, N, w, T, topk, row_of, d_out.data_ptr(), d_w.data_ptr())
     return d_out, d_w

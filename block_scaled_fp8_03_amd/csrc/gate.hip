@@ -149,14 +149,16 @@ __device__ __forceinline__ float sigmoid_of(float z, float x) {
   return (z < 0.0f ? x : 1.0f) * __builtin_amdgcn_rcpf(1.0f + x);
 }
 
-// score[v] in float32, and the sum of all of them (1 for a softmax, 0 where all are masked).
+// score[v] in float32, and the sum of all of them (1 for a softmax, 0 where all are masked);
+// of a sigmoid also x[v] = e^-|z[v]|.
 template <int V>
-__device__ __forceinline__ float scores(const float* z, bool softmax, float* score) {
+__device__ __forceinline__ float scores(const float* z, bool softmax, float* score, float* x) {
   float sum = 0.0f;
   if (!softmax) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      score[v] = sigmoid_of(z[v], exp_f32(-fabsf(z[v])));
+      x[v] = exp_f32(-fabsf(z[v]));
+      score[v] = sigmoid_of(z[v], x[v]);
       sum += score[v];
     }
     return wave_sum(sum);
@@ -171,7 +173,7 @@ __device__ __forceinline__ float scores(const float* z, bool softmax, float* sco
     sum += score[v];
   }
   sum = wave_sum(sum);
-  const float by = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+  const float by = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;   // of at least 1
 #pragma unroll
   for (int v = 0; v < V; ++v) score[v] *= by;
   return sum > 0.0f ? 1.0f : 0.0f;
@@ -184,7 +186,7 @@ __device__ __forceinline__ void shares(float* score, float sum, bool softmax) {
   // 1 / sum is infinite for the sum of the smallest scores: those are taken times 2^64 before it
   const bool tiny = sum < 1e-30f;
   const float up = tiny ? 18446744073709551616.0f : 1.0f;
-  const float by = sum > 0.0f ? __fdiv_rn(1.0f, sum * up) : 0.0f;
+  const float by = sum > 0.0f ? __builtin_amdgcn_rcpf(sum * up) : 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) score[v] = score[v] * up * by;
 }
@@ -452,9 +454,9 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void moe_balance_kernel(const M
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
     for (int t = a + wave; t < b; t += kBalanceWaves) {
       const int32_t id = lane < (int)p.topk ? p.indices[t * (int)p.topk + lane] : -1;
-      float z[V], score[V];
+      float z[V], score[V], x[V];
       load_logits<V, VEC>(p.logits, p.f32, t * p.ld, E, lane, z);
-      const float sum = scores<V>(z, p.softmax, score);
+      const float sum = scores<V>(z, p.softmax, score, x);
       shares<V>(score, sum, p.softmax);
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] += score[v];
@@ -582,7 +584,7 @@ __global__ __launch_bounds__(64 * kWaves) void moe_gate_bwd_kernel(const MoeGate
     uk = p.d_weights[t * K + lane];
     if (e < 0 || e >= E) e = -1, uk = 0.0f;
   }
-  float z[V], score[V], u[V];
+  float z[V], score[V], x[V], u[V];
   load_logits<V, VEC>(p.logits, p.f32, t * p.ld, E, lane, z);
   // the token's sequence, asked for before the scores are made
   int a = 0, b = 0;
@@ -594,12 +596,12 @@ __global__ __launch_bounds__(64 * kWaves) void moe_gate_bwd_kernel(const MoeGate
     load_words<V, false>((const uint32_t*)p.counts + (int64_t)s * E, lane * V, E, 0, hits);
     dl = p.d_loss[s];
   }
-  const float sum = scores<V>(z, p.softmax, score);
+  const float sum = scores<V>(z, p.softmax, score, x);
 #pragma unroll
   for (int v = 0; v < V; ++v) u[v] = 0.0f;
   if (p.d_loss && t >= a && t < b) {
     const float n = (float)(b - a);
-    const float c = __fdiv_rn(__fdiv_rn(dl * (float)E, (float)K * n), n);
+    const float c = dl * (float)E * __builtin_amdgcn_rcpf((float)K * n) * __builtin_amdgcn_rcpf(n);
     float share[V], mean = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) share[v] = score[v];
@@ -645,8 +647,7 @@ __global__ __launch_bounds__(64 * kWaves) void moe_gate_bwd_kernel(const MoeGate
     if (p.softmax) {
       dz[v] = __builtin_fmaf(-score[v], all, u[v]);
     } else {
-      const float x = exp_f32(-fabsf(z[v]));                  // 1 - score without the cancellation near 1
-      dz[v] = u[v] * sigmoid_of(-z[v], x);
+      dz[v] = u[v] * sigmoid_of(-z[v], x[v]);                 // 1 - score without the cancellation near 1
     }
   }
   const int64_t at = (int64_t)t * E + lane * V;
