@@ -652,7 +652,7 @@ int fp8bs_moe_gate(const void* logits, int64_t ld, int logits_dtype, const float
   const Span ins[] = {{logits, extent(T, 1, ld, 0, E) * size_of(logits_dtype)}, {bias, 4 * E}};
   if (clash(outs, ins)) return FP8BS_ERR_ALIAS;
   const fp8bs::MoeGate a{logits, bias, indices, weights, ld, T, E, topk, groups, topk_groups, route_scale,
-                         logits_dtype == FP8BS_OUT_F32, score == FP8BS_SCORE_SOFTMAX, normalize != 0};
+                         logits_dtype == FP8BS_OUT_F32, score == FP8BS_SCORE_SOFTMAX, normalize != 0, false};
   return status_of(fp8bs::launch_moe_gate(a, (hipStream_t)stream));
 }
 

@@ -165,11 +165,15 @@ __device__ __forceinline__ v8bf dequant8_bf16(uint32_t w0, uint32_t w1, float sc
 }
 
 // Sum over a wave, all 64 lanes active, in VALU steps of a fixed order; the result is uniform.
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), CTRL, 0xF, 0xF, true));
+}
 __device__ __forceinline__ float row16_sum(float v) {
-  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0xB1, 0xF, 0xF, false));   // quad_perm 1,0,3,2
-  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0x4E, 0xF, 0xF, false));   // quad_perm 2,3,0,1
-  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0x124, 0xF, 0xF, false));  // row_ror 4
-  v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), 0x128, 0xF, 0xF, false));  // row_ror 8
+  v += dpp_f32<0xB1>(v);    // quad_perm 1,0,3,2
+  v += dpp_f32<0x4E>(v);    // quad_perm 2,3,0,1
+  v += dpp_f32<0x124>(v);   // row_ror 4
+  v += dpp_f32<0x128>(v);   // row_ror 8
   return v;
 }
 __device__ __forceinline__ float wave_sum(float v) {

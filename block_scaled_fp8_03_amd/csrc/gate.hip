@@ -6,8 +6,9 @@
 // and the lowest register of a maximum are the lowest expert.  A token's logits are
 // a few hundred bytes: what these kernels take is a wave's chain of instructions
 // (few tokens) or the instructions of all waves (many), not HBM.  256 experts in 8
-// groups, top 8, from a graph: 32 tokens 4.5 us, 2.2 of it the launch, 4096 tokens 7.1
-// (580 vector instructions a token); counts, loss and both gradients of 4096 tokens 17.7.
+// groups, top 8, from a graph: 32 tokens 4.4 us, 2.2 of it the launch, 4096 tokens 6.8,
+// 30000 tokens 31 (564 vector instructions a token, 8 x 33 of them the choice, 108 the
+// scores); counts, loss and both gradients of 4096 tokens 17.2.
 #include <algorithm>
 
 #include "device_common.h"
@@ -86,16 +87,13 @@ __device__ __forceinline__ void load_logits(const void* logits, bool f32, int64_
   for (int v = 0; v < V; ++v) z[v] = z[v] > minus_inf() ? z[v] : minus_inf();
 }
 
-// e^x for x <= 0 in 64 bits, within 2^-45 of it: x = n ln 2 + r, |r| <= ln 2 / 2, the
-// exponential series of r to r^11 (the next term is below 2^-47 of it).
-__device__ __forceinline__ double exp_f64(double x) {
-  x = fmax(x, -745.0);                                        // below float32's and float64's smallest numbers
-  const double n = __builtin_rint(x * 1.4426950408889634);
-  double r = __builtin_fma(n, -0.6931471805599453, x);
-  r = __builtin_fma(n, -2.3190468138462996e-17, r);
-  double p = 1.0 / 39916800;
-  p = __builtin_fma(p, r, 1.0 / 3628800);
-  p = __builtin_fma(p, r, 1.0 / 362880);
+// e^x for -150 <= x <= 0 in 64 bits, within 2^-36 of it: x = n ln 2 + r, |r| <= ln 2 / 2,
+// the exponential series of r to r^9 (what is left out is below 2^-37).  n comes from x
+// in 32 bits; 216 ln 2 is off by 2^-46 with ln 2 in 64.
+__device__ __forceinline__ double exp_f64(double x, float x32) {
+  const float n = __builtin_rintf(x32 * 1.44269504f);
+  const double r = __builtin_fma((double)n, -0.6931471805599453, x);
+  double p = 1.0 / 362880;
   p = __builtin_fma(p, r, 1.0 / 40320);
   p = __builtin_fma(p, r, 1.0 / 5040);
   p = __builtin_fma(p, r, 1.0 / 720);
@@ -107,23 +105,24 @@ __device__ __forceinline__ double exp_f64(double x) {
   p = __builtin_fma(p, r, 1.0);
   return __builtin_amdgcn_ldexp(p, (int)n);
 }
-// 1 / d of a normal d: the hardware's estimate and two steps of Newton's iteration
+// 1 / d of a normal d: the hardware's estimate (2^-24 at the least) and a step of Newton's iteration
 __device__ __forceinline__ double rcp_f64(double d) {
-  double y = __builtin_amdgcn_rcp(d);
-  y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+  const double y = __builtin_amdgcn_rcp(d);
   return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
 }
 
 // score[v] in 64 bits, rounded once; 0 for masked experts (all of a token masked: all 0).
 // Two scores that float32 arithmetic would exchange, or make equal, change which expert
 // a token takes or their order: with a float32 exponential one token in about 40,000
-// (256 experts in 8 groups, top 8).  Here the sum of errors is 2^-20 of a rounding.
+// (256 experts in 8 groups, top 8).  Here the sum of errors is 2^-11 of a rounding, and
+// of such tokens one in 2000 remains.
 template <int V>
 __device__ __forceinline__ void exact_scores(const float* z, bool softmax, float* score) {
   if (!softmax) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const double x = exp_f64(-fabs((double)z[v]));
+      const float z32 = fmaxf(-fabsf(z[v]), -150.0f);         // below it a float32 score is 0 or 1
+      const double x = exp_f64((double)z32, z32);
       score[v] = (float)((z[v] < 0.0f ? x : 1.0) * rcp_f64(1.0 + x));
     }
     return;
@@ -135,7 +134,9 @@ __device__ __forceinline__ void exact_scores(const float* z, bool softmax, float
   double e[V], sum = 0.0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    e[v] = z[v] == minus_inf() ? 0.0 : z[v] == top ? 1.0 : exp_f64((double)z[v] - (double)top);
+    const float z32 = z[v] - top;
+    e[v] = z[v] == top ? 1.0 : z32 > -150.0f ? exp_f64((double)z[v] - (double)top, z32) : 0.0;
+    e[v] = z[v] == minus_inf() ? 0.0 : e[v];
     sum += e[v];
   }
   sum = wave_sum(sum);
@@ -218,8 +219,8 @@ __device__ __forceinline__ void join_two(uint32_t& a, uint32_t& b, uint32_t c, u
 }
 template <int CTRL>
 __device__ __forceinline__ void join_dpp(uint32_t& a, uint32_t& b) {
-  join_two(a, b, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, CTRL, 0xF, 0xF, false),
-           (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, CTRL, 0xF, 0xF, false));
+  join_two(a, b, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, CTRL, 0xF, 0xF, true),
+           (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, CTRL, 0xF, 0xF, true));
 }
 
 }  // namespace
@@ -239,7 +240,8 @@ __global__ __launch_bounds__(64 * kWaves) void moe_gate_kernel(const MoeGate p) 
   uint32_t key[V];
   if (p.bias) {
     uint32_t b[V];
-    load_words<V, false>((const uint32_t*)p.bias, lane * V, E, 0, b);
+    if (VEC && p.bias_wide) load_words<V, true>((const uint32_t*)p.bias, lane * V, E, 0, b);
+    else load_words<V, false>((const uint32_t*)p.bias, lane * V, E, 0, b);
     float score[V];
     exact_scores<V>(z, p.softmax, score);
 #pragma unroll
@@ -370,7 +372,9 @@ bool wide_rows(const void* p, int64_t ld, int64_t E, int V, bool f32) {
 
 }  // namespace
 
-hipError_t launch_moe_gate(const MoeGate& p, hipStream_t stream) {
+hipError_t launch_moe_gate(const MoeGate& q, hipStream_t stream) {
+  MoeGate p = q;
+  p.bias_wide = (uintptr_t)p.bias % 16 == 0;
   const dim3 grid((unsigned)((p.T + kWaves - 1) / kWaves)), block(64 * kWaves);
 #define CALL(V, VEC) moe_gate_kernel<V, VEC><<<grid, block, 0, stream>>>(p)
   FP8BS_BY_EXPERTS(p, CALL)

@@ -145,6 +145,7 @@ struct MoeGate {
   int64_t ld, T, E, topk, groups, keep;
   float route_scale;
   bool f32, softmax, normalize;
+  bool bias_wide;          // the bias is aligned to 16 bytes
 };
 hipError_t launch_moe_gate(const MoeGate& p, hipStream_t stream);
 struct MoeBalance {
