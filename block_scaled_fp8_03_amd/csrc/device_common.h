@@ -164,7 +164,7 @@ __device__ __forceinline__ v8bf dequant8_bf16(uint32_t w0, uint32_t w1, float sc
   return __builtin_bit_cast(v8bf, u);
 }
 
-// Sum over a wave, all 64 lanes active, in VALU steps of a fixed order; the result is uniform.
+// Sum over the 16 lanes of a DPP row, in VALU steps of a fixed order; every lane receives it.
 template <int CTRL>
 __device__ __forceinline__ float dpp_f32(float v) {
   return bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), CTRL, 0xF, 0xF, true));
@@ -176,6 +176,7 @@ __device__ __forceinline__ float row16_sum(float v) {
   v += dpp_f32<0x128>(v);   // row_ror 8
   return v;
 }
+// Sum over a wave, all 64 lanes active, the same way; uniform.
 __device__ __forceinline__ float wave_sum(float v) {
   v = row16_sum(v);
   v += bits_f32((uint32_t)dpp_or_0<0x142, 0xA>((int)f32_bits(v)));   // row 0 to row 1, row 2 to row 3
@@ -190,10 +191,10 @@ __device__ __forceinline__ uint32_t wave_max_uniform(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// e^x within 2 units in the last place (0 and infinity beyond float32's range): the
-// hardware's power of two of x log2(e) less its whole part, both of whose roundings
-// are made up for by the second half of log2(e).  6 instructions where the library's
-// function takes 14.
+// e^x within 2 units in the last place (0 and infinity beyond float32's range): 2^n times
+// the hardware's power of two of x log2(e) - n, n the nearest whole number, which two
+// fused products with the halves of log2(e) give to 2^-25.  7 instructions where the
+// library's function takes 14.
 __device__ __forceinline__ float exp_f32(float x) {
   constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;
   x = __builtin_amdgcn_fmed3f(x, -150.0f, 150.0f);
