@@ -795,14 +795,26 @@ def _score(score) -> int:
 
 def _shape2(t, message: str, name: str):
     """The two sizes of a 2-D tensor."""
-    try:
-        a, b = t.shape
-        t.device
-    except (AttributeError, TypeError, ValueError):
-        raise _misfit(message, **{name: t}) from None
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise _misfit(message, **{name: t})
-    return a, b
+    return t.shape
+
+
+def _main2(t: torch.Tensor, name: str, dtypes, sizes: str):
+    """The tensor that the others go by, a [M, width] view with a dense last
+    dimension: (M, width, device, pointer, row stride)."""
+    try:
+        M, width = t.shape
+        sm, sw = t.stride()
+        dev = t.device
+        fits = t.dtype in dtypes
+    except (AttributeError, TypeError, ValueError):
+        raise _misfit(f"{name} must be [{sizes}]", **{name: t}) from None
+    if not fits:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if sw != 1 and M > 0 and width > 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return M, width, dev, t.data_ptr(), (sm if M > 1 else 0)
 
 
 def _launch(first: str, dev, fn, *args) -> None:
@@ -819,10 +831,8 @@ def _launch(first: str, dev, fn, *args) -> None:
         raise Fp8bsError(fn.__name__, st)
 
 
-def _rmsnorm(x, M, K, res, norm_w, eps, res_out, y, q, s, scale_fmt) -> None:
-    """fp8bs_rmsnorm of outputs given by their addresses."""
-    dev = x.device
-    xp, ld = _rows2(x, "x", _BF16, (M, K), dev)
+def _rmsnorm(dev, xp, ld, M, K, res, norm_w, eps, res_out, y, q, s, scale_fmt) -> None:
+    """fp8bs_rmsnorm of x and outputs given by their addresses."""
     res_f32 = res is not None and getattr(res, "dtype", None) == torch.float32
     _launch("x", dev, lib().fp8bs_rmsnorm, xp, ld, _opt(res, "res", _FLOATS, (M, K), dev), res_out,
             OUT_F32 if res_f32 else OUT_BF16, _ptr(norm_w, "norm_w", _FLOATS, (K,), dev),
@@ -836,37 +846,34 @@ def fp8bs_rmsnorm(x: torch.Tensor, res: Optional[torch.Tensor], res_out: Optiona
     float32 or None, the sum into res_out (res itself if you like), the norm
     times norm_w [K] (bf16 or float32) into y bf16 [M, K] and / or as codes q
     e4m3 [M, K] with scales s float32 [M, K/128]."""
-    M, K = _shape2(x, "x must be [M, K]", "x")
-    dev = x.device
+    M, K, dev, xp, ld = _main2(x, "x", _BF16, "M, K")
     like = (getattr(res, "dtype", None),) if getattr(res, "dtype", None) in _FLOATS else _FLOATS
-    _rmsnorm(x, M, K, res, norm_w, eps, _opt(res_out, "res_out", like, (M, K), dev), _opt(y, "y", _BF16, (M, K), dev),
-             _opt(q, "q", _F8, (M, K), dev), _opt(s, "s", _F32, (M, K // BLOCK), dev), scale_fmt)
+    _rmsnorm(dev, xp, ld, M, K, res, norm_w, eps, _opt(res_out, "res_out", like, (M, K), dev),
+             _opt(y, "y", _BF16, (M, K), dev), _opt(q, "q", _F8, (M, K), dev), _opt(s, "s", _F32, (M, K // BLOCK), dev), scale_fmt)
 
 
 def rmsnorm(x, norm_w, eps: float, residual=None):
     """fp8bs_rmsnorm: y bf16 [M, K]; with a residual (y, x + residual)."""
-    M, K = _shape2(x, "x must be [M, K]", "x")
+    M, K, dev, xp, ld = _main2(x, "x", _BF16, "M, K")
     y = x.new_empty(M, K, dtype=torch.bfloat16)
     h = None if residual is None else x.new_empty(M, K, dtype=getattr(residual, "dtype", None))
-    _rmsnorm(x, M, K, residual, norm_w, eps, _at(h), y.data_ptr(), None, None, SCALE_FP32)
+    _rmsnorm(dev, xp, ld, M, K, residual, norm_w, eps, _at(h), y.data_ptr(), None, None, SCALE_FP32)
     return y if residual is None else (y, h)
 
 
 def rmsnorm_quant(x, norm_w, eps: float, residual=None, scale_fmt="fp32", return_y: bool = False):
     """fp8bs_rmsnorm: (q e4m3 [M, K], s float32 [M, K/128]), then y bf16 if
     return_y, then x + residual if there is a residual."""
-    M, K = _shape2(x, "x must be [M, K]", "x")
+    M, K, dev, xp, ld = _main2(x, "x", _BF16, "M, K")
     q, s = x.new_empty(M, K, dtype=torch.float8_e4m3fn), x.new_empty(M, K // BLOCK, dtype=torch.float32)
     y = x.new_empty(M, K, dtype=torch.bfloat16) if return_y else None
     h = None if residual is None else x.new_empty(M, K, dtype=getattr(residual, "dtype", None))
-    _rmsnorm(x, M, K, residual, norm_w, eps, _at(h), _at(y), q.data_ptr(), s.data_ptr(), scale_fmt)
+    _rmsnorm(dev, xp, ld, M, K, residual, norm_w, eps, _at(h), _at(y), q.data_ptr(), s.data_ptr(), scale_fmt)
     return tuple(t for t in (q, s, y, h) if t is not None)
 
 
-def _rmsnorm_bwd(dy, h, M, K, norm_w, eps, dres, dx, dw, ws, nbytes) -> None:
-    """fp8bs_rmsnorm_bwd of outputs given by their addresses."""
-    dev = h.device
-    hp, ld = _rows2(h, "h", _FLOATS, (M, K), dev)
+def _rmsnorm_bwd(dev, hp, ld, M, K, dy, h, norm_w, eps, dres, dx, dw, ws, nbytes) -> None:
+    """fp8bs_rmsnorm_bwd of h and outputs given by their addresses."""
     _launch("h", dev, lib().fp8bs_rmsnorm_bwd, _ptr(dy, "dy", _BF16, (M, K), dev), hp, ld, _out_code(h),
             _ptr(norm_w, "norm_w", _FLOATS, (K,), dev), norm_w.dtype == torch.float32, eps,
             _opt(dres, "dres", (h.dtype,), (M, K), dev), dx, dw, M, K, ws, nbytes)
@@ -878,28 +885,26 @@ def fp8bs_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, norm_w: torch.Tensor, e
     """The norm's gradient: dy bf16 [M, K], h [M, K] what was normalised (bf16 or
     float32, row stride free), dres [M, K] of h's type or None, added to dx [M, K]
     of h's type (dx itself if you like); dw float32 [K] or None."""
-    M, K = _shape2(h, "h must be [M, K]", "h")
-    dev = h.device
-    _rmsnorm_bwd(dy, h, M, K, norm_w, eps, dres, _ptr(dx, "dx", (h.dtype,), (M, K), dev),
+    M, K, dev, hp, ld = _main2(h, "h", _FLOATS, "M, K")
+    _rmsnorm_bwd(dev, hp, ld, M, K, dy, h, norm_w, eps, dres, _ptr(dx, "dx", (h.dtype,), (M, K), dev),
                  _opt(dw, "dw", _F32, (K,), dev), *_scratch(workspace, dev))
 
 
 def rmsnorm_bwd(dy, h, norm_w, eps: float, dres=None):
     """fp8bs_rmsnorm_bwd: (dx [M, K] of h's type, dw float32 [K])."""
-    M, K = _shape2(h, "h must be [M, K]", "h")
+    M, K, dev, hp, ld = _main2(h, "h", _FLOATS, "M, K")
     need = lib().fp8bs_rmsnorm_bwd_workspace_size(M, K)
     if need < 0:
         raise ValueError("sizes out of range")
     dx, dw = h.new_empty(M, K, dtype=h.dtype), h.new_empty(K, dtype=torch.float32)
     ws = h.new_empty(need, dtype=torch.uint8) if need else None
-    _rmsnorm_bwd(dy, h, M, K, norm_w, eps, dres, dx.data_ptr(), dw.data_ptr(), _at(ws), need)
+    _rmsnorm_bwd(dev, hp, ld, M, K, dy, h, norm_w, eps, dres, dx.data_ptr(), dw.data_ptr(), _at(ws), need)
     return dx, dw
 
 
-def _moe_gate(logits, T, E, topk, bias, groups, topk_groups, score, normalize, route_scale, indices, weights) -> None:
-    """fp8bs_moe_gate of outputs given by their addresses."""
-    dev = logits.device
-    zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
+def _moe_gate(dev, zp, ld, T, E, logits, topk, bias, groups, topk_groups, score, normalize, route_scale, indices,
+              weights) -> None:
+    """fp8bs_moe_gate of logits and outputs given by their addresses."""
     _launch("logits", dev, lib().fp8bs_moe_gate, zp, ld, _out_code(logits), _opt(bias, "bias", _F32, (E,), dev), T, E,
             topk, groups, topk_groups, _score(score), normalize, route_scale, indices, weights)
 
@@ -908,10 +913,9 @@ def fp8bs_moe_gate(logits: torch.Tensor, bias: Optional[torch.Tensor], groups: i
                    normalize: bool, route_scale: float, indices: torch.Tensor, weights: torch.Tensor) -> None:
     """The gate: logits [T, E] (bf16 or float32, row stride free) -> indices
     int32 [T, topk] (-1 where no expert is left) and weights float32 [T, topk]."""
-    T, E = _shape2(logits, "logits must be [T, E]", "logits")
+    T, E, dev, zp, ld = _main2(logits, "logits", _FLOATS, "T, E")
     topk = _shape2(indices, "indices must be [T, topk]", "indices")[1]
-    dev = logits.device
-    _moe_gate(logits, T, E, topk, bias, groups, topk_groups, score, normalize, route_scale,
+    _moe_gate(dev, zp, ld, T, E, logits, topk, bias, groups, topk_groups, score, normalize, route_scale,
               _ptr(indices, "indices", _I32, (T, topk), dev), _ptr(weights, "weights", _F32, (T, topk), dev))
 
 
@@ -919,10 +923,10 @@ def moe_gate(logits, topk: int, bias=None, groups: int = 1, topk_groups: Optiona
              normalize: bool = True, route_scale: float = 1.0):
     """fp8bs_moe_gate: (indices int32 [T, topk], weights float32 [T, topk]), for
     moe_route and moe_combine.  All groups are kept unless topk_groups says so."""
-    T, E = _shape2(logits, "logits must be [T, E]", "logits")
+    T, E, dev, zp, ld = _main2(logits, "logits", _FLOATS, "T, E")
     indices, weights = logits.new_empty(T, topk, dtype=torch.int32), logits.new_empty(T, topk, dtype=torch.float32)
-    _moe_gate(logits, T, E, topk, bias, groups, groups if topk_groups is None else topk_groups, score, normalize,
-              route_scale, indices.data_ptr(), weights.data_ptr())
+    _moe_gate(dev, zp, ld, T, E, logits, topk, bias, groups, groups if topk_groups is None else topk_groups, score,
+              normalize, route_scale, indices.data_ptr(), weights.data_ptr())
     return indices, weights
 
 
@@ -935,11 +939,9 @@ def _sequences(cu_seq: Optional[torch.Tensor], dev):
     return _ptr(cu_seq, "cu_seq", _I32, cu_seq.shape, dev), cu_seq.shape[0] - 1
 
 
-def _moe_balance(logits, T, E, indices, cu, S, score, counts, probs, loss, ws, nbytes) -> None:
-    """fp8bs_moe_balance of boundaries and outputs given by their addresses."""
+def _moe_balance(dev, zp, ld, T, E, logits, indices, cu, S, score, counts, probs, loss, ws, nbytes) -> None:
+    """fp8bs_moe_balance of logits, boundaries and outputs given by their addresses."""
     topk = _shape2(indices, "indices must be [T, topk]", "indices")[1]
-    dev = logits.device
-    zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
     _launch("logits", dev, lib().fp8bs_moe_balance, zp, ld, _out_code(logits),
             _ptr(indices, "indices", _I32, (T, topk), dev), cu, T, S, E, topk, _score(score), counts, probs, loss, ws, nbytes)
 
@@ -950,33 +952,31 @@ def fp8bs_moe_balance(logits: torch.Tensor, indices: torch.Tensor, cu_seq: Optio
     """Of each sequence (cu_seq int32 [S + 1]; None: one of all tokens): counts
     int32 [S, E] of the gate's indices [T, topk], probs float32 [S, E] the mean
     share of the token's scores, loss float32 [S]."""
-    T, E = _shape2(logits, "logits must be [T, E]", "logits")
-    dev = logits.device
+    T, E, dev, zp, ld = _main2(logits, "logits", _FLOATS, "T, E")
     cu, S = _sequences(cu_seq, dev)
-    _moe_balance(logits, T, E, indices, cu, S, score, _ptr(counts, "counts", _I32, (S, E), dev),
+    _moe_balance(dev, zp, ld, T, E, logits, indices, cu, S, score, _ptr(counts, "counts", _I32, (S, E), dev),
                  _ptr(probs, "probs", _F32, (S, E), dev), _ptr(loss, "loss", _F32, (S,), dev), *_scratch(workspace, dev))
 
 
 def moe_balance(logits, indices, cu_seq=None, score="sigmoid"):
     """fp8bs_moe_balance: (loss float32 [S], counts int32 [S, E], probs float32 [S, E])."""
-    T, E = _shape2(logits, "logits must be [T, E]", "logits")
-    cu, S = _sequences(cu_seq, logits.device)
+    T, E, dev, zp, ld = _main2(logits, "logits", _FLOATS, "T, E")
+    cu, S = _sequences(cu_seq, dev)
     need = lib().fp8bs_moe_balance_workspace_size(T, S, E)
     if need < 0:
         raise ValueError("sizes out of range")
     counts, probs = logits.new_empty(S, E, dtype=torch.int32), logits.new_empty(S, E, dtype=torch.float32)
     loss = logits.new_empty(S, dtype=torch.float32)
     ws = logits.new_empty(need, dtype=torch.uint8) if need else None
-    _moe_balance(logits, T, E, indices, cu, S, score, counts.data_ptr(), probs.data_ptr(), loss.data_ptr(), _at(ws), need)
+    _moe_balance(dev, zp, ld, T, E, logits, indices, cu, S, score, counts.data_ptr(), probs.data_ptr(),
+                 loss.data_ptr(), _at(ws), need)
     return loss, counts, probs
 
 
-def _moe_gate_bwd(logits, T, E, indices, d_weights, score, normalize, route_scale, cu_seq, counts, d_loss, d_logits,
-                  out_code) -> None:
-    """fp8bs_moe_gate_bwd of an output given by its address."""
+def _moe_gate_bwd(dev, zp, ld, T, E, logits, indices, d_weights, score, normalize, route_scale, cu_seq, counts, d_loss,
+                  d_logits, out_code) -> None:
+    """fp8bs_moe_gate_bwd of logits and an output given by their addresses."""
     topk = _shape2(indices, "indices must be [T, topk]", "indices")[1]
-    dev = logits.device
-    zp, ld = _rows2(logits, "logits", _FLOATS, (T, E), dev)
     cu, S = _sequences(cu_seq, dev)
     _launch("logits", dev, lib().fp8bs_moe_gate_bwd, zp, ld, _out_code(logits),
             _ptr(indices, "indices", _I32, (T, topk), dev), _opt(d_weights, "d_weights", _F32, (T, topk), dev),
@@ -990,25 +990,23 @@ def fp8bs_moe_gate_bwd(logits: torch.Tensor, indices: torch.Tensor, d_weights: O
     """The gradient by the logits of the gate's weights (d_weights float32 [T,
     topk] or None) and of the balance losses (d_loss float32 [S] with their
     counts, or None): d_logits [T, E] bf16 or float32."""
-    T, E = _shape2(logits, "logits must be [T, E]", "logits")
-    _moe_gate_bwd(logits, T, E, indices, d_weights, score, normalize, route_scale, cu_seq, counts, d_loss,
-                  _ptr(d_logits, "d_logits", _FLOATS, (T, E), logits.device), _out_code(d_logits))
+    T, E, dev, zp, ld = _main2(logits, "logits", _FLOATS, "T, E")
+    _moe_gate_bwd(dev, zp, ld, T, E, logits, indices, d_weights, score, normalize, route_scale, cu_seq, counts, d_loss,
+                  _ptr(d_logits, "d_logits", _FLOATS, (T, E), dev), _out_code(d_logits))
 
 
 def moe_gate_bwd(logits, indices, d_weights=None, score="sigmoid", normalize: bool = True, route_scale: float = 1.0,
                  cu_seq=None, counts=None, d_loss=None, out_dtype=torch.float32) -> torch.Tensor:
     """fp8bs_moe_gate_bwd: d_logits [T, E]."""
-    T, E = _shape2(logits, "logits must be [T, E]", "logits")
+    T, E, dev, zp, ld = _main2(logits, "logits", _FLOATS, "T, E")
     d_logits = logits.new_empty(T, E, dtype=out_dtype)
-    _moe_gate_bwd(logits, T, E, indices, d_weights, score, normalize, route_scale, cu_seq, counts, d_loss,
+    _moe_gate_bwd(dev, zp, ld, T, E, logits, indices, d_weights, score, normalize, route_scale, cu_seq, counts, d_loss,
                   d_logits.data_ptr(), _out_code(d_logits))
     return d_logits
 
 
-def _swiglu(gate, up, M, N, y, q, s, scale_fmt, n_rows) -> None:
-    """fp8bs_swiglu of outputs given by their addresses."""
-    dev = gate.device
-    gp, ldg = _rows2(gate, "gate", _BF16, (M, N), dev)
+def _swiglu(dev, gp, ldg, M, N, up, y, q, s, scale_fmt, n_rows) -> None:
+    """fp8bs_swiglu of the gate and outputs given by their addresses."""
     up_, ldu = _rows2(up, "up", _BF16, (M, N), dev)
     _launch("gate", dev, lib().fp8bs_swiglu, gp, ldg, up_, ldu, _count(n_rows, dev), y, q, s, _fmt(scale_fmt), M, N)
 
@@ -1019,27 +1017,26 @@ def fp8bs_swiglu(gate: torch.Tensor, up: torch.Tensor, y: Optional[torch.Tensor]
     product's output), into y bf16 [M, N] and / or as codes q e4m3 [M, N] with
     scales s float32 [M, N/128].  Rows from n_rows (one int32 on the device, e.g.
     offsets[-1:] of moe_route) on are left alone."""
-    M, N = _shape2(gate, "gate must be [M, N]", "gate")
-    dev = gate.device
-    _swiglu(gate, up, M, N, _opt(y, "y", _BF16, (M, N), dev), _opt(q, "q", _F8, (M, N), dev),
+    M, N, dev, gp, ldg = _main2(gate, "gate", _BF16, "M, N")
+    _swiglu(dev, gp, ldg, M, N, up, _opt(y, "y", _BF16, (M, N), dev), _opt(q, "q", _F8, (M, N), dev),
             _opt(s, "s", _F32, (M, N // BLOCK), dev), scale_fmt, n_rows)
 
 
 def swiglu(gate, up, n_rows=None) -> torch.Tensor:
     """fp8bs_swiglu: bf16 [M, N], not initialised from row n_rows on."""
-    M, N = _shape2(gate, "gate must be [M, N]", "gate")
+    M, N, dev, gp, ldg = _main2(gate, "gate", _BF16, "M, N")
     y = gate.new_empty(M, N, dtype=torch.bfloat16)
-    _swiglu(gate, up, M, N, y.data_ptr(), None, None, SCALE_FP32, n_rows)
+    _swiglu(dev, gp, ldg, M, N, up, y.data_ptr(), None, None, SCALE_FP32, n_rows)
     return y
 
 
 def swiglu_quant(gate, up, scale_fmt="fp32", n_rows=None, return_y: bool = False):
     """fp8bs_swiglu: (q e4m3 [M, N], s float32 [M, N/128]), then y bf16 if
     return_y; not initialised from row n_rows on."""
-    M, N = _shape2(gate, "gate must be [M, N]", "gate")
+    M, N, dev, gp, ldg = _main2(gate, "gate", _BF16, "M, N")
     q, s = gate.new_empty(M, N, dtype=torch.float8_e4m3fn), gate.new_empty(M, N // BLOCK, dtype=torch.float32)
     y = gate.new_empty(M, N, dtype=torch.bfloat16) if return_y else None
-    _swiglu(gate, up, M, N, _at(y), q.data_ptr(), s.data_ptr(), scale_fmt, n_rows)
+    _swiglu(dev, gp, ldg, M, N, up, _at(y), q.data_ptr(), s.data_ptr(), scale_fmt, n_rows)
     return (q, s, y) if return_y else (q, s)
 
 
@@ -1047,9 +1044,7 @@ def fp8bs_swiglu_bwd(dy: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, dga
                      n_rows: Optional[torch.Tensor] = None) -> None:
     """The gradient of fp8bs_swiglu: dy bf16 [M, N] -> dgate, dup bf16 [M, N] (row
     strides free, e.g. the halves of one tensor); rows from n_rows on are left alone."""
-    M, N = _shape2(gate, "gate must be [M, N]", "gate")
-    dev = gate.device
-    gp, ldg = _rows2(gate, "gate", _BF16, (M, N), dev)
+    M, N, dev, gp, ldg = _main2(gate, "gate", _BF16, "M, N")
     up_, ldu = _rows2(up, "up", _BF16, (M, N), dev)
     dgp, lddg = _rows2(dgate, "dgate", _BF16, (M, N), dev)
     dup_, lddu = _rows2(dup, "dup", _BF16, (M, N), dev)
