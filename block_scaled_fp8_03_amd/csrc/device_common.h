@@ -223,7 +223,9 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 // powers of two, else within 2 units in the last place): c itself has come out of
 // float32 arithmetic and is no nearer to its value, and the correctly rounded quotient
 // that act_quant makes of exact inputs takes three instructions more a value.  It is
-// at most 448 (1 + 2^-21), which the converter rounds to 448.
+// at most 448 (1 + 2^-21), which the converter rounds to 448.  Of a block with an infinity
+// the scale is infinite and 1 / s is 0: codes of 0, and NaN of the infinity itself.  A NaN
+// has the code of a NaN, and the maximum passes over it.
 __device__ __forceinline__ uint2 quant8(const float* c, bool ue8m0, float* scale) {
   float top = 0.0f;
 #pragma unroll
@@ -232,7 +234,7 @@ __device__ __forceinline__ uint2 quant8(const float* c, bool ue8m0, float* scale
   float s, r;
   if (ue8m0) {
     s = block_scale<true>(top);
-    r = bits_f32(0x7F000000u - f32_bits(s));                 // 2^-e of 2^e
+    r = bits_f32((uint32_t)max(0x7F000000 - (int)f32_bits(s), 0));   // 2^-e of 2^e, 0 of infinity
   } else {
     s = block_scale<false>(top);
     r = __builtin_amdgcn_rcpf(s);

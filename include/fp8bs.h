@@ -555,8 +555,12 @@ int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fm
  *   within two roundings (a product with 1 / s)
  * All in float32 from the inputs on, each output rounded once: the norm is
  * that of the unrounded sum, the codes are those of the unrounded norm.  A row
- * whose squares sum to infinity in float32 gives zeros, as does one of zeros;
- * with eps = 0 the latter is NaN.
+ * whose squares sum to infinity in float32 gives zeros (NaN where it is infinite
+ * itself), as does one of zeros; with eps = 0 the latter is NaN.
+ * Codes where c is not finite, for swiglu's too: a block with an infinity has an
+ * infinite scale, the codes of its finite values are 0 and those of its infinities
+ * NaN; a NaN has the code of a NaN, and the scale is that of the block's other
+ * values.
  *
  *   x        in   bf16, element (m, k) at [m*ld_x + k]; ld_x >= 0, a multiple of 8
  *   res      in   [M, K] bf16 or float32 (res_dtype, FP8BS_OUT_*), or NULL

@@ -51,6 +51,23 @@ def check_codes(q, s, c, rel, ue8m0, what):
     inside(q * each, c, c.abs() * (H_E4M3 + 2 * rel) * (1 + rel) + E4M3_LOW * each + 448 * each * 2 * rel, what + ": codes")
 
 
+def check_special_codes(q, s, c, rel, ue8m0, what):
+    """As check_codes, with infinities and NaN in c: the scale is that of a block's numbers, infinite if one of them is; the
+    code of a NaN, and of infinity over infinity, is NaN; a finite value over infinity gives 0."""
+    M, K = c.shape
+    b = c.double().cpu().view(M, -1, 128)
+    top = torch.where(b.isnan(), 0.0, b).abs().amax(-1)
+    codes, s = q.cpu().float().view(M, -1, 128), s.cpu()
+    assert torch.equal(s.isinf(), top.isinf()) and (s > 0).all(), what + ": scales of infinite blocks"
+    inf = top.isinf()[..., None].expand_as(b)
+    nan = b.isnan() | (b.isinf() & inf)
+    assert torch.equal(codes.isnan(), nan), what + ": NaN codes"
+    assert (codes[inf & ~nan] == 0).all(), what + ": finite values of infinite blocks"
+    keep = ~(inf | nan)
+    put = lambda t, v: torch.where(keep, t, v).view(M, K)  # noqa: E731
+    check_codes(put(codes, 0.0), torch.where(top.isinf(), 2.0 ** -22 if ue8m0 else 1e-4 / 448, s), put(b, 0.0), rel, ue8m0, what)
+
+
 # ------------------------------------------------------------------------ norm
 
 def norm_rel(K):

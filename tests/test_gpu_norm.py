@@ -73,6 +73,23 @@ def test_norm_rows_of_their_own():
     assert (fp8bs.rmsnorm(torch.full((1, K), 1e30, dtype=BF16, device=DEV), w.to(DEV), EPS) == 0).all()
 
 
+@pytest.mark.parametrize("K", [512, 1536])
+@pytest.mark.parametrize("fmt", ["fp32", "ue8m0"])
+def test_infinities_and_nan_stay_in_their_rows(K, fmt):
+    """A weight beyond what float32 holds of its column, one that is NaN; a row with an infinity, one with a NaN."""
+    M, inf, nan = 12, float("inf"), float("nan")
+    x, w = eu.normal((M, K), 1, 2.0), eu.normal((K,), 2, 1.0)
+    x[4, 7], x[6, 300], x[9, 5] = inf, nan, -inf
+    w[130], w[200], w[400] = 3e38, nan, inf
+    _, c = eu.norm(x, None, w, EPS)
+    # the row's squares are infinite: zeros, and NaN where an infinity is divided by their root
+    c = torch.where(x.isinf().any(1, keepdim=True), x.double() * 0 * w.double(), c).float()
+    q, s, y = fp8bs.rmsnorm_quant(x.to(DEV), w.to(DEV), EPS, None, fmt, return_y=True)
+    eu.inside(y, c.double(), c.double().abs().nan_to_num(0, 0) * (eu.H_BF16 + eu.norm_rel(K)), "y")
+    eu.check_special_codes(q, s, c, eu.norm_rel(K), fmt == "ue8m0", "codes")
+    assert c.isinf().any() and s.isinf().any()
+
+
 def test_norm_no_rows():
     w = torch.ones(256, dtype=BF16, device=DEV)
     q, s, y = fp8bs.rmsnorm_quant(torch.empty((0, 256), dtype=BF16, device=DEV), w, EPS, return_y=True)

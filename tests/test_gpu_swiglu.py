@@ -88,6 +88,24 @@ def test_swiglu_differences():
         eu.inside((a * v + b * w).sum(), diff, bound, "along a direction")
 
 
+@pytest.mark.parametrize("fmt", ["fp32", "ue8m0"])
+def test_infinities_and_nan_stay_in_their_blocks(fmt):
+    """Products beyond float32, infinite and NaN inputs: values as the formula has them, codes as c / s has them."""
+    M, N = 20, 640
+    gu = eu.normal((M, 2 * N), 11, 3.0)
+    clean = fp8bs.swiglu_quant(gu.to(DEV)[:, :N], gu.to(DEV)[:, N:], fmt, return_y=True)
+    for row, col, g, u in ((3, 5, 1e30, -1e30), (3, 130, 3e38, 3e38), (7, 300, INF, 2.0), (9, 639, NAN, 1.0), (9, 2, 1.0, NAN),
+                           (9, 4, 1.0, 1e30), (12, 250, 1.0, -INF), (15, 400, INF, 0.0)):
+        gu[row, col], gu[row, N + col] = g, u
+    a = eu.swiglu(gu[:, :N], gu[:, N:]).float()   # beyond float32: infinite
+    q, s, y = fp8bs.swiglu_quant(gu.to(DEV)[:, :N], gu.to(DEV)[:, N:], fmt, return_y=True)
+    eu.inside(y, a.double(), a.double().abs().nan_to_num(0, 0) * (eu.H_BF16 + eu.SILU_REL) + TINY, "y")
+    eu.check_special_codes(q, s, a, eu.SILU_REL, fmt == "ue8m0", "codes")
+    for got, want in zip((q.view(torch.uint8), s, y), (clean[0].view(torch.uint8), clean[1], clean[2])):
+        rest = [r for r in range(M) if r not in (3, 7, 9, 12, 15)]
+        assert torch.equal(got[rest], want[rest])
+
+
 def test_swiglu_last_rows_beyond_32_bits():
     M, N, ld = 40000, 256, 1 << 16
     buf = torch.zeros(M * ld, dtype=BF16, device=DEV)
