@@ -3,9 +3,10 @@
 // with block-scaled FP8 output for the second product (act_quant's rule:
 // "DeepSeek-V3 Administrator & Developer Guide" 8.5.1) or bf16, and its gradient.
 // HBM-bound: every element is read and written once; 16 consecutive lanes hold a
-// block of 128.  32768 x 2048 to codes 57.9 us (338 MB, 5.8 TB/s), the gradient of
-// 29999 x 2048 96.4 us (614 MB, 6.4 TB/s).  It was bound by instructions (87 us) with the
-// library's exponential and correctly rounded quotients, 48 a value; it takes 24.
+// block of 128.  32768 x 2048 to codes 58.5 us (338 MB, 5.8 TB/s), the gradient of
+// 29999 x 2048 96.5 us (614 MB, 6.4 TB/s).  It was bound by instructions (87 us) with the
+// library's exponential and correctly rounded quotients, 48 a value; it takes 28, 4 of
+// them for sigmoids below float32's range (57.8 us without).
 #include "device_common.h"
 #include "launch.h"
 
@@ -66,7 +67,10 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(const SwiGlu p, int sh
     unpack8(g[k], a);
     unpack8(u[k], b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = a[i] * sigmoid_f32(a[i]) * b[i];
+    for (int i = 0; i < 8; ++i) {
+      const Sigmoid s(a[i]);
+      a[i] = a[i] * s.kr * (b[i] * s.k);
+    }
     const int64_t at = r * nv + t.col;
     if (p.y) store_nt((uint4*)p.y + at, pack8(a));
     if (p.q) {
@@ -101,9 +105,10 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const SwiGluBwd p,
     unpack8(d[k], e);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = sigmoid_f32(a[i]), x = e[i] * s;
-      e[i] = x * b[i] * __builtin_fmaf(a[i], 1.0f - s, 1.0f);
-      b[i] = x * a[i];
+      const Sigmoid s(a[i]);
+      const float x = e[i] * s.kr, not_s = __builtin_fmaf(-s.kr, s.k, 1.0f);
+      e[i] = x * (b[i] * s.k) * __builtin_fmaf(a[i], not_s, 1.0f);
+      b[i] = x * (a[i] * s.k);
     }
     store_nt((uint4*)((uint16_t*)p.dgate + r * p.ld_dg) + t.col, pack8(e));
     store_nt((uint4*)((uint16_t*)p.dup + r * p.ld_du) + t.col, pack8(b));

@@ -666,6 +666,7 @@ int fp8bs_moe_gate_bwd(const void* logits, int64_t ld, int logits_dtype, const i
 /*
  * swiglu -- the activation between an expert's two products:
  *   a = g * sigmoid(g) * u   (float32),  y = bf16(a),
+ *       (to float32's accuracy also where sigmoid(g) is below its range, to g = -174)
  *   per 128 columns: s by act_quant's rule on a, q = e4m3(a / s) as rmsnorm's
  *   gate, up in   bf16, element (m, n) at [m*ld + n]: two tensors, or the halves
  *                 of one; ld_g, ld_u >= 0, multiples of 8

@@ -88,6 +88,28 @@ def test_swiglu_differences():
         eu.inside((a * v + b * w).sum(), diff, bound, "along a direction")
 
 
+def test_sigmoids_below_float32s_range():
+    """Gates down to -170, whose sigmoid is 2^-245: no allowance but half of bf16's smallest step, 2^-134."""
+    M, N = 64, 1280
+    g = -170 * torch.rand((M, N), generator=eu.gen(1))
+    g[:, :128] = torch.linspace(-86, -105, 128)
+    # up to the size that leaves the product within float32
+    size = 2.0 ** (torch.rand((M, N), generator=eu.gen(2)) * 240 - 120)
+    u = torch.where(torch.rand((M, N), generator=eu.gen(3)) < 0.5, size, -size)
+    g, u, dy = g.to(BF16), u.to(BF16), eu.normal((M, N), 4, 1.0)
+    a = eu.swiglu(g, u)
+    low = 2.0 ** -134 * (1 + eu.H_BF16)
+    # the outputs that the allowance elsewhere passes over are most of these
+    assert ((a.abs() > 2.0 ** -126) & (g < -88)).sum() > 1000
+    eu.inside(fp8bs.swiglu(g.to(DEV), u.to(DEV)), a, a.abs() * (eu.H_BF16 + eu.SILU_REL) + low, "y")
+    q, s = fp8bs.swiglu_quant(g.to(DEV), u.to(DEV), "ue8m0")
+    eu.check_codes(q, s, a, eu.SILU_REL, True, "codes")
+    dg, part, du = eu.swiglu_bwd(dy, g, u)
+    got_g, got_u = fp8bs.swiglu_bwd(dy.to(DEV), g.to(DEV), u.to(DEV))
+    eu.inside(got_g, dg, dg.abs() * eu.H_BF16 + part * 2 * eu.SILU_REL + low, "dgate")
+    eu.inside(got_u, du, du.abs() * (eu.H_BF16 + eu.SILU_REL) + low, "dup")
+
+
 @pytest.mark.parametrize("fmt", ["fp32", "ue8m0"])
 def test_infinities_and_nan_stay_in_their_blocks(fmt):
     """Products beyond float32, infinite and NaN inputs: values as the formula has them, codes as c / s has them."""
