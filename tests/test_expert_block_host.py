@@ -3,6 +3,7 @@ their gradients, the combine's): bad arguments are refused before any HIP call
 (the addresses below are never touched), and the binding refuses tensors that
 do not fit."""
 import os
+import re
 
 import pytest
 import torch
@@ -139,6 +140,22 @@ def test_workspace_sizes(L):
     assert f(-1, 256) == f(1, 100) == f(1, 1 << 16) == f(1 << 22, 1024) == f(1 << 26, 128) == -1
     assert g(0, 1, 64) == g(100, 0, 64) == 0 and g(4096, 1, 256) > 0
     assert g(-1, 1, 64) == g(1 << 24, 1, 64) == g(1, -1, 64) == g(1, 1, 0) == g(1, 1, 1025) == g(1, 1 << 22, 64) == -1
+
+
+def test_float32_sums_stay_in_32_bits(tmp_path):
+    """The balance and the gate's gradient sum floats over a wave: by DPP steps, with no 64-bit additions and no exchanges
+    through LDS, which a sum in 64 bits that takes a float's place would bring."""
+    from block_scaled_fp8_03_amd import build
+    out = str(tmp_path / "gate.s")
+    build._run([build.HIPCC, *build.COMMON_FLAGS, *build.HIP_FLAGS, *build.VGPR_FORM, "-x", "hip", "-S", "--cuda-device-only",
+                os.path.join(build.CSRC, "gate.hip"), "-o", out])
+    with open(out) as f:
+        text = f.read()
+    kernels = re.findall(r"^(_ZN5fp8bs\d+moe_(?:balance|balance_join|gate_bwd)_kernel\w*):.*?$(.*?)^\s+s_endpgm$", text, re.M | re.S)
+    assert len(kernels) == 9 * 3 + 1              # 1 to 16 experts a lane, loads wide or not; the balance twice
+    for name, body in kernels:
+        found = re.findall(r"v_add_f64\w*|ds_bpermute_b32|ds_swizzle_b32", body)
+        assert not found, (name, found)
 
 
 # --------------------------------------------------------------- the binding
