@@ -146,6 +146,50 @@ def test_norm_bwd_differences(M, K):
         eu.inside((dw.double().cpu() * u).sum(), by_w, (dw_bound * u.abs()).sum() + 1e-6, "by w")
 
 
+def _on_device(shape, gen, std, dtype):
+    return (torch.randn(shape, device=DEV, generator=gen) * std).to(dtype)
+
+
+@pytest.mark.parametrize("M,K,res", [(4096, 7168, BF16), (4096, 7168, F32), (8001, 7168, None), (60001, 384, BF16),
+                                     (70001, 256, F32), (3000, 16384, BF16), (1200, 32768, None)])
+def test_norm_many_rows_as_few(M, K, res):
+    """More than 160 MB, where inputs are read with a hint: bit by bit what a few rows at a time give."""
+    g = torch.Generator(DEV)
+    g.manual_seed(K)
+    x, w = _on_device((M, K), g, 2.0, BF16), _on_device((K,), g, 1.0, BF16)
+    r = None if res is None else _on_device((M, K), g, 3.0, res)
+    assert M * K * (5 + {None: 0, BF16: 4, F32: 8}[res]) > 160 << 20
+    got = fp8bs.rmsnorm_quant(x, w, EPS, r, return_y=True)
+    few = (24 << 20) // (K * 13)
+    for a in range(0, M, few):
+        rows = slice(a, min(a + few, M))
+        part = fp8bs.rmsnorm_quant(x[rows], w, EPS, None if r is None else r[rows], return_y=True)
+        for one, many in zip(part, got):
+            assert torch.equal(one.view(torch.uint8), many[rows].view(torch.uint8)), a
+
+
+@pytest.mark.parametrize("M,K,h_type,w_type", [(4096, 7168, BF16, BF16), (2001, 7168, F32, F32), (60001, 384, BF16, F32),
+                                               (90001, 256, BF16, BF16), (200001, 128, BF16, BF16), (11001, 2048, BF16, BF16),
+                                               (1700, 16384, BF16, BF16), (1500, 18432, BF16, BF16), (900, 32768, F32, BF16)])
+def test_norm_bwd_many_rows_as_few(M, K, h_type, w_type):
+    """The same of the gradient by the rows; the weight's against its sum in 64 bits."""
+    g = torch.Generator(DEV)
+    g.manual_seed(K)
+    dy, h = _on_device((M, K), g, 0.5, BF16), _on_device((M, K), g, 2.0, h_type)
+    dres, w = _on_device((M, K), g, 0.5, h_type), _on_device((K,), g, 1.0, w_type)
+    assert M * K * (8 if h_type == BF16 else 14) > 160 << 20
+    dx, dw = fp8bs.rmsnorm_bwd(dy, h, w, EPS, dres)
+    few = (24 << 20) // (K * 14)
+    for a in range(0, M, few):
+        rows = slice(a, min(a + few, M))
+        part, _ = fp8bs.rmsnorm_bwd(dy[rows], h[rows], w, EPS, dres[rows])
+        assert torch.equal(part, dx[rows]), a
+    each = dy.double() * h.double() / (h.double().square().mean(-1, keepdim=True) + EPS).sqrt()
+    eu.inside(dw, each.sum(0), each.abs().sum(0) * (eu.norm_rel(K) + (M + 32) * eu.H_F32), "dw")
+    again, dw2 = fp8bs.rmsnorm_bwd(dy, h, w, EPS, dres)
+    assert torch.equal(again, dx) and torch.equal(dw2, dw)
+
+
 def test_norm_last_rows_beyond_32_bits():
     """Offsets past 2^31 elements: the last rows of a strided input and of large outputs."""
     K, ld, M = 7168, 1 << 16, 40000

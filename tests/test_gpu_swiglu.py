@@ -128,6 +128,34 @@ def test_infinities_and_nan_stay_in_their_blocks(fmt):
         assert torch.equal(got[rest], want[rest])
 
 
+@pytest.mark.parametrize("M,N", [(8001, 2048), (32768, 2048), (30001, 384), (120001, 384)])
+def test_many_rows_as_few(M, N):
+    """More than 8 workgroups a CU (a thread takes rows in turn), below and above 160 MB (where inputs are read with a hint),
+    counts that end inside a thread's rows: bit by bit what a few rows at a time give, and nothing behind the count."""
+    g = torch.Generator(DEV)
+    g.manual_seed(M)
+    gu = (torch.randn((M, 2 * N), device=DEV, generator=g) * 2).to(BF16)
+    dy = torch.randn((M, N), device=DEV, generator=g).to(BF16)
+    few = 2000 if N == 2048 else 10000
+    same = lambda a, b: torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))  # noqa: E731
+    for n in (M, (M - 2768) | 1, (M // 4 - 1) | 1):
+        gu[n:], dy[n:] = NAN, NAN
+        count = torch.tensor([n], dtype=torch.int32, device=DEV)
+        q = torch.full((M, N), 0x5A, dtype=torch.uint8, device=DEV)
+        s, y = torch.full((M, N // 128), -7.0, device=DEV), torch.full((M, N), 9.0, dtype=BF16, device=DEV)
+        d = torch.full((M, 2 * N), 8.0, dtype=BF16, device=DEV)
+        fp8bs.fp8bs_swiglu(gu[:, :N], gu[:, N:], y, q.view(eu.FP8), s, "fp32", None if n == M else count)
+        fp8bs.fp8bs_swiglu_bwd(dy, gu[:, :N], gu[:, N:], d[:, :N], d[:, N:], None if n == M else count)
+        assert (q[n:] == 0x5A).all() and (s[n:] == -7).all() and (y[n:] == 9).all() and (d[n:] == 8).all()
+        for a in range(0, n, few):
+            b = min(a + few, n)
+            part = gu[a:b]
+            q2, s2, y2 = fp8bs.swiglu_quant(part[:, :N], part[:, N:], return_y=True)
+            dg2, du2 = fp8bs.swiglu_bwd(dy[a:b], part[:, :N], part[:, N:])
+            assert same(q[a:b], q2) and same(s[a:b], s2) and same(y[a:b], y2), (n, a)
+            assert same(d[a:b, :N], dg2) and same(d[a:b, N:], du2), (n, a)
+
+
 def test_swiglu_last_rows_beyond_32_bits():
     M, N, ld = 40000, 256, 1 << 16
     buf = torch.zeros(M * ld, dtype=BF16, device=DEV)
@@ -173,6 +201,31 @@ def test_combine_bwd_nothing():
     _, d_w = fp8bs.moe_combine_bwd(e(3, 0), e(4, 0), torch.ones((3, 2), device=DEV),
                                    torch.zeros((3, 2), dtype=torch.int32, device=DEV))
     assert (d_w == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_combine_bwd_many_rows_as_few(dtype):
+    """196 MB of rows, read with a hint: bit by bit what a few tokens at a time give."""
+    T, topk, N = 1500, 8, 4096
+    R = T * topk + 3
+    g = torch.Generator(DEV)
+    g.manual_seed(1)
+    row_of = torch.randperm(R, device=DEV, generator=g)[:T * topk].to(torch.int32)
+    row_of[::50] = -1
+    row_of = row_of.view(T, topk)
+    dy, out = torch.randn((T, N), device=DEV, generator=g).to(dtype), torch.randn((R, N), device=DEV, generator=g).to(BF16)
+    w = torch.rand((T, topk), device=DEV, generator=g)
+    both = [(torch.full((R, N), 9.0, dtype=BF16, device=DEV), torch.full((T, topk), NAN, device=DEV)) for _ in range(2)]
+    fp8bs.fp8bs_moe_combine_bwd(dy, out, w, row_of, *both[0])
+    for a in range(0, T, 100):
+        d_w = torch.full((100, topk), NAN, device=DEV)
+        fp8bs.fp8bs_moe_combine_bwd(dy[a:a + 100], out, w[a:a + 100], row_of[a:a + 100], both[1][0], d_w)
+        both[1][1][a:a + 100] = d_w
+    for one, many in zip(*both):
+        assert torch.equal(one, many)
+    used = torch.zeros(R, dtype=torch.bool, device=DEV)
+    used[row_of[row_of >= 0].long()] = True
+    assert (both[0][0][~used] == 9).all() and int((~used).sum()) == 3 + T * topk // 50
 
 
 def test_combine_bwd_beyond_32_bits():
