@@ -49,6 +49,42 @@ def test_gate_many_tokens_choose_exactly(kind, with_bias):
     _check(z, 8, eu.normal((256,), 6, 0.05, F32) if with_bias else None, 8, 4, kind, True, 2.5)
 
 
+def _near_ties(kind):
+    """Tokens with two experts at the border of the top 4 whose logits are neighbours in float32: their scores are the same
+    number or the next one, decided within 1/20 of a step (but not 1/500) of a rounding's border."""
+    E, topk, many = 64, 4, 400000
+    g = eu.gen(7)
+    lo = (1.0 + 2.5 * torch.rand(many, generator=g)) if kind == "sigmoid" else (0.26 + 0.2 * torch.rand(many, generator=g))
+    lo = lo.numpy().astype(np.float32)
+    hi = np.nextafter(lo, np.float32(10))
+    z = np.full((many, E), -5.0, np.float32) + torch.rand((many, E), generator=g).numpy()
+    z[:, 5:8] = 6.0, 7.0, 8.0
+    z[:, 5:8] -= 0 if kind == "sigmoid" else 5.0
+    z[:, 20], z[:, 41] = lo, hi
+    p = eu.scores(z, kind)[:, [20, 41]]
+    step = np.spacing(p.astype(np.float32)).astype(np.float64)
+    off = np.abs(np.mod(p / step, 1.0) - 0.5)          # from the middle of two float32 numbers, in steps
+    near = (off.min(1) < 0.05) & (off.min(1) > 0.002)
+    z = torch.from_numpy(z[near][:4000])
+    assert z.shape[0] == 4000
+    return z, topk
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("shift", [0.0, -0.5])
+def test_gate_near_ties_choose_exactly(kind, shift):
+    """With a bias the choice goes by scores in 64 bits, rounded once: float32 arithmetic gives hundreds of these tokens another expert."""
+    z, topk = _near_ties(kind)
+    bias = torch.zeros(64)
+    bias[[20, 41]] = shift * (1.0 if kind == "sigmoid" else 0.06)   # key = score + shift is exact
+    sloppy = torch.sigmoid(z) if kind == "sigmoid" else torch.softmax(z, -1)
+    pair = lambda p: (p[:, 41] > p[:, 20])  # noqa: E731
+    exact = torch.from_numpy(eu.scores(z.numpy(), kind)).float()
+    assert pair(exact).any() and not pair(exact).all() and (pair(sloppy) != pair(exact)).sum() > 100
+    idx, _ = _check(z, topk, bias, kind=kind)
+    assert set(idx[:, 3].tolist()) == {20, 41} and torch.equal(idx[:, 3].cpu() == 41, pair(exact))
+
+
 def test_gate_ties_go_to_the_lowest_index():
     for E in (8, 64, 200, 512):
         z = torch.zeros((3, E))
