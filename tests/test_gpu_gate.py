@@ -222,6 +222,43 @@ def test_masks_in_the_loss_and_gradients(kind):
                                        + ref.abs() * eu.H_F32 + 1e-37)[rows], "d_logits")
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+def test_losses_with_masks(kind):
+    """Losses and mean shares of sequences with masked, NaN, infinite and saturated logits, and experts named twice."""
+    T, E, topk = 14, 60, 6
+    z = eu.normal((T, E), 13, 2.0, F32)
+    z[0] = -INF
+    z[1, 5:] = -INF
+    z[2, 4], z[2, 50:] = NAN, -INF
+    z[4] = -120.0                                  # scores that underflow: a sequence of their own
+    z[5] = -95.0
+    z[6] = 90.0
+    z[7, 3] = 60.0
+    z[8, 2], z[8, 9] = INF, INF
+    z[9, ::2] = NAN
+    idx, _ = fp8bs.moe_gate(z.to(DEV), topk, score=kind)
+    idx = idx.cpu()
+    idx[7] = idx[7, 0]
+    idx[10, 1::2] = idx[10, 0]
+    cu = [0, 4, 6, 6, 12, 13]                      # the last token is in none
+    loss, counts, probs = fp8bs.moe_balance(z.to(DEV), idx.to(DEV), torch.tensor(cu, dtype=torch.int32, device=DEV), kind)
+    rl, rc, rp = eu.balance(z, idx, cu, kind)
+    assert torch.equal(counts.cpu(), rc)
+    assert (probs >= 0).all() and torch.isfinite(probs).all() and torch.isfinite(loss).all()
+    rel = 2 * eu.score_rel(z, E) + 100 * eu.H_F32
+    ok = [0, 2, 3, 4] if kind == "sigmoid" else [0, 1, 2, 3, 4]   # sums of denormal scores carry no precision
+    eu.inside(probs[ok], rp[ok], rp[ok] * rel + 1e-37, "probs")
+    eu.inside(loss[ok], rl[ok], rl[ok] * (rel + E * eu.H_F32) + 1e-36, "loss")
+    assert (rl[[0, 3, 4]] > 0).all() and loss[2] == 0
+    dl = torch.tensor([1.0, 0.0, 5.0, -2.0, 3.0])
+    dev = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    d = fp8bs.moe_gate_bwd(z.to(DEV), idx.to(DEV), None, kind, cu_seq=dev, counts=counts, d_loss=dl.to(DEV))
+    ref, size = eu.gate_bwd(z, idx, None, kind, True, 1.0, cu, dl)
+    assert (d.cpu()[~(z > -INF)] == 0).all() and (d[13] == 0).all()
+    rows = [r for r in range(T) if r not in (4, 5)]
+    eu.inside(d[rows], ref[rows], (size * 2 * rel + ref.abs() * eu.H_F32 + 1e-37)[rows], "d_logits")
+
+
 def test_bounds_that_are_wrong_stay_inside():
     """Boundaries out of range or falling: nothing outside the buffers is written."""
     E, guard = 64, 4096
