@@ -195,32 +195,15 @@ __device__ __forceinline__ uint32_t wave_max_uniform(uint32_t v) {
 // the hardware's power of two of x log2(e) - n, n the nearest whole number, which two
 // fused products with the halves of log2(e) give to 2^-25.  8 instructions where the
 // library's function takes 14.
-constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596299e-8f;
 __device__ __forceinline__ float exp_f32(float x) {
+  constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;
   x = __builtin_amdgcn_fmed3f(x, -150.0f, 150.0f);
-  const float n = __builtin_rintf(x * kLog2eHi);
-  const float f = __builtin_fmaf(x, kLog2eLo, __builtin_fmaf(x, kLog2eHi, -n));
+  const float n = __builtin_rintf(x * kHi);
+  const float f = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -n));
   return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
 }
-// e^(-|x| / 2), the same way
-__device__ __forceinline__ float exp_half(float x) {
-  const float y = __builtin_amdgcn_fmed3f(fabsf(x), 0.0f, 300.0f);
-  const float n = __builtin_rintf(y * (-0.5f * kLog2eHi));
-  const float f = __builtin_fmaf(y, -0.5f * kLog2eLo, __builtin_fmaf(y, -0.5f * kLog2eHi, -n));
-  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
-}
-// sigmoid(x) = k * kr within 9 units in the last place, with h = e^(-|x| / 2): k = h below
-// 0 and 1 from 0 on, kr = k / (1 + h * h).  Below -87 a sigmoid leaves float32's normal
-// range, its factors only below -174: a product g * kr * (u * k) is right where it is in
-// that range itself.
-struct Sigmoid {
-  float k, kr;
-  __device__ __forceinline__ explicit Sigmoid(float x) {
-    const float h = exp_half(x);
-    k = x < 0.0f ? h : 1.0f;
-    kr = k * __builtin_amdgcn_rcpf(__builtin_fmaf(h, h, 1.0f));
-  }
-};
+// 1 / (1 + e^-x) within 4 units in the last place for x >= -87; below, where it leaves float32's normal range, 0
+__device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x)); }
 
 // 8 bf16 of a vector as floats, and back
 __device__ __forceinline__ void unpack8(const uint4& u, float* f) {

@@ -3,10 +3,9 @@
 // with block-scaled FP8 output for the second product (act_quant's rule:
 // "DeepSeek-V3 Administrator & Developer Guide" 8.5.1) or bf16, and its gradient.
 // HBM-bound: every element is read and written once; 16 consecutive lanes hold a
-// block of 128.  32768 x 2048 to codes 58.5 us (338 MB, 5.8 TB/s), the gradient of
-// 29999 x 2048 96.5 us (614 MB, 6.4 TB/s).  It was bound by instructions (87 us) with the
-// library's exponential and correctly rounded quotients, 48 a value; it takes 28, 4 of
-// them for sigmoids below float32's range (57.8 us without).
+// block of 128.  32768 x 2048 to codes 58.2 us (338 MB, 5.8 TB/s), the gradient of
+// 29999 x 2048 95.5 us (614 MB, 6.4 TB/s).  It was bound by instructions (87 us) with the
+// library's exponential and correctly rounded quotients, 48 a value; it takes 24.
 #include "device_common.h"
 #include "launch.h"
 
@@ -32,6 +31,17 @@ __device__ __forceinline__ Tile tile_of(int shift, uint32_t chunks, int passes) 
   const int step = kThreads >> shift;
   return {(int64_t)band * (step * passes) + (threadIdx.x >> shift),
           (chunk << shift) + (threadIdx.x & ((1u << shift) - 1)), step};
+}
+
+// Below -80 a gate's sigmoid is e^g to float32's last bit, and soon outside its normal range, while g * e^g * u need not
+// be.  Such values are made in two factors h = e^(g / 2), in range down to -174.  They are rare: a wave without any
+// passes them by with a maximum and a branch.  (All values in two factors: 28 instructions a value, 58.5 us.)
+constexpr float kDeep = -80.0f;
+__device__ __forceinline__ bool any_deep(const float* g) {
+  uint32_t most = f32_bits(g[0]);                            // of negative floats the largest magnitude, above all others
+#pragma unroll
+  for (int i = 1; i < 8; ++i) most = max(most, f32_bits(g[i]));
+  return __any(most > f32_bits(kDeep));
 }
 
 // rows that the call has: all, or fewer by the device's count
@@ -63,13 +73,17 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(const SwiGlu p, int sh
   for (int k = 0; k < PASSES; ++k) {
     const int64_t r = t.row + k * t.step;
     if (r >= rows) return;
-    float a[8], b[8];
-    unpack8(g[k], a);
+    float x[8], b[8], a[8];
+    unpack8(g[k], x);
     unpack8(u[k], b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const Sigmoid s(a[i]);
-      a[i] = a[i] * s.kr * (b[i] * s.k);
+    for (int i = 0; i < 8; ++i) a[i] = x[i] * sigmoid_f32(x[i]) * b[i];
+    if (any_deep(x)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float h = exp_f32(0.5f * x[i]);
+        if (x[i] < kDeep) a[i] = x[i] * h * (b[i] * h);
+      }
     }
     const int64_t at = r * nv + t.col;
     if (p.y) store_nt((uint4*)p.y + at, pack8(a));
@@ -99,19 +113,25 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const SwiGluBwd p,
   for (int k = 0; k < PASSES; ++k) {
     const int64_t r = t.row + k * t.step;
     if (r >= rows) return;
-    float a[8], b[8], e[8];
+    float a[8], b[8], e[8], dg[8], du[8];
     unpack8(g[k], a);
     unpack8(u[k], b);
     unpack8(d[k], e);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const Sigmoid s(a[i]);
-      const float x = e[i] * s.kr, not_s = __builtin_fmaf(-s.kr, s.k, 1.0f);
-      e[i] = x * (b[i] * s.k) * __builtin_fmaf(a[i], not_s, 1.0f);
-      b[i] = x * (a[i] * s.k);
+      const float s = sigmoid_f32(a[i]), x = e[i] * s;
+      dg[i] = x * b[i] * __builtin_fmaf(a[i], 1.0f - s, 1.0f);
+      du[i] = x * a[i];
     }
-    store_nt((uint4*)((uint16_t*)p.dgate + r * p.ld_dg) + t.col, pack8(e));
-    store_nt((uint4*)((uint16_t*)p.dup + r * p.ld_du) + t.col, pack8(b));
+    if (any_deep(a)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float h = exp_f32(0.5f * a[i]), x = e[i] * h;
+        if (a[i] < kDeep) dg[i] = x * (b[i] * h) * (1.0f + a[i]), du[i] = x * (a[i] * h);
+      }
+    }
+    store_nt((uint4*)((uint16_t*)p.dgate + r * p.ld_dg) + t.col, pack8(dg));
+    store_nt((uint4*)((uint16_t*)p.dup + r * p.ld_du) + t.col, pack8(du));
   }
 }
 
