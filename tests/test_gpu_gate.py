@@ -294,6 +294,25 @@ def test_balance_many_sequences_and_long_ones():
     _balance(z, idx, None, "softmax")
 
 
+@pytest.mark.parametrize("runs", [1, 2, 3, 4, 200, 70000])
+def test_balance_runs_of_empty_sequences(runs):
+    """Empty sequences between a workgroup's tokens, before the first and behind the last."""
+    E, topk = 24, 3
+    lens = [0] * runs + [5] + [0] * runs + [1, 1] + [0] * runs + [60, 0, 2] + [0] * runs
+    cu = [0] + np.cumsum(lens).tolist()
+    T = cu[-1] + 7                                 # the last tokens are in none
+    z = eu.normal((T, E), runs, 2.0, F32)
+    idx = torch.randint(0, E, (T, topk), generator=eu.gen(2), dtype=torch.int32)
+    dev = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    loss, counts, probs = (t.cpu() for t in fp8bs.moe_balance(z.to(DEV), idx.to(DEV), dev))
+    has = [n for n, v in enumerate(lens) if v]
+    rl, rc, rp = eu.balance(z, idx, [0] + [cu[n + 1] for n in has], "sigmoid")
+    assert torch.equal(counts[has], rc) and int(counts.sum()) == topk * cu[-1]
+    eu.inside(probs[has], rp, rp * (eu.score_rel(z, E) + 128 * eu.H_F32), "probs")
+    eu.inside(loss[has], rl, rl * (eu.score_rel(z, E) + (128 + E) * eu.H_F32), "loss")
+    assert int((probs != 0).any(1).sum()) == int((loss != 0).sum()) == len(has)
+
+
 def test_balance_no_tokens_and_no_sequences():
     z, idx = torch.empty((0, 64), device=DEV), torch.empty((0, 4), dtype=torch.int32, device=DEV)
     loss, counts, probs = fp8bs.moe_balance(z, idx, torch.zeros(4, dtype=torch.int32, device=DEV))
