@@ -578,7 +578,9 @@ int fp8bs_cache_compact(void* latent, float* lat_scale, void* rope, int cache_fm
  *   g = dy * norm_w, r = 1 / sqrt(mean(h^2) + eps)
  *   dx = r * (g - h * r^2 * mean(g * h)) + dres,   dw = sum over rows of dy * h * r
  * dx is the gradient of x and of res alike; dres is what reaches res_out from
- * elsewhere.  The codes' rounding is passed straight through.
+ * elsewhere.  The codes' rounding is passed straight through.  A row whose
+ * squares sum to infinity, which forward gives zeros, has dx = dres (as long as
+ * g * h sums to a number) and adds nothing to dw.
  *   dy       in   bf16 [M, K]
  *   h        in   bf16 or float32 (h_dtype), element (m, k) at [m*ld_h + k]
  *   dres     in   [M, K] of h's type, or NULL; may be dx itself
@@ -690,7 +692,8 @@ int fp8bs_moe_gate_bwd(const void* logits, int64_t ld, int logits_dtype, const i
  *   d_out    out  bf16 [R, N]; rows that no pair maps to are left untouched
  *   d_w      out  float32 [T, topk]; 0 for pairs outside [0, R)
  *   0 <= T < 2^23, topk >= 1, T * topk < 2^31, R, N >= 0.
- * If row_of maps two pairs to one row, that row of d_out receives either's.
+ * If row_of maps two pairs to one row, each element of that row of d_out
+ * receives either's.
  * dy, out and d_out 16-byte aligned, the others 4-byte.
  */
 int fp8bs_swiglu(const void* gate_bf16, int64_t ld_g, const void* up_bf16, int64_t ld_u, const int32_t* n_rows,

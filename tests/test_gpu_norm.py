@@ -121,6 +121,25 @@ def test_norm_bwd(K, h_type, w_type, dres, pad, M):
         assert torch.equal(a, got) and torch.equal(b, got_w), "the same from call to call"
 
 
+@pytest.mark.parametrize("K", [256, 1536, 32768])
+def test_norm_bwd_rows_beyond_float32(K):
+    """A row whose squares sum to infinity, forward a constant 0: dres goes through, nothing to the weight; its neighbours are
+    as without it.  A row of zeros likewise has its own eps."""
+    M = 9
+    dy, h, dres = eu.normal((M, K), 1, 0.5), eu.normal((M, K), 2, 2.0), eu.normal((M, K), 3, 0.5)
+    w = eu.normal((K,), 4)
+    h[2], h[5] = 1e25, 0.0
+    h[7, 3] = -1e30
+    dx, dw = fp8bs.rmsnorm_bwd(dy.to(DEV), h.to(DEV), w.to(DEV), EPS, dres.to(DEV))
+    ref, bound, _, _ = eu.norm_bwd(dy, h, w, EPS, dres)
+    big = [2, 7]
+    assert torch.equal(dx[big].cpu(), dres[big])
+    rest = [r for r in range(M) if r not in big]
+    eu.inside(dx[rest], ref[rest], ref[rest].abs() * eu.H_BF16 + bound[rest] * 1.01, "dx")
+    _, _, ref_w, bound_w = eu.norm_bwd(dy[rest], h[rest], w, EPS, None)
+    eu.inside(dw, ref_w, bound_w, "dw")
+
+
 def test_norm_bwd_no_rows():
     w = torch.ones(256, dtype=BF16, device=DEV)
     e = torch.empty((0, 256), dtype=BF16, device=DEV)

@@ -228,6 +228,21 @@ def test_combine_bwd_many_rows_as_few(dtype):
     assert (both[0][0][~used] == 9).all() and int((~used).sum()) == 3 + T * topk // 50
 
 
+@pytest.mark.parametrize("N", [1536, 1003])
+def test_combine_bwd_two_pairs_of_one_row(N):
+    """Each element of the row receives one of the two products; both pairs' weights their gradients."""
+    T, topk, R = 6, 2, 5
+    row_of = torch.tensor([[0, 0], [1, 2], [2, 3], [-1, 4], [4, -1], [R, -1]], dtype=torch.int32)
+    dy, out = eu.normal((T, N), 1, 0.5), eu.normal((R, N), 2)
+    w = torch.rand((T, topk), generator=eu.gen(3)) + 0.1
+    d_out, d_w = fp8bs.moe_combine_bwd(dy.to(DEV), out.to(DEV), w.to(DEV), row_of.to(DEV))
+    _, ref_w, size = eu.combine_bwd(dy, out, w, row_of)
+    eu.inside(d_w, ref_w, size * (N / 64 + 16) * eu.H_F32, "d_w")
+    for row in range(R):
+        each = [(w[t, k] * dy[t].float()).to(BF16) for t in range(T) for k in range(topk) if row_of[t, k] == row]
+        assert torch.stack([d_out[row].cpu() == e for e in each]).any(0).all(), row
+
+
 def test_combine_bwd_beyond_32_bits():
     """Rows past 2^31 elements of out and d_out."""
     R, N = 300000, 7168
