@@ -26,7 +26,9 @@ Allocating conveniences: ``act_quant``, ``weight_quant``, ``weight_dequant``,
 
 The operations follow the DeepSeek-V3 inference pages ("DeepSeek-V3
 Administrator & Developer Guide", sections 6.3, 6.4, 8.5.1-8.5.3; "DeepSeek-V3
-User Guide", FAQ on scale_fmt ue8m0).  If the library has not been built the
+User Guide", FAQ on scale_fmt ue8m0).  Gradients are calls of their own (``*_bwd``):
+no operator takes part in autograd, and what comes of a tensor that requires a
+gradient is detached from it.  If the library has not been built the
 calls raise; there is no fallback implementation.
 """
 from __future__ import annotations

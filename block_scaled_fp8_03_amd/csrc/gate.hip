@@ -6,9 +6,9 @@
 // and the lowest register of a maximum are the lowest expert.  A token's logits are
 // a few hundred bytes: what these kernels take is a wave's chain of instructions
 // (few tokens) or the instructions of all waves (many), not HBM.  256 experts in 8
-// groups, top 8, from a graph: 32 tokens 4.4 us, 2.2 of it the launch, 4096 tokens 6.8,
-// 30000 tokens 31 (564 vector instructions a token, 8 x 33 of them the choice, 108 the
-// scores); counts, loss and both gradients of 4096 tokens 16.6.
+// groups, top 8, from a graph: 32 tokens 4.1 us, 1.6 of it the launch, 4096 tokens 6.3,
+// 30000 tokens 29 (564 vector instructions a token, 8 x 33 of them the choice, 108 the
+// scores); counts, loss and both gradients of 4096 tokens 15.8.
 #include <algorithm>
 
 #include "device_common.h"

@@ -3,9 +3,9 @@
 // with block-scaled FP8 output for the second product (act_quant's rule:
 // "DeepSeek-V3 Administrator & Developer Guide" 8.5.1) or bf16, and its gradient.
 // HBM-bound: every element is read and written once; 16 consecutive lanes hold a
-// block of 128.  32768 x 2048 to codes 58.2 us (338 MB, 5.8 TB/s), the gradient of
-// 29999 x 2048 95.5 us (614 MB, 6.4 TB/s).  It was bound by instructions (87 us) with the
-// library's exponential and correctly rounded quotients, 48 a value; it takes 24.
+// block of 128.  32768 x 2048 to codes 58.1 us (338 MB, 5.8 TB/s), the gradient of
+// 29999 x 2048 95.3 us (614 MB, 6.4 TB/s).  It was bound by instructions (87 us) with the
+// library's exponential and correctly rounded quotients, 48 a value; it takes 23.
 #include "device_common.h"
 #include "launch.h"
 
