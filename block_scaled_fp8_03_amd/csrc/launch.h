@@ -106,11 +106,11 @@ hipError_t launch_cache_compact(const PageTask& a, hipStream_t stream);
 // Calls that move at least this many bytes read their inputs with the non-temporal hint;
 // below, what the call before left in the Infinity Cache (256 MB) is found there, which
 // the hint gives up.  us, with the hint / without (inputs of three calls in turn):
-// SwiGLU 84 MB 17.6 / 17.1, 169 MB 31.4 / 33.3, 338 MB 58.0 / 63.0; its gradient 84 MB
-// 15.0 / 13.7, 168 MB 28.1 / 29.4; RMSNorm 132 MB 25.4 / 21.3, 265 MB 46.2 / 47.0; the
+// SwiGLU 84 MB 16.9 / 16.1, 169 MB 29.8 / 32.4, 338 MB 56.1 / 61.3; its gradient 84 MB
+// 14.5 / 13.4, 168 MB 27.2 / 28.6; RMSNorm 132 MB 25.4 / 21.3, 265 MB 46.2 / 47.0; the
 // combine's gradient 98 MB 24.6 / 18.1, 196 MB 48.5 / 51.4, 999 MB 190 / 203.  Rows that a
-// count on the device leaves out count too: 2000 of 32768 rows of 2048, SwiGLU 6.9 / 7.6, its
-// gradient 9.7 / 9.9.
+// count on the device leaves out count too: 2000 of 32768 rows of 2048, SwiGLU 5.7 / 6.6, its
+// gradient 8.1 / 8.2.
 constexpr int64_t kHintBytes = (int64_t)160 << 20;
 
 // fp8bs_rmsnorm's arguments (res and res_out, y, q and s: NULL where there is none)

@@ -3,8 +3,8 @@
 // with block-scaled FP8 output for the second product (act_quant's rule:
 // "DeepSeek-V3 Administrator & Developer Guide" 8.5.1) or bf16, and its gradient.
 // HBM-bound: every element is read and written once; 16 consecutive lanes hold a
-// block of 128.  32768 x 2048 to codes 58.1 us (338 MB, 5.8 TB/s), the gradient of
-// 29999 x 2048 95.3 us (614 MB, 6.4 TB/s).  It was bound by instructions (87 us) with the
+// block of 128.  32768 x 2048 to codes 56.1 us (338 MB, 6.0 TB/s), the gradient of
+// 29999 x 2048 95.5 us (614 MB, 6.4 TB/s).  It was bound by instructions (87 us) with the
 // library's exponential and correctly rounded quotients, 48 a value; it takes 23.
 #include "device_common.h"
 #include "launch.h"
@@ -14,9 +14,9 @@ namespace fp8bs {
 namespace {
 
 constexpr int kThreads = 256;
-// Rows that a thread takes where there are many.  us with 2 / 4 / 8: 32768 x 2048 58.5 / 58.0 / 59.0; gradient of
-// 29999 x 2048 with 2 / 4: 96.7 / 99.5.
-constexpr int kPasses = 4, kBwdPasses = 2;
+// Rows that a thread takes where there are many.  us with 2 / 3 / 4 / 8: 32768 x 2048 55.9 / 56.1 / 58.0 / 58.8, a buffer
+// of them of which a count says that 2000 are there 7.0 / 5.7 / 5.5 / 7.0; gradient of 29999 x 2048 with 2 / 4: 95.5 / 98.4.
+constexpr int kPasses = 3, kBwdPasses = 2;
 
 // A workgroup's 256 threads are R = 256 / C rows of C vectors, C the largest power of
 // two, up to 256, that divides a row's vectors: no lane is idle and a thread's row and
@@ -35,7 +35,7 @@ __device__ __forceinline__ Tile tile_of(int shift, uint32_t chunks, int passes) 
 
 // Below -80 a gate's sigmoid is e^g to float32's last bit, and soon outside its normal range, while g * e^g * u need not
 // be.  Such values are made in two factors h = e^(g / 2), in range down to -174.  They are rare: a wave without any
-// passes them by with a maximum and a branch.  (All values in two factors: 28 instructions a value, 58.5 us.)
+// passes them by with a maximum and a branch.  (All values in two factors: 28 instructions a value for 23.)
 constexpr float kDeep = -80.0f;
 __device__ __forceinline__ bool any_deep(const float* g) {
   uint32_t most = f32_bits(g[0]);                            // of negative floats the largest magnitude, above all others
